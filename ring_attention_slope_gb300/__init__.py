@@ -13,6 +13,15 @@ The calls mirror the C ABI:
 * :func:`lse_merge` - exact log-sum-exp merge of partials.
 * :func:`cp_prefill` - the whole context-parallel prefill attention: ring
   steps (zigzag or contiguous) or chunked prefill, run in order, then merged.
+
+and, around the prefill (``include/slope_serving.h``):
+
+* :func:`qk_norm_rope` - RMS norm of every query and key head and the rotation
+  by position, in one pass (:class:`Rope`, :func:`rope_inv_freq`).
+* :func:`attn_varlen` - causal attention over packed prompts.
+* :class:`KV4Cache`, :func:`kv4_write`, :func:`kv4_read` - a paged key/value
+  cache in 4 bits.
+* :func:`kv4_attn` - attention of each sequence's newest tokens over it.
 """
 from __future__ import annotations
 
@@ -25,6 +34,8 @@ __all__ = [
     "SlopeError", "load", "build", "attn_partial", "lse_merge", "cp_prefill", "cp_prefill_timed",
     "cp_prefill_workspace_size", "cp_prefill_plan", "device_status", "timeout_selftest", "LAYOUTS", "version",
     "cp_prefill_static_scratch", "dck_chunk_sizes",
+    "Rope", "rope_inv_freq", "qk_norm_rope", "attn_varlen", "KV4Cache", "kv4_write", "kv4_read", "kv4_attn",
+    "kv4_attn_workspace_size",
 ]
 
 LAYOUTS = {"contiguous": 0, "zigzag": 1, "chunked": 2, "ulysses": 3}
@@ -120,6 +131,7 @@ def load():
     lib.slope_cp_prefill_ex.restype = c_int
     lib.slope_cp_prefill_workspace_size_ex.argtypes = [i64, i64, i64, c_int, c_int, P(i64), ctypes.c_uint]
     lib.slope_cp_prefill_workspace_size_ex.restype = ctypes.c_size_t
+    _serving.declare(lib)
     _lib = lib
     return lib
 
@@ -432,3 +444,8 @@ def device_status(stream=None):
 def timeout_selftest(limit_ns: int, stream=None):
     """Launch the bounded-wait self-test kernel (its wait is meant to run out)."""
     _check(load().slope_debug_timeout_selftest(int(limit_ns), _stream_ptr(stream)), "slope_debug_timeout_selftest")
+
+
+from . import serving as _serving  # noqa: E402  (it uses the helpers above)
+from .serving import (EXPORTED_SERVING, KV4Cache, Rope, SlopeKV4Cache, SlopeRope, attn_varlen,  # noqa: E402,F401
+                      kv4_attn, kv4_attn_workspace_size, kv4_read, kv4_write, qk_norm_rope, rope_inv_freq)

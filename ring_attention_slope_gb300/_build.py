@@ -18,8 +18,9 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libslope.so")
 
-SOURCES = ["api.cu", "attn_partial.cu", "lse_merge.cu", "status.cu", "dck.cpp"]
-HEADERS = ["kernels.cuh", "sm103_ptx.cuh", "waits.cuh"]
+SOURCES = ["attn_partial.cu", "kv4_attn.cu", "api.cu", "lse_merge.cu", "qk_norm_rope.cu", "kv4_store.cu", "status.cu",
+           "dck.cpp", "rope.cpp"]
+HEADERS = ["host.cuh", "kernels.cuh", "kv4.cuh", "sm103_ptx.cuh", "waits.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "-I", INCLUDE, "-I", CSRC]
@@ -36,7 +37,8 @@ def _stale() -> bool:
     if not os.path.exists(LIB_PATH):
         return True
     t = os.path.getmtime(LIB_PATH)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(INCLUDE, "slope.h"), __file__]
+    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
+    deps += [os.path.join(INCLUDE, f) for f in ("slope.h", "slope_serving.h")] + [__file__]
     return any(os.path.getmtime(d) > t for d in deps)
 
 

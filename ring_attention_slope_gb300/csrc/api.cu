@@ -2,7 +2,6 @@
 // work decomposition of context-parallel prefill, TMA tensor maps and the
 // kernel launches.  The library allocates no device memory.
 #include <cudaTypedefs.h>
-#include <nvtx3/nvToolsExt.h>
 
 #include <algorithm>
 #include <atomic>
@@ -10,11 +9,14 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <exception>
 #include <mutex>
 #include <vector>
 
+#include "host.cuh"
 #include "kernels.cuh"
 #include "slope.h"
+#include "slope_serving.h"
 
 using namespace slope;
 
@@ -29,11 +31,12 @@ constexpr uint64_t kDefaultWaitLimitNs = 2000000000ull;  // 2 s: far beyond any 
 
 // ---------------------------------------------------------------- argument checks
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 thread_local char g_last_error[256] = "";
 
-// Records the text of a failing CUDA call and returns SLOPE_ERR_CUDA.
+}  // namespace
+
+namespace slope {
+
 slope_status cuda_fail(const char* where, cudaError_t e) {
   std::snprintf(g_last_error, sizeof(g_last_error), "%s: %s (%s)", where, cudaGetErrorString(e),
                 cudaGetErrorName(e));
@@ -43,6 +46,10 @@ slope_status cuda_fail(const char* where) {
   std::snprintf(g_last_error, sizeof(g_last_error), "%s", where);
   return SLOPE_ERR_CUDA;
 }
+
+}  // namespace slope
+
+namespace {
 
 // bf16 [S, H, d] readable by TMA: innermost stride 1, other strides multiples of 8 elements.
 slope_status check_qkv(const slope_tensor* t) {
@@ -58,7 +65,10 @@ slope_status check_qkv(const slope_tensor* t) {
   return SLOPE_OK;
 }
 
-// [S, H, dv] output, fp32 (or bf16 when allowed); 16-byte vector stores.
+}  // namespace
+
+namespace slope {
+
 slope_status check_out(const slope_tensor* t, int64_t S, int64_t H, int64_t dv, bool allow_bf16) {
   if (t == nullptr) return SLOPE_ERR_NULL;
   if (t->dtype != SLOPE_F32 && !(allow_bf16 && t->dtype == SLOPE_BF16)) return SLOPE_ERR_DTYPE;
@@ -70,7 +80,6 @@ slope_status check_out(const slope_tensor* t, int64_t S, int64_t H, int64_t dv, 
   return SLOPE_OK;
 }
 
-// fp32 [H, S], any positive strides.
 slope_status check_lse(const slope_tensor* t, int64_t H, int64_t S) {
   if (t == nullptr) return SLOPE_ERR_NULL;
   if (t->dtype != SLOPE_F32) return SLOPE_ERR_DTYPE;
@@ -97,6 +106,10 @@ float resolve_scale(float scale, int64_t dqk) {
   return scale > 0.f ? scale : static_cast<float>(1.0 / std::sqrt(static_cast<double>(dqk)));
 }
 
+}  // namespace slope
+
+namespace {
+
 // ---------------------------------------------------------------- TMA tensor maps
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -114,14 +127,15 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 
 // 3-D view {d, H, S} of a bf16 [S, H, d] tensor; box = 64 columns x 1 head x 128 rows,
 // 128-byte swizzle (the layout the tcgen05 descriptors expect); out-of-range rows read 0.
-bool make_map(CUtensorMap* m, const slope_tensor* t) {
+// With packed heads (Q of packed sequences) the box is 2^pack_shift heads x 128 >> pack_shift rows.
+bool make_map(CUtensorMap* m, const slope_tensor* t, int pack_shift = 0) {
   auto enc = encode_fn();
   if (enc == nullptr) return false;
   std::memset(m, 0, sizeof(*m));
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(t->shape[2]), static_cast<cuuint64_t>(t->shape[1]),
                         static_cast<cuuint64_t>(t->shape[0])};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(t->stride[1]) * 2, static_cast<cuuint64_t>(t->stride[0]) * 2};
-  cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(kBlockN)};
+  cuuint32_t box[3] = {64, 1u << pack_shift, static_cast<cuuint32_t>(kBlockN) >> pack_shift};
   cuuint32_t estr[3] = {1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, t->data, dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -130,10 +144,10 @@ bool make_map(CUtensorMap* m, const slope_tensor* t) {
 
 // 3-D view {dv, H, rows} of an fp32 or bf16 output with row/head strides in elements;
 // box = 128 bytes of columns (32 fp32 or 64 bf16) x 1 head x 32 rows (one softmax warp's
-// rows), 128-byte swizzle, written by TMA stores from the attention kernel's epilogue.
+// rows; with packed heads 2^pack_shift heads x 32 >> pack_shift rows), 128-byte swizzle, written by TMA stores from the attention kernel's epilogue.
 // Returns false if the map cannot be built (the kernel then stores directly).
 bool make_out_map(CUtensorMap* m, void* base, bool bf16, int64_t rows, int64_t H, int64_t dv, int64_t srow,
-                  int64_t shead) {
+                  int64_t shead, int pack_shift = 0) {
   auto enc = encode_fn();
   if (enc == nullptr || rows <= 0 || rows > 0x7fffffffLL) return false;
   const cuuint64_t esize = bf16 ? 2 : 4;
@@ -141,7 +155,7 @@ bool make_out_map(CUtensorMap* m, void* base, bool bf16, int64_t rows, int64_t H
   std::memset(m, 0, sizeof(*m));
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(dv), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(rows)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(shead) * esize, static_cast<cuuint64_t>(srow) * esize};
-  cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / esize), 1, 32};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / esize), 1u << pack_shift, 32u >> pack_shift};
   cuuint32_t estr[3] = {1, 1, 1};
   return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides,
              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
@@ -483,12 +497,13 @@ cudaError_t record(Timing* tm, bool before, int kind, cudaStream_t stream) {
 // what this one writes.  Launches timed with events run the ordinary way.
 slope_status run_attention(const std::vector<WorkItem>& group, int dqk, int dv, const CUtensorMap& tq,
                            const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& to, AttnParams base,
-                           bool dependent, Timing* tm, cudaStream_t stream) {
+                           bool dependent, Timing* tm, cudaStream_t stream, bool packed = false) {
   base.n_items = static_cast<int32_t>(group.size());
   for (size_t i = 0; i < group.size(); ++i) base.items[i] = group[i];
   cudaError_t e;
   if ((e = record(tm, true, 0, stream)) != cudaSuccess) return cuda_fail("cudaEventRecord", e);
-  if ((e = launch_attn_partial(dqk, dv, tq, tk, tv, to, base, dependent && tm == nullptr, stream)) != cudaSuccess)
+  const auto launch = packed ? launch_attn_packed : launch_attn_partial;
+  if ((e = launch(dqk, dv, tq, tk, tv, to, base, dependent && tm == nullptr, stream)) != cudaSuccess)
     return cuda_fail("attention kernel launch", e);
   if ((e = record(tm, false, 0, stream)) != cudaSuccess) return cuda_fail("cudaEventRecord", e);
   return SLOPE_OK;
@@ -811,16 +826,6 @@ BufferSetEvents* buffer_set(int device, const void* key) {
 
 }  // namespace
 
-// One NVTX range around each public call that queues GPU work, named after the call, so that
-// Nsight tools group its launches (ncu --nvtx).  With no tool attached a push or pop is a check
-// of a function pointer.
-struct CallRange {
-  explicit CallRange(const char* name) { nvtxRangePushA(name); }
-  ~CallRange() { nvtxRangePop(); }
-  CallRange(const CallRange&) = delete;
-  CallRange& operator=(const CallRange&) = delete;
-};
-
 extern "C" {
 
 slope_status slope_attn_partial(const slope_tensor* q, const slope_tensor* k, const slope_tensor* v, int64_t q_off,
@@ -902,6 +907,89 @@ slope_status slope_attn_partial(const slope_tensor* q, const slope_tensor* k, co
   if (!base.out_tma) to = tq;  // never used
   return run_attention(groups[0], static_cast<int>(dqk), static_cast<int>(dv), tq, tk, tv, to, base, false, nullptr,
                        static_cast<cudaStream_t>(stream));
+}
+
+slope_status slope_attn_varlen(const slope_tensor* q, const slope_tensor* k, const slope_tensor* v,
+                               const int64_t* cu_seqlens, int64_t n_seqs, int causal, int64_t window, float scale,
+                               slope_tensor* out, slope_tensor* lse, void* stream) {
+  const CallRange range("slope_attn_varlen");
+  slope_status st;
+  if (q == nullptr || k == nullptr || v == nullptr) return SLOPE_ERR_NULL;
+  if (q->ndim != 3 || k->ndim != 3 || v->ndim != 3) return SLOPE_ERR_SHAPE;
+  const int64_t T = q->shape[0], Hq = q->shape[1], dqk = q->shape[2];
+  const int64_t Hkv = k->shape[1], dv = v->shape[2];
+  if ((st = check_qkv(q)) != SLOPE_OK || (st = check_qkv(k)) != SLOPE_OK || (st = check_qkv(v)) != SLOPE_OK) return st;
+  if (T >= kMaxPos || k->shape[0] != T || v->shape[0] != T || v->shape[1] != Hkv || k->shape[2] != dqk)
+    return SLOPE_ERR_SHAPE;
+  if (Hq % Hkv != 0) return SLOPE_ERR_SHAPE;
+  if (!attn_partial_supported(static_cast<int>(dqk), static_cast<int>(dv))) return SLOPE_ERR_UNSUPPORTED;
+  if (window < 0 || window > kMaxSeq) return SLOPE_ERR_SHAPE;
+  if ((st = check_out(out, T, Hq, dv, true)) != SLOPE_OK) return st;
+  if (out->dtype == SLOPE_BF16 && (out->stride[0] % 8 || out->stride[1] % 8 || !aligned(out->data, 16)))
+    return SLOPE_ERR_STRIDE;
+  if ((st = check_lse(lse, Hq, T)) != SLOPE_OK) return st;
+  if (n_seqs < 0 || (n_seqs > 0 && cu_seqlens == nullptr)) return n_seqs < 0 ? SLOPE_ERR_SHAPE : SLOPE_ERR_NULL;
+  int64_t at = 0;
+  for (int64_t s = 0; n_seqs > 0 && s <= n_seqs; ++s) {
+    if (cu_seqlens[s] < at || cu_seqlens[s] > T) return SLOPE_ERR_LAYOUT;
+    at = cu_seqlens[s];
+  }
+  if (n_seqs == 0 || cu_seqlens[0] == cu_seqlens[n_seqs]) return SLOPE_OK;
+
+  AttnParams base{};
+  base.Hq = static_cast<int32_t>(Hq);
+  base.group = static_cast<int32_t>(Hq / Hkv);
+  // As many heads of a KV group to a Q tile as a power of two allows: a tile of 128 (token, head)
+  // pairs then covers 128 / heads tokens, so short sequences fill their tiles.
+  while (base.pack_shift < 5 && base.group % (2 << base.pack_shift) == 0) ++base.pack_shift;
+  base.causal = causal ? 1 : 0;
+  base.window = static_cast<int32_t>(window);
+  base.write_empty_out = 1;
+  base.scale_log2 = resolve_scale(scale, dqk) * 1.44269504088896340736f;
+  base.out = static_cast<float*>(out->data);
+  base.out_srow = out->stride[0];
+  base.out_shead = out->stride[1];
+  base.out_bf16 = out->dtype == SLOPE_BF16 ? 1 : 0;
+  base.lse = static_cast<float*>(lse->data);
+  base.lse_srow = lse->stride[1];
+  base.lse_shead = lse->stride[0];
+  base.status = device_status_ptr();
+  base.wait_limit_ns = wait_limit_ns();
+  if (base.status == nullptr) return cuda_fail("device status word (cudaGetSymbolAddress)");
+  CUtensorMap tq, tk, tv, to;
+  if (!make_map(&tq, q, base.pack_shift) || !make_map(&tk, k) || !make_map(&tv, v))
+    return cuda_fail("cuTensorMapEncodeTiled");
+  base.out_tma = make_out_map(&to, out->data, base.out_bf16 != 0, T, Hq, dv, out->stride[0], out->stride[1],
+                              base.pack_shift)
+                     ? 1
+                     : 0;
+  if (!base.out_tma) to = tq;  // never used
+
+  // One item per sequence: its rows against its own rows as keys, at their row numbers as positions
+  // (the masks only take differences).
+  try {
+    std::vector<PItem> items;
+    items.reserve(static_cast<size_t>(n_seqs));
+    for (int64_t s = 0; s < n_seqs; ++s) {
+      const int64_t len = cu_seqlens[s + 1] - cu_seqlens[s];
+      if (len == 0) continue;
+      PItem it{};
+      it.q_row0 = cu_seqlens[s];
+      it.q_len = len;
+      it.n_kv = 1;
+      it.kv[0] = Range{cu_seqlens[s], len};
+      items.push_back(it);
+    }
+    std::vector<std::vector<WorkItem>> groups;
+    if (!pack_items(std::move(items), causal, Hq, false, groups)) return SLOPE_ERR_UNSUPPORTED;
+    for (size_t g = 0; g < groups.size(); ++g)
+      if ((st = run_attention(groups[g], static_cast<int>(dqk), static_cast<int>(dv), tq, tk, tv, to, base, g > 0,
+                              nullptr, static_cast<cudaStream_t>(stream), true)) != SLOPE_OK)
+        return st;
+  } catch (const std::exception&) {  // out of host memory for the list of sequences
+    return SLOPE_ERR_UNSUPPORTED;
+  }
+  return SLOPE_OK;
 }
 
 slope_status slope_lse_merge(const slope_tensor* outs, const slope_tensor* lses, int n, slope_tensor* out,

@@ -249,12 +249,18 @@ struct Tile {
 
 // First row (within the item) and head of Q tile t of a work tile (QT Q tiles per CTA; with one,
 // a work tile is 128 rows of one head).
-template <int QT>
+// PK (packed heads): a Q tile is 128 >> pack_shift rows of 2^pack_shift query heads of one KV group,
+// its row r being token r >> pack_shift of head h + (r & (2^pack_shift - 1)); with two Q tiles the
+// second holds the tokens after the first's.
+template <int QT, bool PK>
 __device__ __forceinline__ int tile_row0(const AttnParams& p, const Tile& T, int t) {
+  if constexpr (PK) return (T.blk * QT + t) * (kBlockM >> p.pack_shift);
   if constexpr (QT == 1) return T.blk * kBlockM;
   return p.pair_heads ? T.blk * kBlockM : T.blk * kRowsPerCta + t * kBlockM;
 }
+template <bool PK>
 __device__ __forceinline__ int tile_head(const AttnParams& p, const Tile& T, int t) {
+  if constexpr (PK) return T.h;
   return p.pair_heads ? T.h + t : T.h;
 }
 
@@ -265,9 +271,9 @@ __device__ __forceinline__ int tile_head(const AttnParams& p, const Tile& T, int
 // tiles in increasing w, so the item index never decreases and the scan resumes there.
 // kGrouped: tiles run unit group by unit group (p.head_group units each); otherwise every
 // unit of an item is inner to its row blocks.
-template <bool kGrouped, int QT>
+template <bool kGrouped, int QT, bool PK>
 __device__ __forceinline__ void decode_tile(const AttnParams& p, const WorkItem* items, int w, Tile& T, int& ii) {
-  const int ushift = p.pair_heads;  // head units per item = h_count >> ushift
+  const int ushift = PK ? p.pack_shift : p.pair_heads;  // head units per item = h_count >> ushift
   while (ii < p.n_items - 1 && w >= items[ii].tile_begin + items[ii].n_blocks * (items[ii].h_count >> ushift)) ++ii;
   T.itm = items[ii];
   const int local = w - T.itm.tile_begin;
@@ -288,8 +294,8 @@ __device__ __forceinline__ void decode_tile(const AttnParams& p, const WorkItem*
   T.g = T.h / p.group;
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
-    const int r0 = tile_row0<QT>(p, T, t);
-    T.geo.rows[t] = max(0, min(kBlockM, T.itm.q_len - r0));
+    const int r0 = tile_row0<QT, PK>(p, T, t);
+    T.geo.rows[t] = max(0, min(PK ? kBlockM >> p.pack_shift : kBlockM, T.itm.q_len - r0));
     T.geo.qa[t] = p.q_pos_off + T.itm.q_row0 + r0;
     T.geo.qb[t] = T.geo.qa[t] + T.geo.rows[t] - 1;
   }
@@ -325,7 +331,7 @@ __device__ __forceinline__ void release_tiles(const AttnParams& p, int total) {
   }
 }
 
-template <int DQK, int DV, int QT>
+template <int DQK, int DV, int QT, bool PK>
 __global__ void __launch_bounds__(K1Cfg<DQK, DV, QT>::kThreads, K1Cfg<DQK, DV, QT>::kMinBlocks)
     attn_partial_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
@@ -474,7 +480,7 @@ __global__ void __launch_bounds__(K1Cfg<DQK, DV, QT>::kThreads, K1Cfg<DQK, DV, Q
           if (w < 0) break;
         }
         Tile T;
-        decode_tile<C::kGroupedTiles, C::kQTiles>(p, sItems, w, T, item_hint);
+        decode_tile<C::kGroupedTiles, C::kQTiles, PK>(p, sItems, w, T, item_hint);
         if (!has_steps<kQTiles>(T.itm, p, T.geo)) continue;
         // Q of the previous work tile is in use until its last S MMAs are done
         if (wt > 0 && !wait_bounded(bar_qempty, (wt - 1) & 1, cta_abort, p.status, limit, 11)) {
@@ -485,8 +491,8 @@ __global__ void __launch_bounds__(K1Cfg<DQK, DV, QT>::kThreads, K1Cfg<DQK, DV, Q
         mbar_arrive_expect_tx(bar_q, nq * C::kQTileBytes);
         for (int t = 0; t < nq; ++t)
           for (int c = 0; c < C::kQChunks; ++c)
-            tma_load_3d(sQ + t * C::kQTileBytes + c * kChunkBytes, &tm_q, bar_q, 64 * c, tile_head(p, T, t),
-                        T.itm.q_row0 + tile_row0<C::kQTiles>(p, T, t));
+            tma_load_3d(sQ + t * C::kQTileBytes + c * kChunkBytes, &tm_q, bar_q, 64 * c, tile_head<PK>(p, T, t),
+                        T.itm.q_row0 + tile_row0<C::kQTiles, PK>(p, T, t));
         ++wt;  // Q loads issued
         ok = for_each_step<kQTiles>(T.itm, p, T.geo, [&](const Step& s) -> bool {
           {  // K tile
@@ -598,7 +604,7 @@ __global__ void __launch_bounds__(K1Cfg<DQK, DV, QT>::kThreads, K1Cfg<DQK, DV, Q
           if (w < 0) break;
         }
         Tile T;
-        decode_tile<C::kGroupedTiles, C::kQTiles>(p, sItems, w, T, item_hint);
+        decode_tile<C::kGroupedTiles, C::kQTiles, PK>(p, sItems, w, T, item_hint);
         if (!has_steps<kQTiles>(T.itm, p, T.geo)) continue;
         if (!wait_bounded(bar_q, wt & 1, cta_abort, p.status, limit, 3)) {
           ok = false;
@@ -692,6 +698,7 @@ __global__ void __launch_bounds__(K1Cfg<DQK, DV, QT>::kThreads, K1Cfg<DQK, DV, Q
     };
     const float sl2 = p.scale_log2;
     int n = 0;  // steps (= PVs) of this Q tile over all work tiles
+    uint32_t cta_steps = 0;  // PK: steps of the CTA (of either Q tile) before this work tile
     bool ok = true;
     int item_hint = 0;
     int k = 0;
@@ -704,7 +711,7 @@ __global__ void __launch_bounds__(K1Cfg<DQK, DV, QT>::kThreads, K1Cfg<DQK, DV, Q
         if (w < 0) break;
       }
       Tile T;
-      decode_tile<C::kGroupedTiles, C::kQTiles>(p, sItems, w, T, item_hint);
+      decode_tile<C::kGroupedTiles, C::kQTiles, PK>(p, sItems, w, T, item_hint);
       const int rows_t = t == 0 ? T.geo.rows[0] : T.geo.rows[1];
       // turns of this work tile: the step count of the tile with more steps
       int n_turns = 0;
@@ -729,15 +736,23 @@ __global__ void __launch_bounds__(K1Cfg<DQK, DV, QT>::kThreads, K1Cfg<DQK, DV, Q
             if (ok) pass_turn();
           }
         }
+        if constexpr (PK) {  // this Q tile has no rows; the CTA's steps are the first one's
+          for (int r = 0; r < T.itm.n_kv; ++r) {
+            const TileRange R = tile_range(r == 0 ? T.itm.kv[0].row0 : T.itm.kv[1].row0,
+                                           r == 0 ? T.itm.kv[0].len : T.itm.kv[1].len, T.geo.qa[0], T.geo.qb[0], p);
+            cta_steps += static_cast<uint32_t>(max(0, R.hi - R.lo + 1));
+          }
+        }
         continue;
       }
-      const int q_pos = (t == 0 ? T.geo.qa[0] : T.geo.qa[1]) + row;
+      const int q_pos = (t == 0 ? T.geo.qa[0] : T.geo.qa[1]) + (PK ? row >> p.pack_shift : row);
       float m_used = -INFINITY;  // running max in log2-scaled units
       float l = 0.f;             // running sum of exp2(s*sl2 - m_used)
       int nl = 0;                // steps of this work tile
       const int qa_t = t == 0 ? T.geo.qa[0] : T.geo.qa[1];
       const int qb_t = qa_t + rows_t - 1;
-      auto step = [&](const bool full, const int kpos, const int valid) -> bool {
+      // cta_step (PK): the step's number among the CTA's, which tells its K/V slots
+      auto step = [&](const bool full, const int kpos, const int valid, const uint32_t cta_step) -> bool {
         if (!warp_all(wait_bounded(&bar_s[t], n & 1, cta_abort, p.status, limit, 8))) return false;
         tc_fence_after_sync();
         // S_t with the maximum of each 32-column quarter of the row (taken by the load)
@@ -854,6 +869,22 @@ __global__ void __launch_bounds__(K1Cfg<DQK, DV, QT>::kThreads, K1Cfg<DQK, DV, Q
         // O_t holds the previous PV's result here.  Separate P: the P store above waited for
         // that PV.  P inside S_t: the issuer sent S_t(n) only after PV(n-1) completed, and the
         // commit behind bar_s tracks every earlier MMA of that issuer.
+        if constexpr (PK) {
+          // The range ends inside this tile: the V rows after it belong to another sequence (or to
+          // none) and their weights are 0, but 0 times a NaN there would still be NaN.  Zero them in
+          // the slot before this Q tile's PV may read it (both Q tiles do, each before its own PV).
+          if (valid < kBlockN) {
+            const uint32_t vcnt = 2 * cta_step + 1;
+            const uint32_t vslot = vcnt % C::kSlots;
+            if (!warp_all(wait_bounded(&bar_full[vslot], (vcnt / C::kSlots) & 1, cta_abort, p.status, limit, 14)))
+              return false;
+            uint8_t* const sv0 = sSlot + vslot * C::kSlotBytes;
+            for (int c = 0; c < C::kVChunks; ++c)
+              for (int off = valid * 128 + row * 16; off < static_cast<int>(kChunkBytes); off += 128 * 16)
+                *reinterpret_cast<uint4*>(sv0 + c * kChunkBytes + off) = make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_shared();
+          }
+        }
         if (any_need && nl > 0) {
 #pragma unroll 1
           for (int c = 0; c < DV / 16; ++c) {
@@ -880,8 +911,24 @@ __global__ void __launch_bounds__(K1Cfg<DQK, DV, QT>::kThreads, K1Cfg<DQK, DV, Q
       for (int r = 0; r < sit.n_kv && ok; ++r) {
         const KvRange kr = sit.kv[r];
         const TileRange R = tile_range(kr.row0, kr.len, qa_t, qb_t, p);
-        for (int j = R.lo; j <= R.hi && ok; ++j)
-          ok = step(j >= R.flo && j <= R.fhi, R.kpos0 + j * kBlockN, min(kBlockN, R.len - j * kBlockN));
+        // PK: both Q tiles' ranges of key tiles make one without a gap, which the CTA steps through
+        int lo_cta = R.lo;
+        if constexpr (PK) {
+          int hi_cta = R.hi;
+          if (kQTiles == 2 && T.geo.rows[1] > 0) {
+            const int qa_o = t == 0 ? T.geo.qa[1] : T.geo.qa[0];
+            const TileRange O = tile_range(kr.row0, kr.len, qa_o, t == 0 ? T.geo.qb[1] : T.geo.qb[0], p);
+            lo_cta = min(lo_cta, O.lo);
+            hi_cta = max(hi_cta, O.hi);
+          }
+          for (int j = R.lo; j <= R.hi && ok; ++j)
+            ok = step(j >= R.flo && j <= R.fhi, R.kpos0 + j * kBlockN, min(kBlockN, R.len - j * kBlockN),
+                      cta_steps + static_cast<uint32_t>(j - lo_cta));
+          cta_steps += static_cast<uint32_t>(hi_cta - lo_cta + 1);
+        } else {
+          for (int j = R.lo; j <= R.hi && ok; ++j)
+            ok = step(j >= R.flo && j <= R.fhi, R.kpos0 + j * kBlockN, min(kBlockN, R.len - j * kBlockN), 0);
+        }
       }
       // the other tile's extra steps: pass the turns before this tile's epilogue
       if constexpr (C::kTurns) {
@@ -895,9 +942,10 @@ __global__ void __launch_bounds__(K1Cfg<DQK, DV, QT>::kThreads, K1Cfg<DQK, DV, Q
       // ---- epilogue: out = O / l, lse = ln(sum exp(scaled scores))
       // What does not depend on O (the row's 1/l, its lse, the output address) is done before
       // the wait for the tile's last PV.
-      const bool valid_row = row < rows_t;
-      const int head = tile_head(p, T, t);
-      const int64_t orow = static_cast<int64_t>(sit.out_row0) + tile_row0<C::kQTiles>(p, T, t) + row;
+      const bool valid_row = (PK ? row >> p.pack_shift : row) < rows_t;
+      const int head = tile_head<PK>(p, T, t) + (PK ? row & ((1 << p.pack_shift) - 1) : 0);
+      const int64_t orow =
+          static_cast<int64_t>(sit.out_row0) + tile_row0<C::kQTiles, PK>(p, T, t) + (PK ? row >> p.pack_shift : row);
       const int64_t plane = sit.plane;
       if (valid_row) {
         p.lse[plane * p.lse_splane + orow * p.lse_srow + static_cast<int64_t>(head) * p.lse_shead] =
@@ -1084,11 +1132,11 @@ int gcd_int(int a, int b) {
 int tile_head_group(const AttnParams& p, long long grid, bool dynamic_tiles) {
   int common = 0, max_blocks = 1;
   for (int i = 0; i < p.n_items; ++i) {
-    common = gcd_int(common, p.items[i].h_count >> p.pair_heads);
+    common = gcd_int(common, p.items[i].h_count >> (p.pair_heads + p.pack_shift));
     max_blocks = std::max(max_blocks, static_cast<int>(p.items[i].n_blocks));
   }
   if (common <= 0) return 1;
-  if (p.group >= 4) return common;
+  if ((p.group >> p.pack_shift) >= 4) return common;
   if (dynamic_tiles) return 1;
   const long long want = (grid + max_blocks - 1) / max_blocks;
   for (int hg = 1; hg < common; ++hg)
@@ -1096,23 +1144,25 @@ int tile_head_group(const AttnParams& p, long long grid, bool dynamic_tiles) {
   return common;
 }
 
-template <int DQK, int DV, int QT = 2>
+template <int DQK, int DV, int QT = 2, bool PK = false>
 cudaError_t launch_impl(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& to,
                         AttnParams p, bool dependent, cudaStream_t stream) {
   using C = K1Cfg<DQK, DV, QT>;
   if (p.n_items <= 0) return cudaSuccess;
   long long tiles;
-  if constexpr (QT == 1) {
+  if constexpr (QT == 1 || PK) {
     // one Q tile per CTA: work tiles of 128 rows of one head, counted here (the plan counts
-    // them for two Q tiles)
+    // them for two Q tiles); packed heads: QT tiles of 128 >> pack_shift rows of 2^pack_shift heads
     p.pair_heads = 0;
+    const int rows = PK ? QT * (kBlockM >> p.pack_shift) : kBlockM;
+    const int unit_shift = PK ? p.pack_shift : 0;
     tiles = 0;
     for (int i = 0; i < p.n_items; ++i) {
       WorkItem& it = p.items[i];
-      it.n_blocks = (it.q_len + kBlockM - 1) / kBlockM;
+      it.n_blocks = (it.q_len + rows - 1) / rows;
       if (tiles > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
       it.tile_begin = static_cast<int32_t>(tiles);
-      tiles += static_cast<long long>(it.n_blocks) * it.h_count;
+      tiles += static_cast<long long>(it.n_blocks) * (it.h_count >> unit_shift);
     }
   } else {
     const WorkItem& last = p.items[p.n_items - 1];
@@ -1128,11 +1178,11 @@ cudaError_t launch_impl(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
     p.tile_counter = claim_tile_counter();
     if (p.tile_counter == nullptr) return cudaErrorInvalidDevice;
   }
-  cudaError_t e = cudaFuncSetAttribute(attn_partial_kernel<DQK, DV, QT>,
+  cudaError_t e = cudaFuncSetAttribute(attn_partial_kernel<DQK, DV, QT, PK>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
   if constexpr (QT == 1) {  // the whole shared-memory carve-out, so that two CTAs fit on an SM
-    e = cudaFuncSetAttribute(attn_partial_kernel<DQK, DV, QT>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    e = cudaFuncSetAttribute(attn_partial_kernel<DQK, DV, QT, PK>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
@@ -1145,7 +1195,7 @@ cudaError_t launch_impl(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = dependent ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, attn_partial_kernel<DQK, DV, QT>, tq, tk, tv, to, p);
+  return cudaLaunchKernelEx(&cfg, attn_partial_kernel<DQK, DV, QT, PK>, tq, tk, tv, to, p);
 }
 
 }  // namespace
@@ -1177,6 +1227,21 @@ cudaError_t launch_attn_partial(int dqk, int dv, const CUtensorMap& tq, const CU
   if (dqk == 128 && dv == 128) return launch_impl<128, 128>(tq, tk, tv, to, p, dependent, stream);
   if (dqk == 192 && dv == 64) return launch_impl<192, 64>(tq, tk, tv, to, p, dependent, stream);
   if (dqk == 192 && dv == 128) return launch_impl<192, 128>(tq, tk, tv, to, p, dependent, stream);
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_attn_packed(int dqk, int dv, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                               const CUtensorMap& to, const AttnParams& p, bool dependent, cudaStream_t stream) {
+  if (dqk == 64 && dv == 64) {
+    if (p.window > 0 && p.window <= kTwoTileMaxWindow)
+      return launch_impl<64, 64, 2, true>(tq, tk, tv, to, p, dependent, stream);
+    return launch_impl<64, 64, 1, true>(tq, tk, tv, to, p, dependent, stream);
+  }
+  if (dqk == 64 && dv == 128) return launch_impl<64, 128, 2, true>(tq, tk, tv, to, p, dependent, stream);
+  if (dqk == 128 && dv == 64) return launch_impl<128, 64, 2, true>(tq, tk, tv, to, p, dependent, stream);
+  if (dqk == 128 && dv == 128) return launch_impl<128, 128, 2, true>(tq, tk, tv, to, p, dependent, stream);
+  if (dqk == 192 && dv == 64) return launch_impl<192, 64, 2, true>(tq, tk, tv, to, p, dependent, stream);
+  if (dqk == 192 && dv == 128) return launch_impl<192, 128, 2, true>(tq, tk, tv, to, p, dependent, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -51,6 +51,8 @@ struct AttnParams {
                             // per item); set by the launcher
   int32_t pair_heads;       // 1: a work tile's two Q tiles are two heads of one KV group on the same
                             // 128 rows (needs an even Hq / Hkv); 0: 256 consecutive rows of one head
+  int32_t pack_shift;       // packed launches: a Q tile is 128 >> pack_shift rows of 2^pack_shift heads of
+                            // one KV group (0 .. 5); else 0
   int32_t Hq;
   int32_t group;            // Hq / Hkv
   int32_t causal;
@@ -113,6 +115,11 @@ constexpr int kStatusTimeout = 1;
 cudaError_t launch_attn_partial(int dqk, int dv, const CUtensorMap& tq, const CUtensorMap& tk,
                                 const CUtensorMap& tv, const CUtensorMap& to, const AttnParams& p, bool dependent,
                                 cudaStream_t stream);
+// The same over packed sequences: AttnParams::pack_shift heads share a Q tile (the Q and O tensor maps
+// have boxes to match), and keys after the end of an item's range reach no row, whatever V holds there.
+cudaError_t launch_attn_packed(int dqk, int dv, const CUtensorMap& tq, const CUtensorMap& tk,
+                               const CUtensorMap& tv, const CUtensorMap& to, const AttnParams& p, bool dependent,
+                               cudaStream_t stream);
 bool attn_partial_supported(int dqk, int dv);
 cudaError_t launch_lse_merge(const MergeParams& p, cudaStream_t stream);
 cudaError_t launch_lse_fill(const FillParams& p, cudaStream_t stream);

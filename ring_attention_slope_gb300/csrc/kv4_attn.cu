@@ -1,0 +1,768 @@
+// Attention of each sequence's newest tokens over its pages of the 4-bit cache
+// (a decode step).
+//
+// For a query row with scaled scores x_j (log2 units) over the visible keys j:
+//   out = sum_j 2^(x_j - m) v_j / l,  l = sum_j 2^(x_j - m),  lse = (m + log2 l) ln 2,
+// where a cached channel is scale * code + min with one scale and min (bf16) for
+// each group G of 32 channels of a token's head.  The codes go to the tensor
+// cores as they are and the scales stay outside:
+//   q . k_j  = sum_G ( scale_jG * (sum_c q_c code_jc) + min_jG * (sum_c q_c) )
+//   sum_j w_j v_jc = sum_j (w_j scale_jG) code_jc + sum_j w_j min_jG
+// so a code costs a mask and half a shift, not a conversion.
+//
+// Codes as matrix operands.  A 4-bit code in the low bits of a 16-bit float is a
+// subnormal number, code * 2^-24 in fp16 and code * 2^-133 in bf16, which the
+// tensor cores multiply exactly.  Keys use fp16 (two code positions are
+// subnormals there, bits 0-3 and 4-7, so one shift serves eight codes): a query
+// row is scaled by a power of two to a largest value near 2^14, and its channels
+// that meet bits 4-7 by 1/16, both exact.  Values use bf16, because the other
+// operand, weight * scale, needs bf16's range (fp16's would flush it): the weight
+// carries a factor 2^64 so that products with 2^-133 stay normal fp32 numbers.
+// Its rounding to bf16 (2^-9 relative) is the one the attention kernel of the
+// prefill also makes on its weights.
+//
+// Keys are the M rows of S^T = K Q^T (16 keys x 8 query rows), values those of
+// O^T = V^T P^T (16 channels x 8 query rows): with the few query rows of a decode
+// step on the narrow side no multiply is wasted on padding at 8 heads per KV head.
+// The block layout in memory is the operand layout, so a lane's codes of 16 keys
+// are its own 16-byte words; P^T needs one 8x8 transpose (movmatrix) a group.
+//
+// Work split: every sequence's visible 16-token blocks, for each KV head (and each
+// tile of 8 NT query rows), laid end to end and cut into equal ranges, one for each
+// CTA of a grid that fills the GPU once.  The cut knows the lengths only on the
+// device, so ragged batches and captured graphs balance alike.  A range's pieces that
+// are not whole (sequence, head) pairs leave partials (m, l, unnormalised out) in the
+// workspace, and a second launch, queued as a programmatic dependent, joins them in a
+// fixed order.  Inside a CTA four warps take every fourth block, each with its own ring
+// of bulk copies, and join once at the end of a piece.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "host.cuh"
+#include "kernels.cuh"
+#include "kv4.cuh"
+#include "sm103_ptx.cuh"
+#include "waits.cuh"
+
+namespace slope {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kMaxCtas = 640;          // of the attention launch: the workspace has two partials for each
+constexpr int kMinBlocksPerCta = 8;    // a range is at least this many blocks
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kRescale = 8.f;        // the running maximum moves when a score passes it by this (log2)
+constexpr float kNoMax = -1e30f;       // running maximum before any key
+
+struct Kv4AttnParams {
+  const __nv_bfloat16* q;
+  int64_t q_srow, q_shead;
+  const uint8_t* data;
+  int64_t n_pages;
+  const int32_t* table;
+  int64_t table_stride;
+  int64_t max_tokens;  // max_pages * page_size
+  const int32_t* kv_lens;
+  int32_t B, q_len, Hkv, group;
+  int32_t blocks_per_page;
+  int32_t row_tiles;   // tiles of 8 NT of the q_len * group rows of a KV head
+  int32_t window;
+  float scale_log2;
+  void* out;
+  int64_t out_srow, out_shead;
+  int32_t out_bf16;
+  float* lse;  // may be null
+  int64_t lse_srow, lse_shead;
+  int4* heads;      // workspace: for each CTA, the pair it leaves unfinished {sequence or -1, pair, last CTA, -}
+  float* partials;  // workspace: two for each CTA, {m[R], l[R], out[R][DV]}
+  int* status;
+  uint64_t wait_limit_ns;
+};
+
+template <int DQK, int DV, int NT>
+struct Kv4Cfg {
+  static constexpr int R = 8 * NT;  // query rows of a tile
+  static constexpr int NG = DQK / 32, NV = DV / 32, NC = DV / 64, NW = NG + NV;
+  static constexpr int kKeyBytes = kv4_key_bytes(DQK), kValueBytes = kv4_value_bytes(DV);
+  static constexpr int kBlockBytes = kv4_block_bytes(DQK, DV);
+  // CTAs on an SM, by registers: 128 a thread at four, 255 at two
+  static constexpr int kCtas = (DQK == 64 && DV == 64) ? 4 : 2;
+  static constexpr int kStages = kCtas == 4 ? 6 : 5;
+  static constexpr int kRingBytes = kWarps * kStages * kBlockBytes;
+  static constexpr int kRedFloats = kWarps * R * DV + 2 * kWarps * R;
+  static constexpr int kSmemBytes = kRingBytes + kRedFloats * 4 + kWarps * kStages * 8 + 64;
+  static constexpr int kPartialFloats = 2 * R + R * DV;
+  static_assert(kCtas * (kSmemBytes + 1024) <= 232448 + 1024, "shared memory of the resident CTAs");
+};
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Transposes an 8x8 matrix of 16-bit elements held two to a lane (row lane / 4, columns 2 (lane % 4) and the next).
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// The keys of a sequence that some of its queries see, in 16-token blocks.
+struct SeqBlocks {
+  int len;    // tokens in the cache
+  int first;  // first block
+  int count;  // blocks, at least 1 (a sequence without keys still has rows to write)
+};
+__device__ __forceinline__ SeqBlocks seq_blocks(const Kv4AttnParams& p, int b) {
+  SeqBlocks s;
+  const int64_t n = p.kv_lens[b];
+  s.len = static_cast<int>(n < 0 ? 0 : n > p.max_tokens ? p.max_tokens : n);
+  s.first = p.window > 0 ? max(0, s.len - p.q_len - p.window + 1) / kKv4Block : 0;
+  s.count = max(1, (s.len + kKv4Block - 1) / kKv4Block - s.first);
+  return s;
+}
+
+// A CTA's range of units and the sequence it starts in.  A unit is one block of one (KV head, row tile).
+struct Range4 {
+  int64_t begin, end, per;
+  int64_t seq_begin;  // first unit of sequence b
+  int b;
+};
+
+// Every thread of the CTA calls it; `scratch` holds kWarps + 3 values.
+__device__ Range4 cta_range(const Kv4AttnParams& p, int64_t* scratch) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int pairs = p.Hkv * p.row_tiles;
+  int64_t total = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+    const int b = b0 + threadIdx.x;
+    if (b < p.B) total += static_cast<int64_t>(seq_blocks(p, b).count) * pairs;
+  }
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) total += __shfl_xor_sync(0xffffffffu, total, m);
+  if (lane == 0) scratch[warp] = total;
+  __syncthreads();
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) total += scratch[w];
+  Range4 r;
+  r.per = (total + gridDim.x - 1) / gridDim.x;
+  r.per = max(static_cast<int64_t>(kMinBlocksPerCta), (r.per + kWarps - 1) / kWarps * kWarps);
+  r.begin = min(total, static_cast<int64_t>(blockIdx.x) * r.per);
+  r.end = min(total, r.begin + r.per);
+  r.b = 0;
+  r.seq_begin = 0;
+  if (r.begin >= r.end) return r;
+  // the sequence that holds unit `begin`
+  int64_t carry = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+    const int b = b0 + threadIdx.x;
+    const int64_t mine = b < p.B ? static_cast<int64_t>(seq_blocks(p, b).count) * pairs : 0;
+    int64_t incl = mine;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const int64_t o = __shfl_up_sync(0xffffffffu, incl, m);
+      if (lane >= m) incl += o;
+    }
+    __syncthreads();
+    if (lane == 31) scratch[warp] = incl;
+    __syncthreads();
+    int64_t before = carry;
+    for (int w = 0; w < warp; ++w) before += scratch[w];
+    for (int w = 0; w < kWarps; ++w) carry += scratch[w];
+    incl += before;
+    if (mine > 0 && incl - mine <= r.begin && r.begin < incl) {
+      scratch[kWarps] = b;
+      scratch[kWarps + 1] = incl - mine;
+    }
+    if (carry > r.begin) break;  // the same for every thread
+  }
+  __syncthreads();
+  r.b = static_cast<int>(scratch[kWarps]);
+  r.seq_begin = scratch[kWarps + 1];
+  return r;
+}
+
+template <int DV, int R>
+__device__ __forceinline__ void store_row(const Kv4AttnParams& p, int b, int pair, int row, int ch, float4 o, float m,
+                                          float l) {
+  const int h = pair / p.row_tiles, r = (pair - h * p.row_tiles) * R + row;
+  if (r >= p.q_len * p.group) return;
+  const int64_t tok = static_cast<int64_t>(b) * p.q_len + r / p.group;
+  const int head = h * p.group + r % p.group;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int64_t at = tok * p.out_srow + head * p.out_shead + ch;
+  if (p.out_bf16)
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
+        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  else
+    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  if (ch == 0 && p.lse != nullptr)
+    p.lse[tok * p.lse_srow + head * p.lse_shead] = l == 0.f ? -INFINITY : (m + lg2_approx(l)) * kLn2;
+}
+
+template <int DQK, int DV, int NT>
+__global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
+    kv4_attn_kernel(const __grid_constant__ Kv4AttnParams p) {
+  using C = Kv4Cfg<DQK, DV, NT>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int64_t s_scratch[kWarps + 3];
+  __shared__ int s_abort;
+  float* const red = reinterpret_cast<float*>(smem + C::kRingBytes);  // [warp][row][channel]
+  float* const red_m = red + kWarps * C::R * DV;                      // [warp][row]
+  float* const red_l = red_m + kWarps * C::R;
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(red_l + kWarps * C::R);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, q4 = lane & 3;
+  uint8_t* const ring = smem + warp * C::kStages * C::kBlockBytes;
+  uint64_t* const full = bars + warp * C::kStages;
+
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) s_abort = 0;
+  if (lane == 0) {
+    for (int s = 0; s < C::kStages; ++s) mbar_init(&full[s], 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  const Range4 range = cta_range(p, s_scratch);
+  if (threadIdx.x == 0) p.heads[blockIdx.x] = make_int4(-1, 0, 0, 0);
+
+  uint32_t issued = 0, used = 0;  // bulk copies of this warp, over all pieces
+  int b = range.b;
+  int64_t seq_begin = range.seq_begin;
+  bool ok = true;
+  for (int64_t u = range.begin; u < range.end;) {
+    // ---- the piece: blocks [blk0, blk1) of one (sequence, KV head, row tile)
+    const SeqBlocks sb = seq_blocks(p, b);
+    const int pair = static_cast<int>((u - seq_begin) / sb.count);
+    const int64_t pair_begin = seq_begin + static_cast<int64_t>(pair) * sb.count, pair_end = pair_begin + sb.count;
+    const int64_t u_end = min(range.end, pair_end);
+    const int blk0 = sb.first + static_cast<int>(u - pair_begin), blk1 = blk0 + static_cast<int>(u_end - u);
+    const int kvh = pair / p.row_tiles, rt = pair - kvh * p.row_tiles;
+    const int n_it = max(0, (blk1 - blk0 - warp + kWarps - 1) / kWarps);
+
+    // ---- bulk copies: iteration i takes block blk0 + warp + 4 i; each lane holds the page of one of 32 iterations
+    const int32_t* const row = p.table + b * p.table_stride;
+    auto page_of = [&](int i) -> int {  // -1: no such block, or a page outside the cache
+      const int blk = blk0 + warp + kWarps * i;
+      if (i >= n_it || blk * kKv4Block >= sb.len) return -1;
+      const int pg = row[blk / p.blocks_per_page];
+      return pg >= 0 && pg < p.n_pages ? pg : -1;
+    };
+    int pages = page_of(lane), next_pages = page_of(32 + lane);
+    uint32_t held = 0;  // bit i % 32: iteration i has a block
+    int sent = 0;
+    auto send = [&]() {
+      if (sent >= n_it || !ok) return;
+      if (sent > 0 && (sent & 31) == 0) {
+        pages = next_pages;
+        next_pages = page_of(sent + 32 + lane);
+      }
+      const int pg = __shfl_sync(0xffffffffu, pages, sent & 31);
+      const uint32_t bit = 1u << (sent & 31);
+      held = pg >= 0 ? held | bit : held & ~bit;
+      if (pg >= 0) {
+        if (lane == 0) {
+          const int blk = blk0 + warp + kWarps * sent;
+          const int64_t at =
+              (static_cast<int64_t>(pg) * p.Hkv + kvh) * p.blocks_per_page + blk % p.blocks_per_page;
+          uint64_t* const bar = &full[issued % C::kStages];
+          mbar_arrive_expect_tx(bar, C::kBlockBytes);
+          bulk_load(ring + (issued % C::kStages) * C::kBlockBytes, p.data + at * C::kBlockBytes, C::kBlockBytes, bar);
+        }
+        ++issued;
+      }
+      ++sent;
+    };
+    for (int i = 0; i < C::kStages - 1; ++i) send();
+
+    // ---- queries as matrix operands
+    uint32_t qb[NT][C::NG][4];
+    float qsum[NT][C::NG][2];  // of rows 2 q4 and 2 q4 + 1, in the units of the products
+    float sl2[NT][2];
+    int hi[NT][2];             // last position those rows see
+    const int n_rows = p.q_len * p.group;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int r = rt * C::R + t * 8 + g;
+      uint4 w[C::NG];
+      float top = 0.f;
+#pragma unroll
+      for (int G = 0; G < C::NG; ++G) {
+        w[G] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < n_rows)
+          w[G] = *reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(b) * p.q_len + r / p.group) * p.q_srow +
+                                                 (kvh * p.group + r % p.group) * p.q_shead + 32 * G + 8 * q4);
+        const uint32_t x[4] = {w[G].x, w[G].y, w[G].z, w[G].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          top = fmaxf(top, fmaxf(fabsf(__uint_as_float(x[i] << 16)), fabsf(__uint_as_float(x[i] & 0xffff0000u))));
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // 2^k brings the row's largest value to [2^13, 2^14); a row of zeros, or one that is not finite, stays
+      const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+      const int k = (top > 0.f && e < 128) ? min(13 - e, 120) : 0;
+      const float up = __uint_as_float(static_cast<uint32_t>(max(k + 127, 1)) << 23);
+      float sums[C::NG];
+#pragma unroll
+      for (int G = 0; G < C::NG; ++G) {
+        const uint32_t x[4] = {w[G].x, w[G].y, w[G].z, w[G].w};
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[2 * i] = __uint_as_float(x[i] << 16) * up;
+          v[2 * i + 1] = __uint_as_float(x[i] & 0xffff0000u) * up;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // codes i and i + 4 share a word's 16-bit halves; odd i sit at bits 4-7
+          const float f = (i & 1) ? 0.0625f : 1.f;
+          qb[t][G][i] = pack_f16x2(v[i] * f, v[i + 4] * f);
+        }
+        float s = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+        s += __shfl_xor_sync(0xffffffffu, s, 1);
+        s += __shfl_xor_sync(0xffffffffu, s, 2);
+        sums[G] = s * 0x1p-24f;
+      }
+      const float unit = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(min(24 - k + 127, 254)) << 23);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int from = (2 * q4 + j) * 4;
+#pragma unroll
+        for (int G = 0; G < C::NG; ++G) qsum[t][G][j] = __shfl_sync(0xffffffffu, sums[G], from);
+        sl2[t][j] = __shfl_sync(0xffffffffu, unit, from);
+        const int rj = rt * C::R + t * 8 + 2 * q4 + j;
+        hi[t][j] = sb.len - p.q_len + min(rj / p.group, p.q_len - 1);
+      }
+    }
+    const int low_hi = sb.len - p.q_len;                                              // smallest hi of any row
+    const int high_lo = p.window > 0 ? sb.len - p.window : 0;                         // largest first position
+
+    // ---- the blocks
+    float m[NT][2], l[NT][2], bias[NT][C::NV][2], o[C::NC][2][2][NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        m[t][j] = kNoMax;
+        l[t][j] = 0.f;
+#pragma unroll
+        for (int G = 0; G < C::NV; ++G) bias[t][G][j] = 0.f;
+      }
+#pragma unroll
+      for (int c = 0; c < C::NC; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[c][i >> 1][i & 1][t][e] = 0.f;
+    }
+    for (int it = 0; it < n_it; ++it) {
+      // refill first: the stage it takes was read in the last iteration
+      __syncwarp();
+      send();
+      if (!((held >> (it & 31)) & 1u)) continue;
+      const uint32_t stage = used % C::kStages, parity = (used / C::kStages) & 1u;
+      ++used;
+      ok = ok && wait_bounded(&full[stage], parity, &s_abort, p.status, p.wait_limit_ns, 20);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      const uint8_t* const blk_mem = ring + stage * C::kBlockBytes;
+      uint32_t kw[2 * C::NG];  // [token g, g + 8][group]
+#pragma unroll
+      for (int i = 0; i < C::NG / 2; ++i) {
+        const uint4 r = *reinterpret_cast<const uint4*>(blk_mem + (i * 32 + lane) * 16);
+        kw[4 * i] = r.x, kw[4 * i + 1] = r.y, kw[4 * i + 2] = r.z, kw[4 * i + 3] = r.w;
+      }
+      uint32_t words[2][C::NW];  // scale and min of tokens g and g + 8
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint8_t* wp = blk_mem + C::kKeyBytes + C::kValueBytes + (g + 8 * i) * 4 * C::NW;
+        if constexpr (C::NW % 4 == 0) {
+#pragma unroll
+          for (int j = 0; j < C::NW / 4; ++j) {
+            const uint4 r = *reinterpret_cast<const uint4*>(wp + 16 * j);
+            words[i][4 * j] = r.x, words[i][4 * j + 1] = r.y, words[i][4 * j + 2] = r.z, words[i][4 * j + 3] = r.w;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < C::NW / 2; ++j) {
+            const uint2 r = *reinterpret_cast<const uint2*>(wp + 8 * j);
+            words[i][2 * j] = r.x, words[i][2 * j + 1] = r.y;
+          }
+        }
+      }
+      // scores of keys g (elements 0, 1) and g + 8 (2, 3) for rows 2 q4 and 2 q4 + 1
+      float x[NT][4];
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[t][e] = 0.f;
+#pragma unroll
+      for (int G = 0; G < C::NG; ++G) {
+        const uint32_t w0 = kw[G], w1 = kw[C::NG + G], v0 = w0 >> 8, v1 = w1 >> 8;
+        float acc[NT][4];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
+          mma_f16(acc[t], w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u, qb[t][G][0],
+                  qb[t][G][1]);
+          mma_f16(acc[t], v0 & 0x000f000fu, v1 & 0x000f000fu, v0 & 0x00f000f0u, v1 & 0x00f000f0u, qb[t][G][2],
+                  qb[t][G][3]);
+        }
+        const float s0 = __uint_as_float(words[0][G] & 0xffff0000u), s1 = __uint_as_float(words[1][G] & 0xffff0000u);
+        const float n0 = __uint_as_float(words[0][G] << 16), n1 = __uint_as_float(words[1][G] << 16);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          x[t][0] = fmaf(n0, qsum[t][G][0], fmaf(s0, acc[t][0], x[t][0]));
+          x[t][1] = fmaf(n0, qsum[t][G][1], fmaf(s0, acc[t][1], x[t][1]));
+          x[t][2] = fmaf(n1, qsum[t][G][0], fmaf(s1, acc[t][2], x[t][2]));
+          x[t][3] = fmaf(n1, qsum[t][G][1], fmaf(s1, acc[t][3], x[t][3]));
+        }
+      }
+      const int pos0 = (blk0 + warp + kWarps * it) * kKv4Block;
+      const bool edge = pos0 + kKv4Block - 1 > low_hi || pos0 < high_lo;
+      if (edge) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int pos = pos0 + g + 8 * (e >> 1), last = hi[t][e & 1];
+            if (pos > last || (p.window > 0 && last - pos >= p.window)) x[t][e] = -INFINITY;
+          }
+      }
+      // a row whose score passes the running maximum by 2^8 moves it (any other weight stays below 2^8)
+      bool need = false;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) need |= fmaf(x[t][e], sl2[t][e & 1], -m[t][e & 1]) > kRescale;
+      if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float top = fmaxf(x[t][j], x[t][2 + j]) * sl2[t][j];
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+            const float now = fmaxf(m[t][j], top), alpha = ex2_approx(m[t][j] - now);
+            m[t][j] = now;
+            l[t][j] *= alpha;
+#pragma unroll
+            for (int G = 0; G < C::NV; ++G) bias[t][G][j] *= alpha;
+#pragma unroll
+            for (int c = 0; c < C::NC; ++c)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                o[c][i >> 1][i & 1][t][j] *= alpha;
+                o[c][i >> 1][i & 1][t][2 + j] *= alpha;
+              }
+          }
+      }
+      // weights times 2^64, and their operands for each group of values
+      uint32_t pb[NT][C::NV][2];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = ex2_approx(fmaf(x[t][e], sl2[t][e & 1], 64.f - m[t][e & 1]));
+        l[t][0] += w[0] + w[2];
+        l[t][1] += w[1] + w[3];
+#pragma unroll
+        for (int G = 0; G < C::NV; ++G) {
+          const uint32_t c0 = words[0][C::NG + G], c1 = words[1][C::NG + G];
+          const float s0 = __uint_as_float(c0 & 0xffff0000u), s1 = __uint_as_float(c1 & 0xffff0000u);
+          const float n0 = __uint_as_float(c0 << 16), n1 = __uint_as_float(c1 << 16);
+          float ws[4] = {w[0] * s0, w[1] * s0, w[2] * s1, w[3] * s1};
+          if (edge) {
+            // a hidden key's scale may be anything, NaN too
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (x[t][e] == -INFINITY) ws[e] = 0.f;
+            bias[t][G][0] += (x[t][0] == -INFINITY ? 0.f : w[0] * n0) + (x[t][2] == -INFINITY ? 0.f : w[2] * n1);
+            bias[t][G][1] += (x[t][1] == -INFINITY ? 0.f : w[1] * n0) + (x[t][3] == -INFINITY ? 0.f : w[3] * n1);
+          } else {
+            bias[t][G][0] = fmaf(w[0], n0, fmaf(w[2], n1, bias[t][G][0]));
+            bias[t][G][1] = fmaf(w[1], n0, fmaf(w[3], n1, bias[t][G][1]));
+          }
+          pb[t][G][0] = transpose8x8(pack_bf16x2(ws[0], ws[1]));
+          pb[t][G][1] = transpose8x8(pack_bf16x2(ws[2], ws[3]));
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < C::NC; ++c) {
+        const uint4 r = *reinterpret_cast<const uint4*>(blk_mem + C::kKeyBytes + (c * 32 + lane) * 16);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {  // the chunk's two groups
+          const uint32_t z0 = __byte_perm(r.x, r.y, h ? 0x7632 : 0x5410), z1 = __byte_perm(r.z, r.w, h ? 0x7632 : 0x5410);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t a0 = (z0 >> (8 * i)) & 0x000f000fu, a1 = (z0 >> (8 * i + 4)) & 0x000f000fu;
+            const uint32_t a2 = (z1 >> (8 * i)) & 0x000f000fu, a3 = (z1 >> (8 * i + 4)) & 0x000f000fu;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) mma_bf16(o[c][h][i][t], a0, a1, a2, a3, pb[t][2 * c + h][0], pb[t][2 * c + h][1]);
+          }
+        }
+      }
+    }
+
+    // ---- join the warps: l and bias over the lanes that hold other keys, then everything over the warps
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int s = 4; s < 32; s <<= 1) {
+          l[t][j] += __shfl_xor_sync(0xffffffffu, l[t][j], s);
+#pragma unroll
+          for (int G = 0; G < C::NV; ++G) bias[t][G][j] += __shfl_xor_sync(0xffffffffu, bias[t][G][j], s);
+        }
+        const int rr = t * 8 + 2 * q4 + j;
+        if (g == 0) {
+          red_m[warp * C::R + rr] = m[t][j];
+          red_l[warp * C::R + rr] = l[t][j] * 0x1p-64f;
+        }
+#pragma unroll
+        for (int c = 0; c < C::NC; ++c)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float bs = bias[t][2 * c + h][j] * 0x1p-64f;
+            *reinterpret_cast<float4*>(red + (warp * C::R + rr) * DV + 64 * c + 32 * h + 4 * g) =
+                make_float4(fmaf(o[c][h][0][t][j], 0x1p69f, bs), fmaf(o[c][h][0][t][2 + j], 0x1p69f, bs),
+                            fmaf(o[c][h][1][t][j], 0x1p69f, bs), fmaf(o[c][h][1][t][2 + j], 0x1p69f, bs));
+          }
+      }
+    __syncthreads();
+    const bool whole = u == pair_begin && u_end == pair_end;
+    float* const part =
+        p.partials + (static_cast<int64_t>(blockIdx.x) * 2 + (u == pair_begin ? 1 : 0)) * C::kPartialFloats;
+    for (int i = threadIdx.x; i < C::R * DV / 4; i += kThreads) {
+      const int rr = i / (DV / 4), ch = (i % (DV / 4)) * 4;
+      float mm = kNoMax;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, red_m[w * C::R + rr]);
+      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+      float ll = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = ex2_approx(red_m[w * C::R + rr] - mm);
+        const float4 v = *reinterpret_cast<const float4*>(red + (w * C::R + rr) * DV + ch);
+        ll = fmaf(f, red_l[w * C::R + rr], ll);
+        sum.x = fmaf(f, v.x, sum.x), sum.y = fmaf(f, v.y, sum.y);
+        sum.z = fmaf(f, v.z, sum.z), sum.w = fmaf(f, v.w, sum.w);
+      }
+      if (whole) {
+        store_row<DV, C::R>(p, b, pair, rr, ch, sum, mm, ll);
+      } else {
+        *reinterpret_cast<float4*>(part + 2 * C::R + rr * DV + ch) = sum;
+        if (ch == 0) {
+          part[rr] = mm;
+          part[C::R + rr] = ll;
+        }
+      }
+    }
+    if (threadIdx.x == 0 && !whole && u == pair_begin)  // begun here, finished in a later CTA's range
+      p.heads[blockIdx.x] = make_int4(b, pair, static_cast<int>((pair_end - 1) / range.per), 0);
+    __syncthreads();
+    u = u_end;
+    if (u_end == pair_end && pair == p.Hkv * p.row_tiles - 1) {
+      seq_begin = pair_end;
+      ++b;
+    }
+  }
+  if (!ok) {
+    // the copies still in flight land before the CTA gives its shared memory back
+    for (uint32_t i = used; i < issued; ++i) wait_final(&full[i % C::kStages], (i / C::kStages) & 1u, p.wait_limit_ns);
+  }
+}
+
+// Joins the partials of a pair that several CTAs share: CTA c takes the one that CTA c of the
+// attention launch began and did not finish.  Fixed order, so the same result every time.
+template <int DV, int R>
+__global__ void __launch_bounds__(kThreads) kv4_join_kernel(const __grid_constant__ Kv4AttnParams p) {
+  pdl_wait();
+  const int4 head = p.heads[blockIdx.x];
+  if (head.x < 0) return;
+  constexpr int kFloats = 2 * R + R * DV;
+  const int first = blockIdx.x, n = head.z - first + 1;
+  // the first CTA's partial is its second, the others' their first
+  auto part = [&](int i) { return p.partials + (static_cast<int64_t>(first + i) * 2 + (i == 0 ? 1 : 0)) * kFloats; };
+  for (int i = threadIdx.x; i < R * DV / 4; i += kThreads) {
+    const int rr = i / (DV / 4), ch = (i % (DV / 4)) * 4;
+    float mm = kNoMax;
+    for (int c = 0; c < n; ++c) mm = fmaxf(mm, part(c)[rr]);
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    float ll = 0.f;
+    for (int c = 0; c < n; ++c) {
+      const float f = ex2_approx(part(c)[rr] - mm);
+      const float4 v = *reinterpret_cast<const float4*>(part(c) + 2 * R + rr * DV + ch);
+      ll = fmaf(f, part(c)[R + rr], ll);
+      sum.x = fmaf(f, v.x, sum.x), sum.y = fmaf(f, v.y, sum.y);
+      sum.z = fmaf(f, v.z, sum.z), sum.w = fmaf(f, v.w, sum.w);
+    }
+    store_row<DV, R>(p, head.x, head.y, rr, ch, sum, mm, ll);
+  }
+}
+
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
+    return 1;
+  return sms;
+}
+
+template <int DQK, int DV, int NT>
+cudaError_t launch_nt(Kv4AttnParams p, cudaStream_t stream) {
+  using C = Kv4Cfg<DQK, DV, NT>;
+  p.row_tiles = (p.q_len * p.group + C::R - 1) / C::R;
+  cudaError_t e = cudaFuncSetAttribute(kv4_attn_kernel<DQK, DV, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       C::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(kv4_attn_kernel<DQK, DV, NT>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+  if (e != cudaSuccess) return e;
+  const int grid = std::min(kMaxCtas, sm_count() * C::kCtas);
+  kv4_attn_kernel<DQK, DV, NT><<<grid, kThreads, C::kSmemBytes, stream>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv4_join_kernel<DV, C::R>, p);
+}
+
+// One tile of 8 rows while they suffice, else 16: a block's codes are unpacked once for all of them.
+template <int DQK, int DV>
+cudaError_t launch_d(const Kv4AttnParams& p, cudaStream_t stream) {
+  if (p.q_len * p.group <= 8) return launch_nt<DQK, DV, 1>(p, stream);
+  return launch_nt<DQK, DV, 2>(p, stream);
+}
+
+cudaError_t launch_kv4_attn(const Kv4AttnParams& p, int dqk, int dv, cudaStream_t stream) {
+  if (dqk == 64 && dv == 64) return launch_d<64, 64>(p, stream);
+  if (dqk == 64 && dv == 128) return launch_d<64, 128>(p, stream);
+  if (dqk == 128 && dv == 64) return launch_d<128, 64>(p, stream);
+  if (dqk == 128 && dv == 128) return launch_d<128, 128>(p, stream);
+  if (dqk == 192 && dv == 64) return launch_d<192, 64>(p, stream);
+  if (dqk == 192 && dv == 128) return launch_d<192, 128>(p, stream);
+  return cudaErrorInvalidValue;
+}
+
+constexpr size_t kHeadBytes = (kMaxCtas * sizeof(int4) + 255) / 256 * 256;
+
+size_t workspace_bytes_for(int64_t rows, int dv) {
+  const int64_t R = rows <= 8 ? 8 : 16;
+  return kHeadBytes + static_cast<size_t>(kMaxCtas) * 2 * (2 * R + R * dv) * sizeof(float);
+}
+
+}  // namespace
+}  // namespace slope
+
+using namespace slope;
+
+extern "C" {
+
+size_t slope_kv4_attn_workspace_size(int64_t B, int64_t Hq, const slope_kv4_cache* cache, int32_t q_len) {
+  if (cache == nullptr || !kv4_supported(cache->dqk, cache->dv)) return 0;
+  if (B < 0 || B > 65535 || cache->Hkv < 1 || Hq < 1 || Hq > 65535 || Hq % cache->Hkv != 0) return 0;
+  if (q_len < 1 || q_len > SLOPE_KV4_MAX_Q_LEN) return 0;
+  return workspace_bytes_for(Hq / cache->Hkv * q_len, cache->dv);
+}
+
+slope_status slope_kv4_attn(const slope_tensor* q, const slope_kv4_cache* cache, const int32_t* block_table,
+                            int64_t table_stride, int64_t max_pages, const int32_t* kv_lens, int32_t q_len,
+                            int64_t window, float scale, slope_tensor* out, slope_tensor* lse, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  const CallRange range("slope_kv4_attn");
+  slope_status st;
+  if ((st = check_kv4_cache(cache)) != SLOPE_OK) return st;
+  if (q == nullptr) return SLOPE_ERR_NULL;
+  if (q->dtype != SLOPE_BF16) return SLOPE_ERR_DTYPE;
+  if (q->ndim != 3) return SLOPE_ERR_SHAPE;
+  if (q_len < 1) return SLOPE_ERR_SHAPE;
+  if (q_len > SLOPE_KV4_MAX_Q_LEN) return SLOPE_ERR_UNSUPPORTED;
+  const int64_t T = q->shape[0], Hq = q->shape[1];
+  if (T < 0 || T % q_len != 0 || T / q_len > 65535) return SLOPE_ERR_SHAPE;
+  if (Hq < 1 || Hq > 65535 || Hq % cache->Hkv != 0 || q->shape[2] != cache->dqk) return SLOPE_ERR_SHAPE;
+  if (window < 0 || window > (int64_t(1) << 30)) return SLOPE_ERR_SHAPE;
+  if (max_pages < 0 || max_pages > ((int64_t(1) << 28) - 1) / cache->page_size || table_stride < max_pages)
+    return SLOPE_ERR_SHAPE;
+  if ((st = check_out(out, T, Hq, cache->dv, true)) != SLOPE_OK) return st;
+  if (lse != nullptr && (st = check_lse(lse, Hq, T)) != SLOPE_OK) return st;
+  if (T == 0) return SLOPE_OK;
+  if (q->data == nullptr || kv_lens == nullptr || (max_pages > 0 && block_table == nullptr)) return SLOPE_ERR_NULL;
+  if (q->stride[2] != 1 || q->stride[0] <= 0 || q->stride[1] <= 0 || q->stride[0] % 8 || q->stride[1] % 8 ||
+      !aligned(q->data, 16))
+    return SLOPE_ERR_STRIDE;
+  if (!aligned(kv_lens, 4) || !aligned(block_table, 4)) return SLOPE_ERR_STRIDE;
+  const int64_t rows = Hq / cache->Hkv * q_len;
+  if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < workspace_bytes_for(rows, cache->dv))
+    return SLOPE_ERR_WORKSPACE;
+
+  Kv4AttnParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(q->data);
+  p.q_srow = q->stride[0];
+  p.q_shead = q->stride[1];
+  p.data = static_cast<const uint8_t*>(cache->data);
+  p.n_pages = cache->n_pages;
+  p.table = block_table;
+  p.table_stride = table_stride;
+  p.max_tokens = max_pages * cache->page_size;
+  p.kv_lens = kv_lens;
+  p.B = static_cast<int32_t>(T / q_len);
+  p.q_len = q_len;
+  p.Hkv = cache->Hkv;
+  p.group = static_cast<int32_t>(Hq / cache->Hkv);
+  p.blocks_per_page = cache->page_size / kKv4Block;
+  p.window = static_cast<int32_t>(window);
+  p.scale_log2 = resolve_scale(scale, cache->dqk) * 1.44269504088896340736f;
+  p.out = out->data;
+  p.out_srow = out->stride[0];
+  p.out_shead = out->stride[1];
+  p.out_bf16 = out->dtype == SLOPE_BF16 ? 1 : 0;
+  if (lse != nullptr) {
+    p.lse = static_cast<float*>(lse->data);
+    p.lse_srow = lse->stride[1];
+    p.lse_shead = lse->stride[0];
+  }
+  p.heads = static_cast<int4*>(workspace);
+  p.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + kHeadBytes);
+  p.status = device_status_ptr();
+  if (p.status == nullptr) return cuda_fail("device status word (cudaGetSymbolAddress)");
+  p.wait_limit_ns = wait_limit_ns();
+  const cudaError_t e = launch_kv4_attn(p, cache->dqk, cache->dv, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SLOPE_OK : cuda_fail("cache attention kernel launch", e);
+}
+
+}  // extern "C"
