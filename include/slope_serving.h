@@ -147,7 +147,7 @@ SLOPE_API slope_status slope_attn_varlen(const slope_tensor* q, const slope_tens
  *     t % 2 + 2 * (t / 8), code c % 4 + 4 * (c % 64 / 32).
  *
  * dqk in {64, 128, 192}, dv in {64, 128} (else SLOPE_ERR_UNSUPPORTED); page_size a
- * multiple of 16, 16 .. 1024; n_pages * page_size < 2^31; Hkv <= 65535 (else
+ * power of two, 16 .. 1024; n_pages * page_size < 2^31; Hkv <= 65535 (else
  * SLOPE_ERR_SHAPE).  data is 16-byte aligned (else SLOPE_ERR_STRIDE).
  */
 typedef struct {

@@ -27,18 +27,19 @@
 // The block layout in memory is the operand layout, so a lane's codes of 16 keys
 // are its own 16-byte words; P^T needs one 8x8 transpose (movmatrix) a group.
 //
-// Work split: every sequence's visible 16-token blocks, for each KV head (and each
+// Work split: every sequence's visible 32-token steps, for each KV head (and each
 // tile of 8 NT query rows), laid end to end and cut into equal ranges, one for each
 // CTA of a grid that fills the GPU once.  The cut knows the lengths only on the
 // device, so ragged batches and captured graphs balance alike.  A range's pieces that
 // are not whole (sequence, head) pairs leave partials (m, l, unnormalised out) in the
 // workspace, and a second launch, queued as a programmatic dependent, joins them in a
-// fixed order.  Inside a CTA four warps take every fourth block, each with its own ring
-// of bulk copies, and join once at the end of a piece.
+// fixed order.  Inside a CTA four warps take every fourth step of 32 tokens, each with its
+// own ring of bulk copies, and join once at the end of a piece.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "host.cuh"
 #include "kernels.cuh"
@@ -52,7 +53,9 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxCtas = 640;          // of the attention launch: the workspace has two partials for each
-constexpr int kMinBlocksPerCta = 8;    // a range is at least this many blocks
+constexpr int kStep = 32;              // tokens of a step: two blocks, one bulk copy where a page holds both
+constexpr int kMinSteps = kWarps;      // a range is at least this many steps
+constexpr int kPieceSteps = 8;         // steps that a piece's start and end cost, at most (see cta_range)
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kRescale = 8.f;        // the running maximum moves when a score passes it by this (log2)
 constexpr float kNoMax = -1e30f;       // running maximum before any key
@@ -67,7 +70,7 @@ struct Kv4AttnParams {
   int64_t max_tokens;  // max_pages * page_size
   const int32_t* kv_lens;
   int32_t B, q_len, Hkv, group;
-  int32_t blocks_per_page;
+  int32_t page_shift;  // log2 of the page size
   int32_t row_tiles;   // tiles of 8 NT of the q_len * group rows of a KV head
   int32_t window;
   float scale_log2;
@@ -88,10 +91,11 @@ struct Kv4Cfg {
   static constexpr int NG = DQK / 32, NV = DV / 32, NC = DV / 64, NW = NG + NV;
   static constexpr int kKeyBytes = kv4_key_bytes(DQK), kValueBytes = kv4_value_bytes(DV);
   static constexpr int kBlockBytes = kv4_block_bytes(DQK, DV);
-  // CTAs on an SM, by registers: 128 a thread at four, 255 at two
-  static constexpr int kCtas = (DQK == 64 && DV == 64) ? 4 : 2;
-  static constexpr int kStages = kCtas == 4 ? 6 : 5;
-  static constexpr int kRingBytes = kWarps * kStages * kBlockBytes;
+  // CTAs on an SM, by registers: 128 a thread at four, 168 at three, 255 at two
+  static constexpr int kCtas = (DQK == 64 && DV == 64) ? (NT == 1 ? 4 : 3) : 2;
+  static constexpr int kStageBytes = 2 * kBlockBytes;
+  static constexpr int kStages = kCtas > 2 ? 4 : 3;
+  static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
   static constexpr int kRedFloats = kWarps * R * DV + 2 * kWarps * R;
   static constexpr int kSmemBytes = kRingBytes + kRedFloats * 4 + kWarps * kStages * 8 + 64;
   static constexpr int kPartialFloats = 2 * R + R * DV;
@@ -105,6 +109,14 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
+// d = a b (no accumulator in)
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
   asm volatile(
@@ -130,47 +142,57 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// The keys of a sequence that some of its queries see, in 16-token blocks.
-struct SeqBlocks {
+// The keys of a sequence that some of its queries see, in steps of 32 tokens.
+struct SeqSteps {
   int len;    // tokens in the cache
-  int first;  // first block
-  int count;  // blocks, at least 1 (a sequence without keys still has rows to write)
+  int first;  // first step
+  int count;  // steps, at least 1 (a sequence without keys still has rows to write)
 };
-__device__ __forceinline__ SeqBlocks seq_blocks(const Kv4AttnParams& p, int b) {
-  SeqBlocks s;
+__device__ __forceinline__ SeqSteps seq_steps(const Kv4AttnParams& p, int b) {
+  SeqSteps s;
   const int64_t n = p.kv_lens[b];
   s.len = static_cast<int>(n < 0 ? 0 : n > p.max_tokens ? p.max_tokens : n);
-  s.first = p.window > 0 ? max(0, s.len - p.q_len - p.window + 1) / kKv4Block : 0;
-  s.count = max(1, (s.len + kKv4Block - 1) / kKv4Block - s.first);
+  s.first = p.window > 0 ? max(0, s.len - p.q_len - p.window + 1) / kStep : 0;
+  s.count = max(1, (s.len + kStep - 1) / kStep - s.first);
   return s;
 }
 
-// A CTA's range of units and the sequence it starts in.  A unit is one block of one (KV head, row tile).
-struct Range4 {
+// A CTA's range of units and the sequence it starts in.  A pair is a (sequence, KV head, row tile); its
+// units are `cost` for starting and finishing it, then its steps.
+struct CtaRange {
   int64_t begin, end, per;
   int64_t seq_begin;  // first unit of sequence b
   int b;
+  int cost;
 };
 
 // Every thread of the CTA calls it; `scratch` holds kWarps + 3 values.
-__device__ Range4 cta_range(const Kv4AttnParams& p, int64_t* scratch) {
+//
+// A pair's fixed cost (its queries, its first copies' latency, the join of the warps) is worth about eight
+// steps.  Without it in the cut, a batch with many short sequences gave one CTA the tail of all of them:
+// 32 sequences of 8 .. 32768 tokens took 148 us.  Where a range has few steps in all, the cost is
+// taken as half of them, so that a small call still spreads over the CTAs.
+__device__ CtaRange cta_range(const Kv4AttnParams& p, int64_t* scratch) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int pairs = p.Hkv * p.row_tiles;
-  int64_t total = 0;
+  int64_t steps = 0;
   for (int b0 = 0; b0 < p.B; b0 += kThreads) {
     const int b = b0 + threadIdx.x;
-    if (b < p.B) total += static_cast<int64_t>(seq_blocks(p, b).count) * pairs;
+    if (b < p.B) steps += seq_steps(p, b).count;
   }
 #pragma unroll
-  for (int m = 16; m > 0; m >>= 1) total += __shfl_xor_sync(0xffffffffu, total, m);
-  if (lane == 0) scratch[warp] = total;
+  for (int m = 16; m > 0; m >>= 1) steps += __shfl_xor_sync(0xffffffffu, steps, m);
+  if (lane == 0) scratch[warp] = steps;
   __syncthreads();
-  total = 0;
+  steps = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) total += scratch[w];
-  Range4 r;
-  r.per = (total + gridDim.x - 1) / gridDim.x;
-  r.per = max(static_cast<int64_t>(kMinBlocksPerCta), (r.per + kWarps - 1) / kWarps * kWarps);
+  for (int w = 0; w < kWarps; ++w) steps += scratch[w];
+  steps *= pairs;
+  CtaRange r;
+  const int64_t even = (steps + gridDim.x - 1) / gridDim.x;
+  r.cost = static_cast<int>(min(static_cast<int64_t>(kPieceSteps), even / 2));
+  const int64_t total = steps + static_cast<int64_t>(p.B) * pairs * r.cost;
+  r.per = max(static_cast<int64_t>(kMinSteps), (total + gridDim.x - 1) / gridDim.x);
   r.begin = min(total, static_cast<int64_t>(blockIdx.x) * r.per);
   r.end = min(total, r.begin + r.per);
   r.b = 0;
@@ -180,7 +202,7 @@ __device__ Range4 cta_range(const Kv4AttnParams& p, int64_t* scratch) {
   int64_t carry = 0;
   for (int b0 = 0; b0 < p.B; b0 += kThreads) {
     const int b = b0 + threadIdx.x;
-    const int64_t mine = b < p.B ? static_cast<int64_t>(seq_blocks(p, b).count) * pairs : 0;
+    const int64_t mine = b < p.B ? static_cast<int64_t>(seq_steps(p, b).count + r.cost) * pairs : 0;
     int64_t incl = mine;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
@@ -237,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
   uint64_t* const bars = reinterpret_cast<uint64_t*>(red_l + kWarps * C::R);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, q4 = lane & 3;
-  uint8_t* const ring = smem + warp * C::kStages * C::kBlockBytes;
+  uint8_t* const ring = smem + warp * C::kStages * C::kStageBytes;
   uint64_t* const full = bars + warp * C::kStages;
 
   pdl_launch_dependents();
@@ -247,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
     fence_barrier_init();
   }
   __syncthreads();
-  const Range4 range = cta_range(p, s_scratch);
+  const CtaRange range = cta_range(p, s_scratch);
   if (threadIdx.x == 0) p.heads[blockIdx.x] = make_int4(-1, 0, 0, 0);
 
   uint32_t issued = 0, used = 0;  // bulk copies of this warp, over all pieces
@@ -255,46 +277,61 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
   int64_t seq_begin = range.seq_begin;
   bool ok = true;
   for (int64_t u = range.begin; u < range.end;) {
-    // ---- the piece: blocks [blk0, blk1) of one (sequence, KV head, row tile)
-    const SeqBlocks sb = seq_blocks(p, b);
-    const int pair = static_cast<int>((u - seq_begin) / sb.count);
-    const int64_t pair_begin = seq_begin + static_cast<int64_t>(pair) * sb.count, pair_end = pair_begin + sb.count;
+    // ---- the piece: steps [st0, st1) of one pair
+    const SeqSteps sb = seq_steps(p, b);
+    const int pair_units = sb.count + range.cost;
+    const int pair = static_cast<int>((u - seq_begin) / pair_units);
+    const int64_t pair_begin = seq_begin + static_cast<int64_t>(pair) * pair_units, pair_end = pair_begin + pair_units;
     const int64_t u_end = min(range.end, pair_end);
-    const int blk0 = sb.first + static_cast<int>(u - pair_begin), blk1 = blk0 + static_cast<int>(u_end - u);
+    const int st0 = sb.first + max(0, static_cast<int>(u - pair_begin) - range.cost);
+    const int st1 = sb.first + max(0, static_cast<int>(u_end - pair_begin) - range.cost);
     const int kvh = pair / p.row_tiles, rt = pair - kvh * p.row_tiles;
-    const int n_it = max(0, (blk1 - blk0 - warp + kWarps - 1) / kWarps);
+    const int n_it = max(0, (st1 - st0 - warp + kWarps - 1) / kWarps);
 
-    // ---- bulk copies: iteration i takes block blk0 + warp + 4 i; each lane holds the page of one of 32 iterations
+    // ---- bulk copies: iteration i takes step st0 + warp + 4 i.  Lane i % 32 looks its pages up, 32
+    // iterations at a time and those of the next 32 ahead, and starts its copies.
     const int32_t* const row = p.table + b * p.table_stride;
-    auto page_of = [&](int i) -> int {  // -1: no such block, or a page outside the cache
-      const int blk = blk0 + warp + kWarps * i;
-      if (i >= n_it || blk * kKv4Block >= sb.len) return -1;
-      const int pg = row[blk / p.blocks_per_page];
+    const bool small_pages = p.page_shift == 4;  // a step's two blocks lie in two pages
+    auto page_at = [&](int pos) -> int {  // -1: no such token, or a page outside the cache
+      if (pos >= sb.len) return -1;
+      const int pg = row[pos >> p.page_shift];
       return pg >= 0 && pg < p.n_pages ? pg : -1;
     };
-    int pages = page_of(lane), next_pages = page_of(32 + lane);
-    uint32_t held = 0;  // bit i % 32: iteration i has a block
+    auto pages_of = [&](int i, int& a, int& c) {
+      const int pos = (st0 + warp + kWarps * i) * kStep;
+      a = i < n_it ? page_at(pos) : -1;
+      c = !small_pages ? a : i < n_it ? page_at(pos + kKv4Block) : -1;
+    };
+    const uint8_t *src0 = nullptr, *src1 = nullptr;  // of the lane's iteration
+    uint32_t both = 0;                               // bit i % 32: iteration i has both blocks
+    int next0, next1;
+    auto refill = [&](int first) {  // the pages of iterations first .. first + 31 are in next0, next1
+      const int blk = (st0 + warp + kWarps * (first + lane)) * 2;
+      auto at = [&](int pg, int block) {
+        const int in_page = block & ((1 << (p.page_shift - 4)) - 1);
+        return p.data + (((static_cast<int64_t>(pg) * p.Hkv + kvh) << (p.page_shift - 4)) + in_page) * C::kBlockBytes;
+      };
+      src0 = next0 >= 0 ? at(next0, blk) : nullptr;
+      src1 = next1 >= 0 ? at(next1, blk + 1) : nullptr;
+      both = __ballot_sync(0xffffffffu, next0 >= 0 && next1 >= 0);
+      pages_of(first + 32 + lane, next0, next1);
+    };
+    pages_of(lane, next0, next1);
+    refill(0);
     int sent = 0;
     auto send = [&]() {
       if (sent >= n_it || !ok) return;
-      if (sent > 0 && (sent & 31) == 0) {
-        pages = next_pages;
-        next_pages = page_of(sent + 32 + lane);
+      if (sent > 0 && (sent & 31) == 0) refill(sent);
+      if (lane == (sent & 31)) {
+        uint64_t* const bar = &full[issued % C::kStages];
+        uint8_t* const dst = ring + (issued % C::kStages) * C::kStageBytes;
+        const uint32_t bytes0 = src0 == nullptr ? 0 : small_pages ? C::kBlockBytes : C::kStageBytes;
+        const uint32_t bytes1 = small_pages && src1 != nullptr ? C::kBlockBytes : 0;
+        mbar_arrive_expect_tx(bar, bytes0 + bytes1);
+        if (bytes0 != 0) bulk_load(dst, src0, bytes0, bar);
+        if (bytes1 != 0) bulk_load(dst + C::kBlockBytes, src1, bytes1, bar);
       }
-      const int pg = __shfl_sync(0xffffffffu, pages, sent & 31);
-      const uint32_t bit = 1u << (sent & 31);
-      held = pg >= 0 ? held | bit : held & ~bit;
-      if (pg >= 0) {
-        if (lane == 0) {
-          const int blk = blk0 + warp + kWarps * sent;
-          const int64_t at =
-              (static_cast<int64_t>(pg) * p.Hkv + kvh) * p.blocks_per_page + blk % p.blocks_per_page;
-          uint64_t* const bar = &full[issued % C::kStages];
-          mbar_arrive_expect_tx(bar, C::kBlockBytes);
-          bulk_load(ring + (issued % C::kStages) * C::kBlockBytes, p.data + at * C::kBlockBytes, C::kBlockBytes, bar);
-        }
-        ++issued;
-      }
+      ++issued;
       ++sent;
     };
     for (int i = 0; i < C::kStages - 1; ++i) send();
@@ -361,13 +398,13 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
     const int low_hi = sb.len - p.q_len;                                              // smallest hi of any row
     const int high_lo = p.window > 0 ? sb.len - p.window : 0;                         // largest first position
 
-    // ---- the blocks
-    float m[NT][2], l[NT][2], bias[NT][C::NV][2], o[C::NC][2][2][NT][4];
+    // ---- the steps
+    float nm[NT][2], l[NT][2], bias[NT][C::NV][2], o[C::NC][2][2][NT][4];  // nm: 64 - running maximum
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        m[t][j] = kNoMax;
+        nm[t][j] = 64.f - kNoMax;
         l[t][j] = 0.f;
 #pragma unroll
         for (int G = 0; G < C::NV; ++G) bias[t][G][j] = 0.f;
@@ -379,100 +416,93 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[c][i >> 1][i & 1][t][e] = 0.f;
     }
-    for (int it = 0; it < n_it; ++it) {
-      // refill first: the stage it takes was read in the last iteration
-      __syncwarp();
-      send();
-      if (!((held >> (it & 31)) & 1u)) continue;
-      const uint32_t stage = used % C::kStages, parity = (used / C::kStages) & 1u;
-      ++used;
-      ok = ok && wait_bounded(&full[stage], parity, &s_abort, p.status, p.wait_limit_ns, 20);
-      if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
-        break;
-      }
-      const uint8_t* const blk_mem = ring + stage * C::kBlockBytes;
-      uint32_t kw[2 * C::NG];  // [token g, g + 8][group]
+    // One step: its blocks in `mem`, tokens from position pos0 on.  kEdge: some row does not see some of its
+    // keys (bit j of `none`: block j is not there at all).
+    auto step = [&](auto edge_c, const uint8_t* const mem, const int pos0, const int none) {
+      constexpr bool kEdge = decltype(edge_c)::value;
+      // scores of keys g (elements 0, 1) and g + 8 (2, 3) of both blocks for rows 2 q4 and 2 q4 + 1
+      float x[2][NT][4];
 #pragma unroll
-      for (int i = 0; i < C::NG / 2; ++i) {
-        const uint4 r = *reinterpret_cast<const uint4*>(blk_mem + (i * 32 + lane) * 16);
-        kw[4 * i] = r.x, kw[4 * i + 1] = r.y, kw[4 * i + 2] = r.z, kw[4 * i + 3] = r.w;
-      }
-      uint32_t words[2][C::NW];  // scale and min of tokens g and g + 8
+      for (int j = 0; j < 2; ++j) {
+        const uint8_t* const blk_mem = mem + j * C::kBlockBytes;
+        uint32_t kw[2 * C::NG];  // [token g, g + 8][group]
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint8_t* wp = blk_mem + C::kKeyBytes + C::kValueBytes + (g + 8 * i) * 4 * C::NW;
-        if constexpr (C::NW % 4 == 0) {
+        for (int i = 0; i < C::NG / 2; ++i) {
+          const uint4 r = *reinterpret_cast<const uint4*>(blk_mem + (i * 32 + lane) * 16);
+          kw[4 * i] = r.x, kw[4 * i + 1] = r.y, kw[4 * i + 2] = r.z, kw[4 * i + 3] = r.w;
+        }
+        uint32_t word[2][C::NG];  // scale and min of tokens g and g + 8
 #pragma unroll
-          for (int j = 0; j < C::NW / 4; ++j) {
-            const uint4 r = *reinterpret_cast<const uint4*>(wp + 16 * j);
-            words[i][4 * j] = r.x, words[i][4 * j + 1] = r.y, words[i][4 * j + 2] = r.z, words[i][4 * j + 3] = r.w;
+        for (int i = 0; i < 2; ++i) {
+          const uint8_t* const wp = blk_mem + C::kKeyBytes + C::kValueBytes + (g + 8 * i) * 4 * C::NW;
+#pragma unroll
+          for (int h = 0; h < C::NG / 2; ++h) {
+            const uint2 r = *reinterpret_cast<const uint2*>(wp + 8 * h);
+            word[i][2 * h] = r.x, word[i][2 * h + 1] = r.y;
           }
-        } else {
+        }
 #pragma unroll
-          for (int j = 0; j < C::NW / 2; ++j) {
-            const uint2 r = *reinterpret_cast<const uint2*>(wp + 8 * j);
-            words[i][2 * j] = r.x, words[i][2 * j + 1] = r.y;
+        for (int G = 0; G < C::NG; ++G) {
+          const uint32_t w0 = kw[G], w1 = kw[C::NG + G], v0 = w0 >> 8, v1 = w1 >> 8;
+          const float s0 = __uint_as_float(word[0][G] & 0xffff0000u), s1 = __uint_as_float(word[1][G] & 0xffff0000u);
+          const float n0 = __uint_as_float(word[0][G] << 16), n1 = __uint_as_float(word[1][G] << 16);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            float acc[4];
+            mma_f16_first(acc, w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u, qb[t][G][0],
+                          qb[t][G][1]);
+            mma_f16(acc, v0 & 0x000f000fu, v1 & 0x000f000fu, v0 & 0x00f000f0u, v1 & 0x00f000f0u, qb[t][G][2],
+                    qb[t][G][3]);
+            float(&xx)[4] = x[j][t];
+            if (G == 0) {
+              xx[0] = fmaf(s0, acc[0], n0 * qsum[t][G][0]);
+              xx[1] = fmaf(s0, acc[1], n0 * qsum[t][G][1]);
+              xx[2] = fmaf(s1, acc[2], n1 * qsum[t][G][0]);
+              xx[3] = fmaf(s1, acc[3], n1 * qsum[t][G][1]);
+            } else {
+              xx[0] = fmaf(s0, acc[0], fmaf(n0, qsum[t][G][0], xx[0]));
+              xx[1] = fmaf(s0, acc[1], fmaf(n0, qsum[t][G][1], xx[1]));
+              xx[2] = fmaf(s1, acc[2], fmaf(n1, qsum[t][G][0], xx[2]));
+              xx[3] = fmaf(s1, acc[3], fmaf(n1, qsum[t][G][1], xx[3]));
+            }
           }
         }
       }
-      // scores of keys g (elements 0, 1) and g + 8 (2, 3) for rows 2 q4 and 2 q4 + 1
-      float x[NT][4];
+      if constexpr (kEdge) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[t][e] = 0.f;
+          for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int G = 0; G < C::NG; ++G) {
-        const uint32_t w0 = kw[G], w1 = kw[C::NG + G], v0 = w0 >> 8, v1 = w1 >> 8;
-        float acc[NT][4];
+            for (int e = 0; e < 4; ++e) {
+              const int pos = pos0 + j * kKv4Block + g + 8 * (e >> 1), last = hi[t][e & 1];
+              if ((none >> j & 1) || pos > last || (p.window > 0 && last - pos >= p.window)) x[j][t][e] = -INFINITY;
+            }
+      }
+      // y: log2 of the weight times 2^64.  A row whose score passes the running maximum by 2^8 moves it
+      // (any other weight stays below 2^8).
+      float w[2][NT][4];
+      float top = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
-          mma_f16(acc[t], w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u, qb[t][G][0],
-                  qb[t][G][1]);
-          mma_f16(acc[t], v0 & 0x000f000fu, v1 & 0x000f000fu, v0 & 0x00f000f0u, v1 & 0x00f000f0u, qb[t][G][2],
-                  qb[t][G][3]);
+          for (int e = 0; e < 4; ++e) w[j][t][e] = fmaf(x[j][t][e], sl2[t][e & 1], nm[t][e & 1]);
+          top = fmax3(top, fmaxf(w[j][t][0], w[j][t][1]), fmaxf(w[j][t][2], w[j][t][3]));
         }
-        const float s0 = __uint_as_float(words[0][G] & 0xffff0000u), s1 = __uint_as_float(words[1][G] & 0xffff0000u);
-        const float n0 = __uint_as_float(words[0][G] << 16), n1 = __uint_as_float(words[1][G] << 16);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          x[t][0] = fmaf(n0, qsum[t][G][0], fmaf(s0, acc[t][0], x[t][0]));
-          x[t][1] = fmaf(n0, qsum[t][G][1], fmaf(s0, acc[t][1], x[t][1]));
-          x[t][2] = fmaf(n1, qsum[t][G][0], fmaf(s1, acc[t][2], x[t][2]));
-          x[t][3] = fmaf(n1, qsum[t][G][1], fmaf(s1, acc[t][3], x[t][3]));
-        }
-      }
-      const int pos0 = (blk0 + warp + kWarps * it) * kKv4Block;
-      const bool edge = pos0 + kKv4Block - 1 > low_hi || pos0 < high_lo;
-      if (edge) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int pos = pos0 + g + 8 * (e >> 1), last = hi[t][e & 1];
-            if (pos > last || (p.window > 0 && last - pos >= p.window)) x[t][e] = -INFINITY;
-          }
-      }
-      // a row whose score passes the running maximum by 2^8 moves it (any other weight stays below 2^8)
-      bool need = false;
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) need |= fmaf(x[t][e], sl2[t][e & 1], -m[t][e & 1]) > kRescale;
-      if (__any_sync(0xffffffffu, need)) {
+      if (__any_sync(0xffffffffu, top > 64.f + kRescale)) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float top = fmaxf(x[t][j], x[t][2 + j]) * sl2[t][j];
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            const float now = fmaxf(m[t][j], top), alpha = ex2_approx(m[t][j] - now);
-            m[t][j] = now;
+            const float m = 64.f - nm[t][j];
+            float hi_x = fmaxf(fmaxf(x[0][t][j], x[0][t][2 + j]), fmaxf(x[1][t][j], x[1][t][2 + j])) * sl2[t][j];
+            hi_x = fmaxf(hi_x, __shfl_xor_sync(0xffffffffu, hi_x, 4));
+            hi_x = fmaxf(hi_x, __shfl_xor_sync(0xffffffffu, hi_x, 8));
+            hi_x = fmaxf(hi_x, __shfl_xor_sync(0xffffffffu, hi_x, 16));
+            nm[t][j] = 64.f - fmaxf(m, hi_x);
+            const float alpha = ex2_approx(m - (64.f - nm[t][j]));
             l[t][j] *= alpha;
 #pragma unroll
             for (int G = 0; G < C::NV; ++G) bias[t][G][j] *= alpha;
@@ -483,52 +513,90 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
                 o[c][i >> 1][i & 1][t][j] *= alpha;
                 o[c][i >> 1][i & 1][t][2 + j] *= alpha;
               }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              w[i][t][j] = fmaf(x[i][t][j], sl2[t][j], nm[t][j]);
+              w[i][t][2 + j] = fmaf(x[i][t][2 + j], sl2[t][j], nm[t][j]);
+            }
           }
       }
-      // weights times 2^64, and their operands for each group of values
-      uint32_t pb[NT][C::NV][2];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        float w[4];
+      for (int j = 0; j < 2; ++j) {
+        const uint8_t* const blk_mem = mem + j * C::kBlockBytes;
+        uint32_t word[2][C::NV];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = ex2_approx(fmaf(x[t][e], sl2[t][e & 1], 64.f - m[t][e & 1]));
-        l[t][0] += w[0] + w[2];
-        l[t][1] += w[1] + w[3];
+        for (int i = 0; i < 2; ++i) {
+          const uint8_t* const wp = blk_mem + C::kKeyBytes + C::kValueBytes + (g + 8 * i) * 4 * C::NW + 4 * C::NG;
 #pragma unroll
-        for (int G = 0; G < C::NV; ++G) {
-          const uint32_t c0 = words[0][C::NG + G], c1 = words[1][C::NG + G];
-          const float s0 = __uint_as_float(c0 & 0xffff0000u), s1 = __uint_as_float(c1 & 0xffff0000u);
-          const float n0 = __uint_as_float(c0 << 16), n1 = __uint_as_float(c1 << 16);
-          float ws[4] = {w[0] * s0, w[1] * s0, w[2] * s1, w[3] * s1};
-          if (edge) {
-            // a hidden key's scale may be anything, NaN too
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (x[t][e] == -INFINITY) ws[e] = 0.f;
-            bias[t][G][0] += (x[t][0] == -INFINITY ? 0.f : w[0] * n0) + (x[t][2] == -INFINITY ? 0.f : w[2] * n1);
-            bias[t][G][1] += (x[t][1] == -INFINITY ? 0.f : w[1] * n0) + (x[t][3] == -INFINITY ? 0.f : w[3] * n1);
-          } else {
-            bias[t][G][0] = fmaf(w[0], n0, fmaf(w[2], n1, bias[t][G][0]));
-            bias[t][G][1] = fmaf(w[1], n0, fmaf(w[3], n1, bias[t][G][1]));
+          for (int h = 0; h < C::NV / 2; ++h) {
+            const uint2 r = *reinterpret_cast<const uint2*>(wp + 8 * h);
+            word[i][2 * h] = r.x, word[i][2 * h + 1] = r.y;
           }
-          pb[t][G][0] = transpose8x8(pack_bf16x2(ws[0], ws[1]));
-          pb[t][G][1] = transpose8x8(pack_bf16x2(ws[2], ws[3]));
+        }
+        // the weights' operands for each group of values
+        uint32_t pb[NT][C::NV][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          float(&ww)[4] = w[j][t];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) ww[e] = ex2_approx(ww[e]);
+          l[t][0] += ww[0] + ww[2];
+          l[t][1] += ww[1] + ww[3];
+#pragma unroll
+          for (int G = 0; G < C::NV; ++G) {
+            float s[4], n[4];  // scale and min by element
+            s[0] = s[1] = __uint_as_float(word[0][G] & 0xffff0000u), s[2] = s[3] = __uint_as_float(word[1][G] & 0xffff0000u);
+            n[0] = n[1] = __uint_as_float(word[0][G] << 16), n[2] = n[3] = __uint_as_float(word[1][G] << 16);
+            if constexpr (kEdge) {  // a hidden key's scale and min may be anything, NaN too
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (x[j][t][e] == -INFINITY) s[e] = n[e] = 0.f;
+            }
+            bias[t][G][0] = fmaf(ww[0], n[0], fmaf(ww[2], n[2], bias[t][G][0]));
+            bias[t][G][1] = fmaf(ww[1], n[1], fmaf(ww[3], n[3], bias[t][G][1]));
+            pb[t][G][0] = transpose8x8(pack_bf16x2(ww[0] * s[0], ww[1] * s[1]));
+            pb[t][G][1] = transpose8x8(pack_bf16x2(ww[2] * s[2], ww[3] * s[3]));
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < C::NC; ++c) {
+          const uint4 r = *reinterpret_cast<const uint4*>(blk_mem + C::kKeyBytes + (c * 32 + lane) * 16);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // the chunk's two groups
+            const uint32_t z0 = __byte_perm(r.x, r.y, h ? 0x7632 : 0x5410), z1 = __byte_perm(r.z, r.w, h ? 0x7632 : 0x5410);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t a0 = (z0 >> (8 * i)) & 0x000f000fu, a1 = (z0 >> (8 * i + 4)) & 0x000f000fu;
+              const uint32_t a2 = (z1 >> (8 * i)) & 0x000f000fu, a3 = (z1 >> (8 * i + 4)) & 0x000f000fu;
+#pragma unroll
+              for (int t = 0; t < NT; ++t)
+                mma_bf16(o[c][h][i][t], a0, a1, a2, a3, pb[t][2 * c + h][0], pb[t][2 * c + h][1]);
+            }
+          }
         }
       }
-#pragma unroll
-      for (int c = 0; c < C::NC; ++c) {
-        const uint4 r = *reinterpret_cast<const uint4*>(blk_mem + C::kKeyBytes + (c * 32 + lane) * 16);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {  // the chunk's two groups
-          const uint32_t z0 = __byte_perm(r.x, r.y, h ? 0x7632 : 0x5410), z1 = __byte_perm(r.z, r.w, h ? 0x7632 : 0x5410);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t a0 = (z0 >> (8 * i)) & 0x000f000fu, a1 = (z0 >> (8 * i + 4)) & 0x000f000fu;
-            const uint32_t a2 = (z1 >> (8 * i)) & 0x000f000fu, a3 = (z1 >> (8 * i + 4)) & 0x000f000fu;
-#pragma unroll
-            for (int t = 0; t < NT; ++t) mma_bf16(o[c][h][i][t], a0, a1, a2, a3, pb[t][2 * c + h][0], pb[t][2 * c + h][1]);
-          }
-        }
+    };
+    uint32_t have = 0;  // `both` of this iteration's 32
+    for (int it = 0; it < n_it; ++it) {
+      if ((it & 31) == 0) have = both;  // sending is at most a few iterations ahead
+      // refill first: the stage it takes was read in the last iteration
+      __syncwarp();
+      send();
+      const uint32_t stage = used % C::kStages, parity = (used / C::kStages) & 1u;
+      ++used;
+      ok = ok && wait_bounded(&full[stage], parity, &s_abort, p.status, p.wait_limit_ns, 20);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      const uint8_t* const mem = ring + stage * C::kStageBytes;
+      const int pos0 = (st0 + warp + kWarps * it) * kStep;
+      if (pos0 + kStep - 1 <= low_hi && pos0 >= high_lo && (have >> (it & 31) & 1u)) {
+        step(std::false_type{}, mem, pos0, 0);
+      } else {
+        int pg0, pg1;
+        pages_of(it, pg0, pg1);
+        step(std::true_type{}, mem, pos0, (pg0 < 0 ? 1 : 0) | (pg1 < 0 ? 2 : 0));
       }
     }
 
@@ -545,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
         }
         const int rr = t * 8 + 2 * q4 + j;
         if (g == 0) {
-          red_m[warp * C::R + rr] = m[t][j];
+          red_m[warp * C::R + rr] = 64.f - nm[t][j];
           red_l[warp * C::R + rr] = l[t][j] * 0x1p-64f;
         }
 #pragma unroll
@@ -744,7 +812,8 @@ slope_status slope_kv4_attn(const slope_tensor* q, const slope_kv4_cache* cache,
   p.q_len = q_len;
   p.Hkv = cache->Hkv;
   p.group = static_cast<int32_t>(Hq / cache->Hkv);
-  p.blocks_per_page = cache->page_size / kKv4Block;
+  p.page_shift = 4;
+  while ((1 << p.page_shift) < cache->page_size) ++p.page_shift;
   p.window = static_cast<int32_t>(window);
   p.scale_log2 = resolve_scale(scale, cache->dqk) * 1.44269504088896340736f;
   p.out = out->data;

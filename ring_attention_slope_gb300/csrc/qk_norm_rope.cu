@@ -4,11 +4,10 @@
 //
 // Bandwidth-bound: every value is read once and written once.  Eight lanes
 // share a head, each with 16-byte loads of 8 channels (d / 64 of them), so a
-// warp's load instruction covers four heads' consecutive 128 bytes.  A CTA
-// takes a few tokens and first puts the sines and cosines of their angles in
-// shared memory, where all heads use them; the angles are the only arithmetic
-// that would show (two of them per pair of channels would cost more than the
-// memory pass).
+// warp's load instruction covers four heads' consecutive 128 bytes.  A warp takes
+// one token and runs over its heads: the weights and the token's sines and cosines
+// are then the same for every head of a lane, and stay in its registers as
+//   y_e = (x_e A_e + x_partner B_e) / rms,   A = w cos, B = -+ w_partner sin.
 //
 // Angles: position * inv_freq loses everything in fp32 at far positions (at
 // position 10^6 an fp32 angle is off by 0.06 radians).  The frequency is kept as
@@ -32,11 +31,11 @@
 namespace slope {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
 constexpr int kLanesPerHead = 8;
-constexpr int kRowsPerPass = kThreads / kLanesPerHead;  // heads a CTA takes at a time
-constexpr int kMaxHalf = 96;                            // rotated pairs of a head
-constexpr int kMaxTokens = 4;                           // tokens of a CTA
+constexpr int kHeadsPerPass = 32 / kLanesPerHead;  // heads a warp takes at a time
+constexpr int kMaxHalf = 96;                       // rotated pairs of a head
 
 struct NormRopeSide {
   const void* x;
@@ -55,153 +54,224 @@ struct NormRopeParams {
   float eps;
   int32_t norm, rotate, interleaved, begin, half;
   float factor;
-  int32_t tokens;  // of a CTA
-  int32_t heads;   // of a CTA (of side[0].H + side[1].H)
+  int32_t heads;   // of a warp (of side[0].H + side[1].H)
+  int32_t splits;  // warps of a token
   uint64_t turns[kMaxHalf];  // inv_freq / 2 pi modulo 1, times 2^64
 };
 
+// Eight channels as they lie in memory.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
-  if constexpr (sizeof(T) == 2) {
-    const uint4 r = *reinterpret_cast<const uint4*>(p);
-    const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+struct Raw8 {
+  uint4 r[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(u[i] << 16);
-      v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float4 r = *reinterpret_cast<const float4*>(p + 4 * i);
-      v[4 * i] = r.x, v[4 * i + 1] = r.y, v[4 * i + 2] = r.z, v[4 * i + 3] = r.w;
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) r[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+  // channels 2 i and 2 i + 1
+  __device__ __forceinline__ uint64_t pair(int i) const {
+    if constexpr (sizeof(T) == 2) {
+      const uint32_t u = (&r[0].x)[i];
+      return pack_f32x2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+    } else {
+      return pack_f32x2(__uint_as_float((&r[i / 2].x)[i % 2 * 2]), __uint_as_float((&r[i / 2].x)[i % 2 * 2 + 1]));
     }
   }
+};
+__device__ __forceinline__ uint64_t swapped(uint64_t v) {
+  const float2 f = unpack_f32x2(v);
+  return pack_f32x2(f.y, f.x);
 }
 
 template <typename T>
-__device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
+__device__ __forceinline__ void store8(T* p, const uint64_t (&v)[4]) {
+  const float2 a = unpack_f32x2(v[0]), b = unpack_f32x2(v[1]), c = unpack_f32x2(v[2]), d = unpack_f32x2(v[3]);
   if constexpr (sizeof(T) == 2) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                              pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(b.x, b.y), pack_bf16x2(c.x, c.y), pack_bf16x2(d.x, d.y));
   } else {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    *reinterpret_cast<float4*>(p) = make_float4(a.x, a.y, b.x, b.y);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(c.x, c.y, d.x, d.y);
   }
 }
 
 __device__ __forceinline__ float weight_at(const NormRopeSide& s, int64_t i) {
-  if (s.w == nullptr) return 1.f;
   return s.w_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(s.w)[i]) : static_cast<const float*>(s.w)[i];
 }
+__device__ __forceinline__ uint64_t weight_pair(const NormRopeSide& s, int64_t i) {
+  return pack_f32x2(weight_at(s, i), weight_at(s, i + 1));
+}
 
-template <typename TI, typename TO, int D>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
-  __shared__ __align__(16) float s_cos[kMaxTokens * kMaxHalf], s_sin[kMaxTokens * kMaxHalf];
-  __shared__ __align__(16) float s_w[2 * D];  // weights shared by every head of a side
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.tokens;
-  const int n_tok = static_cast<int>(min(static_cast<int64_t>(p.tokens), p.T - t0));
-  const int h0 = blockIdx.y * p.heads;
-  const int n_heads = min(p.heads, p.side[0].H + p.side[1].H - h0);
-
+// kInter: pairs are neighbours (and a pair's partner is in the same lane's channels), else halves.
+template <typename TI, typename TO, int D, bool kInter>
+__global__ void __launch_bounds__(kThreads, D == 64 ? 3 : 2)
+    qk_norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
+  __shared__ __align__(16) float s_cos[kWarps][kMaxHalf], s_sin[kWarps][kMaxHalf];  // of the warp's token
+  __shared__ __align__(16) float s_w[2][D];  // weights shared by every head of a side, else 1
+  constexpr int kChunks = D / 64;
+  // passes whose loads are in flight together
+  constexpr int kAhead = D == 64 && sizeof(TI) == 2 ? 2 : 1;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
     const NormRopeSide& s = p.side[i / D];
-    s_w[i] = s.w_shead == 0 ? weight_at(s, i % D) : 1.f;
+    s_w[i / D][i % D] = s.w != nullptr && s.w_shead == 0 ? weight_at(s, i % D) : 1.f;
   }
-  if (p.rotate) {
-    for (int i = threadIdx.x; i < n_tok * p.half; i += kThreads) {
-      const int tok = i / p.half, f = i - tok * p.half;
-      const int64_t pos = p.positions != nullptr ? p.positions[t0 + tok] : p.pos0 + t0 + tok;
+  const int64_t task = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  const int64_t tok = task / p.splits;
+  if (tok < p.T && p.rotate) {
+    const int64_t pos = p.positions != nullptr ? p.positions[tok] : p.pos0 + tok;
+    for (int f = lane; f < p.half; f += 32) {
       // the fraction of a turn, rounded to 32 bits and taken in [-1/2, 1/2)
       const uint64_t frac = p.turns[f] * static_cast<uint64_t>(pos) + 0x80000000ull;
-      const int32_t turn = static_cast<int32_t>(frac >> 32);
       float sn, cs;
-      sincospif(static_cast<float>(turn) * 0x1p-31f, &sn, &cs);
-      s_cos[tok * kMaxHalf + f] = cs * p.factor;
-      s_sin[tok * kMaxHalf + f] = sn * p.factor;
+      sincospif(static_cast<float>(static_cast<int32_t>(frac >> 32)) * 0x1p-31f, &sn, &cs);
+      s_cos[warp][f] = cs * p.factor;
+      s_sin[warp][f] = sn * p.factor;
     }
   }
   __syncthreads();
+  if (tok >= p.T) return;  // a whole warp
+  const int split = static_cast<int>(task - tok * p.splits);
+  const int first = split * p.heads, last = min(first + p.heads, p.side[0].H + p.side[1].H);
 
-  constexpr int kChunks = D / 64;
-  const int lane8 = threadIdx.x % kLanesPerHead;
-  const int n_rows = n_tok * n_heads;
-  // every thread runs every pass: the shuffles below need whole warps
-  for (int r0 = 0; r0 < n_rows; r0 += kRowsPerPass) {
-    const int r = r0 + threadIdx.x / kLanesPerHead;
-    const bool live = r < n_rows;
-    const int tok = live ? r / n_heads : 0;
-    const int hh = h0 + (live ? r - tok * n_heads : 0);
-    const int which = hh >= p.side[0].H ? 1 : 0;
+  const int lane8 = lane % kLanesPerHead, sub = lane / kLanesPerHead;
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
     const NormRopeSide& s = p.side[which];
-    const int h = which ? hh - p.side[0].H : hh;
-    const TI* x = static_cast<const TI*>(s.x) + (t0 + tok) * s.x_srow + h * s.x_shead;
-    float v[kChunks][8], o[kChunks][8];  // own channels, and their partners in the halves layout
-    int side_of[kChunks];                // 0 not rotated, 1 first half, 2 second half, 3 interleaved
-    float sq = 0.f;
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      const int e = c * 64 + lane8 * 8;
-      side_of[c] = 0;
-      if (live) {
-        load8(x + e, v[c]);
-        if (p.rotate && e >= p.begin && e < p.begin + 2 * p.half) {
-          side_of[c] = p.interleaved ? 3 : e < p.begin + p.half ? 1 : 2;
-          if (!p.interleaved) load8(x + (side_of[c] == 1 ? e + p.half : e - p.half), o[c]);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[c][i] = 0.f;
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sq = fmaf(v[c][i], v[c][i], sq);
-    }
-    float scale = 1.f;
-    if (p.norm) {
-#pragma unroll
-      for (int m = 1; m < kLanesPerHead; m <<= 1) sq += __shfl_xor_sync(0xffffffffu, sq, m);
-      scale = rsqrtf(sq * (1.f / D) + p.eps);
-    }
-    __syncwarp();  // in place: every lane has read what it needs of the head
-    if (!live) continue;
-    TO* y = static_cast<TO*>(s.y) + (t0 + tok) * s.y_srow + h * s.y_shead;
-    const float* sw = s_w + which * D;
+    const int base = which ? p.side[0].H : 0;
+    const int h_begin = max(first - base, 0), h_end = min(last - base, s.H);
+    if (h_begin >= h_end) continue;
     const bool per_head = s.w_shead != 0;
+    // the lane's factors a, b of its channels, and where the other halves lie (in elements; 0: not rotated)
+    uint64_t a[kChunks][4], b[kChunks][4];
+    int partner[kChunks];
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
-      const int e = c * 64 + lane8 * 8;
-      auto apply = [&](float (&a)[8], int at) {
+      const int e = c * 64 + lane8 * 8, off = e - p.begin;
+      const bool in = p.rotate && off >= 0 && off < 2 * p.half;
+      partner[c] = !in ? 0 : kInter ? 1 : off < p.half ? p.half : -p.half;
+      float fa[8], fb[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          a[i] *= scale * (per_head ? weight_at(s, h * s.w_shead + at + i) : sw[at + i]);
-      };
-      if (p.norm) apply(v[c], e);
-      if (side_of[c] == 1 || side_of[c] == 2) {
-        const int po = side_of[c] == 1 ? e + p.half : e - p.half;
-        if (p.norm) apply(o[c], po);
-        const int f0 = tok * kMaxHalf + (side_of[c] == 1 ? e : po) - p.begin;
-        const float sign = side_of[c] == 1 ? -1.f : 1.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[c][i] = fmaf(sign * o[c][i], s_sin[f0 + i], v[c][i] * s_cos[f0 + i]);
-      } else if (side_of[c] == 3) {
-        const int f0 = tok * kMaxHalf + (e - p.begin) / 2;
+      for (int i = 0; i < 8; i += 4) {
+        const float4 w = *reinterpret_cast<const float4*>(&s_w[which][e + i]);
+        fa[i] = w.x, fa[i + 1] = w.y, fa[i + 2] = w.z, fa[i + 3] = w.w;
+        fb[i] = fb[i + 1] = fb[i + 2] = fb[i + 3] = 0.f;
+      }
+      if (in && kInter) {
+        const float4 cs = *reinterpret_cast<const float4*>(&s_cos[warp][off / 2]);
+        const float4 sn = *reinterpret_cast<const float4*>(&s_sin[warp][off / 2]);
+        const float c4[4] = {cs.x, cs.y, cs.z, cs.w}, s4[4] = {sn.x, sn.y, sn.z, sn.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float a = v[c][2 * i], b = v[c][2 * i + 1];
-          v[c][2 * i] = fmaf(-b, s_sin[f0 + i], a * s_cos[f0 + i]);
-          v[c][2 * i + 1] = fmaf(a, s_sin[f0 + i], b * s_cos[f0 + i]);
+          fb[2 * i] = -fa[2 * i + 1] * s4[i];
+          fb[2 * i + 1] = fa[2 * i] * s4[i];
+          fa[2 * i] *= c4[i];
+          fa[2 * i + 1] *= c4[i];
+        }
+      } else if (in) {
+        const int f = off < p.half ? off : off - p.half;
+        const float sign = off < p.half ? -1.f : 1.f;
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+          const float4 cs = *reinterpret_cast<const float4*>(&s_cos[warp][f + i]);
+          const float4 sn = *reinterpret_cast<const float4*>(&s_sin[warp][f + i]);
+          const float4 w = *reinterpret_cast<const float4*>(&s_w[which][e + i + partner[c]]);
+          fb[i] = sign * sn.x * w.x, fb[i + 1] = sign * sn.y * w.y, fb[i + 2] = sign * sn.z * w.z, fb[i + 3] = sign * sn.w * w.w;
+          fa[i] *= cs.x, fa[i + 1] *= cs.y, fa[i + 2] *= cs.z, fa[i + 3] *= cs.w;
         }
       }
-      store8(y + e, v[c]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a[c][i] = pack_f32x2(fa[2 * i], fa[2 * i + 1]);
+        b[c][i] = pack_f32x2(fb[2 * i], fb[2 * i + 1]);
+      }
+    }
+    const TI* x = static_cast<const TI*>(s.x) + tok * s.x_srow + lane8 * 8;
+    TO* y = static_cast<TO*>(s.y) + tok * s.y_srow + lane8 * 8;
+    Raw8<TI> v[kAhead][kChunks], o[kAhead][kChunks];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) o[k][c] = Raw8<TI>{};
+#pragma unroll 1
+    for (int h0 = h_begin; h0 < h_end; h0 += kHeadsPerPass * kAhead) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        // past the last head: its values once more, which are not stored
+        const int h = min(h0 + k * kHeadsPerPass + sub, h_end - 1);
+        const TI* const xh = x + h * s.x_shead;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          v[k][c].load(xh + c * 64);
+          if (!kInter && partner[c] != 0) o[k][c].load(xh + c * 64 + partner[c]);
+        }
+      }
+      float scale[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        scale[k] = 1.f;
+        if (p.norm) {
+          uint64_t sq2 = 0;
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sq2 = fma_f32x2(v[k][c].pair(i), v[k][c].pair(i), sq2);
+          const float2 sq = unpack_f32x2(sq2);
+          float sum = sq.x + sq.y;
+#pragma unroll
+          for (int m = 1; m < kLanesPerHead; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+          scale[k] = rsqrtf(fmaf(sum, 1.f / D, p.eps));
+        }
+      }
+      __syncwarp();  // in place: every lane has read what it needs of these heads
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int h = h0 + k * kHeadsPerPass + sub;
+        if (h >= h_end) continue;
+        const uint64_t scale2 = pack_f32x2(scale[k], scale[k]);
+        TO* const yh = y + h * s.y_shead;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          uint64_t vv[4], oo[4], out[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            vv[i] = v[k][c].pair(i);
+            oo[i] = kInter ? swapped(vv[i]) : o[k][c].pair(i);
+          }
+          if (per_head) {
+            const int64_t wi = h * s.w_shead + c * 64 + lane8 * 8;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              vv[i] = mul_f32x2(vv[i], weight_pair(s, wi + 2 * i));
+              if (!kInter && partner[c] != 0) oo[i] = mul_f32x2(oo[i], weight_pair(s, wi + 2 * i + partner[c]));
+              if (kInter) oo[i] = swapped(vv[i]);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) out[i] = mul_f32x2(vv[i], a[c][i]);
+          if (!kInter || partner[c] != 0) {  // (halves that are not rotated have zeros for partners)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) out[i] = fma_f32x2(oo[i], b[c][i], out[i]);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) out[i] = mul_f32x2(out[i], scale2);
+          store8(yh + c * 64, out);
+        }
+      }
     }
   }
 }
 
 template <typename TI, typename TO>
 cudaError_t launch_d(const NormRopeParams& p, int d, dim3 grid, cudaStream_t stream) {
-  if (d == 64) qk_norm_rope_kernel<TI, TO, 64><<<grid, kThreads, 0, stream>>>(p);
-  if (d == 128) qk_norm_rope_kernel<TI, TO, 128><<<grid, kThreads, 0, stream>>>(p);
-  if (d == 192) qk_norm_rope_kernel<TI, TO, 192><<<grid, kThreads, 0, stream>>>(p);
+  if (d == 64)
+    p.interleaved ? qk_norm_rope_kernel<TI, TO, 64, true><<<grid, kThreads, 0, stream>>>(p)
+                  : qk_norm_rope_kernel<TI, TO, 64, false><<<grid, kThreads, 0, stream>>>(p);
+  else if (d == 128)
+    p.interleaved ? qk_norm_rope_kernel<TI, TO, 128, true><<<grid, kThreads, 0, stream>>>(p)
+                  : qk_norm_rope_kernel<TI, TO, 128, false><<<grid, kThreads, 0, stream>>>(p);
+  else
+    p.interleaved ? qk_norm_rope_kernel<TI, TO, 192, true><<<grid, kThreads, 0, stream>>>(p)
+                  : qk_norm_rope_kernel<TI, TO, 192, false><<<grid, kThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -315,14 +385,15 @@ extern "C" slope_status slope_qk_norm_rope(const slope_tensor* q, const slope_te
   p.eps = eps;
   p.norm = norm != 0 ? 1 : 0;
   const int64_t H = p.side[0].H + p.side[1].H;
-  // Few heads in all: one token and one pass of heads to a CTA, for the shortest call.  Else several
-  // tokens with all their heads, so that the angles and weights are fetched once for many passes.
-  const int64_t passes = (H + kRowsPerPass - 1) / kRowsPerPass;
-  const bool small = T * passes <= 1216;  // a wave of 8 CTAs on each of the 152 SMs
-  p.tokens = small ? 1 : kMaxTokens;
-  p.heads = small ? kRowsPerPass : static_cast<int32_t>(H);
-  const dim3 grid(static_cast<unsigned>((T + p.tokens - 1) / p.tokens),
-                  static_cast<unsigned>((H + p.heads - 1) / p.heads));
+  // A warp to a token once there are enough tokens to fill the GPU (about 32 warps on each of 152 SMs),
+  // else several warps, down to one pass of four heads each, for the shortest call.
+  const int64_t want = (H * T + 4863) / 4864;
+  p.heads = static_cast<int32_t>(std::min<int64_t>(
+      (H + kHeadsPerPass - 1) / kHeadsPerPass, (want + kHeadsPerPass - 1) / kHeadsPerPass) * kHeadsPerPass);
+  p.splits = static_cast<int32_t>((H + p.heads - 1) / p.heads);
+  const int64_t ctas = (T * p.splits + kWarps - 1) / kWarps;
+  if (ctas > 0x7fffffffLL) return SLOPE_ERR_SHAPE;
+  const dim3 grid(static_cast<unsigned>(ctas));
   auto s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (first->dtype == SLOPE_BF16)

@@ -8,7 +8,11 @@ from __future__ import annotations
 
 import ctypes
 
-from . import SlopeError, SlopeTensor, _check, _desc, _stream_ptr, _torch, load
+from array import array
+
+import torch
+
+from . import SlopeError, SlopeTensor, _check, load
 
 EXPORTED_SERVING = ["slope_rope_inv_freq", "slope_qk_norm_rope", "slope_attn_varlen", "slope_kv4_block_bytes",
                     "slope_kv4_cache_bytes", "slope_kv4_write", "slope_kv4_read", "slope_kv4_attn",
@@ -48,30 +52,53 @@ def declare(lib):
         fn.argtypes, fn.restype = args, res
 
 
-def _ref(d):
-    return ctypes.byref(d) if d is not None else None
+_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+# The smallest of these calls takes a few microseconds on the GPU, so its descriptors are made with as few
+# Python operations as they allow.
+
+def _desc(t):
+    """slope_tensor of a CUDA tensor of rank 2 or 3, or None for None."""
+    if t is None:
+        return None
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    shape, stride = t.shape, t.stride()
+    n = len(shape)
+    if n != 3 and n != 2:
+        raise ValueError("tensors must be rank 2 or 3")
+    if not t.is_cuda and t.numel() > 0:
+        raise TypeError("libslope operates on CUDA tensors")
+    return SlopeTensor(t.data_ptr(), dt, n, tuple(shape), stride)
 
 
 def _here(*tensors):
     """The tensors' device has to be the current one: the launch goes to the current device's stream."""
-    torch = _torch()
+    cur = torch.cuda.current_device() if torch.cuda.is_available() else -1
     for t in tensors:
-        if t is not None and t.is_cuda and t.device.index != torch.cuda.current_device():
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+        if t is not None and t.is_cuda and t.get_device() != cur:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{cur}")
+
+
+def _stream(stream):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _index(t, what, n=None):
     """Data pointer of a device int32 array (dense, of n elements)."""
-    torch = _torch()
     if t.dtype != torch.int32:
         raise TypeError(f"{what} must be int32, got {t.dtype}")
-    if t.numel() > 0 and t.device.type != "cuda":
+    if not t.is_cuda and t.numel() > 0:
         raise TypeError(f"{what} must be a CUDA tensor")
     if n is not None and (t.dim() != 1 or t.shape[0] != n):
         raise ValueError(f"{what} must have shape [{n}], got {tuple(t.shape)}")
-    if t.dim() == 1 and t.numel() > 1 and t.stride(0) != 1:
+    if n is not None and n > 1 and t.stride(0) != 1:
         raise ValueError(f"{what} must be contiguous")
-    return ctypes.c_void_p(t.data_ptr() if t.numel() > 0 else 0)
+    return t.data_ptr()
 
 
 # ---------------------------------------------------------------- positions
@@ -93,9 +120,10 @@ class Rope:
     pairs channels 2i and 2i + 1, else i and i + half; both cos and sin are multiplied by ``attention_factor``."""
 
     def __init__(self, inv_freq, *, begin=0, interleaved=False, attention_factor=1.0):
-        self._freq = (ctypes.c_double * max(1, len(inv_freq)))(*[float(f) for f in inv_freq])
-        self._c = SlopeRope(int(begin), 2 * len(inv_freq), int(bool(interleaved)), float(attention_factor),
-                            ctypes.cast(self._freq, ctypes.POINTER(ctypes.c_double)))
+        freq = array("d", inv_freq)
+        n = len(freq)
+        self._c = SlopeRope(int(begin), 2 * n, int(bool(interleaved)), float(attention_factor),
+                            (ctypes.c_double * n).from_buffer(freq) if n else None)
 
 
 def qk_norm_rope(q, k=None, *, norm=True, q_weight=None, k_weight=None, eps=1e-6, rope=None, positions=None, pos0=0,
@@ -106,19 +134,19 @@ def qk_norm_rope(q, k=None, *, norm=True, q_weight=None, k_weight=None, eps=1e-6
     ``norm=False`` rotates alone.  ``positions``: device int32 [T], or None for pos0, pos0 + 1, ...  The outputs
     (of the inputs' type unless given) may be the inputs.  Returns ``(q_out, k_out)`` (k_out None without k).
     """
-    torch = _torch()
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
     if k is not None and k_out is None:
         k_out = torch.empty(k.shape, dtype=out_dtype or k.dtype, device=k.device)
     _here(q, k, q_weight, k_weight, positions, q_out, k_out)
-    weights = [None if w is None else _desc(w.unsqueeze(0) if w.dim() == 1 else w) for w in (q_weight, k_weight)]
+    if q_weight is not None and q_weight.dim() == 1:
+        q_weight = q_weight[None]
+    if k_weight is not None and k_weight.dim() == 1:
+        k_weight = k_weight[None]
     pos = None if positions is None else _index(positions, "positions", q.shape[0])
-    dq, do = _desc(q), _desc(q_out)
-    dk, dko = (_desc(k), _desc(k_out)) if k is not None else (None, None)
-    st = load().slope_qk_norm_rope(_ref(dq), _ref(dk), _ref(weights[0]), _ref(weights[1]), int(bool(norm)), float(eps),
-                                   _ref(rope._c) if rope is not None else None, pos, int(pos0), _ref(do), _ref(dko),
-                                   _stream_ptr(stream))
+    st = load().slope_qk_norm_rope(_desc(q), _desc(k), _desc(q_weight), _desc(k_weight), 1 if norm else 0, eps,
+                                   None if rope is None else rope._c, pos, pos0, _desc(q_out), _desc(k_out),
+                                   _stream(stream))
     _check(st, "slope_qk_norm_rope")
     return q_out, k_out
 
@@ -133,23 +161,22 @@ def attn_varlen(q, k, v, cu_seqlens, *, causal=True, window=0, scale=0.0, out=No
     Returns ``(out, lse)``: out bf16 (default) or fp32 [T,Hq,dv], lse fp32 [Hq,T].  Rows outside the sequences
     are left as they were (uninitialised where the call allocates).
     """
-    torch = _torch()
     T, Hq, _ = q.shape
     if out is None:
         out = torch.empty((T, Hq, v.shape[2]), dtype=out_dtype or torch.bfloat16, device=q.device)
     if lse is None:
         lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
     _here(q, k, v, out, lse)
-    if hasattr(cu_seqlens, "tolist"):
-        if getattr(cu_seqlens, "is_cuda", False):
+    if isinstance(cu_seqlens, torch.Tensor):
+        if cu_seqlens.is_cuda:
             raise TypeError("cu_seqlens lives on the host (reading it back would synchronise)")
         cu_seqlens = cu_seqlens.tolist()
-    if len(cu_seqlens) < 1:
+    n = len(cu_seqlens)
+    if n < 1:
         raise ValueError("cu_seqlens needs at least one entry")
-    cu = (ctypes.c_int64 * len(cu_seqlens))(*[int(c) for c in cu_seqlens])
-    dq, dk, dvv, do, dl = _desc(q), _desc(k), _desc(v), _desc(out), _desc(lse)
-    st = load().slope_attn_varlen(_ref(dq), _ref(dk), _ref(dvv), cu, len(cu_seqlens) - 1, int(bool(causal)),
-                                  int(window), float(scale), _ref(do), _ref(dl), _stream_ptr(stream))
+    cu = (ctypes.c_int64 * n).from_buffer(array("q", cu_seqlens))
+    st = load().slope_attn_varlen(_desc(q), _desc(k), _desc(v), cu, n - 1, 1 if causal else 0, window, scale,
+                                  _desc(out), _desc(lse), _stream(stream))
     _check(st, "slope_attn_varlen")
     return out, lse
 
@@ -161,7 +188,6 @@ class KV4Cache:
     of dqk key and dv value channels.  ``data`` (uint8, CUDA, dense) is allocated unless given."""
 
     def __init__(self, n_pages, page_size, Hkv, dqk, dv, *, data=None, device="cuda"):
-        torch = _torch()
         nbytes = int(load().slope_kv4_cache_bytes(int(n_pages), int(page_size), int(Hkv), int(dqk), int(dv)))
         if nbytes == 0 and int(n_pages) != 0:
             raise SlopeError(-8, "slope_kv4_cache_bytes")
@@ -183,32 +209,28 @@ def kv4_write(cache, k, v, slots, *, stream=None):
     """Writes k [T,Hkv,dqk], v [T,Hkv,dv] (bf16 or fp32) into the cache at slots (device int32 [T]; slot = page *
     page_size + index, out of range: skipped; the others distinct)."""
     _here(cache.data, k, v, slots)
-    dk, dv = _desc(k), _desc(v)
-    st = load().slope_kv4_write(_ref(cache._c), _ref(dk), _ref(dv), _index(slots, "slots", k.shape[0]),
-                                _stream_ptr(stream))
+    st = load().slope_kv4_write(cache._c, _desc(k), _desc(v), _index(slots, "slots", k.shape[0]), _stream(stream))
     _check(st, "slope_kv4_write")
 
 
 def kv4_read(cache, slots, *, k_out=None, v_out=None, out_dtype=None, stream=None):
     """The values the cache holds at slots (device int32 [T]): ``(k [T,Hkv,dqk], v [T,Hkv,dv])``, bf16 (default) or
     fp32.  Rows whose slot is out of range are left as they were (uninitialised where the call allocates)."""
-    torch = _torch()
     T = slots.shape[0]
     if k_out is None:
         k_out = torch.empty((T, cache.Hkv, cache.dqk), dtype=out_dtype or torch.bfloat16, device=cache.data.device)
     if v_out is None:
         v_out = torch.empty((T, cache.Hkv, cache.dv), dtype=out_dtype or torch.bfloat16, device=cache.data.device)
     _here(cache.data, slots, k_out, v_out)
-    dk, dv = _desc(k_out), _desc(v_out)
-    st = load().slope_kv4_read(_ref(cache._c), _index(slots, "slots", k_out.shape[0]), _ref(dk), _ref(dv),
-                               _stream_ptr(stream))
+    st = load().slope_kv4_read(cache._c, _index(slots, "slots", k_out.shape[0]), _desc(k_out), _desc(v_out),
+                               _stream(stream))
     _check(st, "slope_kv4_read")
     return k_out, v_out
 
 
 def kv4_attn_workspace_size(B, Hq, cache, q_len=1) -> int:
     """Workspace bytes of :func:`kv4_attn` (0 for arguments it does not support)."""
-    return int(load().slope_kv4_attn_workspace_size(int(B), int(Hq), _ref(cache._c), int(q_len)))
+    return int(load().slope_kv4_attn_workspace_size(int(B), int(Hq), cache._c, int(q_len)))
 
 
 def kv4_attn(q, cache, block_table, kv_lens, *, q_len=1, window=0, scale=0.0, out=None, lse=None, workspace=None,
@@ -219,7 +241,6 @@ def kv4_attn(q, cache, block_table, kv_lens, *, q_len=1, window=0, scale=0.0, ou
     of a sequence sees positions up to kv_lens - q_len + i (and, with ``window``, that many back).  Returns
     ``(out, lse)``: out bf16 (default) or fp32 [B * q_len,Hq,dv], lse fp32 [Hq,B * q_len] (None if not wanted).
     """
-    torch = _torch()
     T, Hq, _ = q.shape
     if out is None:
         out = torch.empty((T, Hq, cache.dv), dtype=out_dtype or torch.bfloat16, device=q.device)
@@ -239,12 +260,10 @@ def kv4_attn(q, cache, block_table, kv_lens, *, q_len=1, window=0, scale=0.0, ou
             raise SlopeError(-8, "slope_kv4_attn_workspace_size")
         workspace = torch.empty((nbytes,), dtype=torch.uint8, device=q.device)
     _here(q, cache.data, block_table, kv_lens, out, lse, workspace)
-    dq, do = _desc(q), _desc(out)
-    dl = _desc(lse) if lse is not None else None
-    st = load().slope_kv4_attn(_ref(dq), _ref(cache._c), _index(block_table, "block_table"),
-                               block_table.stride(0) if B > 1 else block_table.shape[1], block_table.shape[1],
-                               _index(kv_lens, "kv_lens", B), q_len, int(window), float(scale), _ref(do), _ref(dl),
-                               ctypes.c_void_p(workspace.data_ptr()), workspace.numel() * workspace.element_size(),
-                               _stream_ptr(stream))
+    pages = block_table.shape[1]
+    st = load().slope_kv4_attn(_desc(q), cache._c, _index(block_table, "block_table"),
+                               block_table.stride(0) if B > 1 else pages, pages, _index(kv_lens, "kv_lens", B), q_len,
+                               window, scale, _desc(out), _desc(lse), workspace.data_ptr(),
+                               workspace.numel() * workspace.element_size(), _stream(stream))
     _check(st, "slope_kv4_attn")
     return out, lse

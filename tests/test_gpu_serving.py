@@ -161,7 +161,7 @@ def hard(T, H, d, seed, dtype):
 
 
 SHAPES = [(1, 1, 64, 64, 16), (17, 2, 64, 64, 16), (40, 3, 128, 128, 32), (33, 2, 192, 128, 64), (20, 1, 128, 64, 16),
-          (25, 2, 64, 128, 48), (19, 2, 192, 64, 1024), (130, 8, 64, 64, 64)]
+          (25, 2, 64, 128, 128), (19, 2, 192, 64, 1024), (130, 8, 64, 64, 64)]
 
 
 @pytest.mark.parametrize("T,H,dqk,dv,page", SHAPES)
@@ -294,7 +294,7 @@ def test_decode_heads_and_sizes(dqk, dv, Hq, H, q_len):
     run_decode([3, 130, 41], q_len, Hq, H, dqk, dv, 32)
 
 
-@pytest.mark.parametrize("page", [16, 48, 64, 1024])
+@pytest.mark.parametrize("page", [16, 32, 64, 1024])
 @pytest.mark.parametrize("window,q_len", [(0, 1), (1, 1), (17, 1), (40, 3), (1000, 2), (5, 64)])
 def test_decode_pages_and_windows(page, window, q_len):
     run_decode([100, 1, 33, 259], q_len, 4, 2, 64, 64, page, window=window)

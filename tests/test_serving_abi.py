@@ -194,7 +194,7 @@ def cache(n_pages=4, page=64, H=2, dqk=64, dv=64, data=0x40000):
     return slope.SlopeKV4Cache(data, n_pages, page, H, dqk, dv)
 
 
-BAD_CACHES = [(dict(dqk=96), E_UNSUP), (dict(dv=192), E_UNSUP), (dict(page=8), E_SHAPE), (dict(page=40), E_SHAPE),
+BAD_CACHES = [(dict(dqk=96), E_UNSUP), (dict(dv=192), E_UNSUP), (dict(page=8), E_SHAPE), (dict(page=48), E_SHAPE),
               (dict(page=2048), E_SHAPE), (dict(n_pages=-1), E_SHAPE), (dict(H=0), E_SHAPE), (dict(H=65536), E_SHAPE),
               (dict(n_pages=2 ** 25), E_SHAPE), (dict(data=None), E_NULL), (dict(data=0x40008), E_STRIDE)]
 
