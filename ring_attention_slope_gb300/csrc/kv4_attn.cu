@@ -10,16 +10,15 @@
 //   sum_j w_j v_jc = sum_j (w_j scale_jG) code_jc + sum_j w_j min_jG
 // so a code costs a mask and half a shift, not a conversion.
 //
-// Codes as matrix operands.  A 4-bit code in the low bits of a 16-bit float is a
-// subnormal number, code * 2^-24 in fp16 and code * 2^-133 in bf16, which the
-// tensor cores multiply exactly.  Keys use fp16 (two code positions are
-// subnormals there, bits 0-3 and 4-7, so one shift serves eight codes): a query
-// row is scaled by a power of two to a largest value near 2^14, and its channels
-// that meet bits 4-7 by 1/16, both exact.  Values use bf16, because the other
-// operand, weight * scale, needs bf16's range (fp16's would flush it): the weight
-// carries a factor 2^64 so that products with 2^-133 stay normal fp32 numbers.
-// Its rounding to bf16 (2^-9 relative) is the one the attention kernel of the
-// prefill also makes on its weights.
+// Codes as matrix operands.  A float whose exponent field is 0 or 1 is linear in its bits, so the low 8
+// bits of a 16-bit float, alone, are an exact multiple of its smallest subnormal: a 4-bit code in bits 0-3 is
+// code * 2^-24 in fp16 and code * 2^-133 in bf16, one in bits 4-7 sixteen times that, and the tensor cores
+// multiply both exactly.  One shift by 8 serves the other eight bits, so eight codes take a shift and
+// four masks.  Keys use fp16: a query row is scaled by a power of two to a largest value near 2^14, and its
+// channels that meet bits 4-7 by 1/16, both exact.  Values use bf16, because the other operand, weight *
+// scale, needs bf16's range (fp16's would flush it): the weight carries a factor 2^64 so that products with
+// 2^-133 stay normal fp32 numbers.  Its rounding to bf16 (2^-9 relative) is the one the attention kernel of
+// the prefill also makes on its weights.
 //
 // Keys are the M rows of S^T = K Q^T (16 keys x 8 query rows), values those of
 // O^T = V^T P^T (16 channels x 8 query rows): with the few query rows of a decode
@@ -39,6 +38,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "host.cuh"
@@ -92,9 +92,15 @@ struct Kv4Cfg {
   static constexpr int kKeyBytes = kv4_key_bytes(DQK), kValueBytes = kv4_value_bytes(DV);
   static constexpr int kBlockBytes = kv4_block_bytes(DQK, DV);
   // CTAs on an SM, by registers: 128 a thread at four, 168 at three, 255 at two
-  static constexpr int kCtas = (DQK == 64 && DV == 64) ? (NT == 1 ? 4 : 3) : 2;
+#ifndef KC64
+#define KC64 4
+#define KS64 4
+#define KCW 3
+#define KSW 2
+#endif
+  static constexpr int kCtas = NT == 1 ? (DQK == 64 && DV == 64 ? KC64 : KCW) : (DQK == 64 && DV == 64 ? 3 : 2);
   static constexpr int kStageBytes = 2 * kBlockBytes;
-  static constexpr int kStages = kCtas > 2 ? 4 : 3;
+  static constexpr int kStages = NT == 1 ? (DQK == 64 && DV == 64 ? KS64 : KSW) : kCtas > 2 ? 4 : 3;
   static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
   static constexpr int kRedFloats = kWarps * R * DV + 2 * kWarps * R;
   static constexpr int kSmemBytes = kRingBytes + kRedFloats * 4 + kWarps * kStages * 8 + 64;
@@ -566,8 +572,9 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
             const uint32_t z0 = __byte_perm(r.x, r.y, h ? 0x7632 : 0x5410), z1 = __byte_perm(r.z, r.w, h ? 0x7632 : 0x5410);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const uint32_t a0 = (z0 >> (8 * i)) & 0x000f000fu, a1 = (z0 >> (8 * i + 4)) & 0x000f000fu;
-              const uint32_t a2 = (z1 >> (8 * i)) & 0x000f000fu, a3 = (z1 >> (8 * i + 4)) & 0x000f000fu;
+              // channels 2 i in rows g, and 2 i + 1, sixteen times as large, in rows g + 8
+              const uint32_t a0 = (z0 >> (8 * i)) & 0x000f000fu, a1 = (z0 >> (8 * i)) & 0x00f000f0u;
+              const uint32_t a2 = (z1 >> (8 * i)) & 0x000f000fu, a3 = (z1 >> (8 * i)) & 0x00f000f0u;
 #pragma unroll
               for (int t = 0; t < NT; ++t)
                 mma_bf16(o[c][h][i][t], a0, a1, a2, a3, pb[t][2 * c + h][0], pb[t][2 * c + h][1]);
@@ -622,8 +629,8 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
           for (int h = 0; h < 2; ++h) {
             const float bs = bias[t][2 * c + h][j] * 0x1p-64f;
             *reinterpret_cast<float4*>(red + (warp * C::R + rr) * DV + 64 * c + 32 * h + 4 * g) =
-                make_float4(fmaf(o[c][h][0][t][j], 0x1p69f, bs), fmaf(o[c][h][0][t][2 + j], 0x1p69f, bs),
-                            fmaf(o[c][h][1][t][j], 0x1p69f, bs), fmaf(o[c][h][1][t][2 + j], 0x1p69f, bs));
+                make_float4(fmaf(o[c][h][0][t][j], 0x1p69f, bs), fmaf(o[c][h][0][t][2 + j], 0x1p65f, bs),
+                            fmaf(o[c][h][1][t][j], 0x1p69f, bs), fmaf(o[c][h][1][t][2 + j], 0x1p65f, bs));
           }
       }
     __syncthreads();
@@ -698,11 +705,17 @@ __global__ void __launch_bounds__(kThreads) kv4_join_kernel(const __grid_constan
   }
 }
 
-int sm_count() {
+constexpr int kMaxDevices = 64;
+
+// SMs of the current device, and its number (both looked up once a device).
+int sm_count(int* device) {
+  static std::atomic<int> known[kMaxDevices];
   int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
-    return 1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+  *device = dev;
+  if ((sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) return 0;
+  known[dev].store(sms, std::memory_order_relaxed);
   return sms;
 }
 
@@ -710,12 +723,19 @@ template <int DQK, int DV, int NT>
 cudaError_t launch_nt(Kv4AttnParams p, cudaStream_t stream) {
   using C = Kv4Cfg<DQK, DV, NT>;
   p.row_tiles = (p.q_len * p.group + C::R - 1) / C::R;
-  cudaError_t e = cudaFuncSetAttribute(kv4_attn_kernel<DQK, DV, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       C::kSmemBytes);
-  if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(kv4_attn_kernel<DQK, DV, NT>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-  if (e != cudaSuccess) return e;
-  const int grid = std::min(kMaxCtas, sm_count() * C::kCtas);
+  int dev = 0;
+  const int sms = sm_count(&dev);
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  cudaError_t e;
+  static std::atomic<bool> ready[kMaxDevices];  // the kernel's attributes are set on the device
+  if (!ready[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(kv4_attn_kernel<DQK, DV, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(kv4_attn_kernel<DQK, DV, NT>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    if (e != cudaSuccess) return e;
+    ready[dev].store(true, std::memory_order_release);
+  }
+  const int grid = std::min(kMaxCtas, sms * C::kCtas);
   kv4_attn_kernel<DQK, DV, NT><<<grid, kThreads, C::kSmemBytes, stream>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};

@@ -8,13 +8,14 @@
 // where a run of tokens fills a block, the words of a block's sector come from
 // one warp and those of its neighbours from the same CTA.
 //
-// Rounding a quotient: with inv the correctly rounded reciprocal of the scale and q = d inv,
-// fma(fma(-q, scale, d), inv, q) is the correctly rounded d / scale (Markstein, 1990).  Where
-// d = x - min is exact, as it is for bf16 values within 2^16 of each other, a quotient that rounds to a
-// half is one (d - (n + 1/2) scale is a multiple of d's last place, so a quotient next to a half is further
-// off than half a place), and rounding halves to even decides it rightly: halves are common among bf16 values.
-// Otherwise d's own rounding moves the quotient by at most 2^-24 of 16: one closer than 1e-5 to a
-// half, which is rare then, is divided again in fp64.
+// Rounding a quotient: with inv the scale's reciprocal to 2^-22 and q = d inv, the remainder d - q scale is
+// exact and q + remainder inv differs from d / scale by 2^-44 before its own rounding.  Where d = x - min is
+// exact and has at most 22 bits, as for bf16 values within 2^14 of each other, that decides every code: a
+// quotient that is a half comes out as that half (and halves, common among bf16 values, round to even), and
+// one that is not differs from it by a place of d at least, more than rounding to 24 bits can bridge.
+// Otherwise (fp32 values, or bf16 ones further apart) d's own rounding moves the quotient by at most 2^-24 of
+// 16, and one closer than 1e-5 to a half is decided again from error-free differences (not in fp64, of which
+// this GPU does two operations a clock: with that path the 12K-token store took 39 us).
 #include <cuda_bf16.h>
 
 #include <cfloat>
@@ -27,9 +28,9 @@
 namespace slope {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kTokens = 16;                        // tokens of a CTA
-constexpr int kUnitsPerPass = kThreads / 8 / kTokens;  // (head, 64-channel chunk) pairs a CTA takes at a time
+constexpr int kHeadsPerPass = kThreads / 8 / kTokens;  // heads a CTA takes at a time
 
 struct Kv4StoreParams {
   uint8_t* data;
@@ -40,8 +41,7 @@ struct Kv4StoreParams {
   void* v;
   int64_t k_srow, k_shead, v_srow, v_shead;
   int32_t page_shift, Hkv;
-  int32_t units;     // Hkv * (dqk + dv) / 64
-  int32_t per_cta;   // units of a CTA
+  int32_t per_cta;  // heads of a CTA
 };
 
 // A token's block of head 0, and where it lies in it.
@@ -79,44 +79,133 @@ struct Raw8 {
   }
 };
 
-// Of a lane's 8 channels: smallest, largest, smallest magnitude, and whether one is not finite.
+// Smaller of two numbers, NaN if either is.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// Of a lane's 8 channels: smallest (NaN if any is), largest, smallest magnitude.
 struct Extremes {
   float lo, hi, small;
-  bool bad;
 };
 __device__ __forceinline__ Extremes extremes(const Raw8<__nv_bfloat16>& x) {
   __nv_bfloat162 v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[i] = reinterpret_cast<const __nv_bfloat162*>(&x.r[0])[i];
-  const __nv_bfloat162 lo = __hmin2(__hmin2(v[0], v[1]), __hmin2(v[2], v[3]));
+  const __nv_bfloat162 lo = __hmin2_nan(__hmin2_nan(v[0], v[1]), __hmin2_nan(v[2], v[3]));
   const __nv_bfloat162 hi = __hmax2(__hmax2(v[0], v[1]), __hmax2(v[2], v[3]));
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[i] = __habs2(v[i]);
   const __nv_bfloat162 small = __hmin2(__hmin2(v[0], v[1]), __hmin2(v[2], v[3]));
-  const __nv_bfloat162 large = __hmax2_nan(__hmax2_nan(v[0], v[1]), __hmax2_nan(v[2], v[3]));
-  return {fminf(__low2float(lo), __high2float(lo)), fmaxf(__low2float(hi), __high2float(hi)),
-          fminf(__low2float(small), __high2float(small)),
-          !(__low2float(large) <= FLT_MAX && __high2float(large) <= FLT_MAX)};
+  return {min_nan(__low2float(lo), __high2float(lo)), fmaxf(__low2float(hi), __high2float(hi)),
+          fminf(__low2float(small), __high2float(small))};
 }
 __device__ __forceinline__ Extremes extremes(const Raw8<float>& x) {
-  Extremes e{INFINITY, -INFINITY, 0.f, false};
+  Extremes e{INFINITY, -INFINITY, 0.f};
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float f = __uint_as_float((&x.r[i / 4].x)[i % 4]);
-    e.lo = fminf(e.lo, f);
+    e.lo = min_nan(e.lo, f);
     e.hi = fmaxf(e.hi, f);
-    e.bad |= !(fabsf(f) <= FLT_MAX);
   }
   return e;
 }
 
 constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer, halves to even
 
+// The code of one value, from error-free steps: with d + e = x - mn exactly, n the integer below the quotient
+// (or, next to an integer, the one on its other side), d - (n + 1/2) scale has the sign of the exact difference
+// and is exact where it is small, and e decides a tie.  (An e below 2^-52 of d is one that fp64 does not see.)
+__device__ __noinline__ float code_of(float x, float mn, float scale, float inv) {
+  const float d = __fsub_rn(x, mn);
+  const float back = __fsub_rn(d, x);
+  float e = __fadd_rn(__fsub_rn(x, __fsub_rn(d, back)), __fsub_rn(-mn, back));
+  if (fabsf(e) <= fabsf(d) * 0x1p-52f) e = 0.f;
+  const float q = __fmul_rn(d, inv), t = fmaf(fmaf(-q, scale, d), inv, q);
+  const float n = rintf(fminf(fmaxf(t, 0.f), 15.f) - 0.5f);
+  const float over = __fadd_rn(fmaf(-(n + 0.5f), scale, d), e);
+  const bool odd = static_cast<int>(n) & 1;
+  return fminf(fmaxf(over > 0.f || (over == 0.f && odd) ? n + 1.f : n, 0.f), 15.f);
+}
+
+// Eight lanes' 64 channels of one token's head: the lane's eight codes, and its group's word.
+// Every lane of the warp calls it.
+struct Quantised {
+  uint32_t codes, word;
+};
+template <typename T>
+__device__ __forceinline__ Quantised quantise(const Raw8<T>& x) {
+  const Extremes ex = extremes(x);
+  float lo = ex.lo, hi = ex.hi;
+#pragma unroll
+  for (int m = 1; m < 4; m <<= 1) {
+    lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, m));
+    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, m));
+  }
+  const __nv_bfloat16 min_b = __float2bfloat16_rn(lo);
+  const float mn = __bfloat162float(min_b);
+  const float span = __fsub_rn(hi, mn);
+  const bool nan_group = !(span <= FLT_MAX);  // a NaN or an infinity among them, or too wide a range
+  float scale = __bfloat162float(__float2bfloat16_rn(__fmul_rn(span, 1.f / 15.f)));
+  if (!(scale >= FLT_MIN) || nan_group) scale = 0.f;
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scale));
+  if (scale == 0.f) inv = 0.f;
+  // The quotients; scale 0 makes them 0.  bf16: none is below 0 (the minimum is exact) or above
+  // 15 / (1 - 2^-8), so none rounds to a number past 0 .. 15.
+  uint64_t t[4], r[4];
+  const uint64_t mn2 = pack_f32x2(-mn, -mn), inv2 = pack_f32x2(inv, inv), ns2 = pack_f32x2(-scale, -scale);
+  const uint64_t round2 = pack_f32x2(kRound, kRound);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t d = add_f32x2(x.pair(i), mn2), q = mul_f32x2(d, inv2);
+    t[i] = fma_f32x2(fma_f32x2(q, ns2, d), inv2, q);
+    if constexpr (sizeof(T) == 4) {
+      const float2 f = unpack_f32x2(t[i]);
+      t[i] = pack_f32x2(fminf(fmaxf(f.x, 0.f), 15.f), fminf(fmaxf(f.y, 0.f), 15.f));
+    }
+    r[i] = add_f32x2(t[i], round2);
+  }
+  bool again;
+  if constexpr (sizeof(T) == 2) {
+    again = ex.small * 16384.f < fabsf(mn) || fmaxf(fabsf(lo), fabsf(hi)) > 16384.f * fabsf(mn);
+  } else {
+    float off = 0.f;  // largest distance from the nearest integer
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 a = unpack_f32x2(t[i]), b = unpack_f32x2(r[i]);
+      off = fmaxf(off, fmaxf(fabsf(a.x - (b.x - kRound)), fabsf(a.y - (b.y - kRound))));
+    }
+    again = off > 0.5f - 1e-5f;
+  }
+  if (again && scale > 0.f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = unpack_f32x2(x.pair(i));
+      r[i] = pack_f32x2(code_of(f.x, mn, scale, inv) + kRound, code_of(f.y, mn, scale, inv) + kRound);
+    }
+  }
+  // 1.5 * 2^23 + n has n in its low bits: shifted and added, the eight patterns leave the codes and a constant
+  uint32_t codes = 0u - 0x4b400000u * 0x11111111u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack_f32x2(r[i]);
+    codes += (__float_as_uint(f.x) << (8 * i)) + (__float_as_uint(f.y) << (8 * i + 4));
+  }
+  if (nan_group) codes = 0;
+  const uint32_t word = nan_group ? 0x00007fc0u
+                                  : (__float_as_uint(scale) & 0xffff0000u) | static_cast<uint32_t>(__bfloat16_as_ushort(min_b));
+  return {codes, word};
+}
+
 template <typename T, int DQK, int DV>
 __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const __grid_constant__ Kv4StoreParams p) {
-  constexpr int kKc = DQK / 64, kPerHead = kKc + DV / 64;
+  constexpr int kKc = DQK / 64, kVc = DV / 64, kChunks = kKc + kVc;
   constexpr int kNk = kv4_key_bytes(DQK), kNv = kv4_value_bytes(DV), kWords = kv4_words(DQK, DV);
   const int lane8 = threadIdx.x % 8;
+  const bool high = lane8 >= 4;
   const int64_t tok = static_cast<int64_t>(blockIdx.x) * kTokens + threadIdx.x / 8 % kTokens;
   int64_t slot = -1;
   if (tok < p.T) {
@@ -126,163 +215,112 @@ __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const __grid_consta
   // lanes without a slot go along for the shuffles
   const bool live = slot >= 0;
   const Place at = place_of<DQK, DV>(p, live ? slot : 0);
-  const T* const k = static_cast<const T*>(p.k) + tok * p.k_srow + lane8 * 8;
-  const T* const v = static_cast<const T*>(p.v) + tok * p.v_srow + lane8 * 8;
-  auto fetch = [&](int u, Raw8<T>& x) {
-    const int head = u / kPerHead, c = u - head * kPerHead;
-    x = Raw8<T>{};
-    if (live) x.load(c < kKc ? k + static_cast<int64_t>(head) * p.k_shead + c * 64
-                             : v + static_cast<int64_t>(head) * p.v_shead + (c - kKc) * 64);
-  };
-  const int u_end = min(p.units, static_cast<int>(blockIdx.y + 1) * p.per_cta);
-  int u = blockIdx.y * p.per_cta + threadIdx.x / (8 * kTokens);  // the same for a whole warp
-  Raw8<T> next;
-  if (u < u_end) fetch(u, next);
-  for (; u < u_end; u += kUnitsPerPass) {
-    const Raw8<T> x = next;
-    if (u + kUnitsPerPass < u_end) fetch(u + kUnitsPerPass, next);
-    const Extremes ex = extremes(x);
-    float lo = ex.lo, hi = ex.hi;
+  const int h_end = min(p.Hkv, static_cast<int>(blockIdx.y + 1) * p.per_cta);
+  int h = blockIdx.y * p.per_cta + threadIdx.x / (8 * kTokens);  // the same for a whole warp
+  const T* k = static_cast<const T*>(p.k) + tok * p.k_srow + h * p.k_shead + lane8 * 8;
+  const T* v = static_cast<const T*>(p.v) + tok * p.v_srow + h * p.v_shead + lane8 * 8;
+  // the lane's places in a block: key words of its groups, value words, scale words
+  uint8_t* block = at.block + h * at.head_bytes;
+  const int k_at = (at.t % 8 * 4 + (lane8 & 3)) * 16, k_word = at.t / 8 * (DQK / kKv4Group) + (high ? 1 : 0);
+  const int v_at = kNk + kv4_value_offset(at.t, 0, 2 * (lane8 & 3) + (high ? 1 : 0));
+  const int w_at = kNk + kNv + 4 * (at.t * kWords + (high ? 1 : 0));
+  Raw8<T> x[kChunks];
 #pragma unroll
-    for (int m = 1; m < 4; m <<= 1) {
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, m));
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, m));
-    }
-    const uint32_t bad_lanes = __ballot_sync(0xffffffffu, ex.bad) >> (threadIdx.x & 28);
-    const __nv_bfloat16 min_b = __float2bfloat16_rn(lo);
-    const float mn = __bfloat162float(min_b);
-    const float span = __fsub_rn(hi, mn);
-    float scale = __bfloat162float(__float2bfloat16_rn(__fmul_rn(span, 1.f / 15.f)));
-    const bool nan_group = (bad_lanes & 15u) != 0 || !(fabsf(mn) <= FLT_MAX) || !(span <= FLT_MAX);
-    if (!(scale >= FLT_MIN) || nan_group) scale = 0.f;
-    const float inv = scale > 0.f ? __frcp_rn(scale) : 0.f;
-    // The quotients; scale 0 makes them 0.  bf16: none is below 0 (the minimum is exact) or above
-    // 15 / (1 - 2^-8), so none rounds to a number past 0 .. 15.
-    uint64_t r[4];
-    float off = 0.f;  // largest distance from the nearest integer
-    const uint64_t mn2 = pack_f32x2(-mn, -mn), inv2 = pack_f32x2(inv, inv), ns2 = pack_f32x2(-scale, -scale);
-    const uint64_t round2 = pack_f32x2(kRound, kRound), unround2 = pack_f32x2(-kRound, -kRound);
-    const bool inexact = sizeof(T) == 4 || ex.small * 65536.f < fabsf(mn) ||
-                         fmaxf(fabsf(lo), fabsf(hi)) > 65536.f * fabsf(mn);
+  for (int c = 0; c < kChunks; ++c) {
+    x[c] = Raw8<T>{};
+    if (live && h < h_end) x[c].load(c < kKc ? k + c * 64 : v + (c - kKc) * 64);
+  }
+  for (; h < h_end; h += kHeadsPerPass) {
+    k += kHeadsPerPass * p.k_shead;
+    v += kHeadsPerPass * p.v_shead;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint64_t d = add_f32x2(x.pair(i), mn2), q = mul_f32x2(d, inv2);
-      uint64_t t = fma_f32x2(fma_f32x2(q, ns2, d), inv2, q);
-      if constexpr (sizeof(T) == 4) {
-        const float2 f = unpack_f32x2(t);
-        t = pack_f32x2(fminf(fmaxf(f.x, 0.f), 15.f), fminf(fmaxf(f.y, 0.f), 15.f));
+    for (int c = 0; c < kChunks; ++c) {
+      const Quantised z = quantise(x[c]);
+      // the next head's channels are in flight while this one's other chunks are worked on
+      if (live && h + kHeadsPerPass < h_end) x[c].load(c < kKc ? k + c * 64 : v + (c - kKc) * 64);
+      // a value's lanes l and l + 4 hold the codes of the same operand lanes g = 2 l, 2 l + 1 for the chunk's
+      // two groups: the lower keeps its first four and gets the other's first four, the upper the second ones
+      const uint32_t other = c < kKc ? 0 : __shfl_xor_sync(0xffffffffu, high ? z.codes : z.codes >> 16, 4);
+      if (!live) continue;
+      if (c < kKc) {
+        const int w = k_word + 2 * c;
+        *reinterpret_cast<uint32_t*>(block + k_at + (w >> 2) * 512 + (w & 3) * 4) = z.codes;
+      } else {
+        *reinterpret_cast<uint32_t*>(block + v_at + (c - kKc) * 512) =
+            high ? __byte_perm(other, z.codes, 0x7610) : __byte_perm(z.codes, other, 0x5410);
       }
-      r[i] = add_f32x2(t, round2);
-      if (inexact) {
-        const float2 e = unpack_f32x2(add_f32x2(t, mul_f32x2(add_f32x2(r[i], unround2), pack_f32x2(-1.f, -1.f))));
-        off = fmaxf(off, fmaxf(fabsf(e.x), fabsf(e.y)));
-      }
+      if ((lane8 & 3) == 0) *reinterpret_cast<uint32_t*>(block + w_at + 8 * c) = z.word;
     }
-    if (inexact && off > 0.5f - 1e-5f) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = unpack_f32x2(x.pair(i));
-        auto divide = [&](float v) {
-          const double t = rint((static_cast<double>(v) - static_cast<double>(mn)) / static_cast<double>(scale));
-          return static_cast<float>(fmin(fmax(t, 0.), 15.)) + kRound;
-        };
-        r[i] = pack_f32x2(divide(f.x), divide(f.y));
-      }
-    }
-    // 1.5 * 2^23 + n has n in its low bits: shifted and added, the eight patterns leave the codes and a constant
-    uint32_t codes = 0u - 0x4b400000u * 0x11111111u;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = unpack_f32x2(r[i]);
-      codes += (__float_as_uint(f.x) << (8 * i)) + (__float_as_uint(f.y) << (8 * i + 4));
-    }
-    if (nan_group) codes = 0;
-    const uint32_t c_lo = codes & 0xffffu, c_hi = codes >> 16;
-    const uint32_t word = nan_group ? 0x00007fc0u
-                                    : (__float_as_uint(scale) & 0xffff0000u) | static_cast<uint32_t>(__bfloat16_as_ushort(min_b));
-    const int head = u / kPerHead, c = u - head * kPerHead;
-    uint8_t* const block = at.block + head * at.head_bytes;
-    const bool high = lane8 >= 4;
-    if (c < kKc) {
-      const int group = c * 2 + (high ? 1 : 0);
-      if (live) {
-        *reinterpret_cast<uint32_t*>(block + kv4_key_offset(DQK, at.t, group, lane8 & 3)) = codes;
-        if ((lane8 & 3) == 0) *reinterpret_cast<uint32_t*>(block + kNk + kNv + 4 * (at.t * kWords + group)) = word;
-      }
-    } else {
-      // lanes l and l + 4 hold the codes of the same lanes g = 2 l, 2 l + 1 for the chunk's two groups: the
-      // lower keeps its first four and gets the other's first four, the upper the second ones
-      const uint32_t other = __shfl_xor_sync(0xffffffffu, high ? c_lo : c_hi, 4);
-      const int chunk = c - kKc, g = 2 * (lane8 & 3) + (high ? 1 : 0);
-      if (live) {
-        *reinterpret_cast<uint32_t*>(block + kNk + kv4_value_offset(at.t, chunk, g)) =
-            high ? other | (c_hi << 16) : c_lo | (other << 16);
-        if ((lane8 & 3) == 0)
-          *reinterpret_cast<uint32_t*>(block + kNk + kNv + 4 * (at.t * kWords + DQK / kKv4Group + chunk * 2 + (high ? 1 : 0))) =
-              word;
-      }
-    }
+    block += kHeadsPerPass * at.head_bytes;
   }
 }
 
 template <typename T, int DQK, int DV>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const __grid_constant__ Kv4StoreParams p) {
-  constexpr int kKc = DQK / 64, kPerHead = kKc + DV / 64;
+  constexpr int kKc = DQK / 64, kVc = DV / 64, kChunks = kKc + kVc;
   constexpr int kNk = kv4_key_bytes(DQK), kNv = kv4_value_bytes(DV), kWords = kv4_words(DQK, DV);
+  constexpr int kWide = kChunks == 2 ? 2 : 1;  // heads whose loads are in flight together
   const int lane8 = threadIdx.x % 8, high = lane8 / 4;
   const int64_t tok = static_cast<int64_t>(blockIdx.x) * kTokens + threadIdx.x / 8 % kTokens;
   if (tok >= p.T) return;
   const int64_t slot = p.slots[tok];
   if (slot < 0 || slot >= p.n_slots) return;
   const Place at = place_of<DQK, DV>(p, slot);
-  T* const k = static_cast<T*>(p.k) + tok * p.k_srow + lane8 * 8;
-  T* const v = static_cast<T*>(p.v) + tok * p.v_srow + lane8 * 8;
-  const int u_end = min(p.units, static_cast<int>(blockIdx.y + 1) * p.per_cta);
-  constexpr int kAhead = 4;  // units whose loads are in flight together
-  for (int u0 = blockIdx.y * p.per_cta + threadIdx.x / (8 * kTokens); u0 < u_end; u0 += kAhead * kUnitsPerPass) {
-    uint32_t codes[kAhead], word[kAhead];
+  const int h_end = min(p.Hkv, static_cast<int>(blockIdx.y + 1) * p.per_cta);
+  int h = blockIdx.y * p.per_cta + threadIdx.x / (8 * kTokens);
+  T* k = static_cast<T*>(p.k) + tok * p.k_srow + h * p.k_shead + lane8 * 8;
+  T* v = static_cast<T*>(p.v) + tok * p.v_srow + h * p.v_shead + lane8 * 8;
+  const uint8_t* block = at.block + h * at.head_bytes;
+  const int k_at = (at.t % 8 * 4 + (lane8 & 3)) * 16, k_word = at.t / 8 * (DQK / kKv4Group) + high;
+  const int v_at = kNk + kv4_value_offset(at.t, 0, 2 * (lane8 & 3)) + 2 * high;
+  constexpr int kNextG = kv4_value_offset(0, 0, 1) - kv4_value_offset(0, 0, 0);
+  const int w_at = kNk + kNv + 4 * (at.t * kWords + high);
+  for (; h < h_end; h += kWide * kHeadsPerPass) {
+    uint32_t codes[kWide][kChunks], word[kWide][kChunks];
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      const int u = min(u0 + a * kUnitsPerPass, u_end - 1);
-      const int head = u / kPerHead, c = u - head * kPerHead;
-      const uint8_t* const block = at.block + head * at.head_bytes;
-      const uint8_t* const words = block + kNk + kNv + 4 * (at.t * kWords + high);
-      if (c < kKc) {
-        codes[a] = __ldg(reinterpret_cast<const uint32_t*>(block + kv4_key_offset(DQK, at.t, c * 2 + high, lane8 & 3)));
-        word[a] = __ldg(reinterpret_cast<const uint32_t*>(words + 8 * c));
-      } else {
-        const int chunk = c - kKc;
-        const uint8_t* const b = block + kNk + kv4_value_offset(at.t, chunk, 2 * (lane8 & 3)) + 2 * high;
-        constexpr int kNextG = kv4_value_offset(0, 0, 1) - kv4_value_offset(0, 0, 0);
-        codes[a] = __ldg(reinterpret_cast<const uint16_t*>(b)) |
-                   static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(b + kNextG))) << 16;
-        word[a] = __ldg(reinterpret_cast<const uint32_t*>(words + 4 * (DQK / kKv4Group) + 8 * chunk));
+    for (int a = 0; a < kWide; ++a) {
+      if (h + a * kHeadsPerPass >= h_end) break;
+      const uint8_t* const b = block + a * kHeadsPerPass * at.head_bytes;
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        if (c < kKc) {
+          const int w = k_word + 2 * c;
+          codes[a][c] = __ldg(reinterpret_cast<const uint32_t*>(b + k_at + (w >> 2) * 512 + (w & 3) * 4));
+        } else {
+          const uint8_t* const vb = b + v_at + (c - kKc) * 512;
+          codes[a][c] = __ldg(reinterpret_cast<const uint16_t*>(vb)) |
+                        static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(vb + kNextG))) << 16;
+        }
+        word[a][c] = __ldg(reinterpret_cast<const uint32_t*>(b + w_at + 8 * c));
       }
     }
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      const int u = u0 + a * kUnitsPerPass;
-      if (u >= u_end) break;
-      const int head = u / kPerHead, c = u - head * kPerHead;
-      const float scale = __uint_as_float(word[a] & 0xffff0000u), mn = __uint_as_float(word[a] << 16);
-      const uint64_t s2 = pack_f32x2(scale, scale), m2 = pack_f32x2(mn, mn), base2 = pack_f32x2(-8388608.f, -8388608.f);
-      float2 x[4];
+    for (int a = 0; a < kWide; ++a) {
+      if (h + a * kHeadsPerPass >= h_end) break;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {  // 2^23 + code as a float, less 2^23
-        const uint64_t n = pack_f32x2(__uint_as_float(((codes[a] >> (8 * i)) & 15u) | 0x4b000000u),
-                                      __uint_as_float(((codes[a] >> (8 * i + 4)) & 15u) | 0x4b000000u));
-        x[i] = unpack_f32x2(fma_f32x2(s2, add_f32x2(n, base2), m2));
-      }
-      T* const dst = c < kKc ? k + static_cast<int64_t>(head) * p.k_shead + c * 64
-                             : v + static_cast<int64_t>(head) * p.v_shead + (c - kKc) * 64;
-      if constexpr (sizeof(T) == 2) {
-        *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(x[0].x, x[0].y), pack_bf16x2(x[1].x, x[1].y),
-                                                    pack_bf16x2(x[2].x, x[2].y), pack_bf16x2(x[3].x, x[3].y));
-      } else {
-        *reinterpret_cast<float4*>(dst) = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
-        *reinterpret_cast<float4*>(dst + 4) = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
+      for (int c = 0; c < kChunks; ++c) {
+        const float scale = __uint_as_float(word[a][c] & 0xffff0000u), mn = __uint_as_float(word[a][c] << 16);
+        const uint64_t s2 = pack_f32x2(scale, scale), m2 = pack_f32x2(mn, mn), base2 = pack_f32x2(-8388608.f, -8388608.f);
+        float2 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // 2^23 + code as a float, less 2^23
+          const uint64_t n = pack_f32x2(__uint_as_float(((codes[a][c] >> (8 * i)) & 15u) | 0x4b000000u),
+                                        __uint_as_float(((codes[a][c] >> (8 * i + 4)) & 15u) | 0x4b000000u));
+          x[i] = unpack_f32x2(fma_f32x2(s2, add_f32x2(n, base2), m2));
+        }
+        T* const dst = c < kKc ? k + a * kHeadsPerPass * p.k_shead + c * 64 : v + a * kHeadsPerPass * p.v_shead + (c - kKc) * 64;
+        if constexpr (sizeof(T) == 2) {
+          *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(x[0].x, x[0].y), pack_bf16x2(x[1].x, x[1].y),
+                                                      pack_bf16x2(x[2].x, x[2].y), pack_bf16x2(x[3].x, x[3].y));
+        } else {
+          *reinterpret_cast<float4*>(dst) = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+          *reinterpret_cast<float4*>(dst + 4) = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
+        }
       }
     }
+    k += kWide * kHeadsPerPass * p.k_shead;
+    v += kWide * kHeadsPerPass * p.v_shead;
+    block += kWide * kHeadsPerPass * at.head_bytes;
   }
 }
 
@@ -339,18 +377,16 @@ slope_status prepare_store(const slope_kv4_cache* cache, const slope_tensor* k, 
   p.page_shift = 4;
   while ((1 << p.page_shift) < cache->page_size) ++p.page_shift;
   p.Hkv = cache->Hkv;
-  p.units = cache->Hkv * ((cache->dqk + cache->dv) / 64);
   return SLOPE_OK;
 }
 
 dim3 store_grid(Kv4StoreParams& p) {
   const int64_t tx = (p.T + kTokens - 1) / kTokens;
-  // a few passes to a CTA once there are enough CTAs without them
-  p.per_cta = kUnitsPerPass;
-  while (p.per_cta < p.units && (tx * ((p.units + p.per_cta - 1) / p.per_cta) > 4864 ||
-                                 (p.units + p.per_cta - 1) / p.per_cta > 65535))
-    p.per_cta *= 2;
-  return dim3(static_cast<unsigned>(tx), static_cast<unsigned>((p.units + p.per_cta - 1) / p.per_cta));
+  // a CTA takes one head at a time, and more in turn once that leaves about two waves of eight CTAs on
+  // each of the 152 SMs
+  p.per_cta = kHeadsPerPass;
+  while (p.per_cta < p.Hkv && tx * ((p.Hkv + p.per_cta - 1) / p.per_cta) > 2432) p.per_cta *= 2;
+  return dim3(static_cast<unsigned>(tx), static_cast<unsigned>((p.Hkv + p.per_cta - 1) / p.per_cta));
 }
 
 }  // namespace

@@ -101,6 +101,12 @@ __device__ __forceinline__ uint64_t weight_pair(const NormRopeSide& s, int64_t i
   return pack_f32x2(weight_at(s, i), weight_at(s, i + 1));
 }
 
+// A lane's factors for its channels: y_e = (x_e a_e + x_partner b_e) / rms.
+template <int kChunks>
+struct Factors {
+  uint64_t a[kChunks][4], b[kChunks][4];
+};
+
 // kInter: pairs are neighbours (and a pair's partner is in the same lane's channels), else halves.
 template <typename TI, typename TO, int D, bool kInter>
 __global__ void __launch_bounds__(kThreads, D == 64 ? 3 : 2)
@@ -108,16 +114,63 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 3 : 2)
   __shared__ __align__(16) float s_cos[kWarps][kMaxHalf], s_sin[kWarps][kMaxHalf];  // of the warp's token
   __shared__ __align__(16) float s_w[2][D];  // weights shared by every head of a side, else 1
   constexpr int kChunks = D / 64;
-  // passes whose loads are in flight together
-  constexpr int kAhead = D == 64 && sizeof(TI) == 2 ? 2 : 1;
+  constexpr int kWide = D == 64 && sizeof(TI) == 2 ? 2 : 1;  // groups of four heads in a pass
+  // a 64-channel bf16 head lies in one 16-byte word of its eight lanes: the other half comes by shuffle
+  constexpr bool kShuffle = D == 64 && sizeof(TI) == 2 && !kInter;
+  constexpr bool kLoadPartner = !kInter && !kShuffle;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int lane8 = lane % kLanesPerHead, sub = lane / kLanesPerHead;
+  const int64_t task = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  const int64_t tok = task / p.splits;
+  const bool here = tok < p.T;
+  const int split = static_cast<int>(task - tok * p.splits);
+  const int first = split * p.heads, last = here ? min(first + p.heads, p.side[0].H + p.side[1].H) : first;
+  // the warp's heads of either side, and the passes they take
+  int h_begin[2], h_end[2], n_pass[2];
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const int base = w ? p.side[0].H : 0;
+    h_begin[w] = max(first - base, 0);
+    h_end[w] = min(last - base, p.side[w].H);
+    n_pass[w] = h_begin[w] < h_end[w] ? (h_end[w] - h_begin[w] + kHeadsPerPass * kWide - 1) / (kHeadsPerPass * kWide) : 0;
+  }
+  // elements from a chunk of the lane to the other half of its pairs (0: not rotated; 1: neighbours)
+  int partner[kChunks];
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) {
+    const int off = c * 64 + lane8 * 8 - p.begin;
+    partner[c] = !p.rotate || off < 0 || off >= 2 * p.half ? 0 : kInter ? 1 : off < p.half ? p.half : -p.half;
+  }
+  Raw8<TI> v[kWide][kChunks], o[kWide][kChunks];
+#pragma unroll
+  for (int k = 0; k < kWide; ++k)
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) o[k][c] = Raw8<TI>{};
+  auto fetch = [&](int pass, Raw8<TI>(&fv)[kWide][kChunks], Raw8<TI>(&fo)[kWide][kChunks]) {
+    const int w = pass >= n_pass[0] ? 1 : 0;
+    const NormRopeSide& s = p.side[w];
+    const int h0 = w ? h_begin[1] + (pass - n_pass[0]) * (kHeadsPerPass * kWide) : h_begin[0] + pass * (kHeadsPerPass * kWide);
+    const TI* const x = static_cast<const TI*>(s.x) + tok * s.x_srow + lane8 * 8;
+#pragma unroll
+    for (int k = 0; k < kWide; ++k) {
+      // past the last head: its values once more, which are not stored
+      const int h = min(h0 + k * kHeadsPerPass + sub, (w ? h_end[1] : h_end[0]) - 1);
+      const TI* const xh = x + h * s.x_shead;
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        fv[k][c].load(xh + c * 64);
+        if (kLoadPartner && partner[c] != 0) fo[k][c].load(xh + c * 64 + partner[c]);
+      }
+    }
+  };
+  const int passes = n_pass[0] + n_pass[1];
+  if (passes > 0) fetch(0, v, o);
+
   for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
     const NormRopeSide& s = p.side[i / D];
     s_w[i / D][i % D] = s.w != nullptr && s.w_shead == 0 ? weight_at(s, i % D) : 1.f;
   }
-  const int64_t task = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
-  const int64_t tok = task / p.splits;
-  if (tok < p.T && p.rotate) {
+  if (here && p.rotate) {
     const int64_t pos = p.positions != nullptr ? p.positions[tok] : p.pos0 + tok;
     for (int f = lane; f < p.half; f += 32) {
       // the fraction of a turn, rounded to 32 bits and taken in [-1/2, 1/2)
@@ -129,26 +182,13 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 3 : 2)
     }
   }
   __syncthreads();
-  if (tok >= p.T) return;  // a whole warp
-  const int split = static_cast<int>(task - tok * p.splits);
-  const int first = split * p.heads, last = min(first + p.heads, p.side[0].H + p.side[1].H);
 
-  const int lane8 = lane % kLanesPerHead, sub = lane / kLanesPerHead;
-#pragma unroll 1
-  for (int which = 0; which < 2; ++which) {
-    const NormRopeSide& s = p.side[which];
-    const int base = which ? p.side[0].H : 0;
-    const int h_begin = max(first - base, 0), h_end = min(last - base, s.H);
-    if (h_begin >= h_end) continue;
-    const bool per_head = s.w_shead != 0;
-    // the lane's factors a, b of its channels, and where the other halves lie (in elements; 0: not rotated)
-    uint64_t a[kChunks][4], b[kChunks][4];
-    int partner[kChunks];
+  Factors<kChunks> f;
+  auto set_factors = [&](int which) {
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
       const int e = c * 64 + lane8 * 8, off = e - p.begin;
-      const bool in = p.rotate && off >= 0 && off < 2 * p.half;
-      partner[c] = !in ? 0 : kInter ? 1 : off < p.half ? p.half : -p.half;
+      const bool in = partner[c] != 0;
       float fa[8], fb[8];
 #pragma unroll
       for (int i = 0; i < 8; i += 4) {
@@ -168,12 +208,12 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 3 : 2)
           fa[2 * i + 1] *= c4[i];
         }
       } else if (in) {
-        const int f = off < p.half ? off : off - p.half;
+        const int at = off < p.half ? off : off - p.half;
         const float sign = off < p.half ? -1.f : 1.f;
 #pragma unroll
         for (int i = 0; i < 8; i += 4) {
-          const float4 cs = *reinterpret_cast<const float4*>(&s_cos[warp][f + i]);
-          const float4 sn = *reinterpret_cast<const float4*>(&s_sin[warp][f + i]);
+          const float4 cs = *reinterpret_cast<const float4*>(&s_cos[warp][at + i]);
+          const float4 sn = *reinterpret_cast<const float4*>(&s_sin[warp][at + i]);
           const float4 w = *reinterpret_cast<const float4*>(&s_w[which][e + i + partner[c]]);
           fb[i] = sign * sn.x * w.x, fb[i + 1] = sign * sn.y * w.y, fb[i + 2] = sign * sn.z * w.z, fb[i + 3] = sign * sn.w * w.w;
           fa[i] *= cs.x, fa[i + 1] *= cs.y, fa[i + 2] *= cs.z, fa[i + 3] *= cs.w;
@@ -181,83 +221,91 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 3 : 2)
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        a[c][i] = pack_f32x2(fa[2 * i], fa[2 * i + 1]);
-        b[c][i] = pack_f32x2(fb[2 * i], fb[2 * i + 1]);
+        f.a[c][i] = pack_f32x2(fa[2 * i], fa[2 * i + 1]);
+        f.b[c][i] = pack_f32x2(fb[2 * i], fb[2 * i + 1]);
       }
     }
-    const TI* x = static_cast<const TI*>(s.x) + tok * s.x_srow + lane8 * 8;
-    TO* y = static_cast<TO*>(s.y) + tok * s.y_srow + lane8 * 8;
-    Raw8<TI> v[kAhead][kChunks], o[kAhead][kChunks];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-#pragma unroll
-      for (int c = 0; c < kChunks; ++c) o[k][c] = Raw8<TI>{};
+  };
+
 #pragma unroll 1
-    for (int h0 = h_begin; h0 < h_end; h0 += kHeadsPerPass * kAhead) {
+  for (int pass = 0; pass < passes; ++pass) {
+    const int which = pass >= n_pass[0] ? 1 : 0;
+    const NormRopeSide& s = p.side[which];
+    const int h0 = which ? h_begin[1] + (pass - n_pass[0]) * (kHeadsPerPass * kWide) : h_begin[0] + pass * (kHeadsPerPass * kWide);
+    const int end = which ? h_end[1] : h_end[0];
+    const bool per_head = s.w_shead != 0;
+    if (pass == 0 || pass == n_pass[0]) set_factors(which);
+    // the next pass's loads are in flight during this one (its heads are others, so in place they are unwritten)
+    Raw8<TI> nv[kWide][kChunks], no[kWide][kChunks];
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        // past the last head: its values once more, which are not stored
-        const int h = min(h0 + k * kHeadsPerPass + sub, h_end - 1);
-        const TI* const xh = x + h * s.x_shead;
+    for (int k = 0; k < kWide; ++k)
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-          v[k][c].load(xh + c * 64);
-          if (!kInter && partner[c] != 0) o[k][c].load(xh + c * 64 + partner[c]);
-        }
+      for (int c = 0; c < kChunks; ++c) nv[k][c] = v[k][c], no[k][c] = o[k][c];
+    if (pass + 1 < passes) fetch(pass + 1, nv, no);
+    float scale[kWide];
+#pragma unroll
+    for (int k = 0; k < kWide; ++k) {
+      scale[k] = 1.f;
+      if (p.norm) {
+        uint64_t sq2 = 0;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sq2 = fma_f32x2(v[k][c].pair(i), v[k][c].pair(i), sq2);
+        const float2 sq = unpack_f32x2(sq2);
+        float sum = sq.x + sq.y;
+#pragma unroll
+        for (int m = 1; m < kLanesPerHead; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+        scale[k] = rsqrtf(fmaf(sum, 1.f / D, p.eps));
       }
-      float scale[kAhead];
+    }
+    if constexpr (kShuffle) {
+      const int from = lane + partner[0] / 8;  // lanes that are not rotated get their own, and do not use it
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        scale[k] = 1.f;
-        if (p.norm) {
-          uint64_t sq2 = 0;
+      for (int k = 0; k < kWide; ++k)
 #pragma unroll
-          for (int c = 0; c < kChunks; ++c)
+        for (int i = 0; i < 4; ++i) (&o[k][0].r[0].x)[i] = __shfl_sync(0xffffffffu, (&v[k][0].r[0].x)[i], from);
+    }
+    __syncwarp();  // in place: every lane has read what it needs of these heads
+    TO* const y = static_cast<TO*>(s.y) + tok * s.y_srow + lane8 * 8;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sq2 = fma_f32x2(v[k][c].pair(i), v[k][c].pair(i), sq2);
-          const float2 sq = unpack_f32x2(sq2);
-          float sum = sq.x + sq.y;
+    for (int k = 0; k < kWide; ++k) {
+      const int h = h0 + k * kHeadsPerPass + sub;
+      if (h >= end) continue;
+      const uint64_t scale2 = pack_f32x2(scale[k], scale[k]);
+      TO* const yh = y + h * s.y_shead;
 #pragma unroll
-          for (int m = 1; m < kLanesPerHead; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-          scale[k] = rsqrtf(fmaf(sum, 1.f / D, p.eps));
+      for (int c = 0; c < kChunks; ++c) {
+        uint64_t vv[4], oo[4], out[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          vv[i] = v[k][c].pair(i);
+          oo[i] = kInter ? swapped(vv[i]) : o[k][c].pair(i);
         }
-      }
-      __syncwarp();  // in place: every lane has read what it needs of these heads
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const int h = h0 + k * kHeadsPerPass + sub;
-        if (h >= h_end) continue;
-        const uint64_t scale2 = pack_f32x2(scale[k], scale[k]);
-        TO* const yh = y + h * s.y_shead;
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-          uint64_t vv[4], oo[4], out[4];
+        if (per_head) {
+          const int64_t wi = h * s.w_shead + c * 64 + lane8 * 8;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            vv[i] = v[k][c].pair(i);
-            oo[i] = kInter ? swapped(vv[i]) : o[k][c].pair(i);
+            vv[i] = mul_f32x2(vv[i], weight_pair(s, wi + 2 * i));
+            if (!kInter && partner[c] != 0) oo[i] = mul_f32x2(oo[i], weight_pair(s, wi + 2 * i + partner[c]));
+            if (kInter) oo[i] = swapped(vv[i]);
           }
-          if (per_head) {
-            const int64_t wi = h * s.w_shead + c * 64 + lane8 * 8;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              vv[i] = mul_f32x2(vv[i], weight_pair(s, wi + 2 * i));
-              if (!kInter && partner[c] != 0) oo[i] = mul_f32x2(oo[i], weight_pair(s, wi + 2 * i + partner[c]));
-              if (kInter) oo[i] = swapped(vv[i]);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) out[i] = mul_f32x2(vv[i], a[c][i]);
-          if (!kInter || partner[c] != 0) {  // (halves that are not rotated have zeros for partners)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) out[i] = fma_f32x2(oo[i], b[c][i], out[i]);
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) out[i] = mul_f32x2(out[i], scale2);
-          store8(yh + c * 64, out);
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) out[i] = mul_f32x2(vv[i], f.a[c][i]);
+        if (partner[c] != 0) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) out[i] = fma_f32x2(oo[i], f.b[c][i], out[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) out[i] = mul_f32x2(out[i], scale2);
+        store8(yh + c * 64, out);
       }
     }
+#pragma unroll
+    for (int k = 0; k < kWide; ++k)
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) v[k][c] = nv[k][c], o[k][c] = no[k][c];
   }
 }
 

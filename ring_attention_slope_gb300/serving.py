@@ -7,12 +7,12 @@ call runs on the current stream unless it is given one.
 from __future__ import annotations
 
 import ctypes
-
+import struct
 from array import array
 
 import torch
 
-from . import SlopeError, SlopeTensor, _check, load
+from . import SlopeError, _check, load
 
 EXPORTED_SERVING = ["slope_rope_inv_freq", "slope_qk_norm_rope", "slope_attn_varlen", "slope_kv4_block_bytes",
                     "slope_kv4_cache_bytes", "slope_kv4_write", "slope_kv4_read", "slope_kv4_attn",
@@ -34,14 +34,14 @@ class SlopeKV4Cache(ctypes.Structure):
 def declare(lib):
     """Argument types of the calls of slope_serving.h."""
     P = ctypes.POINTER
-    T = P(SlopeTensor)
+    T = ctypes.c_void_p  # a slope_tensor, as the bytes that _desc packs or by reference
     i32, i64, vp, f32, f64 = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float, ctypes.c_double
     size = ctypes.c_size_t
     C = P(SlopeKV4Cache)
     for name, args, res in (
             ("slope_rope_inv_freq", [i32, f64, ctypes.c_int, f64, f64, f64, f64, P(f64), P(f64)], ctypes.c_int),
             ("slope_qk_norm_rope", [T, T, T, T, ctypes.c_int, f32, P(SlopeRope), vp, i64, T, T, vp], ctypes.c_int),
-            ("slope_attn_varlen", [T, T, T, P(i64), i64, ctypes.c_int, i64, f32, T, T, vp], ctypes.c_int),
+            ("slope_attn_varlen", [T, T, T, vp, i64, ctypes.c_int, i64, f32, T, T, vp], ctypes.c_int),
             ("slope_kv4_block_bytes", [i32, i32], size),
             ("slope_kv4_cache_bytes", [i64, i32, i32, i32, i32], size),
             ("slope_kv4_write", [C, T, T, vp, vp], ctypes.c_int),
@@ -53,52 +53,65 @@ def declare(lib):
 
 
 _DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+_pack = struct.Struct("@Pii6q").pack  # slope_tensor
+_device = torch.cuda.current_device
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-# The smallest of these calls takes a few microseconds on the GPU, so its descriptors are made with as few
-# Python operations as they allow.
+# The smallest of these calls takes a few microseconds on the GPU, so a tensor's descriptor is packed as the
+# bytes of a slope_tensor, with as few Python operations as that takes.
 
-def _desc(t):
-    """slope_tensor of a CUDA tensor of rank 2 or 3, or None for None."""
+def _desc(t, dev):
+    """slope_tensor of a tensor of rank 2 or 3 on device number dev, as bytes; None for None."""
     if t is None:
         return None
+    if t.get_device() != dev and t.numel() > 0:
+        _elsewhere(t, dev)
     dt = _DTYPES.get(t.dtype)
     if dt is None:
         raise TypeError(f"unsupported dtype {t.dtype}")
-    shape, stride = t.shape, t.stride()
+    shape = t.shape
     n = len(shape)
-    if n != 3 and n != 2:
-        raise ValueError("tensors must be rank 2 or 3")
-    if not t.is_cuda and t.numel() > 0:
+    if n == 3:
+        return _pack(t.data_ptr(), dt, 3, *shape, *t.stride())
+    if n == 2:
+        return _pack(t.data_ptr(), dt, 2, *shape, 0, *t.stride(), 0)
+    raise ValueError("tensors must be rank 2 or 3")
+
+
+def _weight(t, dev):
+    """slope_tensor of a weight: [H, d], or [d] taken as [1, d]."""
+    if t is not None and t.dim() == 1:
+        if t.get_device() != dev:
+            _elsewhere(t, dev)
+        if t.dtype not in _DTYPES:
+            raise TypeError(f"unsupported dtype {t.dtype}")
+        return _pack(t.data_ptr(), _DTYPES[t.dtype], 2, 1, t.shape[0], 0, t.shape[0], t.stride(0), 0)
+    return _desc(t, dev)
+
+
+def _elsewhere(t, dev):
+    if not t.is_cuda:
         raise TypeError("libslope operates on CUDA tensors")
-    return SlopeTensor(t.data_ptr(), dt, n, tuple(shape), stride)
+    # the launch goes to the current device's stream
+    raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
 
 
-def _here(*tensors):
-    """The tensors' device has to be the current one: the launch goes to the current device's stream."""
-    cur = torch.cuda.current_device() if torch.cuda.is_available() else -1
-    for t in tensors:
-        if t is not None and t.is_cuda and t.get_device() != cur:
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{cur}")
-
-
-def _stream(stream):
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
-
-
-def _index(t, what, n=None):
+def _index(t, what, dev, n=None):
     """Data pointer of a device int32 array (dense, of n elements)."""
     if t.dtype != torch.int32:
         raise TypeError(f"{what} must be int32, got {t.dtype}")
-    if not t.is_cuda and t.numel() > 0:
-        raise TypeError(f"{what} must be a CUDA tensor")
+    if t.get_device() != dev and t.numel() > 0:
+        _elsewhere(t, dev)
     if n is not None and (t.dim() != 1 or t.shape[0] != n):
         raise ValueError(f"{what} must have shape [{n}], got {tuple(t.shape)}")
     if n is not None and n > 1 and t.stride(0) != 1:
         raise ValueError(f"{what} must be contiguous")
     return t.data_ptr()
+
+
+def _stream(stream, dev):
+    return _raw_stream(dev) if stream is None else stream.cuda_stream
 
 
 # ---------------------------------------------------------------- positions
@@ -135,18 +148,14 @@ def qk_norm_rope(q, k=None, *, norm=True, q_weight=None, k_weight=None, eps=1e-6
     (of the inputs' type unless given) may be the inputs.  Returns ``(q_out, k_out)`` (k_out None without k).
     """
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
+        q_out = torch.empty_like(q, dtype=out_dtype)
     if k is not None and k_out is None:
-        k_out = torch.empty(k.shape, dtype=out_dtype or k.dtype, device=k.device)
-    _here(q, k, q_weight, k_weight, positions, q_out, k_out)
-    if q_weight is not None and q_weight.dim() == 1:
-        q_weight = q_weight[None]
-    if k_weight is not None and k_weight.dim() == 1:
-        k_weight = k_weight[None]
-    pos = None if positions is None else _index(positions, "positions", q.shape[0])
-    st = load().slope_qk_norm_rope(_desc(q), _desc(k), _desc(q_weight), _desc(k_weight), 1 if norm else 0, eps,
-                                   None if rope is None else rope._c, pos, pos0, _desc(q_out), _desc(k_out),
-                                   _stream(stream))
+        k_out = torch.empty_like(k, dtype=out_dtype)
+    dev = _device()
+    pos = None if positions is None else _index(positions, "positions", dev, q.shape[0])
+    st = load().slope_qk_norm_rope(_desc(q, dev), _desc(k, dev), _weight(q_weight, dev), _weight(k_weight, dev),
+                                   1 if norm else 0, eps, None if rope is None else rope._c, pos, pos0,
+                                   _desc(q_out, dev), _desc(k_out, dev), _stream(stream, dev))
     _check(st, "slope_qk_norm_rope")
     return q_out, k_out
 
@@ -166,7 +175,6 @@ def attn_varlen(q, k, v, cu_seqlens, *, causal=True, window=0, scale=0.0, out=No
         out = torch.empty((T, Hq, v.shape[2]), dtype=out_dtype or torch.bfloat16, device=q.device)
     if lse is None:
         lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
-    _here(q, k, v, out, lse)
     if isinstance(cu_seqlens, torch.Tensor):
         if cu_seqlens.is_cuda:
             raise TypeError("cu_seqlens lives on the host (reading it back would synchronise)")
@@ -174,9 +182,11 @@ def attn_varlen(q, k, v, cu_seqlens, *, causal=True, window=0, scale=0.0, out=No
     n = len(cu_seqlens)
     if n < 1:
         raise ValueError("cu_seqlens needs at least one entry")
-    cu = (ctypes.c_int64 * n).from_buffer(array("q", cu_seqlens))
-    st = load().slope_attn_varlen(_desc(q), _desc(k), _desc(v), cu, n - 1, 1 if causal else 0, window, scale,
-                                  _desc(out), _desc(lse), _stream(stream))
+    cu = array("q", cu_seqlens)
+    dev = _device()
+    st = load().slope_attn_varlen(_desc(q, dev), _desc(k, dev), _desc(v, dev), cu.buffer_info()[0], n - 1,
+                                  1 if causal else 0, window, scale, _desc(out, dev), _desc(lse, dev),
+                                  _stream(stream, dev))
     _check(st, "slope_attn_varlen")
     return out, lse
 
@@ -208,8 +218,11 @@ class KV4Cache:
 def kv4_write(cache, k, v, slots, *, stream=None):
     """Writes k [T,Hkv,dqk], v [T,Hkv,dv] (bf16 or fp32) into the cache at slots (device int32 [T]; slot = page *
     page_size + index, out of range: skipped; the others distinct)."""
-    _here(cache.data, k, v, slots)
-    st = load().slope_kv4_write(cache._c, _desc(k), _desc(v), _index(slots, "slots", k.shape[0]), _stream(stream))
+    dev = _device()
+    if cache.data.get_device() != dev and cache.n_pages > 0:
+        _elsewhere(cache.data, dev)
+    st = load().slope_kv4_write(cache._c, _desc(k, dev), _desc(v, dev), _index(slots, "slots", dev, k.shape[0]),
+                                _stream(stream, dev))
     _check(st, "slope_kv4_write")
 
 
@@ -221,9 +234,11 @@ def kv4_read(cache, slots, *, k_out=None, v_out=None, out_dtype=None, stream=Non
         k_out = torch.empty((T, cache.Hkv, cache.dqk), dtype=out_dtype or torch.bfloat16, device=cache.data.device)
     if v_out is None:
         v_out = torch.empty((T, cache.Hkv, cache.dv), dtype=out_dtype or torch.bfloat16, device=cache.data.device)
-    _here(cache.data, slots, k_out, v_out)
-    st = load().slope_kv4_read(cache._c, _index(slots, "slots", k_out.shape[0]), _desc(k_out), _desc(v_out),
-                               _stream(stream))
+    dev = _device()
+    if cache.data.get_device() != dev and cache.n_pages > 0:
+        _elsewhere(cache.data, dev)
+    st = load().slope_kv4_read(cache._c, _index(slots, "slots", dev, k_out.shape[0]), _desc(k_out, dev),
+                               _desc(v_out, dev), _stream(stream, dev))
     _check(st, "slope_kv4_read")
     return k_out, v_out
 
@@ -259,11 +274,13 @@ def kv4_attn(q, cache, block_table, kv_lens, *, q_len=1, window=0, scale=0.0, ou
         if nbytes == 0:
             raise SlopeError(-8, "slope_kv4_attn_workspace_size")
         workspace = torch.empty((nbytes,), dtype=torch.uint8, device=q.device)
-    _here(q, cache.data, block_table, kv_lens, out, lse, workspace)
+    dev = _device()
+    if cache.data.get_device() != dev and cache.n_pages > 0:
+        _elsewhere(cache.data, dev)
     pages = block_table.shape[1]
-    st = load().slope_kv4_attn(_desc(q), cache._c, _index(block_table, "block_table"),
-                               block_table.stride(0) if B > 1 else pages, pages, _index(kv_lens, "kv_lens", B), q_len,
-                               window, scale, _desc(out), _desc(lse), workspace.data_ptr(),
-                               workspace.numel() * workspace.element_size(), _stream(stream))
+    st = load().slope_kv4_attn(_desc(q, dev), cache._c, _index(block_table, "block_table", dev),
+                               block_table.stride(0) if B > 1 else pages, pages, _index(kv_lens, "kv_lens", dev, B),
+                               q_len, window, scale, _desc(out, dev), _desc(lse, dev), workspace.data_ptr(),
+                               workspace.nbytes, _stream(stream, dev))
     _check(st, "slope_kv4_attn")
     return out, lse
