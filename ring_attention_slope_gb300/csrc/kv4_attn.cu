@@ -55,7 +55,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxCtas = 640;          // of the attention launch: the workspace has two partials for each
 constexpr int kStep = 32;              // tokens of a step: two blocks, one bulk copy where a page holds both
 constexpr int kMinSteps = kWarps;      // a range is at least this many steps
-constexpr int kPieceSteps = 8;         // steps that a piece's start and end cost, at most (see cta_range)
+constexpr int kPieceSteps = 14;         // steps that a piece's start and end cost, at most (see cta_range)
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kRescale = 8.f;        // the running maximum moves when a score passes it by this (log2)
 constexpr float kNoMax = -1e30f;       // running maximum before any key
@@ -92,15 +92,9 @@ struct Kv4Cfg {
   static constexpr int kKeyBytes = kv4_key_bytes(DQK), kValueBytes = kv4_value_bytes(DV);
   static constexpr int kBlockBytes = kv4_block_bytes(DQK, DV);
   // CTAs on an SM, by registers: 128 a thread at four, 168 at three, 255 at two
-#ifndef KC64
-#define KC64 4
-#define KS64 4
-#define KCW 3
-#define KSW 2
-#endif
-  static constexpr int kCtas = NT == 1 ? (DQK == 64 && DV == 64 ? KC64 : KCW) : (DQK == 64 && DV == 64 ? 3 : 2);
+  static constexpr int kCtas = NT == 1 ? (DQK == 64 && DV == 64 ? 4 : 3) : (DQK == 64 && DV == 64 ? 3 : 2);
   static constexpr int kStageBytes = 2 * kBlockBytes;
-  static constexpr int kStages = NT == 1 ? (DQK == 64 && DV == 64 ? KS64 : KSW) : kCtas > 2 ? 4 : 3;
+  static constexpr int kStages = kCtas > 3 || NT == 2 && kCtas == 3 ? 4 : 2;
   static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
   static constexpr int kRedFloats = kWarps * R * DV + 2 * kWarps * R;
   static constexpr int kSmemBytes = kRingBytes + kRedFloats * 4 + kWarps * kStages * 8 + 64;
@@ -115,32 +109,31 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
+// The products and the transpose below are functions of their operands: not volatile, so that the compiler
+// may interleave independent ones.  Every warp runs them as a whole.
 // d = a b (no accumulator in)
 __device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                               uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 // Transposes an 8x8 matrix of 16-bit elements held two to a lane (row lane / 4, columns 2 (lane % 4) and the next).
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -278,7 +271,9 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
   const CtaRange range = cta_range(p, s_scratch);
   if (threadIdx.x == 0) p.heads[blockIdx.x] = make_int4(-1, 0, 0, 0);
 
-  uint32_t issued = 0, used = 0;  // bulk copies of this warp, over all pieces
+  // the warp's ring: the stages that the next copy fills and the next step reads, and that one's parity
+  int put = 0, get = 0;
+  uint32_t parity = 0;
   int b = range.b;
   int64_t seq_begin = range.seq_begin;
   bool ok = true;
@@ -294,6 +289,19 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
     const int kvh = pair / p.row_tiles, rt = pair - kvh * p.row_tiles;
     const int n_it = max(0, (st1 - st0 - warp + kWarps - 1) / kWarps);
 
+    // ---- the queries' loads, ahead of the pages' and the copies'
+    const int n_rows = p.q_len * p.group;
+    uint4 qraw[NT][C::NG];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int r = rt * C::R + t * 8 + g;
+      const __nv_bfloat16* const qrow = p.q + (static_cast<int64_t>(b) * p.q_len + r / p.group) * p.q_srow +
+                                        (kvh * p.group + r % p.group) * p.q_shead + 8 * q4;
+#pragma unroll
+      for (int G = 0; G < C::NG; ++G)
+        qraw[t][G] = r < n_rows ? *reinterpret_cast<const uint4*>(qrow + 32 * G) : make_uint4(0u, 0u, 0u, 0u);
+    }
+
     // ---- bulk copies: iteration i takes step st0 + warp + 4 i.  Lane i % 32 looks its pages up, 32
     // iterations at a time and those of the next 32 ahead, and starts its copies.
     const int32_t* const row = p.table + b * p.table_stride;
@@ -308,18 +316,23 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
       a = i < n_it ? page_at(pos) : -1;
       c = !small_pages ? a : i < n_it ? page_at(pos + kKv4Block) : -1;
     };
+    const int low_hi = sb.len - p.q_len;                       // smallest last position of any row
+    const int high_lo = p.window > 0 ? sb.len - p.window : 0;  // largest first position
     const uint8_t *src0 = nullptr, *src1 = nullptr;  // of the lane's iteration
-    uint32_t both = 0;                               // bit i % 32: iteration i has both blocks
+    uint32_t tx0 = 0, tx1 = 0;                       // and the bytes of its copies
+    uint32_t plain = 0;  // bit i % 32: every row sees all of iteration i's tokens
     int next0, next1;
     auto refill = [&](int first) {  // the pages of iterations first .. first + 31 are in next0, next1
-      const int blk = (st0 + warp + kWarps * (first + lane)) * 2;
+      const int pos = (st0 + warp + kWarps * (first + lane)) * kStep;
       auto at = [&](int pg, int block) {
         const int in_page = block & ((1 << (p.page_shift - 4)) - 1);
         return p.data + (((static_cast<int64_t>(pg) * p.Hkv + kvh) << (p.page_shift - 4)) + in_page) * C::kBlockBytes;
       };
-      src0 = next0 >= 0 ? at(next0, blk) : nullptr;
-      src1 = next1 >= 0 ? at(next1, blk + 1) : nullptr;
-      both = __ballot_sync(0xffffffffu, next0 >= 0 && next1 >= 0);
+      src0 = at(next0, pos / kKv4Block);
+      src1 = at(next1, pos / kKv4Block + 1);
+      tx0 = next0 < 0 ? 0 : small_pages ? C::kBlockBytes : C::kStageBytes;
+      tx1 = next1 < 0 || !small_pages ? 0 : C::kBlockBytes;
+      plain = __ballot_sync(0xffffffffu, next0 >= 0 && next1 >= 0 && pos + kStep - 1 <= low_hi && pos >= high_lo);
       pages_of(first + 32 + lane, next0, next1);
     };
     pages_of(lane, next0, next1);
@@ -327,17 +340,15 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
     int sent = 0;
     auto send = [&]() {
       if (sent >= n_it || !ok) return;
-      if (sent > 0 && (sent & 31) == 0) refill(sent);
+      if ((sent & 31) == 0 && sent > 0) refill(sent);
       if (lane == (sent & 31)) {
-        uint64_t* const bar = &full[issued % C::kStages];
-        uint8_t* const dst = ring + (issued % C::kStages) * C::kStageBytes;
-        const uint32_t bytes0 = src0 == nullptr ? 0 : small_pages ? C::kBlockBytes : C::kStageBytes;
-        const uint32_t bytes1 = small_pages && src1 != nullptr ? C::kBlockBytes : 0;
-        mbar_arrive_expect_tx(bar, bytes0 + bytes1);
-        if (bytes0 != 0) bulk_load(dst, src0, bytes0, bar);
-        if (bytes1 != 0) bulk_load(dst + C::kBlockBytes, src1, bytes1, bar);
+        uint64_t* const bar = &full[put];
+        uint8_t* const dst = ring + put * C::kStageBytes;
+        mbar_arrive_expect_tx(bar, tx0 + tx1);
+        if (tx0 != 0) bulk_load(dst, src0, tx0, bar);
+        if (tx1 != 0) bulk_load(dst + C::kBlockBytes, src1, tx1, bar);
       }
-      ++issued;
+      put = put == C::kStages - 1 ? 0 : put + 1;
       ++sent;
     };
     for (int i = 0; i < C::kStages - 1; ++i) send();
@@ -347,18 +358,12 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
     float qsum[NT][C::NG][2];  // of rows 2 q4 and 2 q4 + 1, in the units of the products
     float sl2[NT][2];
     int hi[NT][2];             // last position those rows see
-    const int n_rows = p.q_len * p.group;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const int r = rt * C::R + t * 8 + g;
-      uint4 w[C::NG];
+      const uint4(&w)[C::NG] = qraw[t];
       float top = 0.f;
 #pragma unroll
       for (int G = 0; G < C::NG; ++G) {
-        w[G] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < n_rows)
-          w[G] = *reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(b) * p.q_len + r / p.group) * p.q_srow +
-                                                 (kvh * p.group + r % p.group) * p.q_shead + 32 * G + 8 * q4);
         const uint32_t x[4] = {w[G].x, w[G].y, w[G].z, w[G].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -401,8 +406,6 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
         hi[t][j] = sb.len - p.q_len + min(rj / p.group, p.q_len - 1);
       }
     }
-    const int low_hi = sb.len - p.q_len;                                              // smallest hi of any row
-    const int high_lo = p.window > 0 ? sb.len - p.window : 0;                         // largest first position
 
     // ---- the steps
     float nm[NT][2], l[NT][2], bias[NT][C::NV][2], o[C::NC][2][2][NT][4];  // nm: 64 - running maximum
@@ -422,12 +425,12 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[c][i >> 1][i & 1][t][e] = 0.f;
     }
-    // One step: its blocks in `mem`, tokens from position pos0 on.  kEdge: some row does not see some of its
-    // keys (bit j of `none`: block j is not there at all).
-    auto step = [&](auto edge_c, const uint8_t* const mem, const int pos0, const int none) {
+    // A step in three phases.  kEdge: some row does not see some of its keys.
+    // Scores of the 32 tokens from position pos0 on, whose blocks lie in `mem` (bit j of `none`: block j is not
+    // there at all).
+    auto scores = [&](auto edge_c, const uint8_t* const mem, const int pos0, const int none, float(&x)[2][NT][4]) {
       constexpr bool kEdge = decltype(edge_c)::value;
       // scores of keys g (elements 0, 1) and g + 8 (2, 3) of both blocks for rows 2 q4 and 2 q4 + 1
-      float x[2][NT][4];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const uint8_t* const blk_mem = mem + j * C::kBlockBytes;
@@ -485,9 +488,11 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
               if ((none >> j & 1) || pos > last || (p.window > 0 && last - pos >= p.window)) x[j][t][e] = -INFINITY;
             }
       }
+    };
+    // Their weights times 2^64, and the running maximum and sum.
+    auto weights = [&](const float(&x)[2][NT][4], float(&w)[2][NT][4]) {
       // y: log2 of the weight times 2^64.  A row whose score passes the running maximum by 2^8 moves it
       // (any other weight stays below 2^8).
-      float w[2][NT][4];
       float top = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 2; ++j)
@@ -527,6 +532,19 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
           }
       }
 #pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[j][t][e] = ex2_approx(w[j][t][e]);
+          l[t][0] += w[j][t][0] + w[j][t][2];
+          l[t][1] += w[j][t][1] + w[j][t][3];
+        }
+    };
+    // The weighted values.
+    auto accumulate = [&](auto edge_c, const uint8_t* const mem, const float(&w)[2][NT][4]) {
+      constexpr bool kEdge = decltype(edge_c)::value;
+#pragma unroll
       for (int j = 0; j < 2; ++j) {
         const uint8_t* const blk_mem = mem + j * C::kBlockBytes;
         uint32_t word[2][C::NV];
@@ -543,11 +561,7 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
         uint32_t pb[NT][C::NV][2];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          float(&ww)[4] = w[j][t];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) ww[e] = ex2_approx(ww[e]);
-          l[t][0] += ww[0] + ww[2];
-          l[t][1] += ww[1] + ww[3];
+          const float(&ww)[4] = w[j][t];
 #pragma unroll
           for (int G = 0; G < C::NV; ++G) {
             float s[4], n[4];  // scale and min by element
@@ -556,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
             if constexpr (kEdge) {  // a hidden key's scale and min may be anything, NaN too
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                if (x[j][t][e] == -INFINITY) s[e] = n[e] = 0.f;
+                if (ww[e] == 0.f) s[e] = n[e] = 0.f;
             }
             bias[t][G][0] = fmaf(ww[0], n[0], fmaf(ww[2], n[2], bias[t][G][0]));
             bias[t][G][1] = fmaf(ww[1], n[1], fmaf(ww[3], n[3], bias[t][G][1]));
@@ -583,27 +597,44 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
         }
       }
     };
-    uint32_t have = 0;  // `both` of this iteration's 32
+
+    uint32_t mask = 0;  // `plain` of this iteration's 32
+    float x[2][NT][4], w[2][NT][4];
     for (int it = 0; it < n_it; ++it) {
-      if ((it & 31) == 0) have = both;  // sending is at most a few iterations ahead
+      if ((it & 31) == 0) mask = plain;  // sending is at most a few iterations ahead
       // refill first: the stage it takes was read in the last iteration
       __syncwarp();
       send();
-      const uint32_t stage = used % C::kStages, parity = (used / C::kStages) & 1u;
-      ++used;
-      ok = ok && wait_bounded(&full[stage], parity, &s_abort, p.status, p.wait_limit_ns, 20);
-      if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
-        break;
+      if (!__all_sync(0xffffffffu, mbar_try_wait(&full[get], parity))) {
+        ok = wait_bounded(&full[get], parity, &s_abort, p.status, p.wait_limit_ns, 20);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) {
+          sent -= it;  // copies that no step has taken
+          break;
+        }
       }
-      const uint8_t* const mem = ring + stage * C::kStageBytes;
-      const int pos0 = (st0 + warp + kWarps * it) * kStep;
-      if (pos0 + kStep - 1 <= low_hi && pos0 >= high_lo && (have >> (it & 31) & 1u)) {
-        step(std::false_type{}, mem, pos0, 0);
+      const uint8_t* const mem = ring + get * C::kStageBytes;
+      get = get == C::kStages - 1 ? 0 : get + 1;
+      parity ^= get == 0 ? 1u : 0u;
+      if (mask & 1u) {
+        scores(std::false_type{}, mem, 0, 0, x);
+        weights(x, w);
+        accumulate(std::false_type{}, mem, w);
       } else {
         int pg0, pg1;
         pages_of(it, pg0, pg1);
-        step(std::true_type{}, mem, pos0, (pg0 < 0 ? 1 : 0) | (pg1 < 0 ? 2 : 0));
+        scores(std::true_type{}, mem, (st0 + warp + kWarps * it) * kStep, (pg0 < 0 ? 1 : 0) | (pg1 < 0 ? 2 : 0), x);
+        weights(x, w);
+        accumulate(std::true_type{}, mem, w);
+      }
+      mask >>= 1;
+    }
+    if (!ok) {
+      // the copies still in flight land before anything else uses the CTA's shared memory
+      for (; sent > 0; --sent) {
+        wait_final(&full[get], parity, p.wait_limit_ns);
+        get = get == C::kStages - 1 ? 0 : get + 1;
+        parity ^= get == 0 ? 1u : 0u;
       }
     }
 
@@ -671,38 +702,52 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
       ++b;
     }
   }
-  if (!ok) {
-    // the copies still in flight land before the CTA gives its shared memory back
-    for (uint32_t i = used; i < issued; ++i) wait_final(&full[i % C::kStages], (i / C::kStages) & 1u, p.wait_limit_ns);
-  }
 }
 
 // Joins the partials of a pair that several CTAs share: CTA c takes the one that CTA c of the
-// attention launch began and did not finish.  Fixed order, so the same result every time.
+// attention launch began and did not finish.  Fixed order, so the same result every time.  A thread has
+// four channels of one row, and eight partials' loads in flight: latency is all that this launch costs.
 template <int DV, int R>
 __global__ void __launch_bounds__(kThreads) kv4_join_kernel(const __grid_constant__ Kv4AttnParams p) {
   pdl_wait();
   const int4 head = p.heads[blockIdx.x];
   if (head.x < 0) return;
-  constexpr int kFloats = 2 * R + R * DV;
+  constexpr int kFloats = 2 * R + R * DV, kAhead = 8;
+  static_assert(R * DV / 4 % kThreads == 0, "whole CTAs of four channels");
+  const int i = blockIdx.y * kThreads + threadIdx.x;
+  const int rr = i / (DV / 4), ch = (i % (DV / 4)) * 4;
   const int first = blockIdx.x, n = head.z - first + 1;
-  // the first CTA's partial is its second, the others' their first
-  auto part = [&](int i) { return p.partials + (static_cast<int64_t>(first + i) * 2 + (i == 0 ? 1 : 0)) * kFloats; };
-  for (int i = threadIdx.x; i < R * DV / 4; i += kThreads) {
-    const int rr = i / (DV / 4), ch = (i % (DV / 4)) * 4;
-    float mm = kNoMax;
-    for (int c = 0; c < n; ++c) mm = fmaxf(mm, part(c)[rr]);
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    float ll = 0.f;
-    for (int c = 0; c < n; ++c) {
-      const float f = ex2_approx(part(c)[rr] - mm);
-      const float4 v = *reinterpret_cast<const float4*>(part(c) + 2 * R + rr * DV + ch);
-      ll = fmaf(f, part(c)[R + rr], ll);
-      sum.x = fmaf(f, v.x, sum.x), sum.y = fmaf(f, v.y, sum.y);
-      sum.z = fmaf(f, v.z, sum.z), sum.w = fmaf(f, v.w, sum.w);
+  float mm = kNoMax, ll = 0.f;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c0 = 0; c0 < n; c0 += kAhead) {
+    float m[kAhead], l[kAhead];
+    float4 v[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int c = min(c0 + k, n - 1);
+      // the first CTA's partial is its second, the others' their first
+      const float* const part = p.partials + (static_cast<int64_t>(first + c) * 2 + (c == 0 ? 1 : 0)) * kFloats;
+      m[k] = part[rr];
+      l[k] = part[R + rr];
+      v[k] = *reinterpret_cast<const float4*>(part + 2 * R + rr * DV + ch);
     }
-    store_row<DV, R>(p, head.x, head.y, rr, ch, sum, mm, ll);
+    float now = mm;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) now = fmaxf(now, m[k]);
+    const float alpha = ex2_approx(mm - now);
+    mm = now;
+    ll *= alpha;
+    sum.x *= alpha, sum.y *= alpha, sum.z *= alpha, sum.w *= alpha;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (c0 + k >= n) break;
+      const float f = ex2_approx(m[k] - now);
+      ll = fmaf(f, l[k], ll);
+      sum.x = fmaf(f, v[k].x, sum.x), sum.y = fmaf(f, v[k].y, sum.y);
+      sum.z = fmaf(f, v[k].z, sum.z), sum.w = fmaf(f, v[k].w, sum.w);
+    }
   }
+  store_row<DV, R>(p, head.x, head.y, rr, ch, sum, mm, ll);
 }
 
 constexpr int kMaxDevices = 64;
@@ -739,7 +784,7 @@ cudaError_t launch_nt(Kv4AttnParams p, cudaStream_t stream) {
   kv4_attn_kernel<DQK, DV, NT><<<grid, kThreads, C::kSmemBytes, stream>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), C::R * DV / 4 / kThreads);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
