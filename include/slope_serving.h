@@ -113,7 +113,7 @@ SLOPE_API slope_status slope_qk_norm_rope(const slope_tensor* q, const slope_ten
  * too, does not reach a sequence's rows.  Within a sequence a key or value that
  * is not finite may also make rows NaN that the causal mask or the window keeps
  * from it, where a 128-key tile holds both.
- * Consecutive sequences share a launch up to 32 of them.
+ * Sequences share a launch up to 128 of them, the longest first.
  */
 SLOPE_API slope_status slope_attn_varlen(const slope_tensor* q, const slope_tensor* k, const slope_tensor* v,
                                          const int64_t* cu_seqlens, int64_t n_seqs, int causal, int64_t window,

@@ -497,13 +497,12 @@ cudaError_t record(Timing* tm, bool before, int kind, cudaStream_t stream) {
 // what this one writes.  Launches timed with events run the ordinary way.
 slope_status run_attention(const std::vector<WorkItem>& group, int dqk, int dv, const CUtensorMap& tq,
                            const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& to, AttnParams base,
-                           bool dependent, Timing* tm, cudaStream_t stream, bool packed = false) {
+                           bool dependent, Timing* tm, cudaStream_t stream) {
   base.n_items = static_cast<int32_t>(group.size());
   for (size_t i = 0; i < group.size(); ++i) base.items[i] = group[i];
   cudaError_t e;
   if ((e = record(tm, true, 0, stream)) != cudaSuccess) return cuda_fail("cudaEventRecord", e);
-  const auto launch = packed ? launch_attn_packed : launch_attn_partial;
-  if ((e = launch(dqk, dv, tq, tk, tv, to, base, dependent && tm == nullptr, stream)) != cudaSuccess)
+  if ((e = launch_attn_partial(dqk, dv, tq, tk, tv, to, base, dependent && tm == nullptr, stream)) != cudaSuccess)
     return cuda_fail("attention kernel launch", e);
   if ((e = record(tm, false, 0, stream)) != cudaSuccess) return cuda_fail("cudaEventRecord", e);
   return SLOPE_OK;
@@ -965,27 +964,25 @@ slope_status slope_attn_varlen(const slope_tensor* q, const slope_tensor* k, con
                      : 0;
   if (!base.out_tma) to = tq;  // never used
 
-  // One item per sequence: its rows against its own rows as keys, at their row numbers as positions
-  // (the masks only take differences).
+  // A sequence's rows against its own rows as keys, at their row numbers as positions (the masks only take
+  // differences).  The longest first, so that a launch's last work tiles are its lightest.
   try {
-    std::vector<PItem> items;
-    items.reserve(static_cast<size_t>(n_seqs));
+    std::vector<PackedSeq> seqs;
+    seqs.reserve(static_cast<size_t>(n_seqs));
     for (int64_t s = 0; s < n_seqs; ++s) {
       const int64_t len = cu_seqlens[s + 1] - cu_seqlens[s];
-      if (len == 0) continue;
-      PItem it{};
-      it.q_row0 = cu_seqlens[s];
-      it.q_len = len;
-      it.n_kv = 1;
-      it.kv[0] = Range{cu_seqlens[s], len};
-      items.push_back(it);
+      if (len > 0) seqs.push_back(PackedSeq{static_cast<int32_t>(cu_seqlens[s]), static_cast<int32_t>(len), 0});
     }
-    std::vector<std::vector<WorkItem>> groups;
-    if (!pack_items(std::move(items), causal, Hq, false, groups)) return SLOPE_ERR_UNSUPPORTED;
-    for (size_t g = 0; g < groups.size(); ++g)
-      if ((st = run_attention(groups[g], static_cast<int>(dqk), static_cast<int>(dv), tq, tk, tv, to, base, g > 0,
-                              nullptr, static_cast<cudaStream_t>(stream), true)) != SLOPE_OK)
-        return st;
+    std::stable_sort(seqs.begin(), seqs.end(), [](const PackedSeq& a, const PackedSeq& b) { return a.len > b.len; });
+    for (size_t i = 0; i < seqs.size(); i += kMaxPacked) {
+      const size_t n = std::min<size_t>(kMaxPacked, seqs.size() - i);
+      base.n_items = static_cast<int32_t>(n);
+      std::copy(seqs.begin() + i, seqs.begin() + i + n, base.seqs);
+      // a launch after the first is independent of the one before it and may start as that one's CTAs leave
+      const cudaError_t e = launch_attn_packed(static_cast<int>(dqk), static_cast<int>(dv), tq, tk, tv, to, base, i > 0,
+                                               static_cast<cudaStream_t>(stream));
+      if (e != cudaSuccess) return cuda_fail("attention kernel launch", e);
+    }
   } catch (const std::exception&) {  // out of host memory for the list of sequences
     return SLOPE_ERR_UNSUPPORTED;
   }

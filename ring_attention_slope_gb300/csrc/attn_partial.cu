@@ -45,6 +45,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "kernels.cuh"
 #include "sm103_ptx.cuh"
@@ -271,11 +272,27 @@ __device__ __forceinline__ int tile_head(const AttnParams& p, const Tile& T, int
 // tiles in increasing w, so the item index never decreases and the scan resumes there.
 // kGrouped: tiles run unit group by unit group (p.head_group units each); otherwise every
 // unit of an item is inner to its row blocks.
+template <bool PK>
+using Item = std::conditional_t<PK, PackedSeq, WorkItem>;
+
 template <bool kGrouped, int QT, bool PK>
-__device__ __forceinline__ void decode_tile(const AttnParams& p, const WorkItem* items, int w, Tile& T, int& ii) {
+__device__ __forceinline__ void decode_tile(const AttnParams& p, const Item<PK>* items, int w, Tile& T, int& ii) {
   const int ushift = PK ? p.pack_shift : p.pair_heads;  // head units per item = h_count >> ushift
-  while (ii < p.n_items - 1 && w >= items[ii].tile_begin + items[ii].n_blocks * (items[ii].h_count >> ushift)) ++ii;
-  T.itm = items[ii];
+  if constexpr (PK) {
+    while (ii < p.n_items - 1 && w >= items[ii + 1].tile_begin) ++ii;
+    const PackedSeq seq = items[ii];
+    const int rows_shift = (QT == 2 ? 8 : 7) - p.pack_shift;  // tokens of a work tile
+    T.itm.q_row0 = T.itm.out_row0 = T.itm.kv[0].row0 = seq.row0;
+    T.itm.q_len = T.itm.kv[0].len = seq.len;
+    T.itm.n_kv = 1;
+    T.itm.tile_begin = seq.tile_begin;
+    T.itm.n_blocks = (seq.len + (1 << rows_shift) - 1) >> rows_shift;
+    T.itm.h_begin = 0;
+    T.itm.h_count = p.Hq;
+  } else {
+    while (ii < p.n_items - 1 && w >= items[ii].tile_begin + items[ii].n_blocks * (items[ii].h_count >> ushift)) ++ii;
+    T.itm = items[ii];
+  }
   const int local = w - T.itm.tile_begin;
   int unit;
   if constexpr (kGrouped) {
@@ -407,11 +424,11 @@ __global__ void __launch_bounds__(K1Cfg<DQK, DV, QT>::kThreads, K1Cfg<DQK, DV, Q
     fence_barrier_init();
   }
   // work items into shared memory: dynamically indexed parameter reads miss the constant cache
-  WorkItem* sItems = reinterpret_cast<WorkItem*>(smem + C::kItemsOffset);
+  Item<PK>* sItems = reinterpret_cast<Item<PK>*>(smem + C::kItemsOffset);
   {
-    const uint32_t* src = reinterpret_cast<const uint32_t*>(p.items);
+    const uint32_t* src = PK ? reinterpret_cast<const uint32_t*>(p.seqs) : reinterpret_cast<const uint32_t*>(p.items);
     uint32_t* dst = reinterpret_cast<uint32_t*>(sItems);
-    const int words = p.n_items * static_cast<int>(sizeof(WorkItem) / 4);
+    const int words = p.n_items * static_cast<int>(sizeof(Item<PK>) / 4);
     for (int i = threadIdx.x; i < words; i += blockDim.x) dst[i] = src[i];
   }
   if (threadIdx.x == kTmaWarp * 32) {
@@ -907,9 +924,15 @@ __global__ void __launch_bounds__(K1Cfg<DQK, DV, QT>::kThreads, K1Cfg<DQK, DV, Q
       };
       // the item's fields are read from shared memory where they are used, rather than kept in
       // registers across the steps, which need every register they can get
-      const WorkItem& sit = sItems[item_hint];
-      for (int r = 0; r < sit.n_kv && ok; ++r) {
-        const KvRange kr = sit.kv[r];
+      const Item<PK>& sit = sItems[item_hint];
+      int n_kv = 1;
+      if constexpr (!PK) n_kv = sit.n_kv;
+      for (int r = 0; r < n_kv && ok; ++r) {
+        KvRange kr;
+        if constexpr (PK)
+          kr = KvRange{sit.row0, sit.len};
+        else
+          kr = sit.kv[r];
         const TileRange R = tile_range(kr.row0, kr.len, qa_t, qb_t, p);
         // PK: both Q tiles' ranges of key tiles make one without a gap, which the CTA steps through
         int lo_cta = R.lo;
@@ -944,9 +967,15 @@ __global__ void __launch_bounds__(K1Cfg<DQK, DV, QT>::kThreads, K1Cfg<DQK, DV, Q
       // the wait for the tile's last PV.
       const bool valid_row = (PK ? row >> p.pack_shift : row) < rows_t;
       const int head = tile_head<PK>(p, T, t) + (PK ? row & ((1 << p.pack_shift) - 1) : 0);
+      int64_t out_row0, plane = 0;
+      if constexpr (PK) {
+        out_row0 = sit.row0;
+      } else {
+        out_row0 = sit.out_row0;
+        plane = sit.plane;
+      }
       const int64_t orow =
-          static_cast<int64_t>(sit.out_row0) + tile_row0<C::kQTiles, PK>(p, T, t) + (PK ? row >> p.pack_shift : row);
-      const int64_t plane = sit.plane;
+          out_row0 + tile_row0<C::kQTiles, PK>(p, T, t) + (PK ? row >> p.pack_shift : row);
       if (valid_row) {
         p.lse[plane * p.lse_splane + orow * p.lse_srow + static_cast<int64_t>(head) * p.lse_shead] =
             l > 0.f ? (m_used + lg2_approx(l)) * kLn2 : -INFINITY;
@@ -1132,11 +1161,11 @@ int gcd_int(int a, int b) {
 int tile_head_group(const AttnParams& p, long long grid, bool dynamic_tiles) {
   int common = 0, max_blocks = 1;
   for (int i = 0; i < p.n_items; ++i) {
-    common = gcd_int(common, p.items[i].h_count >> (p.pair_heads + p.pack_shift));
+    common = gcd_int(common, p.items[i].h_count >> p.pair_heads);
     max_blocks = std::max(max_blocks, static_cast<int>(p.items[i].n_blocks));
   }
   if (common <= 0) return 1;
-  if ((p.group >> p.pack_shift) >= 4) return common;
+  if (p.group >= 4) return common;
   if (dynamic_tiles) return 1;
   const long long want = (grid + max_blocks - 1) / max_blocks;
   for (int hg = 1; hg < common; ++hg)
@@ -1150,19 +1179,26 @@ cudaError_t launch_impl(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
   using C = K1Cfg<DQK, DV, QT>;
   if (p.n_items <= 0) return cudaSuccess;
   long long tiles;
-  if constexpr (QT == 1 || PK) {
+  if constexpr (PK) {
+    // work tiles of QT times 128 >> pack_shift tokens of 2^pack_shift heads
+    const int rows = QT * (kBlockM >> p.pack_shift);
+    tiles = 0;
+    for (int i = 0; i < p.n_items; ++i) {
+      if (tiles > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+      p.seqs[i].tile_begin = static_cast<int32_t>(tiles);
+      tiles += static_cast<long long>((p.seqs[i].len + rows - 1) / rows) * (p.Hq >> p.pack_shift);
+    }
+  } else if constexpr (QT == 1) {
     // one Q tile per CTA: work tiles of 128 rows of one head, counted here (the plan counts
-    // them for two Q tiles); packed heads: QT tiles of 128 >> pack_shift rows of 2^pack_shift heads
+    // them for two Q tiles)
     p.pair_heads = 0;
-    const int rows = PK ? QT * (kBlockM >> p.pack_shift) : kBlockM;
-    const int unit_shift = PK ? p.pack_shift : 0;
     tiles = 0;
     for (int i = 0; i < p.n_items; ++i) {
       WorkItem& it = p.items[i];
-      it.n_blocks = (it.q_len + rows - 1) / rows;
+      it.n_blocks = (it.q_len + kBlockM - 1) / kBlockM;
       if (tiles > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
       it.tile_begin = static_cast<int32_t>(tiles);
-      tiles += static_cast<long long>(it.n_blocks) * (it.h_count >> unit_shift);
+      tiles += static_cast<long long>(it.n_blocks) * it.h_count;
     }
   } else {
     const WorkItem& last = p.items[p.n_items - 1];
@@ -1173,7 +1209,10 @@ cudaError_t launch_impl(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
   if (tiles > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   p.total_tiles = static_cast<int32_t>(tiles);
   const long long grid = std::min<long long>(tiles, resident_ctas() * C::kMinBlocks);
-  p.head_group = C::kGroupedTiles ? tile_head_group(p, grid, C::kDynamicTiles) : 0;
+  if constexpr (PK)  // (grouped tiles are also the ones claimed at run time: see tile_head_group)
+    p.head_group = !C::kGroupedTiles ? 0 : (p.group >> p.pack_shift) >= 4 ? p.Hq >> p.pack_shift : 1;
+  else
+    p.head_group = C::kGroupedTiles ? tile_head_group(p, grid, C::kDynamicTiles) : 0;
   if (C::kDynamicTiles) {
     p.tile_counter = claim_tile_counter();
     if (p.tile_counter == nullptr) return cudaErrorInvalidDevice;

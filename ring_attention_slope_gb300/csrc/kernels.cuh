@@ -44,6 +44,16 @@ struct WorkItem {
 };
 static_assert(sizeof(WorkItem) % 4 == 0, "work items are copied as 32-bit words");
 
+// One sequence of a packed launch: its rows are the queries and the keys.  What a WorkItem says beyond that
+// follows from the launch (every head, one plane), so that many short sequences share a launch.
+struct PackedSeq {
+  int32_t row0;
+  int32_t len;
+  int32_t tile_begin;  // first work tile; set by the launcher
+};
+constexpr int kMaxPacked = 128;  // sequences per packed launch
+static_assert(kMaxPacked * sizeof(PackedSeq) <= kMaxItems * sizeof(WorkItem), "they share the items' room");
+
 struct AttnParams {
   int32_t n_items;
   int32_t total_tiles;      // work tiles (sum over items of row blocks x heads); set by the launcher
@@ -72,7 +82,10 @@ struct AttnParams {
   uint32_t* tile_counter;   // 0 at launch: work tiles claimed so far (kernels that claim them at run
                             // time); set by the launcher
   uint64_t wait_limit_ns;   // bound on every barrier wait
-  WorkItem items[kMaxItems];
+  union {
+    WorkItem items[kMaxItems];
+    PackedSeq seqs[kMaxPacked];  // of a packed launch
+  };
 };
 
 // ---------------------------------------------------------------- merge (K2)

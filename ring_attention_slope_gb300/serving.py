@@ -37,10 +37,10 @@ def declare(lib):
     T = ctypes.c_void_p  # a slope_tensor, as the bytes that _desc packs or by reference
     i32, i64, vp, f32, f64 = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float, ctypes.c_double
     size = ctypes.c_size_t
-    C = P(SlopeKV4Cache)
+    C = ctypes.c_void_p  # a slope_kv4_cache, likewise
     for name, args, res in (
             ("slope_rope_inv_freq", [i32, f64, ctypes.c_int, f64, f64, f64, f64, P(f64), P(f64)], ctypes.c_int),
-            ("slope_qk_norm_rope", [T, T, T, T, ctypes.c_int, f32, P(SlopeRope), vp, i64, T, T, vp], ctypes.c_int),
+            ("slope_qk_norm_rope", [T, T, T, T, ctypes.c_int, f32, vp, vp, i64, T, T, vp], ctypes.c_int),
             ("slope_attn_varlen", [T, T, T, vp, i64, ctypes.c_int, i64, f32, T, T, vp], ctypes.c_int),
             ("slope_kv4_block_bytes", [i32, i32], size),
             ("slope_kv4_cache_bytes", [i64, i32, i32, i32, i32], size),
@@ -54,6 +54,8 @@ def declare(lib):
 
 _DTYPES = {torch.bfloat16: 0, torch.float32: 1}
 _pack = struct.Struct("@Pii6q").pack  # slope_tensor
+_pack_rope = struct.Struct("@iiifP").pack  # slope_rope
+_pack_cache = struct.Struct("@Pqiiii").pack  # slope_kv4_cache
 _device = torch.cuda.current_device
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
@@ -133,10 +135,9 @@ class Rope:
     pairs channels 2i and 2i + 1, else i and i + half; both cos and sin are multiplied by ``attention_factor``."""
 
     def __init__(self, inv_freq, *, begin=0, interleaved=False, attention_factor=1.0):
-        freq = array("d", inv_freq)
-        n = len(freq)
-        self._c = SlopeRope(int(begin), 2 * n, int(bool(interleaved)), float(attention_factor),
-                            (ctypes.c_double * n).from_buffer(freq) if n else None)
+        self._freq = freq = array("d", inv_freq)
+        address, n = freq.buffer_info()
+        self._c = _pack_rope(begin, 2 * n, 1 if interleaved else 0, attention_factor, address)
 
 
 def qk_norm_rope(q, k=None, *, norm=True, q_weight=None, k_weight=None, eps=1e-6, rope=None, positions=None, pos0=0,
@@ -198,21 +199,20 @@ class KV4Cache:
     of dqk key and dv value channels.  ``data`` (uint8, CUDA, dense) is allocated unless given."""
 
     def __init__(self, n_pages, page_size, Hkv, dqk, dv, *, data=None, device="cuda"):
-        nbytes = int(load().slope_kv4_cache_bytes(int(n_pages), int(page_size), int(Hkv), int(dqk), int(dv)))
-        if nbytes == 0 and int(n_pages) != 0:
+        nbytes = load().slope_kv4_cache_bytes(n_pages, page_size, Hkv, dqk, dv)
+        if nbytes == 0 and n_pages != 0:
             raise SlopeError(-8, "slope_kv4_cache_bytes")
         if data is None:
             data = torch.empty((nbytes,), dtype=torch.uint8, device=device)
-        if data.dtype != torch.uint8 or not data.is_contiguous():
+        elif data.dtype != torch.uint8 or not data.is_contiguous():
             raise TypeError("the cache's data must be a dense uint8 tensor")
-        if nbytes > 0 and data.device.type != "cuda":
-            raise TypeError("the cache's data must be a CUDA tensor")
-        if data.numel() < nbytes:
+        elif data.numel() < nbytes:
             raise ValueError(f"the cache needs {nbytes} bytes, data holds {data.numel()}")
+        if nbytes > 0 and not data.is_cuda:
+            raise TypeError("the cache's data must be a CUDA tensor")
         self.data = data
-        self.n_pages, self.page_size, self.Hkv, self.dqk, self.dv = (int(x) for x in (n_pages, page_size, Hkv, dqk, dv))
-        self._c = SlopeKV4Cache(data.data_ptr() if nbytes else None, self.n_pages, self.page_size, self.Hkv, self.dqk,
-                                self.dv)
+        self.n_pages, self.page_size, self.Hkv, self.dqk, self.dv = n_pages, page_size, Hkv, dqk, dv
+        self._c = _pack_cache(data.data_ptr() if nbytes else 0, n_pages, page_size, Hkv, dqk, dv)
 
 
 def kv4_write(cache, k, v, slots, *, stream=None):
@@ -245,7 +245,7 @@ def kv4_read(cache, slots, *, k_out=None, v_out=None, out_dtype=None, stream=Non
 
 def kv4_attn_workspace_size(B, Hq, cache, q_len=1) -> int:
     """Workspace bytes of :func:`kv4_attn` (0 for arguments it does not support)."""
-    return int(load().slope_kv4_attn_workspace_size(int(B), int(Hq), cache._c, int(q_len)))
+    return load().slope_kv4_attn_workspace_size(B, Hq, cache._c, q_len)
 
 
 def kv4_attn(q, cache, block_table, kv_lens, *, q_len=1, window=0, scale=0.0, out=None, lse=None, workspace=None,

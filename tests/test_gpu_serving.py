@@ -456,7 +456,8 @@ def packed(lens, Hq, H, dqk, dv, seed, lead=0, tail=0):
     return rand(T, Hq, dqk, seed=seed, scale=s), rand(T, H, dqk, seed=seed + 1, scale=s), rand(T, H, dv, seed=seed + 2, scale=s), cu
 
 
-@pytest.mark.parametrize("lens", [[1], [5, 1, 0, 16, 17], [127, 128, 129], [300, 2, 515], [1] * 70, [0, 0, 33, 0]])
+@pytest.mark.parametrize("lens", [[1], [5, 1, 0, 16, 17], [127, 128, 129], [300, 2, 515], [1] * 70, [0, 0, 33, 0],
+                                  [(7 * i) % 23 for i in range(300)]])
 @pytest.mark.parametrize("Hq,H", [(8, 1), (4, 4), (6, 2), (12, 2)])
 def test_varlen_lengths(lens, Hq, H):
     check_varlen(*packed(lens, Hq, H, 64, 64, 140))

@@ -53,6 +53,13 @@ def test_header_compiles_as_c99_and_matches_the_binding(tmp_path):
                            str(src), "-o", str(exe)])
     got = [tuple(int(x) for x in line.split()) for line in subprocess.check_output([str(exe)], text=True).splitlines()]
     cls = {"slope_rope": slope.SlopeRope, "slope_kv4_cache": slope.SlopeKV4Cache}
+    # the packed forms that the binding passes are the same bytes
+    freq = (ctypes.c_double * 8)()
+    packed = slope.serving._pack_rope(3, 16, 1, 0.5, ctypes.addressof(freq))
+    assert packed == bytes(slope.SlopeRope(3, 16, 1, 0.5, freq))
+    assert slope.serving._pack_cache(4096, 7, 64, 2, 128, 64) == bytes(slope.SlopeKV4Cache(4096, 7, 64, 2, 128, 64))
+    whole = slope.SlopeTensor(4096, 1, 3, (5, 6, 7), (8, 9, 1))
+    assert slope.serving._pack(4096, 1, 3, 5, 6, 7, 8, 9, 1) == bytes(whole)
     for (s, f), have in zip(fields, got):
         field = getattr(cls[s], f)
         assert have == (field.offset, field.size), (s, f)
@@ -108,15 +115,12 @@ def test_inv_freq_refusals(lib):
 # ---------------------------------------------------------------- norm and rotation
 
 def rope(dim=64, begin=0, factor=1.0, freq=None, null=False):
-    r = slope.Rope([1.0] * (dim // 2) if freq is None else freq, begin=begin, attention_factor=factor)
-    r._c.dim = dim
-    if null:
-        r._c.inv_freq = None
-    return r
+    freq = [1.0] * (dim // 2) if freq is None else freq
+    return slope.SlopeRope(begin, dim, 0, factor, None if null else (ctypes.c_double * len(freq))(*freq))
 
 
 def norm_rope(lib, q=None, k=None, qw=None, kw=None, norm=1, eps=1e-6, r=None, pos=None, pos0=0, qo=None, ko=None):
-    return lib.slope_qk_norm_rope(ref(q), ref(k), ref(qw), ref(kw), norm, eps, ref(r._c) if r else None, pos, pos0,
+    return lib.slope_qk_norm_rope(ref(q), ref(k), ref(qw), ref(kw), norm, eps, ref(r), pos, pos0,
                                   ref(qo), ref(ko), None)
 
 
