@@ -26,13 +26,13 @@
 // The block layout in memory is the operand layout, so a lane's codes of 16 keys
 // are its own 16-byte words; P^T needs one 8x8 transpose (movmatrix) a group.
 //
-// Work split: every sequence's visible 32-token steps, for each KV head (and each
+// Work split: every sequence's visible steps of 64 or 32 tokens, for each KV head (and each
 // tile of 8 NT query rows), laid end to end and cut into equal ranges, one for each
 // CTA of a grid that fills the GPU once.  The cut knows the lengths only on the
 // device, so ragged batches and captured graphs balance alike.  A range's pieces that
 // are not whole (sequence, head) pairs leave partials (m, l, unnormalised out) in the
 // workspace, and a second launch, queued as a programmatic dependent, joins them in a
-// fixed order.  Inside a CTA four warps take every fourth step of 32 tokens, each with its
+// fixed order.  Inside a CTA four warps take every fourth step, each with its
 // own ring of bulk copies, and join once at the end of a piece.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -53,9 +53,8 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxCtas = 640;          // of the attention launch: the workspace has two partials for each
-constexpr int kStep = 32;              // tokens of a step: two blocks, one bulk copy where a page holds both
 constexpr int kMinSteps = kWarps;      // a range is at least this many steps
-constexpr int kPieceSteps = 14;         // steps that a piece's start and end cost, at most (see cta_range)
+constexpr int kPieceTokens = 448;      // what a piece's start and end cost, in tokens of steps, at most (see cta_range)
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kRescale = 8.f;        // the running maximum moves when a score passes it by this (log2)
 constexpr float kNoMax = -1e30f;       // running maximum before any key
@@ -93,8 +92,10 @@ struct Kv4Cfg {
   static constexpr int kBlockBytes = kv4_block_bytes(DQK, DV);
   // CTAs on an SM, by registers: 128 a thread at four, 168 at three, 255 at two
   static constexpr int kCtas = NT == 1 ? (DQK == 64 && DV == 64 ? 4 : 3) : (DQK == 64 && DV == 64 ? 3 : 2);
-  static constexpr int kStageBytes = 2 * kBlockBytes;
-  static constexpr int kStages = kCtas > 3 || NT == 2 && kCtas == 3 ? 4 : 2;
+  // tokens of a step, which costs about a hundred instructions whatever its size: four blocks, or two wide ones
+  static constexpr int kStep = kBlockBytes <= 1280 ? 64 : 32, kStepLog = kStep == 64 ? 6 : 5;
+  static constexpr int kStageBytes = kStep / kKv4Block * kBlockBytes;
+  static constexpr int kStages = kCtas == 2 ? 3 : 2;
   static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
   static constexpr int kRedFloats = kWarps * R * DV + 2 * kWarps * R;
   static constexpr int kSmemBytes = kRingBytes + kRedFloats * 4 + kWarps * kStages * 8 + 64;
@@ -141,12 +142,13 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// The keys of a sequence that some of its queries see, in steps of 32 tokens.
+// The keys of a sequence that some of its queries see, in steps of 64 or 32 tokens.
 struct SeqSteps {
   int len;    // tokens in the cache
   int first;  // first step
   int count;  // steps, at least 1 (a sequence without keys still has rows to write)
 };
+template <int kStep>
 __device__ __forceinline__ SeqSteps seq_steps(const Kv4AttnParams& p, int b) {
   SeqSteps s;
   const int64_t n = p.kv_lens[b];
@@ -167,17 +169,18 @@ struct CtaRange {
 
 // Every thread of the CTA calls it; `scratch` holds kWarps + 3 values.
 //
-// A pair's fixed cost (its queries, its first copies' latency, the join of the warps) is worth about eight
-// steps.  Without it in the cut, a batch with many short sequences gave one CTA the tail of all of them:
+// A pair's fixed cost (its queries, its first copies' latency, the join of the warps) is worth about 450
+// tokens.  Without it in the cut, a batch with many short sequences gave one CTA the tail of all of them:
 // 32 sequences of 8 .. 32768 tokens took 148 us.  Where a range has few steps in all, the cost is
 // taken as half of them, so that a small call still spreads over the CTAs.
+template <int kStep>
 __device__ CtaRange cta_range(const Kv4AttnParams& p, int64_t* scratch) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int pairs = p.Hkv * p.row_tiles;
   int64_t steps = 0;
   for (int b0 = 0; b0 < p.B; b0 += kThreads) {
     const int b = b0 + threadIdx.x;
-    if (b < p.B) steps += seq_steps(p, b).count;
+    if (b < p.B) steps += seq_steps<kStep>(p, b).count;
   }
 #pragma unroll
   for (int m = 16; m > 0; m >>= 1) steps += __shfl_xor_sync(0xffffffffu, steps, m);
@@ -189,7 +192,7 @@ __device__ CtaRange cta_range(const Kv4AttnParams& p, int64_t* scratch) {
   steps *= pairs;
   CtaRange r;
   const int64_t even = (steps + gridDim.x - 1) / gridDim.x;
-  r.cost = static_cast<int>(min(static_cast<int64_t>(kPieceSteps), even / 2));
+  r.cost = static_cast<int>(min(static_cast<int64_t>(kPieceTokens / kStep), even / 2));
   const int64_t total = steps + static_cast<int64_t>(p.B) * pairs * r.cost;
   r.per = max(static_cast<int64_t>(kMinSteps), (total + gridDim.x - 1) / gridDim.x);
   r.begin = min(total, static_cast<int64_t>(blockIdx.x) * r.per);
@@ -201,7 +204,7 @@ __device__ CtaRange cta_range(const Kv4AttnParams& p, int64_t* scratch) {
   int64_t carry = 0;
   for (int b0 = 0; b0 < p.B; b0 += kThreads) {
     const int b = b0 + threadIdx.x;
-    const int64_t mine = b < p.B ? static_cast<int64_t>(seq_steps(p, b).count + r.cost) * pairs : 0;
+    const int64_t mine = b < p.B ? static_cast<int64_t>(seq_steps<kStep>(p, b).count + r.cost) * pairs : 0;
     int64_t incl = mine;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
@@ -249,6 +252,7 @@ template <int DQK, int DV, int NT>
 __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
     kv4_attn_kernel(const __grid_constant__ Kv4AttnParams p) {
   using C = Kv4Cfg<DQK, DV, NT>;
+  constexpr int kStep = C::kStep;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t s_scratch[kWarps + 3];
   __shared__ int s_abort;
@@ -268,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
     fence_barrier_init();
   }
   __syncthreads();
-  const CtaRange range = cta_range(p, s_scratch);
+  const CtaRange range = cta_range<kStep>(p, s_scratch);
   if (threadIdx.x == 0) p.heads[blockIdx.x] = make_int4(-1, 0, 0, 0);
 
   // the warp's ring: the stages that the next copy fills and the next step reads, and that one's parity
@@ -279,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
   bool ok = true;
   for (int64_t u = range.begin; u < range.end;) {
     // ---- the piece: steps [st0, st1) of one pair
-    const SeqSteps sb = seq_steps(p, b);
+    const SeqSteps sb = seq_steps<kStep>(p, b);
     const int pair_units = sb.count + range.cost;
     const int pair = static_cast<int>((u - seq_begin) / pair_units);
     const int64_t pair_begin = seq_begin + static_cast<int64_t>(pair) * pair_units, pair_end = pair_begin + pair_units;
@@ -302,52 +306,47 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
         qraw[t][G] = r < n_rows ? *reinterpret_cast<const uint4*>(qrow + 32 * G) : make_uint4(0u, 0u, 0u, 0u);
     }
 
-    // ---- bulk copies: iteration i takes step st0 + warp + 4 i.  Lane i % 32 looks its pages up, 32
-    // iterations at a time and those of the next 32 ahead, and starts its copies.
+    // ---- bulk copies: iteration i takes step st0 + warp + 4 i, in one copy or, where a page is smaller than a
+    // step, in two or four.  Each lane looks one copy's page up, 32 at a time and the next 32 ahead, and starts it.
     const int32_t* const row = p.table + b * p.table_stride;
-    const bool small_pages = p.page_shift == 4;  // a step's two blocks lie in two pages
-    auto page_at = [&](int pos) -> int {  // -1: no such token, or a page outside the cache
-      if (pos >= sb.len) return -1;
+    const int cs = max(0, C::kStepLog - p.page_shift);                   // log2 of an iteration's copies
+    const int low_hi = sb.len - p.q_len;                       // smallest last position of any row
+    const int high_lo = p.window > 0 ? sb.len - p.window : 0;  // largest first position
+    auto pos_of = [&](int copy) { return (st0 + warp + kWarps * (copy >> cs)) * kStep + ((copy & ((1 << cs) - 1)) << (C::kStepLog - cs)); };
+    auto page_of = [&](int copy) -> int {  // -1: no such step or token, or a page outside the cache
+      const int pos = pos_of(copy);
+      if ((copy >> cs) >= n_it || pos >= sb.len) return -1;
       const int pg = row[pos >> p.page_shift];
       return pg >= 0 && pg < p.n_pages ? pg : -1;
     };
-    auto pages_of = [&](int i, int& a, int& c) {
-      const int pos = (st0 + warp + kWarps * i) * kStep;
-      a = i < n_it ? page_at(pos) : -1;
-      c = !small_pages ? a : i < n_it ? page_at(pos + kKv4Block) : -1;
+    const uint8_t* src = nullptr;                               // of the lane's copy
+    const uint32_t copy_bytes = C::kStageBytes >> cs;
+    uint32_t there = 0;  // bit: the copy has a page
+    uint32_t plain = 0;  // bit of an iteration's first copy: every row sees all of its step's tokens
+    int next_page;
+    auto refill = [&](int first) {  // the pages of copies first .. first + 31 are in next_page
+      const int pos = pos_of(first + lane);
+      const int in_page = (pos / kKv4Block) & ((1 << (p.page_shift - 4)) - 1);
+      src = p.data + (((static_cast<int64_t>(next_page) * p.Hkv + kvh) << (p.page_shift - 4)) + in_page) * C::kBlockBytes;
+      there = __ballot_sync(0xffffffffu, next_page >= 0);
+      plain = __ballot_sync(0xffffffffu, next_page >= 0 && pos + (kStep >> cs) - 1 <= low_hi && pos >= high_lo);
+      if (cs > 0) plain &= plain >> 1;
+      if (cs > 1) plain &= plain >> 2;
+      next_page = page_of(first + 32 + lane);
     };
-    const int low_hi = sb.len - p.q_len;                       // smallest last position of any row
-    const int high_lo = p.window > 0 ? sb.len - p.window : 0;  // largest first position
-    const uint8_t *src0 = nullptr, *src1 = nullptr;  // of the lane's iteration
-    uint32_t tx0 = 0, tx1 = 0;                       // and the bytes of its copies
-    uint32_t plain = 0;  // bit i % 32: every row sees all of iteration i's tokens
-    int next0, next1;
-    auto refill = [&](int first) {  // the pages of iterations first .. first + 31 are in next0, next1
-      const int pos = (st0 + warp + kWarps * (first + lane)) * kStep;
-      auto at = [&](int pg, int block) {
-        const int in_page = block & ((1 << (p.page_shift - 4)) - 1);
-        return p.data + (((static_cast<int64_t>(pg) * p.Hkv + kvh) << (p.page_shift - 4)) + in_page) * C::kBlockBytes;
-      };
-      src0 = at(next0, pos / kKv4Block);
-      src1 = at(next1, pos / kKv4Block + 1);
-      tx0 = next0 < 0 ? 0 : small_pages ? C::kBlockBytes : C::kStageBytes;
-      tx1 = next1 < 0 || !small_pages ? 0 : C::kBlockBytes;
-      plain = __ballot_sync(0xffffffffu, next0 >= 0 && next1 >= 0 && pos + kStep - 1 <= low_hi && pos >= high_lo);
-      pages_of(first + 32 + lane, next0, next1);
-    };
-    pages_of(lane, next0, next1);
+    next_page = page_of(lane);
     refill(0);
-    int sent = 0;
+    int sent = 0;  // iterations
     auto send = [&]() {
       if (sent >= n_it || !ok) return;
-      if ((sent & 31) == 0 && sent > 0) refill(sent);
-      if (lane == (sent & 31)) {
-        uint64_t* const bar = &full[put];
-        uint8_t* const dst = ring + put * C::kStageBytes;
-        mbar_arrive_expect_tx(bar, tx0 + tx1);
-        if (tx0 != 0) bulk_load(dst, src0, tx0, bar);
-        if (tx1 != 0) bulk_load(dst + C::kBlockBytes, src1, tx1, bar);
-      }
+      const int at = (sent << cs) & 31;
+      if (at == 0 && sent > 0) refill(sent << cs);
+      uint64_t* const bar = &full[put];
+      const bool mine = lane >> cs == at >> cs;
+      if (lane == at) mbar_arrive_expect_tx(bar, __popc(there >> at & ((2u << ((1 << cs) - 1)) - 1u)) * copy_bytes);
+      __syncwarp();
+      if (mine && (there >> lane & 1u))
+        bulk_load(ring + put * C::kStageBytes + (lane - at) * copy_bytes, src, copy_bytes, bar);
       put = put == C::kStages - 1 ? 0 : put + 1;
       ++sent;
     };
@@ -425,9 +424,9 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[c][i >> 1][i & 1][t][e] = 0.f;
     }
-    // A step in three phases.  kEdge: some row does not see some of its keys.
-    // Scores of the 32 tokens from position pos0 on, whose blocks lie in `mem` (bit j of `none`: block j is not
-    // there at all).
+    // Half a step in three phases.  kEdge: some row does not see some of its keys.
+    // Scores of 32 tokens, a half of a step, from position pos0 on, whose two blocks lie in `mem` (bit j of
+    // `none`: block j is not there at all).
     auto scores = [&](auto edge_c, const uint8_t* const mem, const int pos0, const int none, float(&x)[2][NT][4]) {
       constexpr bool kEdge = decltype(edge_c)::value;
       // scores of keys g (elements 0, 1) and g + 8 (2, 3) of both blocks for rows 2 q4 and 2 q4 + 1
@@ -598,10 +597,10 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
       }
     };
 
-    uint32_t mask = 0;  // `plain` of this iteration's 32
+    uint32_t mask = 0;  // `plain` from this iteration on
     float x[2][NT][4], w[2][NT][4];
     for (int it = 0; it < n_it; ++it) {
-      if ((it & 31) == 0) mask = plain;  // sending is at most a few iterations ahead
+      if (((it << cs) & 31) == 0) mask = plain;  // sending is at most a few iterations ahead
       // refill first: the stage it takes was read in the last iteration
       __syncwarp();
       send();
@@ -617,17 +616,25 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
       get = get == C::kStages - 1 ? 0 : get + 1;
       parity ^= get == 0 ? 1u : 0u;
       if (mask & 1u) {
-        scores(std::false_type{}, mem, 0, 0, x);
-        weights(x, w);
-        accumulate(std::false_type{}, mem, w);
+#pragma unroll 1
+        for (int half = 0; half < kStep / 32; ++half) {
+          const uint8_t* const m = mem + half * 2 * C::kBlockBytes;
+          scores(std::false_type{}, m, 0, 0, x);
+          weights(x, w);
+          accumulate(std::false_type{}, m, w);
+        }
       } else {
-        int pg0, pg1;
-        pages_of(it, pg0, pg1);
-        scores(std::true_type{}, mem, (st0 + warp + kWarps * it) * kStep, (pg0 < 0 ? 1 : 0) | (pg1 < 0 ? 2 : 0), x);
-        weights(x, w);
-        accumulate(std::true_type{}, mem, w);
+#pragma unroll 1
+        for (int half = 0; half < kStep / 32; ++half) {
+          const uint8_t* const m = mem + half * 2 * C::kBlockBytes;
+          const int pos = (st0 + warp + kWarps * it) * kStep + half * 32;
+          auto none = [&](int at) { return page_of((it << cs) + ((at & (kStep - 1)) >> (C::kStepLog - cs))) < 0 ? 1 : 0; };
+          scores(std::true_type{}, m, pos, none(pos) | none(pos + kKv4Block) << 1, x);
+          weights(x, w);
+          accumulate(std::true_type{}, m, w);
+        }
       }
-      mask >>= 1;
+      mask >>= 1 << cs;
     }
     if (!ok) {
       // the copies still in flight land before anything else uses the CTA's shared memory
