@@ -54,7 +54,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxCtas = 640;          // of the attention launch: the workspace has two partials for each
 constexpr int kMinSteps = kWarps;      // a range is at least this many steps
-constexpr int kPieceTokens = 448;      // what a piece's start and end cost, in tokens of steps, at most (see cta_range)
+constexpr int kPieceTokens = 800;      // what a piece's start and end cost, in tokens of steps, at most (see cta_range)
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kRescale = 8.f;        // the running maximum moves when a score passes it by this (log2)
 constexpr float kNoMax = -1e30f;       // running maximum before any key
@@ -169,7 +169,7 @@ struct CtaRange {
 
 // Every thread of the CTA calls it; `scratch` holds kWarps + 3 values.
 //
-// A pair's fixed cost (its queries, its first copies' latency, the join of the warps) is worth about 450
+// A pair's fixed cost (its queries, its first copies' latency, the join of the warps) is worth about 800
 // tokens.  Without it in the cut, a batch with many short sequences gave one CTA the tail of all of them:
 // 32 sequences of 8 .. 32768 tokens took 148 us.  Where a range has few steps in all, the cost is
 // taken as half of them, so that a small call still spreads over the CTAs.
