@@ -13,9 +13,10 @@
 // exact and has at most 22 bits, as for bf16 values within 2^14 of each other, that decides every code: a
 // quotient that is a half comes out as that half (and halves, common among bf16 values, round to even), and
 // one that is not differs from it by a place of d at least, more than rounding to 24 bits can bridge.
-// Otherwise (fp32 values, or bf16 ones further apart) d's own rounding moves the quotient by at most 2^-24 of
-// 16, and one closer than 1e-5 to a half is decided again from error-free differences (not in fp64, of which
-// this GPU does two operations a clock: with that path the 12K-token store took 39 us).
+// Otherwise (fp32 values, bf16 ones further apart, scales whose remainders may be subnormal) a code next to a
+// half is decided again from error-free differences: d's own rounding moves the quotient by at most 2^-24 of 16,
+// so 1e-5 is near enough.  (Not in fp64, of which an SM does two operations a clock: with that path the
+// 12K-token store took 39 us.)
 #include <cuda_bf16.h>
 
 #include <cfloat>
@@ -170,7 +171,7 @@ __device__ __forceinline__ Quantised quantise(const Raw8<T>& x) {
   }
   bool again;
   if constexpr (sizeof(T) == 2) {
-    again = ex.small * 16384.f < fabsf(mn) || fmaxf(fabsf(lo), fabsf(hi)) > 16384.f * fabsf(mn);
+    again = ex.small * 16384.f < fabsf(mn) || fmaxf(fabsf(lo), fabsf(hi)) > 16384.f * fabsf(mn) || scale < 0x1p-100f;
   } else {
     float off = 0.f;  // largest distance from the nearest integer
 #pragma unroll
@@ -178,7 +179,7 @@ __device__ __forceinline__ Quantised quantise(const Raw8<T>& x) {
       const float2 a = unpack_f32x2(t[i]), b = unpack_f32x2(r[i]);
       off = fmaxf(off, fmaxf(fabsf(a.x - (b.x - kRound)), fabsf(a.y - (b.y - kRound))));
     }
-    again = off > 0.5f - 1e-5f;
+    again = off > 0.5f - 1e-5f || scale < 0x1p-100f;
   }
   if (again && scale > 0.f) {
 #pragma unroll
@@ -382,10 +383,10 @@ slope_status prepare_store(const slope_kv4_cache* cache, const slope_tensor* k, 
 
 dim3 store_grid(Kv4StoreParams& p) {
   const int64_t tx = (p.T + kTokens - 1) / kTokens;
-  // a CTA takes one head at a time, and more in turn once that leaves about two waves of eight CTAs on
+  // a CTA takes one head at a time, and more in turn while more than about 32 CTAs are left for
   // each of the 152 SMs
   p.per_cta = kHeadsPerPass;
-  while (p.per_cta < p.Hkv && tx * ((p.Hkv + p.per_cta - 1) / p.per_cta) > 2432) p.per_cta *= 2;
+  while (p.per_cta < p.Hkv && tx * ((p.Hkv + p.per_cta - 1) / p.per_cta) > 4864) p.per_cta *= 2;
   return dim3(static_cast<unsigned>(tx), static_cast<unsigned>((p.Hkv + p.per_cta - 1) / p.per_cta));
 }
 

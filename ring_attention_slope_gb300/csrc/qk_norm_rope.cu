@@ -31,7 +31,7 @@
 namespace slope {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kLanesPerHead = 8;
 constexpr int kHeadsPerPass = 32 / kLanesPerHead;  // heads a warp takes at a time
@@ -109,7 +109,7 @@ struct Factors {
 
 // kInter: pairs are neighbours (and a pair's partner is in the same lane's channels), else halves.
 template <typename TI, typename TO, int D, bool kInter>
-__global__ void __launch_bounds__(kThreads, D == 64 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, D == 64 ? 6 : 4)
     qk_norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
   __shared__ __align__(16) float s_cos[kWarps][kMaxHalf], s_sin[kWarps][kMaxHalf];  // of the warp's token
   __shared__ __align__(16) float s_w[2][D];  // weights shared by every head of a side, else 1
