@@ -1,4 +1,5 @@
-"""Builds ``libslope.so`` (the CUDA kernels and the C ABI) in-tree with nvcc for sm_103a.
+"""Builds ``libslope.so`` (the CUDA kernels and the C ABI) in-tree with nvcc for sm_103a, and
+``_marshal.so``, the Python binding's argument marshalling in C.
 
 Translation units are compiled in parallel and linked into one shared
 library next to this file.  The library is rebuilt only when a source or
@@ -9,6 +10,7 @@ from __future__ import annotations
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -17,6 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libslope.so")
+MARSHAL_PATH = os.path.join(PKG, "_marshal.so")
 
 SOURCES = ["attn_partial.cu", "kv4_attn.cu", "api.cu", "lse_merge.cu", "qk_norm_rope.cu", "kv4_store.cu", "status.cu",
            "dck.cpp", "rope.cpp"]
@@ -34,10 +37,10 @@ def nvcc() -> str:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(MARSHAL_PATH):
         return True
-    t = os.path.getmtime(LIB_PATH)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(MARSHAL_PATH))
+    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS + ["marshal.c"]]
     deps += [os.path.join(INCLUDE, f) for f in ("slope.h", "slope_serving.h")] + [__file__]
     return any(os.path.getmtime(d) > t for d in deps)
 
@@ -59,8 +62,19 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(r.stdout, r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    def compile_marshal():
+        tmp = MARSHAL_PATH + f".tmp{os.getpid()}"
+        cmd = [shutil.which("gcc") or "cc", "-O2", "-Wall", "-Wextra", "-shared", "-fPIC", "-fvisibility=hidden",
+               "-I", sysconfig.get_paths()["include"], "-I", INCLUDE, os.path.join(CSRC, "marshal.c"), "-o", tmp]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"{cmd[0]} failed for marshal.c:\n{r.stdout}\n{r.stderr}")
+        return tmp
+
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        marshal = ex.submit(compile_marshal)
         objs = list(ex.map(compile_one, SOURCES))
+    os.replace(marshal.result(), MARSHAL_PATH)
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     r = subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:

@@ -1,8 +1,9 @@
 """The calls around the prefill attention (``include/slope_serving.h``): head norm with rotation, packed
 prompts, the 4-bit paged key/value cache and attention over it.
 
-Argument marshalling only, as in the package's ``__init__``: tensors have to lie on the current device, and a
-call runs on the current stream unless it is given one.
+Defaults and outputs are made here; the arguments go to the library through the C module ``_marshal``
+(``csrc/marshal.c``), because the smallest of these calls take a few microseconds.  Tensors have to lie on the
+current device, and a call runs on the current stream unless it is given one.
 """
 from __future__ import annotations
 
@@ -34,10 +35,10 @@ class SlopeKV4Cache(ctypes.Structure):
 def declare(lib):
     """Argument types of the calls of slope_serving.h."""
     P = ctypes.POINTER
-    T = ctypes.c_void_p  # a slope_tensor, as the bytes that _desc packs or by reference
+    T = ctypes.c_void_p  # a slope_tensor by reference
     i32, i64, vp, f32, f64 = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float, ctypes.c_double
     size = ctypes.c_size_t
-    C = ctypes.c_void_p  # a slope_kv4_cache, likewise
+    C = ctypes.c_void_p  # a slope_kv4_cache, by reference or as packed bytes
     for name, args, res in (
             ("slope_rope_inv_freq", [i32, f64, ctypes.c_int, f64, f64, f64, f64, P(f64), P(f64)], ctypes.c_int),
             ("slope_qk_norm_rope", [T, T, T, T, ctypes.c_int, f32, vp, vp, i64, T, T, vp], ctypes.c_int),
@@ -52,64 +53,24 @@ def declare(lib):
         fn.argtypes, fn.restype = args, res
 
 
-_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
-_pack = struct.Struct("@Pii6q").pack  # slope_tensor
 _pack_rope = struct.Struct("@iiifP").pack  # slope_rope
 _pack_cache = struct.Struct("@Pqiiii").pack  # slope_kv4_cache
 _device = torch.cuda.current_device
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_marshal = None  # the C module, once load() has found the library
 
 
-# The smallest of these calls takes a few microseconds on the GPU, so a tensor's descriptor is packed as the
-# bytes of a slope_tensor, with as few Python operations as that takes.
+def _bound():
+    """The C module, bound to the library's calls."""
+    global _marshal
+    lib = load()
+    from . import _marshal as m
 
-def _desc(t, dev):
-    """slope_tensor of a tensor of rank 2 or 3 on device number dev, as bytes; None for None."""
-    if t is None:
-        return None
-    if t.get_device() != dev and t.numel() > 0:
-        _elsewhere(t, dev)
-    dt = _DTYPES.get(t.dtype)
-    if dt is None:
-        raise TypeError(f"unsupported dtype {t.dtype}")
-    shape = t.shape
-    n = len(shape)
-    if n == 3:
-        return _pack(t.data_ptr(), dt, 3, *shape, *t.stride())
-    if n == 2:
-        return _pack(t.data_ptr(), dt, 2, *shape, 0, *t.stride(), 0)
-    raise ValueError("tensors must be rank 2 or 3")
-
-
-def _weight(t, dev):
-    """slope_tensor of a weight: [H, d], or [d] taken as [1, d]."""
-    if t is not None and t.dim() == 1:
-        if t.get_device() != dev:
-            _elsewhere(t, dev)
-        if t.dtype not in _DTYPES:
-            raise TypeError(f"unsupported dtype {t.dtype}")
-        return _pack(t.data_ptr(), _DTYPES[t.dtype], 2, 1, t.shape[0], 0, t.shape[0], t.stride(0), 0)
-    return _desc(t, dev)
-
-
-def _elsewhere(t, dev):
-    if not t.is_cuda:
-        raise TypeError("libslope operates on CUDA tensors")
-    # the launch goes to the current device's stream
-    raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
-
-
-def _index(t, what, dev, n=None):
-    """Data pointer of a device int32 array (dense, of n elements)."""
-    if t.dtype != torch.int32:
-        raise TypeError(f"{what} must be int32, got {t.dtype}")
-    if t.get_device() != dev and t.numel() > 0:
-        _elsewhere(t, dev)
-    if n is not None and (t.dim() != 1 or t.shape[0] != n):
-        raise ValueError(f"{what} must have shape [{n}], got {tuple(t.shape)}")
-    if n is not None and n > 1 and t.stride(0) != 1:
-        raise ValueError(f"{what} must be contiguous")
-    return t.data_ptr()
+    address = lambda f: ctypes.cast(f, ctypes.c_void_p).value  # noqa: E731
+    m.bind(torch.bfloat16, torch.float32, torch.int32, address(lib.slope_qk_norm_rope), address(lib.slope_attn_varlen),
+           address(lib.slope_kv4_write), address(lib.slope_kv4_read), address(lib.slope_kv4_attn))
+    _marshal = m
+    return m
 
 
 def _stream(stream, dev):
@@ -153,10 +114,8 @@ def qk_norm_rope(q, k=None, *, norm=True, q_weight=None, k_weight=None, eps=1e-6
     if k is not None and k_out is None:
         k_out = torch.empty_like(k, dtype=out_dtype)
     dev = _device()
-    pos = None if positions is None else _index(positions, "positions", dev, q.shape[0])
-    st = load().slope_qk_norm_rope(_desc(q, dev), _desc(k, dev), _weight(q_weight, dev), _weight(k_weight, dev),
-                                   1 if norm else 0, eps, None if rope is None else rope._c, pos, pos0,
-                                   _desc(q_out, dev), _desc(k_out, dev), _stream(stream, dev))
+    st = (_marshal or _bound()).qk_norm_rope(q, k, q_weight, k_weight, norm, eps, None if rope is None else rope._c,
+                                             positions, pos0, q_out, k_out, _stream(stream, dev), dev)
     _check(st, "slope_qk_norm_rope")
     return q_out, k_out
 
@@ -180,14 +139,9 @@ def attn_varlen(q, k, v, cu_seqlens, *, causal=True, window=0, scale=0.0, out=No
         if cu_seqlens.is_cuda:
             raise TypeError("cu_seqlens lives on the host (reading it back would synchronise)")
         cu_seqlens = cu_seqlens.tolist()
-    n = len(cu_seqlens)
-    if n < 1:
-        raise ValueError("cu_seqlens needs at least one entry")
-    cu = array("q", cu_seqlens)
     dev = _device()
-    st = load().slope_attn_varlen(_desc(q, dev), _desc(k, dev), _desc(v, dev), cu.buffer_info()[0], n - 1,
-                                  1 if causal else 0, window, scale, _desc(out, dev), _desc(lse, dev),
-                                  _stream(stream, dev))
+    st = (_marshal or _bound()).attn_varlen(q, k, v, cu_seqlens, causal, window, scale, out, lse,
+                                            _stream(stream, dev), dev)
     _check(st, "slope_attn_varlen")
     return out, lse
 
@@ -214,15 +168,19 @@ class KV4Cache:
         self.n_pages, self.page_size, self.Hkv, self.dqk, self.dv = n_pages, page_size, Hkv, dqk, dv
         self._c = _pack_cache(data.data_ptr() if nbytes else 0, n_pages, page_size, Hkv, dqk, dv)
 
+    def device_now(self):
+        """The current device, which the cache's data has to be on."""
+        dev = _device()
+        if self.data.get_device() != dev and self.n_pages > 0:
+            raise ValueError(f"cache on {self.data.device}, but the current device is cuda:{dev}")
+        return dev
+
 
 def kv4_write(cache, k, v, slots, *, stream=None):
     """Writes k [T,Hkv,dqk], v [T,Hkv,dv] (bf16 or fp32) into the cache at slots (device int32 [T]; slot = page *
     page_size + index, out of range: skipped; the others distinct)."""
-    dev = _device()
-    if cache.data.get_device() != dev and cache.n_pages > 0:
-        _elsewhere(cache.data, dev)
-    st = load().slope_kv4_write(cache._c, _desc(k, dev), _desc(v, dev), _index(slots, "slots", dev, k.shape[0]),
-                                _stream(stream, dev))
+    dev = cache.device_now()
+    st = (_marshal or _bound()).kv4_write(cache._c, k, v, slots, _stream(stream, dev), dev)
     _check(st, "slope_kv4_write")
 
 
@@ -234,11 +192,8 @@ def kv4_read(cache, slots, *, k_out=None, v_out=None, out_dtype=None, stream=Non
         k_out = torch.empty((T, cache.Hkv, cache.dqk), dtype=out_dtype or torch.bfloat16, device=cache.data.device)
     if v_out is None:
         v_out = torch.empty((T, cache.Hkv, cache.dv), dtype=out_dtype or torch.bfloat16, device=cache.data.device)
-    dev = _device()
-    if cache.data.get_device() != dev and cache.n_pages > 0:
-        _elsewhere(cache.data, dev)
-    st = load().slope_kv4_read(cache._c, _index(slots, "slots", dev, k_out.shape[0]), _desc(k_out, dev),
-                               _desc(v_out, dev), _stream(stream, dev))
+    dev = cache.device_now()
+    st = (_marshal or _bound()).kv4_read(cache._c, slots, k_out, v_out, _stream(stream, dev), dev)
     _check(st, "slope_kv4_read")
     return k_out, v_out
 
@@ -261,26 +216,15 @@ def kv4_attn(q, cache, block_table, kv_lens, *, q_len=1, window=0, scale=0.0, ou
         out = torch.empty((T, Hq, cache.dv), dtype=out_dtype or torch.bfloat16, device=q.device)
     if lse is None and want_lse:
         lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
-    q_len = int(q_len)
-    if q_len < 1 or T % q_len != 0:
-        raise ValueError(f"q has {T} rows, not a multiple of q_len = {q_len}")
-    B = T // q_len
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError(f"block_table must have shape [{B}, pages], got {tuple(block_table.shape)}")
-    if block_table.shape[1] > 1 and block_table.stride(1) != 1:
-        raise ValueError("block_table rows must be contiguous")
     if workspace is None:
-        nbytes = kv4_attn_workspace_size(B, Hq, cache, q_len)
+        nbytes = load().slope_kv4_attn_workspace_size(block_table.shape[0], Hq, cache._c, q_len)
         if nbytes == 0:
             raise SlopeError(-8, "slope_kv4_attn_workspace_size")
         workspace = torch.empty((nbytes,), dtype=torch.uint8, device=q.device)
-    dev = _device()
-    if cache.data.get_device() != dev and cache.n_pages > 0:
-        _elsewhere(cache.data, dev)
-    pages = block_table.shape[1]
-    st = load().slope_kv4_attn(_desc(q, dev), cache._c, _index(block_table, "block_table", dev),
-                               block_table.stride(0) if B > 1 else pages, pages, _index(kv_lens, "kv_lens", dev, B),
-                               q_len, window, scale, _desc(out, dev), _desc(lse, dev), workspace.data_ptr(),
-                               workspace.nbytes, _stream(stream, dev))
+    dev = cache.device_now()
+    if workspace.get_device() != dev:
+        raise ValueError(f"workspace on {workspace.device}, but the current device is cuda:{dev}")
+    st = (_marshal or _bound()).kv4_attn(q, cache._c, block_table, kv_lens, q_len, window, scale, out, lse,
+                                         workspace.data_ptr(), workspace.nbytes, _stream(stream, dev), dev)
     _check(st, "slope_kv4_attn")
     return out, lse
