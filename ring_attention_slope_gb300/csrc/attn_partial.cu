@@ -279,7 +279,14 @@ template <bool kGrouped, int QT, bool PK>
 __device__ __forceinline__ void decode_tile(const AttnParams& p, const Item<PK>* items, int w, Tile& T, int& ii) {
   const int ushift = PK ? p.pack_shift : p.pair_heads;  // head units per item = h_count >> ushift
   if constexpr (PK) {
-    while (ii < p.n_items - 1 && w >= items[ii + 1].tile_begin) ++ii;
+    // the last sequence whose first tile is not after w: with many short ones a CTA's next tile is dozens on
+    for (int hi = p.n_items - 1; ii < hi;) {
+      const int mid = (ii + hi + 1) >> 1;
+      if (items[mid].tile_begin <= w)
+        ii = mid;
+      else
+        hi = mid - 1;
+    }
     const PackedSeq seq = items[ii];
     const int rows_shift = (QT == 2 ? 8 : 7) - p.pack_shift;  // tokens of a work tile
     T.itm.q_row0 = T.itm.out_row0 = T.itm.kv[0].row0 = seq.row0;
