@@ -274,6 +274,14 @@ __device__ __forceinline__ int tile_head(const AttnParams& p, const Tile& T, int
 // unit of an item is inner to its row blocks.
 template <bool PK>
 using Item = std::conditional_t<PK, PackedSeq, WorkItem>;
+__device__ __forceinline__ int item_ranges(const WorkItem& it) { return it.n_kv; }
+__device__ __forceinline__ int item_ranges(const PackedSeq&) { return 1; }
+__device__ __forceinline__ KvRange item_range(const WorkItem& it, int r) { return it.kv[r]; }
+__device__ __forceinline__ KvRange item_range(const PackedSeq& it, int) { return KvRange{it.row0, it.len}; }
+__device__ __forceinline__ int item_out_row0(const WorkItem& it) { return it.out_row0; }
+__device__ __forceinline__ int item_out_row0(const PackedSeq& it) { return it.row0; }
+__device__ __forceinline__ int item_plane(const WorkItem& it) { return it.plane; }
+__device__ __forceinline__ int item_plane(const PackedSeq&) { return 0; }
 
 template <bool kGrouped, int QT, bool PK>
 __device__ __forceinline__ void decode_tile(const AttnParams& p, const Item<PK>* items, int w, Tile& T, int& ii) {
@@ -932,14 +940,8 @@ __global__ void __launch_bounds__(K1Cfg<DQK, DV, QT>::kThreads, K1Cfg<DQK, DV, Q
       // the item's fields are read from shared memory where they are used, rather than kept in
       // registers across the steps, which need every register they can get
       const Item<PK>& sit = sItems[item_hint];
-      int n_kv = 1;
-      if constexpr (!PK) n_kv = sit.n_kv;
-      for (int r = 0; r < n_kv && ok; ++r) {
-        KvRange kr;
-        if constexpr (PK)
-          kr = KvRange{sit.row0, sit.len};
-        else
-          kr = sit.kv[r];
+      for (int r = 0; r < item_ranges(sit) && ok; ++r) {
+        const KvRange kr = item_range(sit, r);
         const TileRange R = tile_range(kr.row0, kr.len, qa_t, qb_t, p);
         // PK: both Q tiles' ranges of key tiles make one without a gap, which the CTA steps through
         int lo_cta = R.lo;
@@ -974,15 +976,9 @@ __global__ void __launch_bounds__(K1Cfg<DQK, DV, QT>::kThreads, K1Cfg<DQK, DV, Q
       // the wait for the tile's last PV.
       const bool valid_row = (PK ? row >> p.pack_shift : row) < rows_t;
       const int head = tile_head<PK>(p, T, t) + (PK ? row & ((1 << p.pack_shift) - 1) : 0);
-      int64_t out_row0, plane = 0;
-      if constexpr (PK) {
-        out_row0 = sit.row0;
-      } else {
-        out_row0 = sit.out_row0;
-        plane = sit.plane;
-      }
       const int64_t orow =
-          out_row0 + tile_row0<C::kQTiles, PK>(p, T, t) + (PK ? row >> p.pack_shift : row);
+          static_cast<int64_t>(item_out_row0(sit)) + tile_row0<C::kQTiles, PK>(p, T, t) + (PK ? row >> p.pack_shift : row);
+      const int64_t plane = item_plane(sit);
       if (valid_row) {
         p.lse[plane * p.lse_splane + orow * p.lse_srow + static_cast<int64_t>(head) * p.lse_shead] =
             l > 0.f ? (m_used + lg2_approx(l)) * kLn2 : -INFINITY;
