@@ -16,7 +16,7 @@
  * The conventions of slope.h hold: device tensors as slope_tensor, statuses,
  * no allocation, no synchronisation, asynchronous on `stream`, argument errors
  * before any launch.  Host arrays are read during the call only.  All tensors
- * lie on the current device.  The kernels read device index arrays (positions,
+ * lie on the current device, and outputs overlap no input but where a call says so.  The kernels read device index arrays (positions,
  * slots, block tables, lengths) when they run; an index out of range there is
  * never followed, as each call says.
  */
@@ -40,7 +40,8 @@ extern "C" {
  * dim: a multiple of 16, 16 .. 192; begin: a multiple of 8.  inv_freq: host
  * array of dim / 2 finite radians per position (slope_rope_inv_freq makes the
  * usual ones).  The angle is reduced in 64-bit fixed point, so far positions
- * lose nothing: an angle is off by at most 2^-24 of a turn.
+ * lose nothing: with frequencies up to 1 an angle is off by at most 2^-24 of a
+ * turn at any position.
  */
 typedef struct {
   int32_t begin;
@@ -113,7 +114,8 @@ SLOPE_API slope_status slope_qk_norm_rope(const slope_tensor* q, const slope_ten
  * too, does not reach a sequence's rows.  Within a sequence a key or value that
  * is not finite may also make rows NaN that the causal mask or the window keeps
  * from it, where a 128-key tile holds both.
- * Sequences share a launch up to 128 of them, the longest first.
+ * Sequences share a launch up to 128 of them, the longest first.  At dqk >= 128 a
+ * launch takes one of the SLOPE_TILE_COUNTERS, as those of slope_attn_partial do.
  */
 SLOPE_API slope_status slope_attn_varlen(const slope_tensor* q, const slope_tensor* k, const slope_tensor* v,
                                          const int64_t* cu_seqlens, int64_t n_seqs, int causal, int64_t window,
@@ -213,7 +215,9 @@ SLOPE_API slope_status slope_kv4_read(const slope_kv4_cache* cache, const int32_
  * scale, are rounded to bf16 on their way into the tensor cores (as the weights
  * of slope_attn_partial are), sums run in fp32.  Value scales have to lie below
  * 2^54 or the output overflows; contributions below about 2^-57 times the
- * weight are lost.
+ * weight are lost.  A query row's channels keep their bits down to 2^-26 of the
+ * row's largest, which has to be below 2^117 (else the row is NaN); scaled scores
+ * have to stay below 2^29 in magnitude, where fp32 no longer tells weights apart.
  */
 #define SLOPE_KV4_MAX_Q_LEN 64
 SLOPE_API slope_status slope_kv4_attn(const slope_tensor* q, const slope_kv4_cache* cache, const int32_t* block_table,

@@ -144,7 +144,8 @@ bool make_map(CUtensorMap* m, const slope_tensor* t, int pack_shift = 0) {
 
 // 3-D view {dv, H, rows} of an fp32 or bf16 output with row/head strides in elements;
 // box = 128 bytes of columns (32 fp32 or 64 bf16) x 1 head x 32 rows (one softmax warp's
-// rows; with packed heads 2^pack_shift heads x 32 >> pack_shift rows), 128-byte swizzle, written by TMA stores from the attention kernel's epilogue.
+// rows; with packed heads 2^pack_shift heads x 32 >> pack_shift rows), 128-byte swizzle,
+// written by TMA stores from the attention kernel's epilogue.
 // Returns false if the map cannot be built (the kernel then stores directly).
 bool make_out_map(CUtensorMap* m, void* base, bool bf16, int64_t rows, int64_t H, int64_t dv, int64_t srow,
                   int64_t shead, int pack_shift = 0) {

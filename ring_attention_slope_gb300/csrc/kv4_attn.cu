@@ -17,7 +17,7 @@
 // four masks.  Keys use fp16: a query row is scaled by a power of two to a largest value near 2^14, and its
 // channels that meet bits 4-7 by 1/16, both exact.  Values use bf16, because the other operand, weight *
 // scale, needs bf16's range (fp16's would flush it): the weight carries a factor 2^64 so that products with
-// 2^-133 stay normal fp32 numbers.  Its rounding to bf16 (2^-9 relative) is the one the attention kernel of
+// 2^-133 stay normal fp32 numbers.  Its rounding to bf16 (2^-8 relative) is the one the attention kernel of
 // the prefill also makes on its weights.
 //
 // Keys are the M rows of S^T = K Q^T (16 keys x 8 query rows), values those of
@@ -394,7 +394,8 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
         s += __shfl_xor_sync(0xffffffffu, s, 2);
         sums[G] = s * 0x1p-24f;
       }
-      const float unit = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(min(24 - k + 127, 254)) << 23);
+      // a largest value of 2^117 or more would need a unit past fp32's range: such a row becomes NaN
+      const float unit = k < -103 ? __uint_as_float(0x7fc00000u) : p.scale_log2 * __uint_as_float(static_cast<uint32_t>(24 - k + 127) << 23);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int from = (2 * q4 + j) * 4;

@@ -242,7 +242,7 @@ static PyObject* qk_norm_rope(PyObject* self, PyObject* const* a, Py_ssize_t n) 
       describe(a[2], dev, 1, &d[2], &qw) < 0 || describe(a[3], dev, 1, &d[3], &kw) < 0 ||
       describe(a[9], dev, 0, &d[4], &qo) < 0 || describe(a[10], dev, 0, &d[5], &ko) < 0)
     return NULL;
-  rows = q != NULL ? q->shape[0] : 0;
+  rows = q != NULL ? q->shape[0] : k != NULL ? k->shape[0] : 0;
   if (a[7] != Py_None && index_array(a[7], "positions", dev, rows, &pos) < 0) return NULL;
   return PyLong_FromLong(lib.qk_norm_rope(q, k, qw, kw, norm, eps, (const slope_rope*)rope, pos, pos0, qo, ko,
                                           (void*)(uintptr_t)stream));

@@ -427,6 +427,7 @@ extern "C" slope_status slope_qk_norm_rope(const slope_tensor* q, const slope_te
     }
   }
   if (T == 0) return SLOPE_OK;
+  if (!aligned(positions, 4)) return SLOPE_ERR_STRIDE;
   p.T = T;
   p.positions = positions;
   p.pos0 = pos0;

@@ -3,7 +3,7 @@ prompts, the 4-bit paged key/value cache and attention over it.
 
 Defaults and outputs are made here; the arguments go to the library through the C module ``_marshal``
 (``csrc/marshal.c``), because the smallest of these calls take a few microseconds.  Tensors have to lie on the
-current device, and a call runs on the current stream unless it is given one.
+current device, and a call runs on the current stream unless it is given one; what it allocates belongs to that stream.
 """
 from __future__ import annotations
 
@@ -77,6 +77,22 @@ def _stream(stream, dev):
     return _raw_stream(dev) if stream is None else stream.cuda_stream
 
 
+def _empty(shape, dtype, device, stream):
+    """What a call allocates belongs to the stream it runs on: a temporary's memory is not handed out again before
+    that stream is done with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _empty_like(t, dtype, stream):
+    if stream is None:
+        return torch.empty_like(t, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(t, dtype=dtype)
+
+
 # ---------------------------------------------------------------- positions
 
 def rope_inv_freq(dim, base=10000.0, *, scaling="plain", factor=1.0, original=0.0, fast=0.0, slow=0.0):
@@ -110,9 +126,9 @@ def qk_norm_rope(q, k=None, *, norm=True, q_weight=None, k_weight=None, eps=1e-6
     (of the inputs' type unless given) may be the inputs.  Returns ``(q_out, k_out)`` (k_out None without k).
     """
     if q_out is None:
-        q_out = torch.empty_like(q, dtype=out_dtype)
+        q_out = _empty_like(q, out_dtype, stream)
     if k is not None and k_out is None:
-        k_out = torch.empty_like(k, dtype=out_dtype)
+        k_out = _empty_like(k, out_dtype, stream)
     dev = _device()
     st = (_marshal or _bound()).qk_norm_rope(q, k, q_weight, k_weight, norm, eps, None if rope is None else rope._c,
                                              positions, pos0, q_out, k_out, _stream(stream, dev), dev)
@@ -132,9 +148,9 @@ def attn_varlen(q, k, v, cu_seqlens, *, causal=True, window=0, scale=0.0, out=No
     """
     T, Hq, _ = q.shape
     if out is None:
-        out = torch.empty((T, Hq, v.shape[2]), dtype=out_dtype or torch.bfloat16, device=q.device)
+        out = _empty((T, Hq, v.shape[2]), out_dtype or torch.bfloat16, q.device, stream)
     if lse is None:
-        lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
+        lse = _empty((Hq, T), torch.float32, q.device, stream)
     if isinstance(cu_seqlens, torch.Tensor):
         if cu_seqlens.is_cuda:
             raise TypeError("cu_seqlens lives on the host (reading it back would synchronise)")
@@ -189,9 +205,9 @@ def kv4_read(cache, slots, *, k_out=None, v_out=None, out_dtype=None, stream=Non
     fp32.  Rows whose slot is out of range are left as they were (uninitialised where the call allocates)."""
     T = slots.shape[0]
     if k_out is None:
-        k_out = torch.empty((T, cache.Hkv, cache.dqk), dtype=out_dtype or torch.bfloat16, device=cache.data.device)
+        k_out = _empty((T, cache.Hkv, cache.dqk), out_dtype or torch.bfloat16, cache.data.device, stream)
     if v_out is None:
-        v_out = torch.empty((T, cache.Hkv, cache.dv), dtype=out_dtype or torch.bfloat16, device=cache.data.device)
+        v_out = _empty((T, cache.Hkv, cache.dv), out_dtype or torch.bfloat16, cache.data.device, stream)
     dev = cache.device_now()
     st = (_marshal or _bound()).kv4_read(cache._c, slots, k_out, v_out, _stream(stream, dev), dev)
     _check(st, "slope_kv4_read")
@@ -213,14 +229,14 @@ def kv4_attn(q, cache, block_table, kv_lens, *, q_len=1, window=0, scale=0.0, ou
     """
     T, Hq, _ = q.shape
     if out is None:
-        out = torch.empty((T, Hq, cache.dv), dtype=out_dtype or torch.bfloat16, device=q.device)
+        out = _empty((T, Hq, cache.dv), out_dtype or torch.bfloat16, q.device, stream)
     if lse is None and want_lse:
-        lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
+        lse = _empty((Hq, T), torch.float32, q.device, stream)
     if workspace is None:
         nbytes = load().slope_kv4_attn_workspace_size(block_table.shape[0], Hq, cache._c, q_len)
         if nbytes == 0:
             raise SlopeError(-8, "slope_kv4_attn_workspace_size")
-        workspace = torch.empty((nbytes,), dtype=torch.uint8, device=q.device)
+        workspace = _empty((nbytes,), torch.uint8, q.device, stream)
     dev = cache.device_now()
     if workspace.get_device() != dev:
         raise ValueError(f"workspace on {workspace.device}, but the current device is cuda:{dev}")

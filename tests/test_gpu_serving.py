@@ -11,6 +11,9 @@ Tolerances, from the arithmetic:
 * packed prompts: the bounds that the prefill attention's own tests use.
 """
 import math
+import subprocess
+import sys
+from pathlib import Path
 
 import numpy as np
 import pytest
@@ -424,6 +427,109 @@ def test_decode_same_bits_streams_and_graphs():
     graph.replay()
     torch.cuda.synchronize()
     check_decode(o3, l3, q, [tuple(x[:m] for x in h) for h, m in zip(held, shorter)], shorter, 1, 0, 0.125)
+
+
+def test_decode_scores_far_below_zero():
+    """One key: weight 1, whatever its score.  A query beyond the documented range gives NaN, not a wrong number."""
+    cache, table, held = paged([1, 1], 16, 1, 64, 64, 140)
+    q = rand(2, 8, 64, seed=141)
+    q[1] = -q[0]  # one of the two scores is negative
+    for scale in (1e3, 1e6):
+        out, lse = slope.kv4_attn(q.cuda(), cache, table.cuda(), i32([1, 1]), scale=scale, out_dtype=torch.float32)
+        assert torch.isfinite(lse).all()
+        for b in range(2):
+            _, v, spread = held[b]
+            assert ((out[b].cpu().double() - v[0]).abs() <= 2.0 ** -8 * spread[0] + 2.0 ** -20 * v[0].abs()).all()
+    q[1, 3, 5] = 2.0 ** 118
+    out, lse = slope.kv4_attn(q.cuda(), cache, table.cuda(), i32([1, 1]))
+    assert torch.isnan(lse[3, 1]) and torch.isfinite(lse[:3]).all() and torch.isfinite(lse[4:]).all()
+
+
+def test_decode_on_a_stream_of_its_own():
+    """What a call allocates for another stream is not handed out while that stream still uses it."""
+    lens = [5000, 40, 900]
+    cache, table, held = paged(lens, 64, 2, 64, 64, 150)
+    q, tab, n = rand(3, 16, 64, seed=151).cuda(), table.cuda(), i32(lens)
+    want, want_lse = slope.kv4_attn(q, cache, tab, n)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    size = slope.kv4_attn_workspace_size(3, 16, cache)
+    results = []
+    for _ in range(8):
+        results.append(slope.kv4_attn(q, cache, tab, n, stream=side))
+        torch.empty(size, dtype=torch.uint8, device="cuda").fill_(0x7F)  # the workspace's size, on the current stream
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) and torch.equal(l, want_lse) for o, l in results)
+
+
+def test_offsets_past_32_bits():
+    """Pages, rows and heads that lie more than 2^32 bytes into their tensors."""
+    page, H, d = 1024, 8, 64
+    n_pages = 2 ** 32 // slope.serving.load().slope_kv4_cache_bytes(1, page, H, d, d) + 40
+    cache = slope.KV4Cache(n_pages, page, H, d, d)
+    assert cache.data.numel() > 2 ** 32
+    n = 1500
+    table = torch.tensor([[n_pages - 1, 3], [1, n_pages - 7]], dtype=torch.int32)
+    held, t = [], torch.arange(n)
+    for b in range(2):
+        k, v = rand(n, H, d, seed=160 + b), rand(n, H, d, seed=170 + b)
+        slots = i32(table[b, t // page].long() * page + t % page)
+        slope.kv4_write(cache, k.cuda(), v.cuda(), slots)
+        kq, vq = so.quantise(k), so.quantise(v)
+        held.append((so.values(*kq), so.values(*vq), so.values(*vq) - vq[2].double().repeat_interleave(32, -1)))
+        ko, vo = slope.kv4_read(cache, slots)
+        assert ((ko.cpu().double() - held[b][0]).abs() <= (2.0 ** -8 + 2.0 ** -24) * held[b][0].abs()).all()
+        assert ((vo.cpu().double() - held[b][1]).abs() <= (2.0 ** -8 + 2.0 ** -24) * held[b][1].abs()).all()
+    q = rand(2, 16, d, seed=180)
+    out, lse = slope.kv4_attn(q.cuda(), cache, table.cuda(), i32([n, n]))
+    check_decode(out, lse, q, held, [n, n], 1, 0, 0.125)
+    del cache
+    # rows 2^26 elements apart
+    T, Hq, row = 40, 4, 2 ** 26
+    buf = torch.empty(T * row, dtype=torch.bfloat16, device="cuda")
+    q, k, v = (buf.as_strided((T, h, d), (row, d, 1), at) for h, at in ((Hq, 0), (1, 1024), (1, 2048)))
+    xq, xk, xv = rand(T, Hq, d, seed=190), rand(T, 1, d, seed=191), rand(T, 1, d, seed=192)
+    for dst, src in ((q, xq), (k, xk), (v, xv)):
+        dst.copy_(src.cuda())
+    qo, ko = buf.as_strided((T, Hq, d), (row, d, 1), 4096), buf.as_strided((T, 1, d), (row, d, 1), 8192)
+    slope.qk_norm_rope(q, k, rope=slope.Rope([0.5] * 32), q_out=qo, k_out=ko)
+    for got, x in ((qo, xq), (ko, xk)):
+        check_rope(got.contiguous(), x, None, 1e-6, torch.arange(T), [0.5] * 32, 0, False, 1.0)
+    out = buf.as_strided((T, Hq, d), (row, d, 1), 16384)
+    slope.attn_varlen(q, k, v, [0, 15, T], out=out)
+    want, _ = slope.attn_varlen(xq.cuda(), xk.cuda(), xv.cuda(), [0, 15, T])
+    assert torch.equal(out, want)
+    pages = slope.KV4Cache(3, 16, 1, d, d)
+    slope.kv4_write(pages, k, v, i32(list(range(T))))
+    dense = slope.KV4Cache(3, 16, 1, d, d)
+    slope.kv4_write(dense, xk.cuda(), xv.cuda(), i32(list(range(T))))
+    assert torch.equal(torch.cat(slope.kv4_read(pages, i32(list(range(T))))), torch.cat(slope.kv4_read(dense, i32(list(range(T))))))
+
+
+FIRST_CALLS = """
+import torch, ring_attention_slope_gb300 as slope
+q, k, v = (torch.randn(40, h, 64, device="cuda").bfloat16() for h in (8, 1, 1))
+cache, slots = slope.KV4Cache(3, 16, 1, 64, 64), torch.arange(40, dtype=torch.int32, device="cuda")
+table, lens = torch.arange(3, dtype=torch.int32, device="cuda").view(1, 3), torch.full((1,), 40, dtype=torch.int32, device="cuda")
+def calls():
+    qr, kr = slope.qk_norm_rope(q, k, rope=slope.Rope([0.5] * 32))
+    out = slope.attn_varlen(qr, kr, v, [0, 15, 40])
+    slope.kv4_write(cache, kr, v, slots)
+    return (*out, *slope.kv4_read(cache, slots), *slope.kv4_attn(qr[39:], cache, table, lens))
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = calls()
+graph.replay()
+torch.cuda.synchronize()
+want = calls()
+assert all(torch.equal(a, b) for a, b in zip(got, want)) and slope.device_status() == (0, 0)
+"""
+
+
+def test_first_calls_of_a_process_are_captured():
+    run = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=Path(__file__).resolve().parents[1], timeout=100,
+                         capture_output=True, text=True)
+    assert run.returncode == 0, run.stderr[-2000:]
 
 
 # ---------------------------------------------------------------- packed prompts

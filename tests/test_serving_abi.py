@@ -155,6 +155,7 @@ def test_norm_rope_refusals(lib):
     assert call(**{**full, "q": t([n, Hq, d], stride=[Hq * d, d, 2])}) == E_STRIDE
     assert call(**{**full, "qo": t([n, Hq, d], data=0x90008)}) == E_STRIDE
     assert call(**{**full, "q": t([n, Hq, d], data=0)}) == E_NULL
+    assert call(**full, pos=0x70002) == E_STRIDE
     same = t([n, Hq, d])
     assert call(**{**full, "q": same, "qo": t([n, Hq, d], stride=[2 * Hq * d, d, 1])}) == E_STRIDE  # not in place
     assert call(**{**full, "q": same, "qo": t([n, Hq, d], F32)}) == E_STRIDE

@@ -77,6 +77,11 @@ def test_norm_rope_arguments(m):
     assert call(norm=False, qw=Fake([64])) == E_UNSUP and call(norm=0) == S_OK and call(eps=-1) == E_SHAPE
     assert call(rope=slope.Rope([1.0] * 32, begin=4)._c) == E_SHAPE and call(rope=None) == S_OK
     assert call(pos0=2 ** 31 + 1) == E_SHAPE
+    # keys alone: one position for each of their rows
+    alone = dict(q=None, qo=None, k=Fake([4, 2, 64], stride=[4, 64, 1]), ko=Fake([4, 2, 64]))
+    assert call(**alone, pos=i32(4)) == E_STRIDE
+    with pytest.raises(ValueError):
+        call(**alone, pos=i32(0, ptr=0))
     for bad, error in ((dict(q=Fake([0, 64])), None), (dict(q=Fake([64])), ValueError), (dict(qw=Fake([1, 1, 1, 64])), ValueError),
                        (dict(pos=i32(1)), ValueError), (dict(pos=Fake([0], torch.int64)), TypeError), (dict(rope=b"x"), TypeError),
                        (dict(q=Fake([0, 8, 64], torch.float16)), TypeError), (dict(eps="1"), TypeError), (dict(pos0=1.5), TypeError),
