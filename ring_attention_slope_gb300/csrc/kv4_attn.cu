@@ -78,7 +78,8 @@ struct Kv4AttnParams {
   int32_t out_bf16;
   float* lse;  // may be null
   int64_t lse_srow, lse_shead;
-  int4* heads;      // workspace: for each CTA, the pair it leaves unfinished {sequence or -1, pair, last CTA, -}
+  int4* heads;      // workspace: {sequence, pair, first CTA, last CTA} of the pairs that several CTAs share, or {-1}
+  int32_t by_pair;  // an entry of `heads` for each pair (where there are fewer than CTAs), else for each first CTA
   float* partials;  // workspace: two for each CTA, {m[R], l[R], out[R][DV]}
   int* status;
   uint64_t wait_limit_ns;
@@ -273,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
   }
   __syncthreads();
   const CtaRange range = cta_range<kStep>(p, s_scratch);
-  if (threadIdx.x == 0) p.heads[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (threadIdx.x == 0 && !p.by_pair) p.heads[blockIdx.x] = make_int4(-1, 0, 0, 0);
 
   // the warp's ring: the stages that the next copy fills and the next step reads, and that one's parity
   int put = 0, get = 0;
@@ -701,8 +702,9 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
         }
       }
     }
-    if (threadIdx.x == 0 && !whole && u == pair_begin)  // begun here, finished in a later CTA's range
-      p.heads[blockIdx.x] = make_int4(b, pair, static_cast<int>((pair_end - 1) / range.per), 0);
+    if (threadIdx.x == 0 && u == pair_begin && (!whole || p.by_pair))  // begun here: finished here or in a later CTA's range
+      p.heads[p.by_pair ? b * p.Hkv * p.row_tiles + pair : blockIdx.x] =
+          make_int4(whole ? -1 : b, pair, blockIdx.x, static_cast<int>((pair_end - 1) / range.per));
     __syncthreads();
     u = u_end;
     if (u_end == pair_end && pair == p.Hkv * p.row_tiles - 1) {
@@ -712,27 +714,43 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
   }
 }
 
-// Joins the partials of a pair that several CTAs share: CTA c takes the one that CTA c of the
-// attention launch began and did not finish.  Fixed order, so the same result every time.  A thread has
-// four channels of one row, and eight partials' loads in flight: latency is all that this launch costs.
-template <int DV, int R>
-__global__ void __launch_bounds__(kThreads) kv4_join_kernel(const __grid_constant__ Kv4AttnParams p) {
+// Joins the partials of a pair that several CTAs share.  CTA (c, y) takes the pair of entry c, 32 lanes times
+// four of its channels, and its warps every kJoinWarps-th partial, which they join at the end: all in a fixed
+// order, so the same result every time.  Latency is all that this launch costs, so each lane has four
+// partials' loads in flight and as many warps share a pair as the launch has room for (see launch_nt).
+template <int DV, int R, int kJoinWarps>
+__global__ void __launch_bounds__(32 * kJoinWarps) kv4_join_kernel(const __grid_constant__ Kv4AttnParams p) {
+  __shared__ float s_m[kJoinWarps][32], s_l[kJoinWarps][32];
+  __shared__ float4 s_v[kJoinWarps][32];
   pdl_wait();
   const int4 head = p.heads[blockIdx.x];
   if (head.x < 0) return;
-  constexpr int kFloats = 2 * R + R * DV, kAhead = 8;
-  static_assert(R * DV / 4 % kThreads == 0, "whole CTAs of four channels");
-  const int i = blockIdx.y * kThreads + threadIdx.x;
+  constexpr int kFloats = 2 * R + R * DV, kAhead = 4;
+  static_assert(R * DV % 128 == 0, "whole CTAs of 32 times four channels");
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int i = blockIdx.y * 32 + lane;
   const int rr = i / (DV / 4), ch = (i % (DV / 4)) * 4;
-  const int first = blockIdx.x, n = head.z - first + 1;
+  const int first = head.z, n = head.w - first + 1;
   float mm = kNoMax, ll = 0.f;
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c0 = 0; c0 < n; c0 += kAhead) {
+  auto add = [&](float m, float l, float4 v, float to) {
+    const float f = ex2_approx(m - to);
+    ll = fmaf(f, l, ll);
+    sum.x = fmaf(f, v.x, sum.x), sum.y = fmaf(f, v.y, sum.y);
+    sum.z = fmaf(f, v.z, sum.z), sum.w = fmaf(f, v.w, sum.w);
+  };
+  auto move = [&](float to) {
+    const float alpha = ex2_approx(mm - to);
+    mm = to;
+    ll *= alpha;
+    sum.x *= alpha, sum.y *= alpha, sum.z *= alpha, sum.w *= alpha;
+  };
+  for (int c0 = warp; c0 < n; c0 += kAhead * kJoinWarps) {
     float m[kAhead], l[kAhead];
     float4 v[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      const int c = min(c0 + k, n - 1);
+      const int c = min(c0 + k * kJoinWarps, n - 1);
       // the first CTA's partial is its second, the others' their first
       const float* const part = p.partials + (static_cast<int64_t>(first + c) * 2 + (c == 0 ? 1 : 0)) * kFloats;
       m[k] = part[rr];
@@ -742,19 +760,20 @@ __global__ void __launch_bounds__(kThreads) kv4_join_kernel(const __grid_constan
     float now = mm;
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) now = fmaxf(now, m[k]);
-    const float alpha = ex2_approx(mm - now);
-    mm = now;
-    ll *= alpha;
-    sum.x *= alpha, sum.y *= alpha, sum.z *= alpha, sum.w *= alpha;
+    move(now);
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      if (c0 + k >= n) break;
-      const float f = ex2_approx(m[k] - now);
-      ll = fmaf(f, l[k], ll);
-      sum.x = fmaf(f, v[k].x, sum.x), sum.y = fmaf(f, v[k].y, sum.y);
-      sum.z = fmaf(f, v[k].z, sum.z), sum.w = fmaf(f, v[k].w, sum.w);
-    }
+    for (int k = 0; k < kAhead; ++k)
+      if (c0 + k * kJoinWarps < n) add(m[k], l[k], v[k], now);
   }
+  s_m[warp][lane] = mm, s_l[warp][lane] = ll, s_v[warp][lane] = sum;
+  __syncthreads();
+  if (warp != 0) return;
+  float now = mm;
+#pragma unroll
+  for (int w = 1; w < kJoinWarps; ++w) now = fmaxf(now, s_m[w][lane]);
+  move(now);
+#pragma unroll
+  for (int w = 1; w < kJoinWarps; ++w) add(s_m[w][lane], s_l[w][lane], s_v[w][lane], now);
   store_row<DV, R>(p, head.x, head.y, rr, ch, sum, mm, ll);
 }
 
@@ -789,18 +808,25 @@ cudaError_t launch_nt(Kv4AttnParams p, cudaStream_t stream) {
     ready[dev].store(true, std::memory_order_release);
   }
   const int grid = std::min(kMaxCtas, sms * C::kCtas);
+  const int64_t pairs = static_cast<int64_t>(p.B) * p.Hkv * p.row_tiles;
+  p.by_pair = pairs <= grid ? 1 : 0;
   kv4_attn_kernel<DQK, DV, NT><<<grid, kThreads, C::kSmemBytes, stream>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid), C::R * DV / 4 / kThreads);
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.by_pair ? pairs : grid), C::R * DV / 128);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_join_kernel<DV, C::R>, p);
+  // Few pairs: each may be shared by many CTAs, and the launch is small.
+  if (p.by_pair && pairs * cfg.gridDim.y <= 2 * sms) {
+    cfg.blockDim = dim3(32 * 16);
+    return cudaLaunchKernelEx(&cfg, kv4_join_kernel<DV, C::R, 16>, p);
+  }
+  cfg.blockDim = dim3(32 * 4);
+  return cudaLaunchKernelEx(&cfg, kv4_join_kernel<DV, C::R, 4>, p);
 }
 
 // One tile of 8 rows while they suffice, else 16: a block's codes are unpacked once for all of them.
