@@ -660,6 +660,9 @@ __global__ void __launch_bounds__(K1Cfg<DQK, DV, QT>::kThreads, K1Cfg<DQK, DV, Q
               uint64_t* b = C::kSepP ? &bar_sfree[t] : &bar_o[t];
               if (!wait_bounded(b, (n - 1) & 1, cta_abort, p.status, limit, 5)) return false;
             }
+            // With S_t the softmax clears the end of this step's V slot, and needs the slot's previous fill known
+            // to be there: of two slots, that is the V whose PV is still pending.
+            if (PK && C::kSepP && C::kSlots == 2 && s.valid < kBlockN && !flush()) return false;
             tc_fence_after_sync();
             issue_qk(kslot);
           }
@@ -786,6 +789,25 @@ __global__ void __launch_bounds__(K1Cfg<DQK, DV, QT>::kThreads, K1Cfg<DQK, DV, Q
       // cta_step (PK): the step's number among the CTA's, which tells its K/V slots
       auto step = [&](const bool full, const int kpos, const int valid, const uint32_t cta_step) -> bool {
         if (!warp_all(wait_bounded(&bar_s[t], n & 1, cta_abort, p.status, limit, 8))) return false;
+        if constexpr (PK) {
+          // The range ends inside this tile: the V rows after it belong to another sequence (or to
+          // none) and their weights are 0, but 0 times a NaN there would still be NaN.  Zero them in
+          // the slot before this Q tile's PV may read it (both Q tiles do, each before its own PV).
+          // S_t is there, so its issuer has waited for every earlier fill of the slot (it takes the steps
+          // in order, whether the Q tile uses them or not), and the parity below can only mean this fill.
+          // (Before the scores are loaded: after them it cost the 128-wide kernels spills and 10%.)
+          if (valid < kBlockN) {
+            const uint32_t vcnt = 2 * cta_step + 1;
+            const uint32_t vslot = vcnt % C::kSlots;
+            if (!warp_all(wait_bounded(&bar_full[vslot], (vcnt / C::kSlots) & 1, cta_abort, p.status, limit, 14)))
+              return false;
+            uint8_t* const sv0 = sSlot + vslot * C::kSlotBytes;
+            for (int c = 0; c < C::kVChunks; ++c)
+              for (int off = valid * 128 + row * 16; off < static_cast<int>(kChunkBytes); off += 128 * 16)
+                *reinterpret_cast<uint4*>(sv0 + c * kChunkBytes + off) = make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_shared();
+          }
+        }
         tc_fence_after_sync();
         // S_t with the maximum of each 32-column quarter of the row (taken by the load)
         uint32_t r0[32], r1[32], r2[32], r3[32];
@@ -901,22 +923,6 @@ __global__ void __launch_bounds__(K1Cfg<DQK, DV, QT>::kThreads, K1Cfg<DQK, DV, Q
         // O_t holds the previous PV's result here.  Separate P: the P store above waited for
         // that PV.  P inside S_t: the issuer sent S_t(n) only after PV(n-1) completed, and the
         // commit behind bar_s tracks every earlier MMA of that issuer.
-        if constexpr (PK) {
-          // The range ends inside this tile: the V rows after it belong to another sequence (or to
-          // none) and their weights are 0, but 0 times a NaN there would still be NaN.  Zero them in
-          // the slot before this Q tile's PV may read it (both Q tiles do, each before its own PV).
-          if (valid < kBlockN) {
-            const uint32_t vcnt = 2 * cta_step + 1;
-            const uint32_t vslot = vcnt % C::kSlots;
-            if (!warp_all(wait_bounded(&bar_full[vslot], (vcnt / C::kSlots) & 1, cta_abort, p.status, limit, 14)))
-              return false;
-            uint8_t* const sv0 = sSlot + vslot * C::kSlotBytes;
-            for (int c = 0; c < C::kVChunks; ++c)
-              for (int off = valid * 128 + row * 16; off < static_cast<int>(kChunkBytes); off += 128 * 16)
-                *reinterpret_cast<uint4*>(sv0 + c * kChunkBytes + off) = make_uint4(0u, 0u, 0u, 0u);
-            fence_proxy_async_shared();
-          }
-        }
         if (any_need && nl > 0) {
 #pragma unroll 1
           for (int c = 0; c < DV / 16; ++c) {
@@ -1213,7 +1219,7 @@ cudaError_t launch_impl(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
   p.total_tiles = static_cast<int32_t>(tiles);
   const long long grid = std::min<long long>(tiles, resident_ctas() * C::kMinBlocks);
   if constexpr (PK)  // (grouped tiles are also the ones claimed at run time: see tile_head_group)
-    p.head_group = !C::kGroupedTiles ? 0 : (p.group >> p.pack_shift) >= 4 ? p.Hq >> p.pack_shift : 1;
+    p.head_group = !C::kGroupedTiles ? 0 : p.group >= 4 ? p.Hq >> p.pack_shift : 1;
   else
     p.head_group = C::kGroupedTiles ? tile_head_group(p, grid, C::kDynamicTiles) : 0;
   if (C::kDynamicTiles) {

@@ -577,9 +577,20 @@ def test_varlen_sizes(dqk, dv, Hq, H, out_dtype):
 
 
 @pytest.mark.parametrize("window,causal", [(1, True), (30, True), (128, True), (300, True), (5000, True), (0, False), (60, False)])
-@pytest.mark.parametrize("dqk,dv,Hq,H", [(64, 64, 8, 1), (64, 64, 3, 3), (192, 128, 2, 2), (128, 128, 8, 2)])
+@pytest.mark.parametrize("dqk,dv,Hq,H", [(64, 64, 8, 1), (64, 64, 3, 3), (192, 128, 2, 2), (128, 128, 8, 2),
+                                        (192, 64, 2, 2)])
 def test_varlen_masks(window, causal, dqk, dv, Hq, H):
     check_varlen(*packed([40, 333, 130, 700], Hq, H, dqk, dv, 160), window=window, causal=causal)
+
+
+@pytest.mark.parametrize("dqk,dv", [(64, 64), (128, 128), (192, 64), (192, 128)])
+def test_varlen_second_tile_starts_at_a_sequence_end(dqk, dv):
+    """A CTA's second Q tile whose first step is the last, partial one, many times over: the V rows that it clears are
+    those of that step and not of the one before."""
+    lens = [129 + i % 40 for i in range(100)]
+    q, k, v, cu = packed(lens, 2, 2, dqk, dv, 165)
+    for window in (2, 20):
+        check_varlen(q, k, v, cu, window=window)
 
 
 @pytest.mark.parametrize("dqk,dv,Hq,H,window", [(64, 64, 8, 1, 0), (64, 64, 8, 1, 50), (64, 64, 1, 1, 0), (192, 128, 2, 2, 0),
