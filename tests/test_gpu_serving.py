@@ -315,6 +315,27 @@ def test_decode_many_sequences():
     run_decode(lens, 1, 8, 1, 64, 64, 16, seed=60)
 
 
+@pytest.mark.parametrize("lens", [[39] * 10, [64] * 70, [200] * 60, [1024] * 24, [2048] * 12, [1500] + [9] * 100,
+                                  [3000, 0, 700] * 5, [40] * 400])
+@pytest.mark.parametrize("q_len,dqk,dv", [(1, 64, 64), (3, 192, 128)])
+def test_decode_cuts(lens, q_len, dqk, dv):
+    """One piece to a CTA or several, whole pairs or shared ones: every kind of cut, and every sequence gets its rows."""
+    H, Hq, page = 4, 16, 64
+    cache, table, held = paged(lens, page, H, dqk, dv, 62)
+    q = rand(len(lens) * q_len, Hq, dqk, seed=63)
+    out = torch.full((len(lens) * q_len, Hq, dv), float("nan"), dtype=torch.bfloat16, device="cuda")
+    _, lse = slope.kv4_attn(q.cuda(), cache, table.cuda(), i32(lens), q_len=q_len, out=out)
+    assert torch.isfinite(out).all()
+    pick = sorted({0, 1, len(lens) // 2, len(lens) - 1})
+    check_decode(out, lse, q, held, lens, q_len, 0, 1 / math.sqrt(dqk), rows=pick)
+    single = [slope.kv4_attn(q[b * q_len:(b + 1) * q_len].cuda(), cache, table[b:b + 1].cuda(), i32(lens[b:b + 1]),
+                             q_len=q_len, out_dtype=torch.float32)[0] for b in range(0, len(lens), 7)]
+    for b, one in zip(range(0, len(lens), 7), single):  # two bf16 roundings of weights, one of the output
+        ours = out[b * q_len:(b + 1) * q_len].float()
+        spread = held[b][2].abs().max().item() if lens[b] else 0.0
+        assert ((ours - one).abs() <= 2.0 ** -8 * one.abs() + 2.0 ** -6 * spread + 1e-6).all(), b
+
+
 def test_decode_scale_and_large_scores():
     """A scale of its own; scores whose maximum moves often and whose weights underflow."""
     run_decode([500], 1, 8, 1, 64, 64, 16, scale=0.01)
