@@ -77,20 +77,23 @@ def _stream(stream, dev):
     return _raw_stream(dev) if stream is None else stream.cuda_stream
 
 
-def _empty(shape, dtype, device, stream):
-    """What a call allocates belongs to the stream it runs on: a temporary's memory is not handed out again before
-    that stream is done with it."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+try:  # the allocation alone: torch.empty's argument parsing costs a small call another 1.5 us each
+    from torch._C._dynamo.guards import _empty_strided_cuda as _alloc
+except ImportError:
+    def _alloc(size, stride, dtype):
+        return torch.empty_strided(size, stride, dtype=dtype, device="cuda")
 
 
-def _empty_like(t, dtype, stream):
+def _empty(shape, dtype, stream):
+    """A dense tensor on the current device.  What a call allocates belongs to the stream it runs on: a temporary's
+    memory is not handed out again before that stream is done with it."""
+    if len(shape) > 3:
+        raise ValueError("tensors must be rank 2 or 3")
+    stride = (shape[1] * shape[2], shape[2], 1) if len(shape) == 3 else (shape[1], 1) if len(shape) == 2 else (1,)
     if stream is None:
-        return torch.empty_like(t, dtype=dtype)
+        return _alloc(shape, stride, dtype)
     with torch.cuda.stream(stream):
-        return torch.empty_like(t, dtype=dtype)
+        return _alloc(shape, stride, dtype)
 
 
 # ---------------------------------------------------------------- positions
@@ -126,9 +129,9 @@ def qk_norm_rope(q, k=None, *, norm=True, q_weight=None, k_weight=None, eps=1e-6
     (of the inputs' type unless given) may be the inputs.  Returns ``(q_out, k_out)`` (k_out None without k).
     """
     if q_out is None:
-        q_out = _empty_like(q, out_dtype, stream)
+        q_out = _empty(tuple(q.shape), out_dtype or q.dtype, stream)
     if k is not None and k_out is None:
-        k_out = _empty_like(k, out_dtype, stream)
+        k_out = _empty(tuple(k.shape), out_dtype or k.dtype, stream)
     dev = _device()
     st = (_marshal or _bound()).qk_norm_rope(q, k, q_weight, k_weight, norm, eps, None if rope is None else rope._c,
                                              positions, pos0, q_out, k_out, _stream(stream, dev), dev)
@@ -148,9 +151,9 @@ def attn_varlen(q, k, v, cu_seqlens, *, causal=True, window=0, scale=0.0, out=No
     """
     T, Hq, _ = q.shape
     if out is None:
-        out = _empty((T, Hq, v.shape[2]), out_dtype or torch.bfloat16, q.device, stream)
+        out = _empty((T, Hq, v.shape[2]), out_dtype or torch.bfloat16, stream)
     if lse is None:
-        lse = _empty((Hq, T), torch.float32, q.device, stream)
+        lse = _empty((Hq, T), torch.float32, stream)
     if isinstance(cu_seqlens, torch.Tensor):
         if cu_seqlens.is_cuda:
             raise TypeError("cu_seqlens lives on the host (reading it back would synchronise)")
@@ -205,9 +208,9 @@ def kv4_read(cache, slots, *, k_out=None, v_out=None, out_dtype=None, stream=Non
     fp32.  Rows whose slot is out of range are left as they were (uninitialised where the call allocates)."""
     T = slots.shape[0]
     if k_out is None:
-        k_out = _empty((T, cache.Hkv, cache.dqk), out_dtype or torch.bfloat16, cache.data.device, stream)
+        k_out = _empty((T, cache.Hkv, cache.dqk), out_dtype or torch.bfloat16, stream)
     if v_out is None:
-        v_out = _empty((T, cache.Hkv, cache.dv), out_dtype or torch.bfloat16, cache.data.device, stream)
+        v_out = _empty((T, cache.Hkv, cache.dv), out_dtype or torch.bfloat16, stream)
     dev = cache.device_now()
     st = (_marshal or _bound()).kv4_read(cache._c, slots, k_out, v_out, _stream(stream, dev), dev)
     _check(st, "slope_kv4_read")
@@ -229,14 +232,14 @@ def kv4_attn(q, cache, block_table, kv_lens, *, q_len=1, window=0, scale=0.0, ou
     """
     T, Hq, _ = q.shape
     if out is None:
-        out = _empty((T, Hq, cache.dv), out_dtype or torch.bfloat16, q.device, stream)
+        out = _empty((T, Hq, cache.dv), out_dtype or torch.bfloat16, stream)
     if lse is None and want_lse:
-        lse = _empty((Hq, T), torch.float32, q.device, stream)
+        lse = _empty((Hq, T), torch.float32, stream)
     if workspace is None:
         nbytes = load().slope_kv4_attn_workspace_size(block_table.shape[0], Hq, cache._c, q_len)
         if nbytes == 0:
             raise SlopeError(-8, "slope_kv4_attn_workspace_size")
-        workspace = _empty((nbytes,), torch.uint8, q.device, stream)
+        workspace = _empty((nbytes,), torch.uint8, stream)
     dev = cache.device_now()
     if workspace.get_device() != dev:
         raise ValueError(f"workspace on {workspace.device}, but the current device is cuda:{dev}")
