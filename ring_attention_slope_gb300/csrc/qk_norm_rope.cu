@@ -2,21 +2,23 @@
 // pass: y = x / sqrt(mean(x^2) + eps) * w, then the pairs (a, b) of the rotated
 // channels become (a cos t - b sin t, b cos t + a sin t), t = position * inv_freq.
 //
-// Bandwidth-bound: every value is read once and written once.  Eight lanes
-// share a head, each with 16-byte loads of 8 channels (d / 64 of them), so a
-// warp's load instruction covers four heads' consecutive 128 bytes.  A warp takes
-// one token and runs over its heads: the weights and the token's sines and cosines
-// are then the same for every head of a lane, and stay in its registers as
+// Bandwidth-bound: every value is read once and written once.  A lane has two words of eight channels (16
+// bytes of bf16) of a head, one and the one half a rotation away, so the pairs that the rotation mixes need no
+// other lane and no second load, whatever part of the head is rotated; words that are not rotated are paired
+// as they come.  A head of 64 channels takes 4 lanes, of 128 8, of 192 12 of 16.  A warp takes one token
+// and runs over its heads, two or three groups of them at a time with the next ones' loads in flight: the weights
+// and the token's sines and cosines are then the same for every head of a lane, and stay in its registers as
 //   y_e = (x_e A_e + x_partner B_e) / rms,   A = w cos, B = -+ w_partner sin.
+//
+// Measured, bf16: 32768 tokens, 64/8 heads of 64, all rotated, 107 us = 5.6 TB/s (83% of the copy rate); 8191 tokens,
+// 128/128 heads of 192, 274 us = 5.9 TB/s; 16384 tokens, 32/8 heads of 128, 62 us.  With eight lanes to a head of
+// any size, the other half fetched again or by shuffles, these took 118, 295 to 364 and 83 us; one group at
+// a time at the same registers 131 us; six CTAs an SM instead of four spill.  16 tokens: 2.7 us, which is the launch.
 //
 // Angles: position * inv_freq loses everything in fp32 at far positions (at
 // position 10^6 an fp32 angle is off by 0.06 radians).  The frequency is kept as
 // turns per position in 64-bit fixed point, so the product's low 64 bits are the
 // fraction of a turn, exactly, with no reduction.
-//
-// Halves layout: a lane needs the channels half a rotation away, which another
-// lane loads too.  It loads them again (they hit L1) rather than shuffle, since
-// with rotated parts of any size they may sit in any lane and register.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -33,9 +35,11 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kLanesPerHead = 8;
-constexpr int kHeadsPerPass = 32 / kLanesPerHead;  // heads a warp takes at a time
-constexpr int kMaxHalf = 96;                       // rotated pairs of a head
+constexpr int kMaxHalf = 96;  // rotated pairs of a head
+
+// Lanes that share a head (of 192 channels 12 of 16), and the heads that a warp's load covers.
+__host__ __device__ constexpr int lanes_per_head(int d) { return d == 64 ? 4 : d == 128 ? 8 : 16; }
+__host__ __device__ constexpr int heads_per_pass(int d) { return 32 / lanes_per_head(d); }
 
 struct NormRopeSide {
   const void* x;
@@ -101,25 +105,16 @@ __device__ __forceinline__ uint64_t weight_pair(const NormRopeSide& s, int64_t i
   return pack_f32x2(weight_at(s, i), weight_at(s, i + 1));
 }
 
-// A lane's factors for its channels: y_e = (x_e a_e + x_partner b_e) / rms.
-template <int kChunks>
-struct Factors {
-  uint64_t a[kChunks][4], b[kChunks][4];
-};
-
-// kInter: pairs are neighbours (and a pair's partner is in the same lane's channels), else halves.
+// kInter: the channels of a pair are neighbours, else half a rotation apart.
 template <typename TI, typename TO, int D, bool kInter>
-__global__ void __launch_bounds__(kThreads, D == 64 ? 6 : 4)
-    qk_norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
+__global__ void __launch_bounds__(kThreads, sizeof(TI) == 2 ? 4 : 3) qk_norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
   __shared__ __align__(16) float s_cos[kWarps][kMaxHalf], s_sin[kWarps][kMaxHalf];  // of the warp's token
   __shared__ __align__(16) float s_w[2][D];  // weights shared by every head of a side, else 1
-  constexpr int kChunks = D / 64;
-  constexpr int kWide = D == 64 && sizeof(TI) == 2 ? 2 : 1;  // groups of four heads in a pass
-  // a 64-channel bf16 head lies in one 16-byte word of its eight lanes: the other half comes by shuffle
-  constexpr bool kShuffle = D == 64 && sizeof(TI) == 2 && !kInter;
-  constexpr bool kLoadPartner = !kInter && !kShuffle;
+  constexpr int kLanes = lanes_per_head(D), kHeads = heads_per_pass(D), kUsed = D / 16;
+  constexpr int kWide = D == 192 && sizeof(TI) == 2 ? 3 : 2;  // groups of kHeads in a pass
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int lane8 = lane % kLanesPerHead, sub = lane / kLanesPerHead;
+  const int li = min(lane % kLanes, kUsed - 1), sub = lane / kLanes;
+  const bool used = lane % kLanes < kUsed;
   const int64_t task = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
   const int64_t tok = task / p.splits;
   const bool here = tok < p.T;
@@ -132,39 +127,41 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 6 : 4)
     const int base = w ? p.side[0].H : 0;
     h_begin[w] = max(first - base, 0);
     h_end[w] = min(last - base, p.side[w].H);
-    n_pass[w] = h_begin[w] < h_end[w] ? (h_end[w] - h_begin[w] + kHeadsPerPass * kWide - 1) / (kHeadsPerPass * kWide) : 0;
+    n_pass[w] = h_begin[w] < h_end[w] ? (h_end[w] - h_begin[w] + kHeads * kWide - 1) / (kHeads * kWide) : 0;
   }
-  // elements from a chunk of the lane to the other half of its pairs (0: not rotated; 1: neighbours)
-  int partner[kChunks];
+  // The lane's two words: a word and the one half a rotation away, the first lanes of a head; then the words that
+  // are not rotated.  Interleaved: neighbours.
+  int ch[2];
+  bool rot[2];
+  if constexpr (kInter) {
 #pragma unroll
-  for (int c = 0; c < kChunks; ++c) {
-    const int off = c * 64 + lane8 * 8 - p.begin;
-    partner[c] = !p.rotate || off < 0 || off >= 2 * p.half ? 0 : kInter ? 1 : off < p.half ? p.half : -p.half;
+    for (int i = 0; i < 2; ++i) {
+      ch[i] = 16 * li + 8 * i;
+      rot[i] = p.rotate && ch[i] >= p.begin && ch[i] < p.begin + 2 * p.half;
+    }
+  } else {
+    const int n = p.rotate ? p.half / 8 : 0;  // pairs of rotated words
+    rot[0] = rot[1] = li < n;
+    const int a = 2 * (li - n);               // among the words that are not rotated
+    ch[0] = li < n ? p.begin + 8 * li : 8 * a + (8 * a < p.begin ? 0 : 16 * n);
+    ch[1] = li < n ? ch[0] + p.half : 8 * a + 8 + (8 * a + 8 < p.begin ? 0 : 16 * n);
   }
-  Raw8<TI> v[kWide][kChunks], o[kWide][kChunks];
-#pragma unroll
-  for (int k = 0; k < kWide; ++k)
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c) o[k][c] = Raw8<TI>{};
-  auto fetch = [&](int pass, Raw8<TI>(&fv)[kWide][kChunks], Raw8<TI>(&fo)[kWide][kChunks]) {
+  Raw8<TI> v[kWide][2];
+  auto fetch = [&](int pass, Raw8<TI>(&fv)[kWide][2]) {
     const int w = pass >= n_pass[0] ? 1 : 0;
     const NormRopeSide& s = p.side[w];
-    const int h0 = w ? h_begin[1] + (pass - n_pass[0]) * (kHeadsPerPass * kWide) : h_begin[0] + pass * (kHeadsPerPass * kWide);
-    const TI* const x = static_cast<const TI*>(s.x) + tok * s.x_srow + lane8 * 8;
+    const int h0 = w ? h_begin[1] + (pass - n_pass[0]) * (kHeads * kWide) : h_begin[0] + pass * (kHeads * kWide);
+    const TI* const x = static_cast<const TI*>(s.x) + tok * s.x_srow;
 #pragma unroll
     for (int k = 0; k < kWide; ++k) {
       // past the last head: its values once more, which are not stored
-      const int h = min(h0 + k * kHeadsPerPass + sub, (w ? h_end[1] : h_end[0]) - 1);
-      const TI* const xh = x + h * s.x_shead;
+      const int h = min(h0 + k * kHeads + sub, (w ? h_end[1] : h_end[0]) - 1);
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        fv[k][c].load(xh + c * 64);
-        if (kLoadPartner && partner[c] != 0) fo[k][c].load(xh + c * 64 + partner[c]);
-      }
+      for (int i = 0; i < 2; ++i) fv[k][i].load(x + h * s.x_shead + ch[i]);
     }
   };
   const int passes = n_pass[0] + n_pass[1];
-  if (passes > 0) fetch(0, v, o);
+  if (passes > 0) fetch(0, v);
 
   for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
     const NormRopeSide& s = p.side[i / D];
@@ -183,129 +180,121 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 6 : 4)
   }
   __syncthreads();
 
-  Factors<kChunks> f;
+  // y_e = (x_e fa_e + x_partner fb_e) / rms
+  uint64_t fa[2][4], fb[2][4];
   auto set_factors = [&](int which) {
+    float a[2][8], b[2][8];
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      const int e = c * 64 + lane8 * 8, off = e - p.begin;
-      const bool in = partner[c] != 0;
-      float fa[8], fb[8];
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int i = 0; i < 8; i += 4) {
-        const float4 w = *reinterpret_cast<const float4*>(&s_w[which][e + i]);
-        fa[i] = w.x, fa[i + 1] = w.y, fa[i + 2] = w.z, fa[i + 3] = w.w;
-        fb[i] = fb[i + 1] = fb[i + 2] = fb[i + 3] = 0.f;
+      for (int e = 0; e < 8; e += 4) {
+        const float4 w = *reinterpret_cast<const float4*>(&s_w[which][ch[i] + e]);
+        a[i][e] = w.x, a[i][e + 1] = w.y, a[i][e + 2] = w.z, a[i][e + 3] = w.w;
+        b[i][e] = b[i][e + 1] = b[i][e + 2] = b[i][e + 3] = 0.f;
       }
-      if (in && kInter) {
-        const float4 cs = *reinterpret_cast<const float4*>(&s_cos[warp][off / 2]);
-        const float4 sn = *reinterpret_cast<const float4*>(&s_sin[warp][off / 2]);
+    if constexpr (kInter) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (!rot[i]) continue;
+        const float4 cs = *reinterpret_cast<const float4*>(&s_cos[warp][(ch[i] - p.begin) / 2]);
+        const float4 sn = *reinterpret_cast<const float4*>(&s_sin[warp][(ch[i] - p.begin) / 2]);
         const float c4[4] = {cs.x, cs.y, cs.z, cs.w}, s4[4] = {sn.x, sn.y, sn.z, sn.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          fb[2 * i] = -fa[2 * i + 1] * s4[i];
-          fb[2 * i + 1] = fa[2 * i] * s4[i];
-          fa[2 * i] *= c4[i];
-          fa[2 * i + 1] *= c4[i];
-        }
-      } else if (in) {
-        const int at = off < p.half ? off : off - p.half;
-        const float sign = off < p.half ? -1.f : 1.f;
-#pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-          const float4 cs = *reinterpret_cast<const float4*>(&s_cos[warp][at + i]);
-          const float4 sn = *reinterpret_cast<const float4*>(&s_sin[warp][at + i]);
-          const float4 w = *reinterpret_cast<const float4*>(&s_w[which][e + i + partner[c]]);
-          fb[i] = sign * sn.x * w.x, fb[i + 1] = sign * sn.y * w.y, fb[i + 2] = sign * sn.z * w.z, fb[i + 3] = sign * sn.w * w.w;
-          fa[i] *= cs.x, fa[i + 1] *= cs.y, fa[i + 2] *= cs.z, fa[i + 3] *= cs.w;
+        for (int e = 0; e < 4; ++e) {
+          b[i][2 * e] = -a[i][2 * e + 1] * s4[e];
+          b[i][2 * e + 1] = a[i][2 * e] * s4[e];
+          a[i][2 * e] *= c4[e];
+          a[i][2 * e + 1] *= c4[e];
         }
       }
+    } else if (rot[0]) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f.a[c][i] = pack_f32x2(fa[2 * i], fa[2 * i + 1]);
-        f.b[c][i] = pack_f32x2(fb[2 * i], fb[2 * i + 1]);
+      for (int e = 0; e < 8; e += 4) {
+        const float4 cs = *reinterpret_cast<const float4*>(&s_cos[warp][8 * li + e]);
+        const float4 sn = *reinterpret_cast<const float4*>(&s_sin[warp][8 * li + e]);
+        const float c4[4] = {cs.x, cs.y, cs.z, cs.w}, s4[4] = {sn.x, sn.y, sn.z, sn.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          b[0][e + j] = -a[1][e + j] * s4[j];
+          b[1][e + j] = a[0][e + j] * s4[j];
+          a[0][e + j] *= c4[j];
+          a[1][e + j] *= c4[j];
+        }
       }
     }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        fa[i][e] = pack_f32x2(a[i][2 * e], a[i][2 * e + 1]);
+        fb[i][e] = pack_f32x2(b[i][2 * e], b[i][2 * e + 1]);
+      }
   };
 
 #pragma unroll 1
   for (int pass = 0; pass < passes; ++pass) {
     const int which = pass >= n_pass[0] ? 1 : 0;
     const NormRopeSide& s = p.side[which];
-    const int h0 = which ? h_begin[1] + (pass - n_pass[0]) * (kHeadsPerPass * kWide) : h_begin[0] + pass * (kHeadsPerPass * kWide);
+    const int h0 = which ? h_begin[1] + (pass - n_pass[0]) * (kHeads * kWide) : h_begin[0] + pass * (kHeads * kWide);
     const int end = which ? h_end[1] : h_end[0];
     const bool per_head = s.w_shead != 0;
     if (pass == 0 || pass == n_pass[0]) set_factors(which);
     // the next pass's loads are in flight during this one (its heads are others, so in place they are unwritten)
-    Raw8<TI> nv[kWide][kChunks], no[kWide][kChunks];
+    Raw8<TI> nv[kWide][2];
 #pragma unroll
     for (int k = 0; k < kWide; ++k)
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) nv[k][c] = v[k][c], no[k][c] = o[k][c];
-    if (pass + 1 < passes) fetch(pass + 1, nv, no);
-    float scale[kWide];
+      for (int i = 0; i < 2; ++i) nv[k][i] = v[k][i];
+    if (pass + 1 < passes) fetch(pass + 1, nv);
+    TO* const y = static_cast<TO*>(s.y) + tok * s.y_srow;
 #pragma unroll
     for (int k = 0; k < kWide; ++k) {
-      scale[k] = 1.f;
+      uint64_t x[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[i][e] = v[k][i].pair(e);
+      float scale = 1.f;
       if (p.norm) {
         uint64_t sq2 = 0;
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sq2 = fma_f32x2(v[k][c].pair(i), v[k][c].pair(i), sq2);
+          for (int e = 0; e < 4; ++e) sq2 = fma_f32x2(x[i][e], x[i][e], sq2);
         const float2 sq = unpack_f32x2(sq2);
-        float sum = sq.x + sq.y;
+        float sum = used ? sq.x + sq.y : 0.f;
 #pragma unroll
-        for (int m = 1; m < kLanesPerHead; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-        scale[k] = rsqrtf(fmaf(sum, 1.f / D, p.eps));
+        for (int m = 1; m < kLanes; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+        scale = rsqrtf(fmaf(sum, 1.f / D, p.eps));
       }
-    }
-    if constexpr (kShuffle) {
-      const int from = lane + partner[0] / 8;  // lanes that are not rotated get their own, and do not use it
+      const int h = h0 + k * kHeads + sub;
+      if (h >= end || !used) continue;
+      if (per_head) {
 #pragma unroll
-      for (int k = 0; k < kWide; ++k)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) (&o[k][0].r[0].x)[i] = __shfl_sync(0xffffffffu, (&v[k][0].r[0].x)[i], from);
-    }
-    __syncwarp();  // in place: every lane has read what it needs of these heads
-    TO* const y = static_cast<TO*>(s.y) + tok * s.y_srow + lane8 * 8;
-#pragma unroll
-    for (int k = 0; k < kWide; ++k) {
-      const int h = h0 + k * kHeadsPerPass + sub;
-      if (h >= end) continue;
-      const uint64_t scale2 = pack_f32x2(scale[k], scale[k]);
+          for (int e = 0; e < 4; ++e) x[i][e] = mul_f32x2(x[i][e], weight_pair(s, h * s.w_shead + ch[i] + 2 * e));
+      }
+      const uint64_t scale2 = pack_f32x2(scale, scale);
       TO* const yh = y + h * s.y_shead;
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        uint64_t vv[4], oo[4], out[4];
+      for (int i = 0; i < 2; ++i) {
+        uint64_t out[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          vv[i] = v[k][c].pair(i);
-          oo[i] = kInter ? swapped(vv[i]) : o[k][c].pair(i);
-        }
-        if (per_head) {
-          const int64_t wi = h * s.w_shead + c * 64 + lane8 * 8;
+        for (int e = 0; e < 4; ++e) out[e] = mul_f32x2(x[i][e], fa[i][e]);
+        if (rot[i]) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            vv[i] = mul_f32x2(vv[i], weight_pair(s, wi + 2 * i));
-            if (!kInter && partner[c] != 0) oo[i] = mul_f32x2(oo[i], weight_pair(s, wi + 2 * i + partner[c]));
-            if (kInter) oo[i] = swapped(vv[i]);
-          }
+          for (int e = 0; e < 4; ++e) out[e] = fma_f32x2(kInter ? swapped(x[i][e]) : x[1 - i][e], fb[i][e], out[e]);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) out[i] = mul_f32x2(vv[i], f.a[c][i]);
-        if (partner[c] != 0) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) out[i] = fma_f32x2(oo[i], f.b[c][i], out[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) out[i] = mul_f32x2(out[i], scale2);
-        store8(yh + c * 64, out);
+        for (int e = 0; e < 4; ++e) out[e] = mul_f32x2(out[e], scale2);
+        store8(yh + ch[i], out);
       }
     }
 #pragma unroll
     for (int k = 0; k < kWide; ++k)
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) v[k][c] = nv[k][c], o[k][c] = no[k][c];
+      for (int i = 0; i < 2; ++i) v[k][i] = nv[k][i];
   }
 }
 
@@ -435,10 +424,10 @@ extern "C" slope_status slope_qk_norm_rope(const slope_tensor* q, const slope_te
   p.norm = norm != 0 ? 1 : 0;
   const int64_t H = p.side[0].H + p.side[1].H;
   // A warp to a token once there are enough tokens to fill the GPU (about 32 warps on each of 152 SMs),
-  // else several warps, down to one pass of four heads each, for the shortest call.
+  // else several warps, down to the heads of one pass each, for the shortest call.
   const int64_t want = (H * T + 4863) / 4864;
-  p.heads = static_cast<int32_t>(std::min<int64_t>(
-      (H + kHeadsPerPass - 1) / kHeadsPerPass, (want + kHeadsPerPass - 1) / kHeadsPerPass) * kHeadsPerPass);
+  const int64_t at_once = d == 192 ? 6 : heads_per_pass(d);
+  p.heads = static_cast<int32_t>(std::min((H + at_once - 1) / at_once, (want + at_once - 1) / at_once) * at_once);
   p.splits = static_cast<int32_t>((H + p.heads - 1) / p.heads);
   const int64_t ctas = (T * p.splits + kWarps - 1) / kWarps;
   if (ctas > 0x7fffffffLL) return SLOPE_ERR_SHAPE;
