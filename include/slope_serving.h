@@ -213,8 +213,9 @@ SLOPE_API slope_status slope_kv4_read(const slope_kv4_cache* cache, const int32_
  *
  * Cached values are exact in the products; the softmax weights, times a group's
  * scale, are rounded to bf16 on their way into the tensor cores (as the weights
- * of slope_attn_partial are), sums run in fp32.  Value scales have to lie below
- * 2^54 or the output overflows; contributions below about 2^-57 times the
+ * of slope_attn_partial are), which moves the output by at most 2^-8 of the
+ * weighted mean of scale * |code - 8|; sums run in fp32.  Value scales have to lie below
+ * 2^51 or the output overflows; contributions below about 2^-57 times the
  * weight are lost.  A query row's channels keep their bits down to 2^-26 of the
  * row's largest, which has to be below 2^117 (else the row is NaN); scaled scores
  * have to stay below 2^29 in magnitude, where fp32 no longer tells weights apart.

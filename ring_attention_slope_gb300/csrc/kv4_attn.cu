@@ -7,8 +7,9 @@
 // each group G of 32 channels of a token's head.  The codes go to the tensor
 // cores as they are and the scales stay outside:
 //   q . k_j  = sum_G ( scale_jG * (sum_c q_c code_jc) + min_jG * (sum_c q_c) )
-//   sum_j w_j v_jc = sum_j (w_j scale_jG) code_jc + sum_j w_j min_jG
-// so a code costs a mask and half a shift, not a conversion.
+//   sum_j w_j v_jc = sum_j r_jG code_jc + sum_j ( w_j (min_jG + 8 scale_jG) - 8 r_jG ),  r_jG = w_j scale_jG
+// so a code costs a mask and half a shift, not a conversion.  r is rounded to bf16 for the tensor cores, and its
+// error meets code - 8 rather than code: most values lie near the middle of their group's range.
 //
 // Codes as matrix operands.  A float whose exponent field is 0 or 1 is linear in its bits, so the low 8
 // bits of a 16-bit float, alone, are an exact multiple of its smallest subnormal: a 4-bit code in bits 0-3 is
@@ -25,6 +26,13 @@
 // step on the narrow side no multiply is wasted on padding at 8 heads per KV head.
 // The block layout in memory is the operand layout, so a lane's codes of 16 keys
 // are its own 16-byte words; P^T needs one 8x8 transpose (movmatrix) a group.
+//
+// Measured at 64/8 heads of 64: 8 sequences of 102400 tokens 102 us = 5.1 TB/s of cache (75% of the copy rate); 32
+// ragged ones up to 32768 29.4 us; one of 65536 17.5 us; one of 1000 7.5 us.  (Around the groups' minimums
+// instead of their middles 3 to 4% less, with 2.4 times the error.)  At the first the ALU pipe is over half busy,
+// the issue slots over 60%, DRAM two thirds: a warp's step of 64 tokens is about as long in instructions as its codes
+// are on the way.  (The copies alone, without the arithmetic, took 84 us.)  The short ones are latency: the
+// lengths, the page table, one copy, the steps, the join of the warps and that of the CTAs, one after another.
 //
 // Work split: every sequence's visible steps of 64 or 32 tokens, for each KV head (and each
 // tile of 8 NT query rows), laid end to end and cut into equal ranges, one for each
@@ -456,16 +464,17 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
     }
 
     // ---- the steps
-    float nm[NT][2], l[NT][2], bias[NT][C::NV][2], o[C::NC][2][2][NT][4];  // nm: 64 - running maximum
+    float nm[NT][2], l[NT][2], o[C::NC][2][2][NT][4];  // nm: 64 - running maximum
+    uint64_t bias[NT][C::NV];                           // of both rows
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         nm[t][j] = 64.f - kNoMax;
         l[t][j] = 0.f;
-#pragma unroll
-        for (int G = 0; G < C::NV; ++G) bias[t][G][j] = 0.f;
       }
+#pragma unroll
+      for (int G = 0; G < C::NV; ++G) bias[t][G] = 0;
 #pragma unroll
       for (int c = 0; c < C::NC; ++c)
 #pragma unroll
@@ -564,7 +573,8 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
             const float alpha = ex2_approx(m - (64.f - nm[t][j]));
             l[t][j] *= alpha;
 #pragma unroll
-            for (int G = 0; G < C::NV; ++G) bias[t][G][j] *= alpha;
+            for (int G = 0; G < C::NV; ++G)
+              bias[t][G] = mul_f32x2(bias[t][G], j == 0 ? pack_f32x2(alpha, 1.f) : pack_f32x2(1.f, alpha));
 #pragma unroll
             for (int c = 0; c < C::NC; ++c)
 #pragma unroll
@@ -605,25 +615,31 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
             word[i][2 * h] = r.x, word[i][2 * h + 1] = r.y;
           }
         }
-        // the weights' operands for each group of values
+        // the weights' operands for each group of values, and what the products leave out (see the top)
+        const uint64_t minus8 = pack_f32x2(-8.f, -8.f);
         uint32_t pb[NT][C::NV][2];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           const float(&ww)[4] = w[j][t];
 #pragma unroll
           for (int G = 0; G < C::NV; ++G) {
-            float s[4], n[4];  // scale and min by element
-            s[0] = s[1] = __uint_as_float(word[0][G] & 0xffff0000u), s[2] = s[3] = __uint_as_float(word[1][G] & 0xffff0000u);
-            n[0] = n[1] = __uint_as_float(word[0][G] << 16), n[2] = n[3] = __uint_as_float(word[1][G] << 16);
-            if constexpr (kEdge) {  // a hidden key's scale and min may be anything, NaN too
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (ww[e] == 0.f) s[e] = n[e] = 0.f;
+            for (int i = 0; i < 2; ++i) {  // tokens g and g + 8
+              const uint64_t w2 = pack_f32x2(ww[2 * i], ww[2 * i + 1]);
+              uint64_t s2 = pack_f32x2(__uint_as_float(word[i][G] & 0xffff0000u), __uint_as_float(word[i][G] & 0xffff0000u));
+              float mid = fmaf(__uint_as_float(word[i][G] & 0xffff0000u), 8.f, __uint_as_float(word[i][G] << 16));
+              uint64_t m2 = pack_f32x2(mid, mid);
+              if constexpr (kEdge) {  // a hidden key's scale and min may be anything, NaN too
+                const float2 sf = unpack_f32x2(s2);
+                s2 = pack_f32x2(ww[2 * i] == 0.f ? 0.f : sf.x, ww[2 * i + 1] == 0.f ? 0.f : sf.y);
+                m2 = pack_f32x2(ww[2 * i] == 0.f ? 0.f : mid, ww[2 * i + 1] == 0.f ? 0.f : mid);
+              }
+              const float2 ws = unpack_f32x2(mul_f32x2(w2, s2));
+              const uint32_t r = pack_bf16x2(ws.x, ws.y);
+              const uint64_t r2 = pack_f32x2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
+              bias[t][G] = fma_f32x2(w2, m2, fma_f32x2(r2, minus8, bias[t][G]));
+              pb[t][G][i] = transpose8x8(r);
             }
-            bias[t][G][0] = fmaf(ww[0], n[0], fmaf(ww[2], n[2], bias[t][G][0]));
-            bias[t][G][1] = fmaf(ww[1], n[1], fmaf(ww[3], n[3], bias[t][G][1]));
-            pb[t][G][0] = transpose8x8(pack_bf16x2(ww[0] * s[0], ww[1] * s[1]));
-            pb[t][G][1] = transpose8x8(pack_bf16x2(ww[2] * s[2], ww[3] * s[3]));
           }
         }
 #pragma unroll
@@ -699,11 +715,14 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
+        float both[C::NV];
+#pragma unroll
+        for (int G = 0; G < C::NV; ++G) both[G] = j == 0 ? unpack_f32x2(bias[t][G]).x : unpack_f32x2(bias[t][G]).y;
 #pragma unroll
         for (int s = 4; s < 32; s <<= 1) {
           l[t][j] += __shfl_xor_sync(0xffffffffu, l[t][j], s);
 #pragma unroll
-          for (int G = 0; G < C::NV; ++G) bias[t][G][j] += __shfl_xor_sync(0xffffffffu, bias[t][G][j], s);
+          for (int G = 0; G < C::NV; ++G) both[G] += __shfl_xor_sync(0xffffffffu, both[G], s);
         }
         const int rr = t * 8 + 2 * q4 + j;
         if (g == 0) {
@@ -714,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
         for (int c = 0; c < C::NC; ++c)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float bs = bias[t][2 * c + h][j] * 0x1p-64f;
+            const float bs = both[2 * c + h] * 0x1p-64f;
             *reinterpret_cast<float4*>(red + (warp * C::R + rr) * DV + 64 * c + 32 * h + 4 * g) =
                 make_float4(fmaf(o[c][h][0][t][j], 0x1p69f, bs), fmaf(o[c][h][0][t][2 + j], 0x1p65f, bs),
                             fmaf(o[c][h][1][t][j], 0x1p69f, bs), fmaf(o[c][h][1][t][2 + j], 0x1p65f, bs));

@@ -56,6 +56,12 @@ def values(code, scale, low):
     return low.double().repeat_interleave(GROUP, -1) + scale.double().repeat_interleave(GROUP, -1) * code.double()
 
 
+def from_middle(code, scale, low):
+    """What the rounding of weight * scale is multiplied by: scale * |code - 8|, and 2^-10 of the scale for the middle's
+    own terms, which are fp32 sums of up to 16 scales each (2^-20 of them, over a thousand steps)."""
+    return scale.double().repeat_interleave(GROUP, -1) * ((code - 8).abs().double() + 2.0 ** -10)
+
+
 def block_bytes(dqk, dv):
     return BLOCK * (dqk // 2 + dv // 2 + 4 * (dqk + dv) // GROUP)
 
@@ -98,7 +104,7 @@ def write_bytes(data, slots, k, v, page_size):
 # ---------------------------------------------------------------- attention over known values
 
 def decode(q, k, v, spread, kv_len, q_len, window, scale):
-    """One sequence: q [q_len, Hq, dqk], k [keys, H, dqk], v [keys, H, dv], spread = v - min >= 0 (fp64).
+    """One sequence: q [q_len, Hq, dqk], k [keys, H, dqk], v [keys, H, dv], spread = from_middle of the values (fp64).
 
     Returns out, lse and, for the bounds, sum p * spread, sum p * |v| per output, and the largest
     sum of |q| |k| of a row's visible scores."""

@@ -6,7 +6,8 @@ Tolerances, from the arithmetic:
 * norm and rotation: an angle is off by at most 2^-24 of a turn (2^-21.3 radians), and fewer than 16 fp32 roundings
   of at most the pair's size follow: 2^-20 of the pair's size, besides the output's own rounding.
 * cache: the codes, scales and minimums are exact; a value is one fp32 rounding, then the output's.
-* cache attention: weight * scale is rounded to bf16 once (2^-8 of sum p * (v - min)); scores are sums of at most 192
+* cache attention: weight * scale is rounded to bf16 once and multiplies code - 8, the rest of a value being added in
+  fp32 (2^-8 of sum p * scale * |code - 8|); scores are sums of at most 192
   products in fp32, off by at most 2^-18 of sum |q| |k|, which moves a weight by as much again.
 * packed prompts: the bounds that the prefill attention's own tests use.
 """
@@ -255,7 +256,7 @@ def paged(lens, page, H, dqk, dv, seed, extra=3, scale=1.0, garbage=True):
             slope.kv4_write(cache, k.cuda(), v.cuda(), i32(slots))
         kq, vq = so.quantise(k), so.quantise(v)
         kk, vv = so.values(*kq), so.values(*vq)
-        held.append((kk, vv, vv - vq[2].double().repeat_interleave(32, -1)))
+        held.append((kk, vv, so.from_middle(*vq)))
     return cache, table, held
 
 
@@ -356,7 +357,7 @@ def test_decode_magnitudes(qs, ks, vs):
         t = torch.arange(n)
         slope.kv4_write(cache, k.cuda(), v.cuda(), i32(table[b, (t // page).long()].long() * page + t % page))
         kq, vq = so.quantise(k), so.quantise(v)
-        held.append((so.values(*kq), so.values(*vq), so.values(*vq) - vq[2].double().repeat_interleave(32, -1)))
+        held.append((so.values(*kq), so.values(*vq), so.from_middle(*vq)))
     q = rand(2, Hq, d, seed=90, scale=qs)
     out, lse = slope.kv4_attn(q.cuda(), cache, table.cuda(), i32(lens), out_dtype=torch.float32)
     check_decode(out, lse, q, held, lens, 1, 0, 0.125)
@@ -387,7 +388,7 @@ def test_decode_hidden_values_do_not_leak():
     out, lse = slope.kv4_attn(q.cuda(), cache, table.cuda(), i32([n]), q_len=2, window=30)
     kq, vq = so.quantise(k), so.quantise(v)
     kk, vv = so.values(*kq), so.values(*vq)
-    ref, rl, wide, size, reach = so.decode(q[:1], kk, vv, vv - vq[2].double().repeat_interleave(32, -1), n - 1, 1, 30, 0.125)
+    ref, rl, wide, size, reach = so.decode(q[:1], kk, vv, so.from_middle(*vq), n - 1, 1, 30, 0.125)
     assert torch.isfinite(out[0].float()).all() and torch.isnan(out[1].float()).all()
     assert ((out[:1].cpu().double() - ref).abs() <= 2.0 ** -7 * (wide + size)).all()
     assert torch.isfinite(lse).all()
@@ -497,7 +498,7 @@ def test_offsets_past_32_bits():
         slots = i32(table[b, t // page].long() * page + t % page)
         slope.kv4_write(cache, k.cuda(), v.cuda(), slots)
         kq, vq = so.quantise(k), so.quantise(v)
-        held.append((so.values(*kq), so.values(*vq), so.values(*vq) - vq[2].double().repeat_interleave(32, -1)))
+        held.append((so.values(*kq), so.values(*vq), so.from_middle(*vq)))
         ko, vo = slope.kv4_read(cache, slots)
         assert ((ko.cpu().double() - held[b][0]).abs() <= (2.0 ** -8 + 2.0 ** -24) * held[b][0].abs()).all()
         assert ((vo.cpu().double() - held[b][1]).abs() <= (2.0 ** -8 + 2.0 ** -24) * held[b][1].abs()).all()
