@@ -48,7 +48,7 @@
 // group, as many as divide the group (at most 32), in (token, head) order.  A tile of 128 tokens of one head
 // would be mostly empty for short prompts and its diagonal half empty for all; 16 tokens of 8 heads fill
 // it: 40 prompts of 50 tokens, 64/8 heads of 64, take 24 us, 5 prompts of 670 to 5200 384 us (7% more with one
-// head to a tile), one of 12288 1.10 ms = 1120 TFLOP/s (1.08 ms unpacked).  TMA boxes of 2^s heads load Q and store the
+// head to a tile), one of 12288 1.08 ms = 1140 TFLOP/s (as unpacked).  TMA boxes of 2^s heads load Q and store the
 // output; rows past a sequence's end are stored directly.  Bound as the unpacked kernel is, by the
 // exponentials and the steps' latency (tensor pipe 41% busy, MUFU 42%), and below 128 tokens by the work
 // tile's start and end, about 4 us each.  (For tiles whose second half no row sees, a softmax of half a tile made
@@ -355,9 +355,18 @@ template <bool kDynamic>
 __device__ __forceinline__ int first_tile() {
   return kDynamic ? 0 : static_cast<int>(blockIdx.x);
 }
-template <bool kDynamic>
-__device__ __forceinline__ int tile_stride() {
-  return kDynamic ? 0 : static_cast<int>(gridDim.x);
+// A packed launch of one sequence, whose tiles are ordered by weight, goes forth and back over the CTAs, so that
+// none has the heaviest of every round (2000 tokens, 64/8 heads of 64: 53 -> 49 us; with several sequences
+// it cost as much as it gained).
+template <bool kDynamic, bool PK>
+__device__ __forceinline__ int tile_stride(const AttnParams& p) {
+  if (kDynamic) return 0;
+  return static_cast<int>(PK && p.n_items == 1 ? 2 * (gridDim.x - blockIdx.x) - 1 : gridDim.x);
+}
+template <bool kDynamic, bool PK>
+__device__ __forceinline__ void next_tile(const AttnParams& p, int& w, int& dw) {
+  w += dw;
+  if (PK && !kDynamic && p.n_items == 1) dw = 2 * static_cast<int>(gridDim.x) - dw;
 }
 
 // For a CTA that computes no more tiles of a launch whose tiles are claimed at run time:
@@ -514,7 +523,7 @@ __global__ void __launch_bounds__(K1Cfg<DQK, DV, QT>::kThreads, K1Cfg<DQK, DV, Q
       bool ok = true;
       int item_hint = 0;
       int k = 0;
-      for (int w = first_tile<C::kDynamicTiles>(); w < total; w += tile_stride<C::kDynamicTiles>()) {
+      for (int w = first_tile<C::kDynamicTiles>(), dw = tile_stride<C::kDynamicTiles, PK>(p); w < total; next_tile<C::kDynamicTiles, PK>(p, w, dw)) {
         if constexpr (C::kDynamicTiles) {
           if (!take_tile(k++, w, false)) {
             ok = false;
@@ -638,7 +647,8 @@ __global__ void __launch_bounds__(K1Cfg<DQK, DV, QT>::kThreads, K1Cfg<DQK, DV, Q
       int wt = 0;
       int item_hint = 0;
       int k = 0;
-      for (int w = first_tile<C::kDynamicTiles>(); w < total && ok; w += tile_stride<C::kDynamicTiles>()) {
+      for (int w = first_tile<C::kDynamicTiles>(), dw = tile_stride<C::kDynamicTiles, PK>(p); w < total && ok;
+           next_tile<C::kDynamicTiles, PK>(p, w, dw)) {
         if constexpr (C::kDynamicTiles) {
           if (!take_tile(k++, w, false)) {
             ok = false;
@@ -748,7 +758,8 @@ __global__ void __launch_bounds__(K1Cfg<DQK, DV, QT>::kThreads, K1Cfg<DQK, DV, Q
     bool ok = true;
     int item_hint = 0;
     int k = 0;
-    for (int w = first_tile<C::kDynamicTiles>(); w < total && ok; w += tile_stride<C::kDynamicTiles>()) {
+    for (int w = first_tile<C::kDynamicTiles>(), dw = tile_stride<C::kDynamicTiles, PK>(p); w < total && ok;
+           next_tile<C::kDynamicTiles, PK>(p, w, dw)) {
       if constexpr (C::kDynamicTiles) {
         if (!take_tile(k++, w, true)) {
           ok = false;
@@ -1289,10 +1300,32 @@ cudaError_t launch_attn_partial(int dqk, int dv, const CUtensorMap& tq, const CU
   return cudaErrorInvalidValue;
 }
 
+// Whether a packed launch at d = 64 takes two Q tiles to a CTA: where its work tiles are short, but longer than one
+// step (1.2 to 4.5 on average), and few of them are half empty, and the CTAs get two rounds of them.  Measured, one
+// tile and two, 64/8 heads: 64 prompts of 128 tokens 61 and 66 us, 53 of 150 83 and 69, 26 of 300 105 and 79, 16 of
+// 500 112 and 90, 8 of 1000 136 and 123, 5 of 1400 129 and 131, 4 of 2000 176 and 183; 8/8 heads, 12 of 500 16
+// and 16.
+bool packed_two_tiles(const AttnParams& p) {
+  const int64_t rows = kBlockM >> p.pack_shift, units = p.Hq >> p.pack_shift;
+  int64_t tiles = 0, pairs = 0, steps = 0;
+  for (int i = 0; i < p.n_items; ++i) {
+    const int64_t len = p.seqs[i].len, n = (len + rows - 1) / rows;
+    const int64_t full = len / kBlockN, before = full << p.pack_shift;  // Q tiles of the full key tiles' rows
+    tiles += n;
+    pairs += (n + 1) / 2;
+    if (p.causal)
+      steps += full * (full + 1) / 2 * (int64_t(1) << p.pack_shift) + (n - before) * (full + 1);
+    else
+      steps += n * ((len + kBlockN - 1) / kBlockN);
+  }
+  return 5 * steps >= 6 * tiles && 2 * steps <= 9 * tiles && 20 * pairs <= 11 * tiles &&
+         pairs * units >= 2 * resident_ctas();
+}
+
 cudaError_t launch_attn_packed(int dqk, int dv, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                const CUtensorMap& to, const AttnParams& p, bool dependent, cudaStream_t stream) {
   if (dqk == 64 && dv == 64) {
-    if (p.window > 0 && p.window <= kTwoTileMaxWindow)
+    if ((p.window > 0 && p.window <= kTwoTileMaxWindow) || packed_two_tiles(p))
       return launch_impl<64, 64, 2, true>(tq, tk, tv, to, p, dependent, stream);
     return launch_impl<64, 64, 1, true>(tq, tk, tv, to, p, dependent, stream);
   }

@@ -605,6 +605,16 @@ def test_varlen_masks(window, causal, dqk, dv, Hq, H):
     check_varlen(*packed([40, 333, 130, 700], Hq, H, dqk, dv, 160), window=window, causal=causal)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lens", [[180] * 30, [256] * 24, [117, 353, 588] * 6, [150, 1] * 36])
+def test_varlen_many_middling(lens, causal):
+    """Enough short work tiles of 64-wide heads that two Q tiles share a CTA, with NaN behind the last sequence."""
+    q, k, v, cu = packed(lens, 16, 2, 64, 64, 168, lead=3, tail=20)
+    for x in (q, k, v):
+        x[:3] = x[cu[-1]:] = float("nan")
+    check_varlen(q, k, v, cu, causal=causal, heads=[0, 7, 8, 15])
+
+
 @pytest.mark.parametrize("dqk,dv", [(64, 64), (128, 128), (192, 64), (192, 128)])
 def test_varlen_second_tile_starts_at_a_sequence_end(dqk, dv):
     """A CTA's second Q tile whose first step is the last, partial one, many times over: the V rows that it clears are
