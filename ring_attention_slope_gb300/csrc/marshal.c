@@ -30,14 +30,16 @@ static struct {
   slope_status (*kv4_read)(const slope_kv4_cache*, const int32_t*, slope_tensor*, slope_tensor*, void*);
   slope_status (*kv4_attn)(const slope_tensor*, const slope_kv4_cache*, const int32_t*, int64_t, int64_t,
                            const int32_t*, int32_t, int64_t, float, slope_tensor*, slope_tensor*, void*, size_t, void*);
+  size_t (*cache_bytes)(int64_t, int32_t, int32_t, int32_t, int32_t);
+  size_t (*attn_workspace_size)(int64_t, int64_t, const slope_kv4_cache*, int32_t);
 } lib;
 
-/* bind(bfloat16, float32, int32, addresses of the five calls in the order above) */
+/* bind(bfloat16, float32, int32, addresses of the seven calls in the order above) */
 static PyObject* bind(PyObject* self, PyObject* args) {
   (void)self;
   PyObject *a, *b, *c;
-  unsigned long long f[5];
-  if (!PyArg_ParseTuple(args, "OOOKKKKK", &a, &b, &c, &f[0], &f[1], &f[2], &f[3], &f[4])) return NULL;
+  unsigned long long f[7];
+  if (!PyArg_ParseTuple(args, "OOOKKKKKKK", &a, &b, &c, &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6])) return NULL;
   Py_INCREF(a), Py_INCREF(b), Py_INCREF(c);
   Py_XSETREF(t_bf16, a);
   Py_XSETREF(t_f32, b);
@@ -47,6 +49,8 @@ static PyObject* bind(PyObject* self, PyObject* args) {
   *(void**)&lib.kv4_write = (void*)(uintptr_t)f[2];
   *(void**)&lib.kv4_read = (void*)(uintptr_t)f[3];
   *(void**)&lib.kv4_attn = (void*)(uintptr_t)f[4];
+  *(void**)&lib.cache_bytes = (void*)(uintptr_t)f[5];
+  *(void**)&lib.attn_workspace_size = (void*)(uintptr_t)f[6];
   Py_RETURN_NONE;
 }
 
@@ -351,6 +355,40 @@ static PyObject* kv4_attn(PyObject* self, PyObject* const* a, Py_ssize_t n) {
                                       (size_t)ws_bytes, (void*)(uintptr_t)stream));
 }
 
+static int as_i32(PyObject* o, int32_t* out) {
+  int64_t v;
+  if (as_i64(o, &v) < 0) return -1;
+  if (v < INT32_MIN || v > INT32_MAX) {
+    PyErr_SetString(PyExc_OverflowError, "size out of range");
+    return -1;
+  }
+  *out = (int32_t)v;
+  return 0;
+}
+
+/* (n_pages, page_size, Hkv, dqk, dv) */
+static PyObject* cache_bytes(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  int64_t pages;
+  int32_t v[4];
+  if (want(n, 5) < 0 || as_i64(a[0], &pages) < 0) return NULL;
+  for (int i = 0; i < 4; ++i)
+    if (as_i32(a[i + 1], &v[i]) < 0) return NULL;
+  return PyLong_FromSize_t(lib.cache_bytes(pages, v[0], v[1], v[2], v[3]));
+}
+
+/* (B, Hq, cache, q_len) */
+static PyObject* attn_workspace_size(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  int64_t batch, heads;
+  int32_t q_len;
+  const void* cache;
+  if (want(n, 4) < 0 || as_i64(a[0], &batch) < 0 || as_i64(a[1], &heads) < 0 ||
+      structure(a[2], sizeof(slope_kv4_cache), &cache) < 0 || as_i32(a[3], &q_len) < 0)
+    return NULL;
+  return PyLong_FromSize_t(lib.attn_workspace_size(batch, heads, (const slope_kv4_cache*)cache, q_len));
+}
+
 static PyMethodDef methods[] = {
     {"bind", bind, METH_VARARGS, "dtypes and addresses of the library's calls"},
     {"qk_norm_rope", (PyCFunction)(void (*)(void))qk_norm_rope, METH_FASTCALL, NULL},
@@ -358,6 +396,8 @@ static PyMethodDef methods[] = {
     {"kv4_write", (PyCFunction)(void (*)(void))kv4_write, METH_FASTCALL, NULL},
     {"kv4_read", (PyCFunction)(void (*)(void))kv4_read, METH_FASTCALL, NULL},
     {"kv4_attn", (PyCFunction)(void (*)(void))kv4_attn, METH_FASTCALL, NULL},
+    {"cache_bytes", (PyCFunction)(void (*)(void))cache_bytes, METH_FASTCALL, NULL},
+    {"attn_workspace_size", (PyCFunction)(void (*)(void))attn_workspace_size, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", "Argument marshalling of the serving calls.", -1,

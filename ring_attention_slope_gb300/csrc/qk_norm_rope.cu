@@ -412,7 +412,8 @@ extern "C" slope_status slope_qk_norm_rope(const slope_tensor* q, const slope_te
     for (int i = 0; i < p.half; ++i) {
       if (!std::isfinite(rope->inv_freq[i])) return SLOPE_ERR_SHAPE;
       const double t = rope->inv_freq[i] / 6.283185307179586476925286766559;
-      p.turns[i] = static_cast<uint64_t>(std::ldexp(t - std::floor(t), 64) < 0x1p64 ? std::ldexp(t - std::floor(t), 64) : 0.0);
+      const double turns = (t - std::floor(t)) * 0x1p64;
+      p.turns[i] = turns < 0x1p64 ? static_cast<uint64_t>(turns) : 0;
     }
   }
   if (T == 0) return SLOPE_OK;

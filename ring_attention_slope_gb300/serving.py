@@ -55,7 +55,7 @@ def declare(lib):
 
 _pack_rope = struct.Struct("@iiifP").pack  # slope_rope
 _pack_cache = struct.Struct("@Pqiiii").pack  # slope_kv4_cache
-_device = torch.cuda.current_device
+_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _marshal = None  # the C module, once load() has found the library
 
@@ -68,7 +68,8 @@ def _bound():
 
     address = lambda f: ctypes.cast(f, ctypes.c_void_p).value  # noqa: E731
     m.bind(torch.bfloat16, torch.float32, torch.int32, address(lib.slope_qk_norm_rope), address(lib.slope_attn_varlen),
-           address(lib.slope_kv4_write), address(lib.slope_kv4_read), address(lib.slope_kv4_attn))
+           address(lib.slope_kv4_write), address(lib.slope_kv4_read), address(lib.slope_kv4_attn),
+           address(lib.slope_kv4_cache_bytes), address(lib.slope_kv4_attn_workspace_size))
     _marshal = m
     return m
 
@@ -84,16 +85,18 @@ except ImportError:
         return torch.empty_strided(size, stride, dtype=dtype, device="cuda")
 
 
-def _empty(shape, dtype, stream):
-    """A dense tensor on the current device.  What a call allocates belongs to the stream it runs on: a temporary's
-    memory is not handed out again before that stream is done with it."""
-    if len(shape) > 3:
-        raise ValueError("tensors must be rank 2 or 3")
-    stride = (shape[1] * shape[2], shape[2], 1) if len(shape) == 3 else (shape[1], 1) if len(shape) == 2 else (1,)
+def _empty(size, stride, dtype, stream):
+    """A tensor on the current device.  What a call allocates belongs to the stream it runs on: a temporary's memory
+    is not handed out again before that stream is done with it."""
     if stream is None:
-        return _alloc(shape, stride, dtype)
+        return _alloc(size, stride, dtype)
     with torch.cuda.stream(stream):
-        return _alloc(shape, stride, dtype)
+        return _alloc(size, stride, dtype)
+
+
+def _heads(T, H, d, dtype, stream):
+    """A dense [T, H, d]."""
+    return _empty((T, H, d), (H * d, d, 1), dtype, stream)
 
 
 # ---------------------------------------------------------------- positions
@@ -129,9 +132,11 @@ def qk_norm_rope(q, k=None, *, norm=True, q_weight=None, k_weight=None, eps=1e-6
     (of the inputs' type unless given) may be the inputs.  Returns ``(q_out, k_out)`` (k_out None without k).
     """
     if q_out is None:
-        q_out = _empty(tuple(q.shape), out_dtype or q.dtype, stream)
+        T, H, d = q.shape
+        q_out = _heads(T, H, d, out_dtype or q.dtype, stream)
     if k is not None and k_out is None:
-        k_out = _empty(tuple(k.shape), out_dtype or k.dtype, stream)
+        T, H, d = k.shape
+        k_out = _heads(T, H, d, out_dtype or k.dtype, stream)
     dev = _device()
     st = (_marshal or _bound()).qk_norm_rope(q, k, q_weight, k_weight, norm, eps, None if rope is None else rope._c,
                                              positions, pos0, q_out, k_out, _stream(stream, dev), dev)
@@ -151,9 +156,9 @@ def attn_varlen(q, k, v, cu_seqlens, *, causal=True, window=0, scale=0.0, out=No
     """
     T, Hq, _ = q.shape
     if out is None:
-        out = _empty((T, Hq, v.shape[2]), out_dtype or torch.bfloat16, stream)
+        out = _heads(T, Hq, v.shape[2], out_dtype or torch.bfloat16, stream)
     if lse is None:
-        lse = _empty((Hq, T), torch.float32, stream)
+        lse = _empty((Hq, T), (T, 1), torch.float32, stream)
     if isinstance(cu_seqlens, torch.Tensor):
         if cu_seqlens.is_cuda:
             raise TypeError("cu_seqlens lives on the host (reading it back would synchronise)")
@@ -172,7 +177,7 @@ class KV4Cache:
     of dqk key and dv value channels.  ``data`` (uint8, CUDA, dense) is allocated unless given."""
 
     def __init__(self, n_pages, page_size, Hkv, dqk, dv, *, data=None, device="cuda"):
-        nbytes = load().slope_kv4_cache_bytes(n_pages, page_size, Hkv, dqk, dv)
+        nbytes = (_marshal or _bound()).cache_bytes(n_pages, page_size, Hkv, dqk, dv)
         if nbytes == 0 and n_pages != 0:
             raise SlopeError(-8, "slope_kv4_cache_bytes")
         if data is None:
@@ -183,14 +188,14 @@ class KV4Cache:
             raise ValueError(f"the cache needs {nbytes} bytes, data holds {data.numel()}")
         if nbytes > 0 and not data.is_cuda:
             raise TypeError("the cache's data must be a CUDA tensor")
-        self.data = data
+        self.data, self._device = data, data.get_device() if nbytes else None
         self.n_pages, self.page_size, self.Hkv, self.dqk, self.dv = n_pages, page_size, Hkv, dqk, dv
         self._c = _pack_cache(data.data_ptr() if nbytes else 0, n_pages, page_size, Hkv, dqk, dv)
 
     def device_now(self):
         """The current device, which the cache's data has to be on."""
         dev = _device()
-        if self.data.get_device() != dev and self.n_pages > 0:
+        if self._device != dev and self._device is not None:
             raise ValueError(f"cache on {self.data.device}, but the current device is cuda:{dev}")
         return dev
 
@@ -208,9 +213,9 @@ def kv4_read(cache, slots, *, k_out=None, v_out=None, out_dtype=None, stream=Non
     fp32.  Rows whose slot is out of range are left as they were (uninitialised where the call allocates)."""
     T = slots.shape[0]
     if k_out is None:
-        k_out = _empty((T, cache.Hkv, cache.dqk), out_dtype or torch.bfloat16, stream)
+        k_out = _heads(T, cache.Hkv, cache.dqk, out_dtype or torch.bfloat16, stream)
     if v_out is None:
-        v_out = _empty((T, cache.Hkv, cache.dv), out_dtype or torch.bfloat16, stream)
+        v_out = _heads(T, cache.Hkv, cache.dv, out_dtype or torch.bfloat16, stream)
     dev = cache.device_now()
     st = (_marshal or _bound()).kv4_read(cache._c, slots, k_out, v_out, _stream(stream, dev), dev)
     _check(st, "slope_kv4_read")
@@ -219,7 +224,7 @@ def kv4_read(cache, slots, *, k_out=None, v_out=None, out_dtype=None, stream=Non
 
 def kv4_attn_workspace_size(B, Hq, cache, q_len=1) -> int:
     """Workspace bytes of :func:`kv4_attn` (0 for arguments it does not support)."""
-    return load().slope_kv4_attn_workspace_size(B, Hq, cache._c, q_len)
+    return (_marshal or _bound()).attn_workspace_size(B, Hq, cache._c, q_len)
 
 
 def kv4_attn(q, cache, block_table, kv_lens, *, q_len=1, window=0, scale=0.0, out=None, lse=None, workspace=None,
@@ -232,14 +237,14 @@ def kv4_attn(q, cache, block_table, kv_lens, *, q_len=1, window=0, scale=0.0, ou
     """
     T, Hq, _ = q.shape
     if out is None:
-        out = _empty((T, Hq, cache.dv), out_dtype or torch.bfloat16, stream)
+        out = _heads(T, Hq, cache.dv, out_dtype or torch.bfloat16, stream)
     if lse is None and want_lse:
-        lse = _empty((Hq, T), torch.float32, stream)
+        lse = _empty((Hq, T), (T, 1), torch.float32, stream)
     if workspace is None:
-        nbytes = load().slope_kv4_attn_workspace_size(block_table.shape[0], Hq, cache._c, q_len)
+        nbytes = (_marshal or _bound()).attn_workspace_size(block_table.shape[0], Hq, cache._c, q_len)
         if nbytes == 0:
             raise SlopeError(-8, "slope_kv4_attn_workspace_size")
-        workspace = _empty((nbytes,), torch.uint8, stream)
+        workspace = _empty((nbytes,), (1,), torch.uint8, stream)
     dev = cache.device_now()
     if workspace.get_device() != dev:
         raise ValueError(f"workspace on {workspace.device}, but the current device is cuda:{dev}")
