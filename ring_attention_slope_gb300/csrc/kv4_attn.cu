@@ -167,26 +167,103 @@ __device__ __forceinline__ SeqSteps seq_steps(const Kv4AttnParams& p, int b) {
   return s;
 }
 
-// A CTA's range of units and the sequence it starts in.  A pair is a (sequence, KV head, row tile); its
+// A CTA's range of units and the pair it starts in.  A pair is a (sequence, KV head, row tile); its
 // units are its steps, after `cost` for starting and finishing it, or (cost < 0) its steps rounded up to
 // whole ranges.
 struct CtaRange {
   int64_t begin, end, per;
-  int64_t seq_begin;  // first unit of sequence b
-  int b;
+  int64_t pair_begin;  // first unit of the pair
+  int b, pair;         // the one that holds unit `begin`
   int cost;
 };
 // Lengths of ranges that are tried for one piece to a CTA: 4, 8, 16 and 32 steps.
 constexpr int kTries = 4;
 __device__ constexpr int try_steps(int i) { return kMinSteps << i; }
 struct CutScratch {
-  int64_t sums[kWarps], seq_begin;
-  int ranges[kWarps][kTries], b;
+  int64_t sums[kWarps], pair_begin;
+  int ranges[kWarps][kTries], b, pair;
 };
 __device__ __forceinline__ int pair_units(int steps, int cost, int64_t per) {
   if (cost >= 0) return steps + cost;
   const unsigned n = static_cast<unsigned>(per);
   return static_cast<int>((steps + n - 1) / n * n);
+}
+
+// The second half of cta_range: U holds every unit (64-bit divisions and scans cost a small call 0.8 us).
+template <int kStep, typename U>
+__device__ __forceinline__ CtaRange cut(const Kv4AttnParams& p, CutScratch& scratch, U steps, int count0) {
+  constexpr U kPiece = kPieceTokens / kStep;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int pairs = p.Hkv * p.row_tiles;
+  const U grid = gridDim.x;
+  bool fits[kTries];
+#pragma unroll
+  for (int i = 0; i < kTries; ++i) {
+    int64_t n = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) n += scratch.ranges[w][i];
+    fits[i] = n * pairs <= gridDim.x;
+  }
+  U per = 0, total;
+  int cost = -1;
+#pragma unroll
+  for (int i = kTries - 1; i >= 0; --i)
+    if (fits[i] && try_steps(i) <= kPiece) per = try_steps(i);
+  if (per == 0) {
+    const U even = (steps + grid - 1) / grid, c = min(kPiece, even / 2);
+    total = steps + static_cast<U>(p.B) * pairs * c;
+    const U evenly = max(static_cast<U>(kMinSteps), (total + grid - 1) / grid);
+#pragma unroll
+    for (int i = kTries - 1; i >= 0; --i)
+      if (fits[i] && try_steps(i) <= evenly) per = try_steps(i);
+    if (per == 0) {
+      per = evenly;
+      cost = static_cast<int>(c);
+    }
+  }
+  if (cost < 0) total = grid * per;  // or less: the search below finds no sequence then
+  const U begin = min(total, static_cast<U>(blockIdx.x) * per), end = min(total, begin + per);
+  CtaRange r;
+  r.per = per;
+  r.cost = cost;
+  r.begin = r.end = begin;
+  r.pair_begin = 0;
+  r.b = r.pair = 0;
+  if (begin >= end) return r;
+  // the sequence that holds unit `begin`
+  U carry = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+    const int b = b0 + threadIdx.x;
+    const int count = b >= p.B ? 0 : b0 == 0 ? count0 : seq_steps<kStep>(p, b).count;
+    const U mine = b < p.B ? static_cast<U>(pair_units(count, cost, per)) * pairs : 0;
+    U incl = mine;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const U o = __shfl_up_sync(0xffffffffu, incl, m);
+      if (lane >= m) incl += o;
+    }
+    __syncthreads();
+    if (lane == 31) scratch.sums[warp] = incl;
+    __syncthreads();
+    U before = carry;
+    for (int w = 0; w < warp; ++w) before += static_cast<U>(scratch.sums[w]);
+    for (int w = 0; w < kWarps; ++w) carry += static_cast<U>(scratch.sums[w]);
+    incl += before;
+    if (mine > 0 && incl - mine <= begin && begin < incl) {
+      const U units = mine / pairs, pair = (begin - (incl - mine)) / units;
+      scratch.b = b;
+      scratch.pair = static_cast<int>(pair);
+      scratch.pair_begin = incl - mine + pair * units;
+    }
+    if (carry > begin) break;  // the same for every thread
+  }
+  if (carry <= begin) return r;  // past the last pair
+  __syncthreads();
+  r.end = end;
+  r.b = scratch.b;
+  r.pair = scratch.pair;
+  r.pair_begin = scratch.pair_begin;
+  return r;
 }
 
 // Every thread of the CTA calls it.
@@ -206,12 +283,12 @@ __device__ CtaRange cta_range(const Kv4AttnParams& p, CutScratch& scratch) {
   const int pairs = p.Hkv * p.row_tiles;
   int64_t steps = 0;
   int ranges[kTries];  // of try_steps(i) steps, kept from overflowing
+  int count0 = 0;      // steps of sequence threadIdx.x
 #pragma unroll
   for (int i = 0; i < kTries; ++i) ranges[i] = 0;
-  for (int b0 = 0; b0 < p.B; b0 += kThreads) {
-    const int b = b0 + threadIdx.x;
-    if (b >= p.B) continue;
+  for (int b = threadIdx.x; b < p.B; b += kThreads) {
     const int count = seq_steps<kStep>(p, b).count;
+    if (b < kThreads) count0 = count;
     steps += count;
 #pragma unroll
     for (int i = 0; i < kTries; ++i) ranges[i] = min(ranges[i] + (count + try_steps(i) - 1) / try_steps(i), 1 << 16);
@@ -230,60 +307,9 @@ __device__ CtaRange cta_range(const Kv4AttnParams& p, CutScratch& scratch) {
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) steps += scratch.sums[w];
   steps *= pairs;
-  CtaRange r;
-  const int64_t even = (steps + gridDim.x - 1) / gridDim.x;
-  r.cost = static_cast<int>(min(static_cast<int64_t>(kPieceTokens / kStep), even / 2));
-  int64_t total = steps + static_cast<int64_t>(p.B) * pairs * r.cost;
-  r.per = max(static_cast<int64_t>(kMinSteps), (total + gridDim.x - 1) / gridDim.x);
-  const int64_t longest = max(r.per, static_cast<int64_t>(kPieceTokens / kStep));
-#pragma unroll
-  for (int i = kTries - 1; i >= 0; --i) {
-    int64_t n = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) n += scratch.ranges[w][i];
-    if (n * pairs <= gridDim.x && try_steps(i) <= longest) {
-      r.cost = -1;
-      r.per = try_steps(i);
-      total = static_cast<int64_t>(gridDim.x) * r.per;  // or less: the search below finds no sequence then
-    }
-  }
-  r.begin = min(total, static_cast<int64_t>(blockIdx.x) * r.per);
-  r.end = min(total, r.begin + r.per);
-  r.b = 0;
-  r.seq_begin = 0;
-  if (r.begin >= r.end) return r;
-  // the sequence that holds unit `begin`
-  int64_t carry = 0;
-  for (int b0 = 0; b0 < p.B; b0 += kThreads) {
-    const int b = b0 + threadIdx.x;
-    const int64_t mine = b < p.B ? static_cast<int64_t>(pair_units(seq_steps<kStep>(p, b).count, r.cost, r.per)) * pairs : 0;
-    int64_t incl = mine;
-#pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-      const int64_t o = __shfl_up_sync(0xffffffffu, incl, m);
-      if (lane >= m) incl += o;
-    }
-    __syncthreads();
-    if (lane == 31) scratch.sums[warp] = incl;
-    __syncthreads();
-    int64_t before = carry;
-    for (int w = 0; w < warp; ++w) before += scratch.sums[w];
-    for (int w = 0; w < kWarps; ++w) carry += scratch.sums[w];
-    incl += before;
-    if (mine > 0 && incl - mine <= r.begin && r.begin < incl) {
-      scratch.b = b;
-      scratch.seq_begin = incl - mine;
-    }
-    if (carry > r.begin) break;  // the same for every thread
-  }
-  if (carry <= r.begin) {  // past the last pair
-    r.end = r.begin;
-    return r;
-  }
-  __syncthreads();
-  r.b = scratch.b;
-  r.seq_begin = scratch.seq_begin;
-  return r;
+  if (steps + static_cast<int64_t>(p.B) * pairs * (kPieceTokens / kStep) < (1u << 31))
+    return cut<kStep, uint32_t>(p, scratch, static_cast<uint32_t>(steps), count0);
+  return cut<kStep, uint64_t>(p, scratch, static_cast<uint64_t>(steps), count0);
 }
 
 template <int DV, int R>
@@ -334,15 +360,14 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
   // the warp's ring: the stages that the next copy fills and the next step reads, and that one's parity
   int put = 0, get = 0;
   uint32_t parity = 0;
-  int b = range.b;
-  int64_t seq_begin = range.seq_begin;
+  int b = range.b, pair = range.pair;
+  int64_t pair_begin = range.pair_begin;
   bool ok = true;
   for (int64_t u = range.begin; u < range.end;) {
     // ---- the piece: steps [st0, st1) of one pair
     const SeqSteps sb = seq_steps<kStep>(p, b);
-    const int units = pair_units(sb.count, range.cost, range.per), cost = max(0, range.cost);
-    const int pair = static_cast<int>((u - seq_begin) / units);
-    const int64_t pair_begin = seq_begin + static_cast<int64_t>(pair) * units, pair_end = pair_begin + units;
+    const int cost = max(0, range.cost);
+    const int64_t pair_end = pair_begin + pair_units(sb.count, range.cost, range.per);
     const int64_t u_end = min(range.end, pair_end);
     const int st0 = sb.first + max(0, static_cast<int>(u - pair_begin) - cost);
     const int st1 = sb.first + min(sb.count, max(0, static_cast<int>(u_end - pair_begin) - cost));
@@ -773,8 +798,9 @@ __global__ void __launch_bounds__(kThreads, Kv4Cfg<DQK, DV, NT>::kCtas)
           make_int4(whole ? -1 : b, pair, blockIdx.x, static_cast<int>((pair_end - 1) / range.per));
     __syncthreads();
     u = u_end;
-    if (u_end == pair_end && pair == p.Hkv * p.row_tiles - 1) {
-      seq_begin = pair_end;
+    pair_begin = pair_end;  // (where the range ends inside the pair, none of this is used)
+    if (++pair == p.Hkv * p.row_tiles) {
+      pair = 0;
       ++b;
     }
   }
