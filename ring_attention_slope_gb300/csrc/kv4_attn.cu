@@ -28,7 +28,7 @@
 // are its own 16-byte words; P^T needs one 8x8 transpose (movmatrix) a group.
 //
 // Measured at 64/8 heads of 64: 8 sequences of 102400 tokens 102 us = 5.1 TB/s of cache (75% of the copy rate); 32
-// ragged ones up to 32768 29.4 us; one of 65536 17.5 us; one of 1000 7.5 us.  (Around the groups' minimums
+// ragged ones up to 32768 29.2 us; one of 65536 17 us; one of 1000 7.2 us.  (Around the groups' minimums
 // instead of their middles 3 to 4% less, with 2.4 times the error.)  At the first the ALU pipe is over half busy,
 // the issue slots over 60%, DRAM two thirds: a warp's step of 64 tokens is about as long in instructions as its codes
 // are on the way.  (The copies alone, without the arithmetic, took 84 us.)  The short ones are latency: the
