@@ -6,12 +6,13 @@
 // bytes of bf16) of a head, one and the one half a rotation away, so the pairs that the rotation mixes need no
 // other lane and no second load, whatever part of the head is rotated; words that are not rotated are paired
 // as they come.  A head of 64 channels takes 4 lanes, of 128 8, of 192 12 of 16.  A warp takes one token
-// and runs over its heads, two or three groups of them at a time with the next ones' loads in flight: the weights
+// and runs over its heads, two or three groups of them at a time with the next ones' loads in flight (then, where
+// that pays, over further tokens): the weights
 // and the token's sines and cosines are then the same for every head of a lane, and stay in its registers as
 //   y_e = (x_e A_e + x_partner B_e) / rms,   A = w cos, B = -+ w_partner sin.
 //
-// Measured, bf16: 32768 tokens, 64/8 heads of 64, all rotated, 107 us = 5.6 TB/s (83% of the copy rate); 8191 tokens,
-// 128/128 heads of 192, 274 us = 5.9 TB/s; 16384 tokens, 32/8 heads of 128, 62 us.  With eight lanes to a head of
+// Measured, bf16: 32768 tokens, 64/8 heads of 64, all rotated, 102 us = 5.9 TB/s (87% of the copy rate); 8191 tokens,
+// 128/128 heads of 192, 274 us = 5.9 TB/s; 16384 tokens, 32/8 heads of 128, 58 us.  With eight lanes to a head of
 // any size, the other half fetched again or by shuffles, these took 118, 295 to 364 and 83 us; one group at
 // a time at the same registers 131 us; six CTAs an SM instead of four spill.  16 tokens: 2.7 us, which is the launch.
 //
@@ -105,8 +106,9 @@ __device__ __forceinline__ uint64_t weight_pair(const NormRopeSide& s, int64_t i
   return pack_f32x2(weight_at(s, i), weight_at(s, i + 1));
 }
 
-// kInter: the channels of a pair are neighbours, else half a rotation apart.
-template <typename TI, typename TO, int D, bool kInter>
+// kInter: the channels of a pair are neighbours, else half a rotation apart.  kLoop: the warps go on to further
+// tokens, whose first heads are fetched during the last pass of the one before.
+template <typename TI, typename TO, int D, bool kInter, bool kLoop>
 __global__ void __launch_bounds__(kThreads, sizeof(TI) == 2 ? 4 : 3) qk_norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
   __shared__ __align__(16) float s_cos[kWarps][kMaxHalf], s_sin[kWarps][kMaxHalf];  // of the warp's token
   __shared__ __align__(16) float s_w[2][D];  // weights shared by every head of a side, else 1
@@ -115,20 +117,23 @@ __global__ void __launch_bounds__(kThreads, sizeof(TI) == 2 ? 4 : 3) qk_norm_rop
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int li = min(lane % kLanes, kUsed - 1), sub = lane / kLanes;
   const bool used = lane % kLanes < kUsed;
-  const int64_t task = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
-  const int64_t tok = task / p.splits;
-  const bool here = tok < p.T;
-  const int split = static_cast<int>(task - tok * p.splits);
-  const int first = split * p.heads, last = here ? min(first + p.heads, p.side[0].H + p.side[1].H) : first;
-  // the warp's heads of either side, and the passes they take
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kWarps, tasks = p.T * p.splits;
+  int64_t task = static_cast<int64_t>(blockIdx.x) * kWarps + warp;  // a token's heads, or a part of them
+  int64_t tok = 0;
+  // the task's heads of either side, and the passes they take
   int h_begin[2], h_end[2], n_pass[2];
+  auto take = [&]() {
+    tok = p.splits == 1 ? task : task / p.splits;
+    const int first = static_cast<int>(task - tok * p.splits) * p.heads;
+    const int last = tok < p.T ? min(first + p.heads, p.side[0].H + p.side[1].H) : first;
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const int base = w ? p.side[0].H : 0;
-    h_begin[w] = max(first - base, 0);
-    h_end[w] = min(last - base, p.side[w].H);
-    n_pass[w] = h_begin[w] < h_end[w] ? (h_end[w] - h_begin[w] + kHeads * kWide - 1) / (kHeads * kWide) : 0;
-  }
+    for (int w = 0; w < 2; ++w) {
+      const int base = w ? p.side[0].H : 0;
+      h_begin[w] = max(first - base, 0);
+      h_end[w] = min(last - base, p.side[w].H);
+      n_pass[w] = h_begin[w] < h_end[w] ? (h_end[w] - h_begin[w] + kHeads * kWide - 1) / (kHeads * kWide) : 0;
+    }
+  };
   // The lane's two words: a word and the one half a rotation away, the first lanes of a head; then the words that
   // are not rotated.  Interleaved: neighbours.
   int ch[2];
@@ -160,24 +165,30 @@ __global__ void __launch_bounds__(kThreads, sizeof(TI) == 2 ? 4 : 3) qk_norm_rop
       for (int i = 0; i < 2; ++i) fv[k][i].load(x + h * s.x_shead + ch[i]);
     }
   };
-  const int passes = n_pass[0] + n_pass[1];
-  if (passes > 0) fetch(0, v);
+  auto position = [&](int64_t t) -> int64_t {
+    return !p.rotate || t >= p.T ? 0 : p.positions != nullptr ? p.positions[t] : p.pos0 + t;
+  };
+  take();
+  int64_t pos = kLoop ? position(tok) : 0;
+  if (n_pass[0] + n_pass[1] > 0) fetch(0, v);
 
   for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
     const NormRopeSide& s = p.side[i / D];
     s_w[i / D][i % D] = s.w != nullptr && s.w_shead == 0 ? weight_at(s, i % D) : 1.f;
   }
-  if (here && p.rotate) {
-    const int64_t pos = p.positions != nullptr ? p.positions[tok] : p.pos0 + tok;
+  auto turn = [&]() {  // the token's sines and cosines
+    if (!p.rotate) return;
+    const int64_t at = kLoop ? pos : position(tok);
     for (int f = lane; f < p.half; f += 32) {
       // the fraction of a turn, rounded to 32 bits and taken in [-1/2, 1/2)
-      const uint64_t frac = p.turns[f] * static_cast<uint64_t>(pos) + 0x80000000ull;
+      const uint64_t frac = p.turns[f] * static_cast<uint64_t>(at) + 0x80000000ull;
       float sn, cs;
       sincospif(static_cast<float>(static_cast<int32_t>(frac >> 32)) * 0x1p-31f, &sn, &cs);
       s_cos[warp][f] = cs * p.factor;
       s_sin[warp][f] = sn * p.factor;
     }
-  }
+  };
+  if (!kLoop) turn();
   __syncthreads();
 
   // y_e = (x_e fa_e + x_partner fb_e) / rms
@@ -231,85 +242,123 @@ __global__ void __launch_bounds__(kThreads, sizeof(TI) == 2 ? 4 : 3) qk_norm_rop
       }
   };
 
-#pragma unroll 1
-  for (int pass = 0; pass < passes; ++pass) {
-    const int which = pass >= n_pass[0] ? 1 : 0;
-    const NormRopeSide& s = p.side[which];
-    const int h0 = which ? h_begin[1] + (pass - n_pass[0]) * (kHeads * kWide) : h_begin[0] + pass * (kHeads * kWide);
-    const int end = which ? h_end[1] : h_end[0];
-    const bool per_head = s.w_shead != 0;
-    if (pass == 0 || pass == n_pass[0]) set_factors(which);
-    // the next pass's loads are in flight during this one (its heads are others, so in place they are unwritten)
-    Raw8<TI> nv[kWide][2];
-#pragma unroll
-    for (int k = 0; k < kWide; ++k)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) nv[k][i] = v[k][i];
-    if (pass + 1 < passes) fetch(pass + 1, nv);
-    TO* const y = static_cast<TO*>(s.y) + tok * s.y_srow;
-#pragma unroll
-    for (int k = 0; k < kWide; ++k) {
-      uint64_t x[2][4];
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[i][e] = v[k][i].pair(e);
-      float scale = 1.f;
-      if (p.norm) {
-        uint64_t sq2 = 0;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sq2 = fma_f32x2(x[i][e], x[i][e], sq2);
-        const float2 sq = unpack_f32x2(sq2);
-        float sum = used ? sq.x + sq.y : 0.f;
-#pragma unroll
-        for (int m = 1; m < kLanes; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-        scale = rsqrtf(fmaf(sum, 1.f / D, p.eps));
-      }
-      const int h = h0 + k * kHeads + sub;
-      if (h >= end || !used) continue;
-      if (per_head) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[i][e] = mul_f32x2(x[i][e], weight_pair(s, h * s.w_shead + ch[i] + 2 * e));
-      }
-      const uint64_t scale2 = pack_f32x2(scale, scale);
-      TO* const yh = y + h * s.y_shead;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint64_t out[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) out[e] = mul_f32x2(x[i][e], fa[i][e]);
-        if (rot[i]) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) out[e] = fma_f32x2(kInter ? swapped(x[i][e]) : x[1 - i][e], fb[i][e], out[e]);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) out[e] = mul_f32x2(out[e], scale2);
-        store8(yh + ch[i], out);
-      }
+  for (;;) {
+    if constexpr (kLoop) {
+      __syncwarp();  // the last token's sines and cosines are read
+      turn();
+      __syncwarp();
     }
+    const int passes = n_pass[0] + n_pass[1];
+#pragma unroll 1
+    for (int pass = 0; pass < passes; ++pass) {
+      const int which = pass >= n_pass[0] ? 1 : 0;
+      const NormRopeSide& s = p.side[which];
+      const int h0 = which ? h_begin[1] + (pass - n_pass[0]) * (kHeads * kWide) : h_begin[0] + pass * (kHeads * kWide);
+      const int end = which ? h_end[1] : h_end[0];
+      const bool per_head = s.w_shead != 0;
+      if (pass == 0 || pass == n_pass[0]) set_factors(which);
+      // the next pass's loads are in flight during this one (its heads are others, so in place they are unwritten)
+      Raw8<TI> nv[kWide][2];
 #pragma unroll
-    for (int k = 0; k < kWide; ++k)
+      for (int k = 0; k < kWide; ++k)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) v[k][i] = nv[k][i];
+        for (int i = 0; i < 2; ++i) nv[k][i] = v[k][i];
+      const int64_t row = tok;
+      if (pass + 1 < passes) {
+        fetch(pass + 1, nv);
+      } else if (kLoop && task + stride < tasks) {  // the next task's first
+        task += stride;
+        take();
+        task -= stride;
+        pos = position(tok);
+        fetch(0, nv);
+      }
+      TO* const y = static_cast<TO*>(s.y) + row * s.y_srow;
+#pragma unroll
+      for (int k = 0; k < kWide; ++k) {
+        uint64_t x[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[i][e] = v[k][i].pair(e);
+        float scale = 1.f;
+        if (p.norm) {
+          uint64_t sq2 = 0;
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sq2 = fma_f32x2(x[i][e], x[i][e], sq2);
+          const float2 sq = unpack_f32x2(sq2);
+          float sum = used ? sq.x + sq.y : 0.f;
+#pragma unroll
+          for (int m = 1; m < kLanes; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+          scale = rsqrtf(fmaf(sum, 1.f / D, p.eps));
+        }
+        const int h = h0 + k * kHeads + sub;
+        if (h >= end || !used) continue;
+        if (per_head) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[i][e] = mul_f32x2(x[i][e], weight_pair(s, h * s.w_shead + ch[i] + 2 * e));
+        }
+        const uint64_t scale2 = pack_f32x2(scale, scale);
+        TO* const yh = y + h * s.y_shead;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint64_t out[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) out[e] = mul_f32x2(x[i][e], fa[i][e]);
+          if (rot[i]) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) out[e] = fma_f32x2(kInter ? swapped(x[i][e]) : x[1 - i][e], fb[i][e], out[e]);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) out[e] = mul_f32x2(out[e], scale2);
+          store8(yh + ch[i], out);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kWide; ++k)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) v[k][i] = nv[k][i];
+    }
+    if (!kLoop || (task += stride) >= tasks) break;
   }
 }
 
-template <typename TI, typename TO>
-cudaError_t launch_d(const NormRopeParams& p, int d, dim3 grid, cudaStream_t stream) {
-  if (d == 64)
-    p.interleaved ? qk_norm_rope_kernel<TI, TO, 64, true><<<grid, kThreads, 0, stream>>>(p)
-                  : qk_norm_rope_kernel<TI, TO, 64, false><<<grid, kThreads, 0, stream>>>(p);
-  else if (d == 128)
-    p.interleaved ? qk_norm_rope_kernel<TI, TO, 128, true><<<grid, kThreads, 0, stream>>>(p)
-                  : qk_norm_rope_kernel<TI, TO, 128, false><<<grid, kThreads, 0, stream>>>(p);
+// CTAs that fit on the GPU (four on each of 152 SMs).
+constexpr int64_t kResident = 608;
+
+template <typename TI, typename TO, int D, bool kLoop>
+void launch_one(const NormRopeParams& p, int64_t ctas, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(kLoop ? kResident : ctas));
+  if (p.interleaved)
+    qk_norm_rope_kernel<TI, TO, D, true, kLoop><<<grid, kThreads, 0, stream>>>(p);
   else
-    p.interleaved ? qk_norm_rope_kernel<TI, TO, 192, true><<<grid, kThreads, 0, stream>>>(p)
-                  : qk_norm_rope_kernel<TI, TO, 192, false><<<grid, kThreads, 0, stream>>>(p);
+    qk_norm_rope_kernel<TI, TO, D, false, kLoop><<<grid, kThreads, 0, stream>>>(p);
+}
+
+// bf16 heads of 64 and 128 channels loop where there are more tokens than the GPU holds warps: 32768 tokens of 64/8
+// heads of 64 take 102 us so and 107 with a CTA for every four tokens, 16000 of 8/1 19 and 20.  Heads of 192 have
+// no registers for it (291 and 274 us for 8191 tokens of 128/128), fp32 gains nothing, small calls lose 0.3 us.
+template <typename TI, typename TO, int D>
+cudaError_t launch_d(const NormRopeParams& p, int64_t ctas, cudaStream_t stream) {
+  if constexpr (sizeof(TI) == 2 && D != 192) {
+    if (ctas > kResident) {
+      launch_one<TI, TO, D, true>(p, ctas, stream);
+      return cudaGetLastError();
+    }
+  }
+  launch_one<TI, TO, D, false>(p, ctas, stream);
   return cudaGetLastError();
+}
+
+template <typename TI, typename TO>
+cudaError_t launch(const NormRopeParams& p, int d, int64_t ctas, cudaStream_t stream) {
+  if (d == 64) return launch_d<TI, TO, 64>(p, ctas, stream);
+  if (d == 128) return launch_d<TI, TO, 128>(p, ctas, stream);
+  return launch_d<TI, TO, 192>(p, ctas, stream);
 }
 
 bool strides8(const slope_tensor* t) {
@@ -432,14 +481,13 @@ extern "C" slope_status slope_qk_norm_rope(const slope_tensor* q, const slope_te
   p.splits = static_cast<int32_t>((H + p.heads - 1) / p.heads);
   const int64_t ctas = (T * p.splits + kWarps - 1) / kWarps;
   if (ctas > 0x7fffffffLL) return SLOPE_ERR_SHAPE;
-  const dim3 grid(static_cast<unsigned>(ctas));
   auto s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (first->dtype == SLOPE_BF16)
-    e = first_out->dtype == SLOPE_BF16 ? launch_d<__nv_bfloat16, __nv_bfloat16>(p, d, grid, s)
-                                       : launch_d<__nv_bfloat16, float>(p, d, grid, s);
+    e = first_out->dtype == SLOPE_BF16 ? launch<__nv_bfloat16, __nv_bfloat16>(p, d, ctas, s)
+                                       : launch<__nv_bfloat16, float>(p, d, ctas, s);
   else
-    e = first_out->dtype == SLOPE_BF16 ? launch_d<float, __nv_bfloat16>(p, d, grid, s)
-                                       : launch_d<float, float>(p, d, grid, s);
+    e = first_out->dtype == SLOPE_BF16 ? launch<float, __nv_bfloat16>(p, d, ctas, s)
+                                       : launch<float, float>(p, d, ctas, s);
   return e == cudaSuccess ? SLOPE_OK : cuda_fail("norm and rotation kernel launch", e);
 }

@@ -62,7 +62,7 @@ def check_rope(got, x, w, eps, pos, freq, begin, inter, factor, norm=True):
     (1, 1, 1, 64, 0, 64, False), (3, 8, 1, 64, 0, 64, True), (5, 3, 3, 64, 16, 16, False), (33, 40, 8, 64, 8, 48, False),
     (7, 5, 1, 128, 0, 128, False), (6, 4, 2, 128, 40, 32, True), (9, 7, 7, 192, 128, 64, True),
     (4, 2, 1, 192, 0, 192, False), (2, 3, 1, 192, 24, 112, False), (300, 12, 4, 64, 0, 32, False),
-    (1300, 64, 8, 64, 0, 64, False)])
+    (1300, 64, 8, 64, 0, 64, False), (5000, 7, 2, 64, 8, 32, False), (4000, 6, 2, 128, 0, 128, True)])
 def test_norm_rope(T, Hq, Hkv, d, begin, dim, inter):
     q, k = rand(T, Hq, d, seed=1, scale=3), rand(T, Hkv, d, seed=2, scale=0.02)
     qw, kw = rand(d, seed=3, dtype=torch.float32), rand(Hkv, d, seed=4)
@@ -113,7 +113,7 @@ def test_norm_or_rope_alone(norm, rotate):
 
 def test_norm_rope_in_place_and_strided():
     """Views into one projection's output [T, (Hq + 2 Hkv) d + 8], rotated in place: the rest of it stays."""
-    T, Hq, Hkv, d = 70, 6, 2, 64
+    T, Hq, Hkv, d = 5070, 6, 2, 64  # enough that warps go on to further tokens
     buf = rand(T, (Hq + 2 * Hkv) * d + 8, seed=11)
     dev = buf.cuda()
     view = lambda b, h0, n: b[:, h0 * d:(h0 + n) * d].unflatten(1, (n, d))  # noqa: E731
