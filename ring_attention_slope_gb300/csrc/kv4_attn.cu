@@ -34,14 +34,13 @@
 // are on the way.  (The copies alone, without the arithmetic, took 84 us.)  The short ones are latency: the
 // lengths, the page table, one copy, the steps, the join of the warps and that of the CTAs, one after another.
 //
-// Work split: every sequence's visible steps of 64 or 32 tokens, for each KV head (and each
-// tile of 8 NT query rows), laid end to end and cut into equal ranges, one for each
-// CTA of a grid that fills the GPU once.  The cut knows the lengths only on the
-// device, so ragged batches and captured graphs balance alike.  A range's pieces that
-// are not whole (sequence, head) pairs leave partials (m, l, unnormalised out) in the
-// workspace, and a second launch, queued as a programmatic dependent, joins them in a
-// fixed order.  Inside a CTA four warps take every fourth step, each with its
-// own ring of bulk copies, and join once at the end of a piece.
+// Work split: every sequence's visible steps of 64 or 32 tokens, for each KV head (and each tile of 8 NT query
+// rows), laid end to end and cut into ranges for the CTAs of a grid that fills the GPU once: equal ones, or, where
+// the CTAs suffice for that, ranges that end with their pairs, one piece to a CTA (see cta_range).  The cut knows the
+// lengths only on the device, so ragged batches and captured graphs balance alike.  Pieces that are not whole
+// (sequence, head) pairs leave partials (m, l, unnormalised out) in the workspace, and a second launch, queued as
+// a programmatic dependent, joins them in a fixed order.  Inside a CTA four warps take every fourth step, each with
+// its own ring of bulk copies, and join once at the end of a piece.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -6,9 +6,9 @@
 // bytes of bf16) of a head, one and the one half a rotation away, so the pairs that the rotation mixes need no
 // other lane and no second load, whatever part of the head is rotated; words that are not rotated are paired
 // as they come.  A head of 64 channels takes 4 lanes, of 128 8, of 192 12 of 16.  A warp takes one token
-// and runs over its heads, two or three groups of them at a time with the next ones' loads in flight (then, where
-// that pays, over further tokens): the weights
-// and the token's sines and cosines are then the same for every head of a lane, and stay in its registers as
+// and runs over its heads, two or three groups of them at a time with the next ones' loads in flight, and then,
+// where that pays, over further tokens.  The weights and the token's sines and cosines are the same for every head
+// of a lane, and stay in its registers as
 //   y_e = (x_e A_e + x_partner B_e) / rms,   A = w cos, B = -+ w_partner sin.
 //
 // Measured, bf16: 32768 tokens, 64/8 heads of 64, all rotated, 102 us = 5.9 TB/s (87% of the copy rate); 8191 tokens,
