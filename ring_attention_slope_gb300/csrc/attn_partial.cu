@@ -49,7 +49,7 @@
 // would be mostly empty for short prompts and its diagonal half empty for all; 16 tokens of 8 heads fill
 // it: 40 prompts of 50 tokens, 64/8 heads of 64, take 24 us, 5 prompts of 670 to 5200 384 us (7% more with one
 // head to a tile), one of 12288 1.08 ms = 1140 TFLOP/s (as unpacked).  TMA boxes of 2^s heads load Q and store the
-// output; rows past a sequence's end are stored directly.  Bound as the unpacked kernel is, by the
+// output; a box that holds rows past a sequence's end is stored row by row.  Bound as the unpacked kernel is, by the
 // exponentials and the steps' latency (tensor pipe 41% busy, MUFU 42%), and below 128 tokens by the work
 // tile's start and end, about 4 us each.  (For tiles whose second half no row sees, a softmax of half a tile made
 // prompts of 16 and 50 tokens 20% faster but every longer step 5% slower, so it is not built.)
