@@ -84,7 +84,8 @@ slope_status check_lse(const slope_tensor* t, int64_t H, int64_t S) {
   if (t == nullptr) return SLOPE_ERR_NULL;
   if (t->dtype != SLOPE_F32) return SLOPE_ERR_DTYPE;
   if (t->ndim != 2 || t->shape[0] != H || t->shape[1] != S) return SLOPE_ERR_SHAPE;
-  if (S > 0 && t->data == nullptr) return SLOPE_ERR_NULL;
+  if (S == 0) return SLOPE_OK;  // no address is made; a dense [H, 0] has a stride of 0
+  if (t->data == nullptr) return SLOPE_ERR_NULL;
   if (t->stride[0] <= 0 || t->stride[1] <= 0) return SLOPE_ERR_STRIDE;
   if (!aligned(t->data, 4)) return SLOPE_ERR_STRIDE;
   return SLOPE_OK;

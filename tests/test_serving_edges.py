@@ -1,0 +1,70 @@
+"""Edges of the serving calls' host side, without a GPU: CPU tensors without elements and plain objects stand in for CUDA
+tensors, and nothing is launched."""
+import ctypes
+
+import pytest
+import torch
+
+import ring_attention_slope_gb300 as slope
+from _lib import built_lib
+from test_serving_abi import BF16, F32, S_OK, cache, ref, t
+from test_serving_marshal import Fake
+
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return built_lib()
+
+
+@pytest.fixture
+def on_cpu(lib, monkeypatch):
+    """The public calls with the host's memory in the place of the device's."""
+    monkeypatch.setattr(slope.serving, "_device", lambda: 0)
+    monkeypatch.setattr(slope.serving, "_raw_stream", lambda dev: 0)
+    monkeypatch.setattr(slope.serving, "_alloc", lambda size, stride, dtype: torch.empty_strided(size, stride, dtype=dtype))
+
+
+# ---------------------------------------------------------------- no tokens
+
+@pytest.mark.parametrize("stride", [[0, 1], [1, 1], [7, 1]])
+def test_lse_strides_without_rows(lib, stride):
+    """A dense [H, S] has strides (S, 1): without rows the first is 0, and no address is made with it."""
+    lse = t([8, 0], F32, data=0, stride=stride)
+    q, k = t([0, 8, 64], data=0), t([0, 2, 64], data=0)
+    cu = (ctypes.c_int64 * 2)(0, 0)
+    assert lib.slope_attn_varlen(ref(q), ref(k), ref(k), cu, 1, 1, 0, 0.0, ref(q), ref(lse), None) == S_OK
+    assert lib.slope_kv4_attn(ref(q), ref(cache()), 0x6000, 5, 5, 0x7000, 1, 0, 0.0, ref(q), ref(lse), None, 0, None) == S_OK
+
+
+def test_lse_strides_with_rows_are_still_checked(lib):
+    q, k = t([3, 8, 64]), t([3, 2, 64])
+    cu = (ctypes.c_int64 * 2)(0, 0)
+    for stride in ([0, 1], [3, 0], [-3, 1]):
+        lse = t([8, 3], F32, stride=stride)
+        assert lib.slope_attn_varlen(ref(q), ref(k), ref(k), cu, 1, 1, 0, 0.0, ref(q), ref(lse), None) == -4
+    assert BF16 == 0
+
+
+def test_calls_without_tokens_make_their_outputs(on_cpu):
+    """Every output left to the call: a batch without sequences is a no-op, not an error."""
+    q, k = torch.empty(0, 8, 64, dtype=BF), torch.empty(0, 2, 64, dtype=BF)
+    for cu in ([0], [0, 0], [0, 0, 0]):
+        out, lse = slope.attn_varlen(q, k, k, cu)
+        assert out.shape == (0, 8, 64) and lse.shape == (8, 0)
+    held = slope.KV4Cache(0, 16, 2, 64, 64, device="cpu")
+    none = torch.empty(0, dtype=torch.int32)
+    for pages in (0, 5):
+        out, lse = slope.kv4_attn(q, held, torch.empty(0, pages, dtype=torch.int32), none, q_len=3,
+                                  workspace=workspace())
+        assert out.shape == (0, 8, 64) and lse.shape == (8, 0)
+    slope.kv4_write(held, k, k, none)
+    assert [x.shape for x in slope.kv4_read(held, none)] == [(0, 2, 64)] * 2
+    assert [x.shape for x in slope.qk_norm_rope(q, k)] == [(0, 8, 64), (0, 2, 64)]
+
+
+def workspace():
+    ws = Fake([1 << 24], torch.uint8, ptr=0x100000)
+    ws.nbytes, ws.is_contiguous = 1 << 24, lambda: True
+    return ws
