@@ -174,29 +174,44 @@ def attn_varlen(q, k, v, cu_seqlens, *, causal=True, window=0, scale=0.0, out=No
 
 class KV4Cache:
     """A paged key/value cache of one layer in 4 bits (slope_kv4_cache): n_pages pages of page_size tokens, Hkv heads
-    of dqk key and dv value channels.  ``data`` (uint8, CUDA, dense) is allocated unless given."""
+    of dqk key and dv value channels.  ``data`` (uint8, CUDA, dense) is allocated unless given; another tensor may take
+    its place later, and a tensor whose memory moves is followed.  The sizes stay as they are."""
+
+    n_pages, page_size, Hkv, dqk, dv = (property(lambda self, i=i: self._sizes[i]) for i in range(5))
 
     def __init__(self, n_pages, page_size, Hkv, dqk, dv, *, data=None, device="cuda"):
-        nbytes = (_marshal or _bound()).cache_bytes(n_pages, page_size, Hkv, dqk, dv)
+        self._sizes = (n_pages, page_size, Hkv, dqk, dv)
+        self._nbytes = nbytes = (_marshal or _bound()).cache_bytes(n_pages, page_size, Hkv, dqk, dv)
         if nbytes == 0 and n_pages != 0:
             raise SlopeError(-8, "slope_kv4_cache_bytes")
-        if data is None:
-            data = torch.empty((nbytes,), dtype=torch.uint8, device=device)
-        elif data.dtype != torch.uint8 or not data.is_contiguous():
+        self.data = torch.empty((nbytes,), dtype=torch.uint8, device=device) if data is None else data
+
+    @property
+    def data(self):
+        return self._data
+
+    @data.setter
+    def data(self, data):
+        nbytes = self._nbytes
+        if data.dtype != torch.uint8 or not data.is_contiguous():
             raise TypeError("the cache's data must be a dense uint8 tensor")
-        elif data.numel() < nbytes:
-            raise ValueError(f"the cache needs {nbytes} bytes, data holds {data.numel()}")
+        room = min(data.numel(), data.untyped_storage().nbytes() - data.storage_offset())
+        if room < nbytes:
+            raise ValueError(f"the cache needs {nbytes} bytes, data holds {room}")
         if nbytes > 0 and not data.is_cuda:
             raise TypeError("the cache's data must be a CUDA tensor")
-        self.data, self._device = data, data.get_device() if nbytes else None
-        self.n_pages, self.page_size, self.Hkv, self.dqk, self.dv = n_pages, page_size, Hkv, dqk, dv
-        self._c = _pack_cache(data.data_ptr() if nbytes else 0, n_pages, page_size, Hkv, dqk, dv)
+        self._data, self._device, self._address = data, data.get_device() if nbytes else None, data.data_ptr()
+        self._end = data.storage_offset() + nbytes  # what its storage has to go on holding
+        self._c = _pack_cache(self._address if nbytes else 0, *self._sizes)
 
     def device_now(self):
-        """The current device, which the cache's data has to be on."""
+        """The current device, which the cache's data has to be on, wherever its memory now is."""
+        data = self._data
+        if data.data_ptr() != self._address or data.untyped_storage().nbytes() < self._end:
+            self.data = data  # moved or cut short in place: look it over again
         dev = _device()
         if self._device != dev and self._device is not None:
-            raise ValueError(f"cache on {self.data.device}, but the current device is cuda:{dev}")
+            raise ValueError(f"cache on {self._data.device}, but the current device is cuda:{dev}")
         return dev
 
 

@@ -1,6 +1,7 @@
 """Edges of the serving calls' host side, without a GPU: CPU tensors without elements and plain objects stand in for CUDA
 tensors, and nothing is launched."""
 import ctypes
+import struct
 
 import pytest
 import torch
@@ -68,3 +69,78 @@ def workspace():
     ws = Fake([1 << 24], torch.uint8, ptr=0x100000)
     ws.nbytes, ws.is_contiguous = 1 << 24, lambda: True
     return ws
+
+
+# ---------------------------------------------------------------- a cache whose memory moves
+
+class FakeData(Fake):
+    """Bytes at an address."""
+
+    def __init__(self, n, ptr, dtype=torch.uint8, cuda=True, dense=True):
+        super().__init__([n], dtype, ptr=ptr)
+        self.is_cuda, self.device, self.dense, self.held = cuda, "cuda:0", dense, n
+
+    def is_contiguous(self):
+        return self.dense
+
+    def untyped_storage(self):
+        return self
+
+    def nbytes(self):
+        return self.held
+
+    def storage_offset(self):
+        return 0
+
+
+class Recorder:
+    """Stands in for the C module: keeps the cache structure that a call was given."""
+
+    def __init__(self, real):
+        self.real, self.got = real, None
+
+    def __getattr__(self, name):
+        if name in ("cache_bytes", "attn_workspace_size"):
+            return getattr(self.real, name)
+
+        def call(*args):
+            packed = next(a for a in args if isinstance(a, bytes))
+            self.got = struct.unpack("@Pqiiii", packed)
+            return 0
+        return call
+
+
+def test_cache_follows_its_data(on_cpu, monkeypatch):
+    """Another tensor in the place of `data`, or the same one with other memory: the next call goes there."""
+    recorder = Recorder(slope.serving._bound())
+    monkeypatch.setattr(slope.serving, "_marshal", recorder)
+    n = 4 * 4 * 2 * 1280
+    held = slope.KV4Cache(4, 64, 2, 64, 64, data=FakeData(n, 0x10000))
+    k, slots, q = Fake([3, 2, 64]), Fake([3], torch.int32), Fake([3, 8, 64])
+    calls = (lambda: slope.kv4_write(held, k, k, slots), lambda: slope.kv4_read(held, slots, k_out=k, v_out=k),
+             lambda: slope.kv4_attn(q, held, Fake([3, 4], torch.int32), slots, out=q, lse=Fake([8, 3], torch.float32),
+                                    workspace=workspace()))
+    for i, call in enumerate(calls):
+        call()
+        assert recorder.got == (held.data.ptr, 4, 64, 2, 64, 64)
+        held.data = FakeData(n + i, 0x20000 + 0x10000 * i)
+        call()
+        assert recorder.got == (0x20000 + 0x10000 * i, 4, 64, 2, 64, 64)
+        held.data.ptr = 0x70000 + 0x10000 * i
+        call()
+        assert recorder.got == (0x70000 + 0x10000 * i, 4, 64, 2, 64, 64)
+    now = held.data
+    for other, error in ((FakeData(n - 1, 0x50000), ValueError), (FakeData(n, 0x50000, torch.int8), TypeError),
+                         (FakeData(n, 0x50000, cuda=False), TypeError), (FakeData(n, 0x50000, dense=False), TypeError)):
+        with pytest.raises(error):
+            held.data = other
+        calls[0]()
+        assert held.data is now and recorder.got[0] == now.ptr
+    now.ptr, now.held = 0x90000, n - 1  # its storage has shrunk
+    for call in calls:
+        with pytest.raises(ValueError):
+            call()
+    for name in ("n_pages", "page_size", "Hkv", "dqk", "dv"):
+        with pytest.raises(AttributeError):
+            setattr(held, name, 1)
+    assert (held.n_pages, held.page_size, held.Hkv, held.dqk, held.dv) == (4, 64, 2, 64, 64)
