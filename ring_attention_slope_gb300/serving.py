@@ -263,6 +263,8 @@ def kv4_attn(q, cache, block_table, kv_lens, *, q_len=1, window=0, scale=0.0, ou
     dev = cache.device_now()
     if workspace.get_device() != dev:
         raise ValueError(f"workspace on {workspace.device}, but the current device is cuda:{dev}")
+    if not workspace.is_contiguous():  # its bytes are counted, and used as one run
+        raise ValueError("the workspace must be a dense tensor")
     st = (_marshal or _bound()).kv4_attn(q, cache._c, block_table, kv_lens, q_len, window, scale, out, lse,
                                          workspace.data_ptr(), workspace.nbytes, _stream(stream, dev), dev)
     _check(st, "slope_kv4_attn")

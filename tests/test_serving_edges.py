@@ -144,3 +144,16 @@ def test_cache_follows_its_data(on_cpu, monkeypatch):
         with pytest.raises(AttributeError):
             setattr(held, name, 1)
     assert (held.n_pages, held.page_size, held.Hkv, held.dqk, held.dv) == (4, 64, 2, 64, 64)
+
+
+def test_strided_workspace_is_refused(on_cpu, monkeypatch):
+    """The workspace's bytes are used as one run: of a view with gaps that would be the gaps' memory too."""
+    monkeypatch.setattr(slope.serving, "_marshal", Recorder(slope.serving._bound()))
+    held = slope.KV4Cache(4, 64, 2, 64, 64, data=FakeData(4 * 4 * 2 * 1280, 0x10000))
+    q, lens = Fake([3, 8, 64]), Fake([3], torch.int32)
+    call = lambda ws: slope.kv4_attn(q, held, Fake([3, 4], torch.int32), lens, out=q, want_lse=False, workspace=ws)  # noqa: E731
+    ws = workspace()
+    call(ws)
+    ws.is_contiguous = lambda: False
+    with pytest.raises(ValueError):
+        call(ws)
