@@ -230,6 +230,16 @@ static int rows_of(PyObject* t, int64_t* out) {
 
 /* ---------------------------------------------------------------- the calls */
 
+/* A library call's status into st, the call made without the interpreter's lock: a launch waits while the stream's
+ * queue is full, perhaps for a host function queued there that wants the lock.  What the call reads is on the C
+ * stack or belongs to arguments that the caller holds. */
+#define UNLOCKED(st, call) \
+  do {                     \
+    Py_BEGIN_ALLOW_THREADS \
+    st = (call);           \
+    Py_END_ALLOW_THREADS   \
+  } while (0)
+
 /* (q, k, q_weight, k_weight, norm, eps, rope, positions, pos0, q_out, k_out, stream, dev) */
 static PyObject* qk_norm_rope(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
@@ -248,8 +258,10 @@ static PyObject* qk_norm_rope(PyObject* self, PyObject* const* a, Py_ssize_t n) 
     return NULL;
   rows = q != NULL ? q->shape[0] : k != NULL ? k->shape[0] : 0;
   if (a[7] != Py_None && index_array(a[7], "positions", dev, rows, &pos) < 0) return NULL;
-  return PyLong_FromLong(lib.qk_norm_rope(q, k, qw, kw, norm, eps, (const slope_rope*)rope, pos, pos0, qo, ko,
-                                          (void*)(uintptr_t)stream));
+  slope_status st;
+  UNLOCKED(st, lib.qk_norm_rope(q, k, qw, kw, norm, eps, (const slope_rope*)rope, pos, pos0, qo, ko,
+                                    (void*)(uintptr_t)stream));
+  return PyLong_FromLong(st);
 }
 
 /* (q, k, v, cu_seqlens as a list or tuple, causal, window, scale, out, lse, stream, dev) */
@@ -276,9 +288,11 @@ static PyObject* attn_varlen(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   } else {
     Py_ssize_t i = 0;
     while (i < m && as_i64(PySequence_Fast_GET_ITEM(seq, i), &cu[i]) == 0) ++i;
-    if (i == m)
-      result = PyLong_FromLong(lib.attn_varlen(q, k, v, cu, m - 1, causal, window, scale, out, lse,
-                                               (void*)(uintptr_t)stream));
+    if (i == m) {
+      slope_status st;
+      UNLOCKED(st, lib.attn_varlen(q, k, v, cu, m - 1, causal, window, scale, out, lse, (void*)(uintptr_t)stream));
+      result = PyLong_FromLong(st);
+    }
   }
   if (cu != few) free(cu);
   Py_DECREF(seq);
@@ -296,7 +310,9 @@ static PyObject* kv4_write(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   if (structure(a[0], sizeof(slope_kv4_cache), &cache) < 0 || describe(a[1], dev, 0, &d[0], &k) < 0 ||
       describe(a[2], dev, 0, &d[1], &v) < 0 || index_array(a[3], "slots", dev, k != NULL ? k->shape[0] : 0, &slots) < 0)
     return NULL;
-  return PyLong_FromLong(lib.kv4_write((const slope_kv4_cache*)cache, k, v, slots, (void*)(uintptr_t)stream));
+  slope_status st;
+  UNLOCKED(st, lib.kv4_write((const slope_kv4_cache*)cache, k, v, slots, (void*)(uintptr_t)stream));
+  return PyLong_FromLong(st);
 }
 
 /* (cache, slots, k, v, stream, dev) */
@@ -310,7 +326,9 @@ static PyObject* kv4_read(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   if (structure(a[0], sizeof(slope_kv4_cache), &cache) < 0 || describe(a[2], dev, 0, &d[0], &k) < 0 ||
       describe(a[3], dev, 0, &d[1], &v) < 0 || index_array(a[1], "slots", dev, k != NULL ? k->shape[0] : 0, &slots) < 0)
     return NULL;
-  return PyLong_FromLong(lib.kv4_read((const slope_kv4_cache*)cache, slots, k, v, (void*)(uintptr_t)stream));
+  slope_status st;
+  UNLOCKED(st, lib.kv4_read((const slope_kv4_cache*)cache, slots, k, v, (void*)(uintptr_t)stream));
+  return PyLong_FromLong(st);
 }
 
 /* (q, cache, block_table, kv_lens, q_len, window, scale, out, lse, workspace address, workspace bytes, stream, dev) */
@@ -350,9 +368,11 @@ static PyObject* kv4_attn(PyObject* self, PyObject* const* a, Py_ssize_t n) {
       describe(a[8], dev, 0, &d[2], &lse) < 0 || index_array(a[2], "block_table", dev, -1, &table) < 0 ||
       index_array(a[3], "kv_lens", dev, batch, &lens) < 0)
     return NULL;
-  return PyLong_FromLong(lib.kv4_attn(q, (const slope_kv4_cache*)cache, table, batch > 1 ? stride[0] : shape[1], shape[1],
-                                      lens, (int32_t)q_len, window, scale, out, lse, (void*)(uintptr_t)ws,
-                                      (size_t)ws_bytes, (void*)(uintptr_t)stream));
+  slope_status st;
+  UNLOCKED(st, lib.kv4_attn(q, (const slope_kv4_cache*)cache, table, batch > 1 ? stride[0] : shape[1], shape[1], lens,
+                            (int32_t)q_len, window, scale, out, lse, (void*)(uintptr_t)ws, (size_t)ws_bytes,
+                            (void*)(uintptr_t)stream));
+  return PyLong_FromLong(st);
 }
 
 static int as_i32(PyObject* o, int32_t* out) {

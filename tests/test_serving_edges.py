@@ -2,6 +2,9 @@
 tensors, and nothing is launched."""
 import ctypes
 import struct
+import subprocess
+import threading
+import time
 
 import pytest
 import torch
@@ -157,3 +160,55 @@ def test_strided_workspace_is_refused(on_cpu, monkeypatch):
     ws.is_contiguous = lambda: False
     with pytest.raises(ValueError):
         call(ws)
+
+
+# ---------------------------------------------------------------- other threads during a call
+
+WAITER = """
+#include <time.h>
+volatile int entered, released;
+/* Stands in for a library call whose launch waits: 0 once another thread has set `released`, -99 after five seconds. */
+int wait_for_release(void) {
+  const struct timespec ms = {0, 1000000};
+  entered = 1;
+  for (int i = 0; i < 5000 && !released; ++i) nanosleep(&ms, 0);
+  return released ? 0 : -99;
+}
+"""
+
+
+def test_other_threads_run_during_a_call(lib, tmp_path):
+    """A call that waits, as a launch into a full queue does, leaves the interpreter to the other threads."""
+    (tmp_path / "waiter.c").write_text(WAITER)
+    subprocess.check_call(["gcc", "-O1", "-shared", "-fPIC", str(tmp_path / "waiter.c"), "-o", str(tmp_path / "waiter.so")])
+    waiter = ctypes.CDLL(str(tmp_path / "waiter.so"))
+    address = ctypes.cast(waiter.wait_for_release, ctypes.c_void_p).value
+    entered, released = (ctypes.c_int.in_dll(waiter, n) for n in ("entered", "released"))
+    m = slope.serving._bound()
+    packed = slope.serving._pack_cache(0x40000, 4, 64, 2, 64, 64)
+    q, k, ints, lse = Fake([3, 8, 64]), Fake([3, 2, 64]), Fake([3], torch.int32), Fake([8, 3], torch.float32)
+    calls = {
+        "qk_norm_rope": lambda: m.qk_norm_rope(q, k, None, None, True, 1e-6, None, None, 0, q, k, 0, 0),
+        "attn_varlen": lambda: m.attn_varlen(q, k, k, [0, 3], True, 0, 0.0, q, lse, 0, 0),
+        "kv4_write": lambda: m.kv4_write(packed, k, k, ints, 0, 0),
+        "kv4_read": lambda: m.kv4_read(packed, ints, k, k, 0, 0),
+        "kv4_attn": lambda: m.kv4_attn(q, packed, Fake([3, 4], torch.int32), ints, 1, 0, 0.0, q, lse, 0, 0, 0, 0),
+    }
+    m.bind(torch.bfloat16, torch.float32, torch.int32, *[address] * 7)
+    try:
+        for name, call in calls.items():
+            entered.value = released.value = 0
+
+            def release():
+                while not entered.value:
+                    time.sleep(0.001)
+                released.value = 1
+
+            thread = threading.Thread(target=release)
+            thread.start()
+            status = call()
+            entered.value = 1
+            thread.join()
+            assert status == 0, name
+    finally:
+        slope.serving._bound()
