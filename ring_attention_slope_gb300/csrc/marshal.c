@@ -277,9 +277,10 @@ static PyObject* attn_varlen(PyObject* self, PyObject* const* a, Py_ssize_t n) {
       describe(a[2], dev, 0, &d[2], &v) < 0 || describe(a[7], dev, 0, &d[3], &out) < 0 ||
       describe(a[8], dev, 0, &d[4], &lse) < 0)
     return NULL;
-  PyObject* seq = PySequence_Fast(a[3], "cu_seqlens must be a sequence of ints");
+  // a tuple of its own: reading an entry may run Python code, which may change the caller's list
+  PyObject* seq = PySequence_Tuple(a[3]);
   if (seq == NULL) return NULL;
-  const Py_ssize_t m = PySequence_Fast_GET_SIZE(seq);
+  const Py_ssize_t m = PyTuple_GET_SIZE(seq);
   PyObject* result = NULL;
   if (m < 1) {
     PyErr_SetString(PyExc_ValueError, "cu_seqlens needs at least one entry");
@@ -287,7 +288,7 @@ static PyObject* attn_varlen(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     PyErr_NoMemory();
   } else {
     Py_ssize_t i = 0;
-    while (i < m && as_i64(PySequence_Fast_GET_ITEM(seq, i), &cu[i]) == 0) ++i;
+    while (i < m && as_i64(PyTuple_GET_ITEM(seq, i), &cu[i]) == 0) ++i;
     if (i == m) {
       slope_status st;
       UNLOCKED(st, lib.attn_varlen(q, k, v, cu, m - 1, causal, window, scale, out, lse, (void*)(uintptr_t)stream));

@@ -1,8 +1,10 @@
 """Edges of the serving calls' host side, without a GPU: CPU tensors without elements and plain objects stand in for CUDA
 tensors, and nothing is launched."""
 import ctypes
+import os
 import struct
 import subprocess
+import sys
 import threading
 import time
 
@@ -10,7 +12,7 @@ import pytest
 import torch
 
 import ring_attention_slope_gb300 as slope
-from _lib import built_lib
+from _lib import ROOT, built_lib
 from test_serving_abi import BF16, F32, S_OK, cache, ref, t
 from test_serving_marshal import Fake
 
@@ -212,3 +214,31 @@ def test_other_threads_run_during_a_call(lib, tmp_path):
             assert status == 0, name
     finally:
         slope.serving._bound()
+
+
+CHANGING_LIST = """
+import sys; sys.path[:0] = [{root!r}, {tests!r}]
+import torch, ring_attention_slope_gb300 as slope
+from test_serving_marshal import Fake
+class Entry:
+    def __index__(self):
+        del cu[1:]
+        junk.append([object() for _ in range(2000)])
+        return 10 ** 6
+cu, junk = [], []
+q, k, lse = Fake([4 * 10 ** 6, 8, 64]), Fake([4 * 10 ** 6, 2, 64]), Fake([8, 4 * 10 ** 6], torch.float32)
+m = slope.serving._bound()
+for n in (3, 300, 5000):
+    cu[:] = [10 ** 6] * 2 + [Entry()] + [10 ** 6 for _ in range(n)]
+    assert m.attn_varlen(q, k, k, cu, True, 0, 0.0, q, lse, 0, 0) == 0 and len(cu) == 1
+    cu[:] = [int(str(10 ** 6)), Entry()] + [int(str(10 ** 6 + i)) for i in range(n)] + [0]
+    assert m.attn_varlen(q, k, k, cu, True, 0, 0.0, q, lse, 0, 0) == -5  # the 0 that stood at its end
+print("done")
+"""
+
+
+def test_list_that_changes_while_it_is_read(lib):
+    """Row indices whose own conversion shortens the list: what the list held when the call began counts."""
+    code = CHANGING_LIST.format(root=ROOT, tests=os.path.join(ROOT, "tests"))
+    run = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=100)
+    assert run.returncode == 0 and run.stdout == "done\n", (run.returncode, run.stderr[-2000:])
