@@ -2,7 +2,7 @@
 ``_marshal.so``, the Python binding's argument marshalling in C.
 
 Translation units are compiled in parallel and linked into one shared
-library next to this file.  The library is rebuilt only when a source or
+library next to this file.  Each is rebuilt only when a source or
 header is newer than it.
 """
 from __future__ import annotations
@@ -11,6 +11,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -36,19 +37,29 @@ def nvcc() -> str:
     return path
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(MARSHAL_PATH):
+def _stale(path, deps) -> bool:
+    if not os.path.exists(path):
         return True
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(MARSHAL_PATH))
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS + ["marshal.c"]]
-    deps += [os.path.join(INCLUDE, f) for f in ("slope.h", "slope_serving.h")] + [__file__]
+    t = os.path.getmtime(path)
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every translation unit for sm_103a and link ``libslope.so``; returns its path."""
-    if not force and not _stale():
-        return LIB_PATH
+def _include(*names):
+    return [os.path.join(INCLUDE, f) for f in names]
+
+
+def _compile_marshal():
+    """Compiles marshal.c for this interpreter, which has to have its headers installed."""
+    tmp = MARSHAL_PATH + f".tmp{os.getpid()}"
+    cmd = [shutil.which("gcc") or "cc", "-O2", "-Wall", "-Wextra", "-shared", "-fPIC", "-fvisibility=hidden",
+           "-I", sysconfig.get_paths()["include"], "-I", INCLUDE, os.path.join(CSRC, "marshal.c"), "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for marshal.c:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL_PATH)
+
+
+def _compile_library(verbose):
     os.makedirs(BUILD_DIR, exist_ok=True)
     cc = nvcc()
 
@@ -62,24 +73,31 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(r.stdout, r.stderr)
         return obj
 
-    def compile_marshal():
-        tmp = MARSHAL_PATH + f".tmp{os.getpid()}"
-        cmd = [shutil.which("gcc") or "cc", "-O2", "-Wall", "-Wextra", "-shared", "-fPIC", "-fvisibility=hidden",
-               "-I", sysconfig.get_paths()["include"], "-I", INCLUDE, os.path.join(CSRC, "marshal.c"), "-o", tmp]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"{cmd[0]} failed for marshal.c:\n{r.stdout}\n{r.stderr}")
-        return tmp
-
-    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        marshal = ex.submit(compile_marshal)
+    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         objs = list(ex.map(compile_one, SOURCES))
-    os.replace(marshal.result(), MARSHAL_PATH)
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     r = subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Compile every translation unit for sm_103a and link ``libslope.so``; returns its path.
+
+    The library needs nothing of Python.  Where the argument marshalling cannot be compiled (no ``Python.h``, say),
+    the library is built all the same, with a warning; the calls that go through the marshalling then raise."""
+    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + _include("slope.h", "slope_serving.h") + [__file__]
+    if force or _stale(LIB_PATH, deps):
+        _compile_library(verbose)
+    deps = [os.path.join(CSRC, "marshal.c")] + _include("slope.h", "slope_serving.h") + [__file__]
+    if force or _stale(MARSHAL_PATH, deps):
+        try:
+            _compile_marshal()
+        except (OSError, RuntimeError) as e:
+            if os.path.exists(MARSHAL_PATH):
+                os.remove(MARSHAL_PATH)  # of older sources: not for this library
+            warnings.warn(f"libslope is built without its Python marshalling: {e}", stacklevel=2)
     return LIB_PATH
 
 

@@ -13,6 +13,7 @@ import torch
 
 import ring_attention_slope_gb300 as slope
 from _lib import ROOT, built_lib
+from ring_attention_slope_gb300 import _build
 from test_serving_abi import BF16, F32, S_OK, cache, ref, t
 from test_serving_marshal import Fake
 
@@ -242,3 +243,18 @@ def test_list_that_changes_while_it_is_read(lib):
     code = CHANGING_LIST.format(root=ROOT, tests=os.path.join(ROOT, "tests"))
     run = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=100)
     assert run.returncode == 0 and run.stdout == "done\n", (run.returncode, run.stderr[-2000:])
+
+
+# ---------------------------------------------------------------- building
+
+def test_library_builds_without_python_headers(lib, tmp_path, monkeypatch):
+    """libslope needs no Python: where marshal.c cannot be compiled it is built all the same, and says so."""
+    monkeypatch.setattr(_build, "MARSHAL_PATH", str(tmp_path / "_marshal.so"))
+    monkeypatch.setattr(_build.sysconfig, "get_paths", lambda: {"include": str(tmp_path)})
+    for older in (False, True):  # a module of older sources is not left to be loaded
+        if older:
+            (tmp_path / "_marshal.so").write_bytes(b"")
+            os.utime(tmp_path / "_marshal.so", (0, 0))
+        with pytest.warns(UserWarning, match="marshal"):
+            assert _build.build() == _build.LIB_PATH
+        assert os.listdir(tmp_path) == []
