@@ -1,5 +1,5 @@
 """Builds ``libslope.so`` (the CUDA kernels and the C ABI) in-tree with nvcc for sm_103a, and
-``_marshal.so``, the Python binding's argument marshalling in C.
+``_marshal``, the Python binding's argument marshalling in C.
 
 Translation units are compiled in parallel and linked into one shared
 library next to this file.  Each is rebuilt only when a source or
@@ -20,7 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libslope.so")
-MARSHAL_PATH = os.path.join(PKG, "_marshal.so")
+# named after the interpreter whose headers it is compiled with: another one finds none and builds its own
+MARSHAL_PATH = os.path.join(PKG, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 SOURCES = ["attn_partial.cu", "kv4_attn.cu", "api.cu", "lse_merge.cu", "qk_norm_rope.cu", "kv4_store.cu", "status.cu",
            "dck.cpp", "rope.cpp"]

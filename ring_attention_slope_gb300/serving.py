@@ -8,12 +8,15 @@ current device, and a call runs on the current stream unless it is given one; wh
 from __future__ import annotations
 
 import ctypes
+import importlib.util
+import os
 import struct
+import sys
 from array import array
 
 import torch
 
-from . import SlopeError, _check, load
+from . import SlopeError, _build, _check, load
 
 EXPORTED_SERVING = ["slope_rope_inv_freq", "slope_qk_norm_rope", "slope_attn_varlen", "slope_kv4_block_bytes",
                     "slope_kv4_cache_bytes", "slope_kv4_write", "slope_kv4_read", "slope_kv4_attn",
@@ -60,12 +63,25 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 _marshal = None  # the C module, once load() has found the library
 
 
+def _module():
+    """The C module built for this interpreter."""
+    name = f"{__package__}._marshal"
+    if name not in sys.modules:
+        path = _build.MARSHAL_PATH
+        if not os.path.exists(path):
+            raise RuntimeError(f"the serving calls' marshalling is not built ({path}); call ring_attention_slope_gb300.build()")
+        spec = importlib.util.spec_from_file_location(name, path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        sys.modules[name] = module
+    return sys.modules[name]
+
+
 def _bound():
     """The C module, bound to the library's calls."""
     global _marshal
     lib = load()
-    from . import _marshal as m
-
+    m = _module()
     address = lambda f: ctypes.cast(f, ctypes.c_void_p).value  # noqa: E731
     m.bind(torch.bfloat16, torch.float32, torch.int32, address(lib.slope_qk_norm_rope), address(lib.slope_attn_varlen),
            address(lib.slope_kv4_write), address(lib.slope_kv4_read), address(lib.slope_kv4_attn),

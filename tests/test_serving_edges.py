@@ -5,6 +5,7 @@ import os
 import struct
 import subprocess
 import sys
+import sysconfig
 import threading
 import time
 
@@ -258,3 +259,15 @@ def test_library_builds_without_python_headers(lib, tmp_path, monkeypatch):
         with pytest.warns(UserWarning, match="marshal"):
             assert _build.build() == _build.LIB_PATH
         assert os.listdir(tmp_path) == []
+
+
+def test_marshalling_belongs_to_its_interpreter(lib, tmp_path, monkeypatch):
+    """The C module carries the interpreter's tag, and no other file is loaded in its place."""
+    m = slope.serving._bound()
+    assert m.__file__ == _build.MARSHAL_PATH
+    assert os.path.basename(m.__file__) == "_marshal" + sysconfig.get_config_var("EXT_SUFFIX") != "_marshal.so"
+    (tmp_path / "_marshal.so").write_bytes(open(m.__file__, "rb").read())
+    monkeypatch.setattr(_build, "MARSHAL_PATH", str(tmp_path / "_marshal.other-interpreter.so"))
+    monkeypatch.delitem(sys.modules, m.__name__)
+    with pytest.raises(RuntimeError, match="not built"):
+        slope.serving._bound()
