@@ -131,8 +131,7 @@ def load():
     lib.slope_cp_prefill_ex.restype = c_int
     lib.slope_cp_prefill_workspace_size_ex.argtypes = [i64, i64, i64, c_int, c_int, P(i64), ctypes.c_uint]
     lib.slope_cp_prefill_workspace_size_ex.restype = ctypes.c_size_t
-    if _serving is not None:
-        _serving.declare(lib)
+    serving.declare(lib)
     _lib = lib
     return lib
 
@@ -447,11 +446,6 @@ def timeout_selftest(limit_ns: int, stream=None):
     _check(load().slope_debug_timeout_selftest(int(limit_ns), _stream_ptr(stream)), "slope_debug_timeout_selftest")
 
 
-try:
-    from . import serving as _serving  # (it uses the helpers above)
-    from .serving import (EXPORTED_SERVING, KV4Cache, Rope, SlopeKV4Cache, SlopeRope, attn_varlen,  # noqa: F401
-                          kv4_attn, kv4_attn_workspace_size, kv4_read, kv4_write, qk_norm_rope, rope_inv_freq)
-except ModuleNotFoundError as e:  # without PyTorch the library can still be built
-    if e.name != "torch":
-        raise
-    _serving = None
+from . import serving  # noqa: E402  (it uses the helpers above)
+from .serving import (EXPORTED_SERVING, KV4Cache, Rope, SlopeKV4Cache, SlopeRope, attn_varlen,  # noqa: E402, F401
+                      kv4_attn, kv4_attn_workspace_size, kv4_read, kv4_write, qk_norm_rope, rope_inv_freq)

@@ -14,8 +14,6 @@ import struct
 import sys
 from array import array
 
-import torch
-
 from . import SlopeError, _build, _check, load
 
 EXPORTED_SERVING = ["slope_rope_inv_freq", "slope_qk_norm_rope", "slope_attn_varlen", "slope_kv4_block_bytes",
@@ -58,9 +56,9 @@ def declare(lib):
 
 _pack_rope = struct.Struct("@iiifP").pack  # slope_rope
 _pack_cache = struct.Struct("@Pqiiii").pack  # slope_kv4_cache
-_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_marshal = None  # the C module, once load() has found the library
+_marshal = None  # the C module, once the first call has found it and the library
+torch = None  # PyTorch, with the first call: the package can be imported, and the library used, without it
+_device = _raw_stream = _alloc = None  # the current device; its current stream; size, stride and type -> tensor there
 
 
 def _module():
@@ -77,11 +75,27 @@ def _module():
     return sys.modules[name]
 
 
+def _use_torch():
+    global torch, _device, _raw_stream, _alloc
+    if torch is not None:
+        return
+    import torch as t
+
+    try:  # the allocation alone: torch.empty's argument parsing costs a small call another 1.5 us each
+        from torch._C._dynamo.guards import _empty_strided_cuda as alloc
+    except ImportError:
+        def alloc(size, stride, dtype):
+            return t.empty_strided(size, stride, dtype=dtype, device="cuda")
+    _device, _raw_stream, _alloc = t._C._cuda_getDevice, t._C._cuda_getCurrentRawStream, alloc
+    torch = t
+
+
 def _bound():
     """The C module, bound to the library's calls."""
     global _marshal
     lib = load()
     m = _module()
+    _use_torch()
     address = lambda f: ctypes.cast(f, ctypes.c_void_p).value  # noqa: E731
     m.bind(torch.bfloat16, torch.float32, torch.int32, address(lib.slope_qk_norm_rope), address(lib.slope_attn_varlen),
            address(lib.slope_kv4_write), address(lib.slope_kv4_read), address(lib.slope_kv4_attn),
@@ -92,13 +106,6 @@ def _bound():
 
 def _stream(stream, dev):
     return _raw_stream(dev) if stream is None else stream.cuda_stream
-
-
-try:  # the allocation alone: torch.empty's argument parsing costs a small call another 1.5 us each
-    from torch._C._dynamo.guards import _empty_strided_cuda as _alloc
-except ImportError:
-    def _alloc(size, stride, dtype):
-        return torch.empty_strided(size, stride, dtype=dtype, device="cuda")
 
 
 def _empty(size, stride, dtype, stream):
@@ -147,6 +154,7 @@ def qk_norm_rope(q, k=None, *, norm=True, q_weight=None, k_weight=None, eps=1e-6
     ``norm=False`` rotates alone.  ``positions``: device int32 [T], or None for pos0, pos0 + 1, ...  The outputs
     (of the inputs' type unless given) may be the inputs.  Returns ``(q_out, k_out)`` (k_out None without k).
     """
+    m = _marshal or _bound()
     if q_out is None:
         T, H, d = q.shape
         q_out = _heads(T, H, d, out_dtype or q.dtype, stream)
@@ -154,8 +162,8 @@ def qk_norm_rope(q, k=None, *, norm=True, q_weight=None, k_weight=None, eps=1e-6
         T, H, d = k.shape
         k_out = _heads(T, H, d, out_dtype or k.dtype, stream)
     dev = _device()
-    st = (_marshal or _bound()).qk_norm_rope(q, k, q_weight, k_weight, norm, eps, None if rope is None else rope._c,
-                                             positions, pos0, q_out, k_out, _stream(stream, dev), dev)
+    st = m.qk_norm_rope(q, k, q_weight, k_weight, norm, eps, None if rope is None else rope._c, positions, pos0, q_out,
+                        k_out, _stream(stream, dev), dev)
     _check(st, "slope_qk_norm_rope")
     return q_out, k_out
 
@@ -170,6 +178,7 @@ def attn_varlen(q, k, v, cu_seqlens, *, causal=True, window=0, scale=0.0, out=No
     Returns ``(out, lse)``: out bf16 (default) or fp32 [T,Hq,dv], lse fp32 [Hq,T].  Rows outside the sequences
     are left as they were (uninitialised where the call allocates).
     """
+    m = _marshal or _bound()
     T, Hq, _ = q.shape
     if out is None:
         out = _heads(T, Hq, v.shape[2], out_dtype or torch.bfloat16, stream)
@@ -180,8 +189,7 @@ def attn_varlen(q, k, v, cu_seqlens, *, causal=True, window=0, scale=0.0, out=No
             raise TypeError("cu_seqlens lives on the host (reading it back would synchronise)")
         cu_seqlens = cu_seqlens.tolist()
     dev = _device()
-    st = (_marshal or _bound()).attn_varlen(q, k, v, cu_seqlens, causal, window, scale, out, lse,
-                                            _stream(stream, dev), dev)
+    st = m.attn_varlen(q, k, v, cu_seqlens, causal, window, scale, out, lse, _stream(stream, dev), dev)
     _check(st, "slope_attn_varlen")
     return out, lse
 
@@ -234,21 +242,23 @@ class KV4Cache:
 def kv4_write(cache, k, v, slots, *, stream=None):
     """Writes k [T,Hkv,dqk], v [T,Hkv,dv] (bf16 or fp32) into the cache at slots (device int32 [T]; slot = page *
     page_size + index, out of range: skipped; the others distinct)."""
+    m = _marshal or _bound()
     dev = cache.device_now()
-    st = (_marshal or _bound()).kv4_write(cache._c, k, v, slots, _stream(stream, dev), dev)
+    st = m.kv4_write(cache._c, k, v, slots, _stream(stream, dev), dev)
     _check(st, "slope_kv4_write")
 
 
 def kv4_read(cache, slots, *, k_out=None, v_out=None, out_dtype=None, stream=None):
     """The values the cache holds at slots (device int32 [T]): ``(k [T,Hkv,dqk], v [T,Hkv,dv])``, bf16 (default) or
     fp32.  Rows whose slot is out of range are left as they were (uninitialised where the call allocates)."""
+    m = _marshal or _bound()
     T = slots.shape[0]
     if k_out is None:
         k_out = _heads(T, cache.Hkv, cache.dqk, out_dtype or torch.bfloat16, stream)
     if v_out is None:
         v_out = _heads(T, cache.Hkv, cache.dv, out_dtype or torch.bfloat16, stream)
     dev = cache.device_now()
-    st = (_marshal or _bound()).kv4_read(cache._c, slots, k_out, v_out, _stream(stream, dev), dev)
+    st = m.kv4_read(cache._c, slots, k_out, v_out, _stream(stream, dev), dev)
     _check(st, "slope_kv4_read")
     return k_out, v_out
 
@@ -266,13 +276,14 @@ def kv4_attn(q, cache, block_table, kv_lens, *, q_len=1, window=0, scale=0.0, ou
     of a sequence sees positions up to kv_lens - q_len + i (and, with ``window``, that many back).  Returns
     ``(out, lse)``: out bf16 (default) or fp32 [B * q_len,Hq,dv], lse fp32 [Hq,B * q_len] (None if not wanted).
     """
+    m = _marshal or _bound()
     T, Hq, _ = q.shape
     if out is None:
         out = _heads(T, Hq, cache.dv, out_dtype or torch.bfloat16, stream)
     if lse is None and want_lse:
         lse = _empty((Hq, T), (T, 1), torch.float32, stream)
     if workspace is None:
-        nbytes = (_marshal or _bound()).attn_workspace_size(block_table.shape[0], Hq, cache._c, q_len)
+        nbytes = m.attn_workspace_size(block_table.shape[0], Hq, cache._c, q_len)
         if nbytes == 0:
             raise SlopeError(-8, "slope_kv4_attn_workspace_size")
         workspace = _empty((nbytes,), (1,), torch.uint8, stream)
@@ -281,7 +292,7 @@ def kv4_attn(q, cache, block_table, kv_lens, *, q_len=1, window=0, scale=0.0, ou
         raise ValueError(f"workspace on {workspace.device}, but the current device is cuda:{dev}")
     if not workspace.is_contiguous():  # its bytes are counted, and used as one run
         raise ValueError("the workspace must be a dense tensor")
-    st = (_marshal or _bound()).kv4_attn(q, cache._c, block_table, kv_lens, q_len, window, scale, out, lse,
-                                         workspace.data_ptr(), workspace.nbytes, _stream(stream, dev), dev)
+    st = m.kv4_attn(q, cache._c, block_table, kv_lens, q_len, window, scale, out, lse, workspace.data_ptr(),
+                    workspace.nbytes, _stream(stream, dev), dev)
     _check(st, "slope_kv4_attn")
     return out, lse

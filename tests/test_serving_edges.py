@@ -29,6 +29,7 @@ def lib():
 @pytest.fixture
 def on_cpu(lib, monkeypatch):
     """The public calls with the host's memory in the place of the device's."""
+    slope.serving._bound()
     monkeypatch.setattr(slope.serving, "_device", lambda: 0)
     monkeypatch.setattr(slope.serving, "_raw_stream", lambda dev: 0)
     monkeypatch.setattr(slope.serving, "_alloc", lambda size, stride, dtype: torch.empty_strided(size, stride, dtype=dtype))
@@ -271,3 +272,25 @@ def test_marshalling_belongs_to_its_interpreter(lib, tmp_path, monkeypatch):
     monkeypatch.delitem(sys.modules, m.__name__)
     with pytest.raises(RuntimeError, match="not built"):
         slope.serving._bound()
+
+
+WITHOUT_TORCH = """
+import sys; sys.path.insert(0, {root!r}); sys.modules["torch"] = None  # as where it is not installed
+from ring_attention_slope_gb300 import *
+import ring_attention_slope_gb300 as slope
+assert slope.load().slope_kv4_block_bytes(64, 64) == 1280 and len(slope.rope_inv_freq(64)[0]) == 32
+assert Rope([1.0] * 8)._c and version()
+try:
+    qk_norm_rope(None)
+except ModuleNotFoundError as e:
+    assert e.name == "torch"
+    print("done")
+"""
+
+
+def test_package_without_torch(lib):
+    """Importing the package, its library and its host-only calls need no PyTorch; calls on tensors say that they do."""
+    run = subprocess.run([sys.executable, "-c", WITHOUT_TORCH.format(root=ROOT)], capture_output=True, text=True, timeout=100)
+    assert run.returncode == 0 and run.stdout == "done\n", (run.returncode, run.stderr[-2000:])
+    lazy = f"import sys; sys.path.insert(0, {ROOT!r}); import ring_attention_slope_gb300 as s; s.load(); print('torch' in sys.modules)"
+    assert subprocess.check_output([sys.executable, "-c", lazy], text=True, timeout=100) == "False\n"
