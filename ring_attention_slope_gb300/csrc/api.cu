@@ -58,7 +58,8 @@ slope_status check_qkv(const slope_tensor* t) {
   if (t->ndim != 3) return SLOPE_ERR_SHAPE;
   if (t->shape[0] < 0 || t->shape[1] <= 0 || t->shape[2] <= 0 || t->shape[0] > kMaxSeq || t->shape[1] > 65535)
     return SLOPE_ERR_SHAPE;
-  if (t->shape[0] > 0 && t->data == nullptr) return SLOPE_ERR_NULL;
+  if (t->shape[0] == 0) return SLOPE_OK;  // no address is made: strides may be anything
+  if (t->data == nullptr) return SLOPE_ERR_NULL;
   if (t->stride[2] != 1) return SLOPE_ERR_STRIDE;
   if (t->stride[0] <= 0 || t->stride[1] <= 0 || t->stride[0] % 8 || t->stride[1] % 8) return SLOPE_ERR_STRIDE;
   if (!aligned(t->data, 16)) return SLOPE_ERR_STRIDE;
@@ -73,7 +74,8 @@ slope_status check_out(const slope_tensor* t, int64_t S, int64_t H, int64_t dv, 
   if (t == nullptr) return SLOPE_ERR_NULL;
   if (t->dtype != SLOPE_F32 && !(allow_bf16 && t->dtype == SLOPE_BF16)) return SLOPE_ERR_DTYPE;
   if (t->ndim != 3 || t->shape[0] != S || t->shape[1] != H || t->shape[2] != dv) return SLOPE_ERR_SHAPE;
-  if (S > 0 && t->data == nullptr) return SLOPE_ERR_NULL;
+  if (S == 0) return SLOPE_OK;
+  if (t->data == nullptr) return SLOPE_ERR_NULL;
   if (t->stride[2] != 1 || t->stride[0] <= 0 || t->stride[1] <= 0) return SLOPE_ERR_STRIDE;
   if (t->stride[0] % 4 || t->stride[1] % 4) return SLOPE_ERR_STRIDE;
   if (!aligned(t->data, t->dtype == SLOPE_F32 ? 16 : 8)) return SLOPE_ERR_STRIDE;
@@ -853,7 +855,7 @@ slope_status slope_attn_partial(const slope_tensor* q, const slope_tensor* k, co
   if (q_off < -kMaxPos || q_off + Sq > kMaxPos || kv_off < -kMaxPos || kv_off + Skv > kMaxPos) return SLOPE_ERR_SHAPE;
   if ((st = check_out(out, Sq, Hq, dv, true)) != SLOPE_OK) return st;
   // bf16 rows are written 16 bytes at a time
-  if (out->dtype == SLOPE_BF16 && (out->stride[0] % 8 || out->stride[1] % 8 || !aligned(out->data, 16)))
+  if (Sq > 0 && out->dtype == SLOPE_BF16 && (out->stride[0] % 8 || out->stride[1] % 8 || !aligned(out->data, 16)))
     return SLOPE_ERR_STRIDE;
   if ((st = check_lse(lse, Hq, Sq)) != SLOPE_OK) return st;
   if (Sq == 0) return SLOPE_OK;
@@ -926,7 +928,7 @@ slope_status slope_attn_varlen(const slope_tensor* q, const slope_tensor* k, con
   if (!attn_partial_supported(static_cast<int>(dqk), static_cast<int>(dv))) return SLOPE_ERR_UNSUPPORTED;
   if (window < 0 || window > kMaxSeq) return SLOPE_ERR_SHAPE;
   if ((st = check_out(out, T, Hq, dv, true)) != SLOPE_OK) return st;
-  if (out->dtype == SLOPE_BF16 && (out->stride[0] % 8 || out->stride[1] % 8 || !aligned(out->data, 16)))
+  if (T > 0 && out->dtype == SLOPE_BF16 && (out->stride[0] % 8 || out->stride[1] % 8 || !aligned(out->data, 16)))
     return SLOPE_ERR_STRIDE;
   if ((st = check_lse(lse, Hq, T)) != SLOPE_OK) return st;
   if (n_seqs < 0 || (n_seqs > 0 && cu_seqlens == nullptr)) return n_seqs < 0 ? SLOPE_ERR_SHAPE : SLOPE_ERR_NULL;

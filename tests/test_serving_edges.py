@@ -56,6 +56,18 @@ def test_lse_strides_with_rows_are_still_checked(lib):
     assert BF16 == 0
 
 
+@pytest.mark.parametrize("stride", [[64, 0, 1], [0, 0, 0], [1, 7, 3]])
+def test_strides_without_rows(lib, stride):
+    """PyTorch gives a [0, 1, d] that an operation made strides of (d, 0, 1): they say nothing."""
+    q, lse = t([0, 1, 64], data=0, stride=stride), t([1, 0], F32, data=0, stride=[0, 1])
+    cu = (ctypes.c_int64 * 1)(0)
+    assert lib.slope_attn_varlen(ref(q), ref(q), ref(q), cu, 0, 1, 0, 0.0, ref(q), ref(lse), None) == S_OK
+    assert lib.slope_kv4_attn(ref(q), ref(cache(H=1)), 0x6000, 5, 5, 0x7000, 1, 0, 0.0, ref(q), ref(lse), None, 0, None) == S_OK
+    assert lib.slope_attn_partial(ref(q), ref(q), ref(q), 0, 0, 1, 0, 0.0, ref(q), ref(lse), None) == S_OK
+    assert lib.slope_kv4_write(ref(cache(H=1)), ref(q), ref(q), None, None) == S_OK
+    assert lib.slope_qk_norm_rope(ref(q), None, None, None, 1, 1e-6, None, None, 0, ref(q), None, None) == S_OK
+
+
 def test_calls_without_tokens_make_their_outputs(on_cpu):
     """Every output left to the call: a batch without sequences is a no-op, not an error."""
     q, k = torch.empty(0, 8, 64, dtype=BF), torch.empty(0, 2, 64, dtype=BF)
