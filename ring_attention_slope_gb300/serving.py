@@ -58,7 +58,9 @@ _pack_rope = struct.Struct("@iiifP").pack  # slope_rope
 _pack_cache = struct.Struct("@Pqiiii").pack  # slope_kv4_cache
 _marshal = None  # the C module, once the first call has found it and the library
 torch = None  # PyTorch, with the first call: the package can be imported, and the library used, without it
-_device = _raw_stream = _alloc = None  # the current device; its current stream; size, stride and type -> tensor there
+_device = _raw_stream = None  # the current device; its current stream
+_alloc = None  # (size, stride, type) -> a tensor on the current device
+_modes = _deterministic = None  # dispatch modes that are on; whether deterministic algorithms are asked for
 
 
 def _module():
@@ -76,18 +78,24 @@ def _module():
 
 
 def _use_torch():
-    global torch, _device, _raw_stream, _alloc
+    global torch, _device, _raw_stream, _alloc, _modes, _deterministic
     if torch is not None:
         return
     import torch as t
 
-    try:  # the allocation alone: torch.empty's argument parsing costs a small call another 1.5 us each
+    try:  # the allocation alone: torch.empty's argument parsing costs a small call another 0.7 us for each output
+        from torch._C import _get_deterministic_algorithms as deterministic
+        from torch._C import _len_torch_dispatch_stack as modes
         from torch._C._dynamo.guards import _empty_strided_cuda as alloc
     except ImportError:
-        def alloc(size, stride, dtype):
-            return t.empty_strided(size, stride, dtype=dtype, device="cuda")
-    _device, _raw_stream, _alloc = t._C._cuda_getDevice, t._C._cuda_getCurrentRawStream, alloc
+        alloc, modes, deterministic = _dispatched_alloc, int, bool
+    _device, _raw_stream = t._C._cuda_getDevice, t._C._cuda_getCurrentRawStream
+    _alloc, _modes, _deterministic = alloc, modes, deterministic
     torch = t
+
+
+def _dispatched_alloc(size, stride, dtype):
+    return torch.empty_strided(size, stride, dtype=dtype, device="cuda")
 
 
 def _bound():
@@ -108,18 +116,22 @@ def _stream(stream, dev):
     return _raw_stream(dev) if stream is None else stream.cuda_stream
 
 
-def _empty(size, stride, dtype, stream):
-    """A tensor on the current device.  What a call allocates belongs to the stream it runs on: a temporary's memory
-    is not handed out again before that stream is done with it."""
+def _allocator(stream):
+    """How a call on the stream allocates.  What it allocates belongs to the stream it runs on: a temporary's memory
+    is not handed out again before that stream is done with it.  Where PyTorch's dispatcher has something to do with an
+    allocation (a mode watches, or deterministic algorithms have uninitialised memory filled) it goes that way."""
     if stream is None:
-        return _alloc(size, stride, dtype)
-    with torch.cuda.stream(stream):
-        return _alloc(size, stride, dtype)
+        return _dispatched_alloc if _modes() or _deterministic() else _alloc
+
+    def alloc(size, stride, dtype):
+        with torch.cuda.stream(stream):
+            return _dispatched_alloc(size, stride, dtype)
+    return alloc
 
 
-def _heads(T, H, d, dtype, stream):
+def _heads(alloc, T, H, d, dtype):
     """A dense [T, H, d]."""
-    return _empty((T, H, d), (H * d, d, 1), dtype, stream)
+    return alloc((T, H, d), (H * d, d, 1), dtype)
 
 
 # ---------------------------------------------------------------- positions
@@ -155,12 +167,13 @@ def qk_norm_rope(q, k=None, *, norm=True, q_weight=None, k_weight=None, eps=1e-6
     (of the inputs' type unless given) may be the inputs.  Returns ``(q_out, k_out)`` (k_out None without k).
     """
     m = _marshal or _bound()
+    alloc = _allocator(stream)
     if q_out is None:
         T, H, d = q.shape
-        q_out = _heads(T, H, d, out_dtype or q.dtype, stream)
+        q_out = _heads(alloc, T, H, d, out_dtype or q.dtype)
     if k is not None and k_out is None:
         T, H, d = k.shape
-        k_out = _heads(T, H, d, out_dtype or k.dtype, stream)
+        k_out = _heads(alloc, T, H, d, out_dtype or k.dtype)
     dev = _device()
     st = m.qk_norm_rope(q, k, q_weight, k_weight, norm, eps, None if rope is None else rope._c, positions, pos0, q_out,
                         k_out, _stream(stream, dev), dev)
@@ -179,11 +192,12 @@ def attn_varlen(q, k, v, cu_seqlens, *, causal=True, window=0, scale=0.0, out=No
     are left as they were (uninitialised where the call allocates).
     """
     m = _marshal or _bound()
+    alloc = _allocator(stream)
     T, Hq, _ = q.shape
     if out is None:
-        out = _heads(T, Hq, v.shape[2], out_dtype or torch.bfloat16, stream)
+        out = _heads(alloc, T, Hq, v.shape[2], out_dtype or torch.bfloat16)
     if lse is None:
-        lse = _empty((Hq, T), (T, 1), torch.float32, stream)
+        lse = alloc((Hq, T), (T, 1), torch.float32)
     if isinstance(cu_seqlens, torch.Tensor):
         if cu_seqlens.is_cuda:
             raise TypeError("cu_seqlens lives on the host (reading it back would synchronise)")
@@ -252,11 +266,12 @@ def kv4_read(cache, slots, *, k_out=None, v_out=None, out_dtype=None, stream=Non
     """The values the cache holds at slots (device int32 [T]): ``(k [T,Hkv,dqk], v [T,Hkv,dv])``, bf16 (default) or
     fp32.  Rows whose slot is out of range are left as they were (uninitialised where the call allocates)."""
     m = _marshal or _bound()
+    alloc = _allocator(stream)
     T = slots.shape[0]
     if k_out is None:
-        k_out = _heads(T, cache.Hkv, cache.dqk, out_dtype or torch.bfloat16, stream)
+        k_out = _heads(alloc, T, cache.Hkv, cache.dqk, out_dtype or torch.bfloat16)
     if v_out is None:
-        v_out = _heads(T, cache.Hkv, cache.dv, out_dtype or torch.bfloat16, stream)
+        v_out = _heads(alloc, T, cache.Hkv, cache.dv, out_dtype or torch.bfloat16)
     dev = cache.device_now()
     st = m.kv4_read(cache._c, slots, k_out, v_out, _stream(stream, dev), dev)
     _check(st, "slope_kv4_read")
@@ -277,16 +292,17 @@ def kv4_attn(q, cache, block_table, kv_lens, *, q_len=1, window=0, scale=0.0, ou
     ``(out, lse)``: out bf16 (default) or fp32 [B * q_len,Hq,dv], lse fp32 [Hq,B * q_len] (None if not wanted).
     """
     m = _marshal or _bound()
+    alloc = _allocator(stream)
     T, Hq, _ = q.shape
     if out is None:
-        out = _heads(T, Hq, cache.dv, out_dtype or torch.bfloat16, stream)
+        out = _heads(alloc, T, Hq, cache.dv, out_dtype or torch.bfloat16)
     if lse is None and want_lse:
-        lse = _empty((Hq, T), (T, 1), torch.float32, stream)
+        lse = alloc((Hq, T), (T, 1), torch.float32)
     if workspace is None:
         nbytes = m.attn_workspace_size(block_table.shape[0], Hq, cache._c, q_len)
         if nbytes == 0:
             raise SlopeError(-8, "slope_kv4_attn_workspace_size")
-        workspace = _empty((nbytes,), (1,), torch.uint8, stream)
+        workspace = alloc((nbytes,), (1,), torch.uint8)
     dev = cache.device_now()
     if workspace.get_device() != dev:
         raise ValueError(f"workspace on {workspace.device}, but the current device is cuda:{dev}")

@@ -1,6 +1,7 @@
 """Edges of the serving calls on the GPU that a server meets and the tests of single calls do not."""
 import pytest
 import torch
+from torch.utils._python_dispatch import TorchDispatchMode
 
 import ring_attention_slope_gb300 as slope
 from test_gpu_serving import i32, rand
@@ -58,3 +59,53 @@ def test_cache_data_replaced():
     cache.data.set_(torch.cat([first, first]))  # in place: other memory behind the same tensor
     old_out, old_lse = slope.kv4_attn(q, cache, table, lens)
     assert torch.equal(out, old_out) and torch.equal(lse, old_lse)
+
+
+# ---------------------------------------------------------------- memory that a call allocates
+
+def outputs_of_the_calls(stream=None):
+    """One of each call with its outputs left to it, rows that no sequence or slot covers among them."""
+    T, H, d = 40, 2, 64
+    q, k = rand(T, 8, d, seed=4).cuda(), rand(T, H, d, seed=5).cuda()
+    cache, slots = slope.KV4Cache(3, 16, H, d, d, data=torch.zeros(3 * H * 1280, dtype=torch.uint8, device="cuda")), i32(range(T))
+    slots[-1] = -1
+    torch.cuda.synchronize()
+    return [*slope.qk_norm_rope(q, k, stream=stream), *slope.attn_varlen(q, k, k, [5, 30], stream=stream),
+            *slope.kv4_read(cache, slots, stream=stream),
+            *slope.kv4_attn(q[:1], cache, i32([[0, 1, 2]]), i32([T]), stream=stream)]
+
+
+@pytest.mark.parametrize("side", [False, True])
+def test_deterministic_fill_of_what_is_not_written(side):
+    """With deterministic algorithms PyTorch fills uninitialised memory, rows that a call leaves as they were too."""
+    stream = torch.cuda.Stream() if side else None
+    for t in outputs_of_the_calls(stream):  # blocks of these sizes with other numbers in them, freed again
+        t.fill_(7)
+    torch.cuda.synchronize()
+    del t
+    torch.use_deterministic_algorithms(True)
+    try:
+        _, _, out, lse, k, v, *_ = outputs_of_the_calls(stream)
+    finally:
+        torch.use_deterministic_algorithms(False)
+    torch.cuda.synchronize()
+    for rest in (out[:5], out[30:], lse[:, :5], lse[:, 30:], k[-1], v[-1]):
+        assert torch.isnan(rest).all()
+    for written in (out[5:30], lse[:, 5:30], k[:-1], v[:-1]):
+        assert torch.isfinite(written).all()
+
+
+def test_dispatch_modes_see_the_allocations():
+    class Watch(TorchDispatchMode):
+        seen = []
+
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            r = func(*args, **(kwargs or {}))
+            if "empty" in str(func):
+                self.seen.append(r.data_ptr())
+            return r
+
+    with Watch():
+        outputs = outputs_of_the_calls()
+    torch.cuda.synchronize()
+    assert {t.data_ptr() for t in outputs} <= set(Watch.seen)
