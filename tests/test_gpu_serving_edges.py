@@ -4,7 +4,7 @@ import torch
 from torch.utils._python_dispatch import TorchDispatchMode
 
 import ring_attention_slope_gb300 as slope
-from test_gpu_serving import i32, rand
+from test_gpu_serving import check_varlen, i32, packed, rand
 
 pytestmark = pytest.mark.gpu
 
@@ -109,3 +109,40 @@ def test_dispatch_modes_see_the_allocations():
         outputs = outputs_of_the_calls()
     torch.cuda.synchronize()
     assert {t.data_ptr() for t in outputs} <= set(Watch.seen)
+
+
+# ---------------------------------------------------------------- long lists of wide prompts
+
+MANY = [(11 * i) % 47 if i % 9 else 0 for i in range(290)] + [1, 300, 0, 129, 700]  # three launches, empty ones among them
+
+
+@pytest.mark.parametrize("dqk,dv", [(128, 128), (192, 64), (192, 128), (128, 64), (64, 128)])
+@pytest.mark.parametrize("Hq,H", [(2, 2), (8, 2), (5, 1)])
+def test_varlen_many_wide_sequences(dqk, dv, Hq, H):
+    """More sequences than a launch takes, where launches overlap and claim their tiles at run time."""
+    q, k, v, cu = packed(MANY, Hq, H, dqk, dv, 400, lead=2, tail=9)
+    for x in (q, k, v):
+        x[:2] = x[cu[-1]:] = float("nan")
+    check_varlen(q, k, v, cu)
+
+
+@pytest.mark.parametrize("dqk,dv,Hq,H", [(128, 128, 4, 1), (192, 128, 2, 2), (192, 64, 8, 2)])
+def test_varlen_wide_captured(dqk, dv, Hq, H):
+    """Replays find the claimed tiles' counters as the capture's launches did, between calls outside the graph too."""
+    q, k, v, cu = packed(MANY, Hq, H, dqk, dv, 410)
+    q, k, v = q.cuda(), k.cuda(), v.cuda()
+    ref, rl = slope.attn_varlen(q, k, v, cu)
+    out, lse = torch.zeros_like(ref), torch.zeros_like(rl)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(2):
+            slope.attn_varlen(q, k, v, cu, out=out, lse=lse)
+    for _ in range(3):
+        out.zero_()
+        lse.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref) and torch.equal(lse, rl)
+        again, al = slope.attn_varlen(q, k, v, cu)
+        assert torch.equal(again, ref) and torch.equal(al, rl)
