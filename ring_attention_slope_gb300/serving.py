@@ -233,20 +233,20 @@ class KV4Cache:
         nbytes = self._nbytes
         if data.dtype != torch.uint8 or not data.is_contiguous():
             raise TypeError("the cache's data must be a dense uint8 tensor")
-        room = min(data.numel(), data.untyped_storage().nbytes() - data.storage_offset())
+        storage, offset, device = data.untyped_storage(), data.storage_offset(), data.get_device()
+        room = min(data.numel(), storage.nbytes() - offset)
         if room < nbytes:
             raise ValueError(f"the cache needs {nbytes} bytes, data holds {room}")
-        if nbytes > 0 and not data.is_cuda:
+        if nbytes > 0 and device < 0:
             raise TypeError("the cache's data must be a CUDA tensor")
-        self._data, self._device, self._address = data, data.get_device() if nbytes else None, data.data_ptr()
-        self._end = data.storage_offset() + nbytes  # what its storage has to go on holding
+        self._data, self._device, self._address = data, device if nbytes else None, data.data_ptr()
+        self._storage, self._end = storage, offset + nbytes  # which has to go on holding as many bytes
         self._c = _pack_cache(self._address if nbytes else 0, *self._sizes)
 
     def device_now(self):
         """The current device, which the cache's data has to be on, wherever its memory now is."""
-        data = self._data
-        if data.data_ptr() != self._address or data.untyped_storage().nbytes() < self._end:
-            self.data = data  # moved or cut short in place: look it over again
+        if self._data.data_ptr() != self._address or self._storage.nbytes() < self._end:
+            self.data = self._data  # moved or cut short in place: look it over again
         dev = _device()
         if self._device != dev and self._device is not None:
             raise ValueError(f"cache on {self._data.device}, but the current device is cuda:{dev}")
@@ -303,11 +303,11 @@ def kv4_attn(q, cache, block_table, kv_lens, *, q_len=1, window=0, scale=0.0, ou
         if nbytes == 0:
             raise SlopeError(-8, "slope_kv4_attn_workspace_size")
         workspace = alloc((nbytes,), (1,), torch.uint8)
+    elif not workspace.is_contiguous():  # its bytes are counted, and used as one run
+        raise ValueError("the workspace must be a dense tensor")
     dev = cache.device_now()
     if workspace.get_device() != dev:
         raise ValueError(f"workspace on {workspace.device}, but the current device is cuda:{dev}")
-    if not workspace.is_contiguous():  # its bytes are counted, and used as one run
-        raise ValueError("the workspace must be a dense tensor")
     st = m.kv4_attn(q, cache._c, block_table, kv_lens, q_len, window, scale, out, lse, workspace.data_ptr(),
                     workspace.nbytes, _stream(stream, dev), dev)
     _check(st, "slope_kv4_attn")

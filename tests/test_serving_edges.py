@@ -97,8 +97,8 @@ class FakeData(Fake):
     """Bytes at an address."""
 
     def __init__(self, n, ptr, dtype=torch.uint8, cuda=True, dense=True):
-        super().__init__([n], dtype, ptr=ptr)
-        self.is_cuda, self.device, self.dense, self.held = cuda, "cuda:0", dense, n
+        super().__init__([n], dtype, ptr=ptr, device=0 if cuda else -1)
+        self.is_cuda, self.device, self.dense, self.held = cuda, "cuda:0" if cuda else "cpu", dense, n
 
     def is_contiguous(self):
         return self.dense
