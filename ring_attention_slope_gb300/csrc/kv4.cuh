@@ -18,11 +18,6 @@ __host__ __device__ constexpr int kv4_block_bytes(int dqk, int dv) {
   return kv4_key_bytes(dqk) + kv4_value_bytes(dv) + kKv4Block * 4 * kv4_words(dqk, dv);
 }
 
-// Byte offset of the 8 key codes of channels 32 * group + 8 * q .. + 7 of token t of the block.
-__host__ __device__ constexpr int kv4_key_offset(int dqk, int t, int group, int q) {
-  const int w = t / 8 * (dqk / kKv4Group) + group;
-  return ((w >> 2) * 32 + t % 8 * 4 + q) * 16 + (w & 3) * 4;
-}
 // Byte offset, in the value codes, of the word that holds channels 64 * chunk + 4 * g .. + 3 (low half) and
 // 64 * chunk + 32 + 4 * g .. + 3 (high half) of token t.
 __host__ __device__ constexpr int kv4_value_offset(int t, int chunk, int g) {
