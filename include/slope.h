@@ -23,7 +23,8 @@
  *  - Q is [Sq, Hq, dqk], K is [Skv, Hkv, dqk], V is [Skv, Hkv, dv], all bf16,
  *    token-major (batch 1).  Row and head strides of Q/K/V must be multiples
  *    of 8 elements (16 bytes) and the data pointer 16-byte aligned, because
- *    the kernels read them with the Tensor Memory Accelerator.
+ *    the kernels read them with the Tensor Memory Accelerator.  Strides and
+ *    pointers of a tensor without rows are not looked at.
  *  - Supported head sizes: dqk in {64, 128, 192} with dv in {64, 128}; other
  *    pairs return SLOPE_ERR_UNSUPPORTED.  dv = 192 is refused because the
  *    attention kernel keeps two 128-row query tiles per SM, each with a 128-

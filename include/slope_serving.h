@@ -16,9 +16,11 @@
  * The conventions of slope.h hold: device tensors as slope_tensor, statuses,
  * no allocation, no synchronisation, asynchronous on `stream`, argument errors
  * before any launch.  Host arrays are read during the call only.  All tensors
- * lie on the current device, and outputs overlap no input but where a call says so.  The kernels read device index arrays (positions,
- * slots, block tables, lengths) when they run; an index out of range there is
- * never followed, as each call says.
+ * lie on the current device, and outputs overlap no input but where a call says
+ * so.  Strides and pointers of a tensor without rows are not looked at.  The
+ * kernels read device index arrays (positions, slots, block tables, lengths)
+ * when they run; an index out of range there is never followed, as each call
+ * says.
  */
 #ifndef SLOPE_SERVING_H
 #define SLOPE_SERVING_H

@@ -47,7 +47,7 @@
 // sequence, whose rows are the queries and the keys, and a Q tile is 128 / 2^s tokens times 2^s query heads of one KV
 // group, as many as divide the group (at most 32), in (token, head) order.  A tile of 128 tokens of one head
 // would be mostly empty for short prompts and its diagonal half empty for all; 16 tokens of 8 heads fill
-// it: 40 prompts of 50 tokens, 64/8 heads of 64, take 24 us, 5 prompts of 670 to 5200 384 us (7% more with one
+// it: 40 prompts of 50 tokens, 64/8 heads of 64, take 25 us, 5 prompts of 694 to 5329 394 us (7% more with one
 // head to a tile), one of 12288 1.08 ms = 1140 TFLOP/s (as unpacked).  TMA boxes of 2^s heads load Q and store the
 // output; a box that holds rows past a sequence's end is stored row by row.  Bound as the unpacked kernel is, by the
 // exponentials and the steps' latency (tensor pipe 41% busy, MUFU 42%), and below 128 tokens by the work
@@ -356,7 +356,7 @@ __device__ __forceinline__ int first_tile() {
   return kDynamic ? 0 : static_cast<int>(blockIdx.x);
 }
 // A packed launch of one sequence, whose tiles are ordered by weight, goes forth and back over the CTAs, so that
-// none has the heaviest of every round (2000 tokens, 64/8 heads of 64: 53 -> 49 us; with several sequences
+// none has the heaviest of every round (2000 tokens, 64/8 heads of 64: 53 -> 50 us; with several sequences
 // it cost as much as it gained).
 template <bool kDynamic, bool PK>
 __device__ __forceinline__ int tile_stride(const AttnParams& p) {
@@ -1304,7 +1304,8 @@ cudaError_t launch_attn_partial(int dqk, int dv, const CUtensorMap& tq, const CU
 // step (1.2 to 4.5 on average), and few of them are half empty, and the CTAs get two rounds of them.  Measured, one
 // tile and two, 64/8 heads: 64 prompts of 128 tokens 61 and 66 us, 53 of 150 83 and 69, 26 of 300 105 and 79, 16 of
 // 500 112 and 90, 8 of 1000 136 and 123, 5 of 1400 129 and 131, 4 of 2000 176 and 183; 8/8 heads, 12 of 500 16
-// and 16.
+// and 16.  A window is not counted: up to kTwoTileMaxWindow it takes two tiles anyway, and a wider one cuts only
+// prompts that are far longer than those for which this says two.
 bool packed_two_tiles(const AttnParams& p) {
   const int64_t rows = kBlockM >> p.pack_shift, units = p.Hq >> p.pack_shift;
   int64_t tiles = 0, pairs = 0, steps = 0;

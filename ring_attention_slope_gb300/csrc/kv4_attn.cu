@@ -27,8 +27,9 @@
 // The block layout in memory is the operand layout, so a lane's codes of 16 keys
 // are its own 16-byte words; P^T needs one 8x8 transpose (movmatrix) a group.
 //
-// Measured at 64/8 heads of 64: 8 sequences of 102400 tokens 102 us = 5.1 TB/s of cache (75% of the copy rate); 32
-// ragged ones up to 32768 29.2 us; one of 65536 17 us; one of 1000 7.2 us.  (Around the groups' minimums
+// Measured at 64/8 heads of 64: 8 sequences of 102400 tokens 103 us = 5.1 TB/s of cache (75% of the copy rate); 32
+// ragged ones up to 32768 29.0 us; one of 65536 19 us; one of 1000 7.0 us; 8 of 16384 26 us with one query each, 35
+// with two and 80 with five (40 rows, three tiles, each of which reads the pages again).  (Around the groups' minimums
 // instead of their middles 3 to 4% less, with 2.4 times the error.)  At the first the ALU pipe is over half busy,
 // the issue slots over 60%, DRAM two thirds: a warp's step of 64 tokens is about as long in instructions as its codes
 // are on the way.  (The copies alone, without the arithmetic, took 84 us.)  The short ones are latency: the

@@ -8,11 +8,12 @@
 // where a run of tokens fills a block, the words of a block's sector come from
 // one warp and those of its neighbours from the same CTA.
 //
-// Measured, bf16: writing 5001 tokens, 32 heads of 192/128, 35 us = 3.8 TB/s, and reading them back 27 us = 5.0 TB/s
-// (56% and 73% of the copy rate); 12288 tokens, 8 heads of 64/64, 12 and 8 us; 32 tokens 2.6 us each, two
-// dependent loads and the launch.  What bounds the write is instructions as much as memory: at 32768 tokens
-// (25 us) the issue slots are 70% busy, the ALU pipe 60%, DRAM 32%.  (A lane with sixteen channels instead of eight
-// was no faster, one CTA for all heads of 16 tokens 13% slower.)
+// Measured, bf16: writing 5001 tokens, 32 heads of 192/128, 37 us = 3.7 TB/s, and reading them back 29 us = 4.6 TB/s
+// (54% and 67% of the copy rate); 12288 tokens, 8 heads of 64/64, 12.6 and 8.2 us (fp32 13.0 and 16.2); 32 tokens 2.8
+// and 2.2 us, two dependent loads and the launch.  What bounds the write is instructions as much as memory: at 32768
+// tokens (27 us) the issue slots are 71% busy, the ALU pipe 61%, DRAM 32%.  So it is for the read: at 32768 tokens
+// (15 us) the ALU pipe is 68% busy, the issue slots 59%, DRAM 24% (most of what it wrote was still in L2).  (A lane
+// with sixteen channels instead of eight was no faster, one CTA for all heads of 16 tokens 13% slower.)
 //
 // Rounding a quotient: with inv the scale's reciprocal to 2^-22 and q = d inv, the remainder d - q scale is
 // exact and q + remainder inv differs from d / scale by 2^-44 before its own rounding.  Where d = x - min is

@@ -11,10 +11,11 @@
 // of a lane, and stay in its registers as
 //   y_e = (x_e A_e + x_partner B_e) / rms,   A = w cos, B = -+ w_partner sin.
 //
-// Measured, bf16: 32768 tokens, 64/8 heads of 64, all rotated, 102 us = 5.9 TB/s (87% of the copy rate); 8191 tokens,
-// 128/128 heads of 192, 274 us = 5.9 TB/s; 16384 tokens, 32/8 heads of 128, 58 us.  With eight lanes to a head of
+// Measured, bf16: 32768 tokens, 64/8 heads of 64, all rotated, 101 us = 6.0 TB/s (88% of the copy rate); 8191 tokens,
+// 128/128 heads of 192, 273 us = 5.9 TB/s; 16384 tokens, 32/8 heads of 128, 58 us.  With eight lanes to a head of
 // any size, the other half fetched again or by shuffles, these took 118, 295 to 364 and 83 us; one group at
-// a time at the same registers 131 us; six CTAs an SM instead of four spill.  16 tokens: 2.7 us, which is the launch.
+// a time at the same registers 131 us; six CTAs an SM instead of four spill.  16 tokens: 2.9 us, which is the launch.
+// fp32, 16384 tokens, 64/8 heads of 64: 94 us = 6.4 TB/s; bf16 to fp32 73 us, fp32 to bf16 76 us.
 //
 // Angles: position * inv_freq loses everything in fp32 at far positions (at
 // position 10^6 an fp32 angle is off by 0.06 radians).  The frequency is kept as
@@ -340,8 +341,8 @@ void launch_one(const NormRopeParams& p, int64_t ctas, cudaStream_t stream) {
 }
 
 // bf16 heads of 64 and 128 channels loop where there are more tokens than the GPU holds warps: 32768 tokens of 64/8
-// heads of 64 take 102 us so and 107 with a CTA for every four tokens, 16000 of 8/1 19 and 20.  Heads of 192 have
-// no registers for it (291 and 274 us for 8191 tokens of 128/128), fp32 gains nothing, small calls lose 0.3 us.
+// heads of 64 take 101 us so and 107 with a CTA for every four tokens, 16000 of 8/1 19 and 20.  Heads of 192 have
+// no registers for it (291 and 273 us for 8191 tokens of 128/128), fp32 gains nothing, small calls lose 0.3 us.
 template <typename TI, typename TO, int D>
 cudaError_t launch_d(const NormRopeParams& p, int64_t ctas, cudaStream_t stream) {
   if constexpr (sizeof(TI) == 2 && D != 192) {
