@@ -15,7 +15,7 @@ import torch
 import ring_attention_slope_gb300 as slope
 from _lib import ROOT, built_lib
 from ring_attention_slope_gb300 import _build
-from test_serving_abi import BF16, F32, S_OK, cache, ref, t
+from test_serving_abi import F32, S_OK, cache, ref, t
 from test_serving_marshal import Fake
 
 BF = torch.bfloat16
@@ -53,7 +53,6 @@ def test_lse_strides_with_rows_are_still_checked(lib):
     for stride in ([0, 1], [3, 0], [-3, 1]):
         lse = t([8, 3], F32, stride=stride)
         assert lib.slope_attn_varlen(ref(q), ref(k), ref(k), cu, 1, 1, 0, 0.0, ref(q), ref(lse), None) == -4
-    assert BF16 == 0
 
 
 @pytest.mark.parametrize("stride", [[64, 0, 1], [0, 0, 0], [1, 7, 3]])
