@@ -22,6 +22,14 @@ and, around the prefill (``include/slope_serving.h``):
 * :class:`KV4Cache`, :func:`kv4_write`, :func:`kv4_read` - a paged key/value
   cache in 4 bits.
 * :func:`kv4_attn` - attention of each sequence's newest tokens over it.
+
+and, on a paged cache in 16 bits (``include/slope_kv.h``):
+
+* :class:`KVCache`, :func:`kv_write` - the cache and its store.
+* :func:`kv_attn` - attention of each sequence's newest tokens, one or a chunk
+  of a prompt, over its pages.
+* :func:`kv_attn_weights`, :func:`kv_evict` - the weight that each cached token
+  got from them, and eviction of the tokens that got least.
 """
 from __future__ import annotations
 
@@ -36,6 +44,8 @@ __all__ = [
     "cp_prefill_static_scratch", "dck_chunk_sizes",
     "Rope", "rope_inv_freq", "qk_norm_rope", "attn_varlen", "KV4Cache", "kv4_write", "kv4_read", "kv4_attn",
     "kv4_attn_workspace_size",
+    "KVCache", "kv_write", "kv_attn", "kv_attn_workspace_size", "kv_attn_weights", "kv_attn_weights_workspace_size",
+    "kv_evict", "kv_evict_workspace_size",
 ]
 
 LAYOUTS = {"contiguous": 0, "zigzag": 1, "chunked": 2, "ulysses": 3}
@@ -132,6 +142,7 @@ def load():
     lib.slope_cp_prefill_workspace_size_ex.argtypes = [i64, i64, i64, c_int, c_int, P(i64), ctypes.c_uint]
     lib.slope_cp_prefill_workspace_size_ex.restype = ctypes.c_size_t
     serving.declare(lib)
+    kv.declare(lib)
     _lib = lib
     return lib
 
@@ -447,5 +458,8 @@ def timeout_selftest(limit_ns: int, stream=None):
 
 
 from . import serving  # noqa: E402  (it uses the helpers above)
+from . import kv  # noqa: E402
+from .kv import (EXPORTED_KV, KVCache, SlopeKVBatch, SlopeKVCache, kv_attn, kv_attn_weights,  # noqa: E402, F401
+                 kv_attn_weights_workspace_size, kv_attn_workspace_size, kv_evict, kv_evict_workspace_size, kv_write)
 from .serving import (EXPORTED_SERVING, KV4Cache, Rope, SlopeKV4Cache, SlopeRope, attn_varlen,  # noqa: E402, F401
                       kv4_attn, kv4_attn_workspace_size, kv4_read, kv4_write, qk_norm_rope, rope_inv_freq)

@@ -23,9 +23,9 @@ LIB_PATH = os.path.join(PKG, "libslope.so")
 # named after the interpreter whose headers it is compiled with: another one finds none and builds its own
 MARSHAL_PATH = os.path.join(PKG, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
 
-SOURCES = ["attn_partial.cu", "kv4_attn.cu", "api.cu", "lse_merge.cu", "qk_norm_rope.cu", "kv4_store.cu", "status.cu",
-           "dck.cpp", "rope.cpp"]
-HEADERS = ["host.cuh", "kernels.cuh", "kv4.cuh", "sm103_ptx.cuh", "waits.cuh"]
+SOURCES = ["attn_partial.cu", "kv4_attn.cu", "api.cu", "lse_merge.cu", "qk_norm_rope.cu", "kv4_store.cu", "kv_attn.cu",
+           "kv_weights.cu", "kv_evict.cu", "kv_store.cu", "status.cu", "dck.cpp", "rope.cpp"]
+HEADERS = ["host.cuh", "kernels.cuh", "kv4.cuh", "kv_cache.cuh", "kv_cut.cuh", "sm103_ptx.cuh", "waits.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "-I", INCLUDE, "-I", CSRC]
@@ -88,10 +88,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
     The library needs nothing of Python.  Where the argument marshalling cannot be compiled (no ``Python.h``, say),
     the library is built all the same, with a warning; the calls that go through the marshalling then raise."""
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + _include("slope.h", "slope_serving.h") + [__file__]
+    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + _include("slope.h", "slope_serving.h", "slope_kv.h") + [__file__]
     if force or _stale(LIB_PATH, deps):
         _compile_library(verbose)
-    deps = [os.path.join(CSRC, "marshal.c")] + _include("slope.h", "slope_serving.h") + [__file__]
+    deps = [os.path.join(CSRC, "marshal.c")] + _include("slope.h", "slope_serving.h", "slope_kv.h") + [__file__]
     if force or _stale(MARSHAL_PATH, deps):
         try:
             _compile_marshal()

@@ -111,11 +111,11 @@ float resolve_scale(float scale, int64_t dqk) {
 
 }  // namespace slope
 
-namespace {
-
 // ---------------------------------------------------------------- TMA tensor maps
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+namespace slope {
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
     void* f = nullptr;
     cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
@@ -128,11 +128,15 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
+}  // namespace slope
+
+namespace {
+
 // 3-D view {d, H, S} of a bf16 [S, H, d] tensor; box = 64 columns x 1 head x 128 rows,
 // 128-byte swizzle (the layout the tcgen05 descriptors expect); out-of-range rows read 0.
 // With packed heads (Q of packed sequences) the box is 2^pack_shift heads x 128 >> pack_shift rows.
 bool make_map(CUtensorMap* m, const slope_tensor* t, int pack_shift = 0) {
-  auto enc = encode_fn();
+  auto enc = tensor_map_encoder();
   if (enc == nullptr) return false;
   std::memset(m, 0, sizeof(*m));
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(t->shape[2]), static_cast<cuuint64_t>(t->shape[1]),
@@ -152,7 +156,7 @@ bool make_map(CUtensorMap* m, const slope_tensor* t, int pack_shift = 0) {
 // Returns false if the map cannot be built (the kernel then stores directly).
 bool make_out_map(CUtensorMap* m, void* base, bool bf16, int64_t rows, int64_t H, int64_t dv, int64_t srow,
                   int64_t shead, int pack_shift = 0) {
-  auto enc = encode_fn();
+  auto enc = tensor_map_encoder();
   if (enc == nullptr || rows <= 0 || rows > 0x7fffffffLL) return false;
   const cuuint64_t esize = bf16 ? 2 : 4;
   if ((srow * esize) % 16 != 0 || (shead * esize) % 16 != 0 || !aligned(base, 16)) return false;

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 #include <nvtx3/nvToolsExt.h>
 
 #include <cstdint>
@@ -21,6 +22,9 @@ inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_
 slope_status check_lse(const slope_tensor* t, int64_t H, int64_t S);
 // [S, H, dv] output, fp32 (or bf16 when allowed); 16-byte vector stores.
 slope_status check_out(const slope_tensor* t, int64_t S, int64_t H, int64_t dv, bool allow_bf16);
+
+// The driver's encoder of TMA tensor maps (null if it cannot be found).
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 uint64_t wait_limit_ns();
 float resolve_scale(float scale, int64_t dqk);

@@ -1,0 +1,959 @@
+// Attention of each sequence's newest tokens over its pages of the 16-bit cache: single tokens (a decode step), chunks
+// of prompts, or both in one launch.
+//
+// out_i = sum_j 2^(x_ij - m_i) v_j / l_i, l_i = sum_j 2^(x_ij - m_i), x_ij = scale log2(e) q_i . k_j over the keys j that
+// token i sees, with a running maximum m and sum l; lse_i = (m_i + log2 l_i) ln 2.
+//
+// A Q tile is 128 rows: as many tokens as fit times all query heads of a KV head, token by token, so a key tile is
+// read once for the whole group and a chunk's diagonal wastes a few tokens' worth, whatever the group's size.  Q is
+// loaded by TMA boxes of {64 channels, heads, tokens}; a key tile of 128 positions by boxes of one page (or 128 of its
+// rows), each lane of the producer warp looking its pages up and starting its own boxes.  Pages that no row of the
+// tile needs, and pages out of range, are boxes past the tensor's end, which read 0 without touching memory.
+//
+// Roles as in the prefill's kernel (attn_partial.cu): S = Q K^T (tcgen05, both operands in shared memory) into TMEM,
+// one row per softmax thread, P back into TMEM, O += P V with P from TMEM.  With 64-wide heads two CTAs of one Q tile
+// share an SM; wider heads have one CTA with two Q tiles, which take the same key tiles.  Warps whose 32 rows are all empty
+// (a decode step has 8 rows, say) skip the softmax.
+//
+// The work: a pair is (sequence, KV head, row block), its steps the key tiles that its rows see.  The lengths are on the
+// device, so every CTA works out the same cut of the pairs into pieces of at most `per` steps (choose_per), and claims
+// pieces from a counter until none is left: long prefills take whole pairs (neighbours share a head's keys through
+// L2), decode steps of few sequences as many pieces as there are CTAs.  Pieces of a pair leave (m, l, O) in the workspace,
+// and a second launch, queued as a programmatic dependent, joins them in order; which CTA computes a piece changes no bit.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "kv_cut.cuh"
+#include "sm103_ptx.cuh"
+#include "waits.cuh"
+
+namespace slope {
+namespace {
+
+constexpr uint32_t kChunkBytes = 128 * 128;  // 128 rows x 64 bf16
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units: the running maximum moves when a score passes it by this
+constexpr int kPieceSteps = 5;             // what a piece's start and end cost, in steps
+constexpr int kHoles = 8;                  // ring of the steps' missing pages: more than the K tiles in flight
+constexpr int kJoinThreads = 512;
+
+// A pair of which several pieces are joined; one for each piece, `pieces` 0 but in the first's.
+struct KvPair {
+  int32_t row0, tokens, head0, heads, pieces, pad[3];
+};
+
+struct KvAttnParams {
+  KvSeqs seqs;
+  int32_t Hkv, group;
+  RowTile tile;
+  int32_t window;
+  float scale_log2;
+  void* out;
+  int64_t out_srow, out_shead;
+  int32_t out_bf16;
+  float* lse;  // may be null
+  int64_t lse_srow, lse_shead;
+  int32_t rows_cap;  // rows of a piece in the workspace
+  int32_t max_slots;
+  int32_t* n_slots;  // workspace: pieces that are joined
+  KvPair* pairs;     // workspace, for each of them
+  float2* ml;        // workspace: m and l of its rows
+  float* part;       // workspace: O of its rows, not normalised
+  int* status;
+  uint32_t* tile_counter;
+  uint64_t wait_limit_ns;
+};
+
+template <int DQK, int DV, int QT>
+struct Cfg {
+  static constexpr int kTmaWarp = 4 * QT, kMmaWarp = kTmaWarp + 1;
+  static constexpr int kThreads = 32 * (5 * QT + 1);
+  static constexpr int kCtas = QT == 2 ? 1 : 2;  // on an SM
+  static constexpr uint32_t kTmemCols = QT == 2 ? 512 : 256;
+  static constexpr int kQChunks = DQK / 64, kVChunks = DV / 64;
+  static constexpr int kQTileBytes = kQChunks * kChunkBytes;
+  static constexpr int kKTileBytes = kQTileBytes, kVTileBytes = kVChunks * kChunkBytes;
+  static constexpr int kSlotBytes = kKTileBytes > kVTileBytes ? kKTileBytes : kVTileBytes;
+  static constexpr int kSlots = (QT == 2 ? 131072 : 65536) / kSlotBytes;
+  static_assert(kSlots % 2 == 0 && kSlots / 2 + 2 <= kHoles, "K tiles in even slots, V tiles in odd ones");
+  static constexpr int kNumBars = 2 + 2 * kSlots + 6 * QT + 4 * QT + 4;
+  static constexpr int kSlotOffset = QT * kQTileBytes;
+  static constexpr int kBarOffset = kSlotOffset + kSlots * kSlotBytes;
+  static constexpr int kListOffset = kBarOffset + ((8 * kNumBars + 15) / 16) * 16;
+  static constexpr int kSmemBytes = 1024 + kListOffset + static_cast<int>(sizeof(CutLists));
+  static constexpr uint32_t kColO = QT * kBlockN, kColP = kColO + QT * DV;
+  static constexpr bool kSepP = kColP + QT * (kBlockN / 2) <= kTmemCols;
+  __device__ static constexpr uint32_t col_p(int t) { return kSepP ? kColP + t * (kBlockN / 2) : t * kBlockN; }
+  // Where P overwrites S (dv = 128) the two softmax warps of an SM sub-partition take turns on their exponentials.
+  static constexpr bool kTurns = QT == 2 && !kSepP;
+  static_assert(kSmemBytes <= (QT == 2 ? 232448 : 115712), "shared memory budget");
+  static_assert(kColO + QT * DV <= kTmemCols, "TMEM budget");
+};
+
+__device__ __forceinline__ bool warp_all(bool v) { return __all_sync(0xffffffffu, v); }
+
+// ---------------------------------------------------------------- the cut
+
+// A sequence's row blocks, and the steps of its longest one at most.
+struct RowCut {
+  int block_tokens, window;
+  __device__ __forceinline__ SeqCut operator()(const KvSeq& s) const {
+    SeqCut c;
+    c.blocks = (s.n + block_tokens - 1) / block_tokens;
+    c.steps = (s.len + kBlockN - 1) / kBlockN;
+    if (window > 0) c.steps = min(c.steps, (window + block_tokens - 2) / kBlockN + 2);
+    return c;
+  }
+};
+
+// A piece: steps [j0, j1) of a pair.
+struct Piece {
+  int32_t tokens;  // of the row block; -1: no pieces left
+  int32_t row0;    // q row of its first token
+  int32_t pos0;    // position of its first token
+  int32_t j0, j1;  // key tiles
+  int32_t len;     // tokens of the sequence
+  int32_t kvh, head0, heads;
+  int32_t slot;    // in the workspace; -1: the whole pair
+  int32_t b, pad;
+};
+
+__device__ __forceinline__ Piece make_piece(const KvAttnParams& p, int per, const CutLists& lists, uint32_t w,
+                                            const RowCut& cut_of, int& pieces, int& c) {
+  Piece r;
+  const int b = seq_of(lists, p.seqs.B, w), block_tokens = cut_of.block_tokens;
+  const KvSeq q = lists.seqs[b];
+  const SeqCut cut = cut_of(q);
+  pieces = pieces_of(cut.steps, per);
+  uint32_t local = w - lists.units[b];
+  const int blk = cut.blocks - 1 - static_cast<int>(local % cut.blocks);
+  local /= cut.blocks;
+  c = static_cast<int>(local % pieces);
+  const int h = static_cast<int>(local / pieces);
+  r.b = p.seqs.b0 + b;
+  r.kvh = h / p.tile.parts;
+  const int first = (h - r.kvh * p.tile.parts) * p.tile.heads;
+  r.head0 = r.kvh * p.group + first;
+  r.heads = min(p.tile.heads, p.group - first);
+  r.tokens = min(block_tokens, q.n - blk * block_tokens);
+  r.row0 = q.row0 + blk * block_tokens;
+  r.pos0 = q.len - q.n + blk * block_tokens;
+  r.len = q.len;
+  const int hi = min(q.len, r.pos0 + r.tokens);  // keys below this
+  const int lo = p.window > 0 ? max(0, r.pos0 - p.window + 1) : 0;
+  const int j_lo = lo / kBlockN, j_hi = max(j_lo, (max(hi, 0) + kBlockN - 1) / kBlockN);
+  const int steps = j_hi - j_lo;
+  r.j0 = j_lo + static_cast<int>(static_cast<int64_t>(steps) * c / pieces);
+  r.j1 = j_lo + static_cast<int>(static_cast<int64_t>(steps) * (c + 1) / pieces);
+  r.slot = pieces > 1 ? static_cast<int32_t>(lists.slots[b]) + (h * cut.blocks + blk) * pieces + c : -1;
+  r.pad = 0;
+  return r;
+}
+
+template <int DQK, int DV, int QT>
+__global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::kCtas)
+    kv_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ KvAttnParams p) {
+  using C = Cfg<DQK, DV, QT>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ CutScratch s_cut;
+  __shared__ Piece s_piece[2];
+  __shared__ uint32_t s_holes[kHoles];  // of a step's 16-token runs, those without a page
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* const sQ = smem;
+  uint8_t* const sSlot = smem + C::kSlotOffset;
+  uint64_t* const bar_q = reinterpret_cast<uint64_t*>(smem + C::kBarOffset);
+  uint64_t* const bar_qempty = bar_q + 1;
+  uint64_t* const bar_full = bar_q + 2;
+  uint64_t* const bar_empty = bar_full + C::kSlots;
+  uint64_t* const bar_s = bar_empty + C::kSlots;
+  uint64_t* const bar_sfree = bar_s + QT;  // softmax t has loaded S_t into registers
+  uint64_t* const bar_p = bar_sfree + QT;
+  uint64_t* const bar_o = bar_p + QT;
+  uint64_t* const bar_ofree = bar_o + QT;
+  uint64_t* const bar_drain = bar_ofree + QT;
+  uint64_t* const bar_turn = bar_drain + QT;     // [t * 4 + quarter]: that softmax warp may exponentiate
+  uint64_t* const bar_wfull = bar_turn + 4 * QT;  // a piece is there
+  uint64_t* const bar_wfree = bar_wfull + 2;      // every role is done with it
+  CutLists& lists = *reinterpret_cast<CutLists*>(smem + C::kListOffset);
+  volatile int* const cta_abort = &s_abort;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const RowCut cut_of{QT * p.tile.tokens, p.window};
+  const uint64_t limit = p.wait_limit_ns;
+
+  pdl_launch_dependents();  // the join may be scheduled as this grid's CTAs leave
+  uint32_t claimed = 0;     // the producer's first claim, on its way during the cut
+  if (threadIdx.x == C::kTmaWarp * 32) {
+    claimed = atomicAdd(p.tile_counter, 1u);
+    prefetch_tensormap(&tm_q);
+    prefetch_tensormap(&tm_k);
+    prefetch_tensormap(&tm_v);
+  }
+  if (threadIdx.x == 0) *cta_abort = *reinterpret_cast<volatile int*>(p.status) != 0 ? 1 : 0;
+  if (warp == C::kMmaWarp) {
+    tmem_alloc(&s_tmem, C::kTmemCols);
+    tmem_relinquish();
+  }
+  if (threadIdx.x == C::kMmaWarp * 32) {
+    mbar_init(bar_q, 1);
+    mbar_init(bar_qempty, QT);
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(&bar_full[i], 1);
+      mbar_init(&bar_empty[i], QT);  // one commit per MMA issuer
+    }
+    for (int t = 0; t < QT; ++t) {
+      mbar_init(&bar_s[t], 1);
+      mbar_init(&bar_sfree[t], 4);
+      mbar_init(&bar_p[t], 4);
+      mbar_init(&bar_o[t], 1);
+      mbar_init(&bar_ofree[t], 4);
+      mbar_init(&bar_drain[t], 1);
+      for (int q = 0; q < 4; ++q) mbar_init(&bar_turn[4 * t + q], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar_wfull[i], 1);
+      mbar_init(&bar_wfree[i], 5 * QT);  // the MMA issuers and the softmax warps
+    }
+    fence_barrier_init();
+  }
+  tc_fence_before_sync();
+  make_cut<kPieceSteps>(p.seqs, p.Hkv * p.tile.parts, cut_of, s_cut, lists);
+  tc_fence_after_sync();
+  const uint32_t tmem = s_tmem;
+
+  // The k-th piece of the CTA, once it is there; false if the wait ran out.
+  auto take_piece = [&](int k) -> bool { return wait_bounded(&bar_wfull[k & 1], (k >> 1) & 1, cta_abort, p.status, limit, 31); };
+
+  if (warp == C::kTmaWarp) {
+    // ================================================================ producer: pieces, pages, loads
+    if (lane == 0 && blockIdx.x == 0) *p.n_slots = static_cast<int32_t>(s_cut.slots);
+    const uint32_t total = s_cut.total;
+    const uint32_t q_bytes = static_cast<uint32_t>(p.tile.heads * p.tile.tokens) * 128 * C::kQChunks;
+    const int boxes_log = max(0, 7 - p.seqs.page_shift);  // log2 of the boxes of 64 channels of a key tile
+    const int boxes = 1 << boxes_log, box_rows = kBlockN >> boxes_log;
+    const int no_page = static_cast<int>(p.seqs.n_pages);  // reads 0
+    uint32_t w = __shfl_sync(0xffffffffu, claimed, 0);
+    uint32_t cnt = 0;   // K and V tiles loaded
+    uint32_t step = 0;  // steps loaded
+    int wt = 0;         // Q tiles loaded
+    bool ok = *cta_abort == 0;
+    for (int k = 0; ok; ++k) {
+      if (k >= 2) ok = warp_all(wait_bounded(&bar_wfree[k & 1], ((k >> 1) - 1) & 1, cta_abort, p.status, limit, 32));
+      if (!ok) break;
+      if (w >= total) {
+        if (lane == 0) {
+          s_piece[k & 1].tokens = -1;
+          mbar_arrive(&bar_wfull[k & 1]);
+        }
+        break;
+      }
+      uint32_t next = 0;
+      if (lane == 0) next = atomicAdd(p.tile_counter, 1u);  // on its way while this piece loads
+      int pieces, c;
+      const Piece pc = make_piece(p, s_cut.per, lists, w, cut_of, pieces, c);
+      if (lane == 0) {
+        s_piece[k & 1] = pc;
+        mbar_arrive(&bar_wfull[k & 1]);
+        if (pc.slot >= 0) {
+          KvPair e;
+          e.row0 = pc.row0, e.tokens = pc.tokens, e.head0 = pc.head0, e.heads = pc.heads;
+          e.pieces = c == 0 ? pieces : 0;
+          e.pad[0] = e.pad[1] = e.pad[2] = 0;
+          p.pairs[pc.slot] = e;
+        }
+      }
+      if (pc.j1 > pc.j0) {
+        // ---- pages: entry e0 + lane of the table in each lane, and the 32 after them on their way
+        const int lo = p.window > 0 ? max(0, pc.pos0 - p.window + 1) : 0;  // positions [lo, hi) that some row sees
+        const int hi = min(pc.len, pc.pos0 + pc.tokens);
+        const int32_t* const row = p.seqs.table + pc.b * p.seqs.table_stride;
+        const int shift = p.seqs.page_shift;
+        auto page_of = [&](int e) -> int {  // -1: a page out of range where one is needed
+          const int64_t first = static_cast<int64_t>(e) << shift;
+          if (first >= hi || first + (int64_t(1) << shift) <= lo) return no_page;
+          const int pg = row[e];
+          return pg >= 0 && pg < no_page ? pg : -1;
+        };
+        int e0 = (pc.j0 * kBlockN) >> shift;
+        int page = page_of(e0 + lane), ahead = page_of(e0 + 32 + lane);
+
+        const int nt = QT == 2 && pc.tokens > p.tile.tokens ? 2 : 1;
+        // Q of the previous piece is in use until its last S MMAs are done
+        if (wt > 0) ok = warp_all(wait_bounded(bar_qempty, (wt - 1) & 1, cta_abort, p.status, limit, 33));
+        if (ok) {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar_q, nt * q_bytes);
+            for (int t = 0; t < nt; ++t)
+              for (int ch = 0; ch < C::kQChunks; ++ch)
+                tma_load_3d(sQ + t * C::kQTileBytes + ch * kChunkBytes, &tm_q, bar_q, 64 * ch, pc.head0,
+                            pc.row0 + t * p.tile.tokens);
+          }
+          ++wt;
+        }
+        for (int j = pc.j0; ok && j < pc.j1; ++j, ++step) {
+          const int e = (j * kBlockN) >> shift;
+          if (e >= e0 + 32) {
+            e0 += 32;
+            page = ahead;
+            ahead = page_of(e0 + 32 + lane);
+          }
+          // lane i loads box i % boxes of channel chunk i / boxes
+          const int mine = __shfl_sync(0xffffffffu, page, (e - e0) + (lane & (boxes - 1)));
+          const uint32_t missing = __ballot_sync(0xffffffffu, mine < 0) & ((1u << boxes) - 1);
+          const int pg = mine < 0 ? no_page : mine;
+          const int in_page = boxes_log > 0 ? 0 : (j * kBlockN) & ((1 << shift) - 1);
+          const int chunk = lane >> boxes_log;
+          const uint32_t at = static_cast<uint32_t>(chunk) * kChunkBytes + (lane & (boxes - 1)) * box_rows * 128;
+          for (int kv = 0; kv < 2 && ok; ++kv) {
+            const uint32_t slot = cnt % C::kSlots, ph = (cnt / C::kSlots) & 1;
+            ok = warp_all(wait_bounded(&bar_empty[slot], ph ^ 1, cta_abort, p.status, limit, 34 + kv));
+            if (!ok) break;
+            if (lane == 0) {
+              if (kv == 0) {  // bit i: positions 16 i .. 16 i + 15 of the tile have no page
+                uint32_t m = 0;
+                for (int i = 0; missing != 0 && i < 8; ++i) m |= ((missing >> ((i << boxes_log) >> 3)) & 1u) << i;
+                s_holes[step % kHoles] = m;
+              }
+              mbar_arrive_expect_tx(&bar_full[slot], kv == 0 ? C::kKTileBytes : C::kVTileBytes);
+            }
+            __syncwarp();
+            if (chunk < (kv == 0 ? C::kQChunks : C::kVChunks))
+              tma_load_4d(sSlot + slot * C::kSlotBytes + at, kv == 0 ? &tm_k : &tm_v, &bar_full[slot], 64 * chunk, in_page,
+                          pc.kvh, pg);
+            ++cnt;
+          }
+        }
+      }
+      w = __shfl_sync(0xffffffffu, next, 0);
+    }
+    if (lane == 0) {
+      release_pieces(p.tile_counter, total, w);
+      if (!ok) {
+        // let the loads already issued land before the CTA gives up its shared memory
+        if (wt > 0) wait_final(bar_q, (wt - 1) & 1, limit);
+        for (uint32_t i = 0; i < C::kSlots && i < cnt; ++i) {
+          const uint32_t last = i + ((cnt - 1 - i) / C::kSlots) * C::kSlots;
+          wait_final(&bar_full[i], (last / C::kSlots) & 1, limit);
+        }
+      }
+    }
+  } else if (warp >= C::kMmaWarp) {
+    // ================================================================ MMA issuers, one for each Q tile
+    // Per step j issuer t issues S_t(j) = Q_t K(j)^T and then, with P in columns of its own, O_t += P_t(j-1) V(j-1); with
+    // P over S_t, O_t += P_t(j) V(j) once softmax t has written P_t(j).  Every issuer commits once per K and V tile and per
+    // piece, whether or not its Q tile has rows.
+    if (lane == 0) {
+      const int t = warp - C::kMmaWarp;
+      constexpr uint32_t idesc_qk = idesc_bf16_f32(kBlockM, kBlockN, 0, 0);
+      constexpr uint32_t idesc_pv = idesc_bf16_f32(kBlockM, DV, 0, 1);
+      constexpr uint32_t kDescHi = smem_desc_hi(1024, kSwizzle128B);
+      const uint32_t qlo = smem_desc_lo(smem_u32(sQ + t * C::kQTileBytes), 16);
+      const uint32_t d_s = tmem + t * kBlockN, d_o = tmem + C::kColO + t * DV, a_p = tmem + C::col_p(t);
+      uint32_t cnt = 0;
+      int n = 0;    // S MMAs issued for this Q tile
+      int pvw = 0;  // pieces whose first PV into O_t has been issued
+      int wt = 0;   // Q tiles waited for
+      bool pend = false, pend_first = false;  // the previous step's PV is due
+      uint32_t pend_vslot = 0, pend_vph = 0;
+
+      auto issue_qk = [&](uint32_t kslot) {
+        const uint32_t klo = smem_desc_lo(smem_u32(sSlot + kslot * C::kSlotBytes), 16);
+#pragma unroll
+        for (int kk = 0; kk < DQK / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * kChunkBytes + (kk & 3) * 32) >> 4;
+          mma_ss_lh(d_s, qlo + off, kDescHi, klo + off, kDescHi, idesc_qk, kk > 0 ? 1u : 0u);
+        }
+        mma_commit(&bar_s[t]);
+      };
+      // The first PV of a piece overwrites O_t: it waits until the epilogue of the one before has read it.
+      auto issue_pv = [&](uint32_t vslot, bool first) -> bool {
+        if (first) {
+          if (pvw > 0) {
+            if (!wait_bounded(&bar_ofree[t], (pvw - 1) & 1, cta_abort, p.status, limit, 36)) return false;
+            tc_fence_after_sync();
+          }
+          ++pvw;
+        }
+        const uint32_t vlo = smem_desc_lo(smem_u32(sSlot + vslot * C::kSlotBytes), kChunkBytes);
+#pragma unroll
+        for (int kk = 0; kk < kBlockN / 16; ++kk)
+          mma_ts_lh(d_o, a_p + kk * 8, vlo + ((kk * 2048) >> 4), kDescHi, idesc_pv, (!first || kk > 0) ? 1u : 0u);
+        mma_commit(&bar_o[t]);
+        return true;
+      };
+      // The pending step's PV, and its V slot's release.  (An issuer waits for every fill it releases, used or not, so
+      // that it never commits for a later fill of a slot before the other issuer has released the earlier one.)
+      auto flush = [&](bool part) -> bool {
+        if (!pend) return true;
+        if (!wait_bounded(&bar_full[pend_vslot], pend_vph, cta_abort, p.status, limit, 37)) return false;
+        if (part) {
+          if (!wait_bounded(&bar_p[t], (n - 1) & 1, cta_abort, p.status, limit, 38)) return false;
+          tc_fence_after_sync();
+          if (!issue_pv(pend_vslot, pend_first)) return false;
+        }
+        mma_commit(&bar_empty[pend_vslot]);
+        pend = false;
+        return true;
+      };
+
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        if (!take_piece(k)) break;
+        const volatile Piece& pc = s_piece[k & 1];
+        const int tokens = pc.tokens, j0 = pc.j0, j1 = pc.j1, len = pc.len;
+        mbar_arrive(&bar_wfree[k & 1]);
+        if (tokens < 0) break;
+        if (j1 <= j0) continue;
+        const bool part = t == 0 || tokens > p.tile.tokens;
+        if (!wait_bounded(bar_q, wt & 1, cta_abort, p.status, limit, 39)) break;
+        ++wt;
+        tc_fence_after_sync();
+        bool first = true;
+        for (int j = j0; ok && j < j1; ++j) {
+          const uint32_t kslot = cnt % C::kSlots, kph = (cnt / C::kSlots) & 1;
+          const uint32_t vslot = (cnt + 1) % C::kSlots, vph = ((cnt + 1) / C::kSlots) & 1;
+          cnt += 2;
+          ok = wait_bounded(&bar_full[kslot], kph, cta_abort, p.status, limit, 40);
+          if (!ok) break;
+          // With S_t the softmax clears the end of this step's V slot, and has to find the slot's previous fill gone:
+          // of two slots, that is the V whose PV is pending.
+          if (C::kSepP && C::kSlots == 2 && (j + 1) * kBlockN > len) ok = flush(part);
+          if (ok && part) {
+            // S_t is free once softmax t has loaded it into registers, or, with P over it, once the PV has read P
+            if (n > 0) ok = wait_bounded(C::kSepP ? &bar_sfree[t] : &bar_o[t], (n - 1) & 1, cta_abort, p.status, limit, 41);
+            if (ok) {
+              tc_fence_after_sync();
+              issue_qk(kslot);
+            }
+          }
+          if (!ok) break;
+          mma_commit(&bar_empty[kslot]);
+          if (C::kSepP) {
+            ok = flush(part);
+            if (!ok) break;
+            pend = true;
+            pend_first = first;
+            pend_vslot = vslot;
+            pend_vph = vph;
+            if (part) ++n;
+          } else {
+            ok = wait_bounded(&bar_full[vslot], vph, cta_abort, p.status, limit, 42);
+            if (ok && part) {
+              ok = wait_bounded(&bar_p[t], n & 1, cta_abort, p.status, limit, 43);
+              if (ok) {
+                tc_fence_after_sync();
+                ok = issue_pv(vslot, first);
+              }
+              ++n;
+            }
+            if (!ok) break;
+            mma_commit(&bar_empty[vslot]);
+          }
+          first = false;
+        }
+        mma_commit(bar_qempty);  // this issuer's S MMAs of the piece are issued
+        if (ok && C::kSepP) ok = flush(part);  // the last PV goes out now: the epilogue waits for it
+      }
+      // every MMA of this issuer, and the arrivals that its commits make, completes before the CTA leaves
+      mma_commit(&bar_drain[t]);
+      wait_final(&bar_drain[t], 0, limit);
+    }
+  } else {
+    // ================================================================ softmax and epilogue, a row to a thread
+    const int t = QT == 2 ? warp >> 2 : 0;
+    const int wq = warp & 3;
+    const int row = wq * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t tS = tmem + lane_base + t * kBlockN;
+    const uint32_t tP = tmem + lane_base + C::col_p(t);
+    const uint32_t tO = tmem + lane_base + C::kColO + t * DV;
+    const int my_token = row / p.tile.heads;  // in the tile (p.tile.tokens and on: none)
+    const int my_head = row - my_token * p.tile.heads;
+    const int warp_token = (wq * 32) / p.tile.heads;  // the warp's first
+    const float sl2 = p.scale_log2;
+    // Turn k of tile 0 waits for tile 1's turn k - 1, turn k of tile 1 for tile 0's turn k; both take one turn a step of
+    // the pieces that have rows in both tiles.
+    int turn = 0;
+    auto take_turn = [&]() -> bool {
+      if (t == 0 && turn == 0) return true;
+      const uint32_t par = static_cast<uint32_t>(t == 0 ? turn - 1 : turn) & 1u;
+      return warp_all(wait_bounded(&bar_turn[t * 4 + wq], par, cta_abort, p.status, limit, 44));
+    };
+    auto pass_turn = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar_turn[(t ^ 1) * 4 + wq]);
+      ++turn;
+    };
+    auto arrive = [&](uint64_t* bar) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    int n = 0;               // steps of this Q tile
+    uint32_t cta_steps = 0;  // steps of the CTA before this piece
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      if (!warp_all(take_piece(k))) break;
+      const volatile Piece& pc = s_piece[k & 1];
+      const int tokens = pc.tokens, pos0 = pc.pos0, j0 = pc.j0, j1 = pc.j1, len = pc.len;
+      if (tokens < 0) break;
+      const int rows_t = min(tokens - t * p.tile.tokens, p.tile.tokens);  // tokens of this Q tile
+      if (rows_t <= 0) {
+        cta_steps += static_cast<uint32_t>(j1 - j0);
+        arrive(&bar_wfree[k & 1]);
+        continue;
+      }
+      const bool turns = C::kTurns && tokens > p.tile.tokens;
+      const bool idle = warp_token >= rows_t;  // none of the warp's rows exists
+      const int qa = pos0 + t * p.tile.tokens, qb = qa + rows_t - 1;
+      const int q_pos = qa + my_token;
+      float m_used = -INFINITY;  // running maximum, log2 units
+      float l = 0.f;             // running sum of exp2(s * sl2 - m_used)
+      for (int j = j0; ok && j < j1; ++j, ++n, ++cta_steps) {
+        const int kpos = j * kBlockN, valid = len - kpos;
+        ok = warp_all(wait_bounded(&bar_s[t], n & 1, cta_abort, p.status, limit, 45));
+        if (!ok) break;
+        if (valid < kBlockN) {
+          // The sequence ends inside this tile.  The V rows behind it have a weight of 0, but 0 times a NaN there would
+          // still be NaN: clear them before this Q tile's PV may read them.  S_t is there, so the issuer has waited for
+          // every earlier fill of the slot, and the parity can only mean this one.
+          const uint32_t vcnt = 2 * cta_steps + 1, vslot = vcnt % C::kSlots;
+          ok = warp_all(wait_bounded(&bar_full[vslot], (vcnt / C::kSlots) & 1, cta_abort, p.status, limit, 46));
+          if (!ok) break;
+          uint8_t* const sv0 = sSlot + vslot * C::kSlotBytes;
+          for (int c = 0; c < C::kVChunks; ++c)
+            for (int off = valid * 128 + row * 16; off < static_cast<int>(kChunkBytes); off += 128 * 16)
+              *reinterpret_cast<uint4*>(sv0 + c * kChunkBytes + off) = make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async_shared();
+        }
+        if (idle) {
+          if (C::kSepP) {
+            arrive(&bar_sfree[t]);
+            // not before the others can be done with the step before
+            if (n > 0) ok = warp_all(wait_bounded(&bar_o[t], (n - 1) & 1, cta_abort, p.status, limit, 47));
+          }
+          if (ok && turns) {
+            ok = take_turn();
+            if (ok) pass_turn();
+          }
+          if (!ok) break;
+          arrive(&bar_p[t]);
+          continue;
+        }
+        const uint32_t holes = *const_cast<volatile uint32_t*>(&s_holes[cta_steps % kHoles]);
+        tc_fence_after_sync();
+        uint32_t r0[32], r1[32], r2[32], r3[32];
+        float q0 = tmem_ld32_max(tS + 0, r0);
+        float q1 = tmem_ld32_max(tS + 32, r1);
+        float q2 = tmem_ld32_max(tS + 64, r2);
+        float q3 = tmem_ld32_max(tS + 96, r3);
+        tmem_ld_wait();
+        reg_fence(r0);
+        reg_fence(r1);
+        reg_fence(r2);
+        reg_fence(r3);
+        reg_fence(q0);
+        reg_fence(q1);
+        reg_fence(q2);
+        reg_fence(q3);
+        float sv[128];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          sv[i] = __uint_as_float(r0[i]);
+          sv[32 + i] = __uint_as_float(r1[i]);
+          sv[64 + i] = __uint_as_float(r2[i]);
+          sv[96 + i] = __uint_as_float(r3[i]);
+        }
+        float mx = fmax3(q0, q1, fmaxf(q2, q3));
+        const bool full = valid >= kBlockN && kpos + kBlockN - 1 <= qa && (p.window == 0 || qb - kpos < p.window) && holes == 0;
+        if (!full) {
+          // the row's visible columns are one interval, less the missing pages
+          int lo = p.window > 0 ? max(0, q_pos - kpos - p.window + 1) : 0;
+          int hi = min(valid - 1, q_pos - kpos);
+          if (hi < lo) lo = hi = kBlockN;  // none: every c - lo is negative
+          const uint32_t span = static_cast<uint32_t>(hi - lo);
+#pragma unroll
+          for (int c = 0; c < kBlockN; ++c)
+            if (static_cast<uint32_t>(c - lo) > span) sv[c] = -INFINITY;
+          if (holes != 0) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if ((holes >> i) & 1u)
+#pragma unroll
+                for (int c = 0; c < 16; ++c) sv[16 * i + c] = -INFINITY;
+          }
+          float qm[4] = {q0, q1, q2, q3};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool all_vis = lo <= 32 * i && 32 * i + 31 <= hi && ((holes >> (2 * i)) & 3u) == 0;
+            const bool none_vis = hi < 32 * i || lo > 32 * i + 31;
+            if (__any_sync(0xffffffffu, !all_vis && !none_vis)) {
+              float a = fmax3(sv[32 * i], sv[32 * i + 1], sv[32 * i + 2]);
+              float b = fmax3(sv[32 * i + 3], sv[32 * i + 4], sv[32 * i + 5]);
+#pragma unroll
+              for (int c = 6; c < 30; c += 4) {
+                a = fmax3(a, sv[32 * i + c], sv[32 * i + c + 1]);
+                b = fmax3(b, sv[32 * i + c + 2], sv[32 * i + c + 3]);
+              }
+              qm[i] = fmax3(a, b, fmaxf(sv[32 * i + 30], sv[32 * i + 31]));
+            } else {
+              qm[i] = all_vis ? qm[i] : -INFINITY;
+            }
+          }
+          mx = fmax3(qm[0], qm[1], fmaxf(qm[2], qm[3]));
+        }
+        const float m_new = mx * sl2;
+        const bool need = m_new > m_used + kRescaleThreshold;
+        const float alpha = need ? ex2_approx(m_used - m_new) : 1.f;
+        m_used = need ? m_new : m_used;
+        l *= alpha;
+        const float msub = (m_used == -INFINITY) ? 0.f : m_used;
+        if (turns) {
+          ok = take_turn();
+          if (!ok) break;
+        }
+        // p = exp2(s * sl2 - m), packed to bf16 pairs; the row's sum in fp32 before that rounding
+        const uint64_t sl2v = pack_f32x2(sl2, sl2), negm = pack_f32x2(-msub, -msub);
+        uint64_t acc[4] = {0, 0, 0, 0};
+        uint32_t pk[64];
+#pragma unroll
+        for (int i = 0; i < 64; ++i) {
+          pk[i] = softmax_pair(sv[2 * i], sv[2 * i + 1], sl2v, negm, acc[i & 3]);
+          if (C::kSepP && i == 15) {  // S_t is in registers: the next S MMA may overwrite it
+            tc_fence_before_sync();
+            arrive(&bar_sfree[t]);
+          }
+          if ((i & 15) == 15) {
+            const int c = i >> 4;
+            if constexpr (!C::kSepP) {
+              tmem_st16(tP + c * 16, *reinterpret_cast<const uint32_t(*)[16]>(&pk[16 * c]));
+            } else if (c == 2) {
+              if (n > 0) {  // the previous PV has read P
+                ok = warp_all(wait_bounded(&bar_o[t], (n - 1) & 1, cta_abort, p.status, limit, 48));
+                if (!ok) break;
+                tc_fence_after_sync();
+              }
+#pragma unroll
+              for (int cc = 0; cc < 3; ++cc)
+                tmem_st16(tP + cc * 16, *reinterpret_cast<const uint32_t(*)[16]>(&pk[16 * cc]));
+            } else if (c == 3) {
+              tmem_st16(tP + 48, *reinterpret_cast<const uint32_t(*)[16]>(&pk[48]));
+            }
+          }
+        }
+        if (!ok) break;
+        const float2 c0 = unpack_f32x2(acc[0]), c1 = unpack_f32x2(acc[1]);
+        const float2 c2 = unpack_f32x2(acc[2]), c3 = unpack_f32x2(acc[3]);
+        l += ((c0.x + c0.y) + (c1.x + c1.y)) + ((c2.x + c2.y) + (c3.x + c3.y));
+        if (turns) pass_turn();
+        // O_t holds the previous PV's result (P's columns, or the issuer's wait before S_t, say that it is done)
+        if (__any_sync(0xffffffffu, need) && j > j0) {
+#pragma unroll 1
+          for (int c = 0; c < DV / 16; ++c) {
+            uint32_t o[16];
+            tmem_ld16(tO + c * 16, o);
+            tmem_ld_wait();
+            reg_fence(o);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st16(tO + c * 16, o);
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before_sync();
+        arrive(&bar_p[t]);
+      }
+      if (!ok) break;
+
+      // ---- epilogue
+      const bool steps = j1 > j0;
+      const int slot = pc.slot, head0 = pc.head0;
+      const bool valid_row = my_token < rows_t && my_token < p.tile.tokens && my_head < pc.heads;
+      const int64_t tok = static_cast<int64_t>(pc.row0) + t * p.tile.tokens + my_token;
+      arrive(&bar_wfree[k & 1]);
+      if (steps) {
+        ok = warp_all(wait_bounded(&bar_o[t], (n - 1) & 1, cta_abort, p.status, limit, 49));
+        if (!ok) break;
+        tc_fence_after_sync();
+      }
+      const float inv = slot < 0 ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+      const int64_t at = tok * p.out_srow + static_cast<int64_t>(head0 + my_head) * p.out_shead;
+      const int64_t prow = static_cast<int64_t>(slot) * p.rows_cap + t * p.tile.tokens * p.tile.heads + row;
+      if (valid_row) {
+        if (slot >= 0)
+          p.ml[prow] = make_float2(m_used, l);
+        else if (p.lse != nullptr)
+          p.lse[tok * p.lse_srow + static_cast<int64_t>(head0 + my_head) * p.lse_shead] =
+              l > 0.f ? (m_used + lg2_approx(l)) * kLn2 : l == 0.f ? -INFINITY : l;
+      }
+      const bool nan_row = !(l >= 0.f);  // its output is NaN
+#pragma unroll 1
+      for (int c = 0; c < DV / 32; ++c) {
+        uint32_t o[32];
+        if (steps && !idle) {
+          tmem_ld32(tO + c * 32, o);
+          tmem_ld_wait();
+          reg_fence(o);
+        }
+        if (c == DV / 32 - 1 && steps) {  // O_t is read
+          tc_fence_before_sync();
+          arrive(&bar_ofree[t]);
+        }
+        if (!valid_row) continue;
+        const bool none = !steps || l == 0.f;
+        float f[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) f[i] = none ? 0.f : nan_row ? l : __uint_as_float(o[i]) * inv;
+        if (slot >= 0) {
+          float4* const dst = reinterpret_cast<float4*>(p.part + prow * DV + c * 32);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dst[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+        } else if (p.out_bf16) {
+          uint4* const dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at + c * 32);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            dst[i] = make_uint4(pack_bf16x2(f[8 * i], f[8 * i + 1]), pack_bf16x2(f[8 * i + 2], f[8 * i + 3]),
+                                pack_bf16x2(f[8 * i + 4], f[8 * i + 5]), pack_bf16x2(f[8 * i + 6], f[8 * i + 7]));
+        } else {
+          float4* const dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at + c * 32);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dst[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+        }
+      }
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == C::kMmaWarp) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// Joins the pieces of the pairs that were cut, in their order.  A work item is 128 lanes, four channels each, of one pair;
+// the CTA's four groups of 128 threads take every fourth piece, four of them in flight, and join at the end.
+template <int DV>
+__global__ void __launch_bounds__(kJoinThreads) kv_attn_join_kernel(const __grid_constant__ KvAttnParams p) {
+  constexpr int kGroups = kJoinThreads / 128, kAhead = 4;
+  __shared__ float s_m[kGroups][128], s_l[kGroups][128];
+  __shared__ float4 s_v[kGroups][128];
+  pdl_wait();
+  if (*reinterpret_cast<volatile int*>(p.status) != 0) return;  // pieces may be missing
+  const int n_slots = min(*p.n_slots, p.max_slots);
+  const int chunks = (p.rows_cap * (DV / 4) + 127) / 128;
+  const int grp = threadIdx.x >> 7, lane = threadIdx.x & 127;
+  for (int64_t item = blockIdx.x; item < static_cast<int64_t>(n_slots) * chunks; item += gridDim.x) {
+    const int slot = static_cast<int>(item / chunks), i = static_cast<int>(item - static_cast<int64_t>(slot) * chunks) * 128 + lane;
+    const KvPair e = p.pairs[slot];
+    const int rows = e.tokens * p.tile.heads;
+    if (e.pieces <= 0 || slot + e.pieces > n_slots || e.row0 < 0 || e.row0 + e.tokens > p.seqs.T || rows > p.rows_cap) continue;
+    if ((i - lane) / (DV / 4) >= rows) continue;  // the same for every thread
+    const int rr = min(i / (DV / 4), rows - 1), ch = (i % (DV / 4)) * 4;
+    float mm = -INFINITY, ll = 0.f;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    // a piece whose row saw nothing has m = -inf and l = 0, and a NaN anywhere stays one
+    auto add = [&](float m, float l, float4 v, float to) {
+      const float f = m == -INFINITY ? 0.f : ex2_approx(m - to);
+      ll = fmaf(f, l, ll);
+      sum.x = fmaf(f, v.x, sum.x), sum.y = fmaf(f, v.y, sum.y);
+      sum.z = fmaf(f, v.z, sum.z), sum.w = fmaf(f, v.w, sum.w);
+    };
+    auto move = [&](float to) {
+      const float alpha = mm == -INFINITY ? 1.f : ex2_approx(mm - to);
+      mm = to;
+      ll *= alpha;
+      sum.x *= alpha, sum.y *= alpha, sum.z *= alpha, sum.w *= alpha;
+    };
+    for (int c0 = grp; c0 < e.pieces; c0 += kAhead * kGroups) {
+      float2 ml[kAhead];
+      float4 v[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int64_t prow = static_cast<int64_t>(slot + min(c0 + k * kGroups, e.pieces - 1)) * p.rows_cap + rr;
+        ml[k] = p.ml[prow];
+        v[k] = *reinterpret_cast<const float4*>(p.part + prow * DV + ch);
+      }
+      float now = mm;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) now = fmaxf(now, ml[k].x);
+      move(now);
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (c0 + k * kGroups < e.pieces) add(ml[k].x, ml[k].y, v[k], now);
+    }
+    __syncthreads();
+    s_m[grp][lane] = mm, s_l[grp][lane] = ll, s_v[grp][lane] = sum;
+    __syncthreads();
+    if (grp != 0) continue;
+    float now = mm;
+#pragma unroll
+    for (int g = 1; g < kGroups; ++g) now = fmaxf(now, s_m[g][lane]);
+    move(now);
+#pragma unroll
+    for (int g = 1; g < kGroups; ++g) add(s_m[g][lane], s_l[g][lane], s_v[g][lane], now);
+    const int token = rr / p.tile.heads, head = rr - token * p.tile.heads;
+    if (i / (DV / 4) >= rows || head >= e.heads) continue;
+    const int64_t tok = static_cast<int64_t>(e.row0) + token, h = e.head0 + head;
+    const float inv = ll == 0.f ? 0.f : 1.f / ll;
+    const int64_t at = tok * p.out_srow + h * p.out_shead + ch;
+    if (p.out_bf16)
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
+          make_uint2(pack_bf16x2(sum.x * inv, sum.y * inv), pack_bf16x2(sum.z * inv, sum.w * inv));
+    else
+      *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) =
+          make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
+    if (ch == 0 && p.lse != nullptr)
+      p.lse[tok * p.lse_srow + h * p.lse_shead] = ll == 0.f ? -INFINITY : (mm + lg2_approx(ll)) * kLn2;
+  }
+}
+
+// ---------------------------------------------------------------- launches
+
+// CTAs of a grid that fills the current device.
+int grid_of(int dqk, int dv) { return kv_sm_count() * (dqk == 64 && dv == 64 ? 2 : 1); }
+
+struct Workspace {
+  int64_t rows_cap, max_slots;
+  size_t pairs, ml, part, total;  // offsets
+};
+Workspace workspace_of(int64_t T, int64_t group, int dqk, int dv, int32_t q_len) {
+  const RowTile tile = row_tile(group);
+  const int64_t tiles = dqk == 64 && dv == 64 ? 1 : 2;
+  const int64_t most = std::max<int64_t>(1, q_len > 0 ? q_len : T);  // new tokens of a sequence
+  Workspace w;
+  w.rows_cap = std::min<int64_t>(tiles * tile.tokens, most) * tile.heads;
+  w.max_slots = 4LL * grid_of(dqk, dv) + 8;
+  auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+  w.pairs = 256;
+  w.ml = w.pairs + up(w.max_slots * sizeof(KvPair));
+  w.part = w.ml + up(w.max_slots * w.rows_cap * sizeof(float2));
+  w.total = w.part + up(w.max_slots * w.rows_cap * dv * sizeof(float));
+  return w;
+}
+
+template <int DQK, int DV, int QT>
+cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, KvAttnParams p, int grid,
+                   cudaStream_t stream) {
+  using C = Cfg<DQK, DV, QT>;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  constexpr int kMaxDevices = 64;
+  static std::atomic<bool> ready[kMaxDevices];  // the kernel's attributes are set on the device
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  if (!ready[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(kv_attn_kernel<DQK, DV, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(kv_attn_kernel<DQK, DV, QT>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    if (e != cudaSuccess) return e;
+    ready[dev].store(true, std::memory_order_release);
+  }
+  p.tile_counter = claim_tile_counter();
+  if (p.tile_counter == nullptr) return cudaErrorInvalidDevice;
+  kv_attn_kernel<DQK, DV, QT><<<grid, C::kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const int64_t items = p.max_slots * ((p.rows_cap * (DV / 4) + 127) / 128);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(items, 4 * kv_sm_count())));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_attn_join_kernel<DV>, p);
+}
+
+cudaError_t launch_kv_attn(int dqk, int dv, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                           const KvAttnParams& p, int grid, cudaStream_t stream) {
+  if (dqk == 64 && dv == 64) return launch<64, 64, 1>(tq, tk, tv, p, grid, stream);
+  if (dqk == 64 && dv == 128) return launch<64, 128, 2>(tq, tk, tv, p, grid, stream);
+  if (dqk == 128 && dv == 64) return launch<128, 64, 2>(tq, tk, tv, p, grid, stream);
+  if (dqk == 128 && dv == 128) return launch<128, 128, 2>(tq, tk, tv, p, grid, stream);
+  if (dqk == 192 && dv == 64) return launch<192, 64, 2>(tq, tk, tv, p, grid, stream);
+  if (dqk == 192 && dv == 128) return launch<192, 128, 2>(tq, tk, tv, p, grid, stream);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+}  // namespace slope
+
+using namespace slope;
+
+extern "C" {
+
+size_t slope_kv_attn_workspace_size(int64_t T, int64_t Hq, const slope_kv_cache* cache, int32_t q_len) {
+  if (cache == nullptr || !attn_partial_supported(cache->dqk, cache->dv)) return 0;
+  if (T < 0 || T >= kKvMaxTokens || cache->Hkv < 1 || Hq < 1 || Hq > 65535 || Hq % cache->Hkv != 0 || q_len < 0) return 0;
+  return workspace_of(T, Hq / cache->Hkv, cache->dqk, cache->dv, q_len).total;
+}
+
+slope_status slope_kv_attn(const slope_tensor* q, const slope_kv_cache* cache, const slope_kv_batch* batch,
+                           int64_t window, float scale, slope_tensor* out, slope_tensor* lse, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  const CallRange range("slope_kv_attn");
+  slope_status st;
+  if ((st = check_kv_cache(cache)) != SLOPE_OK || (st = check_kv_q(q, cache)) != SLOPE_OK) return st;
+  const int64_t T = q->shape[0], Hq = q->shape[1];
+  if (window < 0 || window > (int64_t(1) << 30)) return SLOPE_ERR_SHAPE;
+  if ((st = check_kv_batch(batch, cache, T)) != SLOPE_OK) return st;
+  if ((st = check_out(out, T, Hq, cache->dv, true)) != SLOPE_OK) return st;
+  if (lse != nullptr && (st = check_lse(lse, Hq, T)) != SLOPE_OK) return st;
+  if (T == 0 || batch->B == 0) return SLOPE_OK;
+  const int64_t vec = out->dtype == SLOPE_BF16 ? 8 : 4;
+  if (out->stride[0] % vec || out->stride[1] % vec || !aligned(out->data, 16)) return SLOPE_ERR_STRIDE;
+
+  KvAttnParams p{};
+  p.Hkv = cache->Hkv;
+  p.group = static_cast<int32_t>(Hq / cache->Hkv);
+  p.tile = row_tile(p.group);
+  // pairs of a launch are counted in 32 bits, with room for the pieces
+  const int64_t pairs = (T / p.tile.tokens + kKvMaxSeqs) * p.Hkv * p.tile.parts;
+  if (pairs >= (int64_t(1) << 29)) return SLOPE_ERR_UNSUPPORTED;
+  const int grid = grid_of(cache->dqk, cache->dv);
+  if (grid <= 0) return cuda_fail("device attributes");
+  const Workspace w = workspace_of(T, p.group, cache->dqk, cache->dv, batch->cu_q != nullptr ? 0 : batch->q_len);
+  if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < w.total) return SLOPE_ERR_WORKSPACE;
+  p.seqs = kv_seqs(batch, cache, T);
+  p.window = static_cast<int32_t>(window);
+  p.scale_log2 = resolve_scale(scale, cache->dqk) * 1.44269504088896340736f;
+  p.out = out->data;
+  p.out_srow = out->stride[0];
+  p.out_shead = out->stride[1];
+  p.out_bf16 = out->dtype == SLOPE_BF16 ? 1 : 0;
+  if (lse != nullptr) {
+    p.lse = static_cast<float*>(lse->data);
+    p.lse_srow = lse->stride[1];
+    p.lse_shead = lse->stride[0];
+  }
+  char* const ws = static_cast<char*>(workspace);
+  p.rows_cap = static_cast<int32_t>(w.rows_cap);
+  p.max_slots = static_cast<int32_t>(w.max_slots);
+  p.n_slots = reinterpret_cast<int32_t*>(ws);
+  p.pairs = reinterpret_cast<KvPair*>(ws + w.pairs);
+  p.ml = reinterpret_cast<float2*>(ws + w.ml);
+  p.part = reinterpret_cast<float*>(ws + w.part);
+  p.status = device_status_ptr();
+  if (p.status == nullptr) return cuda_fail("device status word (cudaGetSymbolAddress)");
+  p.wait_limit_ns = wait_limit_ns();
+  CUtensorMap tq, tk, tv;
+  if (!make_q_map(&tq, q, p.tile.heads, p.tile.tokens) || !make_page_map(&tk, cache->k, cache, cache->dqk, cache->k_stride) ||
+      !make_page_map(&tv, cache->v, cache, cache->dv, cache->v_stride))
+    return cuda_fail("cuTensorMapEncodeTiled");
+  for (int64_t b = 0; b < batch->B; b += kKvMaxSeqs) {
+    p.seqs.b0 = static_cast<int32_t>(b);
+    p.seqs.B = static_cast<int32_t>(std::min<int64_t>(kKvMaxSeqs, batch->B - b));
+    const cudaError_t e = launch_kv_attn(cache->dqk, cache->dv, tq, tk, tv, p, grid, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail("cache attention kernel launch", e);
+  }
+  return SLOPE_OK;
+}
+
+}  // extern "C"

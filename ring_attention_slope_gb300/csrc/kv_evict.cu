@@ -1,0 +1,425 @@
+// Eviction from the 16-bit cache: of each sequence and key head the tokens with the largest accumulated weights stay and
+// move together, in order.
+//
+// Selection.  A weight becomes a 32-bit key whose order is the weights' (a missing page 0, NaN 1, then -inf .. inf), and
+// the smallest key that stays is found 11, 11 and 10 bits at a time from the top: a histogram of the keys that match
+// the bits so far, and the bin that holds the wanted rank.  Then every key above it stays, and as many equal ones as are
+// left, the first ones.  A cluster of CTAs shares a (sequence, head) pair: each has a run of tokens, whose keys it keeps
+// in shared memory, and they read one another's histograms and counts there, so the weights are read once.
+//
+// Moving.  Token j of those kept comes from position old[j] >= j, so within its own pages a chunk of kept tokens may
+// overwrite only what chunks before it read.  A CTA takes a chunk by ticket, reads its rows into registers, says so in a
+// flag, waits for the (at most two) chunks whose rows lie where its own go, and writes: each row is read and written
+// once, by as many CTAs as there are chunks.  A chunk waits only for chunks of lower tickets, which are running and
+// read before they wait, so every wait ends; all the same it is bounded.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "kv_cache.cuh"
+#include "sm103_ptx.cuh"
+#include "waits.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace slope {
+namespace {
+
+constexpr int kSelectThreads = 512;
+constexpr int kCluster = 8;
+constexpr int kBins = 2048;
+constexpr int kAloneTokens = 8192;  // sequences up to this long are selected by one CTA
+constexpr int kHeldKeys = 40960;    // keys of a CTA in shared memory; more are made again in every pass
+constexpr int kMoveThreads = 128, kMoveWords = 8;  // of a thread, 16 bytes each
+
+struct KvEvictParams {
+  KvSeqs seqs;
+  int32_t Hkv;
+  const float* weights_in;
+  float* weights;
+  int64_t w_spage, w_shead;
+  int32_t keep, first, recent;
+  const int32_t* out_table;  // null: within the sequence's own pages
+  int64_t out_stride;
+  int32_t* kept;
+  int32_t* out_lens;
+  const uint4* k_in;
+  uint4* k;
+  const uint4* v_in;
+  uint4* v;
+  int64_t k_stride[3], v_stride[3];  // in words of 8 channels
+  int32_t chunk, chunks;             // kept tokens of a chunk, chunks of a pair
+  int32_t held;                      // keys of a CTA in shared memory
+  uint32_t* ticket;                  // workspace
+  uint32_t* flags;                   // workspace: [pair][chunk], the chunk's rows are read
+  int32_t* bounds;                   // workspace: [pair][chunk + 1], kept tokens before position chunk * c
+  int* status;
+  uint64_t wait_limit_ns;
+};
+
+// Keys of weights: larger weight, larger key; equal weights, equal keys.
+__device__ __forceinline__ uint32_t weight_key(float w) {
+  if (w != w) return 1u;
+  const uint32_t u = __float_as_uint(w + 0.f);  // -0 is 0
+  return (u >> 31) != 0 ? ~u : u | 0x80000000u;
+}
+
+// Exclusive sums over the CTA's threads, and the total.
+__device__ __forceinline__ uint2 block_scan(uint2 v, uint2* scratch, uint2& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint2 incl = v;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const uint32_t x = __shfl_up_sync(0xffffffffu, incl.x, m), y = __shfl_up_sync(0xffffffffu, incl.y, m);
+    if (lane >= m) incl.x += x, incl.y += y;
+  }
+  __syncthreads();
+  if (lane == 31) scratch[warp] = incl;
+  __syncthreads();
+  uint2 before = make_uint2(0, 0);
+  total = make_uint2(0, 0);
+#pragma unroll
+  for (int w = 0; w < kSelectThreads / 32; ++w) {
+    const uint2 s = scratch[w];
+    if (w < warp) before.x += s.x, before.y += s.y;
+    total.x += s.x, total.y += s.y;
+  }
+  return make_uint2(before.x + incl.x - v.x, before.y + incl.y - v.y);
+}
+
+__global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const __grid_constant__ KvEvictParams p) {
+  cg::cluster_group cluster = cg::this_cluster();
+  extern __shared__ uint32_t s_keys[];
+  __shared__ uint32_t s_hist[kBins];
+  __shared__ uint32_t s_bin[2];  // the bin with the wanted rank, and the rank within it
+  __shared__ uint2 s_scan[kSelectThreads / 32], s_count;
+  const int ranks = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+  const int pair = blockIdx.x / ranks, b = pair / p.Hkv, h = pair - b * p.Hkv;
+  const KvSeq seq = kv_seq(p.seqs, b);
+  const int n = seq.len, keep = p.keep;
+  int32_t* const kept = p.kept + static_cast<int64_t>(pair) * keep;
+  uint32_t* const flags = p.flags + static_cast<int64_t>(pair) * p.chunks;
+  int32_t* const bounds = p.bounds + static_cast<int64_t>(pair) * (p.chunks + 1);
+  const int stride = ranks * kSelectThreads, me = rank * kSelectThreads + threadIdx.x;
+
+  if (pair == 0 && me == 0) *p.ticket = 0;
+  for (int c = me; c < p.chunks; c += stride) flags[c] = 0;
+  if (n <= keep) {
+    for (int j = me; j < keep; j += stride) kept[j] = j < n ? j : -1;
+    return;  // (the whole cluster does)
+  }
+  // tokens before and after the ones to choose from
+  for (int j = me; j < p.first; j += stride) kept[j] = j;
+  for (int j = me; j < p.recent; j += stride) kept[keep - p.recent + j] = n - p.recent + j;
+  const int mid = n - p.first - p.recent;  // > want
+  const uint32_t want = static_cast<uint32_t>(keep - p.first - p.recent);
+  const int each = (mid + ranks - 1) / ranks;
+  const int t0 = p.first + min(mid, rank * each), t1 = p.first + min(mid, (rank + 1) * each);
+
+  const int32_t* const row = p.seqs.table + static_cast<int64_t>(b) * p.seqs.table_stride;
+  const int in_page = (1 << p.seqs.page_shift) - 1;
+  auto read_key = [&](int t) -> uint32_t {
+    const int pg = row[t >> p.seqs.page_shift];
+    if (pg < 0 || pg >= p.seqs.n_pages) return 0u;
+    return weight_key(p.weights_in[pg * p.w_spage + h * p.w_shead + (t & in_page)]);
+  };
+  for (int i = threadIdx.x; i < min(t1 - t0, p.held); i += kSelectThreads) s_keys[i] = read_key(t0 + i);
+  auto key = [&](int t) -> uint32_t { return t - t0 < p.held ? s_keys[t - t0] : read_key(t); };
+
+  // ---- the smallest key that stays, and how many equal to it
+  uint32_t prefix = 0, left = want;  // of the keys that match the prefix, the left-th largest is looked for
+  int shift = 32;
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int bits = pass < 2 ? 11 : 10;
+    const uint32_t high = shift == 32 ? 0u : ~0u << shift;  // bits known so far
+    shift -= bits;
+    for (int i = threadIdx.x; i < kBins; i += kSelectThreads) s_hist[i] = 0;
+    __syncthreads();
+    for (int t = t0 + threadIdx.x; t < t1; t += kSelectThreads) {
+      const uint32_t k = key(t);
+      if ((k & high) == prefix) atomicAdd(&s_hist[(k >> shift) & ((1u << bits) - 1)], 1u);
+    }
+    cluster.sync();
+    // bins from the top, four to a thread
+    uint32_t c[4];
+    uint2 sum = make_uint2(0, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int bin = kBins - 1 - (threadIdx.x * 4 + i);
+      c[i] = 0;
+      for (int r = 0; r < ranks; ++r) c[i] += cluster.map_shared_rank(s_hist, r)[bin];
+      sum.x += c[i];
+    }
+    uint2 total;
+    uint32_t above = block_scan(sum, s_scan, total).x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (above < left && left <= above + c[i]) {
+        s_bin[0] = kBins - 1 - (threadIdx.x * 4 + i);
+        s_bin[1] = left - above;
+      }
+      above += c[i];
+    }
+    cluster.sync();  // the histograms are read, the bin is written
+    if (want > 0) {
+      prefix |= s_bin[0] << shift;
+      left = s_bin[1];
+    }
+  }
+  if (want == 0) prefix = ~0u, left = 0;  // no key is as large
+
+  // ---- counts of larger and equal keys in this CTA's run, and before it
+  uint2 mine = make_uint2(0, 0), total;
+  for (int t = t0 + threadIdx.x; t < t1; t += kSelectThreads) {
+    const uint32_t k = key(t);
+    mine.x += k > prefix ? 1u : 0u, mine.y += k == prefix ? 1u : 0u;
+  }
+  block_scan(mine, s_scan, total);
+  if (threadIdx.x == 0) s_count = total;
+  cluster.sync();
+  uint2 before = make_uint2(0, 0);
+  for (int r = 0; r < rank; ++r) {
+    const uint2 c = *cluster.map_shared_rank(&s_count, r);
+    before.x += c.x, before.y += c.y;
+  }
+  cluster.sync();  // no CTA leaves before its counts are read
+
+  // ---- places
+  for (int at = t0; at < t1; at += kSelectThreads) {
+    const int t = at + threadIdx.x;
+    const uint32_t k = t < t1 ? key(t) : 0u;
+    const uint2 flag = make_uint2(t < t1 && k > prefix ? 1u : 0u, t < t1 && k == prefix ? 1u : 0u);
+    const uint2 pre = block_scan(flag, s_scan, total);
+    const uint32_t eq = before.y + pre.y;
+    const int j = p.first + static_cast<int>(before.x + pre.x + min(eq, left));
+    if (flag.x || (flag.y && eq < left)) kept[j] = t;
+    if (t < t1 && t % p.chunk == 0 && t / p.chunk <= p.chunks) bounds[t / p.chunk] = j;
+    before.x += total.x, before.y += total.y;
+  }
+  // the bounds outside the chosen range
+  for (int c = me; c <= p.chunks; c += stride) {
+    const int64_t t = static_cast<int64_t>(c) * p.chunk;
+    if (t < p.first)
+      bounds[c] = static_cast<int>(t);
+    else if (t >= n)
+      bounds[c] = keep;
+    else if (t >= n - p.recent)
+      bounds[c] = keep - (n - static_cast<int>(t));
+  }
+}
+
+// Words of a token's head: keys, then values.
+template <int DQK, int DV>
+__global__ void __launch_bounds__(kMoveThreads) kv_move_kernel(const __grid_constant__ KvEvictParams p, int pairs) {
+  constexpr int kKey = DQK / 8, kAll = (DQK + DV) / 8;
+  constexpr int kChunk = kMoveThreads * kMoveWords / kAll / 8 * 8;
+  __shared__ uint32_t s_ticket;
+  __shared__ int64_t s_src[kChunk], s_dst[kChunk];  // page << 32 | index in the page; -1: not moved
+  __shared__ int s_give_up;
+  if (threadIdx.x == 0) {
+    s_ticket = atomicAdd(p.ticket, 1u);
+    s_give_up = 0;
+  }
+  __syncthreads();
+  // the chunks of all pairs in turn, so that a chunk's forerunners are a round ahead
+  const int c = static_cast<int>(s_ticket / static_cast<uint32_t>(pairs)), pair = static_cast<int>(s_ticket % static_cast<uint32_t>(pairs));
+  const int b = pair / p.Hkv, h = pair - b * p.Hkv;
+  if (threadIdx.x == 0 && c == 0 && h == 0) p.out_lens[b] = min(kv_seq(p.seqs, b).len, p.keep);
+  const int j0 = c * kChunk, count = min(kChunk, p.keep - j0);
+  const int shift = p.seqs.page_shift, in_page = (1 << shift) - 1;
+  bool moves = false;
+  for (int i = threadIdx.x; i < kChunk; i += kMoveThreads) {
+    const int j = j0 + i, old = i < count ? p.kept[static_cast<int64_t>(pair) * p.keep + j] : -1;
+    int64_t src = -1, dst = -1;
+    if (old >= 0 && (p.out_table != nullptr || old != j)) {
+      const int32_t* const row = p.seqs.table + static_cast<int64_t>(b) * p.seqs.table_stride;
+      const int from = row[old >> shift];
+      const int to = p.out_table != nullptr ? p.out_table[static_cast<int64_t>(b) * p.out_stride + (j >> shift)] : row[j >> shift];
+      if (from >= 0 && from < p.seqs.n_pages && to >= 0 && to < p.seqs.n_pages) {
+        src = static_cast<int64_t>(from) << 32 | (old & in_page);
+        dst = static_cast<int64_t>(to) << 32 | (j & in_page);
+        moves = true;
+      }
+    }
+    s_src[i] = src, s_dst[i] = dst;
+  }
+  uint32_t* const flags = p.flags + static_cast<int64_t>(pair) * p.chunks;
+  if (!__syncthreads_or(moves)) {
+    if (threadIdx.x == 0) atomicExch(&flags[c], 1u);
+    return;
+  }
+
+  uint4 x[kMoveWords];
+#pragma unroll
+  for (int i = 0; i < kMoveWords; ++i) {
+    const int word = threadIdx.x + i * kMoveThreads, e = word / kAll, w = word - e * kAll;
+    if (e >= kChunk || s_src[e] < 0) continue;
+    const int64_t pg = s_src[e] >> 32, t = s_src[e] & 0xffffffff;
+    x[i] = w < kKey ? p.k_in[pg * p.k_stride[0] + h * p.k_stride[1] + t * p.k_stride[2] + w]
+                    : p.v_in[pg * p.v_stride[0] + h * p.v_stride[1] + t * p.v_stride[2] + (w - kKey)];
+  }
+  float weight = 0.f;
+  if (threadIdx.x < kChunk && s_src[threadIdx.x] >= 0)
+    weight = p.weights_in[(s_src[threadIdx.x] >> 32) * p.w_spage + h * p.w_shead + (s_src[threadIdx.x] & 0xffffffff)];
+
+  if (p.out_table == nullptr) {
+    __threadfence();  // the reads come before the flag
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      atomicExch(&flags[c], 1u);
+      // the kept tokens that lie where this chunk's go, and their chunks
+      const int32_t* const bounds = p.bounds + static_cast<int64_t>(pair) * (p.chunks + 1) + c;
+      const int lo = bounds[0], hi = bounds[1];
+      const uint64_t start = globaltimer_ns();
+      for (int o = lo / kChunk; hi > lo && o <= (hi - 1) / kChunk && o < c && !s_give_up; ++o) {
+        while (atomicAdd(&flags[o], 0u) == 0u) {
+          if (*reinterpret_cast<volatile int*>(p.status) != 0) {
+            s_give_up = 1;
+            break;
+          }
+          if (globaltimer_ns() - start > p.wait_limit_ns) {
+            record_timeout(p.status, 81);
+            s_give_up = 1;
+            break;
+          }
+        }
+      }
+      __threadfence();
+    }
+    __syncthreads();
+    if (s_give_up) return;
+  }
+#pragma unroll
+  for (int i = 0; i < kMoveWords; ++i) {
+    const int word = threadIdx.x + i * kMoveThreads, e = word / kAll, w = word - e * kAll;
+    if (e >= kChunk || s_src[e] < 0) continue;
+    const int64_t pg = s_dst[e] >> 32, t = s_dst[e] & 0xffffffff;
+    if (w < kKey)
+      p.k[pg * p.k_stride[0] + h * p.k_stride[1] + t * p.k_stride[2] + w] = x[i];
+    else
+      p.v[pg * p.v_stride[0] + h * p.v_stride[1] + t * p.v_stride[2] + (w - kKey)] = x[i];
+  }
+  if (threadIdx.x < kChunk && s_src[threadIdx.x] >= 0)
+    p.weights[(s_dst[threadIdx.x] >> 32) * p.w_spage + h * p.w_shead + (s_dst[threadIdx.x] & 0xffffffff)] = weight;
+}
+
+int chunk_of(int dqk, int dv) { return kMoveThreads * kMoveWords / ((dqk + dv) / 8) / 8 * 8; }
+
+template <int DQK, int DV>
+cudaError_t launch_move(const KvEvictParams& p, int64_t pairs, cudaStream_t stream) {
+  static_assert(kMoveThreads * kMoveWords / ((DQK + DV) / 8) / 8 * 8 <= kMoveThreads, "a weight to a thread");
+  kv_move_kernel<DQK, DV><<<static_cast<unsigned>(pairs * p.chunks), kMoveThreads, 0, stream>>>(p, static_cast<int>(pairs));
+  return cudaGetLastError();
+}
+
+cudaError_t launch_evict(const KvEvictParams& p, int64_t pairs, int dqk, int dv, cudaStream_t stream) {
+  const int ranks = p.seqs.max_tokens <= kAloneTokens ? 1 : kCluster;
+  KvEvictParams s = p;
+  s.held = static_cast<int32_t>(std::min<int64_t>(kHeldKeys, (p.seqs.max_tokens + ranks - 1) / ranks));
+  const int bytes = s.held * 4;
+  cudaError_t e = cudaFuncSetAttribute(kv_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeldKeys * 4);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(pairs * ranks));
+  cfg.blockDim = dim3(kSelectThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(ranks);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, kv_select_kernel, s)) != cudaSuccess) return e;
+  if (dqk == 64 && dv == 64) return launch_move<64, 64>(p, pairs, stream);
+  if (dqk == 64 && dv == 128) return launch_move<64, 128>(p, pairs, stream);
+  if (dqk == 128 && dv == 64) return launch_move<128, 64>(p, pairs, stream);
+  if (dqk == 128 && dv == 128) return launch_move<128, 128>(p, pairs, stream);
+  if (dqk == 192 && dv == 64) return launch_move<192, 64>(p, pairs, stream);
+  if (dqk == 192 && dv == 128) return launch_move<192, 128>(p, pairs, stream);
+  return cudaErrorInvalidValue;
+}
+
+constexpr int kMinChunk = 24;  // chunk_of's smallest
+
+struct Workspace {
+  size_t flags, bounds, total;
+};
+Workspace workspace_of(int64_t pairs, int64_t chunks) {
+  auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+  Workspace w;
+  w.flags = 256;
+  w.bounds = w.flags + up(pairs * chunks * 4);
+  w.total = w.bounds + up(pairs * (chunks + 1) * 4);
+  return w;
+}
+
+}  // namespace
+}  // namespace slope
+
+using namespace slope;
+
+extern "C" {
+
+size_t slope_kv_evict_workspace_size(int64_t B, int64_t Hkv, int64_t keep) {
+  if (B < 0 || B > 65535 || Hkv < 1 || Hkv > 65535 || keep < 1 || keep >= kKvMaxTokens) return 0;
+  return workspace_of(B * Hkv, (keep + kMinChunk - 1) / kMinChunk).total;
+}
+
+slope_status slope_kv_evict(const slope_kv_cache* cache, slope_tensor* weights, int64_t B, const int32_t* block_table,
+                            int64_t table_stride, int64_t max_pages, const int32_t* kv_lens, int64_t keep, int64_t first,
+                            int64_t recent, const int32_t* out_table, int64_t out_stride, int64_t out_pages,
+                            int32_t* kept, int32_t* out_lens, void* workspace, size_t workspace_bytes, void* stream) {
+  const CallRange range("slope_kv_evict");
+  slope_status st;
+  if ((st = check_kv_cache(cache)) != SLOPE_OK || (st = check_kv_weights(weights, cache)) != SLOPE_OK) return st;
+  const slope_kv_batch batch{B, nullptr, 0, kv_lens, block_table, table_stride, max_pages};
+  if ((st = check_kv_batch(&batch, cache, 0)) != SLOPE_OK) return st;
+  if (keep < 1 || keep >= kKvMaxTokens || first < 0 || recent < 0 || first > keep || recent > keep - first) return SLOPE_ERR_SHAPE;
+  const int64_t max_tokens = max_pages * cache->page_size;
+  if (out_table != nullptr && (out_pages < 0 || out_stride < out_pages || out_pages > (kKvMaxTokens - 1) / cache->page_size ||
+                               out_pages * cache->page_size < std::min(keep, max_tokens)))
+    return SLOPE_ERR_SHAPE;
+  if (B == 0) return SLOPE_OK;
+  if (kept == nullptr || out_lens == nullptr) return SLOPE_ERR_NULL;
+  if (!aligned(kept, 4) || !aligned(out_lens, 4) || !aligned(out_table, 4)) return SLOPE_ERR_STRIDE;
+  const int64_t pairs = B * cache->Hkv, chunk = chunk_of(cache->dqk, cache->dv), chunks = (keep + chunk - 1) / chunk;
+  if (pairs * chunks >= (int64_t(1) << 31) || pairs * kCluster >= (int64_t(1) << 31)) return SLOPE_ERR_UNSUPPORTED;
+  const Workspace w = workspace_of(pairs, chunks);
+  if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < w.total) return SLOPE_ERR_WORKSPACE;
+
+  KvEvictParams p{};
+  p.seqs = kv_seqs(&batch, cache, 0);
+  p.Hkv = cache->Hkv;
+  p.weights_in = p.weights = static_cast<float*>(weights->data);
+  p.w_spage = weights->stride[0];
+  p.w_shead = weights->stride[1];
+  p.keep = static_cast<int32_t>(keep);
+  p.first = static_cast<int32_t>(first);
+  p.recent = static_cast<int32_t>(recent);
+  p.out_table = out_table;
+  p.out_stride = out_stride;
+  p.kept = kept;
+  p.out_lens = out_lens;
+  p.k_in = p.k = static_cast<uint4*>(cache->k);
+  p.v_in = p.v = static_cast<uint4*>(cache->v);
+  for (int i = 0; i < 3; ++i) {
+    p.k_stride[i] = cache->k_stride[i] / 8;
+    p.v_stride[i] = cache->v_stride[i] / 8;
+  }
+  p.chunk = static_cast<int32_t>(chunk);
+  p.chunks = static_cast<int32_t>(chunks);
+  char* const ws = static_cast<char*>(workspace);
+  p.ticket = reinterpret_cast<uint32_t*>(ws);
+  p.flags = reinterpret_cast<uint32_t*>(ws + w.flags);
+  p.bounds = reinterpret_cast<int32_t*>(ws + w.bounds);
+  p.status = device_status_ptr();
+  if (p.status == nullptr) return cuda_fail("device status word (cudaGetSymbolAddress)");
+  p.wait_limit_ns = wait_limit_ns();
+  const cudaError_t e = launch_evict(p, pairs, cache->dqk, cache->dv, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SLOPE_OK : cuda_fail("cache eviction kernel launch", e);
+}
+
+}  // extern "C"

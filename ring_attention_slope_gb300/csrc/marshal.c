@@ -14,6 +14,7 @@
 #include <stdint.h>
 #include <stdlib.h>
 
+#include "slope_kv.h"
 #include "slope_serving.h"
 
 /* ---------------------------------------------------------------- bound once */
@@ -34,6 +35,21 @@ static struct {
   size_t (*attn_workspace_size)(int64_t, int64_t, const slope_kv4_cache*, int32_t);
 } lib;
 
+static struct { /* the calls of slope_kv.h */
+  slope_status (*write)(const slope_kv_cache*, const slope_tensor*, const slope_tensor*, const int32_t*, slope_tensor*,
+                        void*);
+  slope_status (*attn)(const slope_tensor*, const slope_kv_cache*, const slope_kv_batch*, int64_t, float, slope_tensor*,
+                       slope_tensor*, void*, size_t, void*);
+  slope_status (*weights)(const slope_tensor*, const slope_kv_cache*, const slope_kv_batch*, const slope_tensor*, int64_t,
+                          float, int, slope_tensor*, void*, size_t, void*);
+  slope_status (*evict)(const slope_kv_cache*, slope_tensor*, int64_t, const int32_t*, int64_t, int64_t, const int32_t*,
+                        int64_t, int64_t, int64_t, const int32_t*, int64_t, int64_t, int32_t*, int32_t*, void*, size_t,
+                        void*);
+  size_t (*attn_size)(int64_t, int64_t, const slope_kv_cache*, int32_t);
+  size_t (*weights_size)(int64_t, int64_t, const slope_kv_cache*, int32_t);
+  size_t (*evict_size)(int64_t, int64_t, int64_t);
+} kv;
+
 /* bind(bfloat16, float32, int32, addresses of the seven calls in the order above) */
 static PyObject* bind(PyObject* self, PyObject* args) {
   (void)self;
@@ -51,6 +67,21 @@ static PyObject* bind(PyObject* self, PyObject* args) {
   *(void**)&lib.kv4_attn = (void*)(uintptr_t)f[4];
   *(void**)&lib.cache_bytes = (void*)(uintptr_t)f[5];
   *(void**)&lib.attn_workspace_size = (void*)(uintptr_t)f[6];
+  Py_RETURN_NONE;
+}
+
+/* bind_kv(addresses of the seven calls in the order above); bind comes first */
+static PyObject* bind_kv(PyObject* self, PyObject* args) {
+  (void)self;
+  unsigned long long f[7];
+  if (!PyArg_ParseTuple(args, "KKKKKKK", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6])) return NULL;
+  *(void**)&kv.write = (void*)(uintptr_t)f[0];
+  *(void**)&kv.attn = (void*)(uintptr_t)f[1];
+  *(void**)&kv.weights = (void*)(uintptr_t)f[2];
+  *(void**)&kv.evict = (void*)(uintptr_t)f[3];
+  *(void**)&kv.attn_size = (void*)(uintptr_t)f[4];
+  *(void**)&kv.weights_size = (void*)(uintptr_t)f[5];
+  *(void**)&kv.evict_size = (void*)(uintptr_t)f[6];
   Py_RETURN_NONE;
 }
 
@@ -410,6 +441,149 @@ static PyObject* attn_workspace_size(PyObject* self, PyObject* const* a, Py_ssiz
   return PyLong_FromSize_t(lib.attn_workspace_size(batch, heads, (const slope_kv4_cache*)cache, q_len));
 }
 
+/* ---------------------------------------------------------------- the 16-bit cache */
+
+/* A block table [batch, pages]: its address, pages and the distance of its rows. */
+static int block_table(PyObject* t, const char* what, int64_t dev, int64_t batch, const int32_t** out, int64_t* pages,
+                       int64_t* stride) {
+  int64_t shape[3], strides[3];
+  PyObject* o = PyObject_GetAttr(t, n_shape);
+  if (o == NULL) return -1;
+  Py_ssize_t rank = entries(o, shape, 0, 3);
+  if (rank >= 0 && (rank != 2 || shape[0] != batch))
+    PyErr_Format(PyExc_ValueError, "%s must have shape [%lld, pages], got %S", what, (long long)batch, o);
+  Py_DECREF(o);
+  if (rank != 2 || shape[0] != batch) return -1;
+  o = PyObject_CallMethodNoArgs(t, n_stride);
+  if (o == NULL) return -1;
+  rank = entries(o, strides, 0, 3);
+  Py_DECREF(o);
+  if (rank < 0) return -1;
+  if (shape[1] > 1 && strides[1] != 1) {
+    PyErr_Format(PyExc_ValueError, "%s rows must be contiguous", what);
+    return -1;
+  }
+  *pages = shape[1];
+  *stride = batch > 1 ? strides[0] : shape[1];
+  return index_array(t, what, dev, -1, out);
+}
+
+/* The batch of (block_table, kv_lens, cu_q or None, q_len). */
+static int batch_of(PyObject* const* a, int64_t dev, slope_kv_batch* b) {
+  if (rows_of(a[1], &b->B) < 0 || block_table(a[0], "block_table", dev, b->B, &b->block_table, &b->max_pages, &b->table_stride) < 0 ||
+      index_array(a[1], "kv_lens", dev, b->B, &b->kv_lens) < 0 || as_i32(a[3], &b->q_len) < 0)
+    return -1;
+  b->cu_q = NULL;
+  if (a[2] != Py_None && index_array(a[2], "cu_q", dev, b->B + 1, &b->cu_q) < 0) return -1;
+  return 0;
+}
+
+/* (cache, k, v, slots, weights, stream, dev) */
+static PyObject* kv_write(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  slope_tensor d[3], *k, *v, *w;
+  const int32_t* slots;
+  const void* cache;
+  int64_t stream, dev;
+  if (want(n, 7) < 0 || as_i64(a[5], &stream) < 0 || as_i64(a[6], &dev) < 0) return NULL;
+  if (structure(a[0], sizeof(slope_kv_cache), &cache) < 0 || describe(a[1], dev, 0, &d[0], &k) < 0 ||
+      describe(a[2], dev, 0, &d[1], &v) < 0 || describe(a[4], dev, 0, &d[2], &w) < 0 ||
+      index_array(a[3], "slots", dev, k != NULL ? k->shape[0] : 0, &slots) < 0)
+    return NULL;
+  slope_status st;
+  UNLOCKED(st, kv.write((const slope_kv_cache*)cache, k, v, slots, w, (void*)(uintptr_t)stream));
+  return PyLong_FromLong(st);
+}
+
+/* (q, cache, block_table, kv_lens, cu_q, q_len, window, scale, out, lse, workspace address, workspace bytes, stream, dev) */
+static PyObject* kv_attn(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  slope_tensor d[3], *q, *out, *lse;
+  slope_kv_batch batch;
+  const void* cache;
+  int64_t window, ws, ws_bytes, stream, dev;
+  float scale;
+  if (want(n, 14) < 0 || as_i64(a[12], &stream) < 0 || as_i64(a[13], &dev) < 0) return NULL;
+  if (structure(a[1], sizeof(slope_kv_cache), &cache) < 0 || batch_of(&a[2], dev, &batch) < 0 ||
+      as_i64(a[6], &window) < 0 || as_float(a[7], &scale) < 0 || as_i64(a[10], &ws) < 0 || as_i64(a[11], &ws_bytes) < 0)
+    return NULL;
+  if (describe(a[0], dev, 0, &d[0], &q) < 0 || describe(a[8], dev, 0, &d[1], &out) < 0 ||
+      describe(a[9], dev, 0, &d[2], &lse) < 0)
+    return NULL;
+  slope_status st;
+  UNLOCKED(st, kv.attn(q, (const slope_kv_cache*)cache, &batch, window, scale, out, lse, (void*)(uintptr_t)ws,
+                       (size_t)ws_bytes, (void*)(uintptr_t)stream));
+  return PyLong_FromLong(st);
+}
+
+/* (q, cache, block_table, kv_lens, cu_q, q_len, lse, window, scale, accumulate, weights, workspace address, workspace
+ * bytes, stream, dev) */
+static PyObject* kv_attn_weights(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  slope_tensor d[3], *q, *lse, *w;
+  slope_kv_batch batch;
+  const void* cache;
+  int64_t window, ws, ws_bytes, stream, dev;
+  float scale;
+  if (want(n, 15) < 0 || as_i64(a[13], &stream) < 0 || as_i64(a[14], &dev) < 0) return NULL;
+  const int accumulate = PyObject_IsTrue(a[9]);
+  if (accumulate < 0 || structure(a[1], sizeof(slope_kv_cache), &cache) < 0 || batch_of(&a[2], dev, &batch) < 0 ||
+      as_i64(a[7], &window) < 0 || as_float(a[8], &scale) < 0 || as_i64(a[11], &ws) < 0 || as_i64(a[12], &ws_bytes) < 0)
+    return NULL;
+  if (describe(a[0], dev, 0, &d[0], &q) < 0 || describe(a[6], dev, 0, &d[1], &lse) < 0 ||
+      describe(a[10], dev, 0, &d[2], &w) < 0)
+    return NULL;
+  slope_status st;
+  UNLOCKED(st, kv.weights(q, (const slope_kv_cache*)cache, &batch, lse, window, scale, accumulate, w, (void*)(uintptr_t)ws,
+                          (size_t)ws_bytes, (void*)(uintptr_t)stream));
+  return PyLong_FromLong(st);
+}
+
+/* (cache, weights, block_table, kv_lens, keep, first, recent, out_table or None, kept, out_lens, workspace address,
+ * workspace bytes, stream, dev) */
+static PyObject* kv_evict(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  slope_tensor d, *w;
+  const int32_t *table, *lens, *out_table = NULL, *kept, *out_lens;
+  const void* cache;
+  int64_t batch, pages, stride, out_pages = 0, out_stride = 0, keep, first, recent, ws, ws_bytes, stream, dev;
+  if (want(n, 14) < 0 || as_i64(a[12], &stream) < 0 || as_i64(a[13], &dev) < 0) return NULL;
+  if (structure(a[0], sizeof(slope_kv_cache), &cache) < 0 || describe(a[1], dev, 0, &d, &w) < 0 ||
+      rows_of(a[3], &batch) < 0 || block_table(a[2], "block_table", dev, batch, &table, &pages, &stride) < 0 ||
+      index_array(a[3], "kv_lens", dev, batch, &lens) < 0 || as_i64(a[4], &keep) < 0 || as_i64(a[5], &first) < 0 ||
+      as_i64(a[6], &recent) < 0 || as_i64(a[10], &ws) < 0 || as_i64(a[11], &ws_bytes) < 0)
+    return NULL;
+  if (a[7] != Py_None && block_table(a[7], "out_table", dev, batch, &out_table, &out_pages, &out_stride) < 0) return NULL;
+  if (index_array(a[8], "kept", dev, -1, &kept) < 0 || index_array(a[9], "out_lens", dev, batch, &out_lens) < 0) return NULL;
+  slope_status st;
+  UNLOCKED(st, kv.evict((const slope_kv_cache*)cache, w, batch, table, stride, pages, lens, keep, first, recent, out_table,
+                        out_stride, out_pages, (int32_t*)kept, (int32_t*)out_lens, (void*)(uintptr_t)ws,
+                        (size_t)ws_bytes, (void*)(uintptr_t)stream));
+  return PyLong_FromLong(st);
+}
+
+/* (T, Hq, cache, q_len, weights): the workspace of kv_attn, or with weights that of kv_attn_weights */
+static PyObject* kv_attn_workspace_size(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  int64_t rows, heads;
+  int32_t q_len;
+  const void* cache;
+  if (want(n, 5) < 0 || as_i64(a[0], &rows) < 0 || as_i64(a[1], &heads) < 0 ||
+      structure(a[2], sizeof(slope_kv_cache), &cache) < 0 || as_i32(a[3], &q_len) < 0)
+    return NULL;
+  const int weights = PyObject_IsTrue(a[4]);
+  if (weights < 0) return NULL;
+  return PyLong_FromSize_t((weights ? kv.weights_size : kv.attn_size)(rows, heads, (const slope_kv_cache*)cache, q_len));
+}
+
+/* (B, Hkv, keep) */
+static PyObject* kv_evict_workspace_size(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  int64_t batch, heads, keep;
+  if (want(n, 3) < 0 || as_i64(a[0], &batch) < 0 || as_i64(a[1], &heads) < 0 || as_i64(a[2], &keep) < 0) return NULL;
+  return PyLong_FromSize_t(kv.evict_size(batch, heads, keep));
+}
+
 static PyMethodDef methods[] = {
     {"bind", bind, METH_VARARGS, "dtypes and addresses of the library's calls"},
     {"qk_norm_rope", (PyCFunction)(void (*)(void))qk_norm_rope, METH_FASTCALL, NULL},
@@ -419,6 +593,13 @@ static PyMethodDef methods[] = {
     {"kv4_attn", (PyCFunction)(void (*)(void))kv4_attn, METH_FASTCALL, NULL},
     {"cache_bytes", (PyCFunction)(void (*)(void))cache_bytes, METH_FASTCALL, NULL},
     {"attn_workspace_size", (PyCFunction)(void (*)(void))attn_workspace_size, METH_FASTCALL, NULL},
+    {"bind_kv", bind_kv, METH_VARARGS, "addresses of the library's calls on the 16-bit cache"},
+    {"kv_write", (PyCFunction)(void (*)(void))kv_write, METH_FASTCALL, NULL},
+    {"kv_attn", (PyCFunction)(void (*)(void))kv_attn, METH_FASTCALL, NULL},
+    {"kv_attn_weights", (PyCFunction)(void (*)(void))kv_attn_weights, METH_FASTCALL, NULL},
+    {"kv_evict", (PyCFunction)(void (*)(void))kv_evict, METH_FASTCALL, NULL},
+    {"kv_attn_workspace_size", (PyCFunction)(void (*)(void))kv_attn_workspace_size, METH_FASTCALL, NULL},
+    {"kv_evict_workspace_size", (PyCFunction)(void (*)(void))kv_evict_workspace_size, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", "Argument marshalling of the serving calls.", -1,
