@@ -66,32 +66,6 @@ struct KvAttnParams {
   uint64_t wait_limit_ns;
 };
 
-template <int DQK, int DV, int QT>
-struct Cfg {
-  static constexpr int kTmaWarp = 4 * QT, kMmaWarp = kTmaWarp + 1;
-  static constexpr int kThreads = 32 * (5 * QT + 1);
-  static constexpr int kCtas = QT == 2 ? 1 : 2;  // on an SM
-  static constexpr uint32_t kTmemCols = QT == 2 ? 512 : 256;
-  static constexpr int kQChunks = DQK / 64, kVChunks = DV / 64;
-  static constexpr int kQTileBytes = kQChunks * kChunkBytes;
-  static constexpr int kKTileBytes = kQTileBytes, kVTileBytes = kVChunks * kChunkBytes;
-  static constexpr int kSlotBytes = kKTileBytes > kVTileBytes ? kKTileBytes : kVTileBytes;
-  static constexpr int kSlots = (QT == 2 ? 131072 : 65536) / kSlotBytes;
-  static_assert(kSlots % 2 == 0 && kSlots / 2 + 2 <= kHoles, "K tiles in even slots, V tiles in odd ones");
-  static constexpr int kNumBars = 2 + 2 * kSlots + 6 * QT + 4 * QT + 4;
-  static constexpr int kSlotOffset = QT * kQTileBytes;
-  static constexpr int kBarOffset = kSlotOffset + kSlots * kSlotBytes;
-  static constexpr int kListOffset = kBarOffset + ((8 * kNumBars + 15) / 16) * 16;
-  static constexpr int kSmemBytes = 1024 + kListOffset + static_cast<int>(sizeof(CutLists));
-  static constexpr uint32_t kColO = QT * kBlockN, kColP = kColO + QT * DV;
-  static constexpr bool kSepP = kColP + QT * (kBlockN / 2) <= kTmemCols;
-  __device__ static constexpr uint32_t col_p(int t) { return kSepP ? kColP + t * (kBlockN / 2) : t * kBlockN; }
-  // Where P overwrites S (dv = 128) the two softmax warps of an SM sub-partition take turns on their exponentials.
-  static constexpr bool kTurns = QT == 2 && !kSepP;
-  static_assert(kSmemBytes <= (QT == 2 ? 232448 : 115712), "shared memory budget");
-  static_assert(kColO + QT * DV <= kTmemCols, "TMEM budget");
-};
-
 __device__ __forceinline__ bool warp_all(bool v) { return __all_sync(0xffffffffu, v); }
 
 // ---------------------------------------------------------------- the cut
@@ -117,7 +91,8 @@ struct Piece {
   int32_t len;     // tokens of the sequence
   int32_t kvh, head0, heads;
   int32_t slot;    // in the workspace; -1: the whole pair
-  int32_t b, pad;
+  int32_t b;
+  int32_t flo[2], fhi[2];  // steps [flo, fhi) that every row of Q tile t sees in full
 };
 
 __device__ __forceinline__ Piece make_piece(const KvAttnParams& p, int per, const CutLists& lists, uint32_t w,
@@ -145,28 +120,63 @@ __device__ __forceinline__ Piece make_piece(const KvAttnParams& p, int per, cons
   const int lo = p.window > 0 ? max(0, r.pos0 - p.window + 1) : 0;
   const int j_lo = lo / kBlockN, j_hi = max(j_lo, (max(hi, 0) + kBlockN - 1) / kBlockN);
   const int steps = j_hi - j_lo;
-  r.j0 = j_lo + static_cast<int>(static_cast<int64_t>(steps) * c / pieces);
-  r.j1 = j_lo + static_cast<int>(static_cast<int64_t>(steps) * (c + 1) / pieces);
+  piece_steps(steps, pieces, c, r.j0, r.j1);
+  r.j0 += j_lo, r.j1 += j_lo;
   r.slot = pieces > 1 ? static_cast<int32_t>(lists.slots[b]) + (h * cut.blocks + blk) * pieces + c : -1;
-  r.pad = 0;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int tile_tokens = p.tile.tokens, qa = r.pos0 + t * tile_tokens, rows = min(tile_tokens, r.tokens - t * tile_tokens);
+    r.fhi[t] = min(r.len, qa + 1) >> 7;  // (of a negative position: below every step)
+    r.flo[t] = p.window > 0 ? max(0, (qa + rows - 1 - p.window + kBlockN) >> 7) : 0;
+  }
   return r;
 }
+
+template <int DQK, int DV, int QT>
+struct Cfg {
+  static constexpr int kTmaWarp = 4 * QT, kMmaWarp = kTmaWarp + 1;
+  static constexpr int kThreads = 32 * (5 * QT + 1);
+  static constexpr int kCtas = QT == 2 ? 1 : 2;  // on an SM
+  static constexpr uint32_t kTmemCols = QT == 2 ? 512 : 256;
+  static constexpr int kQChunks = DQK / 64, kVChunks = DV / 64;
+  static constexpr int kQTileBytes = kQChunks * kChunkBytes;
+  static constexpr int kKTileBytes = kQTileBytes, kVTileBytes = kVChunks * kChunkBytes;
+  static constexpr int kSlotBytes = kKTileBytes > kVTileBytes ? kKTileBytes : kVTileBytes;
+  static constexpr int kSlots = (QT == 2 ? 131072 : 65536) / kSlotBytes;
+  static_assert(kSlots % 2 == 0 && kSlots / 2 + 2 <= kHoles, "K tiles in even slots, V tiles in odd ones");
+  static constexpr int kNumBars = 2 + 2 * kSlots + 6 * QT + 4 * QT + 4;
+  static constexpr int kSlotOffset = QT * kQTileBytes;
+  static constexpr int kRestOffset = kSlotOffset + kSlots * kSlotBytes;
+  struct Rest {  // behind the tiles
+    uint64_t bars[kNumBars];
+    Piece piece[2];
+    uint32_t holes[kHoles];  // of a step's 16-token runs, those without a page
+    uint32_t tmem;
+    int abort;
+    CutLists lists;
+  };
+  static constexpr int kSmemBytes = kRestOffset + static_cast<int>(sizeof(Rest));
+  static constexpr uint32_t kColO = QT * kBlockN, kColP = kColO + QT * DV;
+  static constexpr bool kSepP = kColP + QT * (kBlockN / 2) <= kTmemCols;
+  __device__ static constexpr uint32_t col_p(int t) { return kSepP ? kColP + t * (kBlockN / 2) : t * kBlockN; }
+  // Where P overwrites S (dv = 128) the two softmax warps of an SM sub-partition take turns on their exponentials.
+  static constexpr bool kTurns = QT == 2 && !kSepP;
+  static_assert(kSmemBytes <= (QT == 2 ? 232448 : 115712), "shared memory budget");
+  static_assert(kColO + QT * DV <= kTmemCols, "TMEM budget");
+};
 
 template <int DQK, int DV, int QT>
 __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::kCtas)
     kv_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ KvAttnParams p) {
   using C = Cfg<DQK, DV, QT>;
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ CutScratch s_cut;
-  __shared__ Piece s_piece[2];
-  __shared__ uint32_t s_holes[kHoles];  // of a step's 16-token runs, those without a page
-  __shared__ uint32_t s_tmem;
-  __shared__ int s_abort;
-  uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // All of the shared memory is dynamic and starts on a tile's boundary, so that its addresses are constants: computed
+  // ones took registers that the softmax needs.
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* const sQ = smem;
   uint8_t* const sSlot = smem + C::kSlotOffset;
-  uint64_t* const bar_q = reinterpret_cast<uint64_t*>(smem + C::kBarOffset);
+  typename C::Rest& sh = *reinterpret_cast<typename C::Rest*>(smem + C::kRestOffset);
+  uint64_t* const bar_q = sh.bars;
   uint64_t* const bar_qempty = bar_q + 1;
   uint64_t* const bar_full = bar_q + 2;
   uint64_t* const bar_empty = bar_full + C::kSlots;
@@ -179,8 +189,7 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
   uint64_t* const bar_turn = bar_drain + QT;     // [t * 4 + quarter]: that softmax warp may exponentiate
   uint64_t* const bar_wfull = bar_turn + 4 * QT;  // a piece is there
   uint64_t* const bar_wfree = bar_wfull + 2;      // every role is done with it
-  CutLists& lists = *reinterpret_cast<CutLists*>(smem + C::kListOffset);
-  volatile int* const cta_abort = &s_abort;
+  volatile int* const cta_abort = &sh.abort;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const RowCut cut_of{QT * p.tile.tokens, p.window};
@@ -196,7 +205,7 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
   }
   if (threadIdx.x == 0) *cta_abort = *reinterpret_cast<volatile int*>(p.status) != 0 ? 1 : 0;
   if (warp == C::kMmaWarp) {
-    tmem_alloc(&s_tmem, C::kTmemCols);
+    tmem_alloc(&sh.tmem, C::kTmemCols);
     tmem_relinquish();
   }
   if (threadIdx.x == C::kMmaWarp * 32) {
@@ -222,17 +231,18 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
     fence_barrier_init();
   }
   tc_fence_before_sync();
-  make_cut<kPieceSteps>(p.seqs, p.Hkv * p.tile.parts, cut_of, s_cut, lists);
+  __syncthreads();
   tc_fence_after_sync();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = sh.tmem;
 
   // The k-th piece of the CTA, once it is there; false if the wait ran out.
   auto take_piece = [&](int k) -> bool { return wait_bounded(&bar_wfull[k & 1], (k >> 1) & 1, cta_abort, p.status, limit, 31); };
 
   if (warp == C::kTmaWarp) {
     // ================================================================ producer: pieces, pages, loads
-    if (lane == 0 && blockIdx.x == 0) *p.n_slots = static_cast<int32_t>(s_cut.slots);
-    const uint32_t total = s_cut.total;
+    const Cut cut = make_cut<kPieceSteps>(p.seqs, p.Hkv * p.tile.parts, cut_of, sh.lists);
+    if (lane == 0 && blockIdx.x == 0) *p.n_slots = static_cast<int32_t>(cut.slots);
+    const uint32_t total = cut.total;
     const uint32_t q_bytes = static_cast<uint32_t>(p.tile.heads * p.tile.tokens) * 128 * C::kQChunks;
     const int boxes_log = max(0, 7 - p.seqs.page_shift);  // log2 of the boxes of 64 channels of a key tile
     const int boxes = 1 << boxes_log, box_rows = kBlockN >> boxes_log;
@@ -247,7 +257,7 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
       if (!ok) break;
       if (w >= total) {
         if (lane == 0) {
-          s_piece[k & 1].tokens = -1;
+          sh.piece[k & 1].tokens = -1;
           mbar_arrive(&bar_wfull[k & 1]);
         }
         break;
@@ -255,9 +265,9 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
       uint32_t next = 0;
       if (lane == 0) next = atomicAdd(p.tile_counter, 1u);  // on its way while this piece loads
       int pieces, c;
-      const Piece pc = make_piece(p, s_cut.per, lists, w, cut_of, pieces, c);
+      const Piece pc = make_piece(p, cut.per, sh.lists, w, cut_of, pieces, c);
       if (lane == 0) {
-        s_piece[k & 1] = pc;
+        sh.piece[k & 1] = pc;
         mbar_arrive(&bar_wfull[k & 1]);
         if (pc.slot >= 0) {
           KvPair e;
@@ -317,7 +327,7 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
               if (kv == 0) {  // bit i: positions 16 i .. 16 i + 15 of the tile have no page
                 uint32_t m = 0;
                 for (int i = 0; missing != 0 && i < 8; ++i) m |= ((missing >> ((i << boxes_log) >> 3)) & 1u) << i;
-                s_holes[step % kHoles] = m;
+                sh.holes[step % kHoles] = m;
               }
               mbar_arrive_expect_tx(&bar_full[slot], kv == 0 ? C::kKTileBytes : C::kVTileBytes);
             }
@@ -404,7 +414,7 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
       bool ok = true;
       for (int k = 0; ok; ++k) {
         if (!take_piece(k)) break;
-        const volatile Piece& pc = s_piece[k & 1];
+        const volatile Piece& pc = sh.piece[k & 1];
         const int tokens = pc.tokens, j0 = pc.j0, j1 = pc.j1, len = pc.len;
         mbar_arrive(&bar_wfree[k & 1]);
         if (tokens < 0) break;
@@ -472,9 +482,6 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
     const uint32_t tS = tmem + lane_base + t * kBlockN;
     const uint32_t tP = tmem + lane_base + C::col_p(t);
     const uint32_t tO = tmem + lane_base + C::kColO + t * DV;
-    const int my_token = row / p.tile.heads;  // in the tile (p.tile.tokens and on: none)
-    const int my_head = row - my_token * p.tile.heads;
-    const int warp_token = (wq * 32) / p.tile.heads;  // the warp's first
     const float sl2 = p.scale_log2;
     // Turn k of tile 0 waits for tile 1's turn k - 1, turn k of tile 1 for tile 0's turn k; both take one turn a step of
     // the pieces that have rows in both tiles.
@@ -493,40 +500,43 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    int n = 0;               // steps of this Q tile
-    uint32_t cta_steps = 0;  // steps of the CTA before this piece
+    int n = 0;      // steps of this Q tile
+    int skipped = 0;  // steps of the CTA that this Q tile had no rows in
     bool ok = true;
     for (int k = 0; ok; ++k) {
       if (!warp_all(take_piece(k))) break;
-      const volatile Piece& pc = s_piece[k & 1];
-      const int tokens = pc.tokens, pos0 = pc.pos0, j0 = pc.j0, j1 = pc.j1, len = pc.len;
-      if (tokens < 0) break;
-      const int rows_t = min(tokens - t * p.tile.tokens, p.tile.tokens);  // tokens of this Q tile
-      if (rows_t <= 0) {
-        cta_steps += static_cast<uint32_t>(j1 - j0);
-        arrive(&bar_wfree[k & 1]);
-        continue;
+      // The piece's fields are read again where they are needed, rather than kept in registers across the steps, which
+      // need every one of them.
+      const volatile Piece& pc = sh.piece[k & 1];
+      int j = pc.j0;
+      bool idle, turns;
+      {
+        const int tokens = pc.tokens, rows_t = min(tokens - t * p.tile.tokens, p.tile.tokens);  // of this Q tile
+        if (tokens < 0) break;
+        if (QT == 2 && rows_t <= 0) {
+          skipped += pc.j1 - j;
+          arrive(&bar_wfree[k & 1]);
+          continue;
+        }
+        turns = C::kTurns && tokens > p.tile.tokens;
+        idle = (wq * 32) / p.tile.heads >= rows_t;  // none of the warp's rows exists
       }
-      const bool turns = C::kTurns && tokens > p.tile.tokens;
-      const bool idle = warp_token >= rows_t;  // none of the warp's rows exists
-      const int qa = pos0 + t * p.tile.tokens, qb = qa + rows_t - 1;
-      const int q_pos = qa + my_token;
       float m_used = -INFINITY;  // running maximum, log2 units
       float l = 0.f;             // running sum of exp2(s * sl2 - m_used)
-      for (int j = j0; ok && j < j1; ++j, ++n, ++cta_steps) {
-        const int kpos = j * kBlockN, valid = len - kpos;
+      for (; ok && j < pc.j1; ++j, ++n) {
         ok = warp_all(wait_bounded(&bar_s[t], n & 1, cta_abort, p.status, limit, 45));
         if (!ok) break;
-        if (valid < kBlockN) {
+        const bool inside = j >= pc.flo[t] && j < pc.fhi[t];
+        if (!inside && (j + 1) * kBlockN > pc.len) {
           // The sequence ends inside this tile.  The V rows behind it have a weight of 0, but 0 times a NaN there would
           // still be NaN: clear them before this Q tile's PV may read them.  S_t is there, so the issuer has waited for
           // every earlier fill of the slot, and the parity can only mean this one.
-          const uint32_t vcnt = 2 * cta_steps + 1, vslot = vcnt % C::kSlots;
+          const uint32_t vcnt = 2 * static_cast<uint32_t>(n + skipped) + 1, vslot = vcnt % C::kSlots;
           ok = warp_all(wait_bounded(&bar_full[vslot], (vcnt / C::kSlots) & 1, cta_abort, p.status, limit, 46));
           if (!ok) break;
           uint8_t* const sv0 = sSlot + vslot * C::kSlotBytes;
           for (int c = 0; c < C::kVChunks; ++c)
-            for (int off = valid * 128 + row * 16; off < static_cast<int>(kChunkBytes); off += 128 * 16)
+            for (int off = (pc.len - j * kBlockN) * 128 + row * 16; off < static_cast<int>(kChunkBytes); off += 128 * 16)
               *reinterpret_cast<uint4*>(sv0 + c * kChunkBytes + off) = make_uint4(0u, 0u, 0u, 0u);
           fence_proxy_async_shared();
         }
@@ -544,7 +554,7 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
           arrive(&bar_p[t]);
           continue;
         }
-        const uint32_t holes = *const_cast<volatile uint32_t*>(&s_holes[cta_steps % kHoles]);
+        const uint32_t holes = *const_cast<volatile uint32_t*>(&sh.holes[static_cast<uint32_t>(n + skipped) % kHoles]);
         tc_fence_after_sync();
         uint32_t r0[32], r1[32], r2[32], r3[32];
         float q0 = tmem_ld32_max(tS + 0, r0);
@@ -569,11 +579,12 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
           sv[96 + i] = __uint_as_float(r3[i]);
         }
         float mx = fmax3(q0, q1, fmaxf(q2, q3));
-        const bool full = valid >= kBlockN && kpos + kBlockN - 1 <= qa && (p.window == 0 || qb - kpos < p.window) && holes == 0;
-        if (!full) {
+        if (!inside || holes != 0) {
           // the row's visible columns are one interval, less the missing pages
+          const int kpos = j * kBlockN;
+          const int q_pos = pc.pos0 + t * p.tile.tokens + row / p.tile.heads;
           int lo = p.window > 0 ? max(0, q_pos - kpos - p.window + 1) : 0;
-          int hi = min(valid - 1, q_pos - kpos);
+          int hi = min(pc.len - kpos - 1, q_pos - kpos);
           if (hi < lo) lo = hi = kBlockN;  // none: every c - lo is negative
           const uint32_t span = static_cast<uint32_t>(hi - lo);
 #pragma unroll
@@ -651,7 +662,7 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
         l += ((c0.x + c0.y) + (c1.x + c1.y)) + ((c2.x + c2.y) + (c3.x + c3.y));
         if (turns) pass_turn();
         // O_t holds the previous PV's result (P's columns, or the issuer's wait before S_t, say that it is done)
-        if (__any_sync(0xffffffffu, need) && j > j0) {
+        if (__any_sync(0xffffffffu, need) && j > pc.j0) {
 #pragma unroll 1
           for (int c = 0; c < DV / 16; ++c) {
             uint32_t o[16];
@@ -670,9 +681,10 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
       if (!ok) break;
 
       // ---- epilogue
-      const bool steps = j1 > j0;
+      const bool steps = pc.j1 > pc.j0;
       const int slot = pc.slot, head0 = pc.head0;
-      const bool valid_row = my_token < rows_t && my_token < p.tile.tokens && my_head < pc.heads;
+      const int my_token = row / p.tile.heads, my_head = row - my_token * p.tile.heads;
+      const bool valid_row = my_token < min(pc.tokens - t * p.tile.tokens, p.tile.tokens) && my_head < pc.heads;
       const int64_t tok = static_cast<int64_t>(pc.row0) + t * p.tile.tokens + my_token;
       arrive(&bar_wfree[k & 1]);
       if (steps) {
@@ -693,7 +705,8 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
       const bool nan_row = !(l >= 0.f);  // its output is NaN
 #pragma unroll 1
       for (int c = 0; c < DV / 32; ++c) {
-        uint32_t o[32];
+        // (not left undefined: the compiler kept room for it through the steps, and spilled 160 bytes there)
+        uint32_t o[32] = {};
         if (steps && !idle) {
           tmem_ld32(tO + c * 32, o);
           tmem_ld_wait();
@@ -744,13 +757,20 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attn_join_kernel(const __grid
   __shared__ float s_m[kGroups][128], s_l[kGroups][128];
   __shared__ float4 s_v[kGroups][128];
   pdl_wait();
-  if (*reinterpret_cast<volatile int*>(p.status) != 0) return;  // pieces may be missing
-  const int n_slots = min(*p.n_slots, p.max_slots);
   const int chunks = (p.rows_cap * (DV / 4) + 127) / 128;
   const int grp = threadIdx.x >> 7, lane = threadIdx.x & 127;
-  for (int64_t item = blockIdx.x; item < static_cast<int64_t>(n_slots) * chunks; item += gridDim.x) {
-    const int slot = static_cast<int>(item / chunks), i = static_cast<int>(item - static_cast<int64_t>(slot) * chunks) * 128 + lane;
-    const KvPair e = p.pairs[slot];
+  int slot = blockIdx.x / chunks, chunk = blockIdx.x - slot * chunks;
+  // (the first pair's record is read along with what says whether it counts)
+  KvPair e = p.pairs[min(slot, p.max_slots - 1)];
+  const int n_slots = min(*p.n_slots, p.max_slots);
+  if (*reinterpret_cast<volatile int*>(p.status) != 0) return;  // pieces may be missing
+  for (int64_t item = blockIdx.x; slot < n_slots; item += gridDim.x) {
+    if (item != blockIdx.x) {
+      slot = static_cast<int>(item / chunks), chunk = static_cast<int>(item - static_cast<int64_t>(slot) * chunks);
+      if (slot >= n_slots) break;
+      e = p.pairs[slot];
+    }
+    const int i = chunk * 128 + lane;
     const int rows = e.tokens * p.tile.heads;
     if (e.pieces <= 0 || slot + e.pieces > n_slots || e.row0 < 0 || e.row0 + e.tokens > p.seqs.T || rows > p.rows_cap) continue;
     if ((i - lane) / (DV / 4) >= rows) continue;  // the same for every thread
@@ -828,7 +848,7 @@ Workspace workspace_of(int64_t T, int64_t group, int dqk, int dv, int32_t q_len)
   const int64_t most = std::max<int64_t>(1, q_len > 0 ? q_len : T);  // new tokens of a sequence
   Workspace w;
   w.rows_cap = std::min<int64_t>(tiles * tile.tokens, most) * tile.heads;
-  w.max_slots = 4LL * grid_of(dqk, dv) + 8;
+  w.max_slots = max_joined(grid_of(dqk, dv));
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   w.pairs = 256;
   w.ml = w.pairs + up(w.max_slots * sizeof(KvPair));

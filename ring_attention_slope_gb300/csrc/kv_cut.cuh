@@ -1,5 +1,5 @@
-// How the kernels on the paged cache share their work out: every CTA reads the sequences' lengths, works out the same
-// cut into pieces, and claims pieces from a counter until none is left.
+// How the kernels on the paged cache share their work out: every CTA's producer warp reads the sequences' lengths, works
+// out the same cut into pieces, and claims pieces from a counter until none is left.
 //
 // A sequence's work is `heads` times `blocks` pairs of up to `steps` steps each (what a step is, the kernel says).  A
 // pair is cut into equal pieces of at most `per` steps.
@@ -9,126 +9,105 @@
 
 namespace slope {
 
-constexpr int kTries = 6;  // lengths of pieces that are tried
-
 struct SeqCut {
   int blocks, steps;
 };
 __device__ __forceinline__ int pieces_of(int steps, int per) { return max(1, (steps + per - 1) / per); }
 
-constexpr int kCutWarps = 12;  // of a CTA at most
-struct CutScratch {
-  unsigned long long sums[kCutWarps][kTries];
-  int most[kCutWarps];
-  uint32_t total, slots;  // pieces, and those of pairs with several
-  int per;
-};
-
 // The sequences' records and first pieces, in shared memory.
 struct CutLists {
   KvSeq seqs[kKvMaxSeqs];
-  uint32_t units[kKvMaxSeqs + 1];  // pieces before the sequence's
-  uint32_t slots[kKvMaxSeqs + 1];  // joined pieces before the sequence's
+  uint32_t units[kKvMaxSeqs];  // pieces before the sequence's
+  uint32_t slots[kKvMaxSeqs];  // joined pieces before the sequence's
 };
+struct Cut {
+  uint32_t total, slots;  // pieces, and those of pairs with several
+  int per;
+};
+// Joined pieces of a launch at most: no length of pieces is below half a share of the steps (an even division of them
+// by the grid), and a pair of several pieces has fewer than twice as many as its steps divided by their length.
+inline int64_t max_joined(int64_t grid) { return 4 * grid + grid / 8 + 8; }
 
-// Sums over the CTA's threads; every thread gets them.
-template <int kN>
-__device__ __forceinline__ void block_sums(CutScratch& s, unsigned long long (&v)[kN]) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
-  for (int i = 0; i < kN; ++i)
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], m);
-  __syncthreads();
-  if (lane == 0)
-#pragma unroll
-    for (int i = 0; i < kN; ++i) s.sums[warp][i] = v[i];
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kN; ++i) {
-    v[i] = 0;
-    for (int w = 0; w < warps; ++w) v[i] += s.sums[w][i];
-  }
+  for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+  return v;
 }
 
-// Every thread of the CTA calls it: reads the sequences, chooses the pieces' length and fills the lists.  cut_of(seq) gives a
+// One whole warp calls it: reads the sequences, chooses the pieces' length and fills the lists.  cut_of(seq) gives a
 // sequence's SeqCut; kPieceSteps is what a piece's start and end cost, in steps.
 //
-// Lengths from half to three times an even share of all steps are tried; the one whose rounds over the grid are
-// shortest wins.  No length is below half a share, so fewer than 4 * grid pieces are joined (a pair of several pieces
-// has fewer than twice as many as its steps divided by `per`).
-template <int kPieceSteps, typename Cut>
-__device__ __forceinline__ void make_cut(const KvSeqs& p, int heads, const Cut& cut_of, CutScratch& s, CutLists& lists) {
-  const int B = p.B;
-  unsigned long long all[1] = {0};
+// The longest pair is cut into pieces of about half to four times a share, and the length of those is tried as every
+// pair's.  The length with the least time wins: that of one piece or of an even share of all of them, whichever is more,
+// and half a piece for the uneven end where there are more pieces than CTAs.  (Estimates in fp32, the same in every CTA.)
+template <int kPieceSteps, typename CutOf>
+__device__ __forceinline__ Cut make_cut(const KvSeqs& p, int heads, const CutOf& cut_of, CutLists& lists) {
+  constexpr int kTries = 6;
+  constexpr float kShares[kTries] = {0.5f, 0.75f, 1.f, 1.5f, 2.5f, 4.f};
+  const int B = p.B, lane = threadIdx.x & 31;
+  const float per_cta = static_cast<float>(heads) / static_cast<float>(gridDim.x);
+  float all = 0.f;
   int most = 1;
-  for (int b = threadIdx.x; b < B; b += blockDim.x) {
+  for (int b = lane; b < B; b += 32) {
     const KvSeq q = kv_seq(p, b);
     lists.seqs[b] = q;
     const SeqCut c = cut_of(q);
-    all[0] += static_cast<unsigned long long>(c.blocks) * c.steps;
+    all += static_cast<float>(c.blocks) * static_cast<float>(c.steps);
     if (c.blocks > 0) most = max(most, c.steps);
   }
   most = __reduce_max_sync(0xffffffffu, most);
-  if ((threadIdx.x & 31) == 0) s.most[threadIdx.x >> 5] = most;
-  block_sums(s, all);  // (its barriers order s.most too)
-  for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) most = max(most, s.most[w]);
-  const unsigned long long share = max(1ull, (all[0] * heads + gridDim.x - 1) / gridDim.x);
-  constexpr int kQuarters[kTries] = {2, 3, 4, 5, 8, 12};  // of a share
+  const float share = fmaxf(1.f, warp_sum(all) * per_cta);
   int per[kTries];
-  unsigned long long count[kTries];
+  float count[kTries], inv[kTries];
 #pragma unroll
   for (int i = 0; i < kTries; ++i) {
-    per[i] = static_cast<int>(min(static_cast<unsigned long long>(most), (share * kQuarters[i] + 3) / 4));
-    count[i] = 0;
+    const float n = fmaxf(1.f, rintf(__fdividef(static_cast<float>(most), share * kShares[i])));  // pieces of the longest
+    per[i] = static_cast<int>(ceilf(__fdividef(static_cast<float>(most), n)));
+    if (2.f * static_cast<float>(per[i]) < share) per[i] = most;  // (see max_joined)
+    inv[i] = __frcp_rn(static_cast<float>(per[i]));
+    count[i] = 0.f;
   }
-  for (int b = threadIdx.x; b < B; b += blockDim.x) {
+  __syncwarp();
+  for (int b = lane; b < B; b += 32) {
     const SeqCut c = cut_of(lists.seqs[b]);
 #pragma unroll
-    for (int i = 0; i < kTries; ++i) count[i] += static_cast<unsigned long long>(c.blocks) * pieces_of(c.steps, per[i]);
+    for (int i = 0; i < kTries; ++i)
+      count[i] += static_cast<float>(c.blocks) * fmaxf(1.f, ceilf(static_cast<float>(c.steps) * inv[i] - 1e-4f));
   }
-  block_sums(s, count);
-  int best = per[0];
-  unsigned long long best_cost = ~0ull;
+  Cut r;
+  r.per = most;
+  float best = INFINITY;
 #pragma unroll
   for (int i = 0; i < kTries; ++i) {
-    const int pieces = pieces_of(most, per[i]);
-    const unsigned long long rounds = (count[i] * heads + gridDim.x - 1) / gridDim.x;
-    const unsigned long long cost = rounds * ((most + pieces - 1) / pieces + kPieceSteps);
-    if (cost < best_cost) {
-      best_cost = cost;
-      best = per[i];
+    const float rounds = warp_sum(count[i]) * per_cta, piece = static_cast<float>(per[i] + kPieceSteps);
+    const float cost = fmaxf(piece, share + rounds * kPieceSteps) + (rounds > 1.f ? 0.5f * piece : 0.f);
+    if (cost < best) {
+      best = cost;
+      r.per = per[i];
     }
   }
-  if (threadIdx.x < 32) {
-    const int lane = threadIdx.x;
-    uint32_t unit = 0, slot = 0;
-    for (int b0 = 0; b0 < B; b0 += 32) {
-      const int b = b0 + lane;
-      uint32_t u = 0, sl = 0;
-      if (b < B) {
-        const SeqCut c = cut_of(lists.seqs[b]);
-        const int n = pieces_of(c.steps, best);
-        u = static_cast<uint32_t>(heads) * c.blocks * n;
-        sl = n > 1 ? u : 0;
-      }
-      uint32_t iu = u, is = sl;
+  r.total = r.slots = 0;
+  for (int b0 = 0; b0 < B; b0 += 32) {
+    const int b = b0 + lane;
+    uint32_t u = 0, sl = 0;
+    if (b < B) {
+      const SeqCut c = cut_of(lists.seqs[b]);
+      const int n = pieces_of(c.steps, r.per);
+      u = static_cast<uint32_t>(heads) * c.blocks * n;
+      sl = n > 1 ? u : 0;
+    }
+    uint32_t iu = u, is = sl;
 #pragma unroll
-      for (int m = 1; m < 32; m <<= 1) {
-        const uint32_t ou = __shfl_up_sync(0xffffffffu, iu, m), os = __shfl_up_sync(0xffffffffu, is, m);
-        if (lane >= m) iu += ou, is += os;
-      }
-      if (b < B) lists.units[b] = unit + iu - u, lists.slots[b] = slot + is - sl;
-      unit += __shfl_sync(0xffffffffu, iu, 31);
-      slot += __shfl_sync(0xffffffffu, is, 31);
+    for (int m = 1; m < 32; m <<= 1) {
+      const uint32_t ou = __shfl_up_sync(0xffffffffu, iu, m), os = __shfl_up_sync(0xffffffffu, is, m);
+      if (lane >= m) iu += ou, is += os;
     }
-    if (lane == 0) {
-      s.total = unit;
-      s.slots = slot;
-      s.per = best;
-    }
+    if (b < B) lists.units[b] = r.total + iu - u, lists.slots[b] = r.slots + is - sl;
+    r.total += __shfl_sync(0xffffffffu, iu, 31);
+    r.slots += __shfl_sync(0xffffffffu, is, 31);
   }
-  __syncthreads();
+  __syncwarp();
+  return r;
 }
 
 // The sequence (of the launch) that piece w belongs to.
@@ -142,6 +121,13 @@ __device__ __forceinline__ int seq_of(const CutLists& lists, int B, uint32_t w) 
       hi = mid - 1;
   }
   return b;
+}
+
+// Steps [first, last) of piece c out of `pieces`.
+__device__ __forceinline__ void piece_steps(int steps, int pieces, int c, int& first, int& last) {
+  const int each = steps / pieces, more = steps - each * pieces;
+  first = c * each + min(c, more);
+  last = first + each + (c < more ? 1 : 0);
 }
 
 // For a CTA that takes no more pieces: claims until an index past the end comes back, so that every CTA takes exactly one

@@ -64,7 +64,6 @@ struct Cfg {
 };
 constexpr int kSoftmaxWarps = 8, kTmaWarp = 8, kMmaWarp = 9, kLseWarp = 10, kLseWarps = 2;
 constexpr int kThreads = 32 * (kLseWarp + kLseWarps);
-static_assert(kThreads / 32 <= kCutWarps, "the cut's scratch");
 
 __device__ __forceinline__ bool warp_all(bool v) { return __all_sync(0xffffffffu, v); }
 
@@ -114,9 +113,7 @@ __device__ __forceinline__ Piece make_piece(const KvWeightsParams& p, int per, c
   const int hi = p.window > 0 ? max(lo, min(q.n, last + p.window - r.pos0)) : q.n;
   r.blk0 = lo / p.tile.tokens;
   r.count = hi > lo ? (hi + p.tile.tokens - 1) / p.tile.tokens - r.blk0 : 0;
-  const int64_t steps = static_cast<int64_t>(r.count) * p.tile.parts;
-  r.i0 = static_cast<int>(steps * c / pieces);
-  r.i1 = static_cast<int>(steps * (c + 1) / pieces);
+  piece_steps(r.count * p.tile.parts, pieces, c, r.i0, r.i1);
   r.slot = pieces > 1 ? static_cast<int32_t>(lists.slots[b]) + (r.kvh * cut.blocks + blk) * pieces + c : -1;
   return r;
 }
@@ -142,7 +139,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ KvWeightsParams p) {
   using C = Cfg<DQK>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ CutScratch s_cut;
   __shared__ Piece s_piece[kPieces];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
@@ -183,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_barrier_init();
   }
   tc_fence_before_sync();
-  make_cut<kPieceSteps>(p.seqs, p.Hkv, cut_of, s_cut, lists);
+  __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = s_tmem;
   auto wait = [&](uint64_t* bar, uint32_t parity, int site) -> bool {
@@ -193,8 +189,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kTmaWarp) {
     // ================================================================ producer: pieces, pages, loads
-    if (lane == 0 && blockIdx.x == 0) *p.n_slots = static_cast<int32_t>(s_cut.slots);
-    const uint32_t total = s_cut.total;
+    const Cut cut = make_cut<kPieceSteps>(p.seqs, p.Hkv, cut_of, lists);
+    if (lane == 0 && blockIdx.x == 0) *p.n_slots = static_cast<int32_t>(cut.slots);
+    const uint32_t total = cut.total;
     const uint32_t q_bytes = static_cast<uint32_t>(p.tile.heads * p.tile.tokens) * 128 * C::kChunks;
     const int shift = p.seqs.page_shift;
     const int boxes_log = max(0, 7 - shift);  // log2 of the boxes of 64 channels of 128 keys
@@ -216,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t next = 0;
       if (lane == 0) next = atomicAdd(p.tile_counter, 1u);
       int pieces, c;
-      const Piece pc = make_piece(p, s_cut.per, lists, w, cut_of, pieces, c);
+      const Piece pc = make_piece(p, cut.per, lists, w, cut_of, pieces, c);
       if (lane == 0) {
         s_piece[k % kPieces] = pc;
         mbar_arrive(&bar_wfull[k % kPieces]);
@@ -480,7 +477,7 @@ struct Workspace {
 };
 Workspace workspace_of() {
   Workspace w;
-  w.max_slots = 4LL * kv_sm_count() + 8;
+  w.max_slots = max_joined(kv_sm_count());
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   w.pairs = 256;
   w.part = w.pairs + up(w.max_slots * sizeof(int4));
