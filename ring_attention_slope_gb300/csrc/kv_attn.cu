@@ -75,6 +75,7 @@ struct RowCut {
   int block_tokens, window;
   __device__ __forceinline__ SeqCut operator()(const KvSeq& s) const {
     SeqCut c;
+    c.join = true;
     c.blocks = (s.n + block_tokens - 1) / block_tokens;
     c.steps = (s.len + kBlockN - 1) / kBlockN;
     if (window > 0) c.steps = min(c.steps, (window + block_tokens - 2) / kBlockN + 2);

@@ -11,6 +11,7 @@ namespace slope {
 
 struct SeqCut {
   int blocks, steps;
+  bool join;  // the pieces of a pair are joined (else each writes results of its own)
 };
 __device__ __forceinline__ int pieces_of(int steps, int per) { return max(1, (steps + per - 1) / per); }
 
@@ -94,7 +95,7 @@ __device__ __forceinline__ Cut make_cut(const KvSeqs& p, int heads, const CutOf&
       const SeqCut c = cut_of(lists.seqs[b]);
       const int n = pieces_of(c.steps, r.per);
       u = static_cast<uint32_t>(heads) * c.blocks * n;
-      sl = n > 1 ? u : 0;
+      sl = n > 1 && c.join ? u : 0;
     }
     uint32_t iu = u, is = sl;
 #pragma unroll

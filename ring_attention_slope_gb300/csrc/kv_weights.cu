@@ -10,9 +10,12 @@
 // packed multiply-add and half a packed add, and no maximum, no sum across lanes and no second product: the bound is the
 // MUFU unit, at 4 cycles a warp's 32 exponentials (128 x 256 of them take 1024 cycles of an SM).
 //
-// The work: a pair is (sequence, KV head, 256 keys), its steps the row tiles (attention over few rows, a decode step,
-// has one or two, and then this kernel reads K at the copy rate, up to four key blocks ahead).  Pairs of many rows and
-// few keys are cut (kv_cut.cuh); their pieces leave 256 sums each in the workspace, which a second launch adds in order.
+// The work: where the new rows fill several tiles, a pair is (sequence, KV head, 256 keys) and its steps the row tiles
+// that see one of the keys; pairs of many rows and few keys are cut (kv_cut.cuh), and the pieces leave 256 sums each in the
+// workspace, which a second launch adds in order.  Where the rows are one tile (a decode step), a pair is (sequence, KV
+// head) and its steps the blocks of 256 keys: the rows stay and the keys stream past, read once, and nothing is joined.
+// Sixteen softmax warps: the four warps of (buffer, key tile) take every second step, so that each SM sub-partition has four
+// warps with exponentials to issue.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -50,43 +53,63 @@ struct KvWeightsParams {
   uint64_t wait_limit_ns;
 };
 
+constexpr int kSoftmaxWarps = 16, kTmaWarp = 16, kMmaWarp = 17, kLseWarp = 18, kLseWarps = 2;
+constexpr int kThreads = 32 * (kLseWarp + kLseWarps);
+
+// A piece: of a pair of rows that fill several tiles, row tiles [i0, i1) of one key block, numbered from 0 among the
+// `count` of every part that see one of its keys; else key blocks [i0, i1) and one row tile.
+struct Piece {
+  int32_t b;  // sequence; -1: no pieces left
+  int32_t few;
+  int32_t kvh, key0, len;  // (key0: of the block, or of block i0)
+  int32_t row0, n, pos0;   // of the sequence: first q row, new tokens, position of the first
+  int32_t blk0, count;     // first row block that sees a key, and how many
+  int32_t i0, i1;
+  int32_t slot;
+};
+
 template <int DQK>
 struct Cfg {
   static constexpr int kChunks = DQK / 64;
-  static constexpr int kTileBytes = kChunks * kChunkBytes;  // 128 rows of K or Q
-  static constexpr int kKSlots = DQK == 64 ? 4 : DQK == 128 ? 2 : 1;  // of 256 keys
+  static constexpr int kTileBytes = kChunks * kChunkBytes;             // 128 rows of K or Q
+  static constexpr int kKSlots = DQK == 64 ? 8 : DQK == 128 ? 4 : 2;   // of 128 keys
   static constexpr int kQSlots = DQK == 64 ? 4 : 2;
-  static constexpr int kQOffset = kKSlots * 2 * kTileBytes;
-  static constexpr int kLseOffset = kQOffset + kQSlots * kTileBytes;
-  static constexpr int kListOffset = kLseOffset + kQSlots * 128 * 4;
-  static constexpr int kSmemBytes = 1024 + kListOffset + static_cast<int>(sizeof(CutLists));
-  static_assert(kSmemBytes <= 231424, "shared memory budget");
+  static constexpr int kQOffset = kKSlots * kTileBytes;
+  static constexpr int kRestOffset = kQOffset + kQSlots * kTileBytes;
+  struct Rest {  // behind the tiles
+    float lse[kQSlots][128];        // -lse log2(e) of a row tile's columns
+    float few_lse[kPieces][128];    // of a piece's one row tile
+    float sums[kPieces][2][kBlockN];  // [piece][key tile]: what the second buffer's warps found
+    uint64_t kfull[kKSlots], kempty[kKSlots], qfull[kQSlots], qempty[kQSlots];
+    uint64_t s[4], sfree[4];  // [2 * buffer + key tile]
+    uint64_t wfull[kPieces], wfree[kPieces], few_full[kPieces], sums_full[kPieces][2], drain;
+    Piece piece[kPieces];
+    uint32_t tmem;
+    int abort;
+    CutLists lists;
+  };
+  static constexpr int kSmemBytes = kRestOffset + static_cast<int>(sizeof(Rest));
+  static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
-constexpr int kSoftmaxWarps = 8, kTmaWarp = 8, kMmaWarp = 9, kLseWarp = 10, kLseWarps = 2;
-constexpr int kThreads = 32 * (kLseWarp + kLseWarps);
 
 __device__ __forceinline__ bool warp_all(bool v) { return __all_sync(0xffffffffu, v); }
 
-// Key blocks of a sequence, and the row tiles that one of them meets at most.  (The row tiles of a group of more than
-// 128 heads are those of its parts, one part after another.)
+// Key blocks of a sequence, and the row tiles that one of them meets at most (those of a group of more than 128 heads are
+// its parts', one part after another); with one row tile, that and the key blocks.
 struct KeyCut {
   RowTile tile;
+  bool accumulate;
+  __device__ __forceinline__ int row_tiles(const KvSeq& s) const {
+    return (s.n + tile.tokens - 1) / tile.tokens * tile.parts;
+  }
   __device__ __forceinline__ SeqCut operator()(const KvSeq& s) const {
+    const int rows = row_tiles(s), keys = (s.len + kKeys - 1) / kKeys;
     SeqCut c;
-    c.blocks = (s.len + kKeys - 1) / kKeys;
-    c.steps = (s.n + tile.tokens - 1) / tile.tokens * tile.parts;
+    c.join = rows > 1;
+    c.blocks = c.join ? keys : keys > 0 && !(rows == 0 && accumulate) ? 1 : 0;
+    c.steps = c.join ? rows : keys;
     return c;
   }
-};
-
-// A piece: row tiles [i0, i1) of a key block, numbered from 0 among the `count` of every part that see one of its keys.
-struct Piece {
-  int32_t b;  // sequence; -1: no pieces left
-  int32_t kvh, key0, len;
-  int32_t row0, n, pos0;  // of the sequence: first q row, new tokens, position of the first
-  int32_t blk0, count;    // first row block that sees a key, and how many
-  int32_t i0, i1;
-  int32_t slot;
 };
 
 __device__ __forceinline__ Piece make_piece(const KvWeightsParams& p, int per, const CutLists& lists, uint32_t w,
@@ -102,11 +125,20 @@ __device__ __forceinline__ Piece make_piece(const KvWeightsParams& p, int per, c
   c = static_cast<int>(local % pieces);
   r.kvh = static_cast<int>(local / pieces);
   r.b = p.seqs.b0 + b;
-  r.key0 = blk * kKeys;
+  r.few = cut.join ? 0 : 1;
   r.len = q.len;
   r.row0 = q.row0;
   r.n = q.n;
   r.pos0 = q.len - q.n;
+  r.slot = -1;
+  if (r.few) {
+    piece_steps(cut.steps, pieces, c, r.i0, r.i1);
+    r.key0 = r.i0 * kKeys;
+    r.blk0 = 0;
+    r.count = q.n > 0 ? 1 : 0;
+    return r;
+  }
+  r.key0 = blk * kKeys;
   // tokens [lo, hi) see one of the keys [key0, last]
   const int last = min(q.len, r.key0 + kKeys) - 1;
   const int lo = min(q.n, max(0, r.key0 - r.pos0));
@@ -114,7 +146,7 @@ __device__ __forceinline__ Piece make_piece(const KvWeightsParams& p, int per, c
   r.blk0 = lo / p.tile.tokens;
   r.count = hi > lo ? (hi + p.tile.tokens - 1) / p.tile.tokens - r.blk0 : 0;
   piece_steps(r.count * p.tile.parts, pieces, c, r.i0, r.i1);
-  r.slot = pieces > 1 ? static_cast<int32_t>(lists.slots[b]) + (r.kvh * cut.blocks + blk) * pieces + c : -1;
+  if (pieces > 1) r.slot = static_cast<int32_t>(lists.slots[b]) + (r.kvh * cut.blocks + blk) * pieces + c;
   return r;
 }
 
@@ -123,11 +155,12 @@ struct Rows {
   int token, tokens;  // first token among the sequence's new ones, and how many
   int head, heads;    // first head in the group, and how many
 };
-__device__ __forceinline__ Rows rows_of(const KvWeightsParams& p, int i, int blk0, int count, int n) {
+__device__ __forceinline__ Rows rows_of(const KvWeightsParams& p, int i, const Piece& pc) {
   Rows r;
-  const int part = p.tile.parts > 1 ? i / count : 0;
-  r.token = (blk0 + i - part * count) * p.tile.tokens;
-  r.tokens = min(p.tile.tokens, n - r.token);
+  if (pc.few) i = 0;
+  const int part = p.tile.parts > 1 && !pc.few ? i / pc.count : 0;
+  r.token = (pc.blk0 + i - part * pc.count) * p.tile.tokens;
+  r.tokens = min(p.tile.tokens, pc.n - r.token);
   r.head = part * p.tile.heads;
   r.heads = min(p.tile.heads, p.group - r.head);
   return r;
@@ -138,22 +171,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     kv_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ KvWeightsParams p) {
   using C = Cfg<DQK>;
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ Piece s_piece[kPieces];
-  __shared__ uint32_t s_tmem;
-  __shared__ int s_abort;
-  __shared__ uint64_t bar_kfull[C::kKSlots], bar_kempty[C::kKSlots], bar_qfull[C::kQSlots], bar_qempty[C::kQSlots];
-  __shared__ uint64_t bar_s[4], bar_sfree[4];  // [2 * buffer + key tile]
-  __shared__ uint64_t bar_wfull[kPieces], bar_wfree[kPieces], bar_drain;
-  uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];  // all of the shared memory: it starts on a tile's boundary
   uint8_t* const sK = smem;
   uint8_t* const sQ = smem + C::kQOffset;
-  float* const sLse = reinterpret_cast<float*>(smem + C::kLseOffset);  // [slot][column]: -lse log2(e)
-  CutLists& lists = *reinterpret_cast<CutLists*>(smem + C::kListOffset);
-  volatile int* const cta_abort = &s_abort;
+  typename C::Rest& sh = *reinterpret_cast<typename C::Rest*>(smem + C::kRestOffset);
+  volatile int* const cta_abort = &sh.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t limit = p.wait_limit_ns;
-  const KeyCut cut_of{p.tile};
+  const KeyCut cut_of{p.tile, p.accumulate != 0};
 
   pdl_launch_dependents();
   uint32_t claimed = 0;
@@ -164,32 +189,41 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 0) *cta_abort = *reinterpret_cast<volatile int*>(p.status) != 0 ? 1 : 0;
   if (warp == kMmaWarp) {
-    tmem_alloc(&s_tmem, 512);
+    tmem_alloc(&sh.tmem, 512);
     tmem_relinquish();
   }
   if (threadIdx.x == kMmaWarp * 32) {
-    for (int i = 0; i < C::kKSlots; ++i) mbar_init(&bar_kfull[i], 1), mbar_init(&bar_kempty[i], 1);
+    for (int i = 0; i < C::kKSlots; ++i) mbar_init(&sh.kfull[i], 1), mbar_init(&sh.kempty[i], 1);
     for (int i = 0; i < C::kQSlots; ++i) {
-      mbar_init(&bar_qfull[i], 2);                   // the loads, and the lse
-      mbar_init(&bar_qempty[i], 1 + kSoftmaxWarps);  // the products, and the lse's readers
+      mbar_init(&sh.qfull[i], 2);                       // the loads, and the lse
+      mbar_init(&sh.qempty[i], 1 + kSoftmaxWarps / 2);  // the products, and the readers of the last step's lse
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&bar_s[i], 1), mbar_init(&bar_sfree[i], 4);
-    for (int i = 0; i < kPieces; ++i) mbar_init(&bar_wfull[i], 1), mbar_init(&bar_wfree[i], 1 + kLseWarps + kSoftmaxWarps);
-    mbar_init(&bar_drain, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&sh.s[i], 1), mbar_init(&sh.sfree[i], 4);
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(&sh.wfull[i], 1);
+      mbar_init(&sh.wfree[i], 1 + kLseWarps + kSoftmaxWarps);
+      mbar_init(&sh.few_full[i], 1);
+      for (int t = 0; t < 2; ++t) mbar_init(&sh.sums_full[i][t], 4);
+    }
+    mbar_init(&sh.drain, 1);
     fence_barrier_init();
   }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = sh.tmem;
   auto wait = [&](uint64_t* bar, uint32_t parity, int site) -> bool {
     return wait_bounded(bar, parity & 1, cta_abort, p.status, limit, site);
   };
-  auto take_piece = [&](int k) -> bool { return wait(&bar_wfull[k % kPieces], k / kPieces, 61); };
+  auto take_piece = [&](int k) -> bool { return wait(&sh.wfull[k % kPieces], k / kPieces, 61); };
+  auto arrive = [&](uint64_t* bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
 
   if (warp == kTmaWarp) {
     // ================================================================ producer: pieces, pages, loads
-    const Cut cut = make_cut<kPieceSteps>(p.seqs, p.Hkv, cut_of, lists);
+    const Cut cut = make_cut<kPieceSteps>(p.seqs, p.Hkv, cut_of, sh.lists);
     if (lane == 0 && blockIdx.x == 0) *p.n_slots = static_cast<int32_t>(cut.slots);
     const uint32_t total = cut.total;
     const uint32_t q_bytes = static_cast<uint32_t>(p.tile.heads * p.tile.tokens) * 128 * C::kChunks;
@@ -198,63 +232,74 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int boxes = 1 << boxes_log, box_rows = kBlockN >> boxes_log;
     const int no_page = static_cast<int>(p.seqs.n_pages);  // reads 0
     uint32_t w = __shfl_sync(0xffffffffu, claimed, 0);
-    int kcnt = 0, qcnt = 0;  // K blocks and row tiles loaded
+    int kcnt = 0, qcnt = 0;  // key tiles and row tiles loaded
     bool ok = *cta_abort == 0;
     for (int k = 0; ok; ++k) {
-      if (k >= kPieces) ok = warp_all(wait(&bar_wfree[k % kPieces], k / kPieces - 1, 62));
+      if (k >= kPieces) ok = warp_all(wait(&sh.wfree[k % kPieces], k / kPieces - 1, 62));
       if (!ok) break;
       if (w >= total) {
         if (lane == 0) {
-          s_piece[k % kPieces].b = -1;
-          mbar_arrive(&bar_wfull[k % kPieces]);
+          sh.piece[k % kPieces].b = -1;
+          mbar_arrive(&sh.wfull[k % kPieces]);
         }
         break;
       }
       uint32_t next = 0;
       if (lane == 0) next = atomicAdd(p.tile_counter, 1u);
       int pieces, c;
-      const Piece pc = make_piece(p, cut.per, lists, w, cut_of, pieces, c);
+      const Piece pc = make_piece(p, cut.per, sh.lists, w, cut_of, pieces, c);
       if (lane == 0) {
-        s_piece[k % kPieces] = pc;
-        mbar_arrive(&bar_wfull[k % kPieces]);
+        sh.piece[k % kPieces] = pc;
+        mbar_arrive(&sh.wfull[k % kPieces]);
         if (pc.slot >= 0) p.pairs[pc.slot] = make_int4(pc.b, pc.kvh, pc.key0 / kKeys, c == 0 ? pieces : 0);
       }
-      if (pc.i1 > pc.i0) {
-        // ---- the keys: lane i looks up page i of the block, then loads boxes lane, lane + 32, ...
-        const int slot = kcnt % C::kKSlots;
-        const int32_t* const row = p.seqs.table + pc.b * p.seqs.table_stride;
-        const int64_t at = static_cast<int64_t>(pc.key0) + lane * box_rows;
-        int page = no_page;
-        if (lane < 2 * boxes && at < pc.len) {
-          const int pg = row[at >> shift];
-          if (pg >= 0 && pg < no_page) page = pg;
+      const int32_t* const row = p.seqs.table + pc.b * p.seqs.table_stride;
+      // page of the keys of box `lane` of a key block (two tiles of `boxes` each)
+      auto page_of = [&](int key0) -> int {
+        const int64_t at = static_cast<int64_t>(key0) + lane * box_rows;
+        if (lane >= 2 * boxes || at >= pc.len) return no_page;
+        const int pg = row[at >> shift];
+        return pg >= 0 && pg < no_page ? pg : no_page;
+      };
+      auto load_keys = [&](int key0, int page) -> bool {
+        for (int t = 0; t < 2; ++t, ++kcnt) {
+          const int slot = kcnt % C::kKSlots;
+          if (!warp_all(wait(&sh.kempty[slot], kcnt / C::kKSlots + 1, 63))) return false;
+          if (lane == 0) mbar_arrive_expect_tx(&sh.kfull[slot], C::kTileBytes);
+          // lane i loads box i % boxes of channel chunk i / boxes
+          const int box = lane & (boxes - 1), chunk = lane >> boxes_log;
+          const int pg = __shfl_sync(0xffffffffu, page, t * boxes + box);
+          if (chunk < C::kChunks)
+            tma_load_4d(sK + slot * C::kTileBytes + chunk * kChunkBytes + box * box_rows * 128, &tm_k, &sh.kfull[slot],
+                        64 * chunk, (key0 + t * kBlockN + box * box_rows) & ((1 << shift) - 1), pc.kvh, pg);
         }
-        ok = warp_all(wait(&bar_kempty[slot], kcnt / C::kKSlots + 1, 63));
-        if (ok) {
-          if (lane == 0) mbar_arrive_expect_tx(&bar_kfull[slot], 2 * C::kTileBytes);
-          __syncwarp();
-          for (int i0 = 0; i0 < 2 * boxes * C::kChunks; i0 += 32) {
-            const int i = i0 + lane, box = i & (2 * boxes - 1), chunk = i >> (boxes_log + 1);
-            const int pg = __shfl_sync(0xffffffffu, page, box);
-            if (chunk < C::kChunks) {
-              const int tile = box >> boxes_log, in_tile = box & (boxes - 1);
-              tma_load_4d(sK + (slot * 2 + tile) * C::kTileBytes + chunk * kChunkBytes + in_tile * box_rows * 128, &tm_k,
-                          &bar_kfull[slot], 64 * chunk, (pc.key0 + box * box_rows) & ((1 << shift) - 1), pc.kvh, pg);
-            }
-          }
-          ++kcnt;
+        return true;
+      };
+      auto load_rows = [&](int i) -> bool {
+        const int qs = qcnt % C::kQSlots;
+        if (!warp_all(wait(&sh.qempty[qs], qcnt / C::kQSlots + 1, 64))) return false;
+        if (lane == 0) {
+          const Rows r = rows_of(p, i, pc);
+          mbar_arrive_expect_tx(&sh.qfull[qs], q_bytes);
+          for (int ch = 0; ch < C::kChunks; ++ch)
+            tma_load_3d(sQ + qs * C::kTileBytes + ch * kChunkBytes, &tm_q, &sh.qfull[qs], 64 * ch,
+                        pc.kvh * p.group + r.head, pc.row0 + r.token);
         }
-        for (int i = pc.i0; ok && i < pc.i1; ++i, ++qcnt) {
-          const int qs = qcnt % C::kQSlots;
-          ok = warp_all(wait(&bar_qempty[qs], qcnt / C::kQSlots + 1, 64));
-          if (!ok) break;
-          if (lane == 0) {
-            const Rows r = rows_of(p, i, pc.blk0, pc.count, pc.n);
-            mbar_arrive_expect_tx(&bar_qfull[qs], q_bytes);
-            for (int ch = 0; ch < C::kChunks; ++ch)
-              tma_load_3d(sQ + qs * C::kTileBytes + ch * kChunkBytes, &tm_q, &bar_qfull[qs], 64 * ch,
-                          pc.kvh * p.group + r.head, pc.row0 + r.token);
+        ++qcnt;
+        return true;
+      };
+      if (pc.i1 > pc.i0 && pc.count > 0) {
+        int page = page_of(pc.key0);
+        if (pc.few) {
+          ok = load_rows(0);
+          for (int i = pc.i0; ok && i < pc.i1; ++i) {
+            const int ahead = i + 1 < pc.i1 ? page_of((i + 1) * kKeys) : no_page;
+            ok = load_keys(i * kKeys, page);
+            page = ahead;
           }
+        } else {
+          ok = load_keys(pc.key0, page);
+          for (int i = pc.i0; ok && i < pc.i1; ++i) ok = load_rows(i);
         }
       }
       w = __shfl_sync(0xffffffffu, next, 0);
@@ -265,177 +310,226 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the loads already issued land before the CTA gives up its shared memory (the row tiles' barriers also count
         // the lse's arrival, which may never come: their bytes are waited for as long as the limit says)
         for (int i = 0; i < C::kKSlots && i < kcnt; ++i)
-          wait_final(&bar_kfull[i], ((kcnt - 1 - i) / C::kKSlots) & 1, limit);
+          wait_final(&sh.kfull[i], ((kcnt - 1 - i) / C::kKSlots) & 1, limit);
         for (int i = 0; i < C::kQSlots && i < qcnt; ++i)
-          wait_final(&bar_qfull[i], ((qcnt - 1 - i) / C::kQSlots) & 1, limit);
+          wait_final(&sh.qfull[i], ((qcnt - 1 - i) / C::kQSlots) & 1, limit);
       }
     }
   } else if (warp >= kLseWarp) {
     // ================================================================ the rows' lse, next to their tile
-    // Each warp takes every second row tile, and has its next one's loads on their way while it waits for a slot.
+    // Each warp takes every second row tile (or piece of one), and has its next one's loads on their way while it
+    // waits for a slot.
+    const int me = warp - kLseWarp;
     int qcnt = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
       if (!warp_all(take_piece(k))) break;
-      const Piece pc = s_piece[k % kPieces];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar_wfree[k % kPieces]);
+      const Piece pc = sh.piece[k % kPieces];
       if (pc.b < 0) break;
+      const int tiles = pc.i1 <= pc.i0 || pc.count == 0 ? 0 : pc.few ? 1 : pc.i1 - pc.i0;
       float next[4];
       auto fetch = [&](int i) {
-        const Rows r = rows_of(p, i, pc.blk0, pc.count, pc.n);
+        const Rows r = rows_of(p, i, pc);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int col = lane + 32 * j, token = col / p.tile.heads, head = col - token * p.tile.heads;
           next[j] = -INFINITY;
-          if (i < pc.i1 && token < r.tokens && head < r.heads)
+          if (token < r.tokens && head < r.heads)
             next[j] = p.lse[(static_cast<int64_t>(pc.kvh) * p.group + r.head + head) * p.lse_shead +
                             (static_cast<int64_t>(pc.row0) + r.token + token) * p.lse_srow];
         }
       };
-      const int first = pc.i0 + ((qcnt ^ (warp - kLseWarp)) & 1);
-      if (first < pc.i1) fetch(first);
-      for (int i = first; i < pc.i1; i += kLseWarps) {
+      const int first = (qcnt ^ me) & 1;
+      if (first < tiles) fetch(pc.i0 + first);
+      for (int i = first; i < tiles; i += kLseWarps) {
         float v[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = next[j];
-        fetch(min(i + kLseWarps, pc.i1 - 1));
-        const int at = qcnt + (i - pc.i0), qs = at % C::kQSlots;
-        ok = warp_all(wait(&bar_qempty[qs], at / C::kQSlots + 1, 65));
+        for (int j = 0; j < 4; ++j) v[j] = next[j] == -INFINITY ? next[j] : -next[j] * kLog2e;
+        if (i + kLseWarps < tiles) fetch(pc.i0 + i + kLseWarps);
+        const int at = qcnt + i, qs = at % C::kQSlots;
+        ok = warp_all(wait(&sh.qempty[qs], at / C::kQSlots + 1, 65));
         if (!ok) break;
+        float* const dst = pc.few ? sh.few_lse[k % kPieces] : sh.lse[qs];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sLse[qs * 128 + lane + 32 * j] = v[j] == -INFINITY ? v[j] : -v[j] * kLog2e;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_qfull[qs]);
+        for (int j = 0; j < 4; ++j) dst[lane + 32 * j] = v[j];
+        arrive(&sh.qfull[qs]);
+        if (pc.few && lane == 0) mbar_arrive(&sh.few_full[k % kPieces]);
       }
-      qcnt += pc.i1 - pc.i0;
+      if (ok && !(pc.few && tiles > 0) && me == 0 && lane == 0) mbar_arrive(&sh.few_full[k % kPieces]);
+      qcnt += tiles;
+      arrive(&sh.wfree[k % kPieces]);
     }
   } else if (warp == kMmaWarp) {
     // ================================================================ MMA issuer
     if (lane == 0) {
       constexpr uint32_t kDescHi = smem_desc_hi(1024, kSwizzle128B);
-      int kcnt = 0, qcnt = 0;
+      int kcnt = 0, qcnt = 0, scnt = 0;  // key tiles, row tiles, steps
+      // S^T of key tile t, in K slot `kslot`, and the row tile in slot qs
+      auto product = [&](int t, int kslot, int qs, int cols) -> bool {
+        const int buf = 2 * (scnt & 1) + t;
+        if (!wait(&sh.sfree[buf], (scnt >> 1) + 1, 68)) return false;
+        tc_fence_after_sync();
+        const uint32_t idesc = idesc_bf16_f32(kBlockM, 0, 0, 0) | (static_cast<uint32_t>(cols >> 3) << 17);
+        const uint32_t klo = smem_desc_lo(smem_u32(sK + kslot * C::kTileBytes), 16);
+        const uint32_t qlo = smem_desc_lo(smem_u32(sQ + qs * C::kTileBytes), 16);
+#pragma unroll
+        for (int kk = 0; kk < DQK / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * kChunkBytes + (kk & 3) * 32) >> 4;
+          mma_ss_lh(tmem + buf * 128, klo + off, kDescHi, qlo + off, kDescHi, idesc, kk > 0 ? 1u : 0u);
+        }
+        mma_commit(&sh.s[buf]);
+        return true;
+      };
       bool ok = true;
       for (int k = 0; ok; ++k) {
         if (!take_piece(k)) break;
-        const Piece pc = s_piece[k % kPieces];
-        mbar_arrive(&bar_wfree[k % kPieces]);
+        const Piece pc = sh.piece[k % kPieces];
+        mbar_arrive(&sh.wfree[k % kPieces]);
         if (pc.b < 0) break;
-        if (pc.i1 <= pc.i0) continue;
-        const int kslot = kcnt % C::kKSlots;
-        if (!wait(&bar_kfull[kslot], kcnt / C::kKSlots, 66)) break;
-        ++kcnt;
-        for (int i = pc.i0; ok && i < pc.i1; ++i, ++qcnt) {
+        if (pc.i1 <= pc.i0 || pc.count == 0) continue;
+        for (int i = pc.i0; ok && i < pc.i1; ++i, ++scnt) {
+          const bool new_keys = pc.few || i == pc.i0, new_rows = !pc.few || i == pc.i0;
+          const bool last_keys = pc.few || i == pc.i1 - 1, last_rows = !pc.few || i == pc.i1 - 1;
           const int qs = qcnt % C::kQSlots;
-          ok = wait(&bar_qfull[qs], qcnt / C::kQSlots, 67);
-          if (!ok) break;
-          const Rows r = rows_of(p, i, pc.blk0, pc.count, pc.n);
+          if (new_rows) ok = wait(&sh.qfull[qs], qcnt / C::kQSlots, 67);
+          const Rows r = rows_of(p, i, pc);
           const int cols = (r.tokens * p.tile.heads + 15) & ~15;  // 128 at most
-          const uint32_t idesc = idesc_bf16_f32(kBlockM, 0, 0, 0) | (static_cast<uint32_t>(cols >> 3) << 17);
-          const uint32_t qlo = smem_desc_lo(smem_u32(sQ + qs * C::kTileBytes), 16);
           for (int t = 0; t < 2 && ok; ++t) {
-            const int buf = 2 * (qcnt & 1) + t;
-            ok = wait(&bar_sfree[buf], (qcnt >> 1) + 1, 68);
-            if (!ok) break;
-            tc_fence_after_sync();
-            const uint32_t klo = smem_desc_lo(smem_u32(sK + (kslot * 2 + t) * C::kTileBytes), 16);
-#pragma unroll
-            for (int kk = 0; kk < DQK / 16; ++kk) {
-              const uint32_t off = ((kk >> 2) * kChunkBytes + (kk & 3) * 32) >> 4;
-              mma_ss_lh(tmem + buf * 128, klo + off, kDescHi, qlo + off, kDescHi, idesc, kk > 0 ? 1u : 0u);
-            }
-            mma_commit(&bar_s[buf]);
+            const int kslot = (kcnt + t) % C::kKSlots;
+            if (new_keys) ok = wait(&sh.kfull[kslot], (kcnt + t) / C::kKSlots, 66);
+            if (ok) ok = product(t, kslot, qs, cols);
+            if (ok && last_keys) mma_commit(&sh.kempty[kslot]);
           }
-          if (ok) mma_commit(&bar_qempty[qs]);
+          if (ok && last_rows) mma_commit(&sh.qempty[qs]);
+          if (last_keys) kcnt += 2;
+          if (last_rows) ++qcnt;
         }
-        if (ok) mma_commit(&bar_kempty[kslot]);
       }
-      mma_commit(&bar_drain);
-      wait_final(&bar_drain, 0, limit);
+      mma_commit(&sh.drain);
+      wait_final(&sh.drain, 0, limit);
     }
   } else {
     // ================================================================ a key to a thread
-    const int t = warp >> 2;
-    const int key = t * kBlockN + (warp & 3) * 32 + lane;  // in the block
-    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const int buf = warp >> 3, t = (warp >> 2) & 1;
+    const int row = (warp & 3) * 32 + lane, key = t * kBlockN + row;  // in the block
+    const uint32_t tS = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + (2 * buf + t) * 128;
     const uint64_t sl2 = pack_f32x2(p.scale_log2, p.scale_log2);
-    int qcnt = 0;
+    int qcnt = 0, scnt = 0;
     bool ok = true;
+    // The sum over row tile i's columns that see the key at position pos.
+    auto columns = [&](const Piece& pc, int i, int step, int pos, const float* lse, float& sum) -> bool {
+      const int b = 2 * buf + t;
+      const Rows r = rows_of(p, i, pc);
+      const int cols = r.tokens * p.tile.heads, qa = pc.pos0 + r.token, qb = qa + r.tokens - 1;
+      // tokens from the key's position on, and up to the window's end
+      const int lo = min(max(0, pos - qa), r.tokens) * p.tile.heads;
+      const int hi = p.window > 0 && pos + p.window - 1 < qb ? max(0, pos + p.window - qa) * p.tile.heads : cols;
+      const int kfirst = pos - row, klast = kfirst + kBlockN - 1;
+      const bool all = klast <= qa && (p.window == 0 || qb - kfirst < p.window);  // every row sees every key
+      if (!warp_all(wait(&sh.s[b], step >> 1, 70))) return false;
+      tc_fence_after_sync();
+      uint64_t acc[2] = {0, 0};
+#pragma unroll 1
+      for (int c = 0; c < cols; c += 32) {
+        uint32_t s[32];
+        tmem_ld32(tS + c, s);
+        tmem_ld_wait();
+        reg_fence(s);
+        if (c + 32 >= cols) {  // the scores are in registers
+          tc_fence_before_sync();
+          arrive(&sh.sfree[b]);
+        }
+        float x[32];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float4 n = *reinterpret_cast<const float4*>(lse + c + 4 * e);
+          const float2 a = unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(s[4 * e]), __uint_as_float(s[4 * e + 1])), sl2,
+                                                  pack_f32x2(n.x, n.y)));
+          const float2 z = unpack_f32x2(fma_f32x2(
+              pack_f32x2(__uint_as_float(s[4 * e + 2]), __uint_as_float(s[4 * e + 3])), sl2, pack_f32x2(n.z, n.w)));
+          x[4 * e] = a.x, x[4 * e + 1] = a.y, x[4 * e + 2] = z.x, x[4 * e + 3] = z.y;
+        }
+        if (!(all && c + 32 <= cols)) {  // whatever hidden rows and columns without a row hold does not count
+          const uint32_t span = static_cast<uint32_t>(max(0, hi - lo));
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (static_cast<uint32_t>(c + e - lo) >= span) x[e] = -INFINITY;
+        }
+        if (r.heads < p.tile.heads) {  // the last part of a group of more than 128 heads
+          uint32_t none = 0;
+#pragma unroll 1
+          for (int e = 0; e < 32; ++e) none |= ((c + e) % p.tile.heads >= r.heads ? 1u : 0u) << e;
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if ((none >> e) & 1u) x[e] = -INFINITY;
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          acc[e & 1] = add_f32x2(acc[e & 1], pack_f32x2(ex2_approx(x[2 * e]), ex2_approx(x[2 * e + 1])));
+      }
+      const float2 a = unpack_f32x2(acc[0]), z = unpack_f32x2(acc[1]);
+      sum = (a.x + a.y) + (z.x + z.y);
+      return true;
+    };
     for (int k = 0; ok; ++k) {
       if (!warp_all(take_piece(k))) break;
-      const Piece pc = s_piece[k % kPieces];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar_wfree[k % kPieces]);
+      const Piece pc = sh.piece[k % kPieces];
       if (pc.b < 0) break;
-      const int pos = pc.key0 + key;
-      // the place of the key's weight, looked up ahead of the sums
-      float* dst = nullptr;
-      if (pc.slot < 0 && pos < pc.len) {
+      const int steps = pc.count == 0 ? 0 : max(0, pc.i1 - pc.i0);
+      // the place of a key's weight (looked up ahead of the sums)
+      auto place = [&](int pos) -> float* {
+        if (pos >= pc.len) return nullptr;
         const int pg = p.seqs.table[pc.b * p.seqs.table_stride + (pos >> p.seqs.page_shift)];
-        if (pg >= 0 && pg < p.seqs.n_pages)
-          dst = p.weights + pg * p.w_spage + pc.kvh * p.w_shead + (pos & ((1 << p.seqs.page_shift) - 1));
-      }
-      const int kfirst = pc.key0 + t * kBlockN, klast = kfirst + kBlockN - 1;
-      float total = 0.f;
-      for (int i = pc.i0; ok && i < pc.i1; ++i, ++qcnt) {
-        const int qs = qcnt % C::kQSlots, buf = 2 * (qcnt & 1) + t;
-        const Rows r = rows_of(p, i, pc.blk0, pc.count, pc.n);
-        const int cols = r.tokens * p.tile.heads, qa = pc.pos0 + r.token, qb = qa + r.tokens - 1;
-        // the columns whose rows see this key: tokens from its position on, and up to the window's end
-        const int lo = max(0, pos - qa) * p.tile.heads;
-        const int hi = p.window > 0 && pos + p.window - 1 < qb ? (pos + p.window - qa) * p.tile.heads : cols;
-        const bool all = klast <= qa && (p.window == 0 || qb - kfirst < p.window);  // every row sees every key
-        ok = warp_all(wait(&bar_qfull[qs], qcnt / C::kQSlots, 69)) && warp_all(wait(&bar_s[buf], qcnt >> 1, 70));
-        if (!ok) break;
-        tc_fence_after_sync();
-        const float4* const lse = reinterpret_cast<const float4*>(sLse + qs * 128);
-        uint64_t acc[2] = {0, 0};
-#pragma unroll 1
-        for (int c = 0; c < cols; c += 32) {
-          uint32_t s[32];
-          tmem_ld32(tmem + lane_base + buf * 128 + c, s);
-          tmem_ld_wait();
-          reg_fence(s);
-          if (c + 32 >= cols) {  // the scores are in registers
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar_sfree[buf]);
-          }
-          float x[32];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float4 n = lse[c / 4 + e];
-            const float2 a = unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(s[4 * e]), __uint_as_float(s[4 * e + 1])),
-                                                    sl2, pack_f32x2(n.x, n.y)));
-            const float2 b = unpack_f32x2(fma_f32x2(
-                pack_f32x2(__uint_as_float(s[4 * e + 2]), __uint_as_float(s[4 * e + 3])), sl2, pack_f32x2(n.z, n.w)));
-            x[4 * e] = a.x, x[4 * e + 1] = a.y, x[4 * e + 2] = b.x, x[4 * e + 3] = b.y;
-          }
-          if (!(all && c + 32 <= cols)) {  // whatever hidden rows and columns without a row hold does not count
-            const uint32_t span = static_cast<uint32_t>(max(0, hi - lo));
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (static_cast<uint32_t>(c + e - lo) >= span) x[e] = -INFINITY;
-          }
-          if (r.heads < p.tile.heads) {  // the last part of a group of more than 128 heads
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if ((c + e) % p.tile.heads >= r.heads) x[e] = -INFINITY;
-          }
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            acc[e & 1] = add_f32x2(acc[e & 1], pack_f32x2(ex2_approx(x[2 * e]), ex2_approx(x[2 * e + 1])));
+        if (pg < 0 || pg >= p.seqs.n_pages) return nullptr;
+        return p.weights + pg * p.w_spage + pc.kvh * p.w_shead + (pos & ((1 << p.seqs.page_shift) - 1));
+      };
+      auto put = [&](float* dst, float sum) {
+        if (dst != nullptr && !(p.accumulate && sum == 0.f)) *dst = p.accumulate ? *dst + sum : sum;
+      };
+      if (pc.few) {
+        if (steps > 0) ok = warp_all(wait(&sh.few_full[k % kPieces], k / kPieces, 71));
+        const int first = pc.i0 + ((scnt ^ buf) & 1);  // this buffer's first step
+        float* next = first < pc.i1 ? place(first * kKeys + key) : nullptr;
+        for (int i = first; ok && i < pc.i1; i += 2) {
+          float* const dst = next;
+          next = i + 2 < pc.i1 ? place((i + 2) * kKeys + key) : nullptr;
+          float sum = 0.f;
+          if (steps > 0) ok = columns(pc, 0, scnt + (i - pc.i0), i * kKeys + key, sh.few_lse[k % kPieces], sum);
+          if (!ok) break;
+          put(dst, sum);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_qempty[qs]);
-        const float2 a = unpack_f32x2(acc[0]), b = unpack_f32x2(acc[1]);
-        total += (a.x + a.y) + (b.x + b.y);
+        if (!ok) break;
+        if (steps > 0 && ((scnt + steps - 1) & 1) == buf) arrive(&sh.qempty[qcnt % C::kQSlots]);
+        if (steps > 0) ++qcnt;
+        scnt += steps;
+      } else {
+        const int pos = pc.key0 + key;
+        float* const dst = buf == 0 && pc.slot < 0 ? place(pos) : nullptr;
+        float total = 0.f;
+        for (int i = pc.i0; ok && i < pc.i1; ++i, ++scnt, ++qcnt) {
+          if ((scnt & 1) != buf) continue;
+          const int qs = qcnt % C::kQSlots;
+          float sum;
+          ok = warp_all(wait(&sh.qfull[qs], qcnt / C::kQSlots, 69)) && columns(pc, i, scnt, pos, sh.lse[qs], sum);
+          if (!ok) break;
+          arrive(&sh.qempty[qs]);
+          total += sum;
+        }
+        if (!ok) break;
+        if (buf == 1) {
+          sh.sums[k % kPieces][t][row] = total;
+        } else {
+          ok = warp_all(wait(&sh.sums_full[k % kPieces][t], k / kPieces, 72));
+          if (!ok) break;
+          total += sh.sums[k % kPieces][t][row];
+          if (pc.slot >= 0)
+            p.part[static_cast<int64_t>(pc.slot) * kKeys + key] = total;
+          else
+            put(dst, total);
+        }
       }
-      if (!ok) break;
-      if (pc.slot >= 0)
-        p.part[static_cast<int64_t>(pc.slot) * kKeys + key] = total;
-      else if (dst != nullptr && !(p.accumulate && total == 0.f))
-        *dst = p.accumulate ? *dst + total : total;
+      if (buf == 1) arrive(&sh.sums_full[k % kPieces][t]);
+      arrive(&sh.wfree[k % kPieces]);
     }
   }
 
