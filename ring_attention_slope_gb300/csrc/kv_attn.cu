@@ -36,6 +36,7 @@ constexpr uint32_t kChunkBytes = 128 * 128;  // 128 rows x 64 bf16
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: the running maximum moves when a score passes it by this
 constexpr int kPieceSteps = 5;             // what a piece's start and end cost, in steps
+constexpr int kFine = 1;                   // (kv_cut.cuh)
 constexpr int kHoles = 8;                  // ring of the steps' missing pages: more than the K tiles in flight
 constexpr int kJoinThreads = 512;
 
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
 
   if (warp == C::kTmaWarp) {
     // ================================================================ producer: pieces, pages, loads
-    const Cut cut = make_cut<kPieceSteps>(p.seqs, p.Hkv * p.tile.parts, cut_of, sh.lists);
+    const Cut cut = make_cut<kPieceSteps, kFine>(p.seqs, p.Hkv * p.tile.parts, cut_of, sh.lists);
     if (lane == 0 && blockIdx.x == 0) *p.n_slots = static_cast<int32_t>(cut.slots);
     const uint32_t total = cut.total;
     const uint32_t q_bytes = static_cast<uint32_t>(p.tile.heads * p.tile.tokens) * 128 * C::kQChunks;
@@ -849,7 +850,7 @@ Workspace workspace_of(int64_t T, int64_t group, int dqk, int dv, int32_t q_len)
   const int64_t most = std::max<int64_t>(1, q_len > 0 ? q_len : T);  // new tokens of a sequence
   Workspace w;
   w.rows_cap = std::min<int64_t>(tiles * tile.tokens, most) * tile.heads;
-  w.max_slots = max_joined(grid_of(dqk, dv));
+  w.max_slots = max_joined<kFine>(grid_of(dqk, dv));
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   w.pairs = 256;
   w.ml = w.pairs + up(w.max_slots * sizeof(KvPair));

@@ -25,9 +25,12 @@ struct Cut {
   uint32_t total, slots;  // pieces, and those of pairs with several
   int per;
 };
-// Joined pieces of a launch at most: no length of pieces is below half a share of the steps (an even division of them
-// by the grid), and a pair of several pieces has fewer than twice as many as its steps divided by their length.
-inline int64_t max_joined(int64_t grid) { return 4 * grid + grid / 8 + 8; }
+// Joined pieces of a launch at most: no length of pieces is below 1 / (2 kFine) of a share of the steps (an even division
+// of them by the grid), and a pair of several pieces has fewer than twice as many as its steps divided by their length.
+template <int kFine>
+int64_t max_joined(int64_t grid) {
+  return kFine * (4 * grid + grid / 8) + 8;
+}
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -38,10 +41,10 @@ __device__ __forceinline__ float warp_sum(float v) {
 // One whole warp calls it: reads the sequences, chooses the pieces' length and fills the lists.  cut_of(seq) gives a
 // sequence's SeqCut; kPieceSteps is what a piece's start and end cost, in steps.
 //
-// The longest pair is cut into pieces of about half to four times a share, and the length of those is tried as every
-// pair's.  The length with the least time wins: that of one piece or of an even share of all of them, whichever is more,
+// The longest pair is cut into pieces of about 1 / (2 kFine) to 4 / kFine of a share, and the length of those is tried as
+// every pair's.  The length with the least time wins: that of one piece or of an even share of all of them, whichever is more,
 // and half a piece for the uneven end where there are more pieces than CTAs.  (Estimates in fp32, the same in every CTA.)
-template <int kPieceSteps, typename CutOf>
+template <int kPieceSteps, int kFine, typename CutOf>
 __device__ __forceinline__ Cut make_cut(const KvSeqs& p, int heads, const CutOf& cut_of, CutLists& lists) {
   constexpr int kTries = 6;
   constexpr float kShares[kTries] = {0.5f, 0.75f, 1.f, 1.5f, 2.5f, 4.f};
@@ -62,9 +65,9 @@ __device__ __forceinline__ Cut make_cut(const KvSeqs& p, int heads, const CutOf&
   float count[kTries], inv[kTries];
 #pragma unroll
   for (int i = 0; i < kTries; ++i) {
-    const float n = fmaxf(1.f, rintf(__fdividef(static_cast<float>(most), share * kShares[i])));  // pieces of the longest
+    const float n = fmaxf(1.f, rintf(__fdividef(static_cast<float>(most), share * (kShares[i] / kFine))));  // pieces of the longest
     per[i] = static_cast<int>(ceilf(__fdividef(static_cast<float>(most), n)));
-    if (2.f * static_cast<float>(per[i]) < share) per[i] = most;  // (see max_joined)
+    if (2.f * kFine * static_cast<float>(per[i]) < share) per[i] = most;  // (see max_joined)
     inv[i] = __frcp_rn(static_cast<float>(per[i]));
     count[i] = 0.f;
   }

@@ -32,6 +32,7 @@ constexpr uint32_t kChunkBytes = 128 * 128;  // 128 rows x 64 bf16
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kKeys = 2 * kBlockN;  // of a CTA's block
 constexpr int kPieceSteps = 2;      // what a piece's start and end cost, in steps
+constexpr int kFine = 4;            // (kv_cut.cuh: a piece leaves only 1 KB, so they may be short)
 constexpr int kPieces = 4;          // pieces that the producer may be ahead
 
 struct KvWeightsParams {
@@ -53,8 +54,8 @@ struct KvWeightsParams {
   uint64_t wait_limit_ns;
 };
 
-constexpr int kSoftmaxWarps = 16, kTmaWarp = 16, kMmaWarp = 17, kLseWarp = 18, kLseWarps = 2;
-constexpr int kThreads = 32 * (kLseWarp + kLseWarps);
+constexpr int kSoftmaxWarps = 16, kTmaWarp = 16, kMmaWarp = 17, kLseWarp = 19;  // two MMA issuers
+constexpr int kThreads = 32 * 20;                                                   // five warps to a sub-partition
 
 // A piece: of a pair of rows that fill several tiles, row tiles [i0, i1) of one key block, numbered from 0 among the
 // `count` of every part that see one of its keys; else key blocks [i0, i1) and one row tile.
@@ -82,7 +83,7 @@ struct Cfg {
     float sums[kPieces][2][kBlockN];  // [piece][key tile]: what the second buffer's warps found
     uint64_t kfull[kKSlots], kempty[kKSlots], qfull[kQSlots], qempty[kQSlots];
     uint64_t s[4], sfree[4];  // [2 * buffer + key tile]
-    uint64_t wfull[kPieces], wfree[kPieces], few_full[kPieces], sums_full[kPieces][2], drain;
+    uint64_t wfull[kPieces], wfree[kPieces], few_full[kPieces], sums_full[kPieces][2], drain[2];
     Piece piece[kPieces];
     uint32_t tmem;
     int abort;
@@ -93,6 +94,20 @@ struct Cfg {
 };
 
 __device__ __forceinline__ bool warp_all(bool v) { return __all_sync(0xffffffffu, v); }
+
+// acc += {2^(s0 sl2 + n0), 2^(s1 sl2 + n1)}
+__device__ __forceinline__ void exp_pair(uint32_t s0, uint32_t s1, uint64_t sl2, uint64_t n, uint64_t& acc) {
+  asm("{\n\t.reg .b64 s, x;\n\t.reg .f32 x0, x1;\n\t"
+      "mov.b64 s, {%1, %2};\n\t"
+      "fma.rn.f32x2 x, s, %3, %4;\n\t"
+      "mov.b64 {x0, x1}, x;\n\t"
+      "ex2.approx.ftz.f32 x0, x0;\n\t"
+      "ex2.approx.ftz.f32 x1, x1;\n\t"
+      "mov.b64 x, {x0, x1};\n\t"
+      "add.rn.f32x2 %0, %0, x;\n\t}"
+      : "+l"(acc)
+      : "r"(s0), "r"(s1), "l"(sl2), "l"(n));
+}
 
 // Key blocks of a sequence, and the row tiles that one of them meets at most (those of a group of more than 128 heads are
 // its parts', one part after another); with one row tile, that and the key blocks.
@@ -196,18 +211,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < C::kKSlots; ++i) mbar_init(&sh.kfull[i], 1), mbar_init(&sh.kempty[i], 1);
     for (int i = 0; i < C::kQSlots; ++i) {
       mbar_init(&sh.qfull[i], 2);                       // the loads, and the lse
-      mbar_init(&sh.qempty[i], 1 + kSoftmaxWarps / 2);  // the products, and the readers of the last step's lse
+      mbar_init(&sh.qempty[i], 2 + kSoftmaxWarps / 2);  // the products, and the readers of the last step's lse
     }
     for (int i = 0; i < 4; ++i) mbar_init(&sh.s[i], 1), mbar_init(&sh.sfree[i], 4);
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(&sh.wfull[i], 1);
-      mbar_init(&sh.wfree[i], 1 + kLseWarps + kSoftmaxWarps);
+      mbar_init(&sh.wfree[i], 3 + kSoftmaxWarps);
       mbar_init(&sh.few_full[i], 1);
       for (int t = 0; t < 2; ++t) mbar_init(&sh.sums_full[i][t], 4);
     }
-    mbar_init(&sh.drain, 1);
+    for (int t = 0; t < 2; ++t) mbar_init(&sh.drain[t], 1);
     fence_barrier_init();
   }
+  // The rows of a Q slot that no box fills stay 0, and their scores too.
+  for (int i = threadIdx.x; i < C::kQSlots * C::kChunks * 128 * 8; i += kThreads)
+    if (((i >> 3) & 127) >= p.tile.heads * p.tile.tokens) reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_shared();
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -223,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kTmaWarp) {
     // ================================================================ producer: pieces, pages, loads
-    const Cut cut = make_cut<kPieceSteps>(p.seqs, p.Hkv, cut_of, sh.lists);
+    const Cut cut = make_cut<kPieceSteps, kFine>(p.seqs, p.Hkv, cut_of, sh.lists);
     if (lane == 0 && blockIdx.x == 0) *p.n_slots = static_cast<int32_t>(cut.slots);
     const uint32_t total = cut.total;
     const uint32_t q_bytes = static_cast<uint32_t>(p.tile.heads * p.tile.tokens) * 128 * C::kChunks;
@@ -315,11 +334,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait_final(&sh.qfull[i], ((qcnt - 1 - i) / C::kQSlots) & 1, limit);
       }
     }
-  } else if (warp >= kLseWarp) {
+  } else if (warp == kLseWarp) {
     // ================================================================ the rows' lse, next to their tile
-    // Each warp takes every second row tile (or piece of one), and has its next one's loads on their way while it
-    // waits for a slot.
-    const int me = warp - kLseWarp;
+    // (The next one's loads are on their way while this one waits for a slot.)
+    int tokens[4], heads[4];  // of the lane's four columns
+    int64_t offset[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      tokens[j] = (lane + 32 * j) / p.tile.heads;
+      heads[j] = lane + 32 * j - tokens[j] * p.tile.heads;
+      offset[j] = heads[j] * p.lse_shead + tokens[j] * p.lse_srow;
+    }
     int qcnt = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
@@ -330,22 +355,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       float next[4];
       auto fetch = [&](int i) {
         const Rows r = rows_of(p, i, pc);
+        const float* const at = p.lse + (static_cast<int64_t>(pc.kvh) * p.group + r.head) * p.lse_shead +
+                                (static_cast<int64_t>(pc.row0) + r.token) * p.lse_srow;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int col = lane + 32 * j, token = col / p.tile.heads, head = col - token * p.tile.heads;
-          next[j] = -INFINITY;
-          if (token < r.tokens && head < r.heads)
-            next[j] = p.lse[(static_cast<int64_t>(pc.kvh) * p.group + r.head + head) * p.lse_shead +
-                            (static_cast<int64_t>(pc.row0) + r.token + token) * p.lse_srow];
-        }
+        for (int j = 0; j < 4; ++j) next[j] = tokens[j] < r.tokens && heads[j] < r.heads ? at[offset[j]] : -INFINITY;
       };
-      const int first = (qcnt ^ me) & 1;
-      if (first < tiles) fetch(pc.i0 + first);
-      for (int i = first; i < tiles; i += kLseWarps) {
+      if (tiles > 0) fetch(pc.i0);
+      for (int i = 0; i < tiles; ++i) {
         float v[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = next[j] == -INFINITY ? next[j] : -next[j] * kLog2e;
-        if (i + kLseWarps < tiles) fetch(pc.i0 + i + kLseWarps);
+        if (i + 1 < tiles) fetch(pc.i0 + i + 1);
         const int at = qcnt + i, qs = at % C::kQSlots;
         ok = warp_all(wait(&sh.qempty[qs], at / C::kQSlots + 1, 65));
         if (!ok) break;
@@ -353,60 +373,61 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int j = 0; j < 4; ++j) dst[lane + 32 * j] = v[j];
         arrive(&sh.qfull[qs]);
-        if (pc.few && lane == 0) mbar_arrive(&sh.few_full[k % kPieces]);
       }
-      if (ok && !(pc.few && tiles > 0) && me == 0 && lane == 0) mbar_arrive(&sh.few_full[k % kPieces]);
+      if (ok && lane == 0) mbar_arrive(&sh.few_full[k % kPieces]);
       qcnt += tiles;
       arrive(&sh.wfree[k % kPieces]);
     }
-  } else if (warp == kMmaWarp) {
-    // ================================================================ MMA issuer
+  } else if (warp >= kMmaWarp) {
+    // ================================================================ MMA issuers, one for each key tile
+    // (Beside sixteen busy warps an issuer's own instructions count: with one for both tiles a step took 2400 cycles.)
     if (lane == 0) {
+      const int t = warp - kMmaWarp;
       constexpr uint32_t kDescHi = smem_desc_hi(1024, kSwizzle128B);
-      int kcnt = 0, qcnt = 0, scnt = 0;  // key tiles, row tiles, steps
-      // S^T of key tile t, in K slot `kslot`, and the row tile in slot qs
-      auto product = [&](int t, int kslot, int qs, int cols) -> bool {
+      int kcnt = t, qcnt = 0, scnt = 0;  // key tiles, row tiles, steps
+      // S^T of the key tile at klo and the row tile at qlo (descriptors)
+      auto product = [&](uint32_t klo, uint32_t qlo, uint32_t idesc) -> bool {
         const int buf = 2 * (scnt & 1) + t;
         if (!wait(&sh.sfree[buf], (scnt >> 1) + 1, 68)) return false;
         tc_fence_after_sync();
-        const uint32_t idesc = idesc_bf16_f32(kBlockM, 0, 0, 0) | (static_cast<uint32_t>(cols >> 3) << 17);
-        const uint32_t klo = smem_desc_lo(smem_u32(sK + kslot * C::kTileBytes), 16);
-        const uint32_t qlo = smem_desc_lo(smem_u32(sQ + qs * C::kTileBytes), 16);
 #pragma unroll
         for (int kk = 0; kk < DQK / 16; ++kk) {
           const uint32_t off = ((kk >> 2) * kChunkBytes + (kk & 3) * 32) >> 4;
           mma_ss_lh(tmem + buf * 128, klo + off, kDescHi, qlo + off, kDescHi, idesc, kk > 0 ? 1u : 0u);
         }
         mma_commit(&sh.s[buf]);
+        ++scnt;
         return true;
       };
+      const uint32_t klo0 = smem_desc_lo(smem_u32(sK), 16), qlo0 = smem_desc_lo(smem_u32(sQ), 16);
       bool ok = true;
       for (int k = 0; ok; ++k) {
         if (!take_piece(k)) break;
-        const Piece pc = sh.piece[k % kPieces];
+        const Piece& pc = sh.piece[k % kPieces];
+        const int b = pc.b, few = pc.few, count = pc.count, steps = pc.i1 - pc.i0, tokens = pc.n;
         mbar_arrive(&sh.wfree[k % kPieces]);
-        if (pc.b < 0) break;
-        if (pc.i1 <= pc.i0 || pc.count == 0) continue;
-        for (int i = pc.i0; ok && i < pc.i1; ++i, ++scnt) {
-          const bool new_keys = pc.few || i == pc.i0, new_rows = !pc.few || i == pc.i0;
-          const bool last_keys = pc.few || i == pc.i1 - 1, last_rows = !pc.few || i == pc.i1 - 1;
-          const int qs = qcnt % C::kQSlots;
-          if (new_rows) ok = wait(&sh.qfull[qs], qcnt / C::kQSlots, 67);
-          const Rows r = rows_of(p, i, pc);
-          const int cols = (r.tokens * p.tile.heads + 15) & ~15;  // 128 at most
-          for (int t = 0; t < 2 && ok; ++t) {
-            const int kslot = (kcnt + t) % C::kKSlots;
-            if (new_keys) ok = wait(&sh.kfull[kslot], (kcnt + t) / C::kKSlots, 66);
-            if (ok) ok = product(t, kslot, qs, cols);
-            if (ok && last_keys) mma_commit(&sh.kempty[kslot]);
+        if (b < 0) break;
+        if (steps <= 0 || count == 0) continue;
+        const int n_keys = few ? steps : 1, n_rows = few ? 1 : steps;
+        // (128 columns in every step would cost a decode step time)
+        const int cols = few ? (tokens * p.tile.heads + 31) & ~31 : 128;
+        const uint32_t idesc = idesc_bf16_f32(kBlockM, 0, 0, 0) | (static_cast<uint32_t>(cols >> 3) << 17);
+        for (int i = 0; ok && i < n_keys; ++i, kcnt += 2) {
+          const int kslot = kcnt % C::kKSlots;
+          const uint32_t klo = klo0 + kslot * (C::kTileBytes >> 4);
+          ok = wait(&sh.kfull[kslot], kcnt / C::kKSlots, 66);
+          for (int j = 0; ok && j < n_rows; ++j) {
+            const int qs = (qcnt + j) % C::kQSlots;
+            if (i == 0) ok = wait(&sh.qfull[qs], (qcnt + j) / C::kQSlots, 67);
+            if (ok) ok = product(klo, qlo0 + qs * (C::kTileBytes >> 4), idesc);
+            if (ok && i == n_keys - 1) mma_commit(&sh.qempty[qs]);
           }
-          if (ok && last_rows) mma_commit(&sh.qempty[qs]);
-          if (last_keys) kcnt += 2;
-          if (last_rows) ++qcnt;
+          if (ok) mma_commit(&sh.kempty[kslot]);
         }
+        qcnt += n_rows;
       }
-      mma_commit(&sh.drain);
-      wait_final(&sh.drain, 0, limit);
+      mma_commit(&sh.drain[t]);
+      wait_final(&sh.drain[t], 0, limit);
     }
   } else {
     // ================================================================ a key to a thread
@@ -416,8 +437,42 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t sl2 = pack_f32x2(p.scale_log2, p.scale_log2);
     int qcnt = 0, scnt = 0;
     bool ok = true;
+    // The sum over a row tile's columns, all of which count (one without a row has a score of 0 and an lse of inf): each 32
+    // columns' load runs under the exponentials of the 32 before.
+    auto all_columns = [&](int step, const float* lse, float& sum) -> bool {
+      const int b = 2 * buf + t;
+      if (!warp_all(wait(&sh.s[b], step >> 1, 73))) return false;
+      tc_fence_after_sync();
+      uint64_t acc[2] = {0, 0};
+      uint32_t s[2][32];
+      tmem_ld32(tS, s[0]);
+      tmem_ld_wait();
+      reg_fence(s[0]);
+#pragma unroll
+      for (int c = 0; c < kBlockN; c += 32) {
+        uint32_t(&now)[32] = s[(c / 32) & 1], (&then)[32] = s[(c / 32 + 1) & 1];
+        if (c + 32 < kBlockN) tmem_ld32(tS + c + 32, then);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const ulonglong2 n = *reinterpret_cast<const ulonglong2*>(lse + c + 4 * e);
+          exp_pair(now[4 * e], now[4 * e + 1], sl2, n.x, acc[0]);
+          exp_pair(now[4 * e + 2], now[4 * e + 3], sl2, n.y, acc[1]);
+        }
+        if (c + 32 < kBlockN) {
+          tmem_ld_wait();
+          reg_fence(then);
+        }
+        if (c + 64 == kBlockN) {  // the scores are in registers
+          tc_fence_before_sync();
+          arrive(&sh.sfree[b]);
+        }
+      }
+      const float2 a = unpack_f32x2(acc[0]), z = unpack_f32x2(acc[1]);
+      sum = (a.x + a.y) + (z.x + z.y);
+      return true;
+    };
     // The sum over row tile i's columns that see the key at position pos.
-    auto columns = [&](const Piece& pc, int i, int step, int pos, const float* lse, float& sum) -> bool {
+    auto columns = [&](const Piece& pc, int i, int step, int pos, const float* lse, float& sum) -> bool {  // (any tile)
       const int b = 2 * buf + t;
       const Rows r = rows_of(p, i, pc);
       const int cols = r.tokens * p.tile.heads, qa = pc.pos0 + r.token, qb = qa + r.tokens - 1;
@@ -505,17 +560,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         const int pos = pc.key0 + key;
         float* const dst = buf == 0 && pc.slot < 0 ? place(pos) : nullptr;
+        // row tiles [f0, f1) are full, and all their rows see all of the warp's keys (of a group in parts none is taken as such)
+        int f0 = 0, f1 = 0;
+        if (p.tile.parts == 1) {
+          const int kfirst = pos - row, klast = kfirst + kBlockN - 1, tokens = p.tile.tokens;
+          f0 = (max(0, klast - pc.pos0) + tokens - 1) / tokens - pc.blk0;
+          f1 = pc.n / tokens - pc.blk0;
+          if (p.window > 0) f1 = min(f1, max(0, kfirst + p.window - pc.pos0) / tokens - pc.blk0);
+        }
         float total = 0.f;
-        for (int i = pc.i0; ok && i < pc.i1; ++i, ++scnt, ++qcnt) {
-          if ((scnt & 1) != buf) continue;
-          const int qs = qcnt % C::kQSlots;
+        const int i0 = pc.i0 + ((scnt ^ buf) & 1);  // this buffer's first step
+        for (int i = i0; i < pc.i1; i += 2) {
+          const int step = scnt + (i - pc.i0), at = qcnt + (i - pc.i0), qs = at % C::kQSlots;
           float sum;
-          ok = warp_all(wait(&sh.qfull[qs], qcnt / C::kQSlots, 69)) && columns(pc, i, scnt, pos, sh.lse[qs], sum);
+          ok = warp_all(wait(&sh.qfull[qs], at / C::kQSlots, 69));
+          if (ok) ok = i >= f0 && i < f1 ? all_columns(step, sh.lse[qs], sum) : columns(pc, i, step, pos, sh.lse[qs], sum);
           if (!ok) break;
           arrive(&sh.qempty[qs]);
           total += sum;
         }
         if (!ok) break;
+        scnt += steps;
+        qcnt += steps;
         if (buf == 1) {
           sh.sums[k % kPieces][t][row] = total;
         } else {
@@ -571,7 +637,7 @@ struct Workspace {
 };
 Workspace workspace_of() {
   Workspace w;
-  w.max_slots = max_joined(kv_sm_count());
+  w.max_slots = max_joined<kFine>(kv_sm_count());
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   w.pairs = 256;
   w.part = w.pairs + up(w.max_slots * sizeof(int4));
