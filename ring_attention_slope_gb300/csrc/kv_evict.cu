@@ -8,9 +8,9 @@
 // in shared memory, and they read one another's histograms and counts there, so the weights are read once.
 //
 // Moving.  Token j of those kept comes from position old[j] >= j, so within its own pages a chunk of kept tokens may
-// overwrite only what chunks before it read.  A CTA takes a chunk by ticket, reads its rows into registers, says so in a
-// flag, waits for the (at most two) chunks whose rows lie where its own go, and writes: each row is read and written
-// once, by as many CTAs as there are chunks.  A chunk waits only for chunks of lower tickets, which are running and
+// overwrite only what chunks before it read.  A CTA takes one chunk after another by ticket: it reads the rows into
+// registers, says so in a flag, waits for the (at most two) chunks whose rows lie where its own go, and writes.  Each row is
+// read and written once, by as many CTAs as the GPU holds.  A chunk waits only for chunks of lower tickets, which are running and
 // read before they wait, so every wait ends; all the same it is bounded.
 #include <cooperative_groups.h>
 
@@ -25,12 +25,13 @@ namespace cg = cooperative_groups;
 namespace slope {
 namespace {
 
-constexpr int kSelectThreads = 512;
-constexpr int kCluster = 8;
+constexpr int kSelectThreads = 1024;
+constexpr int kMaxCluster = 16;
 constexpr int kBins = 2048;
-constexpr int kAloneTokens = 8192;  // sequences up to this long are selected by one CTA
-constexpr int kHeldKeys = 40960;    // keys of a CTA in shared memory; more are made again in every pass
+constexpr int kRun = 8192;          // keys of a CTA, as long as clusters allow it
+constexpr int kHeldKeys = 40960;    // of them in shared memory at most; more are made again in every pass
 constexpr int kMoveThreads = 128, kMoveWords = 8;  // of a thread, 16 bytes each
+constexpr int kMoveCtas = 7;                       // on an SM, by registers
 
 struct KvEvictParams {
   KvSeqs seqs;
@@ -50,7 +51,8 @@ struct KvEvictParams {
   int64_t k_stride[3], v_stride[3];  // in words of 8 channels
   int32_t chunk, chunks;             // kept tokens of a chunk, chunks of a pair
   int32_t held;                      // keys of a CTA in shared memory
-  uint32_t* ticket;                  // workspace
+  uint32_t* tickets;                 // workspace: one for each launch that moves
+  int32_t launches;
   uint32_t* flags;                   // workspace: [pair][chunk], the chunk's rows are read
   int32_t* bounds;                   // workspace: [pair][chunk + 1], kept tokens before position chunk * c
   int* status;
@@ -76,23 +78,23 @@ __device__ __forceinline__ uint2 block_scan(uint2 v, uint2* scratch, uint2& tota
   __syncthreads();
   if (lane == 31) scratch[warp] = incl;
   __syncthreads();
-  uint2 before = make_uint2(0, 0);
-  total = make_uint2(0, 0);
-#pragma unroll
-  for (int w = 0; w < kSelectThreads / 32; ++w) {
-    const uint2 s = scratch[w];
-    if (w < warp) before.x += s.x, before.y += s.y;
-    total.x += s.x, total.y += s.y;
-  }
+  static_assert(kSelectThreads == 1024, "a warp's lanes for the warps");
+  const uint2 mine = scratch[lane];
+  uint2 before;
+  before.x = __reduce_add_sync(0xffffffffu, lane < warp ? mine.x : 0u);
+  before.y = __reduce_add_sync(0xffffffffu, lane < warp ? mine.y : 0u);
+  total.x = __reduce_add_sync(0xffffffffu, mine.x);
+  total.y = __reduce_add_sync(0xffffffffu, mine.y);
   return make_uint2(before.x + incl.x - v.x, before.y + incl.y - v.y);
 }
 
 __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const __grid_constant__ KvEvictParams p) {
   cg::cluster_group cluster = cg::this_cluster();
   extern __shared__ uint32_t s_keys[];
-  __shared__ uint32_t s_hist[kBins];
+  __shared__ __align__(16) uint32_t s_hist[kBins];
   __shared__ uint32_t s_bin[2];  // the bin with the wanted rank, and the rank within it
   __shared__ uint2 s_scan[kSelectThreads / 32], s_count;
+  pdl_launch_dependents();
   const int ranks = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   const int pair = blockIdx.x / ranks, b = pair / p.Hkv, h = pair - b * p.Hkv;
   const KvSeq seq = kv_seq(p.seqs, b);
@@ -102,7 +104,8 @@ __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const __grid_
   int32_t* const bounds = p.bounds + static_cast<int64_t>(pair) * (p.chunks + 1);
   const int stride = ranks * kSelectThreads, me = rank * kSelectThreads + threadIdx.x;
 
-  if (pair == 0 && me == 0) *p.ticket = 0;
+  if (pair == 0)
+    for (int i = me; i < p.launches; i += stride) p.tickets[i] = 0;
   for (int c = me; c < p.chunks; c += stride) flags[c] = 0;
   if (n <= keep) {
     for (int j = me; j < keep; j += stride) kept[j] = j < n ? j : -1;
@@ -118,13 +121,31 @@ __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const __grid_
 
   const int32_t* const row = p.seqs.table + static_cast<int64_t>(b) * p.seqs.table_stride;
   const int in_page = (1 << p.seqs.page_shift) - 1;
+  const float* const weights = p.weights_in + h * p.w_shead;
   auto read_key = [&](int t) -> uint32_t {
     const int pg = row[t >> p.seqs.page_shift];
-    if (pg < 0 || pg >= p.seqs.n_pages) return 0u;
-    return weight_key(p.weights_in[pg * p.w_spage + h * p.w_shead + (t & in_page)]);
+    return pg < 0 || pg >= p.seqs.n_pages ? 0u : weight_key(weights[pg * p.w_spage + (t & in_page)]);
   };
-  for (int i = threadIdx.x; i < min(t1 - t0, p.held); i += kSelectThreads) s_keys[i] = read_key(t0 + i);
+  // eight loads of pages, then of weights, in flight
+  const int held = min(t1 - t0, p.held);
+  for (int i0 = threadIdx.x; i0 < held; i0 += 8 * kSelectThreads) {
+    int pg[8];
+    float w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) pg[e] = i0 + e * kSelectThreads < held ? row[(t0 + i0 + e * kSelectThreads) >> p.seqs.page_shift] : -1;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (pg[e] >= p.seqs.n_pages) pg[e] = -1;
+      w[e] = pg[e] >= 0 ? weights[pg[e] * p.w_spage + ((t0 + i0 + e * kSelectThreads) & in_page)] : 0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (i0 + e * kSelectThreads < held) s_keys[i0 + e * kSelectThreads] = pg[e] >= 0 ? weight_key(w[e]) : 0u;
+  }
   auto key = [&](int t) -> uint32_t { return t - t0 < p.held ? s_keys[t - t0] : read_key(t); };
+  // the thread's own run of tokens, an odd number of them (which spreads the runs over the banks)
+  const int run = ((t1 - t0 + kSelectThreads - 1) / kSelectThreads) | 1;
+  const int a0 = t0 + min(t1 - t0, static_cast<int>(threadIdx.x) * run), a1 = min(t1, a0 + run);
 
   // ---- the smallest key that stays, and how many equal to it
   uint32_t prefix = 0, left = want;  // of the keys that match the prefix, the left-th largest is looked for
@@ -135,31 +156,29 @@ __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const __grid_
     const uint32_t high = shift == 32 ? 0u : ~0u << shift;  // bits known so far
     shift -= bits;
     for (int i = threadIdx.x; i < kBins; i += kSelectThreads) s_hist[i] = 0;
-    __syncthreads();
+    __syncthreads();  // (and the keys are there)
     for (int t = t0 + threadIdx.x; t < t1; t += kSelectThreads) {
       const uint32_t k = key(t);
       if ((k & high) == prefix) atomicAdd(&s_hist[(k >> shift) & ((1u << bits) - 1)], 1u);
     }
     cluster.sync();
-    // bins from the top, four to a thread
-    uint32_t c[4];
-    uint2 sum = make_uint2(0, 0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int bin = kBins - 1 - (threadIdx.x * 4 + i);
-      c[i] = 0;
-      for (int r = 0; r < ranks; ++r) c[i] += cluster.map_shared_rank(s_hist, r)[bin];
-      sum.x += c[i];
+    // bins from the top, two to a thread
+    static_assert(kBins == 2 * kSelectThreads, "two bins to a thread");
+    const int bin = kBins - 2 - 2 * threadIdx.x;
+    uint2 c = make_uint2(0, 0);  // of bin and bin + 1
+#pragma unroll 4
+    for (int r = 0; r < ranks; ++r) {
+      const uint2 x = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(s_hist, r) + bin);
+      c.x += x.x, c.y += x.y;
     }
     uint2 total;
-    uint32_t above = block_scan(sum, s_scan, total).x;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (above < left && left <= above + c[i]) {
-        s_bin[0] = kBins - 1 - (threadIdx.x * 4 + i);
-        s_bin[1] = left - above;
-      }
-      above += c[i];
+    const uint32_t above = block_scan(make_uint2(c.x + c.y, 0), s_scan, total).x;
+    if (above < left && left <= above + c.y) {
+      s_bin[0] = bin + 1;
+      s_bin[1] = left - above;
+    } else if (above + c.y < left && left <= above + c.y + c.x) {
+      s_bin[0] = bin;
+      s_bin[1] = left - above - c.y;
     }
     cluster.sync();  // the histograms are read, the bin is written
     if (want > 0) {
@@ -169,33 +188,32 @@ __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const __grid_
   }
   if (want == 0) prefix = ~0u, left = 0;  // no key is as large
 
-  // ---- counts of larger and equal keys in this CTA's run, and before it
+  // ---- counts of larger and equal keys before the thread's run, in this CTA and in those before it
   uint2 mine = make_uint2(0, 0), total;
-  for (int t = t0 + threadIdx.x; t < t1; t += kSelectThreads) {
+  for (int t = a0; t < a1; ++t) {
     const uint32_t k = key(t);
     mine.x += k > prefix ? 1u : 0u, mine.y += k == prefix ? 1u : 0u;
   }
-  block_scan(mine, s_scan, total);
+  uint2 before = block_scan(mine, s_scan, total);
   if (threadIdx.x == 0) s_count = total;
   cluster.sync();
-  uint2 before = make_uint2(0, 0);
-  for (int r = 0; r < rank; ++r) {
-    const uint2 c = *cluster.map_shared_rank(&s_count, r);
-    before.x += c.x, before.y += c.y;
+  if (threadIdx.x < 32) {
+    uint2 c = make_uint2(0, 0);
+    if (static_cast<int>(threadIdx.x) < rank) c = *cluster.map_shared_rank(&s_count, threadIdx.x);
+    c.x = __reduce_add_sync(0xffffffffu, c.x);
+    c.y = __reduce_add_sync(0xffffffffu, c.y);
+    if (threadIdx.x == 0) s_scan[0] = c;
   }
-  cluster.sync();  // no CTA leaves before its counts are read
+  cluster.sync();  // (no CTA leaves before its counts are read)
+  before.x += s_scan[0].x, before.y += s_scan[0].y;
 
   // ---- places
-  for (int at = t0; at < t1; at += kSelectThreads) {
-    const int t = at + threadIdx.x;
-    const uint32_t k = t < t1 ? key(t) : 0u;
-    const uint2 flag = make_uint2(t < t1 && k > prefix ? 1u : 0u, t < t1 && k == prefix ? 1u : 0u);
-    const uint2 pre = block_scan(flag, s_scan, total);
-    const uint32_t eq = before.y + pre.y;
-    const int j = p.first + static_cast<int>(before.x + pre.x + min(eq, left));
-    if (flag.x || (flag.y && eq < left)) kept[j] = t;
-    if (t < t1 && t % p.chunk == 0 && t / p.chunk <= p.chunks) bounds[t / p.chunk] = j;
-    before.x += total.x, before.y += total.y;
+  for (int t = a0; t < a1; ++t) {
+    const uint32_t k = key(t);
+    const int j = p.first + static_cast<int>(before.x + min(before.y, left));
+    if (t % p.chunk == 0 && t / p.chunk <= p.chunks) bounds[t / p.chunk] = j;
+    if (k > prefix || (k == prefix && before.y < left)) kept[j] = t;
+    before.x += k > prefix ? 1u : 0u, before.y += k == prefix ? 1u : 0u;
   }
   // the bounds outside the chosen range
   for (int c = me; c <= p.chunks; c += stride) {
@@ -211,117 +229,172 @@ __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const __grid_
 
 // Words of a token's head: keys, then values.
 template <int DQK, int DV>
-__global__ void __launch_bounds__(kMoveThreads) kv_move_kernel(const __grid_constant__ KvEvictParams p, int pairs) {
+__global__ void __launch_bounds__(kMoveThreads, kMoveCtas) kv_move_kernel(const __grid_constant__ KvEvictParams p, int launch) {
   constexpr int kKey = DQK / 8, kAll = (DQK + DV) / 8;
   constexpr int kChunk = kMoveThreads * kMoveWords / kAll / 8 * 8;
-  __shared__ uint32_t s_ticket;
+  __shared__ uint32_t s_first[kKvMaxSeqs];  // chunks before a sequence's
+  __shared__ uint32_t s_total, s_ticket;
   __shared__ int64_t s_src[kChunk], s_dst[kChunk];  // page << 32 | index in the page; -1: not moved
   __shared__ int s_give_up;
-  if (threadIdx.x == 0) {
-    s_ticket = atomicAdd(p.ticket, 1u);
-    s_give_up = 0;
-  }
-  __syncthreads();
-  // the chunks of all pairs in turn, so that a chunk's forerunners are a round ahead
-  const int c = static_cast<int>(s_ticket / static_cast<uint32_t>(pairs)), pair = static_cast<int>(s_ticket % static_cast<uint32_t>(pairs));
-  const int b = pair / p.Hkv, h = pair - b * p.Hkv;
-  if (threadIdx.x == 0 && c == 0 && h == 0) p.out_lens[b] = min(kv_seq(p.seqs, b).len, p.keep);
-  const int j0 = c * kChunk, count = min(kChunk, p.keep - j0);
-  const int shift = p.seqs.page_shift, in_page = (1 << shift) - 1;
-  bool moves = false;
-  for (int i = threadIdx.x; i < kChunk; i += kMoveThreads) {
-    const int j = j0 + i, old = i < count ? p.kept[static_cast<int64_t>(pair) * p.keep + j] : -1;
-    int64_t src = -1, dst = -1;
-    if (old >= 0 && (p.out_table != nullptr || old != j)) {
-      const int32_t* const row = p.seqs.table + static_cast<int64_t>(b) * p.seqs.table_stride;
-      const int from = row[old >> shift];
-      const int to = p.out_table != nullptr ? p.out_table[static_cast<int64_t>(b) * p.out_stride + (j >> shift)] : row[j >> shift];
-      if (from >= 0 && from < p.seqs.n_pages && to >= 0 && to < p.seqs.n_pages) {
-        src = static_cast<int64_t>(from) << 32 | (old & in_page);
-        dst = static_cast<int64_t>(to) << 32 | (j & in_page);
-        moves = true;
-      }
-    }
-    s_src[i] = src, s_dst[i] = dst;
-  }
-  uint32_t* const flags = p.flags + static_cast<int64_t>(pair) * p.chunks;
-  if (!__syncthreads_or(moves)) {
-    if (threadIdx.x == 0) atomicExch(&flags[c], 1u);
-    return;
-  }
-
-  uint4 x[kMoveWords];
+  const int B = p.seqs.B, lane = threadIdx.x & 31;
+  if (threadIdx.x < 32) {
+    uint32_t sum = 0;
+    for (int b0 = 0; b0 < B; b0 += 32) {
+      uint32_t n = 0;
+      if (b0 + lane < B) n = static_cast<uint32_t>((min(kv_seq(p.seqs, b0 + lane).len, p.keep) + kChunk - 1) / kChunk) * p.Hkv;
+      uint32_t incl = n;
 #pragma unroll
-  for (int i = 0; i < kMoveWords; ++i) {
-    const int word = threadIdx.x + i * kMoveThreads, e = word / kAll, w = word - e * kAll;
-    if (e >= kChunk || s_src[e] < 0) continue;
-    const int64_t pg = s_src[e] >> 32, t = s_src[e] & 0xffffffff;
-    x[i] = w < kKey ? p.k_in[pg * p.k_stride[0] + h * p.k_stride[1] + t * p.k_stride[2] + w]
-                    : p.v_in[pg * p.v_stride[0] + h * p.v_stride[1] + t * p.v_stride[2] + (w - kKey)];
+      for (int m = 1; m < 32; m <<= 1) {
+        const uint32_t o = __shfl_up_sync(0xffffffffu, incl, m);
+        if (lane >= m) incl += o;
+      }
+      if (b0 + lane < B) s_first[b0 + lane] = sum + incl - n;
+      sum += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) {
+      s_total = sum;
+      s_give_up = 0;
+    }
   }
-  float weight = 0.f;
-  if (threadIdx.x < kChunk && s_src[threadIdx.x] >= 0)
-    weight = p.weights_in[(s_src[threadIdx.x] >> 32) * p.w_spage + h * p.w_shead + (s_src[threadIdx.x] & 0xffffffff)];
-
-  if (p.out_table == nullptr) {
-    __threadfence();  // the reads come before the flag
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      atomicExch(&flags[c], 1u);
-      // the kept tokens that lie where this chunk's go, and their chunks
-      const int32_t* const bounds = p.bounds + static_cast<int64_t>(pair) * (p.chunks + 1) + c;
-      const int lo = bounds[0], hi = bounds[1];
-      const uint64_t start = globaltimer_ns();
-      for (int o = lo / kChunk; hi > lo && o <= (hi - 1) / kChunk && o < c && !s_give_up; ++o) {
-        while (atomicAdd(&flags[o], 0u) == 0u) {
-          if (*reinterpret_cast<volatile int*>(p.status) != 0) {
-            s_give_up = 1;
-            break;
-          }
-          if (globaltimer_ns() - start > p.wait_limit_ns) {
-            record_timeout(p.status, 81);
-            s_give_up = 1;
-            break;
-          }
+  pdl_wait();
+  // (the lengths may be their own output: a length that has changed gives the same chunks)
+  if (blockIdx.x == 0)
+    for (int b = threadIdx.x; b < B; b += kMoveThreads) p.out_lens[p.seqs.b0 + b] = min(kv_seq(p.seqs, b).len, p.keep);
+  if (threadIdx.x == 0) s_ticket = atomicAdd(&p.tickets[launch], 1u);
+  __syncthreads();
+  const uint32_t total = s_total;
+  const int shift = p.seqs.page_shift, in_page = (1 << shift) - 1;
+  for (uint32_t ticket = s_ticket; ticket < total;) {
+    int seq = 0;
+    for (int hi = B - 1; seq < hi;) {  // the last sequence whose first chunk is not after the ticket's
+      const int mid = (seq + hi + 1) >> 1;
+      if (s_first[mid] <= ticket)
+        seq = mid;
+      else
+        hi = mid - 1;
+    }
+    // a sequence's chunks of all heads in turn, so that a chunk's forerunners are a round ahead
+    const int b = p.seqs.b0 + seq, c = static_cast<int>((ticket - s_first[seq]) / static_cast<uint32_t>(p.Hkv));
+    const int h = static_cast<int>(ticket - s_first[seq]) - c * p.Hkv;
+    const int64_t pair = static_cast<int64_t>(b) * p.Hkv + h;
+    uint32_t next = 0;
+    if (threadIdx.x == 0) next = atomicAdd(&p.tickets[launch], 1u);  // on its way
+    const int j0 = c * kChunk, count = min(kChunk, p.keep - j0);
+    bool moves = false;
+    for (int i = threadIdx.x; i < kChunk; i += kMoveThreads) {
+      const int j = j0 + i, old = i < count ? p.kept[pair * p.keep + j] : -1;
+      int64_t src = -1, dst = -1;
+      if (old >= 0 && (p.out_table != nullptr || old != j)) {
+        const int32_t* const row = p.seqs.table + static_cast<int64_t>(b) * p.seqs.table_stride;
+        const int from = row[old >> shift];
+        const int to = p.out_table != nullptr ? p.out_table[static_cast<int64_t>(b) * p.out_stride + (j >> shift)] : row[j >> shift];
+        if (from >= 0 && from < p.seqs.n_pages && to >= 0 && to < p.seqs.n_pages) {
+          src = static_cast<int64_t>(from) << 32 | (old & in_page);
+          dst = static_cast<int64_t>(to) << 32 | (j & in_page);
+          moves = true;
         }
       }
-      __threadfence();
+      s_src[i] = src, s_dst[i] = dst;
     }
-    __syncthreads();
-    if (s_give_up) return;
-  }
+    uint32_t* const flags = p.flags + pair * p.chunks;
+    moves = __syncthreads_or(moves);
+    if (!moves && threadIdx.x == 0) atomicExch(&flags[c], 1u);
+    if (moves) {
+      uint4 x[kMoveWords];
 #pragma unroll
-  for (int i = 0; i < kMoveWords; ++i) {
-    const int word = threadIdx.x + i * kMoveThreads, e = word / kAll, w = word - e * kAll;
-    if (e >= kChunk || s_src[e] < 0) continue;
-    const int64_t pg = s_dst[e] >> 32, t = s_dst[e] & 0xffffffff;
-    if (w < kKey)
-      p.k[pg * p.k_stride[0] + h * p.k_stride[1] + t * p.k_stride[2] + w] = x[i];
-    else
-      p.v[pg * p.v_stride[0] + h * p.v_stride[1] + t * p.v_stride[2] + (w - kKey)] = x[i];
+      for (int i = 0; i < kMoveWords; ++i) {
+        const int word = threadIdx.x + i * kMoveThreads, e = word / kAll, w = word - e * kAll;
+        if (e >= kChunk || s_src[e] < 0) continue;
+        const int64_t pg = s_src[e] >> 32, t = s_src[e] & 0xffffffff;
+        x[i] = w < kKey ? p.k_in[pg * p.k_stride[0] + h * p.k_stride[1] + t * p.k_stride[2] + w]
+                        : p.v_in[pg * p.v_stride[0] + h * p.v_stride[1] + t * p.v_stride[2] + (w - kKey)];
+      }
+      float weight = 0.f;
+      if (threadIdx.x < kChunk && s_src[threadIdx.x] >= 0)
+        weight = p.weights_in[(s_src[threadIdx.x] >> 32) * p.w_spage + h * p.w_shead + (s_src[threadIdx.x] & 0xffffffff)];
+
+      if (p.out_table == nullptr) {
+        __threadfence();  // the reads come before the flag
+        __syncthreads();
+        if (threadIdx.x == 0) {
+          atomicExch(&flags[c], 1u);
+          // the kept tokens that lie where this chunk's go, and their chunks
+          const int32_t* const bounds = p.bounds + pair * (p.chunks + 1) + c;
+          const int lo = bounds[0], hi = bounds[1];
+          const uint64_t start = globaltimer_ns();
+          for (int o = lo / kChunk; hi > lo && o <= (hi - 1) / kChunk && o < c && !s_give_up; ++o) {
+            while (atomicAdd(&flags[o], 0u) == 0u) {
+              if (*reinterpret_cast<volatile int*>(p.status) != 0) {
+                s_give_up = 1;
+                break;
+              }
+              if (globaltimer_ns() - start > p.wait_limit_ns) {
+                record_timeout(p.status, 81);
+                s_give_up = 1;
+                break;
+              }
+            }
+          }
+          __threadfence();
+        }
+        __syncthreads();
+        if (s_give_up) return;
+      }
+#pragma unroll
+      for (int i = 0; i < kMoveWords; ++i) {
+        const int word = threadIdx.x + i * kMoveThreads, e = word / kAll, w = word - e * kAll;
+        if (e >= kChunk || s_src[e] < 0) continue;
+        const int64_t pg = s_dst[e] >> 32, t = s_dst[e] & 0xffffffff;
+        if (w < kKey)
+          p.k[pg * p.k_stride[0] + h * p.k_stride[1] + t * p.k_stride[2] + w] = x[i];
+        else
+          p.v[pg * p.v_stride[0] + h * p.v_stride[1] + t * p.v_stride[2] + (w - kKey)] = x[i];
+      }
+      if (threadIdx.x < kChunk && s_src[threadIdx.x] >= 0)
+        p.weights[(s_dst[threadIdx.x] >> 32) * p.w_spage + h * p.w_shead + (s_dst[threadIdx.x] & 0xffffffff)] = weight;
+    }
+    if (threadIdx.x == 0) s_ticket = next;
+    __syncthreads();
+    ticket = s_ticket;
+    __syncthreads();
   }
-  if (threadIdx.x < kChunk && s_src[threadIdx.x] >= 0)
-    p.weights[(s_dst[threadIdx.x] >> 32) * p.w_spage + h * p.w_shead + (s_dst[threadIdx.x] & 0xffffffff)] = weight;
 }
 
 int chunk_of(int dqk, int dv) { return kMoveThreads * kMoveWords / ((dqk + dv) / 8) / 8 * 8; }
 
 template <int DQK, int DV>
-cudaError_t launch_move(const KvEvictParams& p, int64_t pairs, cudaStream_t stream) {
+cudaError_t launch_move(KvEvictParams p, int64_t B, cudaStream_t stream) {
   static_assert(kMoveThreads * kMoveWords / ((DQK + DV) / 8) / 8 * 8 <= kMoveThreads, "a weight to a thread");
-  kv_move_kernel<DQK, DV><<<static_cast<unsigned>(pairs * p.chunks), kMoveThreads, 0, stream>>>(p, static_cast<int>(pairs));
-  return cudaGetLastError();
+  for (int i = 0; i < p.launches; ++i) {
+    p.seqs.b0 = i * kKvMaxSeqs;
+    p.seqs.B = static_cast<int32_t>(std::min<int64_t>(kKvMaxSeqs, B - p.seqs.b0));
+    const int64_t chunks = static_cast<int64_t>(p.seqs.B) * p.Hkv * p.chunks;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(chunks, kMoveCtas * kv_sm_count())));
+    cfg.blockDim = dim3(kMoveThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = i == 0 ? 1 : 0;  // the first starts as the selection ends
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_move_kernel<DQK, DV>, p, i);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
-cudaError_t launch_evict(const KvEvictParams& p, int64_t pairs, int dqk, int dv, cudaStream_t stream) {
-  const int ranks = p.seqs.max_tokens <= kAloneTokens ? 1 : kCluster;
+cudaError_t launch_evict(const KvEvictParams& p, int64_t B, int dqk, int dv, cudaStream_t stream) {
+  int ranks = 1;
+  while (ranks < kMaxCluster && p.seqs.max_tokens > static_cast<int64_t>(ranks) * kRun) ranks *= 2;
   KvEvictParams s = p;
   s.held = static_cast<int32_t>(std::min<int64_t>(kHeldKeys, (p.seqs.max_tokens + ranks - 1) / ranks));
   const int bytes = s.held * 4;
   cudaError_t e = cudaFuncSetAttribute(kv_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeldKeys * 4);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kv_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(pairs * ranks));
+  cfg.gridDim = dim3(static_cast<unsigned>(B * p.Hkv * ranks));
   cfg.blockDim = dim3(kSelectThreads);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = stream;
@@ -333,12 +406,12 @@ cudaError_t launch_evict(const KvEvictParams& p, int64_t pairs, int dqk, int dv,
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, kv_select_kernel, s)) != cudaSuccess) return e;
-  if (dqk == 64 && dv == 64) return launch_move<64, 64>(p, pairs, stream);
-  if (dqk == 64 && dv == 128) return launch_move<64, 128>(p, pairs, stream);
-  if (dqk == 128 && dv == 64) return launch_move<128, 64>(p, pairs, stream);
-  if (dqk == 128 && dv == 128) return launch_move<128, 128>(p, pairs, stream);
-  if (dqk == 192 && dv == 64) return launch_move<192, 64>(p, pairs, stream);
-  if (dqk == 192 && dv == 128) return launch_move<192, 128>(p, pairs, stream);
+  if (dqk == 64 && dv == 64) return launch_move<64, 64>(p, B, stream);
+  if (dqk == 64 && dv == 128) return launch_move<64, 128>(p, B, stream);
+  if (dqk == 128 && dv == 64) return launch_move<128, 64>(p, B, stream);
+  if (dqk == 128 && dv == 128) return launch_move<128, 128>(p, B, stream);
+  if (dqk == 192 && dv == 64) return launch_move<192, 64>(p, B, stream);
+  if (dqk == 192 && dv == 128) return launch_move<192, 128>(p, B, stream);
   return cudaErrorInvalidValue;
 }
 
@@ -350,7 +423,7 @@ struct Workspace {
 Workspace workspace_of(int64_t pairs, int64_t chunks) {
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   Workspace w;
-  w.flags = 256;
+  w.flags = 256;  // (64 tickets before them: 65535 sequences in launches of kKvMaxSeqs)
   w.bounds = w.flags + up(pairs * chunks * 4);
   w.total = w.bounds + up(pairs * (chunks + 1) * 4);
   return w;
@@ -386,7 +459,7 @@ slope_status slope_kv_evict(const slope_kv_cache* cache, slope_tensor* weights, 
   if (kept == nullptr || out_lens == nullptr) return SLOPE_ERR_NULL;
   if (!aligned(kept, 4) || !aligned(out_lens, 4) || !aligned(out_table, 4)) return SLOPE_ERR_STRIDE;
   const int64_t pairs = B * cache->Hkv, chunk = chunk_of(cache->dqk, cache->dv), chunks = (keep + chunk - 1) / chunk;
-  if (pairs * chunks >= (int64_t(1) << 31) || pairs * kCluster >= (int64_t(1) << 31)) return SLOPE_ERR_UNSUPPORTED;
+  if (pairs * chunks >= (int64_t(1) << 31) || pairs * kMaxCluster >= (int64_t(1) << 31)) return SLOPE_ERR_UNSUPPORTED;
   const Workspace w = workspace_of(pairs, chunks);
   if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < w.total) return SLOPE_ERR_WORKSPACE;
 
@@ -412,13 +485,15 @@ slope_status slope_kv_evict(const slope_kv_cache* cache, slope_tensor* weights, 
   p.chunk = static_cast<int32_t>(chunk);
   p.chunks = static_cast<int32_t>(chunks);
   char* const ws = static_cast<char*>(workspace);
-  p.ticket = reinterpret_cast<uint32_t*>(ws);
+  p.tickets = reinterpret_cast<uint32_t*>(ws);
+  p.launches = static_cast<int32_t>((B + kKvMaxSeqs - 1) / kKvMaxSeqs);
   p.flags = reinterpret_cast<uint32_t*>(ws + w.flags);
   p.bounds = reinterpret_cast<int32_t*>(ws + w.bounds);
   p.status = device_status_ptr();
   if (p.status == nullptr) return cuda_fail("device status word (cudaGetSymbolAddress)");
   p.wait_limit_ns = wait_limit_ns();
-  const cudaError_t e = launch_evict(p, pairs, cache->dqk, cache->dv, static_cast<cudaStream_t>(stream));
+  if (kv_sm_count() <= 0) return cuda_fail("device attributes");
+  const cudaError_t e = launch_evict(p, B, cache->dqk, cache->dv, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SLOPE_OK : cuda_fail("cache eviction kernel launch", e);
 }
 

@@ -33,6 +33,7 @@ constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kKeys = 2 * kBlockN;  // of a CTA's block
 constexpr int kPieceSteps = 2;      // what a piece's start and end cost, in steps
 constexpr int kFine = 4;            // (kv_cut.cuh: a piece leaves only 1 KB, so they may be short)
+constexpr int kLseSlots = 8;
 constexpr int kPieces = 4;          // pieces that the producer may be ahead
 
 struct KvWeightsParams {
@@ -78,10 +79,10 @@ struct Cfg {
   static constexpr int kQOffset = kKSlots * kTileBytes;
   static constexpr int kRestOffset = kQOffset + kQSlots * kTileBytes;
   struct Rest {  // behind the tiles
-    float lse[kQSlots][128];        // -lse log2(e) of a row tile's columns
+    float lse[kLseSlots][128];      // -lse log2(e) of a row tile's columns
     float few_lse[kPieces][128];    // of a piece's one row tile
     float sums[kPieces][2][kBlockN];  // [piece][key tile]: what the second buffer's warps found
-    uint64_t kfull[kKSlots], kempty[kKSlots], qfull[kQSlots], qempty[kQSlots];
+    uint64_t kfull[kKSlots], kempty[kKSlots], qfull[kQSlots], qempty[kQSlots], lfull[kLseSlots], lempty[kLseSlots];
     uint64_t s[4], sfree[4];  // [2 * buffer + key tile]
     uint64_t wfull[kPieces], wfree[kPieces], few_full[kPieces], sums_full[kPieces][2], drain[2];
     Piece piece[kPieces];
@@ -209,10 +210,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == kMmaWarp * 32) {
     for (int i = 0; i < C::kKSlots; ++i) mbar_init(&sh.kfull[i], 1), mbar_init(&sh.kempty[i], 1);
-    for (int i = 0; i < C::kQSlots; ++i) {
-      mbar_init(&sh.qfull[i], 2);                       // the loads, and the lse
-      mbar_init(&sh.qempty[i], 2 + kSoftmaxWarps / 2);  // the products, and the readers of the last step's lse
-    }
+    for (int i = 0; i < C::kQSlots; ++i) mbar_init(&sh.qfull[i], 1), mbar_init(&sh.qempty[i], 2);
+    for (int i = 0; i < kLseSlots; ++i) mbar_init(&sh.lfull[i], 1), mbar_init(&sh.lempty[i], kSoftmaxWarps / 2);
     for (int i = 0; i < 4; ++i) mbar_init(&sh.s[i], 1), mbar_init(&sh.sfree[i], 4);
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(&sh.wfull[i], 1);
@@ -326,8 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       release_pieces(p.tile_counter, total, w);
       if (!ok) {
-        // the loads already issued land before the CTA gives up its shared memory (the row tiles' barriers also count
-        // the lse's arrival, which may never come: their bytes are waited for as long as the limit says)
+        // the loads already issued land before the CTA gives up its shared memory
         for (int i = 0; i < C::kKSlots && i < kcnt; ++i)
           wait_final(&sh.kfull[i], ((kcnt - 1 - i) / C::kKSlots) & 1, limit);
         for (int i = 0; i < C::kQSlots && i < qcnt; ++i)
@@ -345,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       heads[j] = lane + 32 * j - tokens[j] * p.tile.heads;
       offset[j] = heads[j] * p.lse_shead + tokens[j] * p.lse_srow;
     }
-    int qcnt = 0;
+    int cnt = 0;  // ring slots filled
     bool ok = true;
     for (int k = 0; ok; ++k) {
       if (!warp_all(take_piece(k))) break;
@@ -366,16 +364,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = next[j] == -INFINITY ? next[j] : -next[j] * kLog2e;
         if (i + 1 < tiles) fetch(pc.i0 + i + 1);
-        const int at = qcnt + i, qs = at % C::kQSlots;
-        ok = warp_all(wait(&sh.qempty[qs], at / C::kQSlots + 1, 65));
+        // (that of a piece with one row tile has a place of its own, which lasts as long as the piece)
+        const int slot = cnt % kLseSlots;
+        if (!pc.few) ok = warp_all(wait(&sh.lempty[slot], cnt / kLseSlots + 1, 65));
         if (!ok) break;
-        float* const dst = pc.few ? sh.few_lse[k % kPieces] : sh.lse[qs];
+        float* const dst = pc.few ? sh.few_lse[k % kPieces] : sh.lse[slot];
 #pragma unroll
         for (int j = 0; j < 4; ++j) dst[lane + 32 * j] = v[j];
-        arrive(&sh.qfull[qs]);
+        __syncwarp();
+        if (!pc.few) {
+          if (lane == 0) mbar_arrive(&sh.lfull[slot]);
+          ++cnt;
+        }
       }
       if (ok && lane == 0) mbar_arrive(&sh.few_full[k % kPieces]);
-      qcnt += tiles;
       arrive(&sh.wfree[k % kPieces]);
     }
   } else if (warp >= kMmaWarp) {
@@ -435,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = (warp & 3) * 32 + lane, key = t * kBlockN + row;  // in the block
     const uint32_t tS = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + (2 * buf + t) * 128;
     const uint64_t sl2 = pack_f32x2(p.scale_log2, p.scale_log2);
-    int qcnt = 0, scnt = 0;
+    int lcnt = 0, scnt = 0;
     bool ok = true;
     // The sum over a row tile's columns, all of which count (one without a row has a score of 0 and an lse of inf): each 32
     // columns' load runs under the exponentials of the 32 before.
@@ -531,35 +533,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Piece pc = sh.piece[k % kPieces];
       if (pc.b < 0) break;
       const int steps = pc.count == 0 ? 0 : max(0, pc.i1 - pc.i0);
-      // the place of a key's weight (looked up ahead of the sums)
-      auto place = [&](int pos) -> float* {
-        if (pos >= pc.len) return nullptr;
-        const int pg = p.seqs.table[pc.b * p.seqs.table_stride + (pos >> p.seqs.page_shift)];
-        if (pg < 0 || pg >= p.seqs.n_pages) return nullptr;
-        return p.weights + pg * p.w_spage + pc.kvh * p.w_shead + (pos & ((1 << p.seqs.page_shift) - 1));
+      // The page of a key's weight, looked up ahead of the sums and first looked at when they are there.
+      auto page_of = [&](int pos) -> int {
+        return pos < pc.len ? p.seqs.table[pc.b * p.seqs.table_stride + (pos >> p.seqs.page_shift)] : -1;
       };
-      auto put = [&](float* dst, float sum) {
-        if (dst != nullptr && !(p.accumulate && sum == 0.f)) *dst = p.accumulate ? *dst + sum : sum;
+      auto put = [&](int pg, int pos, float sum) {
+        if (pg < 0 || pg >= p.seqs.n_pages || (p.accumulate && sum == 0.f)) return;
+        float* const dst = p.weights + pg * p.w_spage + pc.kvh * p.w_shead + (pos & ((1 << p.seqs.page_shift) - 1));
+        *dst = p.accumulate ? *dst + sum : sum;
       };
       if (pc.few) {
         if (steps > 0) ok = warp_all(wait(&sh.few_full[k % kPieces], k / kPieces, 71));
         const int first = pc.i0 + ((scnt ^ buf) & 1);  // this buffer's first step
-        float* next = first < pc.i1 ? place(first * kKeys + key) : nullptr;
+        int next = first < pc.i1 ? page_of(first * kKeys + key) : -1;
         for (int i = first; ok && i < pc.i1; i += 2) {
-          float* const dst = next;
-          next = i + 2 < pc.i1 ? place((i + 2) * kKeys + key) : nullptr;
+          const int pg = next;
+          next = i + 2 < pc.i1 ? page_of((i + 2) * kKeys + key) : -1;
           float sum = 0.f;
           if (steps > 0) ok = columns(pc, 0, scnt + (i - pc.i0), i * kKeys + key, sh.few_lse[k % kPieces], sum);
           if (!ok) break;
-          put(dst, sum);
+          put(pg, i * kKeys + key, sum);
         }
         if (!ok) break;
-        if (steps > 0 && ((scnt + steps - 1) & 1) == buf) arrive(&sh.qempty[qcnt % C::kQSlots]);
-        if (steps > 0) ++qcnt;
         scnt += steps;
       } else {
         const int pos = pc.key0 + key;
-        float* const dst = buf == 0 && pc.slot < 0 ? place(pos) : nullptr;
+        const int pg = buf == 0 && pc.slot < 0 ? page_of(pos) : -1;
         // row tiles [f0, f1) are full, and all their rows see all of the warp's keys (of a group in parts none is taken as such)
         int f0 = 0, f1 = 0;
         if (p.tile.parts == 1) {
@@ -571,17 +570,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         float total = 0.f;
         const int i0 = pc.i0 + ((scnt ^ buf) & 1);  // this buffer's first step
         for (int i = i0; i < pc.i1; i += 2) {
-          const int step = scnt + (i - pc.i0), at = qcnt + (i - pc.i0), qs = at % C::kQSlots;
+          const int step = scnt + (i - pc.i0), at = lcnt + (i - pc.i0), slot = at % kLseSlots;
           float sum;
-          ok = warp_all(wait(&sh.qfull[qs], at / C::kQSlots, 69));
-          if (ok) ok = i >= f0 && i < f1 ? all_columns(step, sh.lse[qs], sum) : columns(pc, i, step, pos, sh.lse[qs], sum);
+          ok = warp_all(wait(&sh.lfull[slot], at / kLseSlots, 69));
+          if (ok) ok = i >= f0 && i < f1 ? all_columns(step, sh.lse[slot], sum) : columns(pc, i, step, pos, sh.lse[slot], sum);
           if (!ok) break;
-          arrive(&sh.qempty[qs]);
+          arrive(&sh.lempty[slot]);
           total += sum;
         }
         if (!ok) break;
         scnt += steps;
-        qcnt += steps;
+        lcnt += steps;
         if (buf == 1) {
           sh.sums[k % kPieces][t][row] = total;
         } else {
@@ -591,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (pc.slot >= 0)
             p.part[static_cast<int64_t>(pc.slot) * kKeys + key] = total;
           else
-            put(dst, total);
+            put(pg, pos, total);
         }
       }
       if (buf == 1) arrive(&sh.sums_full[k % kPieces][t]);
