@@ -25,8 +25,8 @@ namespace cg = cooperative_groups;
 namespace slope {
 namespace {
 
-constexpr int kSelectThreads = 1024;
-constexpr int kMaxCluster = 16;
+constexpr int kSelectThreads = 512;
+constexpr int kMaxCluster = 8;
 constexpr int kBins = 2048;
 constexpr int kRun = 8192;          // keys of a CTA, as long as clusters allow it
 constexpr int kHeldKeys = 40960;    // of them in shared memory at most; more are made again in every pass
@@ -78,8 +78,8 @@ __device__ __forceinline__ uint2 block_scan(uint2 v, uint2* scratch, uint2& tota
   __syncthreads();
   if (lane == 31) scratch[warp] = incl;
   __syncthreads();
-  static_assert(kSelectThreads == 1024, "a warp's lanes for the warps");
-  const uint2 mine = scratch[lane];
+  static_assert(kSelectThreads <= 1024, "a warp's lanes for the warps");
+  const uint2 mine = lane < kSelectThreads / 32 ? scratch[lane] : make_uint2(0, 0);
   uint2 before;
   before.x = __reduce_add_sync(0xffffffffu, lane < warp ? mine.x : 0u);
   before.y = __reduce_add_sync(0xffffffffu, lane < warp ? mine.y : 0u);
@@ -88,11 +88,12 @@ __device__ __forceinline__ uint2 block_scan(uint2 v, uint2* scratch, uint2& tota
   return make_uint2(before.x + incl.x - v.x, before.y + incl.y - v.y);
 }
 
-__global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const __grid_constant__ KvEvictParams p) {
+__global__ void __launch_bounds__(kSelectThreads, 2) kv_select_kernel(const __grid_constant__ KvEvictParams p) {
   cg::cluster_group cluster = cg::this_cluster();
   extern __shared__ uint32_t s_keys[];
   __shared__ __align__(16) uint32_t s_hist[kBins];
-  __shared__ uint32_t s_bin[2];  // the bin with the wanted rank, and the rank within it
+  __shared__ uint32_t s_bin[3];             // the bin with the wanted rank, the rank within it, and the keys in it
+  __shared__ uint32_t s_slice[kMaxCluster];  // keys in each CTA's slice of the bins
   __shared__ uint2 s_scan[kSelectThreads / 32], s_count;
   pdl_launch_dependents();
   const int ranks = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
@@ -111,6 +112,12 @@ __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const __grid_
     for (int j = me; j < keep; j += stride) kept[j] = j < n ? j : -1;
     return;  // (the whole cluster does)
   }
+  auto sync = [&]() {
+    if (ranks > 1)
+      cluster.sync();
+    else
+      __syncthreads();
+  };
   // tokens before and after the ones to choose from
   for (int j = me; j < p.first; j += stride) kept[j] = j;
   for (int j = me; j < p.recent; j += stride) kept[keep - p.recent + j] = n - p.recent + j;
@@ -127,19 +134,23 @@ __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const __grid_
     return pg < 0 || pg >= p.seqs.n_pages ? 0u : weight_key(weights[pg * p.w_spage + (t & in_page)]);
   };
   // eight loads of pages, then of weights, in flight
+  constexpr int kAhead = 8;
   const int held = min(t1 - t0, p.held);
-  for (int i0 = threadIdx.x; i0 < held; i0 += 8 * kSelectThreads) {
-    int pg[8];
-    float w[8];
+  for (int i0 = threadIdx.x; i0 < held; i0 += kAhead * kSelectThreads) {
+    int pg[kAhead];
+    float w[kAhead];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) pg[e] = i0 + e * kSelectThreads < held ? row[(t0 + i0 + e * kSelectThreads) >> p.seqs.page_shift] : -1;
+    for (int e = 0; e < kAhead; ++e) {
+      const int i = i0 + e * kSelectThreads;
+      pg[e] = i < held ? row[(t0 + i) >> p.seqs.page_shift] : -1;
+    }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < kAhead; ++e) {
       if (pg[e] >= p.seqs.n_pages) pg[e] = -1;
       w[e] = pg[e] >= 0 ? weights[pg[e] * p.w_spage + ((t0 + i0 + e * kSelectThreads) & in_page)] : 0.f;
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
+    for (int e = 0; e < kAhead; ++e)
       if (i0 + e * kSelectThreads < held) s_keys[i0 + e * kSelectThreads] = pg[e] >= 0 ? weight_key(w[e]) : 0u;
   }
   auto key = [&](int t) -> uint32_t { return t - t0 < p.held ? s_keys[t - t0] : read_key(t); };
@@ -161,29 +172,43 @@ __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const __grid_
       const uint32_t k = key(t);
       if ((k & high) == prefix) atomicAdd(&s_hist[(k >> shift) & ((1u << bits) - 1)], 1u);
     }
-    cluster.sync();
-    // bins from the top, two to a thread
-    static_assert(kBins == 2 * kSelectThreads, "two bins to a thread");
-    const int bin = kBins - 2 - 2 * threadIdx.x;
-    uint2 c = make_uint2(0, 0);  // of bin and bin + 1
-#pragma unroll 4
-    for (int r = 0; r < ranks; ++r) {
-      const uint2 x = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(s_hist, r) + bin);
-      c.x += x.x, c.y += x.y;
+    sync();
+    // Each CTA adds its slice of the bins up, four to a thread from the top (slice 0 is the top one).
+    const int slice = kBins / ranks, bin = kBins - rank * slice - 4 - 4 * static_cast<int>(threadIdx.x);
+    uint32_t c[4] = {0, 0, 0, 0};  // of bin .. bin + 3
+    if (4 * static_cast<int>(threadIdx.x) < slice) {
+#pragma unroll 8
+      for (int r = 0; r < ranks; ++r) {
+        const uint4 x = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(s_hist, r) + bin);
+        c[0] += x.x, c[1] += x.y, c[2] += x.z, c[3] += x.w;
+      }
     }
     uint2 total;
-    const uint32_t above = block_scan(make_uint2(c.x + c.y, 0), s_scan, total).x;
-    if (above < left && left <= above + c.y) {
-      s_bin[0] = bin + 1;
-      s_bin[1] = left - above;
-    } else if (above + c.y < left && left <= above + c.y + c.x) {
-      s_bin[0] = bin;
-      s_bin[1] = left - above - c.y;
+    uint32_t above = block_scan(make_uint2(c[0] + c[1] + c[2] + c[3], 0), s_scan, total).x;
+    if (ranks > 1) {
+      if (static_cast<int>(threadIdx.x) < ranks) *cluster.map_shared_rank(&s_slice[rank], threadIdx.x) = total.x;
+      cluster.sync();
+      for (int r = 0; r < rank; ++r) above += s_slice[r];
     }
-    cluster.sync();  // the histograms are read, the bin is written
+#pragma unroll
+    for (int i = 3; i >= 0; --i) {
+      if (above < left && left <= above + c[i]) {
+        for (int r = 0; r < ranks; ++r) {
+          uint32_t* const to = cluster.map_shared_rank(s_bin, r);
+          to[0] = bin + i, to[1] = left - above, to[2] = c[i];
+        }
+      }
+      above += c[i];
+    }
+    sync();  // the bin is known
     if (want > 0) {
       prefix |= s_bin[0] << shift;
       left = s_bin[1];
+      if (left == s_bin[2]) {  // all of the bin stay: every key above the ones below it
+        prefix -= 1;           // (some key does not stay, so this is not the lowest bin)
+        left = 0;
+        break;
+      }
     }
   }
   if (want == 0) prefix = ~0u, left = 0;  // no key is as large
@@ -196,7 +221,7 @@ __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const __grid_
   }
   uint2 before = block_scan(mine, s_scan, total);
   if (threadIdx.x == 0) s_count = total;
-  cluster.sync();
+  sync();
   if (threadIdx.x < 32) {
     uint2 c = make_uint2(0, 0);
     if (static_cast<int>(threadIdx.x) < rank) c = *cluster.map_shared_rank(&s_count, threadIdx.x);
@@ -204,14 +229,18 @@ __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const __grid_
     c.y = __reduce_add_sync(0xffffffffu, c.y);
     if (threadIdx.x == 0) s_scan[0] = c;
   }
-  cluster.sync();  // (no CTA leaves before its counts are read)
+  sync();  // (no CTA leaves before its counts are read)
   before.x += s_scan[0].x, before.y += s_scan[0].y;
 
   // ---- places
+  int edge = (a0 + p.chunk - 1) / p.chunk;  // the next bound that lies in the run
   for (int t = a0; t < a1; ++t) {
     const uint32_t k = key(t);
     const int j = p.first + static_cast<int>(before.x + min(before.y, left));
-    if (t % p.chunk == 0 && t / p.chunk <= p.chunks) bounds[t / p.chunk] = j;
+    if (t == edge * p.chunk) {
+      if (edge <= p.chunks) bounds[edge] = j;
+      ++edge;
+    }
     if (k > prefix || (k == prefix && before.y < left)) kept[j] = t;
     before.x += k > prefix ? 1u : 0u, before.y += k == prefix ? 1u : 0u;
   }
