@@ -104,13 +104,13 @@ __device__ __forceinline__ Piece make_piece(const KvAttnParams& p, int per, cons
   const KvSeq q = lists.seqs[b];
   const SeqCut cut = cut_of(q);
   pieces = pieces_of(cut.steps, per);
-  uint32_t local = w - lists.units[b];
-  const int blk = cut.blocks - 1 - static_cast<int>(local % cut.blocks);
-  local /= cut.blocks;
-  c = static_cast<int>(local % pieces);
-  const int h = static_cast<int>(local / pieces);
+  // local = (head * pieces + c) * blocks + (blocks - 1 - block)
+  const uint32_t local = w - lists.units[b], rest = cut.blocks == 1 ? local : divide(local, cut.blocks);
+  const int blk = cut.blocks - 1 - static_cast<int>(local - rest * cut.blocks);
+  const int h = static_cast<int>(pieces == 1 ? rest : divide(rest, pieces));
+  c = static_cast<int>(rest) - h * pieces;
   r.b = p.seqs.b0 + b;
-  r.kvh = h / p.tile.parts;
+  r.kvh = p.tile.parts == 1 ? h : h / p.tile.parts;
   const int first = (h - r.kvh * p.tile.parts) * p.tile.heads;
   r.head0 = r.kvh * p.group + first;
   r.heads = min(p.tile.heads, p.group - first);
@@ -762,12 +762,26 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attn_join_kernel(const __grid
   const int chunks = (p.rows_cap * (DV / 4) + 127) / 128;
   const int grp = threadIdx.x >> 7, lane = threadIdx.x & 127;
   int slot = blockIdx.x / chunks, chunk = blockIdx.x - slot * chunks;
-  // (the first pair's record is read along with what says whether it counts)
+  // What the first pair's join reads, read along with what says whether there is one: those latencies are most of a small
+  // call's join.
+  float2 ml[kAhead];
+  float4 v[kAhead];
+  auto fetch = [&](int at, int rr, int ch, int c0, int last) {  // pieces c0, c0 + kGroups, ... up to the last of pair `at`
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int64_t prow = static_cast<int64_t>(at + min(c0 + k * kGroups, last)) * p.rows_cap + rr;
+      ml[k] = p.ml[prow];
+      v[k] = *reinterpret_cast<const float4*>(p.part + prow * DV + ch);
+    }
+  };
   KvPair e = p.pairs[min(slot, p.max_slots - 1)];
+  fetch(min(slot, p.max_slots - 1), min((chunk * 128 + lane) / (DV / 4), p.rows_cap - 1), (lane % (DV / 4)) * 4, grp,
+        max(0, p.max_slots - 1 - slot));
   const int n_slots = min(*p.n_slots, p.max_slots);
   if (*reinterpret_cast<volatile int*>(p.status) != 0) return;  // pieces may be missing
   for (int64_t item = blockIdx.x; slot < n_slots; item += gridDim.x) {
-    if (item != blockIdx.x) {
+    const bool fetched = item == blockIdx.x;
+    if (!fetched) {
       slot = static_cast<int>(item / chunks), chunk = static_cast<int>(item - static_cast<int64_t>(slot) * chunks);
       if (slot >= n_slots) break;
       e = p.pairs[slot];
@@ -793,17 +807,11 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attn_join_kernel(const __grid
       sum.x *= alpha, sum.y *= alpha, sum.z *= alpha, sum.w *= alpha;
     };
     for (int c0 = grp; c0 < e.pieces; c0 += kAhead * kGroups) {
-      float2 ml[kAhead];
-      float4 v[kAhead];
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const int64_t prow = static_cast<int64_t>(slot + min(c0 + k * kGroups, e.pieces - 1)) * p.rows_cap + rr;
-        ml[k] = p.ml[prow];
-        v[k] = *reinterpret_cast<const float4*>(p.part + prow * DV + ch);
-      }
+      if (!(fetched && c0 == grp)) fetch(slot, rr, ch, c0, e.pieces - 1);
       float now = mm;
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) now = fmaxf(now, ml[k].x);
+      for (int k = 0; k < kAhead; ++k)
+        if (c0 + k * kGroups < e.pieces) now = fmaxf(now, ml[k].x);
       move(now);
 #pragma unroll
       for (int k = 0; k < kAhead; ++k)

@@ -13,7 +13,15 @@ struct SeqCut {
   int blocks, steps;
   bool join;  // the pieces of a pair are joined (else each writes results of its own)
 };
-__device__ __forceinline__ int pieces_of(int steps, int per) { return max(1, (steps + per - 1) / per); }
+// a / b, without a division's forty instructions where a < 2^20: a quotient next to a whole number is at least 1 / (2 b) away
+// from it with the half added, and off by at most 2^-22 of itself.
+__device__ __forceinline__ uint32_t divide(uint32_t a, uint32_t b) {
+  if (a >= (1u << 20)) return a / b;
+  return __float2uint_rz(__fdividef(static_cast<float>(a) + 0.5f, static_cast<float>(b)));
+}
+__device__ __forceinline__ int pieces_of(int steps, int per) {
+  return max(1, static_cast<int>(divide(static_cast<uint32_t>(steps + per - 1), static_cast<uint32_t>(per))));
+}
 
 // The sequences' records and first pieces, in shared memory.
 struct CutLists {
@@ -41,56 +49,79 @@ __device__ __forceinline__ float warp_sum(float v) {
 // One whole warp calls it: reads the sequences, chooses the pieces' length and fills the lists.  cut_of(seq) gives a
 // sequence's SeqCut; kPieceSteps is what a piece's start and end cost, in steps.
 //
-// The longest pair is cut into pieces of about 1 / (2 kFine) to 4 / kFine of a share, and the length of those is tried as
-// every pair's.  The length with the least time wins: that of one piece or of an even share of all of them, whichever is more,
-// and half a piece for the uneven end where there are more pieces than CTAs.  (Estimates in fp32, the same in every CTA.)
+// The longest pair is cut into as many pieces as give every CTA one, or into pieces of about 1 / (2 kFine) to 3 / kFine of
+// a share, and the length of those is tried as every pair's.  The length with the least time wins: that of the rounds over
+// the grid where the pieces are all alike, else that of one piece or of an even share of all of them, whichever is
+// more, and half a piece for the uneven end.  (8 sequences of 102400 tokens with 64/8 heads: 640 pieces of 80 steps for 304
+// CTAs took 327 us, 256 of 200 take 260.)  Estimates are in fp32, the same in every CTA.  This runs before a call's
+// first load: the six lengths are tried side by side, as one after another they took 1.3 us.
 template <int kPieceSteps, int kFine, typename CutOf>
 __device__ __forceinline__ Cut make_cut(const KvSeqs& p, int heads, const CutOf& cut_of, CutLists& lists) {
-  constexpr int kTries = 6;
-  constexpr float kShares[kTries] = {0.5f, 0.75f, 1.f, 1.5f, 2.5f, 4.f};
   const int B = p.B, lane = threadIdx.x & 31;
-  const float per_cta = static_cast<float>(heads) / static_cast<float>(gridDim.x);
+  const float per_cta = __fdividef(static_cast<float>(heads), static_cast<float>(gridDim.x));
   float all = 0.f;
   int most = 1;
+  uint32_t pairs = 0;        // of a lane at most 2^24
+  SeqCut mine{0, 0, false};  // of the lane's only sequence, where there are no more than 32
+#pragma unroll 1
   for (int b = lane; b < B; b += 32) {
     const KvSeq q = kv_seq(p, b);
     lists.seqs[b] = q;
-    const SeqCut c = cut_of(q);
-    all += static_cast<float>(c.blocks) * static_cast<float>(c.steps);
-    if (c.blocks > 0) most = max(most, c.steps);
-  }
-  most = __reduce_max_sync(0xffffffffu, most);
-  const float share = fmaxf(1.f, warp_sum(all) * per_cta);
-  int per[kTries];
-  float count[kTries], inv[kTries];
-#pragma unroll
-  for (int i = 0; i < kTries; ++i) {
-    const float n = fmaxf(1.f, rintf(__fdividef(static_cast<float>(most), share * (kShares[i] / kFine))));  // pieces of the longest
-    per[i] = static_cast<int>(ceilf(__fdividef(static_cast<float>(most), n)));
-    if (2.f * kFine * static_cast<float>(per[i]) < share) per[i] = most;  // (see max_joined)
-    inv[i] = __frcp_rn(static_cast<float>(per[i]));
-    count[i] = 0.f;
+    mine = cut_of(q);
+    all += static_cast<float>(mine.blocks) * static_cast<float>(mine.steps);
+    pairs = min(pairs + static_cast<uint32_t>(mine.blocks), 1u << 24);
+    if (mine.blocks > 0) most = max(most, mine.steps);
   }
   __syncwarp();
-  for (int b = lane; b < B; b += 32) {
-    const SeqCut c = cut_of(lists.seqs[b]);
+  most = __reduce_max_sync(0xffffffffu, most);
+  const float share = fmaxf(1.f, warp_sum(all) * per_cta), longest = static_cast<float>(most);
+  constexpr int kTries = 6;
+  constexpr float kShares[kTries] = {0.f, 0.5f, 0.75f, 1.f, 1.6f, 3.f};
+  const float one_each = floorf(__fdividef(1.f, static_cast<float>(__reduce_add_sync(0xffffffffu, pairs)) * per_cta));
+  int per[kTries];
+  float inv[kTries];
+  uint32_t count[kTries];  // of a lane at most 2^24
+  auto add = [&](const SeqCut& c) {
 #pragma unroll
     for (int i = 0; i < kTries; ++i)
-      count[i] += static_cast<float>(c.blocks) * fmaxf(1.f, ceilf(static_cast<float>(c.steps) * inv[i] - 1e-4f));
+      count[i] = static_cast<uint32_t>(fminf(
+          static_cast<float>(count[i]) +
+              static_cast<float>(c.blocks) * fmaxf(1.f, ceilf(static_cast<float>(c.steps) * inv[i] - 1e-4f)),
+          16777216.f));
+  };
+#pragma unroll
+  for (int i = 0; i < kTries; ++i) {
+    // pieces of the longest
+    const float n = fmaxf(1.f, i == 0 ? fminf(one_each, longest) : rintf(__fdividef(longest, share * (kShares[i] / kFine))));
+    per[i] = static_cast<int>(ceilf(__fdividef(longest, n)));
+    if (2.f * kFine * static_cast<float>(per[i]) < share) per[i] = most;  // (see max_joined)
+    inv[i] = __fdividef(1.f, static_cast<float>(per[i]));
+    count[i] = 0;
+  }
+  if (B <= 32) {
+    add(mine);
+  } else {
+#pragma unroll 1
+    for (int b = lane; b < B; b += 32) add(cut_of(lists.seqs[b]));
   }
   Cut r;
   r.per = most;
   float best = INFINITY;
 #pragma unroll
   for (int i = 0; i < kTries; ++i) {
-    const float rounds = warp_sum(count[i]) * per_cta, piece = static_cast<float>(per[i] + kPieceSteps);
-    const float cost = fmaxf(piece, share + rounds * kPieceSteps) + (rounds > 1.f ? 0.5f * piece : 0.f);
+    const float rounds = static_cast<float>(__reduce_add_sync(0xffffffffu, count[i])) * per_cta;
+    const float piece = static_cast<float>(per[i] + kPieceSteps);
+    const float even = share + rounds * kPieceSteps;
+    const float cost = rounds <= 1.f                   ? fmaxf(piece, even)
+                       : even > 0.9f * rounds * piece ? ceilf(rounds) * piece
+                                                       : fmaxf(piece, even) + 0.5f * piece;
     if (cost < best) {
       best = cost;
       r.per = per[i];
     }
   }
   r.total = r.slots = 0;
+#pragma unroll 1
   for (int b0 = 0; b0 < B; b0 += 32) {
     const int b = b0 + lane;
     uint32_t u = 0, sl = 0;
@@ -129,7 +160,8 @@ __device__ __forceinline__ int seq_of(const CutLists& lists, int B, uint32_t w) 
 
 // Steps [first, last) of piece c out of `pieces`.
 __device__ __forceinline__ void piece_steps(int steps, int pieces, int c, int& first, int& last) {
-  const int each = steps / pieces, more = steps - each * pieces;
+  const int each = static_cast<int>(divide(static_cast<uint32_t>(steps), static_cast<uint32_t>(pieces)));
+  const int more = steps - each * pieces;
   first = c * each + min(c, more);
   last = first + each + (c < more ? 1 : 0);
 }

@@ -135,11 +135,11 @@ __device__ __forceinline__ Piece make_piece(const KvWeightsParams& p, int per, c
   const KvSeq q = lists.seqs[b];
   const SeqCut cut = cut_of(q);
   pieces = pieces_of(cut.steps, per);
-  uint32_t local = w - lists.units[b];
-  const int blk = static_cast<int>(local % cut.blocks);
-  local /= cut.blocks;
-  c = static_cast<int>(local % pieces);
-  r.kvh = static_cast<int>(local / pieces);
+  // local = (head * pieces + c) * blocks + block
+  const uint32_t local = w - lists.units[b], rest = cut.blocks == 1 ? local : divide(local, cut.blocks);
+  const int blk = static_cast<int>(local - rest * cut.blocks);
+  r.kvh = static_cast<int>(pieces == 1 ? rest : divide(rest, pieces));
+  c = static_cast<int>(rest) - r.kvh * pieces;
   r.b = p.seqs.b0 + b;
   r.few = cut.join ? 0 : 1;
   r.len = q.len;
