@@ -146,7 +146,7 @@ struct Cfg {
   static constexpr int kSlotBytes = kKTileBytes > kVTileBytes ? kKTileBytes : kVTileBytes;
   static constexpr int kSlots = (QT == 2 ? 131072 : 65536) / kSlotBytes;
   static_assert(kSlots % 2 == 0 && kSlots / 2 + 2 <= kHoles, "K tiles in even slots, V tiles in odd ones");
-  static constexpr int kNumBars = 2 + 2 * kSlots + 6 * QT + 4 * QT + 4;
+  static constexpr int kNumBars = 2 + 2 * kSlots + 7 * QT + 4 * QT + 4;
   static constexpr int kSlotOffset = QT * kQTileBytes;
   static constexpr int kRestOffset = kSlotOffset + kSlots * kSlotBytes;
   struct Rest {  // behind the tiles
@@ -185,7 +185,8 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
   uint64_t* const bar_s = bar_empty + C::kSlots;
   uint64_t* const bar_sfree = bar_s + QT;  // softmax t has loaded S_t into registers
   uint64_t* const bar_p = bar_sfree + QT;
-  uint64_t* const bar_o = bar_p + QT;
+  uint64_t* const bar_p2 = bar_p + QT;  // P over S: the last quarter of P_t
+  uint64_t* const bar_o = bar_p2 + QT;
   uint64_t* const bar_ofree = bar_o + QT;
   uint64_t* const bar_drain = bar_ofree + QT;
   uint64_t* const bar_turn = bar_drain + QT;     // [t * 4 + quarter]: that softmax warp may exponentiate
@@ -221,6 +222,7 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
       mbar_init(&bar_s[t], 1);
       mbar_init(&bar_sfree[t], 4);
       mbar_init(&bar_p[t], 4);
+      mbar_init(&bar_p2[t], 4);
       mbar_init(&bar_o[t], 1);
       mbar_init(&bar_ofree[t], 4);
       mbar_init(&bar_drain[t], 1);
@@ -393,8 +395,13 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
         }
         const uint32_t vlo = smem_desc_lo(smem_u32(sSlot + vslot * C::kSlotBytes), kChunkBytes);
 #pragma unroll
-        for (int kk = 0; kk < kBlockN / 16; ++kk)
+        for (int kk = 0; kk < kBlockN / 16; ++kk) {
+          if (!C::kSepP && kk == 6) {  // the last quarter of P may still have been on its way
+            if (!wait_bounded(&bar_p2[t], n & 1, cta_abort, p.status, limit, 50)) return false;
+            tc_fence_after_sync();
+          }
           mma_ts_lh(d_o, a_p + kk * 8, vlo + ((kk * 2048) >> 4), kDescHi, idesc_pv, (!first || kk > 0) ? 1u : 0u);
+        }
         mma_commit(&bar_o[t]);
         return true;
       };
@@ -425,12 +432,13 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
         if (!wait_bounded(bar_q, wt & 1, cta_abort, p.status, limit, 39)) break;
         ++wt;
         tc_fence_after_sync();
-        bool first = true;
+        bool first = true, keys_there = false;
         for (int j = j0; ok && j < j1; ++j) {
           const uint32_t kslot = cnt % C::kSlots, kph = (cnt / C::kSlots) & 1;
           const uint32_t vslot = (cnt + 1) % C::kSlots, vph = ((cnt + 1) / C::kSlots) & 1;
           cnt += 2;
-          ok = wait_bounded(&bar_full[kslot], kph, cta_abort, p.status, limit, 40);
+          if (!keys_there) ok = wait_bounded(&bar_full[kslot], kph, cta_abort, p.status, limit, 40);
+          keys_there = false;
           if (!ok) break;
           // With S_t the softmax clears the end of this step's V slot, and has to find the slot's previous fill gone:
           // of two slots, that is the V whose PV is pending.
@@ -455,6 +463,8 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
             if (part) ++n;
           } else {
             ok = wait_bounded(&bar_full[vslot], vph, cta_abort, p.status, limit, 42);
+            // (looked at here, where the issuer waits anyway, the next keys need no look between the products)
+            if (ok && part && j + 1 < j1) keys_there = mbar_try_wait(&bar_full[cnt % C::kSlots], (cnt / C::kSlots) & 1);
             if (ok && part) {
               ok = wait_bounded(&bar_p[t], n & 1, cta_abort, p.status, limit, 43);
               if (ok) {
@@ -526,9 +536,9 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
       float m_used = -INFINITY;  // running maximum, log2 units
       float l = 0.f;             // running sum of exp2(s * sl2 - m_used)
       for (; ok && j < pc.j1; ++j, ++n) {
+        const bool inside = j >= pc.flo[t] && j < pc.fhi[t];
         ok = warp_all(wait_bounded(&bar_s[t], n & 1, cta_abort, p.status, limit, 45));
         if (!ok) break;
-        const bool inside = j >= pc.flo[t] && j < pc.fhi[t];
         if (!inside && (j + 1) * kBlockN > pc.len) {
           // The sequence ends inside this tile.  The V rows behind it have a weight of 0, but 0 times a NaN there would
           // still be NaN: clear them before this Q tile's PV may read them.  S_t is there, so the issuer has waited for
@@ -554,6 +564,7 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
           }
           if (!ok) break;
           arrive(&bar_p[t]);
+          if (!C::kSepP) arrive(&bar_p2[t]);
           continue;
         }
         const uint32_t holes = *const_cast<volatile uint32_t*>(&sh.holes[static_cast<uint32_t>(n + skipped) % kHoles]);
@@ -625,6 +636,22 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
         m_used = need ? m_new : m_used;
         l *= alpha;
         const float msub = (m_used == -INFINITY) ? 0.f : m_used;
+        // O_t holds the previous PV's result: with P in columns of its own once the wait for them is over, with P over S
+        // because the issuer waited for that PV before it sent S_t.
+        auto rescale = [&]() {
+          if (!__any_sync(0xffffffffu, need) || j <= pc.j0) return;
+#pragma unroll 1
+          for (int c = 0; c < DV / 16; ++c) {
+            uint32_t o[16];
+            tmem_ld16(tO + c * 16, o);
+            tmem_ld_wait();
+            reg_fence(o);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st16(tO + c * 16, o);
+          }
+        };
+        if (!C::kSepP) rescale();
         if (turns) {
           ok = take_turn();
           if (!ok) break;
@@ -639,6 +666,11 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
           if (C::kSepP && i == 15) {  // S_t is in registers: the next S MMA may overwrite it
             tc_fence_before_sync();
             arrive(&bar_sfree[t]);
+          }
+          if (!C::kSepP && i == 55) {  // three quarters of P are there: the PV may begin
+            tmem_st_wait();
+            tc_fence_before_sync();
+            arrive(&bar_p[t]);
           }
           if ((i & 15) == 15) {
             const int c = i >> 4;
@@ -663,22 +695,10 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
         const float2 c2 = unpack_f32x2(acc[2]), c3 = unpack_f32x2(acc[3]);
         l += ((c0.x + c0.y) + (c1.x + c1.y)) + ((c2.x + c2.y) + (c3.x + c3.y));
         if (turns) pass_turn();
-        // O_t holds the previous PV's result (P's columns, or the issuer's wait before S_t, say that it is done)
-        if (__any_sync(0xffffffffu, need) && j > pc.j0) {
-#pragma unroll 1
-          for (int c = 0; c < DV / 16; ++c) {
-            uint32_t o[16];
-            tmem_ld16(tO + c * 16, o);
-            tmem_ld_wait();
-            reg_fence(o);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-            tmem_st16(tO + c * 16, o);
-          }
-        }
+        if (C::kSepP) rescale();
         tmem_st_wait();
         tc_fence_before_sync();
-        arrive(&bar_p[t]);
+        arrive(C::kSepP ? &bar_p[t] : &bar_p2[t]);
       }
       if (!ok) break;
 
