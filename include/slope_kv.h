@@ -112,7 +112,7 @@ SLOPE_API slope_status slope_kv_write(const slope_kv_cache* cache, const slope_t
  *     need one each, captured graphs that may be replayed at the same time too.
  * B == 0 or T == 0 is a no-op.
  *
- * A launch takes one of the SLOPE_TILE_COUNTERS (slope.h), another for every 1024
+ * A launch takes one of the SLOPE_TILE_COUNTERS (slope.h), another for every 512
  * sequences after the first.  Softmax weights are rounded to bf16 on their way
  * into the tensor cores; scores, maxima, sums and outputs stay in fp32 until the
  * output's rounding.  Whatever the cache holds behind a sequence's last token, NaN

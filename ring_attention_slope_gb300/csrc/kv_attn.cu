@@ -36,13 +36,12 @@ constexpr uint32_t kChunkBytes = 128 * 128;  // 128 rows x 64 bf16
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: the running maximum moves when a score passes it by this
 constexpr int kPieceSteps = 5;             // what a piece's start and end cost, in steps
-constexpr int kFine = 1;                   // (kv_cut.cuh)
 constexpr int kHoles = 8;                  // ring of the steps' missing pages: more than the K tiles in flight
 constexpr int kJoinThreads = 512;
 
-// A pair of which several pieces are joined; one for each piece, `pieces` 0 but in the first's.
+// A pair of which several pieces are joined.
 struct KvPair {
-  int32_t row0, tokens, head0, heads, pieces, pad[3];
+  int32_t row0, tokens, head0, heads, slot, pieces, pad[2];
 };
 
 struct KvAttnParams {
@@ -58,9 +57,9 @@ struct KvAttnParams {
   int64_t lse_srow, lse_shead;
   int32_t rows_cap;  // rows of a piece in the workspace
   int32_t max_slots;
-  int32_t* n_slots;  // workspace: pieces that are joined
-  KvPair* pairs;     // workspace, for each of them
-  float2* ml;        // workspace: m and l of its rows
+  int32_t* n_pairs;  // workspace: pairs that are joined
+  KvPair* pairs;     // workspace: those
+  float2* ml;        // workspace: m and l of a piece's rows
   float* part;       // workspace: O of its rows, not normalised
   int* status;
   uint32_t* tile_counter;
@@ -98,7 +97,7 @@ struct Piece {
 };
 
 __device__ __forceinline__ Piece make_piece(const KvAttnParams& p, int per, const CutLists& lists, uint32_t w,
-                                            const RowCut& cut_of, int& pieces, int& c) {
+                                            const RowCut& cut_of, int& join, int& pieces) {
   Piece r;
   const int b = seq_of(lists, p.seqs.B, w), block_tokens = cut_of.block_tokens;
   const KvSeq q = lists.seqs[b];
@@ -108,7 +107,7 @@ __device__ __forceinline__ Piece make_piece(const KvAttnParams& p, int per, cons
   const uint32_t local = w - lists.units[b], rest = cut.blocks == 1 ? local : divide(local, cut.blocks);
   const int blk = cut.blocks - 1 - static_cast<int>(local - rest * cut.blocks);
   const int h = static_cast<int>(pieces == 1 ? rest : divide(rest, pieces));
-  c = static_cast<int>(rest) - h * pieces;
+  const int c = static_cast<int>(rest) - h * pieces;
   r.b = p.seqs.b0 + b;
   r.kvh = p.tile.parts == 1 ? h : h / p.tile.parts;
   const int first = (h - r.kvh * p.tile.parts) * p.tile.heads;
@@ -124,7 +123,9 @@ __device__ __forceinline__ Piece make_piece(const KvAttnParams& p, int per, cons
   const int steps = j_hi - j_lo;
   piece_steps(steps, pieces, c, r.j0, r.j1);
   r.j0 += j_lo, r.j1 += j_lo;
-  r.slot = pieces > 1 ? static_cast<int32_t>(lists.slots[b]) + (h * cut.blocks + blk) * pieces + c : -1;
+  const int pair = h * cut.blocks + blk;
+  r.slot = pieces > 1 ? static_cast<int32_t>(lists.slots[b]) + pair * pieces + c : -1;
+  join = pieces > 1 && c == 0 ? static_cast<int32_t>(lists.joins[b]) + pair : -1;  // the first piece lists the pair
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int tile_tokens = p.tile.tokens, qa = r.pos0 + t * tile_tokens, rows = min(tile_tokens, r.tokens - t * tile_tokens);
@@ -139,6 +140,7 @@ struct Cfg {
   static constexpr int kTmaWarp = 4 * QT, kMmaWarp = kTmaWarp + 1;
   static constexpr int kThreads = 32 * (5 * QT + 1);
   static constexpr int kCtas = QT == 2 ? 1 : 2;  // on an SM
+  static constexpr int kFine = kCtas;            // (kv_cut.cuh; a piece of two Q tiles leaves 132 KB, so they are longer)
   static constexpr uint32_t kTmemCols = QT == 2 ? 512 : 256;
   static constexpr int kQChunks = DQK / 64, kVChunks = DV / 64;
   static constexpr int kQTileBytes = kQChunks * kChunkBytes;
@@ -244,8 +246,8 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
 
   if (warp == C::kTmaWarp) {
     // ================================================================ producer: pieces, pages, loads
-    const Cut cut = make_cut<kPieceSteps, kFine>(p.seqs, p.Hkv * p.tile.parts, cut_of, sh.lists);
-    if (lane == 0 && blockIdx.x == 0) *p.n_slots = static_cast<int32_t>(cut.slots);
+    const Cut cut = make_cut<kPieceSteps, C::kFine>(p.seqs, p.Hkv * p.tile.parts, cut_of, sh.lists);
+    if (lane == 0 && blockIdx.x == 0) *p.n_pairs = static_cast<int32_t>(cut.joins);
     const uint32_t total = cut.total;
     const uint32_t q_bytes = static_cast<uint32_t>(p.tile.heads * p.tile.tokens) * 128 * C::kQChunks;
     const int boxes_log = max(0, 7 - p.seqs.page_shift);  // log2 of the boxes of 64 channels of a key tile
@@ -268,18 +270,12 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
       }
       uint32_t next = 0;
       if (lane == 0) next = atomicAdd(p.tile_counter, 1u);  // on its way while this piece loads
-      int pieces, c;
-      const Piece pc = make_piece(p, cut.per, sh.lists, w, cut_of, pieces, c);
+      int join, pieces;
+      const Piece pc = make_piece(p, cut.per, sh.lists, w, cut_of, join, pieces);
       if (lane == 0) {
         sh.piece[k & 1] = pc;
         mbar_arrive(&bar_wfull[k & 1]);
-        if (pc.slot >= 0) {
-          KvPair e;
-          e.row0 = pc.row0, e.tokens = pc.tokens, e.head0 = pc.head0, e.heads = pc.heads;
-          e.pieces = c == 0 ? pieces : 0;
-          e.pad[0] = e.pad[1] = e.pad[2] = 0;
-          p.pairs[pc.slot] = e;
-        }
+        if (join >= 0) p.pairs[join] = KvPair{pc.row0, pc.tokens, pc.head0, pc.heads, pc.slot, pieces, {0, 0}};
       }
       if (pc.j1 > pc.j0) {
         // ---- pages: entry e0 + lane of the table in each lane, and the 32 after them on their way
@@ -771,46 +767,32 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
   }
 }
 
-// Joins the pieces of the pairs that were cut, in their order.  A work item is 128 lanes, four channels each, of one pair;
-// the CTA's four groups of 128 threads take every fourth piece, four of them in flight, and join at the end.
+// Joins the pieces of the pairs that were cut, in their order.  A lane has four channels of a row.  Few pieces (many rows:
+// a chunk's pairs): every thread has a row's channels of its own and all of its pieces in flight.  More (few rows: a
+// decode step): the CTA's four groups of 128 threads take every fourth piece, four in flight, and join at the end.
 template <int DV>
-__global__ void __launch_bounds__(kJoinThreads) kv_attn_join_kernel(const __grid_constant__ KvAttnParams p) {
+__global__ void __launch_bounds__(kJoinThreads, 2) kv_attn_join_kernel(const __grid_constant__ KvAttnParams p) {
   constexpr int kGroups = kJoinThreads / 128, kAhead = 4;
   __shared__ float s_m[kGroups][128], s_l[kGroups][128];
   __shared__ float4 s_v[kGroups][128];
-  pdl_wait();
-  const int chunks = (p.rows_cap * (DV / 4) + 127) / 128;
+  const int chunks = (p.rows_cap * (DV / 4) + kJoinThreads - 1) / kJoinThreads;
   const int grp = threadIdx.x >> 7, lane = threadIdx.x & 127;
-  int slot = blockIdx.x / chunks, chunk = blockIdx.x - slot * chunks;
-  // What the first pair's join reads, read along with what says whether there is one: those latencies are most of a small
-  // call's join.
-  float2 ml[kAhead];
-  float4 v[kAhead];
-  auto fetch = [&](int at, int rr, int ch, int c0, int last) {  // pieces c0, c0 + kGroups, ... up to the last of pair `at`
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int64_t prow = static_cast<int64_t>(at + min(c0 + k * kGroups, last)) * p.rows_cap + rr;
-      ml[k] = p.ml[prow];
-      v[k] = *reinterpret_cast<const float4*>(p.part + prow * DV + ch);
-    }
-  };
-  KvPair e = p.pairs[min(slot, p.max_slots - 1)];
-  fetch(min(slot, p.max_slots - 1), min((chunk * 128 + lane) / (DV / 4), p.rows_cap - 1), (lane % (DV / 4)) * 4, grp,
-        max(0, p.max_slots - 1 - slot));
-  const int n_slots = min(*p.n_slots, p.max_slots);
+  int pair = blockIdx.x / chunks, chunk = blockIdx.x - pair * chunks;
+  pdl_wait();
+  // (the first pair's record is read along with what says whether it counts)
+  KvPair e = p.pairs[min(pair, p.max_slots - 1)];
+  const int n_pairs = min(*p.n_pairs, p.max_slots);
   if (*reinterpret_cast<volatile int*>(p.status) != 0) return;  // pieces may be missing
-  for (int64_t item = blockIdx.x; slot < n_slots; item += gridDim.x) {
-    const bool fetched = item == blockIdx.x;
-    if (!fetched) {
-      slot = static_cast<int>(item / chunks), chunk = static_cast<int>(item - static_cast<int64_t>(slot) * chunks);
-      if (slot >= n_slots) break;
-      e = p.pairs[slot];
+  for (int64_t item = blockIdx.x; pair < n_pairs; item += gridDim.x) {
+    if (item != blockIdx.x) {
+      pair = static_cast<int>(item / chunks), chunk = static_cast<int>(item - static_cast<int64_t>(pair) * chunks);
+      if (pair >= n_pairs) break;
+      e = p.pairs[pair];
     }
-    const int i = chunk * 128 + lane;
     const int rows = e.tokens * p.tile.heads;
-    if (e.pieces <= 0 || slot + e.pieces > n_slots || e.row0 < 0 || e.row0 + e.tokens > p.seqs.T || rows > p.rows_cap) continue;
-    if ((i - lane) / (DV / 4) >= rows) continue;  // the same for every thread
-    const int rr = min(i / (DV / 4), rows - 1), ch = (i % (DV / 4)) * 4;
+    if (e.pieces <= 0 || e.slot < 0 || e.slot + e.pieces > p.max_slots || e.row0 < 0 || e.row0 + e.tokens > p.seqs.T ||
+        rows > p.rows_cap)
+      continue;
     float mm = -INFINITY, ll = 0.f;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
     // a piece whose row saw nothing has m = -inf and l = 0, and a NaN anywhere stays one
@@ -826,40 +808,68 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attn_join_kernel(const __grid
       ll *= alpha;
       sum.x *= alpha, sum.y *= alpha, sum.z *= alpha, sum.w *= alpha;
     };
-    for (int c0 = grp; c0 < e.pieces; c0 += kAhead * kGroups) {
-      if (!(fetched && c0 == grp)) fetch(slot, rr, ch, c0, e.pieces - 1);
+    // pieces c0, c0 + stride, ... of row rr
+    auto gather = [&](int rr, int ch, int c0, int stride) {
+      for (; c0 < e.pieces; c0 += kAhead * stride) {
+        float2 ml[kAhead];
+        float4 v[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const int64_t prow = static_cast<int64_t>(e.slot + min(c0 + k * stride, e.pieces - 1)) * p.rows_cap + rr;
+          ml[k] = p.ml[prow];
+          v[k] = *reinterpret_cast<const float4*>(p.part + prow * DV + ch);
+        }
+        float now = mm;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) now = fmaxf(now, ml[k].x);
+        move(now);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+          if (c0 + k * stride < e.pieces) add(ml[k].x, ml[k].y, v[k], now);
+      }
+    };
+    auto store = [&](int rr, int ch) {
+      const int token = rr / p.tile.heads, head = rr - token * p.tile.heads;
+      if (head >= e.heads) return;
+      const int64_t tok = static_cast<int64_t>(e.row0) + token, h = e.head0 + head;
+      const float inv = ll == 0.f ? 0.f : 1.f / ll;
+      const int64_t at = tok * p.out_srow + h * p.out_shead + ch;
+      if (p.out_bf16)
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
+            make_uint2(pack_bf16x2(sum.x * inv, sum.y * inv), pack_bf16x2(sum.z * inv, sum.w * inv));
+      else
+        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) =
+            make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
+      if (ch == 0 && p.lse != nullptr)
+        p.lse[tok * p.lse_srow + h * p.lse_shead] = ll == 0.f ? -INFINITY : (mm + lg2_approx(ll)) * kLn2;
+    };
+    if (e.pieces <= kAhead) {
+      const int i = chunk * kJoinThreads + threadIdx.x, rr = i / (DV / 4), ch = (i % (DV / 4)) * 4;
+      if (rr < rows) {
+        gather(rr, ch, 0, 1);
+        store(rr, ch);
+      }
+      continue;
+    }
+    for (int c = 0; c < kJoinThreads / 128; ++c) {
+      const int i0 = chunk * kJoinThreads + c * 128, i = i0 + lane;
+      if (i0 / (DV / 4) >= rows) break;  // the same for every thread
+      const int rr = min(i / (DV / 4), rows - 1), ch = (i % (DV / 4)) * 4;
+      mm = -INFINITY, ll = 0.f;
+      sum = make_float4(0.f, 0.f, 0.f, 0.f);
+      gather(rr, ch, grp, kGroups);
+      __syncthreads();
+      s_m[grp][lane] = mm, s_l[grp][lane] = ll, s_v[grp][lane] = sum;
+      __syncthreads();
+      if (grp != 0) continue;
       float now = mm;
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k)
-        if (c0 + k * kGroups < e.pieces) now = fmaxf(now, ml[k].x);
+      for (int g = 1; g < kGroups; ++g) now = fmaxf(now, s_m[g][lane]);
       move(now);
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k)
-        if (c0 + k * kGroups < e.pieces) add(ml[k].x, ml[k].y, v[k], now);
+      for (int g = 1; g < kGroups; ++g) add(s_m[g][lane], s_l[g][lane], s_v[g][lane], now);
+      if (i / (DV / 4) < rows) store(rr, ch);
     }
-    __syncthreads();
-    s_m[grp][lane] = mm, s_l[grp][lane] = ll, s_v[grp][lane] = sum;
-    __syncthreads();
-    if (grp != 0) continue;
-    float now = mm;
-#pragma unroll
-    for (int g = 1; g < kGroups; ++g) now = fmaxf(now, s_m[g][lane]);
-    move(now);
-#pragma unroll
-    for (int g = 1; g < kGroups; ++g) add(s_m[g][lane], s_l[g][lane], s_v[g][lane], now);
-    const int token = rr / p.tile.heads, head = rr - token * p.tile.heads;
-    if (i / (DV / 4) >= rows || head >= e.heads) continue;
-    const int64_t tok = static_cast<int64_t>(e.row0) + token, h = e.head0 + head;
-    const float inv = ll == 0.f ? 0.f : 1.f / ll;
-    const int64_t at = tok * p.out_srow + h * p.out_shead + ch;
-    if (p.out_bf16)
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
-          make_uint2(pack_bf16x2(sum.x * inv, sum.y * inv), pack_bf16x2(sum.z * inv, sum.w * inv));
-    else
-      *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) =
-          make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
-    if (ch == 0 && p.lse != nullptr)
-      p.lse[tok * p.lse_srow + h * p.lse_shead] = ll == 0.f ? -INFINITY : (mm + lg2_approx(ll)) * kLn2;
   }
 }
 
@@ -878,7 +888,7 @@ Workspace workspace_of(int64_t T, int64_t group, int dqk, int dv, int32_t q_len)
   const int64_t most = std::max<int64_t>(1, q_len > 0 ? q_len : T);  // new tokens of a sequence
   Workspace w;
   w.rows_cap = std::min<int64_t>(tiles * tile.tokens, most) * tile.heads;
-  w.max_slots = max_joined<kFine>(grid_of(dqk, dv));
+  w.max_slots = tiles == 1 ? max_joined<Cfg<64, 64, 1>::kFine>(grid_of(dqk, dv)) : max_joined<Cfg<128, 128, 2>::kFine>(grid_of(dqk, dv));
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   w.pairs = 256;
   w.ml = w.pairs + up(w.max_slots * sizeof(KvPair));
@@ -908,9 +918,9 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
   if (p.tile_counter == nullptr) return cudaErrorInvalidDevice;
   kv_attn_kernel<DQK, DV, QT><<<grid, C::kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const int64_t items = p.max_slots * ((p.rows_cap * (DV / 4) + 127) / 128);
+  const int64_t items = p.max_slots / 2 * ((p.rows_cap * (DV / 4) + kJoinThreads - 1) / kJoinThreads);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(items, 4 * kv_sm_count())));
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(items, 2 * kv_sm_count())));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -986,7 +996,7 @@ slope_status slope_kv_attn(const slope_tensor* q, const slope_kv_cache* cache, c
   char* const ws = static_cast<char*>(workspace);
   p.rows_cap = static_cast<int32_t>(w.rows_cap);
   p.max_slots = static_cast<int32_t>(w.max_slots);
-  p.n_slots = reinterpret_cast<int32_t*>(ws);
+  p.n_pairs = reinterpret_cast<int32_t*>(ws);
   p.pairs = reinterpret_cast<KvPair*>(ws + w.pairs);
   p.ml = reinterpret_cast<float2*>(ws + w.ml);
   p.part = reinterpret_cast<float*>(ws + w.part);

@@ -11,7 +11,7 @@
 namespace slope {
 
 constexpr int64_t kKvMaxTokens = int64_t(1) << 28;  // of q's rows, and of a sequence
-constexpr int kKvMaxSeqs = 1024;                    // sequences of a launch
+constexpr int kKvMaxSeqs = 512;                     // sequences of a launch
 
 // Argument checks of a cache, its pointers and strides among them.
 slope_status check_kv_cache(const slope_kv_cache* c);

@@ -28,9 +28,10 @@ struct CutLists {
   KvSeq seqs[kKvMaxSeqs];
   uint32_t units[kKvMaxSeqs];  // pieces before the sequence's
   uint32_t slots[kKvMaxSeqs];  // joined pieces before the sequence's
+  uint32_t joins[kKvMaxSeqs];  // pairs of several pieces before the sequence's
 };
 struct Cut {
-  uint32_t total, slots;  // pieces, and those of pairs with several
+  uint32_t total, joins;  // pieces, and pairs that have several
   int per;
 };
 // Joined pieces of a launch at most: no length of pieces is below 1 / (2 kFine) of a share of the steps (an even division
@@ -120,26 +121,29 @@ __device__ __forceinline__ Cut make_cut(const KvSeqs& p, int heads, const CutOf&
       r.per = per[i];
     }
   }
-  r.total = r.slots = 0;
+  r.total = r.joins = 0;
+  uint32_t slots = 0;
 #pragma unroll 1
   for (int b0 = 0; b0 < B; b0 += 32) {
     const int b = b0 + lane;
-    uint32_t u = 0, sl = 0;
+    uint32_t u = 0, sl = 0, jn = 0;
     if (b < B) {
       const SeqCut c = cut_of(lists.seqs[b]);
       const int n = pieces_of(c.steps, r.per);
       u = static_cast<uint32_t>(heads) * c.blocks * n;
-      sl = n > 1 && c.join ? u : 0;
+      if (n > 1 && c.join) sl = u, jn = static_cast<uint32_t>(heads) * c.blocks;
     }
-    uint32_t iu = u, is = sl;
+    uint32_t iu = u, is = sl, ij = jn;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
       const uint32_t ou = __shfl_up_sync(0xffffffffu, iu, m), os = __shfl_up_sync(0xffffffffu, is, m);
-      if (lane >= m) iu += ou, is += os;
+      const uint32_t oj = __shfl_up_sync(0xffffffffu, ij, m);
+      if (lane >= m) iu += ou, is += os, ij += oj;
     }
-    if (b < B) lists.units[b] = r.total + iu - u, lists.slots[b] = r.slots + is - sl;
+    if (b < B) lists.units[b] = r.total + iu - u, lists.slots[b] = slots + is - sl, lists.joins[b] = r.joins + ij - jn;
     r.total += __shfl_sync(0xffffffffu, iu, 31);
-    r.slots += __shfl_sync(0xffffffffu, is, 31);
+    slots += __shfl_sync(0xffffffffu, is, 31);
+    r.joins += __shfl_sync(0xffffffffu, ij, 31);
   }
   __syncwarp();
   return r;

@@ -47,8 +47,8 @@ struct KvWeightsParams {
   float* weights;
   int64_t w_spage, w_shead;
   int32_t max_slots;
-  int32_t* n_slots;  // workspace: pieces that are joined
-  int4* pairs;       // workspace, for each of them: {sequence, KV head, key block, pieces (0 but in the first)}
+  int32_t* n_pairs;  // workspace: pairs that are joined
+  int4* pairs;       // workspace: {sequence, KV head << 16 | pieces, key block, first piece}
   float* part;       // workspace: their sums
   int* status;
   uint32_t* tile_counter;
@@ -129,7 +129,7 @@ struct KeyCut {
 };
 
 __device__ __forceinline__ Piece make_piece(const KvWeightsParams& p, int per, const CutLists& lists, uint32_t w,
-                                            const KeyCut& cut_of, int& pieces, int& c) {
+                                            const KeyCut& cut_of, int& join, int& pieces) {
   Piece r;
   const int b = seq_of(lists, p.seqs.B, w);
   const KvSeq q = lists.seqs[b];
@@ -139,7 +139,8 @@ __device__ __forceinline__ Piece make_piece(const KvWeightsParams& p, int per, c
   const uint32_t local = w - lists.units[b], rest = cut.blocks == 1 ? local : divide(local, cut.blocks);
   const int blk = static_cast<int>(local - rest * cut.blocks);
   r.kvh = static_cast<int>(pieces == 1 ? rest : divide(rest, pieces));
-  c = static_cast<int>(rest) - r.kvh * pieces;
+  const int c = static_cast<int>(rest) - r.kvh * pieces;
+  join = -1;
   r.b = p.seqs.b0 + b;
   r.few = cut.join ? 0 : 1;
   r.len = q.len;
@@ -162,7 +163,11 @@ __device__ __forceinline__ Piece make_piece(const KvWeightsParams& p, int per, c
   r.blk0 = lo / p.tile.tokens;
   r.count = hi > lo ? (hi + p.tile.tokens - 1) / p.tile.tokens - r.blk0 : 0;
   piece_steps(r.count * p.tile.parts, pieces, c, r.i0, r.i1);
-  if (pieces > 1) r.slot = static_cast<int32_t>(lists.slots[b]) + (r.kvh * cut.blocks + blk) * pieces + c;
+  if (pieces > 1) {
+    const int pair = r.kvh * cut.blocks + blk;
+    r.slot = static_cast<int32_t>(lists.slots[b]) + pair * pieces + c;
+    if (c == 0) join = static_cast<int32_t>(lists.joins[b]) + pair;  // the first piece lists the pair
+  }
   return r;
 }
 
@@ -242,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kTmaWarp) {
     // ================================================================ producer: pieces, pages, loads
     const Cut cut = make_cut<kPieceSteps, kFine>(p.seqs, p.Hkv, cut_of, sh.lists);
-    if (lane == 0 && blockIdx.x == 0) *p.n_slots = static_cast<int32_t>(cut.slots);
+    if (lane == 0 && blockIdx.x == 0) *p.n_pairs = static_cast<int32_t>(cut.joins);
     const uint32_t total = cut.total;
     const uint32_t q_bytes = static_cast<uint32_t>(p.tile.heads * p.tile.tokens) * 128 * C::kChunks;
     const int shift = p.seqs.page_shift;
@@ -264,12 +269,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       uint32_t next = 0;
       if (lane == 0) next = atomicAdd(p.tile_counter, 1u);
-      int pieces, c;
-      const Piece pc = make_piece(p, cut.per, sh.lists, w, cut_of, pieces, c);
+      int join, pieces;
+      const Piece pc = make_piece(p, cut.per, sh.lists, w, cut_of, join, pieces);
       if (lane == 0) {
         sh.piece[k % kPieces] = pc;
         mbar_arrive(&sh.wfull[k % kPieces]);
-        if (pc.slot >= 0) p.pairs[pc.slot] = make_int4(pc.b, pc.kvh, pc.key0 / kKeys, c == 0 ? pieces : 0);
+        if (join >= 0) p.pairs[join] = make_int4(pc.b, pc.kvh << 16 | pieces, pc.key0 / kKeys, pc.slot);
       }
       const int32_t* const row = p.seqs.table + pc.b * p.seqs.table_stride;
       // page of the keys of box `lane` of a key block (two tiles of `boxes` each)
@@ -611,10 +616,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 __global__ void __launch_bounds__(kKeys) kv_weights_join_kernel(const __grid_constant__ KvWeightsParams p) {
   pdl_wait();
   if (*reinterpret_cast<volatile int*>(p.status) != 0) return;  // pieces may be missing
-  const int n_slots = min(*p.n_slots, p.max_slots);
-  for (int slot = blockIdx.x; slot < n_slots; slot += gridDim.x) {
-    const int4 e = p.pairs[slot];
-    if (e.w <= 0 || slot + e.w > n_slots || e.x < p.seqs.b0 || e.x >= p.seqs.b0 + p.seqs.B) continue;
+  const int n_pairs = min(*p.n_pairs, p.max_slots);
+  for (int pair = blockIdx.x; pair < n_pairs; pair += gridDim.x) {
+    const int4 e = p.pairs[pair];
+    const int pieces = e.y & 0xffff, kvh = static_cast<int>(static_cast<uint32_t>(e.y) >> 16);
+    if (e.w < 0 || e.w + pieces > p.max_slots || e.x < p.seqs.b0 || e.x >= p.seqs.b0 + p.seqs.B || kvh >= p.Hkv) continue;
     const int pos = e.z * kKeys + threadIdx.x;
     const KvSeq s = kv_seq(p.seqs, e.x - p.seqs.b0);
     if (pos >= s.len) continue;
@@ -622,8 +628,8 @@ __global__ void __launch_bounds__(kKeys) kv_weights_join_kernel(const __grid_con
     if (pg < 0 || pg >= p.seqs.n_pages) continue;
     float sum = 0.f;
 #pragma unroll 8
-    for (int c = 0; c < e.w; ++c) sum += p.part[static_cast<int64_t>(slot + c) * kKeys + threadIdx.x];
-    float* const dst = p.weights + pg * p.w_spage + e.y * p.w_shead + (pos & ((1 << p.seqs.page_shift) - 1));
+    for (int c = 0; c < pieces; ++c) sum += p.part[static_cast<int64_t>(e.w + c) * kKeys + threadIdx.x];
+    float* const dst = p.weights + pg * p.w_spage + kvh * p.w_shead + (pos & ((1 << p.seqs.page_shift) - 1));
     if (!(p.accumulate && sum == 0.f)) *dst = p.accumulate ? *dst + sum : sum;
   }
 }
@@ -724,7 +730,7 @@ slope_status slope_kv_attn_weights(const slope_tensor* q, const slope_kv_cache* 
   p.w_shead = weights->stride[1];
   char* const ws = static_cast<char*>(workspace);
   p.max_slots = static_cast<int32_t>(w.max_slots);
-  p.n_slots = reinterpret_cast<int32_t*>(ws);
+  p.n_pairs = reinterpret_cast<int32_t*>(ws);
   p.pairs = reinterpret_cast<int4*>(ws + w.pairs);
   p.part = reinterpret_cast<float*>(ws + w.part);
   p.status = device_status_ptr();
