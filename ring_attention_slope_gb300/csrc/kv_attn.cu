@@ -154,6 +154,7 @@ struct Cfg {
   struct Rest {  // behind the tiles
     uint64_t bars[kNumBars];
     Piece piece[2];
+    uint16_t rows[kBlockM];  // of a Q tile: token << 8 | head
     uint32_t holes[kHoles];  // of a step's 16-token runs, those without a page
     uint32_t tmem;
     int abort;
@@ -208,6 +209,8 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
     prefetch_tensormap(&tm_k);
     prefetch_tensormap(&tm_v);
   }
+  if (threadIdx.x < kBlockM)
+    sh.rows[threadIdx.x] = static_cast<uint16_t>(threadIdx.x / p.tile.heads << 8 | threadIdx.x % p.tile.heads);
   if (threadIdx.x == 0) *cta_abort = *reinterpret_cast<volatile int*>(p.status) != 0 ? 1 : 0;
   if (warp == C::kMmaWarp) {
     tmem_alloc(&sh.tmem, C::kTmemCols);
@@ -579,6 +582,40 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
         reg_fence(q1);
         reg_fence(q2);
         reg_fence(q3);
+        float qm[4] = {q0, q1, q2, q3};
+        if (!inside || holes != 0) {
+          // The row's visible columns are one interval, less the missing pages.  A quarter of 32 columns that every row
+          // of the warp sees keeps its maximum and its scores.
+          const int kpos = j * kBlockN;
+          const int q_pos = pc.pos0 + t * p.tile.tokens + (sh.rows[row] >> 8);
+          const int lo = p.window > 0 ? q_pos - kpos - p.window + 1 : 0;
+          const int hi = min(pc.len - kpos - 1, q_pos - kpos);
+          auto mask = [&](uint32_t(&r)[32], float& most, int first) {
+            const int a = lo - first, b = hi - first;
+            const uint32_t gone = (holes >> (first / 16)) & 3u;
+            if (!__any_sync(0xffffffffu, a > 0 || b < 31 || gone != 0)) return;
+            // (a branch of its own for a quarter that nobody sees made ptxas spill 1.7 KB)
+            // visible: a <= c <= b
+            const int from = max(a, 0);
+            const uint32_t span = static_cast<uint32_t>(max(-1, min(b, 31) - from) + 1);  // columns
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (static_cast<uint32_t>(c - from) >= span || ((gone >> (c / 16)) & 1u)) r[c] = 0xff800000u;  // -inf
+            float x = fmax3(__uint_as_float(r[0]), __uint_as_float(r[1]), __uint_as_float(r[2]));
+            float y = fmax3(__uint_as_float(r[3]), __uint_as_float(r[4]), __uint_as_float(r[5]));
+#pragma unroll
+            for (int c = 6; c < 30; c += 4) {
+              x = fmax3(x, __uint_as_float(r[c]), __uint_as_float(r[c + 1]));
+              y = fmax3(y, __uint_as_float(r[c + 2]), __uint_as_float(r[c + 3]));
+            }
+            most = fmax3(x, y, fmaxf(__uint_as_float(r[30]), __uint_as_float(r[31])));
+          };
+          mask(r0, qm[0], 0);
+          mask(r1, qm[1], 32);
+          mask(r2, qm[2], 64);
+          mask(r3, qm[3], 96);
+        }
+        const float mx = fmax3(qm[0], qm[1], fmaxf(qm[2], qm[3]));
         float sv[128];
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
@@ -586,45 +623,6 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
           sv[32 + i] = __uint_as_float(r1[i]);
           sv[64 + i] = __uint_as_float(r2[i]);
           sv[96 + i] = __uint_as_float(r3[i]);
-        }
-        float mx = fmax3(q0, q1, fmaxf(q2, q3));
-        if (!inside || holes != 0) {
-          // the row's visible columns are one interval, less the missing pages
-          const int kpos = j * kBlockN;
-          const int q_pos = pc.pos0 + t * p.tile.tokens + row / p.tile.heads;
-          int lo = p.window > 0 ? max(0, q_pos - kpos - p.window + 1) : 0;
-          int hi = min(pc.len - kpos - 1, q_pos - kpos);
-          if (hi < lo) lo = hi = kBlockN;  // none: every c - lo is negative
-          const uint32_t span = static_cast<uint32_t>(hi - lo);
-#pragma unroll
-          for (int c = 0; c < kBlockN; ++c)
-            if (static_cast<uint32_t>(c - lo) > span) sv[c] = -INFINITY;
-          if (holes != 0) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if ((holes >> i) & 1u)
-#pragma unroll
-                for (int c = 0; c < 16; ++c) sv[16 * i + c] = -INFINITY;
-          }
-          float qm[4] = {q0, q1, q2, q3};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const bool all_vis = lo <= 32 * i && 32 * i + 31 <= hi && ((holes >> (2 * i)) & 3u) == 0;
-            const bool none_vis = hi < 32 * i || lo > 32 * i + 31;
-            if (__any_sync(0xffffffffu, !all_vis && !none_vis)) {
-              float a = fmax3(sv[32 * i], sv[32 * i + 1], sv[32 * i + 2]);
-              float b = fmax3(sv[32 * i + 3], sv[32 * i + 4], sv[32 * i + 5]);
-#pragma unroll
-              for (int c = 6; c < 30; c += 4) {
-                a = fmax3(a, sv[32 * i + c], sv[32 * i + c + 1]);
-                b = fmax3(b, sv[32 * i + c + 2], sv[32 * i + c + 3]);
-              }
-              qm[i] = fmax3(a, b, fmaxf(sv[32 * i + 30], sv[32 * i + 31]));
-            } else {
-              qm[i] = all_vis ? qm[i] : -INFINITY;
-            }
-          }
-          mx = fmax3(qm[0], qm[1], fmaxf(qm[2], qm[3]));
         }
         const float m_new = mx * sl2;
         const bool need = m_new > m_used + kRescaleThreshold;
@@ -701,7 +699,7 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
       // ---- epilogue
       const bool steps = pc.j1 > pc.j0;
       const int slot = pc.slot, head0 = pc.head0;
-      const int my_token = row / p.tile.heads, my_head = row - my_token * p.tile.heads;
+      const int my_token = sh.rows[row] >> 8, my_head = sh.rows[row] & 255;
       const bool valid_row = my_token < min(pc.tokens - t * p.tile.tokens, p.tile.tokens) && my_head < pc.heads;
       const int64_t tok = static_cast<int64_t>(pc.row0) + t * p.tile.tokens + my_token;
       arrive(&bar_wfree[k & 1]);
@@ -710,7 +708,10 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
         if (!ok) break;
         tc_fence_after_sync();
       }
-      const float inv = slot < 0 ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+      // (a row that saw nothing gives 0 whatever O holds, and a sum that is NaN gives NaN)
+      const float inv = slot >= 0 || l == 0.f ? 1.f : 1.f / l;
+      const uint32_t keep = l == 0.f ? 0u : ~0u;
+      const uint64_t inv2 = pack_f32x2(inv, inv);
       const int64_t at = tok * p.out_srow + static_cast<int64_t>(head0 + my_head) * p.out_shead;
       const int64_t prow = static_cast<int64_t>(slot) * p.rows_cap + t * p.tile.tokens * p.tile.heads + row;
       if (valid_row) {
@@ -720,7 +721,6 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
           p.lse[tok * p.lse_srow + static_cast<int64_t>(head0 + my_head) * p.lse_shead] =
               l > 0.f ? (m_used + lg2_approx(l)) * kLn2 : l == 0.f ? -INFINITY : l;
       }
-      const bool nan_row = !(l >= 0.f);  // its output is NaN
 #pragma unroll 1
       for (int c = 0; c < DV / 32; ++c) {
         // (not left undefined: the compiler kept room for it through the steps, and spilled 160 bytes there)
@@ -735,10 +735,13 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
           arrive(&bar_ofree[t]);
         }
         if (!valid_row) continue;
-        const bool none = !steps || l == 0.f;
         float f[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) f[i] = none ? 0.f : nan_row ? l : __uint_as_float(o[i]) * inv;
+        for (int i = 0; i < 16; ++i) {
+          const float2 x = unpack_f32x2(mul_f32x2(
+              pack_f32x2(__uint_as_float(o[2 * i] & keep), __uint_as_float(o[2 * i + 1] & keep)), inv2));
+          f[2 * i] = x.x, f[2 * i + 1] = x.y;
+        }
         if (slot >= 0) {
           float4* const dst = reinterpret_cast<float4*>(p.part + prow * DV + c * 32);
 #pragma unroll
