@@ -256,11 +256,35 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
     const int boxes_log = max(0, 7 - p.seqs.page_shift);  // log2 of the boxes of 64 channels of a key tile
     const int boxes = 1 << boxes_log, box_rows = kBlockN >> boxes_log;
     const int no_page = static_cast<int>(p.seqs.n_pages);  // reads 0
+    const int shift = p.seqs.page_shift;
     uint32_t w = __shfl_sync(0xffffffffu, claimed, 0);
     uint32_t cnt = 0;   // K and V tiles loaded
     uint32_t step = 0;  // steps loaded
     int wt = 0;         // Q tiles loaded
     bool ok = *cta_abort == 0;
+    // Entry e of the piece's block table: no_page where no row sees a key, -1 for a page out of range where one does.
+    auto page_of = [&](const Piece& pc, int e) -> int {
+      const int64_t first = static_cast<int64_t>(e) << shift;
+      const int lo = p.window > 0 ? pc.pos0 - p.window + 1 : 0;  // positions [lo, hi) that some row sees
+      const int hi = min(pc.len, pc.pos0 + pc.tokens);
+      if (first >= hi || first + (int64_t(1) << shift) <= lo) return no_page;
+      const int pg = p.seqs.table[pc.b * p.seqs.table_stride + e];
+      return pg >= 0 && pg < no_page ? pg : -1;
+    };
+    // A piece, and its first 64 pages: entry e0 + lane of the table in each lane, and the 32 after them on their way.  The next
+    // one is made out while the first loads of this one are under way.
+    struct Work {
+      Piece pc;
+      int join, pieces, e0, page, ahead;
+    };
+    auto prepare = [&](Work& q) {
+      q.pc = make_piece(p, cut.per, sh.lists, w, cut_of, q.join, q.pieces);
+      q.e0 = (q.pc.j0 * kBlockN) >> shift;
+      q.page = q.pc.j1 > q.pc.j0 ? page_of(q.pc, q.e0 + lane) : no_page;
+      q.ahead = q.pc.j1 > q.pc.j0 ? page_of(q.pc, q.e0 + 32 + lane) : no_page;
+    };
+    Work now{}, then{};
+    if (ok && w < total) prepare(now);
     for (int k = 0; ok; ++k) {
       if (k >= 2) ok = warp_all(wait_bounded(&bar_wfree[k & 1], ((k >> 1) - 1) & 1, cta_abort, p.status, limit, 32));
       if (!ok) break;
@@ -273,76 +297,74 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
       }
       uint32_t next = 0;
       if (lane == 0) next = atomicAdd(p.tile_counter, 1u);  // on its way while this piece loads
-      int join, pieces;
-      const Piece pc = make_piece(p, cut.per, sh.lists, w, cut_of, join, pieces);
+      const Piece& pc = now.pc;
       if (lane == 0) {
         sh.piece[k & 1] = pc;
         mbar_arrive(&bar_wfull[k & 1]);
-        if (join >= 0) p.pairs[join] = KvPair{pc.row0, pc.tokens, pc.head0, pc.heads, pc.slot, pieces, {0, 0}};
+        if (now.join >= 0) p.pairs[now.join] = KvPair{pc.row0, pc.tokens, pc.head0, pc.heads, pc.slot, now.pieces, {0, 0}};
       }
-      if (pc.j1 > pc.j0) {
-        // ---- pages: entry e0 + lane of the table in each lane, and the 32 after them on their way
-        const int lo = p.window > 0 ? max(0, pc.pos0 - p.window + 1) : 0;  // positions [lo, hi) that some row sees
-        const int hi = min(pc.len, pc.pos0 + pc.tokens);
-        const int32_t* const row = p.seqs.table + pc.b * p.seqs.table_stride;
-        const int shift = p.seqs.page_shift;
-        auto page_of = [&](int e) -> int {  // -1: a page out of range where one is needed
-          const int64_t first = static_cast<int64_t>(e) << shift;
-          if (first >= hi || first + (int64_t(1) << shift) <= lo) return no_page;
-          const int pg = row[e];
-          return pg >= 0 && pg < no_page ? pg : -1;
-        };
-        int e0 = (pc.j0 * kBlockN) >> shift;
-        int page = page_of(e0 + lane), ahead = page_of(e0 + 32 + lane);
-
-        const int nt = QT == 2 && pc.tokens > p.tile.tokens ? 2 : 1;
+      auto load_rows = [&]() -> bool {
         // Q of the previous piece is in use until its last S MMAs are done
-        if (wt > 0) ok = warp_all(wait_bounded(bar_qempty, (wt - 1) & 1, cta_abort, p.status, limit, 33));
-        if (ok) {
-          if (lane == 0) {
-            mbar_arrive_expect_tx(bar_q, nt * q_bytes);
-            for (int t = 0; t < nt; ++t)
-              for (int ch = 0; ch < C::kQChunks; ++ch)
-                tma_load_3d(sQ + t * C::kQTileBytes + ch * kChunkBytes, &tm_q, bar_q, 64 * ch, pc.head0,
-                            pc.row0 + t * p.tile.tokens);
-          }
-          ++wt;
+        if (wt > 0 && !warp_all(wait_bounded(bar_qempty, (wt - 1) & 1, cta_abort, p.status, limit, 33))) return false;
+        if (lane == 0) {
+          const int nt = QT == 2 && pc.tokens > p.tile.tokens ? 2 : 1;
+          mbar_arrive_expect_tx(bar_q, nt * q_bytes);
+          for (int t = 0; t < nt; ++t)
+            for (int ch = 0; ch < C::kQChunks; ++ch)
+              tma_load_3d(sQ + t * C::kQTileBytes + ch * kChunkBytes, &tm_q, bar_q, 64 * ch, pc.head0,
+                          pc.row0 + t * p.tile.tokens);
         }
-        for (int j = pc.j0; ok && j < pc.j1; ++j, ++step) {
-          const int e = (j * kBlockN) >> shift;
-          if (e >= e0 + 32) {
-            e0 += 32;
-            page = ahead;
-            ahead = page_of(e0 + 32 + lane);
-          }
-          // lane i loads box i % boxes of channel chunk i / boxes
-          const int mine = __shfl_sync(0xffffffffu, page, (e - e0) + (lane & (boxes - 1)));
-          const uint32_t missing = __ballot_sync(0xffffffffu, mine < 0) & ((1u << boxes) - 1);
-          const int pg = mine < 0 ? no_page : mine;
-          const int in_page = boxes_log > 0 ? 0 : (j * kBlockN) & ((1 << shift) - 1);
-          const int chunk = lane >> boxes_log;
-          const uint32_t at = static_cast<uint32_t>(chunk) * kChunkBytes + (lane & (boxes - 1)) * box_rows * 128;
-          for (int kv = 0; kv < 2 && ok; ++kv) {
-            const uint32_t slot = cnt % C::kSlots, ph = (cnt / C::kSlots) & 1;
-            ok = warp_all(wait_bounded(&bar_empty[slot], ph ^ 1, cta_abort, p.status, limit, 34 + kv));
-            if (!ok) break;
-            if (lane == 0) {
-              if (kv == 0) {  // bit i: positions 16 i .. 16 i + 15 of the tile have no page
-                uint32_t m = 0;
-                for (int i = 0; missing != 0 && i < 8; ++i) m |= ((missing >> ((i << boxes_log) >> 3)) & 1u) << i;
-                sh.holes[step % kHoles] = m;
-              }
-              mbar_arrive_expect_tx(&bar_full[slot], kv == 0 ? C::kKTileBytes : C::kVTileBytes);
+        ++wt;
+        return true;
+      };
+      const bool rows_first = wt == 0;
+      if (rows_first && pc.j1 > pc.j0) ok = load_rows();
+      bool prepared = false;
+      for (int j = pc.j0; ok && j < pc.j1; ++j, ++step) {
+        const int e = (j * kBlockN) >> shift;
+        if (e >= now.e0 + 32) {
+          now.e0 += 32;
+          now.page = now.ahead;
+          now.ahead = page_of(pc, now.e0 + 32 + lane);
+        }
+        // lane i loads box i % boxes of channel chunk i / boxes
+        const int mine = __shfl_sync(0xffffffffu, now.page, (e - now.e0) + (lane & (boxes - 1)));
+        const uint32_t missing = __ballot_sync(0xffffffffu, mine < 0) & ((1u << boxes) - 1);
+        const int pg = mine < 0 ? no_page : mine;
+        const int in_page = boxes_log > 0 ? 0 : (j * kBlockN) & ((1 << shift) - 1);
+        const int chunk = lane >> boxes_log;
+        const uint32_t at = static_cast<uint32_t>(chunk) * kChunkBytes + (lane & (boxes - 1)) * box_rows * 128;
+        for (int kv = 0; kv < 2 && ok; ++kv) {
+          const uint32_t slot = cnt % C::kSlots, ph = (cnt / C::kSlots) & 1;
+          ok = warp_all(wait_bounded(&bar_empty[slot], ph ^ 1, cta_abort, p.status, limit, 34 + kv));
+          if (!ok) break;
+          if (lane == 0) {
+            if (kv == 0) {  // bit i: positions 16 i .. 16 i + 15 of the tile have no page
+              uint32_t m = 0;
+              for (int i = 0; missing != 0 && i < 8; ++i) m |= ((missing >> ((i << boxes_log) >> 3)) & 1u) << i;
+              sh.holes[step % kHoles] = m;
             }
-            __syncwarp();
-            if (chunk < (kv == 0 ? C::kQChunks : C::kVChunks))
-              tma_load_4d(sSlot + slot * C::kSlotBytes + at, kv == 0 ? &tm_k : &tm_v, &bar_full[slot], 64 * chunk, in_page,
-                          pc.kvh, pg);
-            ++cnt;
+            mbar_arrive_expect_tx(&bar_full[slot], kv == 0 ? C::kKTileBytes : C::kVTileBytes);
           }
+          __syncwarp();
+          if (chunk < (kv == 0 ? C::kQChunks : C::kVChunks))
+            tma_load_4d(sSlot + slot * C::kSlotBytes + at, kv == 0 ? &tm_k : &tm_v, &bar_full[slot], 64 * chunk, in_page,
+                        pc.kvh, pg);
+          ++cnt;
+        }
+        // the first keys need not wait for the previous piece's rows to be done with
+        if (ok && !rows_first && j == pc.j0) ok = load_rows();
+        if (ok && j == pc.j0 + 1) {
+          w = __shfl_sync(0xffffffffu, next, 0);
+          prepared = true;
+          if (w < total) prepare(then);
         }
       }
-      w = __shfl_sync(0xffffffffu, next, 0);
+      if (!prepared) {
+        w = __shfl_sync(0xffffffffu, next, 0);
+        if (ok && w < total) prepare(then);
+      }
+      now = then;
     }
     if (lane == 0) {
       release_pieces(p.tile_counter, total, w);
