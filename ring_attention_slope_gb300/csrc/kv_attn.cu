@@ -202,16 +202,13 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
   const uint64_t limit = p.wait_limit_ns;
 
   pdl_launch_dependents();  // the join may be scheduled as this grid's CTAs leave
-  uint32_t claimed = 0;     // the producer's first claim, on its way during the cut
   if (threadIdx.x == C::kTmaWarp * 32) {
-    claimed = atomicAdd(p.tile_counter, 1u);
     prefetch_tensormap(&tm_q);
     prefetch_tensormap(&tm_k);
     prefetch_tensormap(&tm_v);
   }
   if (threadIdx.x < kBlockM)
     sh.rows[threadIdx.x] = static_cast<uint16_t>(threadIdx.x / p.tile.heads << 8 | threadIdx.x % p.tile.heads);
-  if (threadIdx.x == 0) *cta_abort = *reinterpret_cast<volatile int*>(p.status) != 0 ? 1 : 0;
   if (warp == C::kMmaWarp) {
     tmem_alloc(&sh.tmem, C::kTmemCols);
     tmem_relinquish();
@@ -239,6 +236,10 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
     }
     fence_barrier_init();
   }
+  pdl_wait();               // the kernels before this one are done; nothing above touches memory
+  uint32_t claimed = 0;     // the producer's first claim, on its way during the cut
+  if (threadIdx.x == C::kTmaWarp * 32) claimed = atomicAdd(p.tile_counter, 1u);
+  if (threadIdx.x == 0) *cta_abort = *reinterpret_cast<volatile int*>(p.status) != 0 ? 1 : 0;
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -941,19 +942,12 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
   }
   p.tile_counter = claim_tile_counter();
   if (p.tile_counter == nullptr) return cudaErrorInvalidDevice;
-  kv_attn_kernel<DQK, DV, QT><<<grid, C::kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  e = launch_early(kv_attn_kernel<DQK, DV, QT>, dim3(static_cast<unsigned>(grid)), C::kThreads, C::kSmemBytes, stream, tq, tk,
+                   tv, p);
+  if (e != cudaSuccess) return e;
   const int64_t items = p.max_slots / 2 * ((p.rows_cap * (DV / 4) + kJoinThreads - 1) / kJoinThreads);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(items, 2 * kv_sm_count())));
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_attn_join_kernel<DV>, p);
+  const int64_t ctas = std::min<int64_t>(items, 2 * kv_sm_count());
+  return launch_early(kv_attn_join_kernel<DV>, dim3(static_cast<unsigned>(ctas)), kJoinThreads, 0, stream, p);
 }
 
 cudaError_t launch_kv_attn(int dqk, int dv, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,

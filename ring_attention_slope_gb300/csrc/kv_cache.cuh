@@ -4,6 +4,8 @@
 
 #include <cuda.h>
 
+#include <utility>
+
 #include "host.cuh"
 #include "kernels.cuh"
 #include "slope_kv.h"
@@ -55,6 +57,23 @@ struct KvSeq {
 };
 
 #ifdef __CUDACC__
+// Launches a kernel that begins with what needs no memory and then waits for the kernel before it (pdl_wait): its start
+// runs under that one's end.
+template <typename... Args, typename... Given>
+cudaError_t launch_early(void (*kernel)(Args...), dim3 grid, int threads, size_t bytes, cudaStream_t stream, Given&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Given>(args)...);
+}
+
 __device__ __forceinline__ KvSeq kv_seq(const KvSeqs& s, int b) {
   KvSeq r;
   const int at = s.b0 + b;

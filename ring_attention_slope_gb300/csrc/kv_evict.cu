@@ -95,7 +95,8 @@ __global__ void __launch_bounds__(kSelectThreads, 2) kv_select_kernel(const __gr
   __shared__ uint32_t s_bin[3];             // the bin with the wanted rank, the rank within it, and the keys in it
   __shared__ uint32_t s_slice[kMaxCluster];  // keys in each CTA's slice of the bins
   __shared__ uint2 s_scan[kSelectThreads / 32], s_count;
-  pdl_launch_dependents();
+  pdl_wait();
+  pdl_launch_dependents();  // (not before: the move reads the lengths ahead of its own wait)
   const int ranks = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   const int pair = blockIdx.x / ranks, b = pair / p.Hkv, h = pair - b * p.Hkv;
   const KvSeq seq = kv_seq(p.seqs, b);
@@ -427,13 +428,15 @@ cudaError_t launch_evict(const KvEvictParams& p, int64_t B, int dqk, int dv, cud
   cfg.blockDim = dim3(kSelectThreads);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(ranks);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   if ((e = cudaLaunchKernelEx(&cfg, kv_select_kernel, s)) != cudaSuccess) return e;
   if (dqk == 64 && dv == 64) return launch_move<64, 64>(p, B, stream);
   if (dqk == 64 && dv == 128) return launch_move<64, 128>(p, B, stream);

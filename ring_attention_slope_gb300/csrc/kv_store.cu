@@ -43,6 +43,7 @@ __device__ __forceinline__ uint4 load8(const X* x) {
 
 template <typename X>
 __global__ void __launch_bounds__(256) kv_write_kernel(const __grid_constant__ KvWriteParams p) {
+  pdl_wait();
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTokens;
   const int word = blockIdx.y * blockDim.x + threadIdx.x;
   int64_t slot[kTokens];
@@ -80,8 +81,7 @@ cudaError_t launch_write(const KvWriteParams& p, cudaStream_t stream) {
   const int64_t words = static_cast<int64_t>(p.Hkv) * (p.k_words + p.v_words);
   const int threads = static_cast<int>(std::min<int64_t>(256, (words + 31) / 32 * 32));
   const dim3 grid(static_cast<unsigned>((p.T + kTokens - 1) / kTokens), static_cast<unsigned>((words + threads - 1) / threads));
-  kv_write_kernel<X><<<grid, threads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_early(kv_write_kernel<X>, grid, threads, 0, stream, p);
 }
 
 bool strides_ok(const int64_t* s) {

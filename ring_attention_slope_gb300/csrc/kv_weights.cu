@@ -202,13 +202,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const KeyCut cut_of{p.tile, p.accumulate != 0};
 
   pdl_launch_dependents();
-  uint32_t claimed = 0;
   if (threadIdx.x == kTmaWarp * 32) {
-    claimed = atomicAdd(p.tile_counter, 1u);
     prefetch_tensormap(&tm_q);
     prefetch_tensormap(&tm_k);
   }
-  if (threadIdx.x == 0) *cta_abort = *reinterpret_cast<volatile int*>(p.status) != 0 ? 1 : 0;
   if (warp == kMmaWarp) {
     tmem_alloc(&sh.tmem, 512);
     tmem_relinquish();
@@ -231,6 +228,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int i = threadIdx.x; i < C::kQSlots * C::kChunks * 128 * 8; i += kThreads)
     if (((i >> 3) & 127) >= p.tile.heads * p.tile.tokens) reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_shared();
+  pdl_wait();  // the kernels before this one are done; nothing above touches memory
+  uint32_t claimed = 0;
+  if (threadIdx.x == kTmaWarp * 32) claimed = atomicAdd(p.tile_counter, 1u);
+  if (threadIdx.x == 0) *cta_abort = *reinterpret_cast<volatile int*>(p.status) != 0 ? 1 : 0;
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -667,18 +668,9 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, KvWeightsParams
   p.tile_counter = claim_tile_counter();
   if (p.tile_counter == nullptr) return cudaErrorInvalidDevice;
   const int sms = kv_sm_count();
-  kv_weights_kernel<DQK><<<sms, kThreads, C::kSmemBytes, stream>>>(tq, tk, p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * sms));
-  cfg.blockDim = dim3(kKeys);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_weights_join_kernel, p);
+  e = launch_early(kv_weights_kernel<DQK>, dim3(static_cast<unsigned>(sms)), kThreads, C::kSmemBytes, stream, tq, tk, p);
+  if (e != cudaSuccess) return e;
+  return launch_early(kv_weights_join_kernel, dim3(static_cast<unsigned>(2 * sms)), kKeys, 0, stream, p);
 }
 
 }  // namespace
