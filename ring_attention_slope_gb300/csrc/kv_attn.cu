@@ -139,18 +139,24 @@ template <int DQK, int DV, int QT>
 struct Cfg {
   static constexpr int kTmaWarp = 4 * QT, kMmaWarp = kTmaWarp + 1;
   static constexpr int kThreads = 32 * (5 * QT + 1);
-  static constexpr int kCtas = QT == 2 ? 1 : 2;  // on an SM
+  static constexpr int kCtas = QT == 1 && DQK == 64 && DV == 64 ? 2 : 1;  // on an SM
   static constexpr int kFine = kCtas;            // (kv_cut.cuh; a piece of two Q tiles leaves 132 KB, so they are longer)
-  static constexpr uint32_t kTmemCols = QT == 2 ? 512 : 256;
+  static constexpr uint32_t kTmemCols = 512 / kCtas;
   static constexpr int kQChunks = DQK / 64, kVChunks = DV / 64;
   static constexpr int kQTileBytes = kQChunks * kChunkBytes;
   static constexpr int kKTileBytes = kQTileBytes, kVTileBytes = kVChunks * kChunkBytes;
-  static constexpr int kSlotBytes = kKTileBytes > kVTileBytes ? kKTileBytes : kVTileBytes;
-  static constexpr int kSlots = (QT == 2 ? 131072 : 65536) / kSlotBytes;
-  static_assert(kSlots % 2 == 0 && kSlots / 2 + 2 <= kHoles, "K tiles in even slots, V tiles in odd ones");
+  // Steps whose K and V tiles fit: with one Q tile and wide heads (decode steps) two or more, so that the copies keep an
+  // SM's share of HBM busy.
+  static constexpr int kRoom = (kCtas == 2 ? 115712 : 232448) - 16384 - QT * kQTileBytes;
+  static constexpr int kStages = kRoom / (kKTileBytes + kVTileBytes) < 4 ? kRoom / (kKTileBytes + kVTileBytes) : 4;
+  static constexpr int kSlots = 2 * kStages;  // K tiles in even ones, V tiles in odd ones
+  static_assert(kStages >= 1 && kStages + 2 <= kHoles, "the holes' ring");
   static constexpr int kNumBars = 2 + 2 * kSlots + 7 * QT + 4 * QT + 4;
   static constexpr int kSlotOffset = QT * kQTileBytes;
-  static constexpr int kRestOffset = kSlotOffset + kSlots * kSlotBytes;
+  static constexpr int kRestOffset = kSlotOffset + kStages * (kKTileBytes + kVTileBytes);
+  __device__ static constexpr int slot_offset(uint32_t slot) {  // from kSlotOffset
+    return static_cast<int>(slot / 2) * (kKTileBytes + kVTileBytes) + (slot % 2 ? kKTileBytes : 0);
+  }
   struct Rest {  // behind the tiles
     uint64_t bars[kNumBars];
     Piece piece[2];
@@ -166,7 +172,7 @@ struct Cfg {
   __device__ static constexpr uint32_t col_p(int t) { return kSepP ? kColP + t * (kBlockN / 2) : t * kBlockN; }
   // Where P overwrites S (dv = 128) the two softmax warps of an SM sub-partition take turns on their exponentials.
   static constexpr bool kTurns = QT == 2 && !kSepP;
-  static_assert(kSmemBytes <= (QT == 2 ? 232448 : 115712), "shared memory budget");
+  static_assert(kSmemBytes <= (kCtas == 1 ? 232448 : 115712), "shared memory budget");
   static_assert(kColO + QT * DV <= kTmemCols, "TMEM budget");
 };
 
@@ -349,7 +355,7 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
           }
           __syncwarp();
           if (chunk < (kv == 0 ? C::kQChunks : C::kVChunks))
-            tma_load_4d(sSlot + slot * C::kSlotBytes + at, kv == 0 ? &tm_k : &tm_v, &bar_full[slot], 64 * chunk, in_page,
+            tma_load_4d(sSlot + C::slot_offset(slot) + at, kv == 0 ? &tm_k : &tm_v, &bar_full[slot], 64 * chunk, in_page,
                         pc.kvh, pg);
           ++cnt;
         }
@@ -398,7 +404,7 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
       uint32_t pend_vslot = 0, pend_vph = 0;
 
       auto issue_qk = [&](uint32_t kslot) {
-        const uint32_t klo = smem_desc_lo(smem_u32(sSlot + kslot * C::kSlotBytes), 16);
+        const uint32_t klo = smem_desc_lo(smem_u32(sSlot + C::slot_offset(kslot)), 16);
 #pragma unroll
         for (int kk = 0; kk < DQK / 16; ++kk) {
           const uint32_t off = ((kk >> 2) * kChunkBytes + (kk & 3) * 32) >> 4;
@@ -415,7 +421,7 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
           }
           ++pvw;
         }
-        const uint32_t vlo = smem_desc_lo(smem_u32(sSlot + vslot * C::kSlotBytes), kChunkBytes);
+        const uint32_t vlo = smem_desc_lo(smem_u32(sSlot + C::slot_offset(vslot)), kChunkBytes);
 #pragma unroll
         for (int kk = 0; kk < kBlockN / 16; ++kk) {
           if (!C::kSepP && kk == 6) {  // the last quarter of P may still have been on its way
@@ -568,7 +574,7 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
           const uint32_t vcnt = 2 * static_cast<uint32_t>(n + skipped) + 1, vslot = vcnt % C::kSlots;
           ok = warp_all(wait_bounded(&bar_full[vslot], (vcnt / C::kSlots) & 1, cta_abort, p.status, limit, 46));
           if (!ok) break;
-          uint8_t* const sv0 = sSlot + vslot * C::kSlotBytes;
+          uint8_t* const sv0 = sSlot + C::slot_offset(vslot);
           for (int c = 0; c < C::kVChunks; ++c)
             for (int off = (pc.len - j * kBlockN) * 128 + row * 16; off < static_cast<int>(kChunkBytes); off += 128 * 16)
               *reinterpret_cast<uint4*>(sv0 + c * kChunkBytes + off) = make_uint4(0u, 0u, 0u, 0u);
@@ -950,9 +956,19 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
   return launch_early(kv_attn_join_kernel<DV>, dim3(static_cast<unsigned>(ctas)), kJoinThreads, 0, stream, p);
 }
 
-cudaError_t launch_kv_attn(int dqk, int dv, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+// `few`: the sequences have no more new tokens than a Q tile, on average.  Then wide heads too take one Q tile to a CTA,
+// and the room of the second one for keys and values (4 sequences of 8192 tokens, 32 heads of 192/128 with a query head
+// each, one new token: 159 -> 132 us; 8 of 16384, 32/8 heads of 128: 113 -> 95 us).
+cudaError_t launch_kv_attn(int dqk, int dv, bool few, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                            const KvAttnParams& p, int grid, cudaStream_t stream) {
   if (dqk == 64 && dv == 64) return launch<64, 64, 1>(tq, tk, tv, p, grid, stream);
+  if (few) {
+    if (dqk == 64 && dv == 128) return launch<64, 128, 1>(tq, tk, tv, p, grid, stream);
+    if (dqk == 128 && dv == 64) return launch<128, 64, 1>(tq, tk, tv, p, grid, stream);
+    if (dqk == 128 && dv == 128) return launch<128, 128, 1>(tq, tk, tv, p, grid, stream);
+    if (dqk == 192 && dv == 64) return launch<192, 64, 1>(tq, tk, tv, p, grid, stream);
+    if (dqk == 192 && dv == 128) return launch<192, 128, 1>(tq, tk, tv, p, grid, stream);
+  }
   if (dqk == 64 && dv == 128) return launch<64, 128, 2>(tq, tk, tv, p, grid, stream);
   if (dqk == 128 && dv == 64) return launch<128, 64, 2>(tq, tk, tv, p, grid, stream);
   if (dqk == 128 && dv == 128) return launch<128, 128, 2>(tq, tk, tv, p, grid, stream);
@@ -997,6 +1013,7 @@ slope_status slope_kv_attn(const slope_tensor* q, const slope_kv_cache* cache, c
   const int64_t pairs = (T / p.tile.tokens + kKvMaxSeqs) * p.Hkv * p.tile.parts;
   if (pairs >= (int64_t(1) << 29)) return SLOPE_ERR_UNSUPPORTED;
   const int grid = grid_of(cache->dqk, cache->dv);
+  const bool few = T <= batch->B * p.tile.tokens;
   if (grid <= 0) return cuda_fail("device attributes");
   const Workspace w = workspace_of(T, p.group, cache->dqk, cache->dv, batch->cu_q != nullptr ? 0 : batch->q_len);
   if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < w.total) return SLOPE_ERR_WORKSPACE;
@@ -1029,7 +1046,8 @@ slope_status slope_kv_attn(const slope_tensor* q, const slope_kv_cache* cache, c
   for (int64_t b = 0; b < batch->B; b += kKvMaxSeqs) {
     p.seqs.b0 = static_cast<int32_t>(b);
     p.seqs.B = static_cast<int32_t>(std::min<int64_t>(kKvMaxSeqs, batch->B - b));
-    const cudaError_t e = launch_kv_attn(cache->dqk, cache->dv, tq, tk, tv, p, grid, static_cast<cudaStream_t>(stream));
+    const cudaError_t e =
+        launch_kv_attn(cache->dqk, cache->dv, few, tq, tk, tv, p, grid, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail("cache attention kernel launch", e);
   }
   return SLOPE_OK;
