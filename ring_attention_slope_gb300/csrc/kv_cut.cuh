@@ -50,7 +50,7 @@ __device__ __forceinline__ float warp_sum(float v) {
 // One whole warp calls it: reads the sequences, chooses the pieces' length and fills the lists.  cut_of(seq) gives a
 // sequence's SeqCut; kPieceSteps is what a piece's start and end cost, in steps.
 //
-// The longest pair is cut into as many pieces as give every CTA one, or into pieces of about 1 / (2 kFine) to 3 / kFine of
+// The longest pair is cut so that no CTA has more than one piece, or into pieces of about 1 / (2 kFine) to 3 / kFine of
 // a share, and the length of those is tried as every pair's.  The length with the least time wins: that of the rounds over
 // the grid where the pieces are all alike, else that of one piece or of an even share of all of them, whichever is
 // more, and half a piece for the uneven end.  (8 sequences of 102400 tokens with 64/8 heads: 640 pieces of 80 steps for 304
@@ -75,10 +75,13 @@ __device__ __forceinline__ Cut make_cut(const KvSeqs& p, int heads, const CutOf&
   }
   __syncwarp();
   most = __reduce_max_sync(0xffffffffu, most);
-  const float share = fmaxf(1.f, warp_sum(all) * per_cta), longest = static_cast<float>(most);
+  const float sum = warp_sum(all) * per_cta, share = fmaxf(1.f, sum), longest = static_cast<float>(most);
   constexpr int kTries = 6;
   constexpr float kShares[kTries] = {0.f, 0.5f, 0.75f, 1.f, 1.6f, 3.f};
-  const float one_each = floorf(__fdividef(1.f, static_cast<float>(__reduce_add_sync(0xffffffffu, pairs)) * per_cta));
+  // the shortest length with which the pieces are surely no more than the CTAs (a pair has less than one more than its
+  // steps divided by it)
+  const float spare = 1.f - static_cast<float>(__reduce_add_sync(0xffffffffu, pairs)) * per_cta;
+  const float one_each = spare > 0.f ? fmaxf(1.f, ceilf(__fdividef(sum, spare))) : longest;
   int per[kTries];
   float inv[kTries];
   uint32_t count[kTries];  // of a lane at most 2^24
@@ -93,7 +96,8 @@ __device__ __forceinline__ Cut make_cut(const KvSeqs& p, int heads, const CutOf&
 #pragma unroll
   for (int i = 0; i < kTries; ++i) {
     // pieces of the longest
-    const float n = fmaxf(1.f, i == 0 ? fminf(one_each, longest) : rintf(__fdividef(longest, share * (kShares[i] / kFine))));
+    const float n = fmaxf(1.f, i == 0 ? ceilf(__fdividef(longest, one_each) - 1e-4f)
+                                      : rintf(__fdividef(longest, share * (kShares[i] / kFine))));
     per[i] = static_cast<int>(ceilf(__fdividef(longest, n)));
     if (2.f * kFine * static_cast<float>(per[i]) < share) per[i] = most;  // (see max_joined)
     inv[i] = __fdividef(1.f, static_cast<float>(per[i]));

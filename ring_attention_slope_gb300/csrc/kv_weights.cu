@@ -10,12 +10,13 @@
 // packed multiply-add and half a packed add, and no maximum, no sum across lanes and no second product: the bound is the
 // MUFU unit, at 4 cycles a warp's 32 exponentials (128 x 256 of them take 1024 cycles of an SM).
 //
-// The work: where the new rows fill several tiles, a pair is (sequence, KV head, 256 keys) and its steps the row tiles
+// The work: where the new rows fill many tiles, a pair is (sequence, KV head, 256 keys) and its steps the row tiles
 // that see one of the keys; pairs of many rows and few keys are cut (kv_cut.cuh), and the pieces leave 256 sums each in the
-// workspace, which a second launch adds in order.  Where the rows are one tile (a decode step), a pair is (sequence, KV
-// head) and its steps the blocks of 256 keys: the rows stay and the keys stream past, read once, and nothing is joined.
-// Sixteen softmax warps: the four warps of (buffer, key tile) take every second step, so that each SM sub-partition has four
-// warps with exponentials to issue.
+// workspace, which a second launch adds in order.  Where the rows are few tiles (a decode step, the last queries of a prompt),
+// a pair is (sequence, KV head) and its steps run along the blocks of 256 keys: the rows stay and the keys stream past, read
+// once, and nothing is joined.
+// Sixteen softmax warps: the four warps of (buffer, key tile) take every second row tile, or of few rows every second key
+// block, so that each SM sub-partition has four warps with exponentials to issue.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -58,15 +59,15 @@ struct KvWeightsParams {
 constexpr int kSoftmaxWarps = 16, kTmaWarp = 16, kMmaWarp = 17, kLseWarp = 19;  // two MMA issuers
 constexpr int kThreads = 32 * 20;                                                   // five warps to a sub-partition
 
-// A piece: of a pair of rows that fill several tiles, row tiles [i0, i1) of one key block, numbered from 0 among the
-// `count` of every part that see one of its keys; else key blocks [i0, i1) and one row tile.
+// A piece: of a pair of many row tiles, those numbered [i0, i1) among the `count` of every part that see one of the block's
+// keys; of few, key blocks [i0, i1), of which those from `seen` on are seen, and the `count` row tiles of every part.
 struct Piece {
   int32_t b;  // sequence; -1: no pieces left
   int32_t few;
-  int32_t kvh, key0, len;  // (key0: of the block, or of block i0)
+  int32_t kvh, key0, len;  // (key0: of the block)
   int32_t row0, n, pos0;   // of the sequence: first q row, new tokens, position of the first
-  int32_t blk0, count;     // first row block that sees a key, and how many
-  int32_t i0, i1;
+  int32_t blk0, count;     // first row block, and how many
+  int32_t i0, i1, seen;
   int32_t slot;
 };
 
@@ -76,11 +77,13 @@ struct Cfg {
   static constexpr int kTileBytes = kChunks * kChunkBytes;             // 128 rows of K or Q
   static constexpr int kKSlots = DQK == 64 ? 8 : DQK == 128 ? 4 : 2;   // of 128 keys
   static constexpr int kQSlots = DQK == 64 ? 4 : 2;
+  static constexpr int kFew = DQK == 64 ? 4 : DQK == 128 ? 2 : 1;     // row tiles that may stay
+  static_assert(kFew <= kQSlots && (kFew == 1 || kKSlots >= 4), "they stay beside two key blocks");
   static constexpr int kQOffset = kKSlots * kTileBytes;
   static constexpr int kRestOffset = kQOffset + kQSlots * kTileBytes;
   struct Rest {  // behind the tiles
     float lse[kLseSlots][128];      // -lse log2(e) of a row tile's columns
-    float few_lse[kPieces][128];    // of a piece's one row tile
+    float few_lse[kPieces][kFew][128];  // of a piece's few row tiles
     float sums[kPieces][2][kBlockN];  // [piece][key tile]: what the second buffer's warps found
     uint64_t kfull[kKSlots], kempty[kKSlots], qfull[kQSlots], qempty[kQSlots], lfull[kLseSlots], lempty[kLseSlots];
     uint64_t s[4], sfree[4];  // [2 * buffer + key tile]
@@ -111,9 +114,10 @@ __device__ __forceinline__ void exp_pair(uint32_t s0, uint32_t s1, uint64_t sl2,
 }
 
 // Key blocks of a sequence, and the row tiles that one of them meets at most (those of a group of more than 128 heads are
-// its parts', one part after another); with one row tile, that and the key blocks.
+// its parts', one part after another); with few row tiles, one block for all keys.
 struct KeyCut {
   RowTile tile;
+  int few;
   bool accumulate;
   __device__ __forceinline__ int row_tiles(const KvSeq& s) const {
     return (s.n + tile.tokens - 1) / tile.tokens * tile.parts;
@@ -121,9 +125,9 @@ struct KeyCut {
   __device__ __forceinline__ SeqCut operator()(const KvSeq& s) const {
     const int rows = row_tiles(s), keys = (s.len + kKeys - 1) / kKeys;
     SeqCut c;
-    c.join = rows > 1;
+    c.join = rows > few;
     c.blocks = c.join ? keys : keys > 0 && !(rows == 0 && accumulate) ? 1 : 0;
-    c.steps = c.join ? rows : keys;
+    c.steps = c.join ? rows : keys * max(rows, 1);
     return c;
   }
 };
@@ -148,11 +152,14 @@ __device__ __forceinline__ Piece make_piece(const KvWeightsParams& p, int per, c
   r.n = q.n;
   r.pos0 = q.len - q.n;
   r.slot = -1;
+  r.seen = 0;
   if (r.few) {
-    piece_steps(cut.steps, pieces, c, r.i0, r.i1);
-    r.key0 = r.i0 * kKeys;
+    piece_steps((q.len + kKeys - 1) / kKeys, pieces, c, r.i0, r.i1);
+    r.key0 = 0;
     r.blk0 = 0;
-    r.count = q.n > 0 ? 1 : 0;
+    r.count = (q.n + p.tile.tokens - 1) / p.tile.tokens;
+    if (p.window > 0) r.seen = max(0, r.pos0 - p.window + 1) / kKeys;
+    if (r.count == 0) r.seen = r.i1;
     return r;
   }
   r.key0 = blk * kKeys;
@@ -178,8 +185,7 @@ struct Rows {
 };
 __device__ __forceinline__ Rows rows_of(const KvWeightsParams& p, int i, const Piece& pc) {
   Rows r;
-  if (pc.few) i = 0;
-  const int part = p.tile.parts > 1 && !pc.few ? i / pc.count : 0;
+  const int part = p.tile.parts > 1 ? i / pc.count : 0;
   r.token = (pc.blk0 + i - part * pc.count) * p.tile.tokens;
   r.tokens = min(p.tile.tokens, pc.n - r.token);
   r.head = part * p.tile.heads;
@@ -199,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* const cta_abort = &sh.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t limit = p.wait_limit_ns;
-  const KeyCut cut_of{p.tile, p.accumulate != 0};
+  const KeyCut cut_of{p.tile, C::kFew, p.accumulate != 0};
 
   pdl_launch_dependents();
   if (threadIdx.x == kTmaWarp * 32) {
@@ -312,19 +318,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++qcnt;
         return true;
       };
-      if (pc.i1 > pc.i0 && pc.count > 0) {
-        int page = page_of(pc.key0);
-        if (pc.few) {
-          ok = load_rows(0);
-          for (int i = pc.i0; ok && i < pc.i1; ++i) {
-            const int ahead = i + 1 < pc.i1 ? page_of((i + 1) * kKeys) : no_page;
-            ok = load_keys(i * kKeys, page);
-            page = ahead;
-          }
-        } else {
-          ok = load_keys(pc.key0, page);
-          for (int i = pc.i0; ok && i < pc.i1; ++i) ok = load_rows(i);
+      if (pc.few) {
+        const int first = max(pc.i0, pc.seen), tiles = pc.count * p.tile.parts;
+        int page = first < pc.i1 ? page_of(first * kKeys) : no_page;
+        for (int i = 0; ok && i < tiles && first < pc.i1; ++i) ok = load_rows(i);
+        for (int i = first; ok && i < pc.i1; ++i) {
+          const int ahead = i + 1 < pc.i1 ? page_of((i + 1) * kKeys) : no_page;
+          ok = load_keys(i * kKeys, page);
+          page = ahead;
         }
+      } else if (pc.i1 > pc.i0) {
+        ok = load_keys(pc.key0, page_of(pc.key0));
+        for (int i = pc.i0; ok && i < pc.i1; ++i) ok = load_rows(i);
       }
       w = __shfl_sync(0xffffffffu, next, 0);
     }
@@ -355,7 +360,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!warp_all(take_piece(k))) break;
       const Piece pc = sh.piece[k % kPieces];
       if (pc.b < 0) break;
-      const int tiles = pc.i1 <= pc.i0 || pc.count == 0 ? 0 : pc.few ? 1 : pc.i1 - pc.i0;
+      const int t0 = pc.few ? 0 : pc.i0;
+      const int tiles = pc.few ? (pc.seen < pc.i1 ? pc.count * p.tile.parts : 0) : pc.i1 - pc.i0;
       float next[4];
       auto fetch = [&](int i) {
         const Rows r = rows_of(p, i, pc);
@@ -364,17 +370,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int j = 0; j < 4; ++j) next[j] = tokens[j] < r.tokens && heads[j] < r.heads ? at[offset[j]] : -INFINITY;
       };
-      if (tiles > 0) fetch(pc.i0);
+      if (tiles > 0) fetch(t0);
       for (int i = 0; i < tiles; ++i) {
         float v[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = next[j] == -INFINITY ? next[j] : -next[j] * kLog2e;
-        if (i + 1 < tiles) fetch(pc.i0 + i + 1);
-        // (that of a piece with one row tile has a place of its own, which lasts as long as the piece)
+        if (i + 1 < tiles) fetch(t0 + i + 1);
+        // (that of few row tiles has a place of its own, which lasts as long as the piece)
         const int slot = cnt % kLseSlots;
         if (!pc.few) ok = warp_all(wait(&sh.lempty[slot], cnt / kLseSlots + 1, 65));
         if (!ok) break;
-        float* const dst = pc.few ? sh.few_lse[k % kPieces] : sh.lse[slot];
+        float* const dst = pc.few ? sh.few_lse[k % kPieces][i] : sh.lse[slot];
 #pragma unroll
         for (int j = 0; j < 4; ++j) dst[lane + 32 * j] = v[j];
         __syncwarp();
@@ -392,47 +398,68 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       const int t = warp - kMmaWarp;
       constexpr uint32_t kDescHi = smem_desc_hi(1024, kSwizzle128B);
-      int kcnt = t, qcnt = 0, scnt = 0;  // key tiles, row tiles, steps
+      int kcnt = 0, qcnt = 0, used[2] = {0, 0};  // key tiles and row tiles taken, uses of each buffer
       // S^T of the key tile at klo and the row tile at qlo (descriptors)
-      auto product = [&](uint32_t klo, uint32_t qlo, uint32_t idesc) -> bool {
-        const int buf = 2 * (scnt & 1) + t;
-        if (!wait(&sh.sfree[buf], (scnt >> 1) + 1, 68)) return false;
+      auto product = [&](int buf, uint32_t klo, uint32_t qlo, uint32_t idesc) -> bool {
+        const int b = 2 * buf + t;
+        int& n = buf == 0 ? used[0] : used[1];
+        if (!wait(&sh.sfree[b], n + 1, 68)) return false;
+        ++n;
         tc_fence_after_sync();
 #pragma unroll
         for (int kk = 0; kk < DQK / 16; ++kk) {
           const uint32_t off = ((kk >> 2) * kChunkBytes + (kk & 3) * 32) >> 4;
-          mma_ss_lh(tmem + buf * 128, klo + off, kDescHi, qlo + off, kDescHi, idesc, kk > 0 ? 1u : 0u);
+          mma_ss_lh(tmem + b * 128, klo + off, kDescHi, qlo + off, kDescHi, idesc, kk > 0 ? 1u : 0u);
         }
-        mma_commit(&sh.s[buf]);
-        ++scnt;
+        mma_commit(&sh.s[b]);
         return true;
       };
       const uint32_t klo0 = smem_desc_lo(smem_u32(sK), 16), qlo0 = smem_desc_lo(smem_u32(sQ), 16);
+      auto idesc_of = [](int cols) { return idesc_bf16_f32(kBlockM, 0, 0, 0) | (static_cast<uint32_t>(cols >> 3) << 17); };
       bool ok = true;
       for (int k = 0; ok; ++k) {
         if (!take_piece(k)) break;
         const Piece& pc = sh.piece[k % kPieces];
-        const int b = pc.b, few = pc.few, count = pc.count, steps = pc.i1 - pc.i0, tokens = pc.n;
+        const int b = pc.b, few = pc.few, i0 = pc.i0, i1 = pc.i1, first = max(i0, pc.seen);
+        const int tiles = pc.count * p.tile.parts, tokens = pc.n;
         mbar_arrive(&sh.wfree[k % kPieces]);
         if (b < 0) break;
-        if (steps <= 0 || count == 0) continue;
-        const int n_keys = few ? steps : 1, n_rows = few ? 1 : steps;
-        // (128 columns in every step would cost a decode step time)
-        const int cols = few ? (tokens * p.tile.heads + 31) & ~31 : 128;
-        const uint32_t idesc = idesc_bf16_f32(kBlockM, 0, 0, 0) | (static_cast<uint32_t>(cols >> 3) << 17);
-        for (int i = 0; ok && i < n_keys; ++i, kcnt += 2) {
-          const int kslot = kcnt % C::kKSlots;
-          const uint32_t klo = klo0 + kslot * (C::kTileBytes >> 4);
-          ok = wait(&sh.kfull[kslot], kcnt / C::kKSlots, 66);
-          for (int j = 0; ok && j < n_rows; ++j) {
-            const int qs = (qcnt + j) % C::kQSlots;
-            if (i == 0) ok = wait(&sh.qfull[qs], (qcnt + j) / C::kQSlots, 67);
-            if (ok) ok = product(klo, qlo0 + qs * (C::kTileBytes >> 4), idesc);
-            if (ok && i == n_keys - 1) mma_commit(&sh.qempty[qs]);
+        if (few) {
+          if (first >= i1) continue;
+          // (128 columns in every step would cost a decode step time)
+          const uint32_t idesc = idesc_of(tiles == 1 ? (tokens * p.tile.heads + 31) & ~31 : 128);
+          bool rows_there = false;
+          for (int m = i0; ok && m < i1; m += 2) {  // two blocks at a time, one to each buffer
+            for (int r = 0; ok && r < tiles; ++r) {
+              const int qs = (qcnt + r) % C::kQSlots;
+              if (!rows_there) ok = wait(&sh.qfull[qs], (qcnt + r) / C::kQSlots, 67);
+#pragma unroll
+              for (int buf = 0; buf < 2; ++buf) {
+                if (!ok || m + buf < first || m + buf >= i1) continue;
+                const int at = kcnt + 2 * (m + buf - first) + t, kslot = at % C::kKSlots;
+                if (r == 0) ok = wait(&sh.kfull[kslot], at / C::kKSlots, 66);
+                if (ok) ok = product(buf, klo0 + kslot * (C::kTileBytes >> 4), qlo0 + qs * (C::kTileBytes >> 4), idesc);
+                if (ok && r == tiles - 1) mma_commit(&sh.kempty[kslot]);
+              }
+            }
+            rows_there = true;
+          }
+          for (int r = 0; ok && r < tiles; ++r) mma_commit(&sh.qempty[(qcnt + r) % C::kQSlots]);
+          kcnt += 2 * (i1 - first);
+          qcnt += tiles;
+        } else if (i1 > i0) {
+          const uint32_t idesc = idesc_of(128);
+          const int kslot = (kcnt + t) % C::kKSlots;
+          ok = wait(&sh.kfull[kslot], (kcnt + t) / C::kKSlots, 66);
+          for (int i = i0; ok && i < i1; ++i, ++qcnt) {
+            const int qs = qcnt % C::kQSlots;
+            ok = wait(&sh.qfull[qs], qcnt / C::kQSlots, 67) &&
+                 product((i - i0) & 1, klo0 + kslot * (C::kTileBytes >> 4), qlo0 + qs * (C::kTileBytes >> 4), idesc);
+            if (ok) mma_commit(&sh.qempty[qs]);
           }
           if (ok) mma_commit(&sh.kempty[kslot]);
+          kcnt += 2;
         }
-        qcnt += n_rows;
       }
       mma_commit(&sh.drain[t]);
       wait_final(&sh.drain[t], 0, limit);
@@ -443,13 +470,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = (warp & 3) * 32 + lane, key = t * kBlockN + row;  // in the block
     const uint32_t tS = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + (2 * buf + t) * 128;
     const uint64_t sl2 = pack_f32x2(p.scale_log2, p.scale_log2);
-    int lcnt = 0, scnt = 0;
+    int lcnt = 0, used = 0;  // row tiles' lse taken, uses of this buffer
     bool ok = true;
     // The sum over a row tile's columns, all of which count (one without a row has a score of 0 and an lse of inf): each 32
     // columns' load runs under the exponentials of the 32 before.
     auto all_columns = [&](int step, const float* lse, float& sum) -> bool {
       const int b = 2 * buf + t;
-      if (!warp_all(wait(&sh.s[b], step >> 1, 73))) return false;
+      if (!warp_all(wait(&sh.s[b], step, 73))) return false;
       tc_fence_after_sync();
       uint64_t acc[2] = {0, 0};
       uint32_t s[2][32];
@@ -479,6 +506,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       sum = (a.x + a.y) + (z.x + z.y);
       return true;
     };
+    // Whether row tile i is full and all its rows see all of the warp's keys.
+    auto seen_by_all = [&](const Piece& pc, int i, int pos) -> bool {
+      const Rows r = rows_of(p, i, pc);
+      const int kfirst = pos - row, qa = pc.pos0 + r.token;
+      return r.tokens == p.tile.tokens && r.heads == p.tile.heads && kfirst + kBlockN - 1 <= qa &&
+             (p.window == 0 || qa + r.tokens - 1 - kfirst < p.window);
+    };
     // The sum over row tile i's columns that see the key at position pos.
     auto columns = [&](const Piece& pc, int i, int step, int pos, const float* lse, float& sum) -> bool {  // (any tile)
       const int b = 2 * buf + t;
@@ -489,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int hi = p.window > 0 && pos + p.window - 1 < qb ? max(0, pos + p.window - qa) * p.tile.heads : cols;
       const int kfirst = pos - row, klast = kfirst + kBlockN - 1;
       const bool all = klast <= qa && (p.window == 0 || qb - kfirst < p.window);  // every row sees every key
-      if (!warp_all(wait(&sh.s[b], step >> 1, 70))) return false;
+      if (!warp_all(wait(&sh.s[b], step, 70))) return false;
       tc_fence_after_sync();
       uint64_t acc[2] = {0, 0};
 #pragma unroll 1
@@ -538,7 +572,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!warp_all(take_piece(k))) break;
       const Piece pc = sh.piece[k % kPieces];
       if (pc.b < 0) break;
-      const int steps = pc.count == 0 ? 0 : max(0, pc.i1 - pc.i0);
       // The page of a key's weight, looked up ahead of the sums and first looked at when they are there.
       auto page_of = [&](int pos) -> int {
         return pos < pc.len ? p.seqs.table[pc.b * p.seqs.table_stride + (pos >> p.seqs.page_shift)] : -1;
@@ -549,19 +582,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         *dst = p.accumulate ? *dst + sum : sum;
       };
       if (pc.few) {
-        if (steps > 0) ok = warp_all(wait(&sh.few_full[k % kPieces], k / kPieces, 71));
-        const int first = pc.i0 + ((scnt ^ buf) & 1);  // this buffer's first step
+        const int tiles = pc.count * p.tile.parts;
+        ok = warp_all(wait(&sh.few_full[k % kPieces], k / kPieces, 71));
+        const int first = pc.i0 + buf;  // this buffer's first block
         int next = first < pc.i1 ? page_of(first * kKeys + key) : -1;
         for (int i = first; ok && i < pc.i1; i += 2) {
-          const int pg = next;
+          const int pg = next, pos = i * kKeys + key;
           next = i + 2 < pc.i1 ? page_of((i + 2) * kKeys + key) : -1;
-          float sum = 0.f;
-          if (steps > 0) ok = columns(pc, 0, scnt + (i - pc.i0), i * kKeys + key, sh.few_lse[k % kPieces], sum);
+          float total = 0.f;
+          for (int r = 0; ok && i >= pc.seen && r < tiles; ++r, ++used) {
+            float sum;
+            ok = tiles > 1 && seen_by_all(pc, r, pos) ? all_columns(used, sh.few_lse[k % kPieces][r], sum)
+                                                      : columns(pc, r, used, pos, sh.few_lse[k % kPieces][r], sum);
+            total += sum;
+          }
           if (!ok) break;
-          put(pg, i * kKeys + key, sum);
+          put(pg, pos, total);
         }
         if (!ok) break;
-        scnt += steps;
       } else {
         const int pos = pc.key0 + key;
         const int pg = buf == 0 && pc.slot < 0 ? page_of(pos) : -1;
@@ -574,19 +612,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (p.window > 0) f1 = min(f1, max(0, kfirst + p.window - pc.pos0) / tokens - pc.blk0);
         }
         float total = 0.f;
-        const int i0 = pc.i0 + ((scnt ^ buf) & 1);  // this buffer's first step
-        for (int i = i0; i < pc.i1; i += 2) {
-          const int step = scnt + (i - pc.i0), at = lcnt + (i - pc.i0), slot = at % kLseSlots;
+        for (int i = pc.i0 + buf; i < pc.i1; i += 2, ++used) {  // this buffer's
+          const int at = lcnt + (i - pc.i0), slot = at % kLseSlots;
           float sum;
           ok = warp_all(wait(&sh.lfull[slot], at / kLseSlots, 69));
-          if (ok) ok = i >= f0 && i < f1 ? all_columns(step, sh.lse[slot], sum) : columns(pc, i, step, pos, sh.lse[slot], sum);
+          if (ok) ok = i >= f0 && i < f1 ? all_columns(used, sh.lse[slot], sum) : columns(pc, i, used, pos, sh.lse[slot], sum);
           if (!ok) break;
           arrive(&sh.lempty[slot]);
           total += sum;
         }
         if (!ok) break;
-        scnt += steps;
-        lcnt += steps;
+        lcnt += pc.i1 - pc.i0;
         if (buf == 1) {
           sh.sums[k % kPieces][t][row] = total;
         } else {
