@@ -126,8 +126,8 @@ SLOPE_API slope_status slope_kv_attn(const slope_tensor* q, const slope_kv_cache
                                      void* workspace, size_t workspace_bytes, void* stream);
 
 /*
- * Workspace bytes slope_kv_attn needs on the current device for T rows in sequences of at most q_len new tokens (0: any
- * number) (0 for arguments it does not support).
+ * Workspace bytes slope_kv_attn needs for T rows in sequences of at most q_len new tokens (0: any number); 0 for arguments
+ * it does not support.
  */
 SLOPE_API size_t slope_kv_attn_workspace_size(int64_t T, int64_t Hq, const slope_kv_cache* cache, int32_t q_len);
 

@@ -907,8 +907,8 @@ __global__ void __launch_bounds__(kJoinThreads, 2) kv_attn_join_kernel(const __g
 
 // ---------------------------------------------------------------- launches
 
-// CTAs of a grid that fills the current device.
-int grid_of(int dqk, int dv) { return kv_sm_count() * (dqk == 64 && dv == 64 ? 2 : 1); }
+// CTAs of a grid that fills a device of so many SMs.
+int grid_of(int dqk, int dv, int sms) { return sms * (dqk == 64 && dv == 64 ? 2 : 1); }
 
 struct Workspace {
   int64_t rows_cap, max_slots;
@@ -920,7 +920,8 @@ Workspace workspace_of(int64_t T, int64_t group, int dqk, int dv, int32_t q_len)
   const int64_t most = std::max<int64_t>(1, q_len > 0 ? q_len : T);  // new tokens of a sequence
   Workspace w;
   w.rows_cap = std::min<int64_t>(tiles * tile.tokens, most) * tile.heads;
-  w.max_slots = tiles == 1 ? max_joined<Cfg<64, 64, 1>::kFine>(grid_of(dqk, dv)) : max_joined<Cfg<128, 128, 2>::kFine>(grid_of(dqk, dv));
+  const int64_t grid = grid_of(dqk, dv, kKvMaxSms);
+  w.max_slots = tiles == 1 ? max_joined<Cfg<64, 64, 1>::kFine>(grid) : max_joined<Cfg<128, 128, 2>::kFine>(grid);
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   w.pairs = 256;
   w.ml = w.pairs + up(w.max_slots * sizeof(KvPair));
@@ -1012,11 +1013,11 @@ slope_status slope_kv_attn(const slope_tensor* q, const slope_kv_cache* cache, c
   // pairs of a launch are counted in 32 bits, with room for the pieces
   const int64_t pairs = (T / p.tile.tokens + kKvMaxSeqs) * p.Hkv * p.tile.parts;
   if (pairs >= (int64_t(1) << 29)) return SLOPE_ERR_UNSUPPORTED;
-  const int grid = grid_of(cache->dqk, cache->dv);
   const bool few = T <= batch->B * p.tile.tokens;
-  if (grid <= 0) return cuda_fail("device attributes");
   const Workspace w = workspace_of(T, p.group, cache->dqk, cache->dv, batch->cu_q != nullptr ? 0 : batch->q_len);
   if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < w.total) return SLOPE_ERR_WORKSPACE;
+  const int grid = grid_of(cache->dqk, cache->dv, kv_sm_count());
+  if (grid <= 0) return cuda_fail("device attributes");
   p.seqs = kv_seqs(batch, cache, T);
   p.window = static_cast<int32_t>(window);
   p.scale_log2 = resolve_scale(scale, cache->dqk) * 1.44269504088896340736f;

@@ -28,7 +28,8 @@ bool make_page_map(CUtensorMap* m, const void* base, const slope_kv_cache* c, in
 // {64 channels, `heads` heads, `tokens` tokens} boxes of q, 128-byte swizzle.
 bool make_q_map(CUtensorMap* m, const slope_tensor* q, int heads, int tokens);
 
-// SMs of the current device (0 on failure).
+// SMs of the current device that the calls make use of (0 on failure), and how many at most: workspaces are sized for those.
+constexpr int kKvMaxSms = 160;
 int kv_sm_count();
 
 inline int log2_of(int64_t n) {

@@ -187,6 +187,7 @@ int kv_sm_count() {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
   if ((sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) return 0;
+  sms = std::min(sms, kKvMaxSms);
   known[dev].store(sms, std::memory_order_relaxed);
   return sms;
 }

@@ -679,7 +679,7 @@ struct Workspace {
 };
 Workspace workspace_of() {
   Workspace w;
-  w.max_slots = max_joined<kFine>(kv_sm_count());
+  w.max_slots = max_joined<kFine>(kKvMaxSms);
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   w.pairs = 256;
   w.part = w.pairs + up(w.max_slots * sizeof(int4));
@@ -743,9 +743,9 @@ slope_status slope_kv_attn_weights(const slope_tensor* q, const slope_kv_cache* 
   const int64_t blocks = (batch->max_pages * cache->page_size + kKeys - 1) / kKeys;
   if (std::min<int64_t>(batch->B, kKvMaxSeqs) * blocks * p.Hkv >= (int64_t(1) << 31)) return SLOPE_ERR_UNSUPPORTED;
   if ((T + p.tile.tokens) / p.tile.tokens * p.tile.parts >= (int64_t(1) << 30)) return SLOPE_ERR_UNSUPPORTED;
-  if (kv_sm_count() <= 0) return cuda_fail("device attributes");
   const Workspace w = workspace_of();
   if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < w.total) return SLOPE_ERR_WORKSPACE;
+  if (kv_sm_count() <= 0) return cuda_fail("device attributes");
   p.seqs = kv_seqs(batch, cache, T);
   p.window = static_cast<int32_t>(window);
   p.accumulate = accumulate ? 1 : 0;
