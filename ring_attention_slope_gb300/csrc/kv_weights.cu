@@ -688,7 +688,7 @@ Workspace workspace_of() {
 }
 
 template <int DQK>
-cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, KvWeightsParams p, cudaStream_t stream) {
+cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, KvWeightsParams p, int64_t tiles, cudaStream_t stream) {
   using C = Cfg<DQK>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -705,7 +705,7 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, KvWeightsParams
   if (p.tile_counter == nullptr) return cudaErrorInvalidDevice;
   const int sms = kv_sm_count();
   e = launch_early(kv_weights_kernel<DQK>, dim3(static_cast<unsigned>(sms)), kThreads, C::kSmemBytes, stream, tq, tk, p);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || tiles <= C::kFew) return e;  // (no sequence's rows fill more tiles: nothing is joined)
   return launch_early(kv_weights_join_kernel, dim3(static_cast<unsigned>(2 * sms)), kKeys, 0, stream, p);
 }
 
@@ -770,13 +770,16 @@ slope_status slope_kv_attn_weights(const slope_tensor* q, const slope_kv_cache* 
     tq = tk;  // no row is loaded
   else if (!make_q_map(&tq, q, p.tile.heads, p.tile.tokens))
     return cuda_fail("cuTensorMapEncodeTiled");
+  // row tiles of a sequence at most
+  const int64_t most = batch->cu_q != nullptr ? T : batch->q_len;
+  const int64_t tiles = (most + p.tile.tokens - 1) / p.tile.tokens * p.tile.parts;
   for (int64_t b = 0; b < batch->B; b += kKvMaxSeqs) {
     p.seqs.b0 = static_cast<int32_t>(b);
     p.seqs.B = static_cast<int32_t>(std::min<int64_t>(kKvMaxSeqs, batch->B - b));
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = cache->dqk == 64    ? launch<64>(tq, tk, p, s)
-                          : cache->dqk == 128 ? launch<128>(tq, tk, p, s)
-                                              : launch<192>(tq, tk, p, s);
+    const cudaError_t e = cache->dqk == 64    ? launch<64>(tq, tk, p, tiles, s)
+                          : cache->dqk == 128 ? launch<128>(tq, tk, p, tiles, s)
+                                              : launch<192>(tq, tk, p, tiles, s);
     if (e != cudaSuccess) return cuda_fail("cache weights kernel launch", e);
   }
   return SLOPE_OK;
