@@ -16,16 +16,16 @@
 // (a decode step has 8 rows, say) skip the softmax.
 //
 // The work: a pair is (sequence, KV head, row block), its steps the key tiles that its rows see.  The lengths are on the
-// device, so every CTA works out the same cut of the pairs into pieces of at most `per` steps (choose_per), and claims
-// pieces from a counter until none is left: long prefills take whole pairs (neighbours share a head's keys through
-// L2), decode steps of few sequences as many pieces as there are CTAs.  Pieces of a pair leave (m, l, O) in the workspace,
-// and a second launch, queued as a programmatic dependent, joins them in order; which CTA computes a piece changes no bit.
+// device, so every CTA works out the same shares of all pairs (kv_share.cuh) and claims them from a counter until none is
+// left.  Pieces of a pair that lies in several shares leave (m, l, O) in the workspace, and a second launch, queued as a
+// programmatic dependent, joins them in order; which CTA computes a share changes no bit.
 #include <cuda_bf16.h>
 
 #include <algorithm>
 #include <atomic>
+#include <climits>
 
-#include "kv_cut.cuh"
+#include "kv_share.cuh"
 #include "sm103_ptx.cuh"
 #include "waits.cuh"
 
@@ -68,20 +68,7 @@ struct KvAttnParams {
 
 __device__ __forceinline__ bool warp_all(bool v) { return __all_sync(0xffffffffu, v); }
 
-// ---------------------------------------------------------------- the cut
-
-// A sequence's row blocks, and the steps of its longest one at most.
-struct RowCut {
-  int block_tokens, window;
-  __device__ __forceinline__ SeqCut operator()(const KvSeq& s) const {
-    SeqCut c;
-    c.join = true;
-    c.blocks = (s.n + block_tokens - 1) / block_tokens;
-    c.steps = (s.len + kBlockN - 1) / kBlockN;
-    if (window > 0) c.steps = min(c.steps, (window + block_tokens - 2) / kBlockN + 2);
-    return c;
-  }
-};
+// ---------------------------------------------------------------- pieces
 
 // A piece: steps [j0, j1) of a pair.
 struct Piece {
@@ -96,19 +83,19 @@ struct Piece {
   int32_t flo[2], fhi[2];  // steps [flo, fhi) that every row of Q tile t sees in full
 };
 
-__device__ __forceinline__ Piece make_piece(const KvAttnParams& p, int per, const CutLists& lists, uint32_t w,
-                                            const RowCut& cut_of, int& join, int& pieces) {
+// Steps [from, to) of pair g of the line; `to` may lie past its last.  s: a sequence of the list not behind the pair's, set to
+// that one.
+__device__ __forceinline__ Piece make_piece(const KvAttnParams& p, const ShareLists& lists, const Shares& shares,
+                                            const RowCut& cut, uint32_t g, int from, int to, uint32_t share, int& s) {
   Piece r;
-  const int b = seq_of(lists, p.seqs.B, w), block_tokens = cut_of.block_tokens;
-  const KvSeq q = lists.seqs[b];
-  const SeqCut cut = cut_of(q);
-  pieces = pieces_of(cut.steps, per);
-  // local = (head * pieces + c) * blocks + (blocks - 1 - block)
-  const uint32_t local = w - lists.units[b], rest = cut.blocks == 1 ? local : divide(local, cut.blocks);
-  const int blk = cut.blocks - 1 - static_cast<int>(local - rest * cut.blocks);
-  const int h = static_cast<int>(pieces == 1 ? rest : divide(rest, pieces));
-  const int c = static_cast<int>(rest) - h * pieces;
-  r.b = p.seqs.b0 + b;
+  while (s + 1 < shares.seqs && lists.pairs[s + 1] <= g) ++s;
+  const int block_tokens = cut.block_tokens;
+  const KvSeq q = lists.at(s);
+  // local = head * blocks + (blocks - 1 - block)
+  const uint32_t blocks = static_cast<uint32_t>(cut.blocks(q)), local = g - lists.pairs[s];
+  const int h = static_cast<int>(blocks == 1 ? local : divide(local, blocks));
+  const int blk = static_cast<int>(blocks - 1 - (local - h * blocks));
+  r.b = p.seqs.b0 + lists.index[s];
   r.kvh = p.tile.parts == 1 ? h : h / p.tile.parts;
   const int first = (h - r.kvh * p.tile.parts) * p.tile.heads;
   r.head0 = r.kvh * p.group + first;
@@ -117,15 +104,11 @@ __device__ __forceinline__ Piece make_piece(const KvAttnParams& p, int per, cons
   r.row0 = q.row0 + blk * block_tokens;
   r.pos0 = q.len - q.n + blk * block_tokens;
   r.len = q.len;
-  const int hi = min(q.len, r.pos0 + r.tokens);  // keys below this
-  const int lo = p.window > 0 ? max(0, r.pos0 - p.window + 1) : 0;
-  const int j_lo = lo / kBlockN, j_hi = max(j_lo, (max(hi, 0) + kBlockN - 1) / kBlockN);
-  const int steps = j_hi - j_lo;
-  piece_steps(steps, pieces, c, r.j0, r.j1);
-  r.j0 += j_lo, r.j1 += j_lo;
-  const int pair = h * cut.blocks + blk;
-  r.slot = pieces > 1 ? static_cast<int32_t>(lists.slots[b]) + pair * pieces + c : -1;
-  join = pieces > 1 && c == 0 ? static_cast<int32_t>(lists.joins[b]) + pair : -1;  // the first piece lists the pair
+  int j_lo, j_hi;
+  cut.range(q, blk, j_lo, j_hi);
+  r.j0 = j_lo + from;
+  r.j1 = min(j_hi, j_lo + to);
+  r.slot = from > 0 ? 2 * static_cast<int32_t>(share) : r.j1 < j_hi ? 2 * static_cast<int32_t>(share) + 1 : -1;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int tile_tokens = p.tile.tokens, qa = r.pos0 + t * tile_tokens, rows = min(tile_tokens, r.tokens - t * tile_tokens);
@@ -140,7 +123,6 @@ struct Cfg {
   static constexpr int kTmaWarp = 4 * QT, kMmaWarp = kTmaWarp + 1;
   static constexpr int kThreads = 32 * (5 * QT + 1);
   static constexpr int kCtas = QT == 1 && DQK == 64 && DV == 64 ? 2 : 1;  // on an SM
-  static constexpr int kFine = kCtas;            // (kv_cut.cuh; a piece of two Q tiles leaves 132 KB, so they are longer)
   static constexpr uint32_t kTmemCols = 512 / kCtas;
   static constexpr int kQChunks = DQK / 64, kVChunks = DV / 64;
   static constexpr int kQTileBytes = kQChunks * kChunkBytes;
@@ -164,7 +146,7 @@ struct Cfg {
     uint32_t holes[kHoles];  // of a step's 16-token runs, those without a page
     uint32_t tmem;
     int abort;
-    CutLists lists;
+    ShareLists lists;
   };
   static constexpr int kSmemBytes = kRestOffset + static_cast<int>(sizeof(Rest));
   static constexpr uint32_t kColO = QT * kBlockN, kColP = kColO + QT * DV;
@@ -204,7 +186,7 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
   volatile int* const cta_abort = &sh.abort;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const RowCut cut_of{QT * p.tile.tokens, p.window};
+  const RowCut cut{QT * p.tile.tokens, p.window};
   const uint64_t limit = p.wait_limit_ns;
 
   pdl_launch_dependents();  // the join may be scheduled as this grid's CTAs leave
@@ -256,15 +238,16 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
 
   if (warp == C::kTmaWarp) {
     // ================================================================ producer: pieces, pages, loads
-    const Cut cut = make_cut<kPieceSteps, C::kFine>(p.seqs, p.Hkv * p.tile.parts, cut_of, sh.lists);
-    if (lane == 0 && blockIdx.x == 0) *p.n_pairs = static_cast<int32_t>(cut.joins);
-    const uint32_t total = cut.total;
+    const Shares shares = make_shares<kPieceSteps, C::kCtas>(p.seqs, p.Hkv * p.tile.parts, cut, sh.lists);
+    if (lane == 0 && blockIdx.x == 0) *p.n_pairs = static_cast<int32_t>(shares.shares);
+    const uint32_t total = shares.whole + shares.shares;
     const uint32_t q_bytes = static_cast<uint32_t>(p.tile.heads * p.tile.tokens) * 128 * C::kQChunks;
     const int boxes_log = max(0, 7 - p.seqs.page_shift);  // log2 of the boxes of 64 channels of a key tile
     const int boxes = 1 << boxes_log, box_rows = kBlockN >> boxes_log;
     const int no_page = static_cast<int>(p.seqs.n_pages);  // reads 0
     const int shift = p.seqs.page_shift;
-    uint32_t w = __shfl_sync(0xffffffffu, claimed, 0);
+    uint32_t w = 0, next = claimed;  // the claim being worked on, and (in lane 0) the one after it,
+    bool fresh = true;               // which has not been looked at
     uint32_t cnt = 0;   // K and V tiles loaded
     uint32_t step = 0;  // steps loaded
     int wt = 0;         // Q tiles loaded
@@ -278,37 +261,66 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
       const int pg = p.seqs.table[pc.b * p.seqs.table_stride + e];
       return pg >= 0 && pg < no_page ? pg : -1;
     };
+    // What is left of the claim: from step `step0` of pair `pair` to step `end_step` of pair `end`.
+    uint32_t pair = 0, end = 0, share = 0;
+    int step0 = 0, end_step = 0, seq = 0;
+    bool over = false;  // w is past the last claim
     // A piece, and its first 64 pages: entry e0 + lane of the table in each lane, and the 32 after them on their way.  The next
     // one is made out while the first loads of this one are under way.
     struct Work {
       Piece pc;
-      int join, pieces, e0, page, ahead;
+      uint32_t pair, share;
+      int seq, e0, page, ahead;
     };
-    auto prepare = [&](Work& q) {
-      q.pc = make_piece(p, cut.per, sh.lists, w, cut_of, q.join, q.pieces);
+    auto used_up = [&]() { return pair > end || (pair == end && step0 >= end_step); };
+    auto prepare = [&](Work& q) -> bool {
+      while (used_up()) {
+        if (!fresh && lane == 0) next = atomicAdd(p.tile_counter, 1u);
+        fresh = false;
+        w = __shfl_sync(0xffffffffu, next, 0);
+        if (w >= total) {
+          over = true;
+          return false;
+        }
+        if (w < shares.whole) {
+          pair = w, end = w + 1, step0 = end_step = 0;
+          continue;
+        }
+        share = w - shares.whole;
+        const ShareStart at = share_start<kPieceSteps>(sh.lists, shares, cut, share + (lane & 1));  // its start and its end
+        pair = __shfl_sync(0xffffffffu, at.pair, 0), end = __shfl_sync(0xffffffffu, at.pair, 1);
+        step0 = __shfl_sync(0xffffffffu, at.step, 0), end_step = __shfl_sync(0xffffffffu, at.step, 1);
+        // no pair begins in this share and goes on in others
+        if (lane == 0 && (end_step == 0 || (end == pair && step0 > 0))) p.pairs[share].pieces = 0;
+      }
+      q.pc = make_piece(p, sh.lists, shares, cut, pair, step0, pair == end ? end_step : INT_MAX / 2, share, seq);
+      q.pair = pair, q.share = share, q.seq = seq;
+      ++pair, step0 = 0;
       q.e0 = (q.pc.j0 * kBlockN) >> shift;
       q.page = q.pc.j1 > q.pc.j0 ? page_of(q.pc, q.e0 + lane) : no_page;
       q.ahead = q.pc.j1 > q.pc.j0 ? page_of(q.pc, q.e0 + 32 + lane) : no_page;
+      return true;
     };
     Work now{}, then{};
-    if (ok && w < total) prepare(now);
-    for (int k = 0; ok; ++k) {
+    bool more = true;
+    for (int k = -1; ok; ++k) {  // (before the first piece there is only the next one to be made out)
       if (k >= 2) ok = warp_all(wait_bounded(&bar_wfree[k & 1], ((k >> 1) - 1) & 1, cta_abort, p.status, limit, 32));
       if (!ok) break;
-      if (w >= total) {
+      if (!more) {
         if (lane == 0) {
           sh.piece[k & 1].tokens = -1;
           mbar_arrive(&bar_wfull[k & 1]);
         }
         break;
       }
-      uint32_t next = 0;
-      if (lane == 0) next = atomicAdd(p.tile_counter, 1u);  // on its way while this piece loads
+      if (k >= 0 && used_up()) {  // the next claim, on its way while this piece loads
+        fresh = true;
+        if (lane == 0) next = atomicAdd(p.tile_counter, 1u);
+      }
       const Piece& pc = now.pc;
-      if (lane == 0) {
+      if (lane == 0 && k >= 0) {
         sh.piece[k & 1] = pc;
         mbar_arrive(&bar_wfull[k & 1]);
-        if (now.join >= 0) p.pairs[now.join] = KvPair{pc.row0, pc.tokens, pc.head0, pc.heads, pc.slot, now.pieces, {0, 0}};
       }
       auto load_rows = [&]() -> bool {
         // Q of the previous piece is in use until its last S MMAs are done
@@ -327,7 +339,12 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
       const bool rows_first = wt == 0;
       if (rows_first && pc.j1 > pc.j0) ok = load_rows();
       bool prepared = false;
-      for (int j = pc.j0; ok && j < pc.j1; ++j, ++step) {
+      for (int j = pc.j0; ok; ++j, ++step) {
+        if (!prepared && (j == pc.j0 + 2 || j >= pc.j1)) {
+          prepared = true;
+          more = prepare(then);
+        }
+        if (j >= pc.j1) break;
         const int e = (j * kBlockN) >> shift;
         if (e >= now.e0 + 32) {
           now.e0 += 32;
@@ -361,18 +378,15 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
         }
         // the first keys need not wait for the previous piece's rows to be done with
         if (ok && !rows_first && j == pc.j0) ok = load_rows();
-        if (ok && j == pc.j0 + 1) {
-          w = __shfl_sync(0xffffffffu, next, 0);
-          prepared = true;
-          if (w < total) prepare(then);
-        }
       }
-      if (!prepared) {
-        w = __shfl_sync(0xffffffffu, next, 0);
-        if (ok && w < total) prepare(then);
+      // The pair that begins here and goes on in other shares (looked up after the loads, which should not wait for it).
+      if (lane == 0 && k >= 0 && pc.slot == 2 * static_cast<int32_t>(now.share) + 1) {
+        const int n = static_cast<int>(last_share<kPieceSteps>(sh.lists, shares, cut, now.pair, now.seq) - now.share) + 1;
+        p.pairs[now.share] = KvPair{pc.row0, pc.tokens, pc.head0, pc.heads, pc.slot, n, {0, 0}};
       }
       now = then;
     }
+    if (!over && fresh) w = __shfl_sync(0xffffffffu, next, 0);  // (given up before)
     if (lane == 0) {
       release_pieces(p.tile_counter, total, w);
       if (!ok) {
@@ -807,24 +821,41 @@ __global__ void __launch_bounds__(kJoinThreads, 2) kv_attn_join_kernel(const __g
   constexpr int kGroups = kJoinThreads / 128, kAhead = 4;
   __shared__ float s_m[kGroups][128], s_l[kGroups][128];
   __shared__ float4 s_v[kGroups][128];
+  __shared__ int16_t s_list[kJoinThreads];
+  __shared__ int s_count[kJoinThreads / 32];
   const int chunks = (p.rows_cap * (DV / 4) + kJoinThreads - 1) / kJoinThreads;
   const int grp = threadIdx.x >> 7, lane = threadIdx.x & 127;
-  int pair = blockIdx.x / chunks, chunk = blockIdx.x - pair * chunks;
   pdl_wait();
-  // (the first pair's record is read along with what says whether it counts)
-  KvPair e = p.pairs[min(pair, p.max_slots - 1)];
-  const int n_pairs = min(*p.n_pairs, p.max_slots);
+  // (the first record is read along with what says whether it counts)
+  KvPair e = p.pairs[min(static_cast<int>(blockIdx.x), p.max_slots / 2 - 1)];
+  const int shares = min(*p.n_pairs, p.max_slots / 2);
   if (*reinterpret_cast<volatile int*>(p.status) != 0) return;  // pieces may be missing
-  for (int64_t item = blockIdx.x; pair < n_pairs; item += gridDim.x) {
-    if (item != blockIdx.x) {
-      pair = static_cast<int>(item / chunks), chunk = static_cast<int>(item - static_cast<int64_t>(pair) * chunks);
-      if (pair >= n_pairs) break;
-      e = p.pairs[pair];
+  int n = shares;  // of the list
+  if (chunks > 1) {
+    // the shares in which a pair begins that goes on in others
+    static_assert(2 * kKvMaxSms <= kJoinThreads, "a share to a thread");
+    const int t = threadIdx.x, w = t >> 5;
+    const bool mine = t < shares && p.pairs[t].pieces > 0;
+    const uint32_t some = __ballot_sync(0xffffffffu, mine);
+    if ((t & 31) == 0) s_count[w] = __popc(some);
+    __syncthreads();
+    int at = 0;
+    n = 0;
+    for (int i = 0; i < kJoinThreads / 32; ++i) {
+      if (i == w) at = n;
+      n += s_count[i];
     }
+    if (mine) s_list[at + __popc(some & ((1u << (t & 31)) - 1u))] = static_cast<int16_t>(t);
+    __syncthreads();
+  }
+  for (int item = blockIdx.x; item < n * chunks; item += gridDim.x) {
+    const int share = chunks > 1 ? s_list[item / chunks] : item, chunk = chunks > 1 ? item % chunks : 0;
+    if (chunks > 1 || item != static_cast<int>(blockIdx.x)) e = p.pairs[share];
     const int rows = e.tokens * p.tile.heads;
-    if (e.pieces <= 0 || e.slot < 0 || e.slot + e.pieces > p.max_slots || e.row0 < 0 || e.row0 + e.tokens > p.seqs.T ||
-        rows > p.rows_cap)
+    if (e.pieces <= 0 || e.slot != 2 * share + 1 || 2 * (share + e.pieces) > p.max_slots || e.row0 < 0 ||
+        e.row0 + e.tokens > p.seqs.T || rows > p.rows_cap)
       continue;
+    auto slot_of = [&](int c) { return c == 0 ? e.slot : 2 * (share + c); };
     float mm = -INFINITY, ll = 0.f;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
     // a piece whose row saw nothing has m = -inf and l = 0, and a NaN anywhere stays one
@@ -847,7 +878,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) kv_attn_join_kernel(const __g
         float4 v[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-          const int64_t prow = static_cast<int64_t>(e.slot + min(c0 + k * stride, e.pieces - 1)) * p.rows_cap + rr;
+          const int64_t prow = static_cast<int64_t>(slot_of(min(c0 + k * stride, e.pieces - 1))) * p.rows_cap + rr;
           ml[k] = p.ml[prow];
           v[k] = *reinterpret_cast<const float4*>(p.part + prow * DV + ch);
         }
@@ -920,8 +951,7 @@ Workspace workspace_of(int64_t T, int64_t group, int dqk, int dv, int32_t q_len)
   const int64_t most = std::max<int64_t>(1, q_len > 0 ? q_len : T);  // new tokens of a sequence
   Workspace w;
   w.rows_cap = std::min<int64_t>(tiles * tile.tokens, most) * tile.heads;
-  const int64_t grid = grid_of(dqk, dv, kKvMaxSms);
-  w.max_slots = tiles == 1 ? max_joined<Cfg<64, 64, 1>::kFine>(grid) : max_joined<Cfg<128, 128, 2>::kFine>(grid);
+  w.max_slots = 2 * grid_of(dqk, dv, kKvMaxSms);  // a share has two pieces that are joined at most
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   w.pairs = 256;
   w.ml = w.pairs + up(w.max_slots * sizeof(KvPair));
@@ -952,8 +982,7 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
   e = launch_early(kv_attn_kernel<DQK, DV, QT>, dim3(static_cast<unsigned>(grid)), C::kThreads, C::kSmemBytes, stream, tq, tk,
                    tv, p);
   if (e != cudaSuccess) return e;
-  const int64_t items = p.max_slots / 2 * ((p.rows_cap * (DV / 4) + kJoinThreads - 1) / kJoinThreads);
-  const int64_t ctas = std::min<int64_t>(items, 2 * kv_sm_count());
+  const int ctas = std::min(grid * ((p.rows_cap * (DV / 4) + kJoinThreads - 1) / kJoinThreads), 2 * kv_sm_count());
   return launch_early(kv_attn_join_kernel<DV>, dim3(static_cast<unsigned>(ctas)), kJoinThreads, 0, stream, p);
 }
 

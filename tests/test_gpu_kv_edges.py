@@ -235,7 +235,8 @@ def test_outputs_and_workspaces_given():
     q = batch.q.cuda()
     ref = ko.attention(batch)
     size = slope.kv_attn_workspace_size(4, 8, cache, 2)
-    guard = torch.full((size + 512,), 0xA5, dtype=torch.uint8, device="cuda")
+    most = max(size, slope.kv_attn_weights_workspace_size(4, 8, cache, 2), slope.kv_evict_workspace_size(2, cache, 100))
+    guard = torch.full((most + 512,), 0xA5, dtype=torch.uint8, device="cuda")
     room = torch.full((4, 10, 72), 3.0, device="cuda")
     out, lse = room[:, 1:9, 4:68], torch.full((4, 16), 3.0, device="cuda").t()[::2, :]
     got = slope.kv_attn(q, cache, table, n, q_len=2, out=out, lse=lse, workspace=guard[256:256 + size])
@@ -247,7 +248,6 @@ def test_outputs_and_workspaces_given():
     with pytest.raises(slope.SlopeError):
         slope.kv_attn(q, cache, table, n, q_len=2, workspace=guard[256:256 + size - 1])
     wsize = slope.kv_attn_weights_workspace_size(4, 8, cache, 2)
-    assert wsize <= guard.numel() - 256
     w = torch.zeros(batch.n_pages, 2, 16, device="cuda")
     slope.kv_attn_weights(q, cache, table, n, lse.contiguous(), w, q_len=2, workspace=guard[256:256 + wsize])
     check_weights(batch, w, lse.cpu())
