@@ -15,8 +15,10 @@ struct SeqCut {
 };
 // a / b, without a division's forty instructions where a < 2^20: a quotient next to a whole number is at least 1 / (2 b) away
 // from it with the half added, and off by at most 2^-22 of itself.
+// (The rare other case is kept out of line: code that runs once, before a call's first load, is as slow as it is long.)
+static __device__ __noinline__ uint32_t divide_any(uint32_t a, uint32_t b) { return a / b; }
 __device__ __forceinline__ uint32_t divide(uint32_t a, uint32_t b) {
-  if (a >= (1u << 20)) return a / b;
+  if (__builtin_expect(a >= (1u << 20), 0)) return divide_any(a, b);
   return __float2uint_rz(__fdividef(static_cast<float>(a) + 0.5f, static_cast<float>(b)));
 }
 __device__ __forceinline__ int pieces_of(int steps, int per) {
