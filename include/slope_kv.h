@@ -25,6 +25,9 @@
 
 #include "slope.h"
 
+/* Launches of slope_kv_attn and slope_kv_attn_weights that may be queued at a time. */
+#define SLOPE_KV_COUNTERS 65536
+
 #ifdef __cplusplus
 extern "C" {
 #endif
@@ -112,14 +115,17 @@ SLOPE_API slope_status slope_kv_write(const slope_kv_cache* cache, const slope_t
  *     need one each, captured graphs that may be replayed at the same time too.
  * B == 0 or T == 0 is a no-op.
  *
- * A launch takes one of the SLOPE_TILE_COUNTERS (slope.h), another for every 512
- * sequences after the first.  Softmax weights are rounded to bf16 on their way
- * into the tensor cores; scores, maxima, sums and outputs stay in fp32 until the
- * output's rounding.  Whatever the cache holds behind a sequence's last token, NaN
- * too, reaches no row.  Among a sequence's tokens a value that is not finite may also
- * make rows NaN that the causal mask or the window keeps from it, where 128
- * consecutive positions hold both.  Results do not depend on how the work was dealt
- * to the GPU's CTAs in time: the same call gives the same bits.
+ * A launch takes a counter out of SLOPE_KV_COUNTERS on the device, another for every
+ * 512 sequences after the first: keep fewer launches queued or running at a time.
+ * Launches recorded into a graph take theirs out of as many others and keep them, so
+ * replays of one recording must not overlap; other calls may run beside them.
+ * Softmax weights are rounded to bf16 on their way into the tensor cores; scores,
+ * maxima, sums and outputs stay in fp32 until the output's rounding.  Whatever the
+ * cache holds behind a sequence's last token, NaN too, reaches no row.  Among a
+ * sequence's tokens a value that is not finite may also make rows NaN that the causal
+ * mask or the window keeps from it, where 128 consecutive positions hold both.
+ * Results do not depend on how the work was dealt to the GPU's CTAs in time: the same
+ * call gives the same bits.
  */
 SLOPE_API slope_status slope_kv_attn(const slope_tensor* q, const slope_kv_cache* cache, const slope_kv_batch* batch,
                                      int64_t window, float scale, slope_tensor* out, slope_tensor* lse,

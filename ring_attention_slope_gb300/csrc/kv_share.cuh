@@ -89,7 +89,7 @@ __device__ __forceinline__ uint32_t step_cost(uint32_t w, int fewest) {
 template <int kPieceSteps, int kCtas>
 __device__ __forceinline__ Shares make_shares(const KvSeqs& p, int heads, const RowCut& cut, ShareLists& lists) {
   const int lane = threadIdx.x & 31;
-  uint32_t sum = 0, my_pairs = 0;  // of a lane no more than 2^26
+  uint32_t sum = 0, block_sum = 0;  // of a lane no more than 2^26
   int most = 1;
   KvSeq mine{};
   int my_blocks = 0, my_most = 0;  // of the lane's last sequence, its only one where there are no more than 32
@@ -100,7 +100,7 @@ __device__ __forceinline__ Shares make_shares(const KvSeqs& p, int heads, const 
     my_most = cut.most(mine);
     if (my_blocks > 0) {
       most = max(most, my_most);
-      my_pairs = min(my_pairs + static_cast<uint32_t>(my_blocks), 1u << 26);
+      block_sum = min(block_sum + static_cast<uint32_t>(my_blocks), 1u << 26);
       sum = static_cast<uint32_t>(
           fminf(static_cast<float>(sum) + static_cast<float>(my_blocks) * static_cast<float>(my_most), 67108864.f));
     }
@@ -110,7 +110,8 @@ __device__ __forceinline__ Shares make_shares(const KvSeqs& p, int heads, const 
   const float steps = static_cast<float>(__reduce_add_sync(0xffffffffu, sum)) * per_cta;  // a CTA's, evenly
   Shares r;
   r.per_step = max(0, min(static_cast<int>(fminf(steps, 100.f)) - 1, kPieceSteps));
-  const float all_rounds = static_cast<float>(__reduce_add_sync(0xffffffffu, my_pairs)) * per_cta;
+  const uint32_t all_blocks = __reduce_add_sync(0xffffffffu, block_sum);
+  const float all_rounds = static_cast<float>(all_blocks) * per_cta;
   const float even = steps + all_rounds * kPieceSteps;
   // the line, in two passes: the long sequences, then the others
   uint32_t pairs = 0, long_pairs = 0, finest = 8, cost = 0;
@@ -182,6 +183,9 @@ __device__ __forceinline__ Shares make_shares(const KvSeqs& p, int heads, const 
   // Shares of many long pairs each would have all heads' keys read at once; and costs are counted in 32 bits.
   if (r.shares == 0 || wholes * piece + share >= uncut || share > 3.f * piece || steps * static_cast<float>(gridDim.x) > 6e7f)
     r.whole = pairs, r.shares = 0;
+  // Row ranges that overlap can make more pairs than can be counted (those of a call that is in order are below 2^29 and its
+  // blocks below 2^26): no work then.
+  if (all_blocks >= 1u << 26 || all_rounds * static_cast<float>(gridDim.x) > 1.0e9f) r.whole = r.shares = 0;
   return r;
 }
 

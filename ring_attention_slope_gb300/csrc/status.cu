@@ -7,6 +7,7 @@
 #include <atomic>
 
 #include "kernels.cuh"
+#include "slope_kv.h"
 #include "sm103_ptx.cuh"
 #include "waits.cuh"
 
@@ -23,6 +24,9 @@ __device__ int g_slope_status[2];
 // an SM until that previous grid is done, and the device has far fewer SMs than slots.
 // Across streams two such launches would have to be queued or running at the same time.
 __device__ uint32_t g_slope_tile_counters[kTileCounterSlots];
+// Of launches on the 16-bit cache: [0] on streams, [1] recorded into graphs.
+constexpr uint32_t kCacheCounterSlots = SLOPE_KV_COUNTERS;
+__device__ uint32_t g_slope_cache_counters[2][kCacheCounterSlots];
 
 namespace {
 
@@ -30,6 +34,8 @@ constexpr int kMaxDevices = 64;
 std::atomic<int*> g_status_ptr[kMaxDevices];
 std::atomic<uint32_t*> g_counters_ptr[kMaxDevices];
 std::atomic<uint32_t> g_counter_next[kMaxDevices];
+std::atomic<uint32_t*> g_cache_counters_ptr[kMaxDevices];
+std::atomic<uint32_t> g_cache_counter_next[kMaxDevices][2];
 
 // One block waits on a barrier that nothing ever arrives on; the bounded wait
 // must run out, record the timeout and let the kernel return normally.
@@ -72,6 +78,23 @@ uint32_t* claim_tile_counter() {
     g_counters_ptr[dev].store(base, std::memory_order_release);
   }
   return base + g_counter_next[dev].fetch_add(1, std::memory_order_relaxed) % kTileCounterSlots;
+}
+
+uint32_t* claim_cache_counter(cudaStream_t stream) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
+  uint32_t* base = g_cache_counters_ptr[dev].load(std::memory_order_acquire);
+  if (base == nullptr) {
+    void* addr = nullptr;
+    if (cudaGetSymbolAddress(&addr, g_slope_cache_counters) != cudaSuccess) return nullptr;
+    base = static_cast<uint32_t*>(addr);
+    g_cache_counters_ptr[dev].store(base, std::memory_order_release);
+  }
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(stream, &capture) != cudaSuccess) return nullptr;  // (nor could a kernel be launched)
+  const uint32_t ring = capture == cudaStreamCaptureStatusNone ? 0 : 1;
+  const uint32_t k = g_cache_counter_next[dev][ring].fetch_add(1, std::memory_order_relaxed) % kCacheCounterSlots;
+  return base + ring * kCacheCounterSlots + k;
 }
 
 cudaError_t launch_timeout_selftest(uint64_t limit_ns, int* status, cudaStream_t stream) {

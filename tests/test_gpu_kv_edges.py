@@ -283,3 +283,31 @@ def test_long_sequences_of_many_pieces():
         w = torch.zeros(batch.n_pages, heads[1], 64, device="cuda")
         slope.kv_attn_weights(batch.q.cuda(), cache, table, n, lse, w, cu_q=cu)
         check_weights(batch, w, lse.cpu())
+
+
+def test_a_graph_replayed_beside_thousands_of_calls():
+    """A recorded call keeps the counter that its CTAs claim their work from; calls on streams never come round to it."""
+    batch = ko.Batch([700, 90, 1500], [1, 1, 1], 16, 2, 64, 64, 16, seed=21)
+    cache, table, n, _ = on_gpu(batch)
+    q = batch.q.cuda()
+    out, lse = slope.kv_attn(q, cache, table, n, q_len=1)
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        got = [slope.kv_attn(q, cache, table, n, q_len=1) for _ in range(4)]
+    mine = torch.zeros_like(out)
+    work = torch.empty(slope.kv_attn_workspace_size(3, 16, cache, 1), dtype=torch.uint8, device="cuda")
+    side.wait_stream(torch.cuda.current_stream())
+    for i in range(4500):
+        if i % 20 == 0:
+            graph.replay()
+        slope.kv_attn(q, cache, table, n, q_len=1, out=mine, want_lse=False, workspace=work, stream=side)
+        if i % 500 == 499:
+            torch.cuda.synchronize()
+            assert (mine == out).all()
+            for o, l in got:
+                assert (o == out).all() and (l == lse).all()
+                o.zero_(), l.zero_()
+            mine.zero_()
+            torch.cuda.synchronize()
+    assert slope.device_status() == (0, 0)
