@@ -18,7 +18,16 @@
 // The work: a pair is (sequence, KV head, row block), its steps the key tiles that its rows see.  The lengths are on the
 // device, so every CTA works out the same shares of all pairs (kv_share.cuh) and claims them from a counter until none is
 // left.  Pieces of a pair that lies in several shares leave (m, l, O) in the workspace, and a second launch, queued as a
-// programmatic dependent, joins them in order; which CTA computes a share changes no bit.
+// programmatic dependent, joins them in order; which CTA computes a share changes no bit.  Equal pieces of each pair, about as
+// many as fill the rounds over the grid, in place of equal shares of the line: 2K chunk at 16K, 32 heads of 192/128, 559
+// -> 502 us; 32/4 heads of 128/128 494 -> 439; a 1000-token chunk at 16K and 15 decoding sequences, 64/8 heads of 64,
+// 292 -> 265; 1 x 1000 tokens 11.2 -> 11.7 (the shares take longer to work out).  The join inside this kernel by the CTA that
+// is last at a pair was faster for one short sequence (10.9) and slower elsewhere (the mixed step by 35).
+//
+// What bounds it, on one GB300: long chunks the tensor cores with the softmax beside them (64/8 heads of 64, 4096 tokens at
+// 64K: 3640 us, 1.17 PFLOP/s; if a 64-wide PV takes as long as a 128-wide one, 90% of the tensor pipe's time); decode steps
+// HBM (8 x 102400 tokens: 255 us, 6.58 TB/s of the 6.68 of a copy; 32 ragged up to 32K: 65 us, 4.4 TB/s); short ones latencies
+// (1 x 1000: 11.7 us, of which the join's launch 3, lengths and shares 2).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -816,6 +825,8 @@ __global__ void __launch_bounds__(Cfg<DQK, DV, QT>::kThreads, Cfg<DQK, DV, QT>::
 // Joins the pieces of the pairs that were cut, in their order.  A lane has four channels of a row.  Few pieces (many rows:
 // a chunk's pairs): every thread has a row's channels of its own and all of its pieces in flight.  More (few rows: a
 // decode step): the CTA's four groups of 128 threads take every fourth piece, four in flight, and join at the end.
+// (32 heads of 192/128, 4 chunks of 777: 15 us for 28 MB from HBM and more from L2.  A CTA for each part of a share, most of
+// them without work, cost 2 us a thousand.)
 template <int DV>
 __global__ void __launch_bounds__(kJoinThreads, 2) kv_attn_join_kernel(const __grid_constant__ KvAttnParams p) {
   constexpr int kGroups = kJoinThreads / 128, kAhead = 4;

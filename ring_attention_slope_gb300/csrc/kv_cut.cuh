@@ -1,5 +1,6 @@
-// How the kernels on the paged cache share their work out: every CTA's producer warp reads the sequences' lengths, works
-// out the same cut into pieces, and claims pieces from a counter until none is left.
+// How the weights' kernel on the paged cache shares its work out: every CTA's producer warp reads the sequences' lengths, works
+// out the same cut into pieces, and claims pieces from a counter until none is left.  (Attention: kv_share.cuh.  The weights'
+// pieces mostly write results of their own, so cutting a pair costs them little.)
 //
 // A sequence's work is `heads` times `blocks` pairs of up to `steps` steps each (what a step is, the kernel says).  A
 // pair is cut into equal pieces of at most `per` steps.
@@ -55,8 +56,7 @@ __device__ __forceinline__ float warp_sum(float v) {
 // The longest pair is cut so that no CTA has more than one piece, or into pieces of about 1 / (2 kFine) to 3 / kFine of
 // a share, and the length of those is tried as every pair's.  The length with the least time wins: that of the rounds over
 // the grid where the pieces are all alike, else that of one piece or of an even share of all of them, whichever is
-// more, and half a piece for the uneven end.  (8 sequences of 102400 tokens with 64/8 heads: 640 pieces of 80 steps for 304
-// CTAs took 327 us, 256 of 200 take 260.)  Estimates are in fp32, the same in every CTA.  This runs before a call's
+// more, and half a piece for the uneven end.  Estimates are in fp32, the same in every CTA.  This runs before a call's
 // first load: the six lengths are tried side by side, as one after another they took 1.3 us.
 template <int kPieceSteps, int kFine, typename CutOf>
 __device__ __forceinline__ Cut make_cut(const KvSeqs& p, int heads, const CutOf& cut_of, CutLists& lists) {

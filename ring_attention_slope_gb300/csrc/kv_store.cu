@@ -2,7 +2,8 @@
 //
 // The store is a scatter of rows: bf16 is copied, fp32 rounded to nearest even.  A thread takes the same 8 channels (16 bytes
 // in the cache) of kTokens tokens, whose slots and then rows it loads together, so a call of a few tokens costs two loads'
-// latency and a chunk of a prompt runs at the copy rate.
+// latency and a chunk of a prompt runs near the copy rate (8 heads of 64: 32 tokens 1.7 us, 12288 9.7 us, 5.3 TB/s, of which
+// the start and the end take 1.5).
 #include <cuda_bf16.h>
 
 #include <algorithm>
