@@ -285,6 +285,30 @@ def test_long_sequences_of_many_pieces():
         check_weights(batch, w, lse.cpu())
 
 
+def ragged(n, longest, most, seed):
+    gen = torch.Generator().manual_seed(seed)
+    lens = torch.randint(0, longest + 1, (n,), generator=gen).tolist()
+    return lens, [min(a, int(torch.randint(0, most + 1, (1,), generator=gen))) for a in lens]
+
+
+@pytest.mark.parametrize("lens, new, heads, window", [
+    ([1500, 1490], [640, 640], (32, 4, 64, 64), 0),          # more pairs than CTAs: full rounds, then shares
+    ([900] * 8, [600] * 8, (8, 4, 128, 128), 0),             # the same with two Q tiles, the last block half empty
+    ([2600, 2600, 400], [520, 300, 90], (5, 1, 64, 64), 700),
+    (*ragged(70, 1500, 60, 1), (5, 1, 64, 64), 0),           # more than two warps' lanes of sequences
+    (*ragged(70, 1500, 60, 2), (10, 2, 64, 64), 200),
+    (*ragged(45, 900, 300, 3), (4, 2, 192, 128), 0),
+    (*ragged(530, 300, 3, 4), (4, 1, 64, 64), 0),            # two launches
+    (*ragged(40, 5000, 1, 5), (8, 4, 64, 64), 0),
+], ids=["rounds", "two_tiles", "window", "many", "many_window", "wide", "two_launches", "decode"])
+def test_shares_of_many_pairs(lens, new, heads, window):
+    """Where the work is dealt out in full rounds of whole pairs and equal shares of the rest, every pair is there once."""
+    batch = ko.Batch(lens, new, *heads, 16, seed=len(lens))
+    cache, table, n, cu = on_gpu(batch)
+    out, lse = slope.kv_attn(batch.q.cuda(), cache, table, n, cu_q=cu, window=window, out_dtype=torch.float32)
+    check(out, lse, ko.attention(batch, window=window))
+
+
 def test_a_graph_replayed_beside_thousands_of_calls():
     """A recorded call keeps the counter that its CTAs claim their work from; calls on streams never come round to it."""
     batch = ko.Batch([700, 90, 1500], [1, 1, 1], 16, 2, 64, 64, 16, seed=21)
