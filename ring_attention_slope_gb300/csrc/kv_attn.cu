@@ -832,7 +832,8 @@ __global__ void __launch_bounds__(kJoinThreads, 2) kv_attn_join_kernel(const __g
   constexpr int kGroups = kJoinThreads / 128, kAhead = 4;
   __shared__ float s_m[kGroups][128], s_l[kGroups][128];
   __shared__ float4 s_v[kGroups][128];
-  __shared__ int16_t s_list[kJoinThreads];
+  __shared__ KvPair s_pairs[2 * kKvMaxSms];
+  __shared__ int16_t s_list[2 * kKvMaxSms];
   __shared__ int s_count[kJoinThreads / 32];
   const int chunks = (p.rows_cap * (DV / 4) + kJoinThreads - 1) / kJoinThreads;
   const int grp = threadIdx.x >> 7, lane = threadIdx.x & 127;
@@ -846,7 +847,9 @@ __global__ void __launch_bounds__(kJoinThreads, 2) kv_attn_join_kernel(const __g
     // the shares in which a pair begins that goes on in others
     static_assert(2 * kKvMaxSms <= kJoinThreads, "a share to a thread");
     const int t = threadIdx.x, w = t >> 5;
-    const bool mine = t < shares && p.pairs[t].pieces > 0;
+    KvPair r{};
+    if (t < shares) r = p.pairs[t];
+    const bool mine = r.pieces > 0;
     const uint32_t some = __ballot_sync(0xffffffffu, mine);
     if ((t & 31) == 0) s_count[w] = __popc(some);
     __syncthreads();
@@ -856,12 +859,22 @@ __global__ void __launch_bounds__(kJoinThreads, 2) kv_attn_join_kernel(const __g
       if (i == w) at = n;
       n += s_count[i];
     }
-    if (mine) s_list[at + __popc(some & ((1u << (t & 31)) - 1u))] = static_cast<int16_t>(t);
+    if (mine) {
+      at += __popc(some & ((1u << (t & 31)) - 1u));
+      s_list[at] = static_cast<int16_t>(t);
+      s_pairs[at] = r;
+    }
     __syncthreads();
   }
   for (int item = blockIdx.x; item < n * chunks; item += gridDim.x) {
-    const int share = chunks > 1 ? s_list[item / chunks] : item, chunk = chunks > 1 ? item % chunks : 0;
-    if (chunks > 1 || item != static_cast<int>(blockIdx.x)) e = p.pairs[share];
+    int share = item, chunk = 0;
+    if (chunks > 1) {
+      const int i = item / chunks;
+      share = s_list[i], chunk = item - i * chunks;
+      e = s_pairs[i];
+    } else if (item != static_cast<int>(blockIdx.x)) {
+      e = p.pairs[share];
+    }
     const int rows = e.tokens * p.tile.heads;
     if (e.pieces <= 0 || e.slot != 2 * share + 1 || 2 * (share + e.pieces) > p.max_slots || e.row0 < 0 ||
         e.row0 + e.tokens > p.seqs.T || rows > p.rows_cap)
@@ -889,7 +902,9 @@ __global__ void __launch_bounds__(kJoinThreads, 2) kv_attn_join_kernel(const __g
         float4 v[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-          const int64_t prow = static_cast<int64_t>(slot_of(min(c0 + k * stride, e.pieces - 1))) * p.rows_cap + rr;
+          const int64_t prow = static_cast<int64_t>(slot_of(c0 + k * stride)) * p.rows_cap + rr;
+          ml[k] = make_float2(-INFINITY, 0.f), v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (c0 + k * stride >= e.pieces) continue;
           ml[k] = p.ml[prow];
           v[k] = *reinterpret_cast<const float4*>(p.part + prow * DV + ch);
         }
