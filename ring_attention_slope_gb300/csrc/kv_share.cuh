@@ -8,8 +8,9 @@
 // inside pairs, so a CTA has at most two pieces that are to be joined with others', and a pair's pieces are those of
 // consecutive shares.  Where that is slower (few steps to a pair) every pair is claimed whole.
 //
-// Measured in kv_attn.cu.  Half the cost for a block whose second Q tile is empty, as it has half the work, was wrong (4 chunks
-// of 777 tokens, 192/128: 198 -> 240 us): its steps are one chain of latencies after another and take as long.
+// Measured in kv_attn.cu.  Half, three quarters or seven eighths of the cost for a block whose second Q tile is empty, as it has half
+// the work, was wrong (4 chunks of 777 tokens, 192/128: 198 -> 240, 201, 199 us): its steps, one chain of latencies after
+// another, take as long.
 #pragma once
 
 #include "kv_cache.cuh"
