@@ -97,7 +97,7 @@ struct Piece {
 __device__ __forceinline__ Piece make_piece(const KvAttnParams& p, const ShareLists& lists, const Shares& shares,
                                             const RowCut& cut, uint32_t g, int from, int to, uint32_t share, int& s) {
   Piece r;
-  while (s + 1 < shares.seqs && lists.pairs[s + 1] <= g) ++s;
+  s = last_not_above(lists.pairs, shares.seqs, g, s);
   const int block_tokens = cut.block_tokens;
   const KvSeq q = lists.at(s);
   // local = head * blocks + (blocks - 1 - block)

@@ -86,6 +86,19 @@ __device__ __forceinline__ uint32_t step_cost(uint32_t w, int fewest) {
   return divide(w + static_cast<uint32_t>(fewest) - 1u, static_cast<uint32_t>(fewest)) + (s > 0 ? 1u << s : 0u);
 }
 
+// The last entry of first[s .. n - 1] that is not above x; first[s] is not.
+__device__ __forceinline__ int last_not_above(const uint32_t* first, int n, uint32_t x, int s) {
+  if (s + 1 >= n || first[s + 1] > x) return s;
+  for (int hi = n - 1; s < hi;) {
+    const int mid = (s + hi + 1) >> 1;
+    if (first[mid] <= x)
+      s = mid;
+    else
+      hi = mid - 1;
+  }
+  return s;
+}
+
 // One whole warp calls it.  Estimates are in fp32, the same in every CTA; what says where a share begins is in whole
 // numbers.
 template <int kPieceSteps, int kCtas>
@@ -166,8 +179,7 @@ __device__ __forceinline__ Shares make_shares(const KvSeqs& p, int heads, const 
   r.whole = rounds * gridDim.x;
   r.from = 0;
   if (r.whole > 0) {
-    int s = 0;
-    while (s + 1 < listed && lists.pairs[s + 1] <= r.whole) ++s;
+    const int s = last_not_above(lists.pairs, listed, r.whole, 0);
     r.from = lists.cost[s] + (r.whole - lists.pairs[s]) * cost_of<kPieceSteps>(cut.most(lists.at(s)), r.per_step);
   }
   r.cost = cost - r.from;
@@ -207,14 +219,7 @@ __device__ __forceinline__ ShareStart share_start(const ShareLists& lists, const
   ShareStart r{sh.pairs, 0};
   if (k >= sh.shares) return r;
   const uint32_t x = sh.from + share_begin(sh, k);
-  int s = 0;
-  for (int hi = sh.seqs - 1; s < hi;) {
-    const int mid = (s + hi + 1) >> 1;
-    if (lists.cost[mid] <= x)
-      s = mid;
-    else
-      hi = mid - 1;
-  }
+  const int s = last_not_above(lists.cost, sh.seqs, x, 0);
   const KvSeq q = lists.at(s);
   const uint32_t w = cost_of<kPieceSteps>(cut.most(q), sh.per_step), o = x - lists.cost[s], local = divide(o, w);
   const uint32_t blocks = static_cast<uint32_t>(cut.blocks(q));
