@@ -13,7 +13,8 @@
 namespace slope {
 
 constexpr int64_t kKvMaxTokens = int64_t(1) << 28;  // of q's rows, and of a sequence
-constexpr int kKvMaxSeqs = 512;                     // sequences of a launch
+constexpr int64_t kKvMaxBatch = 65535;              // sequences of a call
+constexpr int kKvMaxSeqs = 512;                     // of a launch
 
 // Argument checks of a cache, its pointers and strides among them.
 slope_status check_kv_cache(const slope_kv_cache* c);

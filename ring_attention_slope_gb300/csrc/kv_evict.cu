@@ -453,6 +453,7 @@ cudaError_t launch_evict(const KvEvictParams& p, int64_t B, int dqk, int dv, cud
 }
 
 constexpr int kMinChunk = 24;  // chunk_of's smallest
+constexpr int64_t kMoveLaunches = (kKvMaxBatch + kKvMaxSeqs - 1) / kKvMaxSeqs;  // of a call, a ticket each
 
 struct Workspace {
   size_t flags, bounds, total;
@@ -460,9 +461,9 @@ struct Workspace {
 Workspace workspace_of(int64_t pairs, int64_t chunks) {
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   Workspace w;
-  w.flags = 256;  // (64 tickets before them: 65535 sequences in launches of kKvMaxSeqs)
-  w.bounds = w.flags + up(pairs * chunks * 4);
-  w.total = w.bounds + up(pairs * (chunks + 1) * 4);
+  w.flags = up(kMoveLaunches * sizeof(uint32_t));  // the tickets are before them
+  w.bounds = w.flags + up(pairs * chunks * sizeof(uint32_t));
+  w.total = w.bounds + up(pairs * (chunks + 1) * sizeof(int32_t));
   return w;
 }
 
@@ -474,7 +475,7 @@ using namespace slope;
 extern "C" {
 
 size_t slope_kv_evict_workspace_size(int64_t B, int64_t Hkv, int64_t keep) {
-  if (B < 0 || B > 65535 || Hkv < 1 || Hkv > 65535 || keep < 1 || keep >= kKvMaxTokens) return 0;
+  if (B < 0 || B > kKvMaxBatch || Hkv < 1 || Hkv > 65535 || keep < 1 || keep >= kKvMaxTokens) return 0;
   return workspace_of(B * Hkv, (keep + kMinChunk - 1) / kMinChunk).total;
 }
 

@@ -134,7 +134,7 @@ slope_status check_kv_q(const slope_tensor* q, const slope_kv_cache* c) {
 
 slope_status check_kv_batch(const slope_kv_batch* b, const slope_kv_cache* c, int64_t T) {
   if (b == nullptr) return SLOPE_ERR_NULL;
-  if (b->B < 0 || b->B > 65535) return SLOPE_ERR_SHAPE;
+  if (b->B < 0 || b->B > kKvMaxBatch) return SLOPE_ERR_SHAPE;
   if (b->cu_q == nullptr && (b->q_len < 0 || b->B * static_cast<int64_t>(b->q_len) != T)) return SLOPE_ERR_SHAPE;
   if (b->max_pages < 0 || b->max_pages > (kKvMaxTokens - 1) / c->page_size || b->table_stride < b->max_pages)
     return SLOPE_ERR_SHAPE;

@@ -267,3 +267,9 @@ def test_cache_objects_refuse_what_does_not_fit():
         make(k.transpose(2, 3).contiguous().transpose(2, 3), v)  # channels apart
     with pytest.raises(TypeError):
         make(k, v)  # right, but not on a GPU
+
+
+def test_evict_workspace_holds_a_ticket_for_each_launch(lib):
+    """A launch moves 512 sequences at most: its ticket, and a flag and two bounds for each of the pairs, have places of their own."""
+    for B in (1, 512, 513, 32768, 32769, 65535):
+        assert lib.slope_kv_evict_workspace_size(B, 1, 1) >= 4 * -(-B // 512) + 4 * B + 8 * B, B
