@@ -141,7 +141,7 @@ SLOPE_API size_t slope_kv_attn_workspace_size(int64_t T, int64_t Hq, const slope
  * The attention weights of the cached tokens: for sequence b, key head g and token j
  *   w = sum over the query heads h of g and the new tokens i of b that see j of
  *       exp(scale * q_ih . k_jg - lse[h][i]),
- * with lse as slope_kv_attn gives it.  A row whose lse is -inf adds nothing.
+ * with lse as slope_kv_attn gives it.  A row whose lse is -inf adds nothing, whatever it holds.
  *
  *   q, window, scale: as for slope_kv_attn, which rows are whose too; q may be
  *     the last rows of a chunk only.

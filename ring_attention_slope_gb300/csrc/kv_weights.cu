@@ -89,6 +89,7 @@ struct Cfg {
     float lse[kLseSlots][128];      // -lse log2(e) of a row tile's columns
     float few_lse[kPieces][kFew][128];  // of a piece's few row tiles
     float sums[kPieces][2][kBlockN];  // [piece][key tile]: what the second buffer's warps found
+    int none[kLseSlots], few_none[kPieces][kFew];  // the tile has rows of -inf: the caller's, or heads past the group
     uint64_t kfull[kKSlots], kempty[kKSlots], qfull[kQSlots], qempty[kQSlots], lfull[kLseSlots], lempty[kLseSlots];
     uint64_t s[4], sfree[4];  // [2 * buffer + key tile]
     uint64_t wfull[kPieces], wfree[kPieces], few_full[kPieces], sums_full[kPieces][2], drain[2];
@@ -367,10 +368,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int t0 = pc.few ? 0 : pc.i0;
       const int tiles = pc.few ? (pc.seen < pc.i1 ? pc.count * p.tile.parts : 0) : pc.i1 - pc.i0;
       float next[4];
+      int have = 0;  // tokens of that tile
       auto fetch = [&](int i) {
         const Rows r = rows_of(p, i, pc);
         const float* const at = p.lse + (static_cast<int64_t>(pc.kvh) * p.group + r.head) * p.lse_shead +
                                 (static_cast<int64_t>(pc.row0) + r.token) * p.lse_srow;
+        have = r.tokens;
 #pragma unroll
         for (int j = 0; j < 4; ++j) next[j] = tokens[j] < r.tokens && heads[j] < r.heads ? at[offset[j]] : -INFINITY;
       };
@@ -379,6 +382,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         float v[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = next[j] == -INFINITY ? next[j] : -next[j] * kLog2e;
+        bool none = false;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) none |= tokens[j] < have && v[j] == -INFINITY;
+        const int some = __any_sync(0xffffffffu, none);
         if (i + 1 < tiles) fetch(t0 + i + 1);
         // (that of few row tiles has a place of its own, which lasts as long as the piece)
         const int slot = cnt % kLseSlots;
@@ -387,6 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float* const dst = pc.few ? sh.few_lse[k % kPieces][i] : sh.lse[slot];
 #pragma unroll
         for (int j = 0; j < 4; ++j) dst[lane + 32 * j] = v[j];
+        if (lane == 0) (pc.few ? sh.few_none[k % kPieces][i] : sh.none[slot]) = some;
         __syncwarp();
         if (!pc.few) {
           if (lane == 0) mbar_arrive(&sh.lfull[slot]);
@@ -476,12 +484,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t sl2 = pack_f32x2(p.scale_log2, p.scale_log2);
     int lcnt = 0, used = 0;  // row tiles' lse taken, uses of this buffer
     bool ok = true;
+    auto scores_there = [&](int step) -> bool {
+      if (!warp_all(wait(&sh.s[2 * buf + t], step, 70))) return false;
+      tc_fence_after_sync();
+      return true;
+    };
     // The sum over a row tile's columns, all of which count (one without a row has a score of 0 and an lse of inf): each 32
     // columns' load runs under the exponentials of the 32 before.
-    auto all_columns = [&](int step, const float* lse, float& sum) -> bool {
-      const int b = 2 * buf + t;
-      if (!warp_all(wait(&sh.s[b], step, 73))) return false;
-      tc_fence_after_sync();
+    auto all_columns = [&](const float* lse) -> float {
       uint64_t acc[2] = {0, 0};
       uint32_t s[2][32];
       tmem_ld32(tS, s[0]);
@@ -503,12 +513,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (c + 64 == kBlockN) {  // the scores are in registers
           tc_fence_before_sync();
-          arrive(&sh.sfree[b]);
+          arrive(&sh.sfree[2 * buf + t]);
         }
       }
       const float2 a = unpack_f32x2(acc[0]), z = unpack_f32x2(acc[1]);
-      sum = (a.x + a.y) + (z.x + z.y);
-      return true;
+      return (a.x + a.y) + (z.x + z.y);
     };
     // Whether row tile i is full and all its rows see all of the warp's keys.
     auto seen_by_all = [&](const Piece& pc, int i, int pos) -> bool {
@@ -517,9 +526,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       return r.tokens == p.tile.tokens && r.heads == p.tile.heads && kfirst + kBlockN - 1 <= qa &&
              (p.window == 0 || qa + r.tokens - 1 - kfirst < p.window);
     };
-    // The sum over row tile i's columns that see the key at position pos.
-    auto columns = [&](const Piece& pc, int i, int step, int pos, const float* lse, float& sum) -> bool {  // (any tile)
-      const int b = 2 * buf + t;
+    // The sum over row tile i's columns that see the key at position pos.  (any tile; none: of its rows some add nothing)
+    auto columns = [&](const Piece& pc, int i, int pos, const float* lse, int none) -> float {
       const Rows r = rows_of(p, i, pc);
       const int cols = r.tokens * p.tile.heads, qa = pc.pos0 + r.token, qb = qa + r.tokens - 1;
       // tokens from the key's position on, and up to the window's end
@@ -527,8 +535,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int hi = p.window > 0 && pos + p.window - 1 < qb ? max(0, pos + p.window - qa) * p.tile.heads : cols;
       const int kfirst = pos - row, klast = kfirst + kBlockN - 1;
       const bool all = klast <= qa && (p.window == 0 || qb - kfirst < p.window);  // every row sees every key
-      if (!warp_all(wait(&sh.s[b], step, 70))) return false;
-      tc_fence_after_sync();
       uint64_t acc[2] = {0, 0};
 #pragma unroll 1
       for (int c = 0; c < cols; c += 32) {
@@ -538,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         reg_fence(s);
         if (c + 32 >= cols) {  // the scores are in registers
           tc_fence_before_sync();
-          arrive(&sh.sfree[b]);
+          arrive(&sh.sfree[2 * buf + t]);
         }
         float x[32];
 #pragma unroll
@@ -556,21 +562,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 32; ++e)
             if (static_cast<uint32_t>(c + e - lo) >= span) x[e] = -INFINITY;
         }
-        if (r.heads < p.tile.heads) {  // the last part of a group of more than 128 heads
-          uint32_t none = 0;
-#pragma unroll 1
-          for (int e = 0; e < 32; ++e) none |= ((c + e) % p.tile.heads >= r.heads ? 1u : 0u) << e;
+        if (none != 0) {  // (a score that is not finite may have made them NaN)
+          const uint32_t out = __ballot_sync(0xffffffffu, lse[c + lane] == -INFINITY);
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            if ((none >> e) & 1u) x[e] = -INFINITY;
+            if ((out >> e) & 1u) x[e] = -INFINITY;
         }
 #pragma unroll
         for (int e = 0; e < 16; ++e)
           acc[e & 1] = add_f32x2(acc[e & 1], pack_f32x2(ex2_approx(x[2 * e]), ex2_approx(x[2 * e + 1])));
       }
       const float2 a = unpack_f32x2(acc[0]), z = unpack_f32x2(acc[1]);
-      sum = (a.x + a.y) + (z.x + z.y);
-      return true;
+      return (a.x + a.y) + (z.x + z.y);
     };
     for (int k = 0; ok; ++k) {
       if (!warp_all(take_piece(k))) break;
@@ -595,10 +598,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           next = i + 2 < pc.i1 ? page_of((i + 2) * kKeys + key) : -1;
           float total = 0.f;
           for (int r = 0; ok && i >= pc.seen && r < tiles; ++r, ++used) {
-            float sum;
-            ok = tiles > 1 && seen_by_all(pc, r, pos) ? all_columns(used, sh.few_lse[k % kPieces][r], sum)
-                                                      : columns(pc, r, used, pos, sh.few_lse[k % kPieces][r], sum);
-            total += sum;
+            const float* const lse = sh.few_lse[k % kPieces][r];
+            const int none = sh.few_none[k % kPieces][r];
+            const bool all = tiles > 1 && seen_by_all(pc, r, pos);
+            ok = scores_there(used);
+            if (ok) total += all && none == 0 ? all_columns(lse) : columns(pc, r, pos, lse, none);
           }
           if (!ok) break;
           put(pg, pos, total);
@@ -618,12 +622,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         float total = 0.f;
         for (int i = pc.i0 + buf; i < pc.i1; i += 2, ++used) {  // this buffer's
           const int at = lcnt + (i - pc.i0), slot = at % kLseSlots;
-          float sum;
           ok = warp_all(wait(&sh.lfull[slot], at / kLseSlots, 69));
-          if (ok) ok = i >= f0 && i < f1 ? all_columns(used, sh.lse[slot], sum) : columns(pc, i, used, pos, sh.lse[slot], sum);
           if (!ok) break;
+          const int none = sh.none[slot];  // (on its way during the wait)
+          ok = scores_there(used);
+          if (!ok) break;
+          total += i >= f0 && i < f1 && none == 0 ? all_columns(sh.lse[slot]) : columns(pc, i, pos, sh.lse[slot], none);
           arrive(&sh.lempty[slot]);
-          total += sum;
         }
         if (!ok) break;
         lcnt += pc.i1 - pc.i0;
