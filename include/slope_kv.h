@@ -25,7 +25,7 @@
 
 #include "slope.h"
 
-/* Launches of slope_kv_attn and slope_kv_attn_weights that may be queued at a time. */
+/* Launches of slope_kv_attn and slope_kv_attn_weights that may be queued at a time, and as many recorded into graphs. */
 #define SLOPE_KV_COUNTERS 65536
 
 #ifdef __cplusplus
@@ -117,8 +117,10 @@ SLOPE_API slope_status slope_kv_write(const slope_kv_cache* cache, const slope_t
  *
  * A launch takes a counter out of SLOPE_KV_COUNTERS on the device, another for every
  * 512 sequences after the first: keep fewer launches queued or running at a time.
- * Launches recorded into a graph take theirs out of as many others and keep them, so
- * replays of one recording must not overlap; other calls may run beside them.
+ * Launches recorded into a graph take theirs out of as many others and keep them until
+ * the graph and everything instantiated from it are destroyed, so replays of one
+ * recording must not overlap; other calls may run beside them.  Where that many are
+ * recorded in graphs that exist, a further one returns SLOPE_ERR_CUDA.
  * Softmax weights are rounded to bf16 on their way into the tensor cores; scores,
  * maxima, sums and outputs stay in fp32 until the output's rounding.  Whatever the
  * cache holds behind a sequence's last token, NaN too, reaches no row.  Among a

@@ -25,7 +25,7 @@ MARSHAL_PATH = os.path.join(PKG, "_marshal" + sysconfig.get_config_var("EXT_SUFF
 
 SOURCES = ["attn_partial.cu", "kv4_attn.cu", "api.cu", "lse_merge.cu", "qk_norm_rope.cu", "kv4_store.cu", "kv_attn.cu",
            "kv_weights.cu", "kv_evict.cu", "kv_store.cu", "status.cu", "dck.cpp", "rope.cpp"]
-HEADERS = ["host.cuh", "kernels.cuh", "kv4.cuh", "kv_cache.cuh", "kv_cut.cuh", "kv_share.cuh", "sm103_ptx.cuh", "waits.cuh"]
+HEADERS = ["host.cuh", "kernels.cuh", "kv4.cuh", "kv_cache.cuh", "kv_cut.cuh", "kv_share.cuh", "slot_pool.hpp", "sm103_ptx.cuh", "waits.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "-I", INCLUDE, "-I", CSRC]

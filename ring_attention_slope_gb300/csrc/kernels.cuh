@@ -144,8 +144,9 @@ int* device_status_ptr();  // per current device; nullptr on failure
 // memory, each 0 between launches).
 constexpr int kTileCounterSlots = SLOPE_TILE_COUNTERS;
 uint32_t* claim_tile_counter();  // the next counter of the current device; nullptr on failure
-// The same for launches on the 16-bit cache, from rings of their own: one for launches on a stream, one for those recorded
-// into a graph, which keep theirs for every replay while launches on streams go on.
-uint32_t* claim_cache_counter(cudaStream_t stream);
+// The same for launches on the 16-bit cache, from counters of their own: a ring for launches on a stream; and others for those
+// recorded into a graph, which keep theirs for as long as the graph, or what is made of it, may run (none left:
+// cudaErrorLaunchOutOfResources).
+cudaError_t claim_cache_counter(cudaStream_t stream, uint32_t** counter);
 
 }  // namespace slope

@@ -1003,8 +1003,7 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
     if (e != cudaSuccess) return e;
     ready[dev].store(true, std::memory_order_release);
   }
-  p.tile_counter = claim_cache_counter(stream);
-  if (p.tile_counter == nullptr) return cudaErrorInvalidDevice;
+  if ((e = claim_cache_counter(stream, &p.tile_counter)) != cudaSuccess) return e;
   e = launch_early(kv_attn_kernel<DQK, DV, QT>, dim3(static_cast<unsigned>(grid)), C::kThreads, C::kSmemBytes, stream, tq, tk,
                    tv, p);
   if (e != cudaSuccess) return e;

@@ -710,8 +710,7 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, KvWeightsParams
     if (e != cudaSuccess) return e;
     ready[dev].store(true, std::memory_order_release);
   }
-  p.tile_counter = claim_cache_counter(stream);
-  if (p.tile_counter == nullptr) return cudaErrorInvalidDevice;
+  if ((e = claim_cache_counter(stream, &p.tile_counter)) != cudaSuccess) return e;
   const int sms = kv_sm_count();
   e = launch_early(kv_weights_kernel<DQK>, dim3(static_cast<unsigned>(sms)), kThreads, C::kSmemBytes, stream, tq, tk, p);
   if (e != cudaSuccess || tiles <= C::kFew) return e;  // (no sequence's rows fill more tiles: nothing is joined)

@@ -8,6 +8,7 @@
 
 #include "kernels.cuh"
 #include "slope_kv.h"
+#include "slot_pool.hpp"
 #include "sm103_ptx.cuh"
 #include "waits.cuh"
 
@@ -35,7 +36,14 @@ std::atomic<int*> g_status_ptr[kMaxDevices];
 std::atomic<uint32_t*> g_counters_ptr[kMaxDevices];
 std::atomic<uint32_t> g_counter_next[kMaxDevices];
 std::atomic<uint32_t*> g_cache_counters_ptr[kMaxDevices];
-std::atomic<uint32_t> g_cache_counter_next[kMaxDevices][2];
+std::atomic<uint32_t> g_cache_counter_next[kMaxDevices];  // of launches on streams
+SlotPool<kCacheCounterSlots> g_recorded[kMaxDevices];     // counters of recorded launches that are in use
+
+// What a graph calls when nothing can run its launch any more; the place is (device, counter), and one more than that.
+void CUDART_CB give_counter_back(void* place) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(place) - 1;
+  g_recorded[at / kCacheCounterSlots].give_back(static_cast<uint32_t>(at % kCacheCounterSlots));
+}
 
 // One block waits on a barrier that nothing ever arrives on; the bounded wait
 // must run out, record the timeout and let the kernel return normally.
@@ -80,21 +88,43 @@ uint32_t* claim_tile_counter() {
   return base + g_counter_next[dev].fetch_add(1, std::memory_order_relaxed) % kTileCounterSlots;
 }
 
-uint32_t* claim_cache_counter(cudaStream_t stream) {
+cudaError_t claim_cache_counter(cudaStream_t stream, uint32_t** counter) {
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
   uint32_t* base = g_cache_counters_ptr[dev].load(std::memory_order_acquire);
   if (base == nullptr) {
     void* addr = nullptr;
-    if (cudaGetSymbolAddress(&addr, g_slope_cache_counters) != cudaSuccess) return nullptr;
+    if ((e = cudaGetSymbolAddress(&addr, g_slope_cache_counters)) != cudaSuccess) return e;
     base = static_cast<uint32_t*>(addr);
     g_cache_counters_ptr[dev].store(base, std::memory_order_release);
   }
   cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-  if (cudaStreamIsCapturing(stream, &capture) != cudaSuccess) return nullptr;  // (nor could a kernel be launched)
-  const uint32_t ring = capture == cudaStreamCaptureStatusNone ? 0 : 1;
-  const uint32_t k = g_cache_counter_next[dev][ring].fetch_add(1, std::memory_order_relaxed) % kCacheCounterSlots;
-  return base + ring * kCacheCounterSlots + k;
+  if ((e = cudaStreamIsCapturing(stream, &capture)) != cudaSuccess) return e;  // (nor could a kernel be launched)
+  if (capture == cudaStreamCaptureStatusNone) {
+    *counter = base + g_cache_counter_next[dev].fetch_add(1, std::memory_order_relaxed) % kCacheCounterSlots;
+    return cudaSuccess;
+  }
+  // The graph, and what is made of it, holds an object that gives the counter back as it goes.
+  cudaGraph_t graph = nullptr;
+  if ((e = cudaStreamGetCaptureInfo(stream, &capture, nullptr, &graph, nullptr, nullptr, nullptr)) != cudaSuccess) return e;
+  if (capture != cudaStreamCaptureStatusActive) return cudaErrorStreamCaptureInvalidated;
+  const uint32_t k = g_recorded[dev].take();
+  if (k == kCacheCounterSlots) return cudaErrorLaunchOutOfResources;
+  void* const place = reinterpret_cast<void*>(static_cast<uintptr_t>(dev) * kCacheCounterSlots + k + 1);
+  cudaUserObject_t object = nullptr;
+  e = cudaUserObjectCreate(&object, place, give_counter_back, 1, cudaUserObjectNoDestructorSync);
+  if (e != cudaSuccess) {
+    g_recorded[dev].give_back(k);
+    return e;
+  }
+  if ((e = cudaGraphRetainUserObject(graph, object, 1, cudaGraphUserObjectMove)) != cudaSuccess) {
+    cudaUserObjectRelease(object, 1);  // (which gives it back)
+    return e;
+  }
+  *counter = base + kCacheCounterSlots + k;
+  return cudaSuccess;
 }
 
 cudaError_t launch_timeout_selftest(uint64_t limit_ns, int* status, cudaStream_t stream) {
