@@ -54,6 +54,25 @@ class Call:
         return graph
 
 
+def test_a_graph_beside_more_calls_than_there_are_counters():
+    """Calls on streams go once round their counters while a recorded call runs."""
+    long, short = Call([40000, 30000, 35000], 1), Call([700], 2)
+    graph, side = long.recorded(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for i in range(COUNTERS + 200):
+        if i % 4 == 0:
+            graph.replay()
+        short(side)
+        if i % 64 == 63:
+            with torch.cuda.stream(side):
+                short.look()
+        if i % 1024 == 1023:
+            torch.cuda.synchronize()
+            assert int(long.bad) == 0 and int(short.bad) == 0, i
+    torch.cuda.synchronize()
+    assert int(long.bad) == 0 and int(short.bad) == 0
+
+
 def test_counters_of_graphs_that_are_gone_come_again():
     """A recorded call keeps its counter while others are recorded and dropped, more of them than there are counters; where
     all are kept, a further recording is refused; and they are there again once the graphs are gone."""
