@@ -134,8 +134,8 @@ SLOPE_API slope_status slope_kv_attn(const slope_tensor* q, const slope_kv_cache
                                      void* workspace, size_t workspace_bytes, void* stream);
 
 /*
- * Workspace bytes slope_kv_attn needs for T rows in sequences of at most q_len new tokens (0: any number); 0 for arguments
- * it does not support.
+ * Workspace bytes slope_kv_attn needs for T rows: of a batch without cu_q, with its q_len; of one with cu_q, whose ranges only
+ * the device knows, with q_len = 0 (a workspace sized for a q_len is refused there).  0 for arguments it does not support.
  */
 SLOPE_API size_t slope_kv_attn_workspace_size(int64_t T, int64_t Hq, const slope_kv_cache* cache, int32_t q_len);
 

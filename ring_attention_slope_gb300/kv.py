@@ -148,7 +148,7 @@ def kv_write(cache, k, v, slots, *, weights=None, stream=None):
 
 
 def kv_attn_workspace_size(T, Hq, cache, q_len=0) -> int:
-    """Workspace bytes of :func:`kv_attn` for T rows in sequences of at most q_len new tokens (0: any number); 0 for
+    """Workspace bytes of :func:`kv_attn` for T rows in runs of q_len, or (q_len = 0) in those that a ``cu_q`` gives; 0 for
     arguments it does not support."""
     return (_marshal or _bound()).kv_attn_workspace_size(T, Hq, cache._c, q_len, False)
 

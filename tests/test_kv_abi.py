@@ -273,3 +273,13 @@ def test_evict_workspace_holds_a_ticket_for_each_launch(lib):
     """A launch moves 512 sequences at most: its ticket, and a flag and two bounds for each of the pairs, have places of their own."""
     for B in (1, 512, 513, 32768, 32769, 65535):
         assert lib.slope_kv_evict_workspace_size(B, 1, 1) >= 4 * -(-B // 512) + 4 * B + 8 * B, B
+
+
+def test_a_batch_with_row_indices_needs_the_workspace_of_any_length(lib):
+    """What its longest run is, only the device knows."""
+    rows = dict(q=t([32, 64, 64]), c=cache(H=8), out=t([32, 64, 64]), lse=t([64, 32], F32), w=weights(cache(H=8)))
+    size = lambda q_len: lib.slope_kv_attn_workspace_size(32, 64, ref(cache(H=8)), q_len)  # noqa: E731
+    assert size(4) < size(0)
+    for n in (size(4), size(0) - 1):
+        assert both_attentions(lib, **rows, b=batch(cu_q=0x9000, q_len=4), n=n)[0] == E_WS
+    assert both_attentions(lib, **rows, b=batch(B=8, q_len=4), n=size(4) - 1)[0] == E_WS
