@@ -184,8 +184,9 @@ SLOPE_API size_t slope_kv_attn_weights_workspace_size(int64_t T, int64_t Hq, con
  *     after keep what they hold.  Or device int32 [B, out_pages], out_pages * page_size
  *     >= min(keep, max_pages * page_size) (else SLOPE_ERR_SHAPE), rows out_stride elements
  *     apart: the tokens are copied to the positions of these pages of the same cache,
- *     and the old ones keep what they hold.  A page that one sequence's tokens go to may be no
- *     other page of the call.
+ *     and the old ones keep what they hold.
+ *     In both forms a page that one sequence's tokens go to may be no other page of the call: a
+ *     prefix that sequences share is copied by each into pages of its own, not moved in place.
  *   kept: device int32 [B, Hkv, keep], dense: the old positions of the tokens kept, in order; -1 after them.
  *   out_lens: device int32 [B]: min(n, keep).  May be kv_lens itself.
  *   workspace: slope_kv_evict_workspace_size() bytes, 256-byte aligned, no initial contents, one for each

@@ -211,8 +211,9 @@ def kv_evict(cache, weights, block_table, kv_lens, keep, *, first=0, recent=0, o
              workspace=None, stream=None):
     """Keeps of each sequence and key head ``keep`` tokens: the first ``first``, the last ``recent`` and of those between
     the ones with the largest ``weights`` (fp32 [n_pages,Hkv,page_size]; of equal ones the earlier).  They move, in
-    order, to the sequence's positions 0, 1, ..., or to those of the pages of ``out_table`` (device int32 [B,pages]),
-    which may be no other pages of the call; weights move along.  Returns ``(kept, out_lens)``: device int32
+    order, to the sequence's positions 0, 1, ..., or to those of the pages of ``out_table`` (device int32 [B,pages]);
+    weights move along.  The pages that they go to may be no other pages of the call: sequences that share pages need an
+    ``out_table``.  Returns ``(kept, out_lens)``: device int32
     [B,Hkv,keep], the kept tokens' old positions and -1 after them, and [B], the new lengths."""
     m = _marshal or _bound()
     alloc = _allocator(stream)
