@@ -109,7 +109,8 @@ SLOPE_API slope_status slope_kv_write(const slope_kv_cache* cache, const slope_t
  *   window, scale: as in slope.h.
  *   out bf16 or fp32 [T, Hq, dv]; lse fp32 [Hq, T] or NULL: as for
  *     slope_attn_partial (out 16-byte aligned, its strides multiples of 16
- *     bytes); a row that sees no key gets 0 and -inf.
+ *     bytes); a row that sees no key gets 0 and -inf, and so does one all of whose visible
+ *     scores are -inf (where a softmax would be 0 / 0).
  *   workspace: device buffer of slope_kv_attn_workspace_size() bytes, 256-byte
  *     aligned; it needs no initial contents.  Calls that may overlap on the GPU
  *     need one each, captured graphs that may be replayed at the same time too.
@@ -155,7 +156,8 @@ SLOPE_API size_t slope_kv_attn_workspace_size(int64_t T, int64_t Hq, const slope
  *     be written for two sequences of one call.
  *   workspace: slope_kv_attn_weights_workspace_size() bytes, as for slope_kv_attn.
  * B == 0 is a no-op, T == 0 a call whose sums are all 0.
- * Sums run in fp32 in an order that depends on the call's sizes alone.
+ * Sums run in fp32 in an order that depends on the call's sizes and lengths alone.  A key that is not
+ * finite may get a NaN whatever its scores; no other key's weight does by it.
  */
 SLOPE_API slope_status slope_kv_attn_weights(const slope_tensor* q, const slope_kv_cache* cache,
                                              const slope_kv_batch* batch, const slope_tensor* lse, int64_t window,
