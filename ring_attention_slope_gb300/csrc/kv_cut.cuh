@@ -119,6 +119,9 @@ __device__ __forceinline__ Cut make_cut(const KvSeqs& p, int heads, const CutOf&
     const float rounds = static_cast<float>(__reduce_add_sync(0xffffffffu, count[i])) * per_cta;
     const float piece = static_cast<float>(per[i] + kPieceSteps);
     const float even = share + rounds * kPieceSteps;
+    // Alike: if full rounds of the longest pieces would be no more than a ninth longer than the even share (a 1K chunk at 16K,
+    // 32/4 heads of 128: 116 us, and 17 queries each of 30 sequences of 2040, 64/8 heads of 64, 25.4; at 0.8 the same; with
+    // none alike, 1.0, 108 and 31).  The half piece decides in no call measured: 0 and a whole one are as fast.
     const float cost = rounds <= 1.f                   ? fmaxf(piece, even)
                        : even > 0.9f * rounds * piece ? ceilf(rounds) * piece
                                                        : fmaxf(piece, even) + 0.5f * piece;

@@ -13,10 +13,11 @@
 // read and written once, by as many CTAs as the GPU holds.  A chunk waits only for chunks of lower tickets, which are running and
 // read before they wait, so every wait ends; all the same it is bounded.
 //
-// On one GB300, 8 heads of 64: four sequences of up to 64K to 16384 tokens 38 us (selection 23 and moving 21 by themselves:
-// three passes after one another over the bins of a cluster, then rows that wait for others' reads); 8 x 100K to 32768 244 us,
-// 4.6 TB/s read and written; one of 2000 tokens 11.7 us, latencies.  Keys loaded one at a time and a CTA for every
-// chunk took 75 us for the first of these.
+// On one GB300, 8 heads of 64, into other pages and in place: sequences of 65536, 3251, 161 and 9 tokens to 16384 38 us and as
+// much (selection 23 and moving 21 by themselves: three passes after one another over the bins of a cluster; then chunk after chunk,
+// two or three to a CTA, a chain of old positions, pages, rows and stores); 8 x 100K to 32768 244 us, 4.6 TB/s read and
+// written, and 279, where chunks wait for others' reads too; 32 x 8K to 4096 113 and 136; one of 2000 tokens 11.7 us, latencies,
+// and 2 more.  Keys loaded one at a time and a CTA for every chunk took 75 us for the first of these.
 #include <cooperative_groups.h>
 
 #include <algorithm>

@@ -185,7 +185,9 @@ __device__ __forceinline__ Shares make_shares(const KvSeqs& p, int heads, const 
   r.cost = cost - r.from;
   r.shares = min(gridDim.x, divide(r.cost, finest));
   const float piece = static_cast<float>(most + kPieceSteps);
-  // (a last round that leaves every SM one of its two CTAs is shorter)
+  // A last round that leaves every SM one of its two CTAs is shorter: 0.65 of one (four 2K chunks at 32K, window 1024: 223 us, as
+  // with 0.5 and 0.8; with a whole one 236).  Whole pairs that are not alike end unevenly, half a piece later on average (a
+  // chunk beside 15 single tokens: 265 us in shares, which it takes by that, and 292 whole; with a whole piece as with half).
   const float last = all_rounds - floorf(all_rounds);
   const float uncut = all_rounds <= 1.f        ? fmaxf(piece, even)
                       : long_pairs == pairs ? (kCtas == 2 && last <= 0.5f ? floorf(all_rounds) + 0.65f : ceilf(all_rounds)) * piece
@@ -194,7 +196,9 @@ __device__ __forceinline__ Shares make_shares(const KvSeqs& p, int heads, const 
   const float wholes = static_cast<float>(rounds), spread = __fdividef(static_cast<float>(gridDim.x), static_cast<float>(r.shares));
   const float share = fmaxf(0.f, steps - wholes * static_cast<float>(most)) * spread +
                       (fmaxf(0.f, all_rounds - wholes) * spread + 1.f) * kPieceSteps;
-  // Shares of many long pairs each would have all heads' keys read at once; and costs are counted in 32 bits.
+  // Shares of many long pairs each would have all heads' keys read at once; and costs are counted in 32 bits.  (Of 44 calls
+  // the limit of 3 pieces decides in none, as without it all take the same time.  256 sequences up to 4096 tokens, one new each,
+  // would be faster whole, as with a limit of 2: 105 us, in shares 141.)
   if (r.shares == 0 || wholes * piece + share >= uncut || share > 3.f * piece || steps * static_cast<float>(gridDim.x) > 6e7f)
     r.whole = pairs, r.shares = 0;
   // Row ranges that overlap can make more pairs than can be counted (those of a call that is in order are below 2^29 and its

@@ -19,8 +19,9 @@
 // block, so that each SM sub-partition has four warps with exponentials to issue.
 //
 // On one GB300, 64/8 heads of 64: every query of a 2K chunk at 16K 339 us, 70% of the MUFU unit's rate (eight softmax warps and one
-// MMA issuer, which was the bound, 571); the last 64 queries of 32K 34.9 (38 before the keys' pieces were as short as gives
-// no CTA two); a decode step of 16 x 8K 32 us and of 8 x 100K 147, 5.9 TB/s of keys (70 and 394 before the rows stayed).
+// MMA issuer, which was the bound, 571); the last 64 queries of 32K 35.7 (38 before the keys' pieces were as short as gives
+// no CTA two); a decode step of 16 x 8K 32 us and of 8 x 100K 147, 5.9 TB/s of keys (70 and 394 before the rows stayed), 36 and
+// 162 where the sums are added to what is there.
 #include <cuda_bf16.h>
 
 #include <algorithm>
