@@ -119,9 +119,9 @@ SLOPE_API slope_status slope_kv_write(const slope_kv_cache* cache, const slope_t
  * A launch takes a counter out of SLOPE_KV_COUNTERS on the device, another for every
  * 512 sequences after the first: keep fewer launches queued or running at a time.
  * Launches recorded into a graph take theirs out of as many others and keep them until
- * the graph and everything instantiated from it are destroyed, so replays of one
- * recording must not overlap; other calls may run beside them.  Where that many are
- * recorded in graphs that exist, a further one returns SLOPE_ERR_CUDA.
+ * the graph and the executable graphs made of it (or updated with it) are destroyed, so
+ * replays of one recording must not overlap; other calls may run beside them.  Where that
+ * many are recorded in graphs that exist, a further one returns SLOPE_ERR_CUDA.
  * Softmax weights are rounded to bf16 on their way into the tensor cores; scores,
  * maxima, sums and outputs stay in fp32 until the output's rounding.  Whatever the
  * cache holds behind a sequence's last token, NaN too, reaches no row.  Among a
@@ -153,7 +153,8 @@ SLOPE_API size_t slope_kv_attn_workspace_size(int64_t T, int64_t Hq, const slope
  *     j is in its page's place.  accumulate != 0 adds w to what is there (where w is 0
  *     nothing is written), else w replaces it; in both cases for positions below
  *     kv_lens[b] whose page is in range, and nowhere else.  No place of weights may
- *     be written for two sequences of one call.
+ *     be written twice in one call: not for two sequences that share a page, nor for
+ *     two positions of one.
  *   workspace: slope_kv_attn_weights_workspace_size() bytes, as for slope_kv_attn.
  * B == 0 is a no-op, T == 0 a call whose sums are all 0.
  * Sums run in fp32 in an order that depends on the call's sizes and lengths alone.  A key that is not
