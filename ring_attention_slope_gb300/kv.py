@@ -188,8 +188,8 @@ def kv_attn_weights(q, cache, block_table, kv_lens, lse, weights, *, cu_q=None, 
                     accumulate=True, workspace=None, stream=None):
     """Adds to ``weights`` (fp32 [n_pages,Hkv,page_size]) the attention weight exp(scale q k - lse) that each cached
     token gets from each sequence's newest tokens, summed over them and the query heads of its key head;
-    ``accumulate=False`` puts the sums in its place.  ``lse``: fp32 [Hq,T], of :func:`kv_attn` on the same rows; the
-    other arguments are as there.  Returns ``weights``."""
+    ``accumulate=False`` puts the sums in its place.  ``lse``: fp32 [Hq,T], of :func:`kv_attn` on the same rows (-inf: the
+    row adds nothing); the other arguments are as there, but no page may be of two sequences.  Returns ``weights``."""
     m = _marshal or _bound()
     alloc = _allocator(stream)
     T, Hq, _ = q.shape
